@@ -80,8 +80,10 @@ typedef enum {
     SAF_EWORKSPACE = -5,    /* workspace NULL or smaller than saf_attn_workspace_bytes    */
     SAF_ETIMEOUT = -6,      /* a bounded device wait expired (from saf_device_status)    */
     SAF_ECUDA = -8,         /* a CUDA runtime query failed (no device, driver error)    */
-    SAF_ESCRATCH = -9       /* saf_attn_fwd_noalloc: the problem needs more workspace
+    SAF_ESCRATCH = -9,      /* saf_attn_fwd_noalloc: the problem needs more workspace
                                than its fixed device scratch holds                     */
+    SAF_EPAGE = -10         /* a paged call met a page or a token count outside its
+                               bounds (from saf_device_status)                         */
 } saf_status_t;
 
 /* Bytes of device workspace that saf_attn_fwd (backward = 0) or
@@ -232,6 +234,123 @@ SAF_API int saf_attn_bwd_prepared(const void* q, const void* k, const void* v, c
                                   saf_dtype_t dt, void* dq, void* dk, void* dv, void* workspace, size_t ws_bytes,
                                   void* stream);
 
+/* ---- Sliding window with sinks -------------------------------------------------
+ * The layer (saf_attn_fwd_gqa / saf_attn_bwd_gqa, Hkv = H for the multi-head
+ * layer) with ordinary heads that see the last `window` keys and the first
+ * `sinks`: query i attends to the keys j <= i with i - j < window or j < sinks,
+ *     A(i, j) = exp(S(i, j)) / sum over the keys that i sees,
+ * and its own key is always among them. Only key blocks that a block of queries
+ * sees are visited, forward and backward. Frozen heads keep their whole pattern
+ * (Eq. 3): it is a fixed matrix, cut by its own r.
+ *
+ * window >= 0, sinks >= 0 (else SAF_EINVAL); window = 0 or window >= T is the layer
+ * without a window, with the same bits. state: NULL, or the prepared state of
+ * saf_frozen_prepare for these a, r and frozen (as for the _prepared calls).
+ * Everything else (shapes, workspace, empty calls, errors, outputs) is as for the
+ * calls named above. Keys and values that the window hides from a row must still be
+ * finite where another row of the same 128-row block (64 in SAF_FP32) sees them. */
+SAF_API int saf_attn_fwd_window(const void* q, const void* k, const void* v, const float* a, const float* r,
+                                int ld_prior, const uint8_t* frozen, const void* state, int window, int sinks, int B,
+                                int H, int Hkv, int T, int d, saf_dtype_t dt, void* o, float* lse, void* workspace,
+                                size_t ws_bytes, void* stream);
+SAF_API int saf_attn_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                                const float* lse, const float* a, const float* r, int ld_prior,
+                                const uint8_t* frozen, const void* state, int window, int sinks, int B, int H,
+                                int Hkv, int T, int d, saf_dtype_t dt, void* dq, void* dk, void* dv, void* workspace,
+                                size_t ws_bytes, void* stream);
+
+/* ---- Paged cache ---------------------------------------------------------------
+ * Serving: keys and values of B sequences live in fixed-size pages of two caches,
+ *     k_cache, v_cache [num_pages, Hkv, page_size, d]  (dt, contiguous, 16-byte aligned),
+ * and page_table [B, max_pages] (DEVICE int32) names a sequence's pages in order: slot x
+ * of sequence b is row x mod page_size of page page_table[b, x / page_size]. page_size is
+ * a power of two, 8 to 1024; num_pages * Hkv <= 2^31 - 1.
+ *
+ * A step brings up to T new tokens per sequence. ctx [B] (DEVICE int32) counts the
+ * tokens in the cache before them and n_new [B] (DEVICE int32, NULL: T each) the new
+ * ones, 0 <= n_new[b] <= T; rows t >= n_new[b] of a padded batch hold no token. The
+ * counts are read on the device, so a captured graph serves every step.
+ *
+ * What the device finds outside its bounds (a negative ctx, an n_new outside [0, T],
+ * tokens past max_pages * page_size or max_len, a page outside [0, num_pages)) never
+ * leads to an access: counts are cut to their bounds (a negative ctx: no tokens), keys
+ * of such a page are not written and not seen, and the call ORs a bit into its status
+ * words, which saf_device_status answers with SAF_EPAGE. The status words of these
+ * calls stay as they are until the caller clears them; zero them when you make them.
+ * Entries of page_table behind a sequence's last token, and behind the window of a call
+ * whose heads are all cut by one, are not read as pages and may hold anything.
+ *
+ * saf_kv_append
+ * writes the new tokens' k and v into the caches: token t of sequence b into slot
+ * ctx[b] + t, with the rotary position rotation applied to k, and to q for the
+ * attention that follows:
+ *     pair c of a row:  (y0, y1) = (x0 cos w - x1 sin w, x0 sin w + x1 cos w),
+ *     w = (pos_base + ctx[b] + t) inv_freq[c],
+ * for the rope_dim / 2 pairs of the first rope_dim elements (a multiple of 16, 0: no
+ * rotation): elements (c, c + rope_dim / 2), or (2c, 2c + 1) when interleaved = 1. The
+ * rest is copied. The angle is exact modulo a turn for every position, in fp32 from there
+ * on; results are rounded once to dt.
+ * In:  q [B,H,T,d] (NULL: no q), k, v [B,Hkv,T,d] with element strides (sequence, head,
+ *      token) strides[0..2], [3..5], [6..8] (HOST; NULL: contiguous), rows of d elements
+ *      contiguous, every row 16-byte aligned: slices of one projection's output do.
+ *      inv_freq: HOST double [rope_dim / 2], finite. frozen: as elsewhere; q rows of
+ *      frozen heads are neither read nor written, and keys of key/value heads that no
+ *      ordinary head reads are not either (k and k_cache may be NULL if that is all).
+ * Out: q_out [B,H,T,d] contiguous (q_out = q only where q is contiguous; else they must
+ *      not overlap), the slots of k_cache and v_cache. Rows without a token, and every
+ *      other slot, stay as they were. Two tokens of one call must not share a slot.
+ * status: DEVICE uint32[2] (see above), for example a paged workspace.
+ *
+ * saf_attn_paged
+ * is the attention of the new tokens over their sequence's cache, after saf_kv_append:
+ * token t of sequence b stands at position i = ctx[b] + t and sees the keys j <= i,
+ * ordinary heads within (window, sinks) as for saf_attn_fwd_window (window = 0: all),
+ * frozen heads with the weights of Eq. 3 at row i (k is not read for them):
+ * ld_prior >= max_len.
+ * In:  q [B,H,T,d]; max_len: an upper bound of ctx[b] + n_new[b], at most
+ *      max_pages * page_size, known on the host: it sets the launch's size.
+ * Out: o [B,H,T,d], lse [B,H,T] as for saf_attn_fwd; o = 0, lse = -inf for rows without
+ *      a token and rows that see no key.
+ * T is 1 for a decoding step, a few for drafted tokens, and may be any length for a
+ * chunk of a prompt. SAF_FP32 is computed in fp32 throughout; sums and softmax statistics
+ * are fp32 in both types.
+ *
+ * saf_attn_paged_shared
+ * is the same for sequences that all begin with one prefix of prefix_len tokens (HOST;
+ * 0: as saf_attn_paged), held once in prefix_pages [ceil(prefix_len / page_size)] (DEVICE
+ * int32): key j < prefix_len is the prefix's slot j, key prefix_len + x slot x of the
+ * sequence's own pages (which begin with a page of their own), and token t stands at
+ * position prefix_len + ctx[b] + t: ctx, n_new and max_len count own tokens, append them
+ * with pos_base = prefix_len. ld_prior >= prefix_len + max_len. The prefix's keys and
+ * values are read for all sequences together.
+ *
+ * workspace: DEVICE, 256-byte aligned, saf_attn_paged_workspace_bytes(...) bytes (enough
+ * for every window and choice of frozen heads; 0 for invalid sizes); it begins with the
+ * status words. Calls that share one must be ordered on one stream, replays of captured
+ * graphs among them.
+ * Errors before any work is enqueued: SAF_EINVAL, SAF_EALIGN, SAF_EWORKSPACE,
+ * SAF_EUNSUPPORTED, SAF_ECUDA as elsewhere (prefix_len + max_len <= 2^30 and B H T <= 2^30,
+ * else SAF_EINVAL). B = 0 or T = 0 is an empty call. */
+SAF_API int saf_kv_append(const void* q, const void* k, const void* v, const int64_t* strides, const int32_t* ctx,
+                          const int32_t* n_new, const int32_t* page_table, int max_pages, const double* inv_freq,
+                          int rope_dim, int interleaved, int64_t pos_base, const uint8_t* frozen, int B, int H,
+                          int Hkv, int T, int d, int num_pages, int page_size, saf_dtype_t dt, void* q_out,
+                          void* k_cache, void* v_cache, uint32_t* status, void* stream);
+SAF_API size_t saf_attn_paged_workspace_bytes(int B, int H, int Hkv, int T, int d, int max_len, int prefix_len,
+                                              saf_dtype_t dt);
+SAF_API int saf_attn_paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                           int max_pages, const int32_t* ctx, const int32_t* n_new, const float* a, const float* r,
+                           int ld_prior, const uint8_t* frozen, int window, int sinks, int B, int H, int Hkv, int T,
+                           int d, int max_len, int num_pages, int page_size, saf_dtype_t dt, void* o, float* lse,
+                           void* workspace, size_t ws_bytes, void* stream);
+SAF_API int saf_attn_paged_shared(const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* prefix_pages, int prefix_len, const int32_t* page_table,
+                                  int max_pages, const int32_t* ctx, const int32_t* n_new, const float* a,
+                                  const float* r, int ld_prior, const uint8_t* frozen, int window, int sinks, int B,
+                                  int H, int Hkv, int T, int d, int max_len, int num_pages, int page_size,
+                                  saf_dtype_t dt, void* o, float* lse, void* workspace, size_t ws_bytes,
+                                  void* stream);
+
 /* Diagnostic forward pass for testing failure detection (the paper has no
  * counterpart; it exercises this library's bounded waits).
  *
@@ -256,8 +375,8 @@ SAF_API int saf_attn_fwd_diag(const void* q, const void* k, const void* v,
                               int withhold, unsigned wait_limit_us);
 
 /* Waits for `stream`, then reads the error word that the kernels of the last
- * call on `workspace` left there. Returns SAF_OK, SAF_ETIMEOUT, or
- * SAF_ECUDA if the stream reported a CUDA error. */
+ * call on `workspace` left there. Returns SAF_OK, SAF_ETIMEOUT, SAF_EPAGE (paged
+ * calls), or SAF_ECUDA if the stream reported a CUDA error. */
 SAF_API int saf_device_status(const void* workspace, void* stream);
 
 /* Static, human-readable text for a status code. Never NULL. */
@@ -383,7 +502,9 @@ typedef enum {
     SAF_KERNEL_DQ_FINISH = 7,   /* dQ accumulator -> dq (scale, dtype, zeros)  */
     SAF_KERNEL_PATTERN_PREP = 8, /* backward: init kernel (clears the status   *
                                   * words; maxima and padded a, r slices)       */
-    SAF_KERNEL_PATTERN_GRAD = 9  /* saf_pattern_grad_tc: all of its launches    */
+    SAF_KERNEL_PATTERN_GRAD = 9, /* saf_pattern_grad_tc: all of its launches    */
+    SAF_KERNEL_KV_APPEND = 10,  /* saf_kv_append                               */
+    SAF_KERNEL_PAGED = 11       /* saf_attn_paged(_shared): all of its launches */
 } saf_kernel_t;
 
 /* From the next call on, record `start` (a cudaEvent_t as void*) on the

@@ -80,6 +80,7 @@ struct BwdParams {
     const uint32_t* hflag; // per head: bit 1 = use the exact form
     uint32_t* status;
     int B, H, Hkv, G, T, Tp;
+    int window, sinks;                 // ordinary heads (kWin kernels)
     int nqb, n_items, n_act_items;
     int n_act, n_pas;                  // key/value heads with / without an ordinary query head
     uint8_t act_kv[SAF_MAX_HEADS];     // the former
@@ -159,7 +160,9 @@ struct Barriers {
 
 // kGrouped = false compiles the multi-head layer (one query head per key/value
 // head) with the group size fixed at 1, so that its loops keep their simple form.
-template <bool kGrouped>
+// kWin: ordinary heads with a sliding window and sinks; their tiles are the query blocks
+// that see a key of the item's block.
+template <bool kGrouped, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1) bwd_tc_kernel(const __grid_constant__ BwdParams p) {
     extern __shared__ uint8_t smem_raw[];
     // 1024-byte aligned base (swizzled tiles), derived from the shared array itself so that
@@ -246,7 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_tc_kernel(const __grid_consta
                     const int bh = it.b * p.H + h;
                     const bool frz = gi >= it.nord;
                     const bool exact = frz && (p.hflag[h] & 2u) != 0;
-                    for (int qb = it.kb; qb < nqb; ++qb) {
+                    const int q_end = it.kb + (frz ? nqb - it.kb : query_blocks<kWin>(it.kb, nqb, p.window, p.sinks, 128));
+                    for (int qb = it.kb; qb < q_end; ++qb) {
                         if (!(ok = mbar_wait(&bars.st_empty[stage], (st_empty_bits >> stage) & 1u, abort, status,
                                              kStatusTimeout)))
                             break;
@@ -328,8 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_tc_kernel(const __grid_consta
                 slot = (slot + 1) % kRing;
                 if (idx < 0) break;
                 const Item it = decode_item(p, idx);
-                const int n = G * (nqb - it.kb);        // tiles of the item
-                const int n_ord = it.nord * (nqb - it.kb);   // its ordinary tiles come first
+                // its ordinary tiles come first
+                const int n_ord = it.nord * query_blocks<kWin>(it.kb, nqb, p.window, p.sinks, 128);
+                const int n = n_ord + (G - it.nord) * (nqb - it.kb);   // tiles of the item
                 if (n_ord > 0) {
                     if (!(ok = mbar_wait(&bars.kv_full, kv_full_ph, abort, status, kStatusTimeout))) break;
                     kv_full_ph ^= 1;
@@ -468,10 +473,12 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_tc_kernel(const __grid_consta
             const Item it = decode_item(p, idx);
             const int bkv = it.b * p.Hkv + it.hk;   // the key/value slice whose dK, dV this item writes
             const int key = it.kb * 128 + j;
-            const int n = G * (nqb - it.kb);
             // tile i: query head gheads[hk G + gi] (ordinary for gi < nord), query block qb
             int gi = 0, qb = it.kb;
-            const int n_ord = it.nord * (nqb - it.kb);   // the ordinary tiles come first
+            const int nq_ord = query_blocks<kWin>(it.kb, nqb, p.window, p.sinks, 128);   // of an ordinary head
+            const int q_last = it.kb + nq_ord - 1;
+            const int n_ord = it.nord * nq_ord;   // the ordinary tiles come first
+            const int n = n_ord + (G - it.nord) * (nqb - it.kb);
             // In the multi-head layer a frozen item's tiles all belong to one head: the factor
             // exp(a[j] - A) of its key rows stays out of W^T and is applied to dV at the end.
             // A group of query heads puts it into each W^T tile instead.
@@ -506,6 +513,9 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_tc_kernel(const __grid_consta
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bars.s_consumed);   // S^T of the next tile may land
+                        // queries from q_far on do not see my key through the window
+                        const bool cut = kWin && window_cuts(qb, it.kb, p.window, 128);
+                        const int q_far = !cut || key < p.sinks ? 128 : key + p.window - qb * 128;
                         // lse * log2(e) of four query columns per (broadcast) shared-memory load
                         const float4* lse4 = reinterpret_cast<const float4*>(vec + 64 * half);
 #pragma unroll
@@ -523,6 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_tc_kernel(const __grid_consta
                                 float p1 = fast_exp2(x.y);
                                 if (diag && j > q0) p0 = 0.f;
                                 if (diag && j > q0 + 1) p1 = 0.f;
+                                if (kWin && q0 >= q_far) p0 = 0.f;
+                                if (kWin && q0 + 1 >= q_far) p1 = 0.f;
                                 pk[(e + u) >> 1] = pack_bf16(p0, p1);
                             }
                         }
@@ -639,11 +651,11 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_tc_kernel(const __grid_consta
                 } else if (i > 0 && i - 1 < n_ord) {
                     const bool first = qb == it.kb;
                     const int bhp = it.b * p.H + p.gheads[it.hk * G + (first ? gi - 1 : gi)];
-                    drain_dq(bhp, first ? nqb - 1 : qb - 1, dsbuf((frz ? gto - 1 : gto) & 1));
+                    drain_dq(bhp, first ? q_last : qb - 1, dsbuf((frz ? gto - 1 : gto) & 1));
                 }
                 pending = stage;
                 stage = (stage + 1) % kStages;
-                if (kGrouped && ++qb == nqb) {   // next query head of the group
+                if (kGrouped && ++qb == (frz ? nqb : q_last + 1)) {   // next query head of the group
                     qb = it.kb;
                     if (++gi >= it.nord && gi < G) exact = (p.hflag[p.gheads[it.hk * G + gi]] & 2u) != 0;
                 }
@@ -652,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_tc_kernel(const __grid_consta
             // all MMAs of this item done: the last dQ, then the dV and dK rows (my 32 d-columns)
             if (!(ok = wait_tile_done())) break;
             if (n > 0 && n - 1 < n_ord)   // the last tile was ordinary
-                drain_dq(it.b * p.H + p.gheads[it.hk * G + G - 1], nqb - 1, dsbuf((gto - 1) & 1));
+                drain_dq(it.b * p.H + p.gheads[it.hk * G + G - 1], q_last, dsbuf((gto - 1) & 1));
             uint32_t dv[32], dk[32];
             tmem_ld32(lane_base + kColDV + 32 * half, dv);
             if (it.nord > 0) tmem_ld32(lane_base + kColDK + 32 * half, dk);
@@ -759,6 +771,8 @@ cudaError_t launch_tc_bwd(const LayerArgs& a, cudaStream_t s) {
     p.T = a.T;
     p.nqb = (a.T + 127) / 128;
     p.Tp = p.nqb * 128;
+    p.window = a.window;
+    p.sinks = a.sinks;
     // per key/value head: its query heads, ordinary first
     for (int hk = 0; hk < Hkv; ++hk) {
         int n = 0;
@@ -784,7 +798,8 @@ cudaError_t launch_tc_bwd(const LayerArgs& a, cudaStream_t s) {
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int smem = Smem::total + 1024;
-    void (*kernel)(BwdParams) = p.G > 1 ? bwd_tc_kernel<true> : bwd_tc_kernel<false>;
+    void (*kernel)(BwdParams) = p.window > 0 ? (p.G > 1 ? bwd_tc_kernel<true, true> : bwd_tc_kernel<false, true>)
+                                             : (p.G > 1 ? bwd_tc_kernel<true, false> : bwd_tc_kernel<false, false>);
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int grid = p.n_items < sms ? p.n_items : sms;

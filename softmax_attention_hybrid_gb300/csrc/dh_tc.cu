@@ -104,6 +104,7 @@ struct DhParams {
     uint32_t* status;
     int B, H, T, d, Tp, nqb;
     int Hkv, G;            // key/value heads; query head h reads key/value head h / G
+    int window, sinks;     // ordinary heads (kWin kernels)
     float scale_log2;      // log2(e) / sqrt(d)
     float scale;           // 1 / sqrt(d)
     HeadMask mask;
@@ -128,6 +129,7 @@ struct FwdBars {
     uint64_t q_full, k_full, k_empty, v_full, v_empty, s_full, p_ready, o_done, mma_idle;
 };
 
+template <bool kWin>
 __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_constant__ DhParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -142,7 +144,9 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
     const int h = bh % p.H;
     const int bkv = (bh / p.H) * p.Hkv + h / p.G;   // key/value slice
     const bool frz = head_frozen(p.mask, h);
-    const int nblk = qb + 1;
+    // the key blocks that the rows see (every causal one for a frozen head)
+    const KeyBlocks<kWin> blocks(qb * 128, qb, kWin && frz ? p.T : p.window, p.sinks, 128);
+    const int nblk = blocks.n;
     if (threadIdx.x == 0) {
         abort_flag = 0;
         mbar_init(&bars.q_full, 1);
@@ -181,12 +185,12 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
                 if (!frz) {
                     if (!mbar_wait(&bars.k_empty, (j & 1) ^ 1u, abort, status, kStatusTimeout)) break;
                     mbar_expect_tx(&bars.k_full, kTile);
-                    load_tile(sm + FwdSmem::k, &p.tm_k, &bars.k_full, j * 128, bkv);
+                    load_tile(sm + FwdSmem::k, &p.tm_k, &bars.k_full, blocks.id(j) * 128, bkv);
                 }
                 if (!mbar_wait(&bars.v_empty, (j & 1) ^ 1u, abort, status, kStatusTimeout)) break;
                 mbar_expect_tx(&bars.v_full, frz ? kTile + 512 + 1024 : kTile);
-                load_tile(sm + FwdSmem::v, &p.tm_v, &bars.v_full, j * 128, bkv);
-                if (frz) {
+                load_tile(sm + FwdSmem::v, &p.tm_v, &bars.v_full, blocks.id(j) * 128, bkv);
+                if (frz) {   // (a frozen head visits block j as its j-th)
                     bulk_load(vec, p.a2p + (size_t)h * p.Tp + (size_t)j * 128, 512, &bars.v_full);
                     bulk_load(vec + 128, p.r2p + (size_t)h * (p.Tp + 256) + (size_t)(qb - j) * 128, 1024,
                               &bars.v_full);
@@ -249,7 +253,14 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
 #pragma unroll
                     for (int e = 0; e < 32; ++e) sv[32 * c4 + e] = __uint_as_float(u[e]) * p.scale_log2;
                 }
-                if (j == qb) {
+                const int kb = blocks.id(j);
+                if (kWin && window_cuts(qb, kb, p.window, 128)) {
+                    // hidden past the diagonal, and before the window unless a sink
+                    const int hi = (qb - kb) * 128 + t, lo = hi - p.window + 1, sink = p.sinks - kb * 128;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c > hi || (c < lo && c >= sink)) sv[c] = -INFINITY;
+                } else if (kb == qb) {
 #pragma unroll
                     for (int c = 0; c < 128; ++c)
                         if (c > t) sv[c] = -INFINITY;
@@ -257,14 +268,17 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
                 float mx = m;
 #pragma unroll
                 for (int c = 0; c < 128; ++c) mx = fmaxf(mx, sv[c]);
+                // a row of a windowed layer that has seen no key yet: weights 2^-inf = 0 with any
+                // finite reference
+                const float m_ref = kWin && mx == -INFINITY ? 0.f : mx;
                 float sum = 0.f;
 #pragma unroll
                 for (int c = 0; c < 128; c += 2) {
-                    const float e0 = fast_exp2(sv[c] - mx), e1 = fast_exp2(sv[c + 1] - mx);
+                    const float e0 = fast_exp2(sv[c] - m_ref), e1 = fast_exp2(sv[c + 1] - m_ref);
                     sum += e0 + e1;
                     pk[c >> 1] = pack_bf16(e0, e1);
                 }
-                const float corr = fast_exp2(m - mx);   // 0 on the first block (m = -inf)
+                const float corr = fast_exp2(m - m_ref);   // 0 on the first block (m = -inf)
                 l = l * corr + sum;
                 // P(j - 1) V has been added before O is rescaled (S(j) was computed after it,
                 // so its columns are free for P(j) already)
@@ -390,6 +404,7 @@ struct KvBars {
     uint64_t kv_full, st_full[2], st_empty[2], sdp_full, pds_ready, tile_done, mma_idle;
 };
 
+template <bool kWin>
 __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_constant__ DhParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -402,10 +417,15 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
     const int kb = (int)blockIdx.x;
     const int bkv = blockIdx.y;                        // key/value slice
     const int b = bkv / p.Hkv, h0 = (bkv - b * p.Hkv) * p.G;   // its query heads: h0 .. h0 + G - 1
-    const int nq = p.nqb - kb;                         // query tiles per query head
-    const int ntiles = p.G * nq;
+    // query tiles per query head: those that see a key of the block through a window
+    const int nq_frz = p.nqb - kb, nq_ord = query_blocks<kWin>(kb, p.nqb, p.window, p.sinks, 128);
+    int ntiles = 0;
     bool any_ord = false, any_frz = false;
-    for (int gi = 0; gi < p.G; ++gi) (head_frozen(p.mask, h0 + gi) ? any_frz : any_ord) = true;
+    for (int gi = 0; gi < p.G; ++gi) {
+        const bool frz = head_frozen(p.mask, h0 + gi);
+        (frz ? any_frz : any_ord) = true;
+        ntiles += kWin && !frz ? nq_ord : nq_frz;
+    }
     if (threadIdx.x == 0) {
         abort_flag = 0;
         mbar_init(&bars.kv_full, 1);
@@ -439,7 +459,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                 const int qb = kb + qi, s = i & 1;
                 const int h = h0 + gi, bh = b * p.H + h;
                 const bool frz = head_frozen(p.mask, h);
-                if (++qi == nq) {
+                if (++qi == (kWin && !frz ? nq_ord : nq_frz)) {
                     qi = 0;
                     ++gi;
                 }
@@ -467,7 +487,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                 for (int i = 0, gi = 0, qi = 0; i < ntiles && ok; ++i) {
                     const int s = i & 1;
                     const bool frz = M == 0 ? false : M == 1 ? true : head_frozen(p.mask, h0 + gi);
-                    if (++qi == nq) {
+                    if (++qi == (kWin && !frz ? nq_ord : nq_frz)) {
                         qi = 0;
                         ++gi;
                     }
@@ -523,8 +543,10 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                 const bool diag = qi == 0;   // the query head's first tile: query block kb
                 const int h = h0 + gi;
                 const bool frz = M == 0 ? false : M == 1 ? true : head_frozen(p.mask, h);
+                // queries of the tile from q_far on do not see my key through the window
+                const int q_far = !kWin || key < p.sinks ? 128 : t + p.window - qi * 128;
                 if (frz && diag) a2k = p.a2p[(size_t)h * p.Tp + key];   // in flight during the wait below
-                if (++qi == nq) {
+                if (++qi == (kWin && !frz ? nq_ord : nq_frz)) {
                     qi = 0;
                     ++gi;
                 }
@@ -551,6 +573,8 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                             float p1 = fast_exp2(__uint_as_float(su[e + 1]) * p.scale_log2 - vec[q0 + 1]);
                             if (diag && q0 < t) p0 = 0.f;
                             if (diag && q0 + 1 < t) p1 = 0.f;
+                            if (kWin && q0 >= q_far) p0 = 0.f;
+                            if (kWin && q0 + 1 >= q_far) p1 = 0.f;
                             const float d0 = p0 * (__uint_as_float(du[e]) - vec[128 + q0]);
                             const float d1 = p1 * (__uint_as_float(du[e + 1]) - vec[128 + q0 + 1]);
                             pk[e >> 1] = pack_bf16(p0, p1);
@@ -641,6 +665,7 @@ struct QBars {
     uint64_t q_full, st_full[2], st_empty[2], sdp_full, ds_ready, tile_done, mma_idle;
 };
 
+template <bool kWin>
 __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_constant__ DhParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -665,7 +690,8 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_c
         }
         return;
     }
-    const int nblk = qb + 1;
+    const KeyBlocks<kWin> blocks(qb * 128, qb, p.window, p.sinks, 128);   // the key blocks that the rows see
+    const int nblk = blocks.n;
     if (threadIdx.x == 0) {
         abort_flag = 0;
         mbar_init(&bars.q_full, 1);
@@ -700,8 +726,8 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_c
                 if (!mbar_wait(&bars.st_empty[s], ((j >> 1) & 1) ^ 1u, abort, status, kStatusTimeout)) break;
                 uint8_t* st = sm + QSmem::st + s * QSmem::st_bytes;
                 mbar_expect_tx(&bars.st_full[s], 2 * kTile);
-                load_tile(st + QSmem::st_k, &p.tm_k, &bars.st_full[s], j * 128, bkv);
-                load_tile(st + QSmem::st_v, &p.tm_v, &bars.st_full[s], j * 128, bkv);
+                load_tile(st + QSmem::st_k, &p.tm_k, &bars.st_full[s], blocks.id(j) * 128, bkv);
+                load_tile(st + QSmem::st_v, &p.tm_v, &bars.st_full[s], blocks.id(j) * 128, bkv);
             }
         }
     } else if (warp == 9) {
@@ -745,6 +771,9 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_c
         for (int j = 0; j < nblk; ++j) {
             if (!(ok = mbar_wait(&bars.sdp_full, j & 1, abort, status, kStatusTimeout))) break;
             tc_fence_after();
+            // keys of the block before k_near are hidden by the window unless they are sinks
+            const int kb = blocks.id(j);
+            const int k_near = kWin ? (qb - kb) * 128 + t - p.window + 1 : 0, sink = p.sinks - kb * 128;
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
                 const int c4 = 2 * half + cc;   // chunk of 32 keys
@@ -757,8 +786,10 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_c
                     const int k0 = 32 * c4 + e;
                     float p0 = fast_exp2(__uint_as_float(su[e]) * p.scale_log2 - l2);
                     float p1 = fast_exp2(__uint_as_float(su[e + 1]) * p.scale_log2 - l2);
-                    if (j == qb && k0 > t) p0 = 0.f;
-                    if (j == qb && k0 + 1 > t) p1 = 0.f;
+                    if (kb == qb && k0 > t) p0 = 0.f;
+                    if (kb == qb && k0 + 1 > t) p1 = 0.f;
+                    if (kWin && k0 < k_near && k0 >= sink) p0 = 0.f;
+                    if (kWin && k0 + 1 < k_near && k0 + 1 >= sink) p1 = 0.f;
                     dk[e >> 1] = pack_bf16(p0 * (__uint_as_float(du[e]) - dd), p1 * (__uint_as_float(du[e + 1]) - dd));
                 }
                 tmem_st16(lane_base + 32 * c4, dk);   // chunk c4's own columns, already read
@@ -807,6 +838,8 @@ DhParams make_params(const LayerArgs& a) {
     p.rowvec = a.rowvec;
     p.Hkv = a.Hkv > 0 ? a.Hkv : a.H;
     p.G = a.H / p.Hkv;
+    p.window = a.window;
+    p.sinks = a.sinks;
     return p;
 }
 
@@ -827,10 +860,11 @@ cudaError_t launch_dh_fwd(const LayerArgs& a, cudaStream_t s) {
     p.o = (__nv_bfloat16*)a.out;
     p.lse = a.lse_out;
     const int smem = FwdSmem::total + 1024;
-    cudaError_t e = cudaFuncSetAttribute(dh_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    void (*kernel)(DhParams) = a.window > 0 ? dh_fwd_kernel<true> : dh_fwd_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     before_launch(SAF_KERNEL_FWD, s);
-    e = launch_ex(dh_fwd_kernel, dim3((unsigned)p.nqb, (unsigned)(a.B * a.H)), dim3(kThreads), (size_t)smem, s,
+    e = launch_ex(kernel, dim3((unsigned)p.nqb, (unsigned)(a.B * a.H)), dim3(kThreads), (size_t)smem, s,
                   true, 1, p);
     after_launch(SAF_KERNEL_FWD, s);
     return e;
@@ -851,16 +885,18 @@ cudaError_t launch_dh_bwd(const LayerArgs& a, cudaStream_t s) {
     after_launch(SAF_KERNEL_BWD_DELTA, s);
     if (e != cudaSuccess) return e;
     const int smem_kv = KvSmem::total + 1024, smem_q = QSmem::total + 1024;
-    e = cudaFuncSetAttribute(dh_bwd_kv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(dh_bwd_q_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
+    void (*kv_kernel)(DhParams) = a.window > 0 ? dh_bwd_kv_kernel<true> : dh_bwd_kv_kernel<false>;
+    void (*q_kernel)(DhParams) = a.window > 0 ? dh_bwd_q_kernel<true> : dh_bwd_q_kernel<false>;
+    e = cudaFuncSetAttribute(kv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(q_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
     if (e != cudaSuccess) return e;
     before_launch(SAF_KERNEL_BWD_KV, s);
-    e = launch_ex(dh_bwd_kv_kernel, dim3((unsigned)p.nqb, (unsigned)(a.B * p.Hkv)), dim3(kThreadsBwd),
+    e = launch_ex(kv_kernel, dim3((unsigned)p.nqb, (unsigned)(a.B * p.Hkv)), dim3(kThreadsBwd),
                   (size_t)smem_kv, s, true, 1, p);
     after_launch(SAF_KERNEL_BWD_KV, s);
     if (e != cudaSuccess) return e;
     before_launch(SAF_KERNEL_BWD_Q, s);
-    e = launch_ex(dh_bwd_q_kernel, grid, dim3(kThreadsBwd), (size_t)smem_q, s, true, 1, p);
+    e = launch_ex(q_kernel, grid, dim3(kThreadsBwd), (size_t)smem_q, s, true, 1, p);
     after_launch(SAF_KERNEL_BWD_Q, s);
     return e;
 }

@@ -82,6 +82,7 @@ struct FwdParams {
     int slice_group;   // (batch, head) slices per item group
     unsigned long long wait_ns;   // limit of every bounded wait (kWaitLimitNs unless a diagnostic call sets it)
     int withhold;      // diagnostic: the producer publishes no work item, so every waiter gives up
+    int window, sinks;   // ordinary heads (kWin kernels)
     int n_ord, n_frz;
     uint8_t ord_heads[SAF_MAX_HEADS];
     uint8_t frz_heads[SAF_MAX_HEADS];
@@ -153,6 +154,18 @@ struct Barriers {
     uint64_t mma_idle[2];   // every MMA issuer g issued has completed (before TMEM is freed)
 };
 
+// The key blocks of an item: for ordinary items of a windowed layer those that the rows of
+// its two tiles see (tile 0's last one is the last but one), else every causal block.
+template <bool kWin>
+__device__ __forceinline__ KeyBlocks<kWin> item_blocks(const FwdParams& p, const Item& it) {
+    const int qb0 = 2 * it.pair, last = qb0 + 1 < p.nqb ? qb0 + 1 : qb0;
+    // (a frozen item has no window: one that reaches past every key)
+    return KeyBlocks<kWin>(qb0 * 128, last, kWin && it.frozen ? p.T : p.window, p.sinks, 128);
+}
+
+// kWin: ordinary heads with a sliding window and sinks. Its instance visits the visible key
+// blocks only and masks those that the window cuts; the other one is the layer without.
+template <bool kWin>
 __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_constant__ FwdParams p) {
     extern __shared__ uint8_t smem_raw[];
     // 1024-byte aligned base (swizzled tiles), derived from the shared array itself so that
@@ -242,7 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
                 const int bkv = it.b * p.Hkv + it.h / p.G;   // the key/value slice this head reads
                 const int qb0 = 2 * it.pair, qb1 = qb0 + 1;
                 const bool t1 = qb1 < p.nqb;
-                const int nblk = t1 ? qb1 + 1 : qb0 + 1;
+                const KeyBlocks<kWin> blocks = item_blocks<kWin>(p, it);
+                const int nblk = blocks.n;
                 const bool exact = it.frozen && (p.hflag[it.h] & 2u) != 0;
                 if (!it.frozen) {
                     // the next item's Q goes to the other slot while this CTA may still work
@@ -257,7 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
                     tma_load_3d(sq, &p.tm_q, &bars.q_full[qs], 0, qb0 * 128, bh);
                     if (t1) tma_load_3d(sq + kTileBytes, &p.tm_q, &bars.q_full[qs], 0, qb1 * 128, bh);
                 }
-                for (int j = 0; j < nblk; ++j) {
+                for (int jj = 0; jj < nblk; ++jj) {
+                    const int j = blocks.id(jj);
                     if (!(ok = mbar_wait(&bars.kv_empty[stage], (kv_empty_bits >> stage) & 1u, abort, status,
                                          kStatusTimeout, p.wait_ns)))
                         break;
@@ -311,8 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
                 const Item it = decode_item(p, idx);
                 const int qb0 = 2 * it.pair, qb1 = qb0 + 1;
                 const bool t1 = qb1 < p.nqb;
-                const int ng = g == 0 ? qb0 + 1 : (t1 ? qb1 + 1 : 0);   // key blocks of my tile
-                const int nblk = t1 ? qb1 + 1 : qb0 + 1;                 // key blocks of the item
+                const int nblk = item_blocks<kWin>(p, it).n;                  // key blocks of the item
+                const int ng = g == 0 ? (t1 ? nblk - 1 : nblk) : (t1 ? nblk : 0);   // of my tile
                 if (!it.frozen) {
                     qs = nord++ & 1;
                     if (!(ok = mbar_wait_warp(&bars.q_full[qs], (q_full_bits >> qs) & 1u, abort, status, kStatusTimeout, p.wait_ns)))
@@ -452,14 +467,15 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
             slot = (slot + 1) % kRing;
             if (idx < 0) break;
             const Item it = decode_item(p, idx);
-            const int item_blocks = (2 * it.pair + 1 < p.nqb) ? 2 * it.pair + 2 : 2 * it.pair + 1;
+            const KeyBlocks<kWin> blocks = item_blocks<kWin>(p, it);
             const int gblk0 = gblk;
-            gblk += item_blocks;
+            gblk += blocks.n;
             const int qb = 2 * it.pair + g;
             if (qb >= p.nqb) continue;
             const int bh = it.b * p.H + it.h;
             const int row = qb * 128 + r;
-            const int nblk = qb + 1;
+            // tile 0 of a pair ends one block before tile 1
+            const int nblk = blocks.n - (g == 0 && qb + 1 < p.nqb ? 1 : 0);
             if (!it.frozen) {
                 float m_used = -INFINITY, l = 0.f;
                 for (int j = 0; j < nblk && ok; ++j) {
@@ -473,7 +489,16 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.s_empty[g]);
-                    if (j == qb) {
+                    const int kb = blocks.id(j);
+                    if (kWin && window_cuts(qb, kb, p.window, 128)) {
+                        // key c of the block is hidden past the diagonal, and before the window
+                        // unless it is a sink
+                        const int lo = (qb - kb) * 128 + r - p.window + 1, hi = (qb - kb) * 128 + r;
+                        const int sink = p.sinks - kb * 128;
+#pragma unroll
+                        for (int c = 0; c < 128; ++c)
+                            if (c > hi || (c < lo && c >= sink)) sr[c] = __float_as_uint(-INFINITY);
+                    } else if (kb == qb) {
                         // causal mask on the diagonal tile: keys c > r are dropped
 #pragma unroll
                         for (int c = 0; c < 128; ++c)
@@ -497,7 +522,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
                     // P = 2^(S log2(e) / sqrt(d) - m), two columns per FFMA and per FADD, packed
                     // into registers while the previous block's P V may still run
                     const float2 sc2 = make_float2(kScaleLog2, kScaleLog2);
-                    const float2 nm2 = make_float2(-m_used, -m_used);
+                    // a row of a windowed layer that has seen no key yet has no maximum: its weights
+                    // are 2^-inf = 0 with any finite reference
+                    const float m_ref = kWin && m_used == -INFINITY ? 0.f : m_used;
+                    const float2 nm2 = make_float2(-m_ref, -m_ref);
                     float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
                     uint32_t pk[64];   // packed bf16 pairs of the row's 128 columns of P
 #pragma unroll
@@ -686,6 +714,8 @@ cudaError_t launch_tc_fwd(const LayerArgs& a, cudaStream_t s) {
     p.slice_group = kv_all <= kL2GroupBytes ? a.B * a.H : kSliceGroup;
     p.wait_ns = a.diag_wait_ns ? a.diag_wait_ns : kWaitLimitNs;
     p.withhold = a.diag_withhold;
+    p.window = a.window;
+    p.sinks = a.sinks;
     for (int h = 0; h < a.H; ++h) {
         if (head_frozen(a.mask, h))
             p.frz_heads[p.n_frz++] = (uint8_t)h;
@@ -696,18 +726,19 @@ cudaError_t launch_tc_fwd(const LayerArgs& a, cudaStream_t s) {
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int smem = SmemLayout::total + 1024;
-    cudaError_t e = cudaFuncSetAttribute(fwd_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    void (*kernel)(FwdParams) = a.window > 0 ? fwd_tc_kernel<true> : fwd_tc_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // The register split inside the kernel draws on the registers the launch hands out: a
     // build that launches with fewer than kRegsLaunch per thread is refused here, since the
     // softmax warpgroups could then never obtain theirs.
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, fwd_tc_kernel);
+    e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess) return e;
     if (2 * 128 * kRegsSoftmax + 128 * kRegsOther > kThreads * fa.numRegs) return cudaErrorInvalidConfiguration;
     const int grid = p.n_items < sms ? p.n_items : sms;
     before_launch(SAF_KERNEL_FWD, s);
-    e = launch_ex(fwd_tc_kernel, dim3(grid), dim3(kThreads), smem, s, true, 1, p);
+    e = launch_ex(kernel, dim3(grid), dim3(kThreads), smem, s, true, 1, p);
     after_launch(SAF_KERNEL_FWD, s);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();

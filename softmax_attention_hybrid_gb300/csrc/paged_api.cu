@@ -1,0 +1,282 @@
+// Host side of attention over a paged cache (saf_attn_paged, saf_attn_paged_shared):
+// argument checks, the split of the keys over work items, the workspace, and the kernel
+// that joins the items of a row.
+#include <string.h>
+
+#include "paged.h"
+
+namespace saf {
+namespace {
+
+constexpr int kSms = 152;   // GB300
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Items that one call aims at. More items fill the GPU better and level sequences of
+// different lengths; fewer leave less to join.
+constexpr int kItemsSimt = kSms * 6;
+
+// One warp per row: the row's items, then its output.
+template <typename E, int D>
+__global__ void __launch_bounds__(128) join_kernel(const float2* __restrict__ ml, const float* __restrict__ po,
+                                                   E* __restrict__ o, float* __restrict__ lse, long long rows,
+                                                   int nsplit) {
+    grid_dep_wait();   // the items are done
+    grid_dep_launch();
+    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    const float2* r = ml + row * nsplit;
+    float M = -INFINITY;
+    for (int c = lane; c < nsplit; c += 32) M = fmaxf(M, r[c].x);
+    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    constexpr int N = D / 32;
+    float acc[N];
+#pragma unroll
+    for (int c = 0; c < N; ++c) acc[c] = 0.f;
+    float l = 0.f;
+    if (M > -INFINITY)
+        for (int c0 = 0; c0 < nsplit; c0 += 32) {
+            const float2 e = c0 + lane < nsplit ? r[c0 + lane] : make_float2(-INFINITY, 0.f);
+            const float w = exp2f(e.x - M);
+            l += w * e.y;
+            const int n = min(32, nsplit - c0);
+            for (int u = 0; u < n; ++u) {
+                const float wu = __shfl_sync(0xffffffffu, w, u);
+                if (wu == 0.f) continue;   // an item whose keys the row does not see wrote no output
+                const float* src = po + (row * nsplit + c0 + u) * D + lane;
+#pragma unroll
+                for (int c = 0; c < N; ++c) acc[c] = fmaf(wu, src[32 * c], acc[c]);
+            }
+        }
+    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int c = 0; c < N; ++c) from_f(o + row * D + lane + 32 * c, acc[c] * inv);
+    if (lane == 0) lse[row] = l > 0.f ? (M + log2f(l)) * kLn2 : -INFINITY;
+}
+
+template <typename E>
+cudaError_t launch_join(const PagedArgs& p, cudaStream_t s) {
+    const long long rows = (long long)p.B * p.H * p.T;
+    const dim3 grid((unsigned)((rows + 3) / 4));
+    auto go = [&](auto kernel) {
+        return launch_ex(kernel, grid, dim3(128), 0, s, true, 1, (const float2*)p.ml, (const float*)p.po, (E*)p.o,
+                         p.lse, rows, p.nsplit);
+    };
+    switch (p.d) {
+        case 96: return go(join_kernel<E, 96>);
+        case 128: return go(join_kernel<E, 128>);
+        default: return go(join_kernel<E, 64>);
+    }
+}
+
+long long ceil_div(long long x, long long y) { return (x + y - 1) / y; }
+
+struct Plan {
+    int tile, rows;
+    int nrb[2];
+    long long units[2];    // (sequence, key/value head, row block) triples
+    long long tiles[2];    // key tiles of one of them, at most, without a window
+    long long target;      // items aimed at
+    long long max_split;   // items of a row, at most, whatever the window
+};
+
+Plan make_plan(int B, int H, int Hkv, int T, int max_len, int P) {
+    Plan x;
+    x.tile = kSimtTile;
+    x.rows = kSimtRows;
+    x.target = kItemsSimt;
+    const long long G = H / Hkv;
+    const long long rb[2] = {P > 0 ? ceil_div(G * B * T, x.rows) : 0, ceil_div(G * T, x.rows)};
+    x.units[0] = rb[0] * Hkv;
+    x.units[1] = rb[1] * Hkv * B;
+    x.tiles[0] = ceil_div(P, x.tile);
+    x.tiles[1] = ceil_div(max_len, x.tile);
+    x.max_split = 0;
+    for (int i = 0; i < 2; ++i) {
+        x.nrb[i] = (int)rb[i];
+        if (x.units[i] == 0) continue;
+        const long long c = ceil_div(x.target, x.units[i]);
+        x.max_split += c < x.tiles[i] ? c : x.tiles[i];
+    }
+    return x;
+}
+
+// The items: both parts' tiles in equal shares of `per` tiles, so that about
+// `target` items come out; a part then has ceil(tiles / per) <= ceil(target / units)
+// items along the keys (the bound that the workspace is sized by).
+void set_items(PagedArgs& p, const Plan& x, int nfrozen) {
+    long long nt[2] = {x.tiles[0], x.tiles[1]};
+    if (p.window > 0 && nfrozen == 0) {
+        // a block's rows stand within T positions in part 1 and past the prefix in part 0:
+        // the tiles that hold window + T - 1 consecutive keys, and those of the sinks
+        const long long span[2] = {p.window, (long long)p.window + p.T - 1};
+        for (int i = 0; i < 2; ++i) {
+            const long long off = i ? p.P : 0;
+            const long long sinks = p.sinks > off ? p.sinks - off : 0;
+            const long long n = ceil_div(span[i], x.tile) + 1 + ceil_div(sinks, x.tile);
+            if (n < nt[i]) nt[i] = n;
+        }
+    }
+    const long long total = x.units[0] * nt[0] + x.units[1] * nt[1];
+    const long long per = total > x.target ? ceil_div(total, x.target) : 1;
+    for (int i = 0; i < 2; ++i) {
+        p.nrb[i] = x.nrb[i];
+        p.per_chunk[i] = (int)per;
+        p.chunks[i] = x.units[i] ? (int)ceil_div(nt[i], per) : 0;
+    }
+    p.tile = x.tile;
+    p.rows = x.rows;
+    p.nsplit = p.chunks[0] + p.chunks[1];
+    p.items0 = x.units[0] * p.chunks[0];
+    p.items = p.items0 + x.units[1] * p.chunks[1];
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t workspace_bytes(const Plan& x, int B, int H, int T, int d, size_t* po_off) {
+    const size_t rows = (size_t)B * H * T;
+    const size_t ml = align256(rows * (size_t)x.max_split * sizeof(float2));
+    if (po_off) *po_off = kStatusBytes + ml;
+    if (x.max_split <= 1) return kStatusBytes;
+    return kStatusBytes + ml + align256(rows * (size_t)x.max_split * d * sizeof(float));
+}
+
+bool power_of_two(int n) { return n > 0 && (n & (n - 1)) == 0; }
+bool aligned(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// Sizes, in the order of the workspace query and of both calls.
+int check_sizes(int B, int H, int Hkv, int T, int d, int max_len, int prefix_len, saf_dtype_t dt) {
+    if (B < 0 || H <= 0 || T < 0 || H > SAF_MAX_HEADS || Hkv <= 0 || H % Hkv != 0) return SAF_EINVAL;
+    if (dt != SAF_BF16 && dt != SAF_FP32) return SAF_EINVAL;
+    if (!head_dim_supported(d, dt)) return SAF_EUNSUPPORTED;
+    if (max_len < 1 || prefix_len < 0 || (long long)max_len + prefix_len > (1ll << 30)) return SAF_EINVAL;
+    if ((long long)B * H * T > (1ll << 30)) return SAF_EINVAL;
+    return SAF_OK;
+}
+
+int paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* prefix_pages, int prefix_len,
+          const int32_t* page_table, int max_pages, const int32_t* ctx, const int32_t* n_new, const float* a,
+          const float* r, int ld_prior, const uint8_t* frozen, int window, int sinks, int B, int H, int Hkv, int T,
+          int d, int max_len, int num_pages, int page_size, saf_dtype_t dt, void* o, float* lse, void* workspace,
+          size_t ws_bytes, void* stream) {
+    int st = check_sizes(B, H, Hkv, T, d, max_len, prefix_len, dt);
+    if (st != SAF_OK) return st;
+    if (window < 0 || sinks < 0) return SAF_EINVAL;
+    if (B == 0 || T == 0) return SAF_OK;
+    if (!power_of_two(page_size) || page_size < 8 || page_size > 1024) return SAF_EINVAL;
+    if (num_pages < 1 || max_pages < 1 || (long long)num_pages * Hkv > 0x7fffffffll) return SAF_EINVAL;
+    if (max_len > (long long)max_pages * page_size) return SAF_EINVAL;
+    PagedArgs p;
+    memset(&p, 0, sizeof(p));
+    const int G = H / Hkv;
+    int nfrozen = 0;
+    for (int hk = 0; hk < Hkv; ++hk) {   // a group's ordinary query heads first
+        int n = 0;
+        for (int pass = 0; pass < 2; ++pass)
+            for (int gi = 0; gi < G; ++gi) {
+                const int h = hk * G + gi;
+                if ((frozen && frozen[h]) == (pass == 1)) p.gheads[hk * G + n++] = (uint8_t)h;
+            }
+        int f = 0;
+        for (int gi = 0; gi < G; ++gi)
+            if (frozen && frozen[hk * G + gi]) {
+                p.mask.w[(hk * G + gi) >> 6] |= 1ull << ((hk * G + gi) & 63);
+                ++f;
+            }
+        p.gord[hk] = (uint8_t)(G - f);
+        nfrozen += f;
+    }
+    if (!v_cache || !page_table || !ctx || !o || !lse || (prefix_len > 0 && !prefix_pages)) return SAF_EINVAL;
+    if (nfrozen < H && (!q || !k_cache)) return SAF_EINVAL;
+    if (nfrozen > 0 && (!a || !r || ld_prior < prefix_len + max_len)) return SAF_EINVAL;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
+        !aligned(a, 4) || !aligned(r, 4) || !aligned(page_table, 4) || !aligned(prefix_pages, 4) ||
+        !aligned(ctx, 4) || !aligned(n_new, 4))
+        return SAF_EALIGN;
+    if (!workspace) return SAF_EWORKSPACE;
+    if (!aligned(workspace, 256)) return SAF_EALIGN;
+    const Plan plan = make_plan(B, H, Hkv, T, max_len, prefix_len);
+    size_t po_off;
+    if (ws_bytes < workspace_bytes(plan, B, H, T, d, &po_off)) return SAF_EWORKSPACE;
+    if ((st = check_device()) != SAF_OK) return st;
+
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.prefix_pages = prefix_pages;
+    p.page_table = page_table;
+    p.ctx = ctx;
+    p.n_new = n_new;
+    p.a = a;
+    p.r = r;
+    p.o = o;
+    p.lse = lse;
+    p.status = (uint32_t*)workspace;
+    p.ml = (float2*)((char*)workspace + kStatusBytes);
+    p.po = (float*)((char*)workspace + po_off);
+    p.B = B;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.G = G;
+    p.T = T;
+    p.d = d;
+    p.ld = ld_prior;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    while ((1 << p.page_log2) < page_size) ++p.page_log2;
+    p.P = prefix_len;
+    p.max_len = max_len;
+    p.window = window >= prefix_len + max_len ? 0 : window;   // a window that reaches every key is none
+    p.sinks = sinks < prefix_len + max_len ? sinks : prefix_len + max_len;
+    p.scale_log2 = 1.4426950408889634f / sqrtf((float)d);
+    set_items(p, plan, nfrozen);
+    if (p.items > 0x7fffffffll) return SAF_EINVAL;
+
+    cudaStream_t s = (cudaStream_t)stream;
+    const bool bf16 = dt == SAF_BF16;
+    before_launch(SAF_KERNEL_PAGED, s);
+    cudaError_t e = launch_paged_simt(p, bf16, s);
+    if (e == cudaSuccess && p.nsplit > 1) {
+        note_launch();
+        e = bf16 ? launch_join<__nv_bfloat16>(p, s) : launch_join<float>(p, s);
+    }
+    after_launch(SAF_KERNEL_PAGED, s);
+    return launch_status(e);
+}
+
+}  // namespace
+}  // namespace saf
+
+using namespace saf;
+
+extern "C" {
+
+size_t saf_attn_paged_workspace_bytes(int B, int H, int Hkv, int T, int d, int max_len, int prefix_len,
+                                      saf_dtype_t dt) {
+    if (check_sizes(B, H, Hkv, T, d, max_len, prefix_len, dt) != SAF_OK) return 0;
+    if (B == 0 || T == 0) return kStatusBytes;
+    return workspace_bytes(make_plan(B, H, Hkv, T, max_len, prefix_len), B, H, T, d, nullptr);
+}
+
+int saf_attn_paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table, int max_pages,
+                   const int32_t* ctx, const int32_t* n_new, const float* a, const float* r, int ld_prior,
+                   const uint8_t* frozen, int window, int sinks, int B, int H, int Hkv, int T, int d, int max_len,
+                   int num_pages, int page_size, saf_dtype_t dt, void* o, float* lse, void* workspace,
+                   size_t ws_bytes, void* stream) {
+    return paged(q, k_cache, v_cache, nullptr, 0, page_table, max_pages, ctx, n_new, a, r, ld_prior, frozen, window,
+                 sinks, B, H, Hkv, T, d, max_len, num_pages, page_size, dt, o, lse, workspace, ws_bytes, stream);
+}
+
+int saf_attn_paged_shared(const void* q, const void* k_cache, const void* v_cache, const int32_t* prefix_pages,
+                          int prefix_len, const int32_t* page_table, int max_pages, const int32_t* ctx,
+                          const int32_t* n_new, const float* a, const float* r, int ld_prior, const uint8_t* frozen,
+                          int window, int sinks, int B, int H, int Hkv, int T, int d, int max_len, int num_pages,
+                          int page_size, saf_dtype_t dt, void* o, float* lse, void* workspace, size_t ws_bytes,
+                          void* stream) {
+    return paged(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, max_pages, ctx, n_new, a, r, ld_prior,
+                 frozen, window, sinks, B, H, Hkv, T, d, max_len, num_pages, page_size, dt, o, lse, workspace,
+                 ws_bytes, stream);
+}
+
+}  // extern "C"

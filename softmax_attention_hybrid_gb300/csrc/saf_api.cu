@@ -48,7 +48,7 @@ WorkspaceLayout workspace_layout(int B, int H, int T, int backward, int bf16) {
 }
 
 namespace {
-constexpr int kNumKernelIds = SAF_KERNEL_PATTERN_GRAD + 1;
+constexpr int kNumKernelIds = SAF_KERNEL_PAGED + 1;
 cudaEvent_t g_trace_start[kNumKernelIds] = {};
 cudaEvent_t g_trace_stop[kNumKernelIds] = {};
 unsigned long long g_launches = 0;
@@ -70,8 +70,8 @@ void after_launch(int kernel, cudaStream_t s) {
 }
 
 namespace {
-
 int g_device_ok = -1;  // cached: 1 = sm_103 device present, 0 = not
+}  // namespace
 
 int check_device() {
     if (g_device_ok >= 0) return g_device_ok ? SAF_OK : SAF_EUNSUPPORTED;
@@ -88,6 +88,14 @@ int check_device() {
     g_device_ok = (prop.major == 10 && prop.minor == 3) ? 1 : 0;
     return g_device_ok ? SAF_OK : SAF_EUNSUPPORTED;
 }
+
+int launch_status(cudaError_t e) {
+    if (e == cudaSuccess) return SAF_OK;
+    cudaGetLastError();
+    return SAF_ELAUNCH;
+}
+
+namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -154,12 +162,6 @@ LayerArgs make_args(const void* q, const void* k, const void* v, const float* a,
     p.erp = bf16 ? (float*)(ws + L.erp) : nullptr;
     p.invz = bf16 ? (float*)(ws + L.invz) : nullptr;
     return p;
-}
-
-int launch_status(cudaError_t e) {
-    if (e == cudaSuccess) return SAF_OK;
-    cudaGetLastError();
-    return SAF_ELAUNCH;
 }
 
 // The kernels that run before the main kernel of a pass. The first one
@@ -365,6 +367,11 @@ cudaError_t clear_call(const LayerArgs& ws_view, bool bf16, cudaStream_t s) {
     memset(&q.mask, 0, sizeof(q.mask));
     return launch_call_init(q, false, bf16, s);
 }
+// A window that reaches every key is none: the call then runs the layer's own kernels.
+void set_window(LayerArgs& p, int window, int sinks) {
+    p.window = window >= p.T ? 0 : window;
+    p.sinks = sinks < p.T ? sinks : p.T;
+}
 }  // namespace
 }  // namespace saf
 
@@ -436,6 +443,77 @@ int saf_attn_bwd_prepared(const void* q, const void* k, const void* v, const voi
     return launch_status(e);
 }
 
+// ---------------------------------------------------------------------------
+// The layer with a sliding window and sinks on its ordinary heads.
+// ---------------------------------------------------------------------------
+
+int saf_attn_fwd_window(const void* q, const void* k, const void* v, const float* a, const float* r, int ld_prior,
+                        const uint8_t* frozen, const void* state, int window, int sinks, int B, int H, int Hkv, int T,
+                        int d, saf_dtype_t dt, void* o, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+    if (Hkv <= 0 || H <= 0 || H % Hkv != 0 || window < 0 || sinks < 0) return SAF_EINVAL;
+    Common c;
+    int st = validate(q, k, v, a, r, ld_prior, frozen, B, H, T, d, dt, workspace, ws_bytes, 0, &c);
+    if (st != SAF_OK) return st;
+    if (B == 0 || T == 0) return SAF_OK;
+    if (!o || !lse) return SAF_EINVAL;
+    if (!aligned16(o) || !aligned16(lse)) return SAF_EALIGN;
+    if (state && ((uintptr_t)state & 255u) != 0) return SAF_EALIGN;
+    if ((st = check_device()) != SAF_OK) return st;
+    cudaStream_t s = (cudaStream_t)stream;
+    const bool bf16 = dt == SAF_BF16;
+    LayerArgs p = make_args(q, k, v, a, r, ld_prior, B, H, T, c, workspace, 0, bf16);
+    p.Hkv = Hkv;
+    p.d = d;
+    p.out = o;
+    p.lse_out = lse;
+    set_window(p, window, sinks);
+    cudaError_t e = state ? clear_call(p, bf16, s) : begin_call(p, c, false, bf16, s);
+    if (state) use_state(p, state, H, T, bf16);
+    if (e == cudaSuccess)
+        e = !bf16 ? launch_simt_fwd(p, false, s) : d == kHeadDim ? launch_tc_fwd(p, s) : launch_dh_fwd(p, s);
+    return launch_status(e);
+}
+
+int saf_attn_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dO, const float* lse,
+                        const float* a, const float* r, int ld_prior, const uint8_t* frozen, const void* state,
+                        int window, int sinks, int B, int H, int Hkv, int T, int d, saf_dtype_t dt, void* dq, void* dk,
+                        void* dv, void* workspace, size_t ws_bytes, void* stream) {
+    if (Hkv <= 0 || H <= 0 || H % Hkv != 0 || window < 0 || sinks < 0) return SAF_EINVAL;
+    Common c;
+    int st = validate(q, k, v, a, r, ld_prior, frozen, B, H, T, d, dt, workspace, ws_bytes, 1, &c);
+    if (st != SAF_OK) return st;
+    if (B == 0 || T == 0) return SAF_OK;
+    if (!o || !dO || !lse || !dq || !dk || !dv) return SAF_EINVAL;
+    if (!aligned16(o) || !aligned16(dO) || !aligned16(lse) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+        return SAF_EALIGN;
+    if (state && ((uintptr_t)state & 255u) != 0) return SAF_EALIGN;
+    if ((st = check_device()) != SAF_OK) return st;
+    cudaStream_t s = (cudaStream_t)stream;
+    const bool bf16 = dt == SAF_BF16;
+    LayerArgs p = make_args(q, k, v, a, r, ld_prior, B, H, T, c, workspace, 1, bf16);
+    p.Hkv = Hkv;
+    p.d = d;
+    p.o = o;
+    p.dO = dO;
+    p.lse = lse;
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    set_window(p, window, sinks);
+    cudaError_t e = state ? clear_call(p, bf16, s) : begin_call(p, c, true, bf16, s);
+    if (state) use_state(p, state, H, T, bf16);
+    if (bf16 && d != kHeadDim) {
+        if (e == cudaSuccess) e = launch_dh_bwd(p, s);
+    } else if (bf16) {
+        if (e == cudaSuccess) e = launch_bwd_prep(p, s, !state);
+        if (e == cudaSuccess) e = launch_tc_bwd(p, s);
+    } else {
+        if (e == cudaSuccess && c.nfrozen < H) e = launch_bwd_delta(p, false, s);
+        if (e == cudaSuccess) e = launch_simt_bwd(p, false, s);
+    }
+    return launch_status(e);
+}
+
 int saf_device_status(const void* workspace, void* stream) {
     if (!workspace) return SAF_EWORKSPACE;
     cudaStream_t s = (cudaStream_t)stream;
@@ -446,6 +524,7 @@ int saf_device_status(const void* workspace, void* stream) {
         return SAF_ECUDA;
     }
     if (words[0] & kStatusTimeout) return SAF_ETIMEOUT;
+    if (words[0] & kStatusPage) return SAF_EPAGE;
     return SAF_OK;
 }
 
@@ -460,6 +539,7 @@ const char* saf_error_string(int status) {
         case SAF_ETIMEOUT: return "a bounded device wait expired";
         case SAF_ECUDA: return "CUDA runtime error";
         case SAF_ESCRATCH: return "problem too large for the 8 MiB fixed scratch of saf_attn_fwd_noalloc";
+        case SAF_EPAGE: return "a page or a token count of a paged call is outside its bounds";
         default: return "unknown status";
     }
 }

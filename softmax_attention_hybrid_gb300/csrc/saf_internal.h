@@ -89,6 +89,7 @@ enum : uint32_t {
 // per-head flags (hflag[h]): bit 0 the normaliser prep needed its exact
 // fallback, bit 1 the tensor-core kernels must use the exact form
     kStatusTimeout = 1u << 1,   // a bounded mbarrier wait expired
+    kStatusPage = 1u << 2,      // paged calls: a page or a token count outside its bounds
 };
 constexpr size_t kStatusBytes = 256;
 constexpr int kCounterBwd = 8;
@@ -143,12 +144,54 @@ struct LayerArgs {
     int B, H, T, ld_prior;
     int Hkv;             // key/value heads: query head h reads key/value head h / (H / Hkv)
     int d;               // head dimension
+    // ordinary heads: query i sees the keys j <= i with i - j < window or j < sinks
+    // (window 0: every j <= i); 0 < window < T otherwise. Frozen heads are not cut.
+    int window, sinks;
     HeadMask mask;
     // diagnostic forward only (saf_attn_fwd_diag): a shorter limit for every bounded
     // wait (0: the default), and a producer that withholds every work item
     unsigned long long diag_wait_ns;
     int diag_withhold;
 };
+
+// The key blocks that a run of query rows sees through a sliding window with sinks, for
+// blocks of `blk` keys: blocks [0, n_sink) hold sinks, blocks [lo, last] the window. Block
+// jj of the n visited ones is id(jj); without a window they are 0 .. last.
+template <bool kWin>
+struct KeyBlocks {
+    int n, n_sink, lo;
+    // q0: the run's first row; last: the key block of its last row
+    __device__ __forceinline__ KeyBlocks(int q0, int last, int window, int sinks, int blk) {
+        n = last + 1;
+        n_sink = lo = 0;
+        if (kWin) {
+            const int first = q0 - window + 1;   // the first row's first key
+            lo = first > 0 ? first / blk : 0;
+            n_sink = min((sinks + blk - 1) / blk, lo);
+            n = n_sink + last + 1 - lo;
+        }
+    }
+    __device__ __forceinline__ int id(int jj) const { return !kWin || jj < n_sink ? jj : lo + jj - n_sink; }
+};
+
+// Query blocks (of `blk` rows) that see a key of block kb through the window or as a sink:
+// kb .. kb + n - 1 of nqb.
+template <bool kWin>
+__device__ __forceinline__ int query_blocks(int kb, int nqb, int window, int sinks, int blk) {
+    if (!kWin || kb * blk < sinks) return nqb - kb;
+    const long long last = ((long long)kb * blk + blk - 1 + window - 1) / blk;   // of the block's last key
+    return (last < nqb - 1 ? (int)last : nqb - 1) - kb + 1;
+}
+
+// Whether a tile of query block qb and key block kb holds a pair that the window may hide
+// (the diagonal is masked apart from this).
+__device__ __forceinline__ bool window_cuts(int qb, int kb, int window, int blk) {
+    return (qb - kb) * blk + blk - 1 >= window;
+}
+
+// saf_api.cu: SAF_OK on an sm_103 device, else the error to return; a launch's result as a status.
+int check_device();
+int launch_status(cudaError_t e);
 
 // Launch bookkeeping (saf_api.cu): call before_launch(kernel id, stream)
 // right before a launch and after_launch(...) right after it; they count

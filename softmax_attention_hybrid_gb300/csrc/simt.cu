@@ -12,6 +12,9 @@
 //              and a query-block pass (dQ for ordinary heads), as App. D.2
 //              describes; frozen heads get dV = W^T dO and exact-zero dQ, dK.
 //
+// kWin instances serve ordinary heads with a sliding window and sinks: they visit the key
+// (query) blocks that some row of the block sees and hide the other pairs.
+//
 // Tile: 64 query rows x 64 keys, head dimension D = 64, 96 or 128, 256
 // threads. Thread (ty, tx), ty = tid / 16, tx = tid % 16, owns rows
 // 4*ty .. 4*ty+3 and the columns tx, tx+16, ... of the key axis (4 of them)
@@ -40,6 +43,12 @@ __device__ __forceinline__ void load_tile(float* s, const E* g, int r0, int T) {
     }
 }
 
+// Whether query i of an ordinary head sees key j <= i.
+template <bool kWin>
+__device__ __forceinline__ bool in_window(const LayerArgs& p, int i, int j) {
+    return !kWin || i - j < p.window || j < p.sinks;
+}
+
 __device__ __forceinline__ float quad16_max(float x) {
     for (int o = 1; o < 16; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
     return x;
@@ -52,7 +61,7 @@ __device__ __forceinline__ float quad16_sum(float x) {
 // ---------------------------------------------------------------------------
 // Forward. Grid (ceil(T/64), B*H).
 // ---------------------------------------------------------------------------
-template <typename E, int D>
+template <typename E, int D, bool kWin>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
     extern __shared__ float sm[];
     float* Qs = sm;
@@ -88,7 +97,9 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
         for (int c = 0; c < NC; ++c) acc[i][c] = 0.f;
     }
 
-    for (int kb = 0; kb <= qb; ++kb) {
+    const KeyBlocks<kWin> blocks(q0, qb, kWin && frozen ? T : p.window, p.sinks, kB);
+    for (int jj = 0; jj < blocks.n; ++jj) {
+        const int kb = blocks.id(jj);
         __syncthreads();
         if (!frozen) load_tile<D>(Ks, k, kb * kB, T);
         load_tile<D>(Vs, v, kb * kB, T);
@@ -110,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
                     const float* kr = Ks + (tx + 16 * c) * LdD;
 #pragma unroll 16
                     for (int e = 0; e < D; ++e) dot = fmaf(qr[e], kr[e], dot);
-                    s[i][c] = (key <= row && key < T) ? dot * scale : -INFINITY;
+                    s[i][c] = (key <= row && key < T && in_window<kWin>(p, row, key)) ? dot * scale : -INFINITY;
                 }
             }
         }
@@ -119,11 +130,13 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
             for (int i = 0; i < 4; ++i) {
                 float mx = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
                 const float mnew = fmaxf(m[i], quad16_max(mx));
-                const float corr = expf(m[i] - mnew);
+                // a row of a windowed layer that has seen no key yet: any finite reference
+                const float ref = kWin && mnew == -INFINITY ? 0.f : mnew;
+                const float corr = expf(m[i] - ref);
                 float ls = 0.f;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    s[i][c] = expf(s[i][c] - mnew);
+                    s[i][c] = expf(s[i][c] - ref);
                     ls += s[i][c];
                 }
                 l[i] = l[i] * corr + quad16_sum(ls);
@@ -170,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
 // query blocks qb >= kb, so that the slice's dV and dK are group sums formed
 // without atomics. Thread rows = keys.
 // ---------------------------------------------------------------------------
-template <typename E, int D>
+template <typename E, int D, bool kWin>
 __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
     extern __shared__ float sm[];
     constexpr int LdD = D + 1, NC = D / 16, kT = tile_floats<D>();
@@ -212,7 +225,8 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
     const E* dO = (const E*)p.dO + base;
     const float* a = p.a + (size_t)h * p.ld_prior;
     const float* r = p.r + (size_t)h * p.ld_prior;
-    for (int qb = kb; qb < nqb; ++qb) {
+    const int q_end = kb + (kWin && frozen ? nqb - kb : query_blocks<kWin>(kb, nqb, p.window, p.sinks, kB));
+    for (int qb = kb; qb < q_end; ++qb) {
         const int q0 = qb * kB;
         __syncthreads();
         if (!frozen) load_tile<D>(Qs, q, q0, T);
@@ -249,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
                         dot = fmaf(kr[e], qr[e], dot);
                         dpt = fmaf(vr[e], gr[e], dpt);
                     }
-                    pt = ok ? expf(dot * scale - rowstat[qq]) : 0.f;
+                    pt = ok && in_window<kWin>(p, qi, key) ? expf(dot * scale - rowstat[qq]) : 0.f;
                     dst = pt * (dpt - rowD[qq]);
                 }
                 Pt[(ty * 4 + i) * kLd + qq] = pt;
@@ -297,7 +311,7 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
 // Backward, query-block pass (dQ). Grid (ceil(T/64), B*H). Frozen heads
 // write zeros.
 // ---------------------------------------------------------------------------
-template <typename E, int D>
+template <typename E, int D, bool kWin>
 __global__ void __launch_bounds__(kThreads) bwd_q_kernel(LayerArgs p) {
     extern __shared__ float sm[];
     constexpr int LdD = D + 1, NC = D / 16, kT = tile_floats<D>();
@@ -339,7 +353,9 @@ __global__ void __launch_bounds__(kThreads) bwd_q_kernel(LayerArgs p) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc[i][c] = 0.f;
     }
-    for (int kb = 0; kb <= qb; ++kb) {
+    const KeyBlocks<kWin> blocks(q0, qb, p.window, p.sinks, kB);
+    for (int jj = 0; jj < blocks.n; ++jj) {
+        const int kb = blocks.id(jj);
         __syncthreads();
         load_tile<D>(Ks, k, kb * kB, T);
         load_tile<D>(Vs, v, kb * kB, T);
@@ -360,7 +376,7 @@ __global__ void __launch_bounds__(kThreads) bwd_q_kernel(LayerArgs p) {
                     dot = fmaf(qr[e], kr[e], dot);
                     dp = fmaf(gr[e], vr[e], dp);
                 }
-                const bool ok = key <= row && row < T;
+                const bool ok = key <= row && row < T && in_window<kWin>(p, row, key);
                 const float pij = ok ? expf(dot * scale - lse[i]) : 0.f;
                 dSs[(ty * 4 + i) * kLd + tx + 16 * c] = pij * (dp - Dr[i]);
             }
@@ -400,36 +416,46 @@ cudaError_t launch(K kernel, int id, int tiles, const LayerArgs& p, cudaStream_t
     return cudaGetLastError();
 }
 
-template <typename E, int D>
+template <typename E, int D, bool kWin>
 cudaError_t fwd_d(const LayerArgs& p, cudaStream_t s) {
-    return launch<D>(fwd_kernel<E, D>, SAF_KERNEL_FWD, 4, p, s, p.B * p.H);
+    return launch<D>(fwd_kernel<E, D, kWin>, SAF_KERNEL_FWD, 4, p, s, p.B * p.H);
 }
 
-template <typename E, int D>
+template <typename E, int D, bool kWin>
 cudaError_t bwd_d(const LayerArgs& p, cudaStream_t s) {
-    cudaError_t e = launch<D>(bwd_kv_kernel<E, D>, SAF_KERNEL_BWD_KV, 6, p, s, p.B * p.Hkv);
+    cudaError_t e = launch<D>(bwd_kv_kernel<E, D, kWin>, SAF_KERNEL_BWD_KV, 6, p, s, p.B * p.Hkv);
     if (e != cudaSuccess) return e;
-    return launch<D>(bwd_q_kernel<E, D>, SAF_KERNEL_BWD_Q, 5, p, s, p.B * p.H);
+    return launch<D>(bwd_q_kernel<E, D, kWin>, SAF_KERNEL_BWD_Q, 5, p, s, p.B * p.H);
+}
+
+template <bool kWin>
+cudaError_t fwd_f32(const LayerArgs& p, cudaStream_t s) {
+    switch (p.d) {
+        case 96: return fwd_d<float, 96, kWin>(p, s);
+        case 128: return fwd_d<float, 128, kWin>(p, s);
+        default: return fwd_d<float, 64, kWin>(p, s);
+    }
+}
+
+template <bool kWin>
+cudaError_t bwd_f32(const LayerArgs& p, cudaStream_t s) {
+    switch (p.d) {
+        case 96: return bwd_d<float, 96, kWin>(p, s);
+        case 128: return bwd_d<float, 128, kWin>(p, s);
+        default: return bwd_d<float, 64, kWin>(p, s);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_simt_fwd(const LayerArgs& p, bool bf16, cudaStream_t s) {
-    if (bf16) return fwd_d<__nv_bfloat16, 64>(p, s);
-    switch (p.d) {
-        case 96: return fwd_d<float, 96>(p, s);
-        case 128: return fwd_d<float, 128>(p, s);
-        default: return fwd_d<float, 64>(p, s);
-    }
+    if (bf16) return fwd_d<__nv_bfloat16, 64, false>(p, s);
+    return p.window > 0 ? fwd_f32<true>(p, s) : fwd_f32<false>(p, s);
 }
 
 cudaError_t launch_simt_bwd(const LayerArgs& p, bool bf16, cudaStream_t s) {
-    if (bf16) return bwd_d<__nv_bfloat16, 64>(p, s);
-    switch (p.d) {
-        case 96: return bwd_d<float, 96>(p, s);
-        case 128: return bwd_d<float, 128>(p, s);
-        default: return bwd_d<float, 64>(p, s);
-    }
+    if (bf16) return bwd_d<__nv_bfloat16, 64, false>(p, s);
+    return p.window > 0 ? bwd_f32<true>(p, s) : bwd_f32<false>(p, s);
 }
 
 }  // namespace saf

@@ -28,6 +28,7 @@ SAF_EWORKSPACE = -5
 SAF_ETIMEOUT = -6
 SAF_ECUDA = -8
 SAF_ESCRATCH = -9
+SAF_EPAGE = -10
 
 # Every symbol that include/saf.h declares.
 EXPORTED = ("saf_attn_workspace_bytes", "saf_attn_fwd", "saf_attn_bwd", "saf_device_status",
@@ -36,7 +37,9 @@ EXPORTED = ("saf_attn_workspace_bytes", "saf_attn_fwd", "saf_attn_bwd", "saf_dev
             "saf_pattern_grad", "saf_attn_fwd_gqa", "saf_attn_bwd_gqa", "saf_fit_stats_workspace_bytes",
             "saf_fit_target_stats", "saf_fit_from_target_workspace_bytes", "saf_fit_from_target",
             "saf_attn_fwd_diag", "saf_frozen_state_bytes", "saf_frozen_prepare", "saf_attn_fwd_prepared",
-            "saf_attn_bwd_prepared", "saf_pattern_grad_tc_workspace_bytes", "saf_pattern_grad_tc")
+            "saf_attn_bwd_prepared", "saf_pattern_grad_tc_workspace_bytes", "saf_pattern_grad_tc",
+            "saf_attn_fwd_window", "saf_attn_bwd_window", "saf_kv_append", "saf_attn_paged_workspace_bytes",
+            "saf_attn_paged", "saf_attn_paged_shared")
 
 SAF_KERNEL_NONE = 0
 SAF_KERNEL_LOGNORM = 1
@@ -48,6 +51,8 @@ SAF_KERNEL_BWD = 6
 SAF_KERNEL_DQ_FINISH = 7
 SAF_KERNEL_PATTERN_PREP = 8
 SAF_KERNEL_PATTERN_GRAD = 9
+SAF_KERNEL_KV_APPEND = 10
+SAF_KERNEL_PAGED = 11
 
 
 class SafError(RuntimeError):
@@ -114,6 +119,22 @@ def _load():
     lib.saf_pattern_grad_tc_workspace_bytes.restype = sz
     lib.saf_pattern_grad_tc.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, i, i, i, i, vp, vp, vp, sz, vp]
     lib.saf_pattern_grad_tc.restype = i
+    lib.saf_attn_fwd_window.argtypes = [vp, vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp, sz, vp]
+    lib.saf_attn_fwd_window.restype = i
+    lib.saf_attn_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp,
+                                        vp, sz, vp]
+    lib.saf_attn_bwd_window.restype = i
+    lib.saf_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, vp, i, i, ctypes.c_int64, vp, i, i, i, i, i, i, i, i,
+                                  vp, vp, vp, vp, vp]
+    lib.saf_kv_append.restype = i
+    lib.saf_attn_paged_workspace_bytes.argtypes = [i, i, i, i, i, i, i, i]
+    lib.saf_attn_paged_workspace_bytes.restype = sz
+    lib.saf_attn_paged.argtypes = [vp, vp, vp, vp, i, vp, vp, vp, vp, i, vp, i, i, i, i, i, i, i, i, i, i, i, vp, vp,
+                                   vp, sz, vp]
+    lib.saf_attn_paged.restype = i
+    lib.saf_attn_paged_shared.argtypes = [vp, vp, vp, vp, i, vp, i, vp, vp, vp, vp, i, vp, i, i, i, i, i, i, i, i, i,
+                                          i, i, vp, vp, vp, sz, vp]
+    lib.saf_attn_paged_shared.restype = i
     return lib
 
 
@@ -355,6 +376,244 @@ def saf_attn_bwd_prepared(q, k, v, o, do, lse, a, r, frozen, state, dq=None, dk=
     if st != SAF_OK:
         raise SafError(st, "saf_attn_bwd_prepared")
     return dq, dk, dv
+
+
+def _on(t, dev, dtype=None, name="tensor"):
+    """Address of an optional contiguous tensor on device `dev`."""
+    if t is None:
+        return None
+    if t.device != dev:
+        raise ValueError(f"{name} must live on {dev}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _cuda(t):
+    if not t.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    return t.device
+
+
+def _flags(frozen, H):
+    """The frozen flags as H bytes; a bytes object is passed on as it is."""
+    if frozen is None:
+        return None
+    if isinstance(frozen, bytes):
+        if len(frozen) != H:
+            raise ValueError("frozen mask must have H entries")
+        return frozen
+    return bytes(_frozen_bytes(frozen, H))
+
+
+def _run(where, dev, stream, fn, *args):
+    """Call fn(*args, stream) with `dev` current, on `stream` or the device's current one."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _run(where, dev, stream, fn, *args)
+    st = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    if st != SAF_OK:
+        raise SafError(st, where)
+
+
+def _prior(a, r, H, dev, need):
+    """Addresses and row length of a, r ([H, ld_prior] fp32, or None when nothing is frozen)."""
+    if a is None or r is None:
+        return None, None, need
+    if a.dim() != 2 or a.shape != r.shape or a.shape[0] != H:
+        raise ValueError("a and r must both be [H, ld_prior]")
+    return _on(a, dev, torch.float32, "a"), _on(r, dev, torch.float32, "r"), a.shape[1]
+
+
+def saf_attn_fwd_window(q, k, v, a, r, frozen, window, sinks=0, state=None, o=None, lse=None, workspace=None,
+                        stream=None):
+    """Forward of the layer whose ordinary heads see the last `window` keys and the first
+    `sinks` (query i: keys j <= i with i - j < window or j < sinks; window 0: every key);
+    returns (o, lse). q: [B, H, T, d]; k, v: [B, Hkv, T, d]; a, r, frozen as for
+    saf_attn_fwd_gqa; state: a prepared frozen-pattern state (saf_frozen_prepare) or None."""
+    dev = _cuda(v)
+    B, H, Hkv, T, d = _gqa_shape(q, v, frozen)
+    dt, f32 = v.dtype, torch.float32
+    _same_shapes(("q", q, (B, H, T, d)), ("k", k, v.shape), ("o", o, (B, H, T, d)), ("lse", lse, (B, H, T)))
+    if o is None:
+        o = torch.empty((B, H, T, d), dtype=dt, device=dev)
+    if lse is None:
+        lse = torch.empty((B, H, T), dtype=f32, device=dev)
+    if workspace is None:
+        workspace = alloc_workspace(B, H, T, d, dt, False, dev)
+    ap, rp, ld = _prior(a, r, H, dev, T)
+    _run("saf_attn_fwd_window", dev, stream, _lib.saf_attn_fwd_window, _on(q, dev, dt, "q"), _on(k, dev, dt, "k"),
+         _on(v, dev), ap, rp, ld, _flags(frozen, H), _on(state, dev, torch.uint8, "state"), int(window), int(sinks), B,
+         H, Hkv, T, d, _dt(v), _on(o, dev, dt, "o"), _on(lse, dev, f32, "lse"),
+         _on(workspace, dev, torch.uint8, "workspace"), workspace.numel())
+    return o, lse
+
+
+def saf_attn_bwd_window(q, k, v, o, do, lse, a, r, frozen, window, sinks=0, state=None, dq=None, dk=None, dv=None,
+                        workspace=None, stream=None):
+    """Backward of saf_attn_fwd_window (o, lse: its outputs for the same inputs); returns
+    dq [B, H, T, d] and dk, dv [B, Hkv, T, d]."""
+    dev = _cuda(v)
+    B, H, Hkv, T, d = _gqa_shape(q, v, frozen)
+    dt, f32 = v.dtype, torch.float32
+    full = (B, H, T, d)
+    _same_shapes(("q", q, full), ("k", k, v.shape), ("o", o, full), ("do", do, full), ("lse", lse, (B, H, T)),
+                 ("dq", dq, full), ("dk", dk, v.shape), ("dv", dv, v.shape))
+    dq = torch.empty(full, dtype=dt, device=dev) if dq is None else dq
+    dk = torch.empty(v.shape, dtype=dt, device=dev) if dk is None else dk
+    dv = torch.empty(v.shape, dtype=dt, device=dev) if dv is None else dv
+    if workspace is None:
+        workspace = alloc_workspace(B, H, T, d, dt, True, dev)
+    ap, rp, ld = _prior(a, r, H, dev, T)
+    _run("saf_attn_bwd_window", dev, stream, _lib.saf_attn_bwd_window, _on(q, dev, dt, "q"), _on(k, dev, dt, "k"),
+         _on(v, dev), _on(o, dev, dt, "o"), _on(do, dev, dt, "do"), _on(lse, dev, f32, "lse"), ap, rp, ld,
+         _flags(frozen, H), _on(state, dev, torch.uint8, "state"), int(window), int(sinks), B, H, Hkv, T, d, _dt(v),
+         _on(dq, dev, dt, "dq"), _on(dk, dev, dt, "dk"), _on(dv, dev, dt, "dv"),
+         _on(workspace, dev, torch.uint8, "workspace"), workspace.numel())
+    return dq, dk, dv
+
+
+def _same_shapes(*given):
+    for name, t, shape in given:
+        if t is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _counts(ctx, n_new, page_table, B, dev):
+    """Addresses of the int32 counts and the page table of B sequences."""
+    _same_shapes(("ctx", ctx, (B,)), ("n_new", n_new, (B,)))
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, max_pages]")
+    i32 = torch.int32
+    return _on(ctx, dev, i32, "ctx"), _on(n_new, dev, i32, "n_new"), _on(page_table, dev, i32, "page_table")
+
+
+def _caches(k_cache, v_cache, d, dt, dev):
+    if v_cache.dim() != 4 or v_cache.shape[3] != d:
+        raise ValueError("the caches must be [num_pages, Hkv, page_size, d]")
+    _same_shapes(("k_cache", k_cache, v_cache.shape))
+    return _on(k_cache, dev, dt, "k_cache"), _on(v_cache, dev, dt, "v_cache")
+
+
+def _rows(t, dev, dt, name):
+    """Address and (sequence, head, token) strides of a [B, heads, T, d] tensor with contiguous rows."""
+    if t.device != dev:
+        raise ValueError(f"{name} must live on {dev}")
+    if t.dtype != dt:
+        raise TypeError(f"{name} must be {dt}")
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), s[:3]
+
+
+def saf_kv_append(k, v, k_cache, v_cache, page_table, ctx, n_new=None, q=None, q_out=None, inv_freq=None,
+                  interleaved=False, pos_base=0, frozen=None, status=None, stream=None):
+    """Write the new tokens' k, v [B, Hkv, T, d] (any strides with contiguous rows) into the
+    paged caches [num_pages, Hkv, page_size, d] at slots ctx[b] + t of page_table [B, max_pages],
+    with the rotary rotation of k, and of q [B, H, T, d] into q_out; returns q_out (None
+    without q). ctx, n_new: int32 [B] on the device (n_new None: T tokens each).
+    inv_freq: rope_dim / 2 angles per position (CPU float64 tensor or a sequence; None: no
+    rotation). frozen: flags of the H query heads (their q, and keys that no ordinary head
+    reads, are left alone); without q it also gives H (default Hkv). status: an int32 or uint8
+    CUDA tensor whose first 8 bytes, zeroed once by the caller, collect errors for
+    saf_device_status; by default none are kept."""
+    dev, dt = _cuda(v), v.dtype
+    B, Hkv, T, d = v.shape
+    H = q.shape[1] if q is not None else len(frozen) if frozen is not None else Hkv
+    _same_shapes(("k", k, v.shape), ("q", q, (B, H, T, d)), ("q_out", q_out, (B, H, T, d)))
+    ctxp, newp, table = _counts(ctx, n_new, page_table, B, dev)
+    kc, vc = _caches(k_cache, v_cache, d, dt, dev)
+    if v_cache.shape[1] != Hkv:
+        raise ValueError("the caches' heads are not v's")
+    none = (None, (0, 0, 0))
+    qp, qs = _rows(q, dev, dt, "q") if q is not None else none
+    kp, ks = _rows(k, dev, dt, "k") if k is not None else none
+    vp, vs = _rows(v, dev, dt, "v")
+    if q is not None and q_out is None:
+        # rows that are not written (frozen heads, rows without a token) come back as zeros
+        q_out = torch.zeros((B, H, T, d), dtype=dt, device=dev)
+    freq, rope = None, 0
+    if inv_freq is not None:
+        freq = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
+        rope = 2 * freq.numel()
+    if status is None:
+        status = torch.zeros(2, dtype=torch.int32, device=dev)
+    elif status.numel() * status.element_size() < 8:
+        raise ValueError("status needs 8 bytes")
+    _run("saf_kv_append", dev, stream, _lib.saf_kv_append, qp, kp, vp, _I64x9(*qs, *ks, *vs), ctxp, newp, table,
+         page_table.shape[1], freq.data_ptr() if rope else None, rope, int(bool(interleaved)), int(pos_base),
+         _flags(frozen, H), B, H, Hkv, T, d, v_cache.shape[0], v_cache.shape[2], _dt(v),
+         _on(q_out, dev, dt, "q_out"), kc, vc, _on(status, dev, None, "status"))
+    return q_out
+
+
+_I64x9 = ctypes.c_int64 * 9
+
+
+def saf_attn_paged_workspace_bytes(B, H, Hkv, T, d, max_len, dtype, prefix_len=0) -> int:
+    dt = SAF_BF16 if dtype in (torch.bfloat16, SAF_BF16, "bf16") else SAF_FP32
+    return int(_lib.saf_attn_paged_workspace_bytes(B, H, Hkv, T, d, int(max_len), int(prefix_len), dt))
+
+
+def alloc_paged_workspace(B, H, Hkv, T, d, max_len, dtype, prefix_len=0, device="cuda"):
+    """A workspace for saf_attn_paged / saf_attn_paged_shared with cleared status words."""
+    n = saf_attn_paged_workspace_bytes(B, H, Hkv, T, d, max_len, dtype, prefix_len)
+    w = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    w[:256].zero_()
+    return w
+
+
+def _paged(where, q, k_cache, v_cache, prefix, page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o, lse,
+           workspace, stream):
+    dev, dt = _cuda(q), q.dtype
+    B, H, T, d = q.shape
+    kc, vc = _caches(k_cache, v_cache, d, dt, dev)
+    num_pages, Hkv, page_size, _ = v_cache.shape
+    ctxp, newp, table = _counts(ctx, n_new, page_table, B, dev)
+    _same_shapes(("o", o, (B, H, T, d)), ("lse", lse, (B, H, T)))
+    P = 0
+    if prefix is not None:
+        pages, P = prefix[0], int(prefix[1])
+        if pages is not None and pages.numel() < -(-P // page_size):
+            raise ValueError("prefix_pages holds fewer pages than prefix_len tokens take")
+        prefix = (_on(pages, dev, torch.int32, "prefix_pages"), P)
+    else:
+        prefix = ()
+    if o is None:
+        o = torch.empty((B, H, T, d), dtype=dt, device=dev)
+    if lse is None:
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = alloc_paged_workspace(B, H, Hkv, T, d, max_len, dt, P, dev)
+    ap, rp, ld = _prior(a, r, H, dev, P + max_len)
+    _run(where, dev, stream, getattr(_lib, where), _on(q, dev, dt, "q"), kc, vc, *prefix, table, page_table.shape[1],
+         ctxp, newp, ap, rp, ld, _flags(frozen, H), int(window), int(sinks), B, H, Hkv, T, d, int(max_len), num_pages,
+         page_size, _dt(q), _on(o, dev, dt, "o"), _on(lse, dev, torch.float32, "lse"),
+         _on(workspace, dev, torch.uint8, "workspace"), workspace.numel())
+    return o, lse
+
+
+def saf_attn_paged(q, k_cache, v_cache, page_table, ctx, max_len, n_new=None, a=None, r=None, frozen=None, window=0,
+                   sinks=0, o=None, lse=None, workspace=None, stream=None):
+    """Attention of the newest tokens q [B, H, T, d] over the paged caches
+    [num_pages, Hkv, page_size, d]; returns (o, lse). Token t of sequence b stands at position
+    ctx[b] + t; rows t >= n_new[b] come back as o = 0, lse = -inf. max_len: an upper bound of
+    ctx[b] + n_new[b]. a, r [H, ld_prior >= max_len] and frozen as for saf_attn_fwd; window and
+    sinks as for saf_attn_fwd_window. workspace: alloc_paged_workspace."""
+    return _paged("saf_attn_paged", q, k_cache, v_cache, None, page_table, ctx, max_len, n_new, a, r, frozen, window,
+                  sinks, o, lse, workspace, stream)
+
+
+def saf_attn_paged_shared(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, ctx, max_len, n_new=None, a=None,
+                          r=None, frozen=None, window=0, sinks=0, o=None, lse=None, workspace=None, stream=None):
+    """saf_attn_paged for sequences that share a prefix of prefix_len tokens, held once in the
+    pages prefix_pages (int32, on the device): token t of sequence b stands at position
+    prefix_len + ctx[b] + t, and ctx, n_new, max_len and page_table count own tokens."""
+    return _paged("saf_attn_paged_shared", q, k_cache, v_cache, (prefix_pages, prefix_len), page_table, ctx, max_len,
+                  n_new, a, r, frozen, window, sinks, o, lse, workspace, stream)
 
 
 def saf_set_trace_events(kernel: int, start=None, stop=None) -> None:

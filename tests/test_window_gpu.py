@@ -1,0 +1,213 @@
+"""GPU parity of the layer with a sliding window and sinks (saf_attn_fwd_window,
+saf_attn_bwd_window) against the fp64 reference, with bounds from tests/_bounds.py.
+
+Sizes where it can go wrong: windows of one key, around a tile's edge and longer than
+several tiles, sinks inside and across the first tile and behind the window, lengths of one
+token, a full tile and odd ones, groups with and without frozen heads.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving_oracle as so
+from softmax_attention_hybrid_gb300.inputs import custom_workload, make_gqa_inputs
+from tests import _bounds
+
+pytestmark = pytest.mark.gpu
+
+# (T, window, sinks)
+SPANS = [(1, 1, 0), (1, 5, 3), (2, 1, 0), (64, 7, 0), (127, 1, 1), (129, 128, 0), (130, 127, 4), (257, 1, 0),
+         (300, 64, 4), (385, 129, 130), (513, 100, 300), (640, 256, 0), (700, 333, 1), (701, 2, 700)]
+
+
+@pytest.fixture(scope="module")
+def saf():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from softmax_attention_hybrid_gb300 import saf as mod
+    return mod
+
+
+def _inputs(dtype, B, H, Hkv, T, d, frozen, seed):
+    w = custom_workload(B, H, T, d=d, dtype=dtype, frozen=frozen, scale=1.0, slope=0.03)
+    x = make_gqa_inputs(w, Hkv, seed=seed)
+    g = {n: x[n].cuda() for n in ("q", "k", "v", "do", "a", "r")}
+    return x, g
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _run(saf, g, frozen, window, sinks, **kw):
+    o, lse = saf.saf_attn_fwd_window(g["q"], g["k"], g["v"], g["a"], g["r"], frozen, window, sinks, **kw)
+    dq = torch.full_like(g["q"], 7.0)
+    dq, dk, dv = saf.saf_attn_bwd_window(g["q"], g["k"], g["v"], o, g["do"], lse, g["a"], g["r"], frozen, window,
+                                         sinks, dq=dq, **kw)
+    return {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
+
+
+def _check(dtype, x, out, frozen, window, sinks):
+    """Ordinary heads and the groups without a frozen head, against the reference."""
+    q, k, v, do, a, r = (_np(x[n]) for n in ("q", "k", "v", "do", "a", "r"))
+    B, H, T, d = q.shape
+    Hkv = k.shape[1]
+    G = H // Hkv
+    got = {n: _np(t) for n, t in out.items()}
+    assert all(np.isfinite(t).all() for t in got.values())
+    u = _bounds.HALF[dtype]
+    i = np.arange(T)
+    for b in range(B):
+        for hk in range(Hkv):
+            tk, tv = np.zeros((T, d)), np.zeros((T, d))
+            dk, dv = np.zeros((T, d)), np.zeros((T, d))
+            for h in range(hk * G, hk * G + G):
+                if frozen[h]:
+                    assert not got["dq"][b, h].any()
+                    continue
+                W, lse = so.row_weights(q[b, h], k[b, hk], i, a[h], r[h], False, window, sinks)
+                o = W @ v[b, hk]
+                s = _bounds.logit_error(q[b, h], k[b, hk], a[h], r[h], i, False)
+                o_tol, l_tol = _bounds.fwd(dtype, W, v[b, hk], o, lse, s)
+                assert (np.abs(got["o"][b, h] - o) <= o_tol).all()
+                assert (np.abs(got["lse"][b, h] - lse) <= l_tol).all()
+                dW = do[b, h] @ v[b, hk].T
+                dS = W * (dW - (W * dW).sum(axis=1, keepdims=True)) / np.sqrt(d)
+                tq, tk1, tv1 = _bounds.bwd(dtype, W, q[b, h], k[b, hk], v[b, hk], do[b, h], o, o_tol, s)
+                dq = dS @ k[b, hk]
+                assert (np.abs(got["dq"][b, h] - dq) <= tq + u * np.abs(dq) + 1e-30).all()
+                tk, tv = tk + tk1, tv + tv1
+                dk += dS.T @ q[b, h]
+                dv += W.T @ do[b, h]
+            if not any(frozen[hk * G:hk * G + G]):
+                assert (np.abs(got["dk"][b, hk] - dk) <= tk + u * np.abs(dk) + 1e-30).all()
+                assert (np.abs(got["dv"][b, hk] - dv) <= tv + u * np.abs(dv) + 1e-30).all()
+            elif not all(frozen[hk * G:hk * G + G]):   # frozen heads add nothing to dk
+                assert (np.abs(got["dk"][b, hk] - dk) <= tk + u * np.abs(dk) + 1e-30).all()
+            else:
+                assert not got["dk"][b, hk].any()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 96), ("bf16", 128), ("fp32", 64), ("fp32", 96),
+                                     ("fp32", 128)])
+@pytest.mark.parametrize("T,window,sinks", SPANS)
+def test_multi_head(saf, dtype, d, T, window, sinks):
+    frozen = [0, 1, 0]
+    x, g = _inputs(dtype, 1, 3, 3, T, d, (1,), seed=T + d)
+    out = _run(saf, g, frozen, window, sinks)
+    _check(dtype, x, out, frozen, window, sinks)
+    # a frozen head keeps the layer's bits
+    o, lse = saf.saf_attn_fwd_gqa(g["q"], g["k"], g["v"], g["a"], g["r"], frozen)
+    assert torch.equal(out["o"][:, 1], o[:, 1]) and torch.equal(out["lse"][:, 1], lse[:, 1])
+    _, _, dv = saf.saf_attn_bwd_gqa(g["q"], g["k"], g["v"], o, g["do"], lse, g["a"], g["r"], frozen)
+    assert torch.equal(out["dv"][:, 1], dv[:, 1])
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+@pytest.mark.parametrize("frozen", [(), (1, 3, 6), (4, 5, 6, 7)])
+@pytest.mark.parametrize("T,window,sinks", [(300, 64, 4), (513, 200, 0), (389, 1, 140)])
+def test_grouped(saf, dtype, d, frozen, T, window, sinks):
+    flags = [1 if h in frozen else 0 for h in range(8)]
+    x, g = _inputs(dtype, 2, 8, 2, T, d, frozen, seed=T)
+    out = _run(saf, g, flags, window, sinks)
+    _check(dtype, x, out, flags, window, sinks)
+    # dv of a group with frozen heads: the whole group against the reference, to bf16's rounding of
+    # weights and result (u each, the factorised weights one more) and the fp32 terms of the bounds
+    dv = so.window_bwd(*(_np(x[n]) for n in ("q", "k", "v", "do", "a", "r")), flags, window, sinks)[2]
+    u = _bounds.HALF[dtype]
+    for hk in range(2):
+        A = np.zeros((2, T, d))
+        for h in range(4 * hk, 4 * hk + 4):
+            for b in range(2):
+                W, _ = so.row_weights(_np(x["q"])[b, h], _np(x["k"])[b, hk], np.arange(T), _np(x["a"])[h],
+                                      _np(x["r"])[h], flags[h], window, sinks)
+                A[b] += W.T @ np.abs(_np(x["do"])[b, h])
+        slack = 2e-5 + (1e-4 if any(flags[4 * hk:4 * hk + 4]) else 0)   # logits of frozen heads reach 60: 6 e |logit|
+        assert (np.abs(_np(out["dv"])[:, hk] - dv[:, hk]) <= (2 * u + slack) * A + u * np.abs(dv[:, hk])).all()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 96), ("fp32", 64)])
+def test_window_that_reaches_every_key_has_the_layers_bits(saf, dtype, d):
+    frozen = [0, 1, 0, 0]
+    x, g = _inputs(dtype, 2, 4, 2, 200, d, (1,), seed=3)
+    o, lse = saf.saf_attn_fwd_gqa(g["q"], g["k"], g["v"], g["a"], g["r"], frozen)
+    for window in (0, 200, 2 ** 31 - 1):
+        for sinks in (0, 7, 2 ** 31 - 1):
+            o2, lse2 = saf.saf_attn_fwd_window(g["q"], g["k"], g["v"], g["a"], g["r"], frozen, window, sinks)
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    # sinks that cover every key, with a window that does not: the masked kernels, the same weights
+    o2, lse2 = saf.saf_attn_fwd_window(g["q"], g["k"], g["v"], g["a"], g["r"], frozen, 5, 2 ** 31 - 1)
+    torch.testing.assert_close(lse, lse2, atol=1e-5, rtol=1e-5)
+
+
+def test_prepared_state(saf):
+    for dtype, d in (("bf16", 64), ("bf16", 128), ("fp32", 64)):
+        frozen = [0, 1, 0, 1]
+        x, g = _inputs(dtype, 1, 4, 4, 333, d, (1, 3), seed=9)
+        state = saf.saf_frozen_prepare(g["a"], g["r"], frozen, 333, g["v"].dtype)
+        a, b = _run(saf, g, frozen, 50, 3), _run(saf, g, frozen, 50, 3, state=state)
+        assert torch.equal(a["o"], b["o"]) and torch.equal(a["lse"], b["lse"])
+        assert torch.equal(a["dk"][:, ::2], b["dk"][:, ::2])
+        _check(dtype, x, b, frozen, 50, 3)
+
+
+def test_nan_keys_outside_every_window(saf):
+    # whole key blocks that no row of a query block sees are not visited: a NaN there stays there.
+    # 640 tokens, window 100, no sinks: rows from 384 on see keys from 285 on, in blocks from 256 on
+    for dtype, d in (("bf16", 64), ("bf16", 128), ("fp32", 64)):
+        x, g = _inputs(dtype, 1, 2, 2, 640, d, (), seed=12)
+        clean, _ = saf.saf_attn_fwd_window(g["q"], g["k"], g["v"], None, None, None, 100, 0)
+        g["k"][:, :, :128], g["v"][:, :, :128] = float("nan"), float("nan")
+        o, _ = saf.saf_attn_fwd_window(g["q"], g["k"], g["v"], None, None, None, 100, 0)
+        assert torch.equal(o[:, :, 384:], clean[:, :, 384:])
+
+
+def test_gradients_against_differences(saf):
+    # fp32: <o, do> along a direction; central differences at h = 0.02 are off by h^2 f''' / 6
+    # (about 1e-4 of |f'| for scores of size 1) and 2^-24 sqrt(n) |f| / h of rounding
+    x, g = _inputs("fp32", 1, 2, 1, 150, 64, (), seed=21)
+    for n in ("q", "k"):
+        g[n] *= 0.3
+    out = _run(saf, g, None, 40, 3)
+    gen = torch.Generator().manual_seed(5)
+    for n, grad in (("q", "dq"), ("k", "dk"), ("v", "dv")):
+        dirn = torch.randn(g[n].shape, generator=gen).cuda()
+        dirn /= dirn.norm()
+        f = []
+        for h in (0.02, -0.02):
+            y = dict(g)
+            y[n] = g[n] + h * dirn
+            o, _ = saf.saf_attn_fwd_window(y["q"], y["k"], y["v"], None, None, None, 40, 3)
+            f.append((o.double() * g["do"].double()).sum().item())
+        diff, want = (f[0] - f[1]) / 0.04, (out[grad].double() * dirn.double()).sum().item()
+        scale = out[grad].double().norm().item()
+        assert abs(diff - want) <= 2e-3 * scale, (n, diff, want)
+
+
+def test_captured_and_replayed(saf):
+    x, g = _inputs("bf16", 2, 4, 2, 260, 64, (1,), seed=30)
+    frozen = [0, 1, 0, 0]
+    first = _run(saf, g, frozen, 70, 2)
+    ws = [saf.alloc_workspace(2, 4, 260, 64, torch.bfloat16, b) for b in (False, True)]
+    o, lse = torch.empty_like(first["o"]), torch.empty_like(first["lse"])
+    grads = [torch.empty_like(first[n]) for n in ("dq", "dk", "dv")]
+
+    def step():
+        saf.saf_attn_fwd_window(g["q"], g["k"], g["v"], g["a"], g["r"], frozen, 70, 2, o=o, lse=lse, workspace=ws[0])
+        saf.saf_attn_bwd_window(g["q"], g["k"], g["v"], o, g["do"], lse, g["a"], g["r"], frozen, 70, 2, dq=grads[0],
+                                dk=grads[1], dv=grads[2], workspace=ws[1])
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(2):
+        for t in (o, lse, *grads):
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, first["o"]) and torch.equal(lse, first["lse"])
+        assert torch.equal(grads[1], first["dk"]) and torch.equal(grads[2], first["dv"])
+        # dq adds key blocks' shares in fp32 in any order, then rounds to bf16: one step apart
+        torch.testing.assert_close(grads[0], first["dq"], rtol=2.0 ** -7, atol=1e-5)
