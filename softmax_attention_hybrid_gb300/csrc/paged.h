@@ -43,7 +43,7 @@ struct PagedArgs {
     int max_pages, num_pages, page_log2;
     int P, max_len, window, sinks;
     int tile;                      // keys per tile of the kernel that runs
-    int rows;                      // rows per block of the kernel that runs
+    int rows[2];                   // rows per block of the kernel that runs: part 0, part 1
     int nrb[2];                    // row blocks of part 0 and part 1
     int chunks[2];                 // items along the keys: part 0, part 1
     int per_chunk[2];              // tiles of an item
@@ -162,8 +162,11 @@ __device__ __forceinline__ size_t paged_out_row(const PagedArgs& p, const PagedR
     return ((size_t)w.b * p.H + w.h) * p.T + w.t;
 }
 
-// paged_simt.cu: any type, CUDA cores. rows and tile are kSimtRows and kSimtTile.
+// paged_tc.cu: bf16, tensor cores; rows 32, 64 or 128 per block. paged_simt.cu: fp32, CUDA cores;
+// rows kSimtRows.
+constexpr int kTcTile = 64;
+cudaError_t launch_paged_tc(const PagedArgs& p, cudaStream_t s);
 constexpr int kSimtRows = 8, kSimtTile = 64;
-cudaError_t launch_paged_simt(const PagedArgs& p, bool bf16, cudaStream_t s);
+cudaError_t launch_paged_simt(const PagedArgs& p, cudaStream_t s);
 
 }  // namespace saf

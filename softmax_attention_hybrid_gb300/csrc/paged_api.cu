@@ -11,9 +11,11 @@ namespace {
 constexpr int kSms = 152;   // GB300
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Items that one call aims at. More items fill the GPU better and level sequences of
-// different lengths; fewer leave less to join.
-constexpr int kItemsSimt = kSms * 6;
+// Items that run at the same time, and the most that a call is split into. Small calls get
+// one round of items; larger ones more rounds, which level sequences of different lengths.
+constexpr int kSlotsSimt = kSms * 3, kSlotsTc = kSms * 2;
+constexpr int kRounds = 4;
+constexpr int kMinTiles = 8;   // tiles of an item before a second round is worth its set-up
 
 // One warp per row: the row's items, then its output.
 template <typename E, int D>
@@ -73,21 +75,26 @@ cudaError_t launch_join(const PagedArgs& p, cudaStream_t s) {
 long long ceil_div(long long x, long long y) { return (x + y - 1) / y; }
 
 struct Plan {
-    int tile, rows;
+    int tile, rows[2];
     int nrb[2];
     long long units[2];    // (sequence, key/value head, row block) triples
     long long tiles[2];    // key tiles of one of them, at most, without a window
-    long long target;      // items aimed at
+    long long slots;       // items that run at the same time
     long long max_split;   // items of a row, at most, whatever the window
 };
 
-Plan make_plan(int B, int H, int Hkv, int T, int max_len, int P) {
+Plan make_plan(int B, int H, int Hkv, int T, int max_len, int P, bool bf16) {
     Plan x;
-    x.tile = kSimtTile;
-    x.rows = kSimtRows;
-    x.target = kItemsSimt;
+    x.tile = bf16 ? kTcTile : kSimtTile;
+    x.slots = bf16 ? kSlotsTc : kSlotsSimt;
     const long long G = H / Hkv;
-    const long long rb[2] = {P > 0 ? ceil_div(G * B * T, x.rows) : 0, ceil_div(G * T, x.rows)};
+    const long long n[2] = {P > 0 ? G * B * T : 0, G * T};
+    long long rb[2];
+    for (int i = 0; i < 2; ++i) {
+        // tensor cores: copies of the rows fill the 128 of a tile (paged_tc.cu)
+        x.rows[i] = !bf16 ? kSimtRows : n[i] <= 32 ? 32 : n[i] <= 64 ? 64 : 128;
+        rb[i] = ceil_div(n[i], x.rows[i]);
+    }
     x.units[0] = rb[0] * Hkv;
     x.units[1] = rb[1] * Hkv * B;
     x.tiles[0] = ceil_div(P, x.tile);
@@ -96,15 +103,15 @@ Plan make_plan(int B, int H, int Hkv, int T, int max_len, int P) {
     for (int i = 0; i < 2; ++i) {
         x.nrb[i] = (int)rb[i];
         if (x.units[i] == 0) continue;
-        const long long c = ceil_div(x.target, x.units[i]);
+        const long long c = ceil_div(x.slots * kRounds, x.units[i]);
         x.max_split += c < x.tiles[i] ? c : x.tiles[i];
     }
     return x;
 }
 
-// The items: both parts' tiles in equal shares of `per` tiles, so that about
-// `target` items come out; a part then has ceil(tiles / per) <= ceil(target / units)
-// items along the keys (the bound that the workspace is sized by).
+// The items: both parts' tiles in equal shares of `per` tiles, at least total / (slots
+// kRounds); a part then has ceil(tiles / per) <= ceil(slots kRounds / units) items along
+// the keys (the bound that the workspace is sized by).
 void set_items(PagedArgs& p, const Plan& x, int nfrozen) {
     long long nt[2] = {x.tiles[0], x.tiles[1]};
     if (p.window > 0 && nfrozen == 0) {
@@ -119,14 +126,16 @@ void set_items(PagedArgs& p, const Plan& x, int nfrozen) {
         }
     }
     const long long total = x.units[0] * nt[0] + x.units[1] * nt[1];
-    const long long per = total > x.target ? ceil_div(total, x.target) : 1;
+    const long long one = ceil_div(total, x.slots), most = ceil_div(total, x.slots * kRounds);
+    const long long per = one < kMinTiles ? one : most > kMinTiles ? most : kMinTiles;
     for (int i = 0; i < 2; ++i) {
         p.nrb[i] = x.nrb[i];
         p.per_chunk[i] = (int)per;
         p.chunks[i] = x.units[i] ? (int)ceil_div(nt[i], per) : 0;
     }
     p.tile = x.tile;
-    p.rows = x.rows;
+    p.rows[0] = x.rows[0];
+    p.rows[1] = x.rows[1];
     p.nsplit = p.chunks[0] + p.chunks[1];
     p.items0 = x.units[0] * p.chunks[0];
     p.items = p.items0 + x.units[1] * p.chunks[1];
@@ -196,7 +205,7 @@ int paged(const void* q, const void* k_cache, const void* v_cache, const int32_t
         return SAF_EALIGN;
     if (!workspace) return SAF_EWORKSPACE;
     if (!aligned(workspace, 256)) return SAF_EALIGN;
-    const Plan plan = make_plan(B, H, Hkv, T, max_len, prefix_len);
+    const Plan plan = make_plan(B, H, Hkv, T, max_len, prefix_len, dt == SAF_BF16);
     size_t po_off;
     if (ws_bytes < workspace_bytes(plan, B, H, T, d, &po_off)) return SAF_EWORKSPACE;
     if ((st = check_device()) != SAF_OK) return st;
@@ -236,7 +245,7 @@ int paged(const void* q, const void* k_cache, const void* v_cache, const int32_t
     cudaStream_t s = (cudaStream_t)stream;
     const bool bf16 = dt == SAF_BF16;
     before_launch(SAF_KERNEL_PAGED, s);
-    cudaError_t e = launch_paged_simt(p, bf16, s);
+    cudaError_t e = bf16 ? launch_paged_tc(p, s) : launch_paged_simt(p, s);
     if (e == cudaSuccess && p.nsplit > 1) {
         note_launch();
         e = bf16 ? launch_join<__nv_bfloat16>(p, s) : launch_join<float>(p, s);
@@ -256,7 +265,7 @@ size_t saf_attn_paged_workspace_bytes(int B, int H, int Hkv, int T, int d, int m
                                       saf_dtype_t dt) {
     if (check_sizes(B, H, Hkv, T, d, max_len, prefix_len, dt) != SAF_OK) return 0;
     if (B == 0 || T == 0) return kStatusBytes;
-    return workspace_bytes(make_plan(B, H, Hkv, T, max_len, prefix_len), B, H, T, d, nullptr);
+    return workspace_bytes(make_plan(B, H, Hkv, T, max_len, prefix_len, dt == SAF_BF16), B, H, T, d, nullptr);
 }
 
 int saf_attn_paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table, int max_pages,

@@ -1,4 +1,4 @@
-// Paged attention on the CUDA cores, in fp32 arithmetic (see paged.h for the split).
+// Paged attention of fp32 caches on the CUDA cores (see paged.h for the split).
 //
 // An item holds up to 8 query rows and walks its tiles of 64 keys:
 //   scores   thread (key, half): the key's products with four rows, K and q from shared memory;
@@ -32,13 +32,8 @@ struct Smem {
 };
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
-}
 
-template <typename E, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_constant__ PagedArgs p) {
     extern __shared__ __align__(16) uint8_t raw[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
@@ -80,8 +75,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
     const PagedRange g = paged_range(p, it, sm.imin, sm.imax, sm.full || p.window == 0);
     const int e0 = min(it.chunk * p.per_chunk[it.part], g.n), e1 = min(e0 + p.per_chunk[it.part], g.n);
     const int off = it.part ? p.P : 0;
-    const E* kc = (const E*)p.k_cache;
-    const E* vc = (const E*)p.v_cache;
+    const float* kc = (const float*)p.k_cache;
+    const float* vc = (const float*)p.v_cache;
     const bool any_ord = sm.any_ord != 0;
 
     if (any_ord && e0 < e1)
@@ -90,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (sm.pos[rr] >= 0 && !sm.frozen[rr]) {
                 const PagedRow u = paged_row(p, it, r0 + rr);
-                x = load4((const E*)p.q + paged_out_row(p, u) * D + c);
+                x = load4((const float*)p.q + paged_out_row(p, u) * D + c);
             }
             *reinterpret_cast<float4*>(&sm.q[rr][c]) = x;
         }
@@ -224,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
             const size_t row = paged_out_row(p, u);
             if (p.nsplit == 1) {
                 const float l = sm.l[x];
-                from_f((E*)p.o + row * D + col, l > 0.f ? acc[x] / l : 0.f);
+                ((float*)p.o)[row * D + col] = l > 0.f ? acc[x] / l : 0.f;
                 if (col == 0) p.lse[row] = l > 0.f ? (sm.m[x] + log2f(l)) * kLn2 : -INFINITY;
             } else {
                 p.po[(row * p.nsplit + split) * D + col] = acc[x];
@@ -234,27 +229,22 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
     }
 }
 
-template <typename E, int D>
+template <int D>
 cudaError_t launch_d(const PagedArgs& p, cudaStream_t s) {
     const size_t smem = sizeof(Smem<D>);
-    cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_ex(paged_simt_kernel<E, D>, dim3((unsigned)p.items), dim3(kThreads), smem, s, true, 1, p);
-}
-
-template <typename E>
-cudaError_t launch_e(const PagedArgs& p, cudaStream_t s) {
-    switch (p.d) {
-        case 96: return launch_d<E, 96>(p, s);
-        case 128: return launch_d<E, 128>(p, s);
-        default: return launch_d<E, 64>(p, s);
-    }
+    return launch_ex(paged_simt_kernel<D>, dim3((unsigned)p.items), dim3(kThreads), smem, s, true, 1, p);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_simt(const PagedArgs& p, bool bf16, cudaStream_t s) {
-    return bf16 ? launch_e<__nv_bfloat16>(p, s) : launch_e<float>(p, s);
+cudaError_t launch_paged_simt(const PagedArgs& p, cudaStream_t s) {
+    switch (p.d) {
+        case 96: return launch_d<96>(p, s);
+        case 128: return launch_d<128>(p, s);
+        default: return launch_d<64>(p, s);
+    }
 }
 
 }  // namespace saf
