@@ -299,7 +299,7 @@ SAF_API int saf_attn_bwd_window(const void* q, const void* k, const void* v, con
  * Out: q_out [B,H,T,d] contiguous (q_out = q only where q is contiguous; else they must
  *      not overlap), the slots of k_cache and v_cache. Rows without a token, and every
  *      other slot, stay as they were. Two tokens of one call must not share a slot.
- * status: DEVICE uint32[2] (see above), for example a paged workspace.
+ * status: DEVICE uint32[2] (see above), for example a paged workspace; NULL: not recorded.
  *
  * saf_attn_paged
  * is the attention of the new tokens over their sequence's cache, after saf_kv_append:

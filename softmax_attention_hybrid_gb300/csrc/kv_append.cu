@@ -90,14 +90,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const int n = p.n_new ? p.n_new[b] : p.T;
     const long long room = (long long)p.max_pages << p.page_log2;
     if (c < 0 || n < 0 || n > p.T || c + (long long)n > room) {
-        if (t == 0 && group == 0 && u == 0) atomicOr(p.status, kStatusPage);
+        if (t == 0 && group == 0 && u == 0 && p.status) atomicOr(p.status, kStatusPage);
         if (c < 0) return;
     }
     if (t >= n) return;
     const long long slot = (long long)c + t;
     int page = slot < room ? p.table[(size_t)b * p.max_pages + (slot >> p.page_log2)] : -1;
     if (slot < room && (page < 0 || page >= p.num_pages)) {
-        if (group == 0 && u == 0) atomicOr(p.status, kStatusPage);
+        if (group == 0 && u == 0 && p.status) atomicOr(p.status, kStatusPage);
         page = -1;
     }
     const size_t page_row = (size_t)(slot & ((1 << p.page_log2) - 1));
@@ -194,7 +194,7 @@ extern "C" int saf_kv_append(const void* q, const void* k, const void* v, const 
         for (int gi = 0; gi < G; ++gi) live |= !(frozen && frozen[hk * G + gi]);
         if (live) p.heads[p.nq + p.nk++] = (uint8_t)hk;
     }
-    if (!v || !v_cache || !ctx || !page_table || !status || (p.nq > 0 && !q_out)) return SAF_EINVAL;
+    if (!v || !v_cache || !ctx || !page_table || (p.nq > 0 && !q_out)) return SAF_EINVAL;
     if (p.nk > 0 && (!k || !k_cache)) return SAF_EINVAL;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) ||
         !aligned(v_cache, 16) || !aligned(ctx, 4) || !aligned(n_new, 4) || !aligned(page_table, 4) ||

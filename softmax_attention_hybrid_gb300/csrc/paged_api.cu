@@ -17,58 +17,95 @@ constexpr int kSlotsSimt = kSms * 3, kSlotsTc = kSms * 2;
 constexpr int kRounds = 4;
 constexpr int kMinTiles = 8;   // tiles of an item before a second round is worth its set-up
 
-// One warp per row: the row's items, then its output.
-template <typename E, int D>
+// Joins the items of a row. kWarps warps share a row (a block of four warps holds 4 / kWarps
+// rows): with few items a warp each, with many the four warps of a block, whose loads are
+// then all in flight together.
+template <typename E, int D, int kWarps>
 __global__ void __launch_bounds__(128) join_kernel(const float2* __restrict__ ml, const float* __restrict__ po,
                                                    E* __restrict__ o, float* __restrict__ lse, long long rows,
                                                    int nsplit) {
+    __shared__ float4 part[4][32];
+    __shared__ float part_l[4];
     grid_dep_wait();   // the items are done
     grid_dep_launch();
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= rows) return;
-    const float2* r = ml + row * nsplit;
-    float M = -INFINITY;
-    for (int c = lane; c < nsplit; c += 32) M = fmaxf(M, r[c].x);
-    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    constexpr int N = D / 32;
-    float acc[N];
-#pragma unroll
-    for (int c = 0; c < N; ++c) acc[c] = 0.f;
-    float l = 0.f;
-    if (M > -INFINITY)
-        for (int c0 = 0; c0 < nsplit; c0 += 32) {
-            const float2 e = c0 + lane < nsplit ? r[c0 + lane] : make_float2(-INFINITY, 0.f);
-            const float w = exp2f(e.x - M);
-            l += w * e.y;
-            const int n = min(32, nsplit - c0);
-            for (int u = 0; u < n; ++u) {
-                const float wu = __shfl_sync(0xffffffffu, w, u);
-                if (wu == 0.f) continue;   // an item whose keys the row does not see wrote no output
-                const float* src = po + (row * nsplit + c0 + u) * D + lane;
-#pragma unroll
-                for (int c = 0; c < N; ++c) acc[c] = fmaf(wu, src[32 * c], acc[c]);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = warp % kWarps;
+    const long long row = (long long)blockIdx.x * (4 / kWarps) + warp / kWarps;
+    constexpr int kLanes = D / 4;             // lanes of one item's row
+    constexpr int kSide = kLanes <= 16 ? 2 : 1;   // items next to each other in a warp
+    const int side = kSide == 2 ? lane >> 4 : 0, c = kSide == 2 ? lane & 15 : lane;
+    float M = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row < rows) {
+        const float2* r = ml + row * nsplit;
+        for (int s = lane; s < nsplit; s += 32) M = fmaxf(M, r[s].x);
+        for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+        if (M > -INFINITY) {
+#pragma unroll 4
+            for (int s = mine * kSide + side; s < nsplit; s += kWarps * kSide) {
+                const float2 e = r[s];
+                const float w = exp2f(e.x - M);
+                l += w * e.y;
+                // an item whose keys the row does not see wrote no output
+                if (w > 0.f && c < kLanes) {
+                    const float4 x = *reinterpret_cast<const float4*>(po + (row * nsplit + s) * D + 4 * c);
+                    acc.x = fmaf(w, x.x, acc.x);
+                    acc.y = fmaf(w, x.y, acc.y);
+                    acc.z = fmaf(w, x.z, acc.z);
+                    acc.w = fmaf(w, x.w, acc.w);
+                }
             }
         }
-    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    }
+    if (kSide == 2) {
+        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+        acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+        acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+    }
+    if (kWarps > 1) {
+        part[warp][lane] = acc;
+        if (lane == 0) part_l[warp] = l;
+        __syncthreads();
+        if (mine != 0) return;
 #pragma unroll
-    for (int c = 0; c < N; ++c) from_f(o + row * D + lane + 32 * c, acc[c] * inv);
+        for (int x = 1; x < kWarps; ++x) {
+            const float4 y = part[warp + x][lane];
+            acc.x += y.x;
+            acc.y += y.y;
+            acc.z += y.z;
+            acc.w += y.w;
+            l += part_l[warp + x];
+        }
+    }
+    if (row >= rows) return;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    if (side == 0 && c < kLanes) {
+        E* dst = o + row * D + 4 * c;
+        from_f(dst, acc.x * inv);
+        from_f(dst + 1, acc.y * inv);
+        from_f(dst + 2, acc.z * inv);
+        from_f(dst + 3, acc.w * inv);
+    }
     if (lane == 0) lse[row] = l > 0.f ? (M + log2f(l)) * kLn2 : -INFINITY;
+}
+
+template <typename E, int D>
+cudaError_t launch_join_d(const PagedArgs& p, cudaStream_t s) {
+    const long long rows = (long long)p.B * p.H * p.T;
+    if (p.nsplit > 8)
+        return launch_ex(join_kernel<E, D, 4>, dim3((unsigned)rows), dim3(128), 0, s, true, 1, (const float2*)p.ml,
+                         (const float*)p.po, (E*)p.o, p.lse, rows, p.nsplit);
+    return launch_ex(join_kernel<E, D, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, true, 1,
+                     (const float2*)p.ml, (const float*)p.po, (E*)p.o, p.lse, rows, p.nsplit);
 }
 
 template <typename E>
 cudaError_t launch_join(const PagedArgs& p, cudaStream_t s) {
-    const long long rows = (long long)p.B * p.H * p.T;
-    const dim3 grid((unsigned)((rows + 3) / 4));
-    auto go = [&](auto kernel) {
-        return launch_ex(kernel, grid, dim3(128), 0, s, true, 1, (const float2*)p.ml, (const float*)p.po, (E*)p.o,
-                         p.lse, rows, p.nsplit);
-    };
     switch (p.d) {
-        case 96: return go(join_kernel<E, 96>);
-        case 128: return go(join_kernel<E, 128>);
-        default: return go(join_kernel<E, 64>);
+        case 96: return launch_join_d<E, 96>(p, s);
+        case 128: return launch_join_d<E, 128>(p, s);
+        default: return launch_join_d<E, 64>(p, s);
     }
 }
 
@@ -128,10 +165,13 @@ void set_items(PagedArgs& p, const Plan& x, int nfrozen) {
     const long long total = x.units[0] * nt[0] + x.units[1] * nt[1];
     const long long one = ceil_div(total, x.slots), most = ceil_div(total, x.slots * kRounds);
     const long long per = one < kMinTiles ? one : most > kMinTiles ? most : kMinTiles;
+    // a prefix's items write many rows each: no more than one round of them
+    const long long shared = ceil_div(x.units[0] * nt[0], x.slots);
     for (int i = 0; i < 2; ++i) {
+        const long long n = i == 0 && shared > per ? shared : per;
         p.nrb[i] = x.nrb[i];
-        p.per_chunk[i] = (int)per;
-        p.chunks[i] = x.units[i] ? (int)ceil_div(nt[i], per) : 0;
+        p.per_chunk[i] = (int)n;
+        p.chunks[i] = x.units[i] ? (int)ceil_div(nt[i], n) : 0;
     }
     p.tile = x.tile;
     p.rows[0] = x.rows[0];

@@ -26,7 +26,7 @@ struct Smem {
     float p[TK][R];       // weights of the tile, [key][row]
     float s[R][TK + 1];
     float corr[R], m[R], l[R];
-    int pos[R], head[R];
+    int pos[R], head[R], out[R];   // out: the row's place in o, -1: none
     uint8_t frozen[R], live[TK];
     int imin, imax, full, any_ord;
 };
@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
         w = paged_row(p, it, r0 + tid);
         sm.pos[tid] = w.i;
         sm.head[tid] = w.h;
+        sm.out[tid] = w.there ? (int)paged_out_row(p, w) : -1;
         sm.frozen[tid] = w.frozen;
         sm.m[tid] = -INFINITY;
         sm.l[tid] = 0.f;
@@ -83,10 +84,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
         for (int e = tid; e < R * (D / 4); e += kThreads) {
             const int rr = e / (D / 4), c = 4 * (e - rr * (D / 4));
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (sm.pos[rr] >= 0 && !sm.frozen[rr]) {
-                const PagedRow u = paged_row(p, it, r0 + rr);
-                x = load4((const float*)p.q + paged_out_row(p, u) * D + c);
-            }
+            if (sm.pos[rr] >= 0 && !sm.frozen[rr]) x = load4((const float*)p.q + (size_t)sm.out[rr] * D + c);
             *reinterpret_cast<float4*>(&sm.q[rr][c]) = x;
         }
 
@@ -214,9 +212,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
     if (kh == 0 && col < D) {
 #pragma unroll
         for (int x = 0; x < R; ++x) {
-            const PagedRow u = paged_row(p, it, r0 + x);
-            if (!u.there) continue;
-            const size_t row = paged_out_row(p, u);
+            if (sm.out[x] < 0) continue;
+            const size_t row = (size_t)sm.out[x];
             if (p.nsplit == 1) {
                 const float l = sm.l[x];
                 ((float*)p.o)[row * D + col] = l > 0.f ? acc[x] / l : 0.f;

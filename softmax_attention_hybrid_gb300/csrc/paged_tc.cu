@@ -11,12 +11,13 @@
 // others: the softmax of a row runs on 2 (4) threads, the MMAs cost the same, and the
 // copies' (m, l, O) are added at the end like items.
 //
-// Warps (224 threads, two CTAs per SM): 0-3 rows, one thread per row of the tile (TMEM lane);
-// 4 loads K, 6 loads V (each of its lanes fetches one page of the tile, and looks up the next
+// Warps (192 threads, two CTAs per SM): 0-3 rows, one thread per row of the tile (TMEM lane);
+// 4 loads K and V (each of its lanes fetches one page of the tile, and looks up a later
 // tile's page while it waits); 5 owns tensor memory and issues the MMAs.
 // Tensor memory (256 columns): S [0, 64) fp32 | P [64, 96) bf16 pairs | O [128, 128 + d).
 // S has columns of its own so that the next tile's S runs under this one's softmax.
-// Shared memory: Q, and two stages each of K and V.
+// Shared memory: Q, and a ring of slots of one tile of K or V each, filled in the order in
+// which the MMAs use them: K0, K1, V0, K2, V1, ... (V0, V1, ... where no row is ordinary).
 //
 // Bound by memory in decoding: a tile of K and V is 32 KB at d = 128, 1400 cycles of an SM's share
 // of the memory, against 512 cycles of MMAs.
@@ -30,7 +31,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 224;
+constexpr int kThreads = 192;
 constexpr int TK = kTcTile;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -51,16 +52,17 @@ struct Smem {
     static constexpr int tile = atom * (kD / 64);
     static constexpr int q_atom = 128 * 128;
     static constexpr int q = 0;
-    static constexpr int k = q + q_atom * (kD / 64);    // 2 stages
-    static constexpr int v = k + 2 * tile;              // 2 stages
-    static constexpr int total = v + 2 * tile;
+    static constexpr int ring = q + q_atom * (kD / 64);
+    static constexpr int slots = kD == 64 ? 10 : 4;     // 80 KB, 64 KB: what two CTAs of an SM leave
+    static constexpr int total = ring + slots * tile;
     // after the last MMA the whole region stages the output rows
     static constexpr int out_pitch = kD + 4;
     static_assert(128 * out_pitch * 4 <= total, "output staging");
 };
 
+template <int kD>
 struct Bars {
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t full[Smem<kD>::slots], empty[Smem<kD>::slots];
     uint64_t s_full, s_empty, p_ready, o_done, mma_idle;
 };
 
@@ -95,70 +97,104 @@ struct Work {
     int e0, e1;       // tiles
     int imin, imax;   // positions of the rows that see anything
     int off;          // position of the part's slot 0
-    bool any_ord;
+    bool any_ord;     // an ordinary row is among them: K is loaded
+    bool lost;        // a page that is needed is not in the cache
+
+    // place of tile e0 + j's K and V in the order of loads
+    __device__ __forceinline__ int k_load(int j) const { return j == 0 ? 0 : 2 * j - 1; }
+    __device__ __forceinline__ int v_load(int j) const {
+        if (!any_ord) return j;
+        return j + 1 < e1 - e0 ? 2 * j + 2 : 2 * j + 1;
+    }
 };
 
-// Boxes of a tile: bit b of the result where keys [x0 + b box, ...) hold a seen key.
+// Whether keys [bx, bx + box) of the part hold one that some row sees.
 __device__ __forceinline__ bool box_seen(const PagedRange& g, int bx, int box) {
     return bx < g.hi && (bx + box > g.lo || bx < g.sink);
 }
 
-// One of the two loading warps: tiles e0 .. e1 - 1 of cache `map` into its two stages. Lane l
-// fetches box l of a tile. With `mask`, the boxes that were found in the cache go to mask[stage].
+// The loading warp. Lane l fetches box l of every tile, from its page.
 template <int kD>
-__device__ __forceinline__ void load_warp(const TcParams& P, const Work& w, const CUtensorMap* map, uint8_t* stages,
-                                          uint64_t* full, uint64_t* empty, bool load, uint32_t* mask,
+__device__ __forceinline__ void load_warp(const TcParams& P, const Work& w, uint8_t* sm, Bars<kD>& bars,
                                           volatile int* abort) {
+    using S = Smem<kD>;
     const PagedArgs& p = P.a;
     const int lane = threadIdx.x & 31;
-    const int nbox = TK / P.box;
+    const int nbox = TK / P.box, n = w.e1 - w.e0;
     const int in_page = (1 << p.page_log2) - 1;
     const uint32_t box_bytes = (uint32_t)P.box * 128u * (kD / 64);
-    auto look = [&](int e) -> int {   // my box's page: -1 none needed, -2 needed and not in the cache
-        if (lane >= nbox || e >= w.e1) return -1;
-        const int bx = paged_tile(w.g, e) * TK + lane * P.box;
-        if (!box_seen(w.g, bx, P.box)) return -1;
-        const int pg = paged_page(p, w.it, bx);
-        return pg < 0 ? -2 : pg;
+    if (lane == 0) {
+        tma_prefetch_desc(&P.tm_k);
+        tma_prefetch_desc(&P.tm_v);
+    }
+    auto look = [&](int j) -> int {   // my box's page, -1: nothing to fetch
+        if (lane >= nbox || j >= n) return -1;
+        const int bx = paged_tile(w.g, w.e0 + j) * TK + lane * P.box;
+        return box_seen(w.g, bx, P.box) ? paged_page(p, w.it, bx) : -1;
     };
-    int next = look(w.e0);
-    for (int e = w.e0, n = 0; e < w.e1; ++e, ++n) {
-        const int s = n & 1, pg = next;
-        next = look(e + 1);
-        if (!mbar_wait_warp(&empty[s], ((n >> 1) & 1) ^ 1u, abort, p.status, kStatusTimeout)) break;
+    auto fetch = [&](int load, const CUtensorMap* map, int j, int pg) -> bool {
+        const int s = load % S::slots;
+        if (!mbar_wait_warp(&bars.empty[s], ((load / S::slots) & 1) ^ 1u, abort, p.status, kStatusTimeout)) return false;
         const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0);
-        const uint32_t lost = __ballot_sync(0xffffffffu, pg == -2);
-        if (lane == 0) {
-            if (mask) mask[s] = have;
-            if (lost) atomicOr(p.status, kStatusPage);
-            mbar_expect_tx(&full[s], load ? __popc(have) * box_bytes : 0u);
-        }
+        if (lane == 0) mbar_expect_tx(&bars.full[s], __popc(have) * box_bytes);
         __syncwarp();
-        if (load && pg >= 0) {
-            const int bx = paged_tile(w.g, e) * TK + lane * P.box;
-            uint8_t* dst = stages + s * Smem<kD>::tile + lane * P.box * 128;
+        if (pg >= 0) {
+            const int bx = paged_tile(w.g, w.e0 + j) * TK + lane * P.box;
+            uint8_t* dst = sm + S::ring + s * S::tile + lane * P.box * 128;
             const int z = pg * p.Hkv + w.it.hk;
 #pragma unroll
-            for (int c = 0; c < kD / 64; ++c) tma_load_3d(dst + c * Smem<kD>::atom, map, &full[s], 64 * c, bx & in_page, z);
+            for (int c = 0; c < kD / 64; ++c) tma_load_3d(dst + c * S::atom, map, &bars.full[s], 64 * c, bx & in_page, z);
         }
         __syncwarp();
+        return true;
+    };
+    int pg = look(0), next = look(1);
+    bool ok = !w.any_ord || fetch(0, &P.tm_k, 0, pg);
+    for (int j = 0; j < n && ok; ++j) {
+        const int later = look(j + 2);
+        if (w.any_ord && j + 1 < n) ok = fetch(w.k_load(j + 1), &P.tm_k, j + 1, next);
+        ok = ok && fetch(w.v_load(j), &P.tm_v, j, pg);
+        pg = next;
+        next = later;
     }
+}
+
+// kN consecutive values p[0 .. kN), of which p - 3 .. p + kN + 3 may be read, through aligned
+// 16-byte loads (a quarter of the requests; neighbouring threads read far apart).
+template <int kN>
+__device__ __forceinline__ void load_run(const float* p, float* v) {
+    const int m = (int)((uintptr_t)p >> 2) & 3;
+    const float4* a = reinterpret_cast<const float4*>(p - m);
+    float u[kN + 4];
+#pragma unroll
+    for (int c = 0; c < kN / 4 + 1; ++c) {
+        const float4 x = __ldg(a + c);
+        u[4 * c] = x.x;
+        u[4 * c + 1] = x.y;
+        u[4 * c + 2] = x.z;
+        u[4 * c + 3] = x.w;
+    }
+#pragma unroll
+    for (int c = 0; c < kN + 3; ++c) u[c] = (m & 1) ? u[c + 1] : u[c];
+#pragma unroll
+    for (int c = 0; c < kN; ++c) v[c] = (m & 2) ? u[c + 2] : u[c];
 }
 
 // The rows' part of an item: kCopies copies of 128 / kCopies rows; thread t holds row t mod
 // (128 / kCopies) and the keys [kCols copy, ...) of every tile.
 template <int kD, int kCopies>
-__device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, const PagedRow& row, uint8_t* sm, Bars& bars,
-                                          const uint32_t* mask, uint32_t tmem, volatile int* abort) {
+__device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, const PagedRow& row, uint8_t* sm,
+                                          Bars<kD>& bars, const int* out_row, uint32_t tmem, volatile int* abort) {
+    using S = Smem<kD>;
     const PagedArgs& p = P.a;
     constexpr int kCols = TK / kCopies, kRows = 128 / kCopies;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int c0 = (t / kRows) * kCols;   // my keys of a tile
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    const uint32_t all = P.box == TK ? 1u : (1u << (TK / P.box)) - 1u;
     const int box_log2 = __ffs(P.box) - 1;
     const int i = row.i < 0 ? -1 : row.i - w.off;   // my last visible slot of the part
     const float sc = row.frozen ? 1.f : p.scale_log2;
+    const bool frozen = row.frozen && i >= 0;
     const float* ra = p.a + (size_t)row.h * p.ld + w.off;
     const float* rr = p.r + (size_t)row.h * p.ld;
     float m = -INFINITY, l = 0.f;
@@ -174,7 +210,27 @@ __device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, cons
     int n = 0;
     for (int e = w.e0; e < w.e1; ++e, ++n) {
         const int x0 = paged_tile(w.g, e) * TK;
-        const int s = n & 1;
+        float lg[kCols];   // a frozen row's logits (Eq. 3), loaded while S is computed
+        if (frozen) {
+            const int x = x0 + c0, back = i - x - (kCols - 1);   // r[back ..] backwards
+            if (back >= 3 && i - x + 4 < p.ld) {
+                load_run<kCols>(rr + back, lg);
+#pragma unroll
+                for (int c = 0; c < kCols / 2; ++c) {
+                    const float y = lg[c];
+                    lg[c] = lg[kCols - 1 - c];
+                    lg[kCols - 1 - c] = y;
+                }
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) lg[c] += __ldg(ra + x + c);
+            } else {   // slots past my own position are masked below
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) {
+                    const int y = min(x + c, i);
+                    lg[c] = ra[y] + rr[i - y];
+                }
+            }
+        }
         uint32_t sv[kCols];
         if (w.any_ord) {
             if (!(ok = mbar_wait(&bars.s_full, n & 1, abort, p.status, kStatusTimeout))) break;
@@ -182,25 +238,20 @@ __device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, cons
             tmem_ld_n<kCols>(lane_base + c0, sv);
             tmem_ld_wait();
             tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.s_empty);
         }
-        if (!(ok = mbar_wait(&bars.k_full[s], (n >> 1) & 1, abort, p.status, kStatusTimeout))) break;
-        const uint32_t have = mask[s];
-        __syncwarp();
-        if (lane == 0) {
-            if (w.any_ord) mbar_arrive(&bars.s_empty);
-            mbar_arrive(&bars.k_empty[s]);
-        }
-        const bool lost = have != all;
-        if (row.frozen && i >= 0) {
-            // the fixed pattern's logits, base 2 (Eq. 3); slots past my own position are masked below
+        if (frozen)
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) {
-                const int x = min(x0 + c0 + c, i);
-                sv[c] = __float_as_uint((ra[x] + rr[i - x]) * kLog2e);
+            for (int c = 0; c < kCols; ++c) sv[c] = __float_as_uint(lg[c] * kLog2e);
+        uint32_t have = 0xffffffffu;   // boxes whose page is in the cache
+        if (w.lost)
+            for (int b = 0; b < TK / P.box; ++b) {
+                const int bx = x0 + b * P.box;
+                if (box_seen(w.g, bx, P.box) && paged_page(p, w.it, bx) < 0) have &= ~(1u << b);
             }
-        }
         // masks, in tiles that some row does not see whole
-        if (lost || x0 + TK > w.g.hi || x0 + TK - 1 > w.imin - w.off ||
+        if (w.lost || x0 + TK > w.g.hi || x0 + TK - 1 > w.imin - w.off ||
             (p.window > 0 && x0 <= w.imax - w.off - p.window)) {
             const int lo = row.frozen || p.window == 0 ? -1 : i - p.window;   // slots <= lo: sinks only
             const int sink = p.sinks - w.off, last = min(i, w.g.hi - 1);   // (a prefix ends before i)
@@ -238,21 +289,16 @@ __device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, cons
         }
         l += (acc0.x + acc1.x) + (acc0.y + acc1.y);
         // values of slots that no row sees may be anything: zeros, for 0 * NaN is none
-        if (lost || x0 + TK > w.g.hi || (x0 < w.g.lo && x0 + TK > w.g.sink)) {
-            if (!(ok = mbar_wait(&bars.v_full[s], (n >> 1) & 1, abort, p.status, kStatusTimeout))) break;
+        if (w.lost || x0 + TK > w.g.hi || (x0 < w.g.lo && x0 + TK > w.g.sink)) {
+            const int ld = w.v_load(n), s = ld % S::slots;
+            if (!(ok = mbar_wait(&bars.full[s], (ld / S::slots) & 1, abort, p.status, kStatusTimeout))) break;
             const int kk = t & 63, x = x0 + kk;
             const bool seen = x < w.g.hi && (x >= w.g.lo || x < w.g.sink) && ((have >> (kk >> box_log2)) & 1u);
             if (!seen) {
-                uint8_t* vrow = sm + Smem<kD>::v + s * Smem<kD>::tile + kk * 128;
-                if (kD == 128) {
-                    vrow += (t >> 6) * Smem<kD>::atom;
+                constexpr int kHalf = kD == 128 ? 8 : 4;   // two threads per key
+                uint8_t* vrow = sm + S::ring + s * S::tile + kk * 128 + (t >> 6) * (kD == 128 ? S::atom : 64);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vrow + 16 * c) = make_uint4(0, 0, 0, 0);
-                } else {
-                    vrow += (t >> 6) * 64;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(vrow + 16 * c) = make_uint4(0, 0, 0, 0);
-                }
+                for (int c = 0; c < kHalf; ++c) *reinterpret_cast<uint4*>(vrow + 16 * c) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
         }
@@ -305,7 +351,7 @@ __device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, cons
             tmem_ld_wait();
 #pragma unroll
             for (int c = 0; c < 32; c += 4)
-                *reinterpret_cast<float4*>(out + t * Smem<kD>::out_pitch + q + c) =
+                *reinterpret_cast<float4*>(out + t * S::out_pitch + q + c) =
                     make_float4(__uint_as_float(ov[c]) * f, __uint_as_float(ov[c + 1]) * f,
                                 __uint_as_float(ov[c + 2]) * f, __uint_as_float(ov[c + 3]) * f);
         }
@@ -324,9 +370,8 @@ __device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, cons
     // a warp per row: whole rows to memory
     const int split = w.it.part ? p.chunks[0] + w.it.chunk : w.it.chunk;
     for (int x = warp; x < kRows; x += 4) {
-        const PagedRow u = paged_row(p, w.it, w.it.rb * kRows + x);
-        if (!u.there) break;   // rows that are there come first
-        const size_t at = paged_out_row(p, u);
+        if (out_row[x] < 0) break;   // rows that are there come first
+        const size_t at = (size_t)out_row[x];
         const float l_row = sh_l[x], m_row = sh_m[x];
         const float inv = p.nsplit > 1 ? 1.f : l_row > 0.f ? 1.f / l_row : 0.f;
         for (int c = 2 * lane; c < p.d; c += 64) {
@@ -334,7 +379,7 @@ __device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, cons
             if (l_row > 0.f)
 #pragma unroll
                 for (int k = 0; k < kCopies; ++k)
-                    y = fadd2(y, *reinterpret_cast<const float2*>(out + (k * kRows + x) * Smem<kD>::out_pitch + c));
+                    y = fadd2(y, *reinterpret_cast<const float2*>(out + (k * kRows + x) * S::out_pitch + c));
             if (p.nsplit > 1)
                 *reinterpret_cast<float2*>(p.po + (at * p.nsplit + split) * p.d + c) = y;
             else
@@ -349,11 +394,12 @@ __device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, cons
 
 template <int kD>
 __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_constant__ TcParams P) {
+    using S = Smem<kD>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ Bars bars;
-    __shared__ uint32_t tmem_base_sh, mask[2];
-    __shared__ int abort_flag, sh_imin, sh_imax, sh_kinds;
+    __shared__ Bars<kD> bars;
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_flag, sh_imin, sh_imax, sh_kinds, out_row[128];
     const PagedArgs& p = P.a;
     grid_dep_wait();
     grid_dep_launch();
@@ -366,11 +412,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_cons
         sh_imin = 0x7fffffff;
         sh_imax = -1;
         sh_kinds = 0;
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.k_full[i], 1);
-            mbar_init(&bars.k_empty[i], 5);   // the MMAs and the four row warps (they read mask)
-            mbar_init(&bars.v_full[i], 1);
-            mbar_init(&bars.v_empty[i], 1);
+        for (int i = 0; i < S::slots; ++i) {
+            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.empty[i], 1);
         }
         mbar_init(&bars.s_full, 1);
         mbar_init(&bars.s_empty, 4);
@@ -378,18 +422,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_cons
         mbar_init(&bars.o_done, 1);
         mbar_init(&bars.mma_idle, 1);
         fence_mbar_init();
-        if (w.it.part == 1 && w.it.chunk == 0 && w.it.rb == 0 && w.it.hk == 0) {
-            int c;   // each sequence's counts are checked once
-            bool bad;
-            paged_tokens(p, w.it.b, &c, &bad);
-            if (bad) atomicOr(p.status, kStatusPage);
-        }
     }
     __syncthreads();
     PagedRow row;
     if (t < 128) {
         row = paged_row(p, w.it, w.it.rb * rows + (t & (rows - 1)));
-        if ((t & (rows - 1)) != t && rows < 128) row.there = false;   // a copy is stored by its first
+        out_row[t] = row.there ? (int)paged_out_row(p, row) : -1;
         int lo = row.i >= 0 ? row.i : 0x7fffffff, hi = row.i;
         const int kinds = row.i < 0 ? 0 : row.frozen ? 2 : 1;
         lo = __reduce_min_sync(0xffffffffu, lo);
@@ -400,6 +438,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_cons
             atomicMax(&sh_imax, hi);
             atomicOr(&sh_kinds, k);
         }
+    } else if (t == 128 && w.it.part == 1 && w.it.chunk == 0 && w.it.rb == 0 && w.it.hk == 0) {
+        int c;   // each sequence's counts are checked once
+        bool bad;
+        paged_tokens(p, w.it.b, &c, &bad);
+        if (bad) atomicOr(p.status, kStatusPage);
     }
     __syncthreads();
     w.imin = sh_imin;
@@ -413,9 +456,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_cons
     if (w.e0 >= w.e1) {   // no keys: nothing but the rows' empty sums
         const int split = w.it.part ? p.chunks[0] + w.it.chunk : w.it.chunk;
         for (int x = warp; x < rows; x += kThreads / 32) {
-            const PagedRow u = paged_row(p, w.it, w.it.rb * rows + x);
-            if (!u.there) break;
-            const size_t at = paged_out_row(p, u);
+            if (out_row[x] < 0) break;
+            const size_t at = (size_t)out_row[x];
             if (p.nsplit > 1) {
                 if (lane == 0) p.ml[at * p.nsplit + split] = make_float2(-INFINITY, 0.f);
             } else {
@@ -425,6 +467,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_cons
         }
         return;
     }
+    if (warp == 5) {
+        tmem_alloc(&tmem_base_sh, 256);
+        tmem_relinquish();
+    }
     // Q, one row per thread (zeros for frozen rows and those without a token)
     if (t < 128 && w.any_ord) {
         const bool have = row.i >= 0 && !row.frozen;
@@ -433,64 +479,67 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_cons
         for (int c = 0; c < kD / 8; ++c) {
             uint4 x = make_uint4(0, 0, 0, 0);
             if (have && 8 * c < p.d) x = __ldg(src + c);
-            *reinterpret_cast<uint4*>(sm + Smem<kD>::q + (c >> 3) * Smem<kD>::q_atom + sw128_offset(t, 16 * (c & 7))) = x;
+            *reinterpret_cast<uint4*>(sm + S::q + (c >> 3) * S::q_atom + sw128_offset(t, 16 * (c & 7))) = x;
         }
         fence_proxy_async_smem();
     }
-    if (warp == 5) {
-        tmem_alloc(&tmem_base_sh, 256);
-        tmem_relinquish();
+    // pages that the item needs and the table does not have
+    bool lost = false;
+    {
+        const int nbox = TK / P.box;
+        for (int b = t; b < (w.e1 - w.e0) * nbox; b += kThreads) {
+            const int bx = paged_tile(w.g, w.e0 + b / nbox) * TK + (b % nbox) * P.box;
+            if (box_seen(w.g, bx, P.box) && paged_page(p, w.it, bx) < 0) lost = true;
+        }
     }
     tc_fence_before();
-    __syncthreads();
+    w.lost = __syncthreads_or(lost) != 0;
     tc_fence_after();
+    if (w.lost && t == 0) atomicOr(p.status, kStatusPage);
     const uint32_t tmem = tmem_base_sh;
     volatile int* abort = &abort_flag;
 
     if (warp < 4) {
         switch (rows) {
-            case 32: row_warps<kD, 4>(P, w, row, sm, bars, mask, tmem, abort); break;
-            case 64: row_warps<kD, 2>(P, w, row, sm, bars, mask, tmem, abort); break;
-            default: row_warps<kD, 1>(P, w, row, sm, bars, mask, tmem, abort); break;
+            case 32: row_warps<kD, 4>(P, w, row, sm, bars, out_row, tmem, abort); break;
+            case 64: row_warps<kD, 2>(P, w, row, sm, bars, out_row, tmem, abort); break;
+            default: row_warps<kD, 1>(P, w, row, sm, bars, out_row, tmem, abort); break;
         }
     } else if (warp == 4) {
-        load_warp<kD>(P, w, &P.tm_k, sm + Smem<kD>::k, bars.k_full, bars.k_empty, w.any_ord, mask, abort);
-    } else if (warp == 6) {
-        load_warp<kD>(P, w, &P.tm_v, sm + Smem<kD>::v, bars.v_full, bars.v_empty, true, nullptr, abort);
+        load_warp<kD>(P, w, sm, bars, abort);
     } else if (lane == 0) {
         const uint32_t id_s = idesc_bf16(128, TK, 0, 0), id_o = idesc_bf16(128, kD, 0, 1);
-        const uint32_t sq = smem_u32(sm + Smem<kD>::q);
+        const uint32_t sq = smem_u32(sm + S::q), ring = smem_u32(sm + S::ring);
         const int n = w.e1 - w.e0;
         bool ok = true;
         auto issue_s = [&](int j) -> bool {
-            const int s = j & 1;
-            if (!mbar_wait(&bars.k_full[s], (j >> 1) & 1, abort, p.status, kStatusTimeout)) return false;
+            const int ld = w.k_load(j), s = ld % S::slots;
+            if (!mbar_wait(&bars.full[s], (ld / S::slots) & 1, abort, p.status, kStatusTimeout)) return false;
             if (j > 0 && !mbar_wait(&bars.s_empty, (j - 1) & 1, abort, p.status, kStatusTimeout)) return false;
             tc_fence_after();
-            const uint32_t sk = smem_u32(sm + Smem<kD>::k + s * Smem<kD>::tile);
+            const uint32_t sk = ring + s * S::tile;
 #pragma unroll
             for (int k = 0; k < kD / 16; ++k)
-                mma_ss(tmem, sdesc_sw128(sq + (k >> 2) * Smem<kD>::q_atom + (k & 3) * 32, 16, 1024),
-                       sdesc_sw128(sk + (k >> 2) * Smem<kD>::atom + (k & 3) * 32, 16, 1024), id_s, k > 0);
+                mma_ss(tmem, sdesc_sw128(sq + (k >> 2) * S::q_atom + (k & 3) * 32, 16, 1024),
+                       sdesc_sw128(sk + (k >> 2) * S::atom + (k & 3) * 32, 16, 1024), id_s, k > 0);
             mma_commit(&bars.s_full);
-            mma_commit(&bars.k_empty[s]);
+            mma_commit(&bars.empty[s]);
             return true;
         };
         if (w.any_ord) ok = issue_s(0);
         for (int j = 0; j < n && ok; ++j) {
-            const int s = j & 1;
-            if (j + 1 < n && w.any_ord && !(ok = issue_s(j + 1))) break;
-            if (!w.any_ord) mbar_arrive(&bars.k_empty[s]);   // no S reads this stage
-            if (!(ok = mbar_wait(&bars.v_full[s], (j >> 1) & 1, abort, p.status, kStatusTimeout))) break;
+            if (w.any_ord && j + 1 < n && !(ok = issue_s(j + 1))) break;
+            const int ld = w.v_load(j), s = ld % S::slots;
+            if (!(ok = mbar_wait(&bars.full[s], (ld / S::slots) & 1, abort, p.status, kStatusTimeout))) break;
             if (!(ok = mbar_wait(&bars.p_ready, j & 1, abort, p.status, kStatusTimeout))) break;
             tc_fence_after();
-            const uint32_t sv = smem_u32(sm + Smem<kD>::v + s * Smem<kD>::tile);
+            const uint32_t sv = ring + s * S::tile;
 #pragma unroll
             for (int k = 0; k < TK / 16; ++k)
-                mma_ts(tmem + kColO, tmem + kColP + 8 * k, sdesc_sw128(sv + k * 2048, Smem<kD>::atom, 1024), id_o,
+                mma_ts(tmem + kColO, tmem + kColP + 8 * k, sdesc_sw128(sv + k * 2048, S::atom, 1024), id_o,
                        (j > 0 || k > 0) ? 1u : 0u);
             mma_commit(&bars.o_done);
-            mma_commit(&bars.v_empty[s]);
+            mma_commit(&bars.empty[s]);
         }
         mma_commit(&bars.mma_idle);
         mbar_wait_bounded(&bars.mma_idle, 0, kWaitLimitNs);

@@ -378,53 +378,76 @@ def saf_attn_bwd_prepared(q, k, v, o, do, lse, a, r, frozen, state, dq=None, dk=
     return dq, dk, dv
 
 
-def _on(t, dev, dtype=None, name="tensor"):
-    """Address of an optional contiguous tensor on device `dev`."""
+# The calls below are short enough on the GPU that their checks in Python count: each tensor is
+# looked at once, and what is wrong is named on a second look (_refuse).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_I64x9 = ctypes.c_int64 * 9
+
+
+def _at(t, idx, dtype):
+    """Address of an optional contiguous tensor of `dtype` on device `idx`."""
     if t is None:
         return None
-    if t.device != dev:
-        raise ValueError(f"{name} must live on {dev}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != idx or t.dtype is not dtype or not t.is_contiguous():
+        _refuse(t, idx, dtype)
     return t.data_ptr()
 
 
-def _cuda(t):
-    if not t.is_cuda:
+def _refuse(t, idx, dtype):
+    if t.get_device() != idx:
+        raise ValueError(f"a tensor of shape {tuple(t.shape)} must live on cuda:{idx}")
+    if t.dtype is not dtype:
+        raise TypeError(f"a tensor of shape {tuple(t.shape)} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"a tensor of shape {tuple(t.shape)} must be contiguous")
+
+
+def _device(t):
+    idx = t.get_device()
+    if idx < 0:
         raise ValueError("tensor must live on a CUDA device")
-    return t.device
+    return idx
+
+
+def _shapes(*given):
+    """Raise for the first (name, tensor or None, shape) whose shape is another."""
+    for name, t, shape in given:
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _flags(frozen, H):
     """The frozen flags as H bytes; a bytes object is passed on as it is."""
     if frozen is None:
         return None
-    if isinstance(frozen, bytes):
+    if type(frozen) is bytes:
         if len(frozen) != H:
             raise ValueError("frozen mask must have H entries")
         return frozen
     return bytes(_frozen_bytes(frozen, H))
 
 
-def _run(where, dev, stream, fn, *args):
-    """Call fn(*args, stream) with `dev` current, on `stream` or the device's current one."""
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
-            return _run(where, dev, stream, fn, *args)
-    st = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+def _run(where, fn, idx, stream, *args):
+    """fn(*args, stream) with device `idx` current, on `stream` or the device's current one."""
+    if torch.cuda.current_device() != idx:
+        with torch.cuda.device(idx):
+            return _run(where, fn, idx, stream, *args)
+    if stream is not None:
+        raw = stream.cuda_stream
+    else:
+        raw = _raw_stream(idx) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    st = fn(*args, raw)
     if st != SAF_OK:
         raise SafError(st, where)
 
 
-def _prior(a, r, H, dev, need):
+def _prior(a, r, H, idx, none):
     """Addresses and row length of a, r ([H, ld_prior] fp32, or None when nothing is frozen)."""
     if a is None or r is None:
-        return None, None, need
-    if a.dim() != 2 or a.shape != r.shape or a.shape[0] != H:
+        return None, None, none
+    shape = a.shape
+    if len(shape) != 2 or shape[0] != H or r.shape != shape:
         raise ValueError("a and r must both be [H, ld_prior]")
-    return _on(a, dev, torch.float32, "a"), _on(r, dev, torch.float32, "r"), a.shape[1]
+    return _at(a, idx, torch.float32), _at(r, idx, torch.float32), shape[1]
 
 
 def saf_attn_fwd_window(q, k, v, a, r, frozen, window, sinks=0, state=None, o=None, lse=None, workspace=None,
@@ -433,21 +456,20 @@ def saf_attn_fwd_window(q, k, v, a, r, frozen, window, sinks=0, state=None, o=No
     `sinks` (query i: keys j <= i with i - j < window or j < sinks; window 0: every key);
     returns (o, lse). q: [B, H, T, d]; k, v: [B, Hkv, T, d]; a, r, frozen as for
     saf_attn_fwd_gqa; state: a prepared frozen-pattern state (saf_frozen_prepare) or None."""
-    dev = _cuda(v)
+    idx, dt = _device(v), v.dtype
     B, H, Hkv, T, d = _gqa_shape(q, v, frozen)
-    dt, f32 = v.dtype, torch.float32
-    _same_shapes(("q", q, (B, H, T, d)), ("k", k, v.shape), ("o", o, (B, H, T, d)), ("lse", lse, (B, H, T)))
+    full, rows = (B, H, T, d), (B, H, T)
+    _shapes(("q", q, full), ("k", k, v.shape), ("o", o, full), ("lse", lse, rows))
     if o is None:
-        o = torch.empty((B, H, T, d), dtype=dt, device=dev)
+        o = torch.empty(full, dtype=dt, device=v.device)
     if lse is None:
-        lse = torch.empty((B, H, T), dtype=f32, device=dev)
+        lse = torch.empty(rows, dtype=torch.float32, device=v.device)
     if workspace is None:
-        workspace = alloc_workspace(B, H, T, d, dt, False, dev)
-    ap, rp, ld = _prior(a, r, H, dev, T)
-    _run("saf_attn_fwd_window", dev, stream, _lib.saf_attn_fwd_window, _on(q, dev, dt, "q"), _on(k, dev, dt, "k"),
-         _on(v, dev), ap, rp, ld, _flags(frozen, H), _on(state, dev, torch.uint8, "state"), int(window), int(sinks), B,
-         H, Hkv, T, d, _dt(v), _on(o, dev, dt, "o"), _on(lse, dev, f32, "lse"),
-         _on(workspace, dev, torch.uint8, "workspace"), workspace.numel())
+        workspace = alloc_workspace(B, H, T, d, dt, False, v.device)
+    ap, rp, ld = _prior(a, r, H, idx, T)
+    _run("saf_attn_fwd_window", _lib.saf_attn_fwd_window, idx, stream, _at(q, idx, dt), _at(k, idx, dt),
+         _at(v, idx, dt), ap, rp, ld, _flags(frozen, H), _at(state, idx, torch.uint8), int(window), int(sinks), B, H, Hkv, T, d,
+         _dt(v), _at(o, idx, dt), _at(lse, idx, torch.float32), _at(workspace, idx, torch.uint8), workspace.numel())
     return o, lse
 
 
@@ -455,58 +477,44 @@ def saf_attn_bwd_window(q, k, v, o, do, lse, a, r, frozen, window, sinks=0, stat
                         workspace=None, stream=None):
     """Backward of saf_attn_fwd_window (o, lse: its outputs for the same inputs); returns
     dq [B, H, T, d] and dk, dv [B, Hkv, T, d]."""
-    dev = _cuda(v)
+    idx, dt = _device(v), v.dtype
     B, H, Hkv, T, d = _gqa_shape(q, v, frozen)
-    dt, f32 = v.dtype, torch.float32
-    full = (B, H, T, d)
-    _same_shapes(("q", q, full), ("k", k, v.shape), ("o", o, full), ("do", do, full), ("lse", lse, (B, H, T)),
-                 ("dq", dq, full), ("dk", dk, v.shape), ("dv", dv, v.shape))
-    dq = torch.empty(full, dtype=dt, device=dev) if dq is None else dq
-    dk = torch.empty(v.shape, dtype=dt, device=dev) if dk is None else dk
-    dv = torch.empty(v.shape, dtype=dt, device=dev) if dv is None else dv
+    full, kv = (B, H, T, d), v.shape
+    _shapes(("q", q, full), ("k", k, kv), ("o", o, full), ("do", do, full), ("lse", lse, (B, H, T)),
+            ("dq", dq, full), ("dk", dk, kv), ("dv", dv, kv))
+    dq = torch.empty(full, dtype=dt, device=v.device) if dq is None else dq
+    dk = torch.empty(kv, dtype=dt, device=v.device) if dk is None else dk
+    dv = torch.empty(kv, dtype=dt, device=v.device) if dv is None else dv
     if workspace is None:
-        workspace = alloc_workspace(B, H, T, d, dt, True, dev)
-    ap, rp, ld = _prior(a, r, H, dev, T)
-    _run("saf_attn_bwd_window", dev, stream, _lib.saf_attn_bwd_window, _on(q, dev, dt, "q"), _on(k, dev, dt, "k"),
-         _on(v, dev), _on(o, dev, dt, "o"), _on(do, dev, dt, "do"), _on(lse, dev, f32, "lse"), ap, rp, ld,
-         _flags(frozen, H), _on(state, dev, torch.uint8, "state"), int(window), int(sinks), B, H, Hkv, T, d, _dt(v),
-         _on(dq, dev, dt, "dq"), _on(dk, dev, dt, "dk"), _on(dv, dev, dt, "dv"),
-         _on(workspace, dev, torch.uint8, "workspace"), workspace.numel())
+        workspace = alloc_workspace(B, H, T, d, dt, True, v.device)
+    ap, rp, ld = _prior(a, r, H, idx, T)
+    _run("saf_attn_bwd_window", _lib.saf_attn_bwd_window, idx, stream, _at(q, idx, dt), _at(k, idx, dt),
+         _at(v, idx, dt), _at(o, idx, dt), _at(do, idx, dt), _at(lse, idx, torch.float32), ap, rp, ld,
+         _flags(frozen, H), _at(state, idx, torch.uint8), int(window), int(sinks), B, H, Hkv, T, d, _dt(v), _at(dq, idx, dt),
+         _at(dk, idx, dt), _at(dv, idx, dt), _at(workspace, idx, torch.uint8), workspace.numel())
     return dq, dk, dv
 
 
-def _same_shapes(*given):
-    for name, t, shape in given:
-        if t is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _counts(ctx, n_new, page_table, B, dev):
-    """Addresses of the int32 counts and the page table of B sequences."""
-    _same_shapes(("ctx", ctx, (B,)), ("n_new", n_new, (B,)))
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("page_table must be [B, max_pages]")
-    i32 = torch.int32
-    return _on(ctx, dev, i32, "ctx"), _on(n_new, dev, i32, "n_new"), _on(page_table, dev, i32, "page_table")
-
-
-def _caches(k_cache, v_cache, d, dt, dev):
-    if v_cache.dim() != 4 or v_cache.shape[3] != d:
-        raise ValueError("the caches must be [num_pages, Hkv, page_size, d]")
-    _same_shapes(("k_cache", k_cache, v_cache.shape))
-    return _on(k_cache, dev, dt, "k_cache"), _on(v_cache, dev, dt, "v_cache")
-
-
-def _rows(t, dev, dt, name):
+def _strided(t, idx, dt):
     """Address and (sequence, head, token) strides of a [B, heads, T, d] tensor with contiguous rows."""
-    if t.device != dev:
-        raise ValueError(f"{name} must live on {dev}")
-    if t.dtype != dt:
-        raise TypeError(f"{name} must be {dt}")
+    if t is None:
+        return None, (0, 0, 0)
     s = t.stride()
+    if t.get_device() != idx or t.dtype is not dt:
+        _refuse(t, idx, dt)
     if s[3] != 1:
-        raise ValueError(f"{name} must have contiguous rows")
+        raise ValueError(f"a tensor of shape {tuple(t.shape)} must have contiguous rows")
     return t.data_ptr(), s[:3]
+
+
+def _table(ctx, n_new, page_table, B):
+    """max_pages, after the shapes of the counts and the page table of B sequences."""
+    shape = page_table.shape
+    if len(shape) != 2 or shape[0] != B:
+        raise ValueError("page_table must be [B, max_pages]")
+    if ctx.shape != (B,) or (n_new is not None and n_new.shape != (B,)):
+        raise ValueError("ctx and n_new must be [B]")
+    return shape[1]
 
 
 def saf_kv_append(k, v, k_cache, v_cache, page_table, ctx, n_new=None, q=None, q_out=None, inv_freq=None,
@@ -517,40 +525,37 @@ def saf_kv_append(k, v, k_cache, v_cache, page_table, ctx, n_new=None, q=None, q
     without q). ctx, n_new: int32 [B] on the device (n_new None: T tokens each).
     inv_freq: rope_dim / 2 angles per position (CPU float64 tensor or a sequence; None: no
     rotation). frozen: flags of the H query heads (their q, and keys that no ordinary head
-    reads, are left alone); without q it also gives H (default Hkv). status: an int32 or uint8
-    CUDA tensor whose first 8 bytes, zeroed once by the caller, collect errors for
-    saf_device_status; by default none are kept."""
-    dev, dt = _cuda(v), v.dtype
+    reads, are left alone); without q it also gives H (default Hkv). status: a CUDA tensor
+    whose first 8 bytes, zeroed once by the caller, collect errors for saf_device_status
+    (None: errors are not recorded)."""
+    idx, dt, i32 = _device(v), v.dtype, torch.int32
     B, Hkv, T, d = v.shape
     H = q.shape[1] if q is not None else len(frozen) if frozen is not None else Hkv
-    _same_shapes(("k", k, v.shape), ("q", q, (B, H, T, d)), ("q_out", q_out, (B, H, T, d)))
-    ctxp, newp, table = _counts(ctx, n_new, page_table, B, dev)
-    kc, vc = _caches(k_cache, v_cache, d, dt, dev)
-    if v_cache.shape[1] != Hkv:
-        raise ValueError("the caches' heads are not v's")
-    none = (None, (0, 0, 0))
-    qp, qs = _rows(q, dev, dt, "q") if q is not None else none
-    kp, ks = _rows(k, dev, dt, "k") if k is not None else none
-    vp, vs = _rows(v, dev, dt, "v")
+    num_pages, heads, page_size, width = v_cache.shape
+    if heads != Hkv or width != d:
+        raise ValueError("the caches must be [num_pages, Hkv, page_size, d]")
+    _shapes(("k", k, v.shape), ("q", q, (B, H, T, d)), ("q_out", q_out, (B, H, T, d)), ("k_cache", k_cache, v_cache.shape))
+    max_pages = _table(ctx, n_new, page_table, B)
+    qp, qs = _strided(q, idx, dt)
+    kp, ks = _strided(k, idx, dt)
+    vp, vs = _strided(v, idx, dt)
     if q is not None and q_out is None:
         # rows that are not written (frozen heads, rows without a token) come back as zeros
-        q_out = torch.zeros((B, H, T, d), dtype=dt, device=dev)
+        q_out = torch.zeros((B, H, T, d), dtype=dt, device=v.device)
     freq, rope = None, 0
     if inv_freq is not None:
-        freq = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
-        rope = 2 * freq.numel()
-    if status is None:
-        status = torch.zeros(2, dtype=torch.int32, device=dev)
-    elif status.numel() * status.element_size() < 8:
+        if not (torch.is_tensor(inv_freq) and inv_freq.dtype is torch.float64 and inv_freq.get_device() < 0
+                and inv_freq.is_contiguous()):
+            inv_freq = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
+        freq, rope = inv_freq.data_ptr(), 2 * inv_freq.numel()
+    if status is not None and status.numel() * status.element_size() < 8:
         raise ValueError("status needs 8 bytes")
-    _run("saf_kv_append", dev, stream, _lib.saf_kv_append, qp, kp, vp, _I64x9(*qs, *ks, *vs), ctxp, newp, table,
-         page_table.shape[1], freq.data_ptr() if rope else None, rope, int(bool(interleaved)), int(pos_base),
-         _flags(frozen, H), B, H, Hkv, T, d, v_cache.shape[0], v_cache.shape[2], _dt(v),
-         _on(q_out, dev, dt, "q_out"), kc, vc, _on(status, dev, None, "status"))
+    _run("saf_kv_append", _lib.saf_kv_append, idx, stream, qp, kp, vp, _I64x9(*qs, *ks, *vs), _at(ctx, idx, i32),
+         _at(n_new, idx, i32), _at(page_table, idx, i32), max_pages, freq if rope else None, rope,
+         1 if interleaved else 0, pos_base, _flags(frozen, H), B, H, Hkv, T, d, num_pages, page_size, _dt(v),
+         _at(q_out, idx, dt), _at(k_cache, idx, dt), _at(v_cache, idx, dt),
+         None if status is None else _at(status, idx, status.dtype))
     return q_out
-
-
-_I64x9 = ctypes.c_int64 * 9
 
 
 def saf_attn_paged_workspace_bytes(B, H, Hkv, T, d, max_len, dtype, prefix_len=0) -> int:
@@ -566,33 +571,30 @@ def alloc_paged_workspace(B, H, Hkv, T, d, max_len, dtype, prefix_len=0, device=
     return w
 
 
-def _paged(where, q, k_cache, v_cache, prefix, page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o, lse,
-           workspace, stream):
-    dev, dt = _cuda(q), q.dtype
-    B, H, T, d = q.shape
-    kc, vc = _caches(k_cache, v_cache, d, dt, dev)
-    num_pages, Hkv, page_size, _ = v_cache.shape
-    ctxp, newp, table = _counts(ctx, n_new, page_table, B, dev)
-    _same_shapes(("o", o, (B, H, T, d)), ("lse", lse, (B, H, T)))
-    P = 0
-    if prefix is not None:
-        pages, P = prefix[0], int(prefix[1])
-        if pages is not None and pages.numel() < -(-P // page_size):
-            raise ValueError("prefix_pages holds fewer pages than prefix_len tokens take")
-        prefix = (_on(pages, dev, torch.int32, "prefix_pages"), P)
-    else:
-        prefix = ()
+def _paged(where, fn, q, k_cache, v_cache, prefix, P, page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o,
+           lse, workspace, stream):
+    idx, dt, i32 = _device(q), q.dtype, torch.int32
+    full = q.shape
+    B, H, T, d = full
+    num_pages, Hkv, page_size, width = v_cache.shape
+    if width != d or (k_cache is not None and k_cache.shape != v_cache.shape):
+        raise ValueError("the caches must both be [num_pages, Hkv, page_size, d]")
+    max_pages = _table(ctx, n_new, page_table, B)
     if o is None:
-        o = torch.empty((B, H, T, d), dtype=dt, device=dev)
+        o = torch.empty(full, dtype=dt, device=q.device)
+    elif o.shape != full:
+        raise ValueError(f"o must have shape {tuple(full)}")
     if lse is None:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
+        lse = torch.empty(full[:3], dtype=torch.float32, device=q.device)
+    elif lse.shape != full[:3]:
+        raise ValueError(f"lse must have shape {tuple(full[:3])}")
     if workspace is None:
-        workspace = alloc_paged_workspace(B, H, Hkv, T, d, max_len, dt, P, dev)
-    ap, rp, ld = _prior(a, r, H, dev, P + max_len)
-    _run(where, dev, stream, getattr(_lib, where), _on(q, dev, dt, "q"), kc, vc, *prefix, table, page_table.shape[1],
-         ctxp, newp, ap, rp, ld, _flags(frozen, H), int(window), int(sinks), B, H, Hkv, T, d, int(max_len), num_pages,
-         page_size, _dt(q), _on(o, dev, dt, "o"), _on(lse, dev, torch.float32, "lse"),
-         _on(workspace, dev, torch.uint8, "workspace"), workspace.numel())
+        workspace = alloc_paged_workspace(B, H, Hkv, T, d, max_len, dt, P, q.device)
+    ap, rp, ld = _prior(a, r, H, idx, P + max_len)
+    _run(where, fn, idx, stream, _at(q, idx, dt), _at(k_cache, idx, dt), _at(v_cache, idx, dt), *prefix,
+         _at(page_table, idx, i32), max_pages, _at(ctx, idx, i32), _at(n_new, idx, i32), ap, rp, ld,
+         _flags(frozen, H), int(window), int(sinks), B, H, Hkv, T, d, max_len, num_pages, page_size, _dt(q), _at(o, idx, dt),
+         _at(lse, idx, torch.float32), _at(workspace, idx, torch.uint8), workspace.numel())
     return o, lse
 
 
@@ -603,8 +605,8 @@ def saf_attn_paged(q, k_cache, v_cache, page_table, ctx, max_len, n_new=None, a=
     ctx[b] + t; rows t >= n_new[b] come back as o = 0, lse = -inf. max_len: an upper bound of
     ctx[b] + n_new[b]. a, r [H, ld_prior >= max_len] and frozen as for saf_attn_fwd; window and
     sinks as for saf_attn_fwd_window. workspace: alloc_paged_workspace."""
-    return _paged("saf_attn_paged", q, k_cache, v_cache, None, page_table, ctx, max_len, n_new, a, r, frozen, window,
-                  sinks, o, lse, workspace, stream)
+    return _paged("saf_attn_paged", _lib.saf_attn_paged, q, k_cache, v_cache, (), 0, page_table, ctx, max_len, n_new, a,
+                  r, frozen, window, sinks, o, lse, workspace, stream)
 
 
 def saf_attn_paged_shared(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, ctx, max_len, n_new=None, a=None,
@@ -612,8 +614,11 @@ def saf_attn_paged_shared(q, k_cache, v_cache, prefix_pages, prefix_len, page_ta
     """saf_attn_paged for sequences that share a prefix of prefix_len tokens, held once in the
     pages prefix_pages (int32, on the device): token t of sequence b stands at position
     prefix_len + ctx[b] + t, and ctx, n_new, max_len and page_table count own tokens."""
-    return _paged("saf_attn_paged_shared", q, k_cache, v_cache, (prefix_pages, prefix_len), page_table, ctx, max_len,
-                  n_new, a, r, frozen, window, sinks, o, lse, workspace, stream)
+    if prefix_pages is not None and prefix_pages.numel() * v_cache.shape[2] < prefix_len:
+        raise ValueError("prefix_pages holds fewer pages than prefix_len tokens take")
+    prefix = (_at(prefix_pages, _device(q), torch.int32), prefix_len)
+    return _paged("saf_attn_paged_shared", _lib.saf_attn_paged_shared, q, k_cache, v_cache, prefix, prefix_len,
+                  page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o, lse, workspace, stream)
 
 
 def saf_set_trace_events(kernel: int, start=None, stop=None) -> None:
