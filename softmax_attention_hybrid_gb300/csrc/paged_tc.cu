@@ -11,9 +11,11 @@
 // others: the softmax of a row runs on 2 (4) threads, the MMAs cost the same, and the
 // copies' (m, l, O) are added at the end like items.
 //
-// Warps (192 threads, two CTAs per SM): 0-3 rows, one thread per row of the tile (TMEM lane);
-// 4 loads K and V (each of its lanes fetches one page of the tile, and looks up a later
-// tile's page while it waits); 5 owns tensor memory and issues the MMAs.
+// Warps (256 threads, two CTAs per SM): 0-3 rows, one thread per row of the tile (TMEM lane);
+// 4 loads K and V (each of its lanes fetches one page of the tile); 5 owns tensor memory and
+// issues S, 6 issues P V; 7 idles. Two issuers, since a tile's waits, MMAs and commits take
+// one about 1600 cycles at d = 64 (traced; a wait costs about 100 and a commit as much),
+// longer than the softmax of a tile.
 // Tensor memory (256 columns): S [0, 64) fp32 | P [64, 96) bf16 pairs | O [128, 128 + d).
 // S has columns of its own so that the next tile's S runs under this one's softmax.
 // Shared memory: Q, and a ring of slots of one tile of K or V each, filled in the order in
@@ -31,7 +33,11 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 256;
+// Register split (setmaxnreg): warps 4-7 drop to kRegsOther, the row warps rise to kRegsRows, within
+// the kRegsLaunch per thread that the launch hands out (checked on the host).
+constexpr int kRegsLaunch = 128, kRegsRows = 184, kRegsOther = 72;
+static_assert(kRegsRows + kRegsOther <= 2 * kRegsLaunch, "register split too large");
 constexpr int TK = kTcTile;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -63,7 +69,7 @@ struct Smem {
 template <int kD>
 struct Bars {
     uint64_t full[Smem<kD>::slots], empty[Smem<kD>::slots];
-    uint64_t s_full, s_empty, p_ready, o_done, mma_idle;
+    uint64_t s_full, s_empty, p_ready, o_done, mma_idle[2];
 };
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -108,6 +114,11 @@ struct Work {
     }
 };
 
+// A wait of a converged warp: every lane waits and the warp goes on, or gives up, together.
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, kStatusTimeout));
+}
+
 // Whether keys [bx, bx + box) of the part hold one that some row sees.
 __device__ __forceinline__ bool box_seen(const PagedRange& g, int bx, int box) {
     return bx < g.hi && (bx + box > g.lo || bx < g.sink);
@@ -127,14 +138,32 @@ __device__ __forceinline__ void load_warp(const TcParams& P, const Work& w, uint
         tma_prefetch_desc(&P.tm_k);
         tma_prefetch_desc(&P.tm_v);
     }
-    auto look = [&](int j) -> int {   // my box's page, -1: nothing to fetch
-        if (lane >= nbox || j >= n) return -1;
-        const int bx = paged_tile(w.g, w.e0 + j) * TK + lane * P.box;
-        return box_seen(w.g, bx, P.box) ? paged_page(p, w.it, bx) : -1;
+    // The pages of a batch of tiles are looked up together, lane l those of tile l / nbox, box
+    // l mod nbox, a batch ahead of their use: a lookup for each tile would wait for the memory
+    // in every one.
+    const int batch = 32 / nbox;
+    auto look = [&](int first) -> int {   // a page as the table has it, -1: nothing to fetch
+        const int j = first + lane / nbox;
+        if (j >= n) return -1;
+        const int bx = paged_tile(w.g, w.e0 + j) * TK + (lane & (nbox - 1)) * P.box;
+        if (!box_seen(w.g, bx, P.box)) return -1;
+        const int at = bx >> p.page_log2;
+        return __ldg(w.it.part ? p.page_table + (size_t)w.it.b * p.max_pages + at : p.prefix_pages + at);
+    };
+    int looked = look(0), ahead = look(batch);   // tiles [base, base + batch), and the batch behind
+    int base = 0;
+    auto page_of = [&](int j) -> int {   // my box's page of tile j (ascending), -1: nothing to fetch
+        if (j == base + batch) {
+            base = j;
+            looked = ahead;
+            ahead = look(base + batch);
+        }
+        const int pg = __shfl_sync(0xffffffffu, looked, ((j - base) * nbox + lane) & 31);
+        return lane < nbox && pg >= 0 && pg < p.num_pages ? pg : -1;
     };
     auto fetch = [&](int load, const CUtensorMap* map, int j, int pg) -> bool {
         const int s = load % S::slots;
-        if (!mbar_wait_warp(&bars.empty[s], ((load / S::slots) & 1) ^ 1u, abort, p.status, kStatusTimeout)) return false;
+        if (!wait_all(&bars.empty[s], ((load / S::slots) & 1) ^ 1u, abort, p.status)) return false;
         const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0);
         if (lane == 0) mbar_expect_tx(&bars.full[s], __popc(have) * box_bytes);
         __syncwarp();
@@ -148,14 +177,13 @@ __device__ __forceinline__ void load_warp(const TcParams& P, const Work& w, uint
         __syncwarp();
         return true;
     };
-    int pg = look(0), next = look(1);
+    int pg = page_of(0);
     bool ok = !w.any_ord || fetch(0, &P.tm_k, 0, pg);
     for (int j = 0; j < n && ok; ++j) {
-        const int later = look(j + 2);
+        const int next = j + 1 < n ? page_of(j + 1) : -1;
         if (w.any_ord && j + 1 < n) ok = fetch(w.k_load(j + 1), &P.tm_k, j + 1, next);
         ok = ok && fetch(w.v_load(j), &P.tm_v, j, pg);
         pg = next;
-        next = later;
     }
 }
 
@@ -420,7 +448,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_cons
         mbar_init(&bars.s_empty, 4);
         mbar_init(&bars.p_ready, 4);
         mbar_init(&bars.o_done, 1);
-        mbar_init(&bars.mma_idle, 1);
+        mbar_init(&bars.mma_idle[0], 1);
+        mbar_init(&bars.mma_idle[1], 1);
         fence_mbar_init();
     }
     __syncthreads();
@@ -499,50 +528,60 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_cons
     const uint32_t tmem = tmem_base_sh;
     volatile int* abort = &abort_flag;
 
+    const int n = w.e1 - w.e0;
+    const uint32_t ring = smem_u32(sm + S::ring);
     if (warp < 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
         switch (rows) {
             case 32: row_warps<kD, 4>(P, w, row, sm, bars, out_row, tmem, abort); break;
             case 64: row_warps<kD, 2>(P, w, row, sm, bars, out_row, tmem, abort); break;
             default: row_warps<kD, 1>(P, w, row, sm, bars, out_row, tmem, abort); break;
         }
-    } else if (warp == 4) {
-        load_warp<kD>(P, w, sm, bars, abort);
-    } else if (lane == 0) {
-        const uint32_t id_s = idesc_bf16(128, TK, 0, 0), id_o = idesc_bf16(128, kD, 0, 1);
-        const uint32_t sq = smem_u32(sm + S::q), ring = smem_u32(sm + S::ring);
-        const int n = w.e1 - w.e0;
-        bool ok = true;
-        auto issue_s = [&](int j) -> bool {
-            const int ld = w.k_load(j), s = ld % S::slots;
-            if (!mbar_wait(&bars.full[s], (ld / S::slots) & 1, abort, p.status, kStatusTimeout)) return false;
-            if (j > 0 && !mbar_wait(&bars.s_empty, (j - 1) & 1, abort, p.status, kStatusTimeout)) return false;
-            tc_fence_after();
-            const uint32_t sk = ring + s * S::tile;
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == 4) {
+            load_warp<kD>(P, w, sm, bars, abort);
+        } else if (warp == 5) {
+            // S of tile j, when K is there and the rows have read S of tile j - 1
+            const uint32_t id_s = idesc_bf16(128, TK, 0, 0);
+            const uint64_t d_q = sdesc_sw128(smem_u32(sm + S::q), 16, 1024);   // K-major, as K
+            const uint64_t d_ring = sdesc_sw128(ring, 16, 1024);
+            for (int j = 0; j < n && w.any_ord; ++j) {
+                const int ld = w.k_load(j), s = ld % S::slots;
+                if (!wait_all(&bars.full[s], (ld / S::slots) & 1, abort, p.status)) break;
+                if (j > 0 && !wait_all(&bars.s_empty, (j - 1) & 1, abort, p.status)) break;
+                tc_fence_after();
+                const uint64_t d_k = sdesc_advance(d_ring, s * S::tile);
 #pragma unroll
-            for (int k = 0; k < kD / 16; ++k)
-                mma_ss(tmem, sdesc_sw128(sq + (k >> 2) * S::q_atom + (k & 3) * 32, 16, 1024),
-                       sdesc_sw128(sk + (k >> 2) * S::atom + (k & 3) * 32, 16, 1024), id_s, k > 0);
-            mma_commit(&bars.s_full);
-            mma_commit(&bars.empty[s]);
-            return true;
-        };
-        if (w.any_ord) ok = issue_s(0);
-        for (int j = 0; j < n && ok; ++j) {
-            if (w.any_ord && j + 1 < n && !(ok = issue_s(j + 1))) break;
-            const int ld = w.v_load(j), s = ld % S::slots;
-            if (!(ok = mbar_wait(&bars.full[s], (ld / S::slots) & 1, abort, p.status, kStatusTimeout))) break;
-            if (!(ok = mbar_wait(&bars.p_ready, j & 1, abort, p.status, kStatusTimeout))) break;
-            tc_fence_after();
-            const uint32_t sv = ring + s * S::tile;
+                for (int k = 0; k < kD / 16; ++k)
+                    mma_ss_warp(tmem, sdesc_advance(d_q, (k >> 2) * S::q_atom + (k & 3) * 32),
+                                sdesc_advance(d_k, (k >> 2) * S::atom + (k & 3) * 32), id_s, k > 0);
+                mma_commit_warp(&bars.s_full);
+                mma_commit_warp(&bars.empty[s]);
+            }
+        } else if (warp == 6) {
+            // O += P V of tile j, when V and the rows' weights are there
+            const uint32_t id_o = idesc_bf16(128, kD, 0, 1);
+            const uint64_t d_ring = sdesc_sw128(ring, S::atom, 1024);   // MN-major
+            for (int j = 0; j < n; ++j) {
+                const int ld = w.v_load(j), s = ld % S::slots;
+                if (!wait_all(&bars.full[s], (ld / S::slots) & 1, abort, p.status)) break;
+                if (!wait_all(&bars.p_ready, j & 1, abort, p.status)) break;
+                tc_fence_after();
+                const uint64_t d_v = sdesc_advance(d_ring, s * S::tile);
 #pragma unroll
-            for (int k = 0; k < TK / 16; ++k)
-                mma_ts(tmem + kColO, tmem + kColP + 8 * k, sdesc_sw128(sv + k * 2048, S::atom, 1024), id_o,
-                       (j > 0 || k > 0) ? 1u : 0u);
-            mma_commit(&bars.o_done);
-            mma_commit(&bars.empty[s]);
+                for (int k = 0; k < TK / 16; ++k)
+                    mma_ts_warp(tmem + kColO, tmem + kColP + 8 * k, sdesc_advance(d_v, k * 2048), id_o,
+                                (j > 0 || k > 0) ? 1u : 0u);
+                mma_commit_warp(&bars.o_done);
+                mma_commit_warp(&bars.empty[s]);
+            }
         }
-        mma_commit(&bars.mma_idle);
-        mbar_wait_bounded(&bars.mma_idle, 0, kWaitLimitNs);
+        if (warp == 5 || warp == 6) {   // every MMA issued here is done before tensor memory is freed
+            mma_commit_warp(&bars.mma_idle[warp - 5]);
+            if (lane == 0) mbar_wait_bounded(&bars.mma_idle[warp - 5], 0, kWaitLimitNs);
+            __syncwarp();
+        }
     }
 
     tc_fence_before();
@@ -558,6 +597,11 @@ cudaError_t launch_d(const TcParams& P, cudaStream_t s) {
     const int smem = Smem<kD>::total + 1024;
     cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    // a build that launches with fewer registers could never hand the row warps theirs
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, paged_tc_kernel<kD>);
+    if (e != cudaSuccess) return e;
+    if (kRegsRows + kRegsOther > 2 * fa.numRegs) return cudaErrorInvalidConfiguration;
     return launch_ex(paged_tc_kernel<kD>, dim3((unsigned)P.a.items), dim3(kThreads), (size_t)smem, s, true, 1, P);
 }
 
