@@ -329,7 +329,7 @@ SAF_API int saf_attn_bwd_window(const void* q, const void* k, const void* v, con
  * status words. Calls that share one must be ordered on one stream, replays of captured
  * graphs among them.
  * Errors before any work is enqueued: SAF_EINVAL, SAF_EALIGN, SAF_EWORKSPACE,
- * SAF_EUNSUPPORTED, SAF_ECUDA as elsewhere (prefix_len + max_len <= 2^30 and B H T <= 2^30,
+ * SAF_EUNSUPPORTED, SAF_ECUDA as elsewhere (prefix_len + max_len <= 2^30 and B H T <= 2^29,
  * else SAF_EINVAL). B = 0 or T = 0 is an empty call. */
 SAF_API int saf_kv_append(const void* q, const void* k, const void* v, const int64_t* strides, const int32_t* ctx,
                           const int32_t* n_new, const int32_t* page_table, int max_pages, const double* inv_freq,

@@ -42,13 +42,13 @@ struct PagedArgs {
     int B, H, Hkv, G, T, d, ld;
     int max_pages, num_pages, page_log2;
     int P, max_len, window, sinks;
-    int tile;                      // keys per tile of the kernel that runs
+    int tile[2];                   // keys per tile of the kernel that runs: part 0, part 1
     int rows[2];                   // rows per block of the kernel that runs: part 0, part 1
     int nrb[2];                    // row blocks of part 0 and part 1
     int chunks[2];                 // items along the keys: part 0, part 1
     int per_chunk[2];              // tiles of an item
     int nsplit;                    // chunks[0] + chunks[1]
-    long long items0, items;       // items of part 0, of both parts
+    unsigned items0, items;        // items of part 0, of both parts
     float scale_log2;              // log2(e) / sqrt(d)
     HeadMask mask;
     uint8_t gheads[SAF_MAX_HEADS]; // query heads of key/value head hk at [hk G, hk G + G), ordinary first
@@ -61,18 +61,17 @@ struct PagedItem {
 
 // Items are numbered part 0 first (its items carry the most rows), and in a part the
 // chunks of one (sequence, key/value head, row block) next to each other.
-__device__ __forceinline__ PagedItem paged_item(const PagedArgs& p, long long idx) {
+__device__ __forceinline__ PagedItem paged_item(const PagedArgs& p, unsigned idx) {
     PagedItem it;
     it.part = idx >= p.items0;
     if (it.part) idx -= p.items0;
-    const int C = p.chunks[it.part];
-    long long u = idx / C;
+    const unsigned C = (unsigned)p.chunks[it.part], nrb = (unsigned)p.nrb[it.part];
+    unsigned u = idx / C;
     it.chunk = (int)(idx - u * C);
-    const int nrb = p.nrb[it.part];
-    it.rb = (int)(u % nrb);
-    u /= nrb;
-    it.hk = (int)(u % p.Hkv);
-    it.b = (int)(u / p.Hkv);       // 0 in part 0
+    const unsigned v = u / nrb;
+    it.rb = (int)(u - v * nrb);
+    it.b = (int)(v / (unsigned)p.Hkv);       // 0 in part 0
+    it.hk = (int)(v - (unsigned)it.b * (unsigned)p.Hkv);
     return it;
 }
 
@@ -132,6 +131,7 @@ struct PagedRange {
 __device__ __forceinline__ PagedRange paged_range(const PagedArgs& p, const PagedItem& it, int imin, int imax,
                                                   bool full) {
     PagedRange g;
+    const int tile = p.tile[it.part];
     const int off = it.part ? p.P : 0;
     g.hi = imax < 0 ? 0 : it.part ? imax + 1 - off : (imax + 1 < p.P ? imax + 1 : p.P);
     g.lo = g.sink = g.n_sink = g.t_lo = 0;
@@ -141,9 +141,9 @@ __device__ __forceinline__ PagedRange paged_range(const PagedArgs& p, const Page
         const int sink = p.sinks - off;
         g.sink = sink < 0 ? 0 : sink < g.hi ? sink : g.hi;
     }
-    const int t_hi = (g.hi + p.tile - 1) / p.tile;
-    g.t_lo = g.lo < g.hi ? g.lo / p.tile : t_hi;
-    g.n_sink = (g.sink + p.tile - 1) / p.tile;
+    const int t_hi = (g.hi + tile - 1) / tile;
+    g.t_lo = g.lo < g.hi ? g.lo / tile : t_hi;
+    g.n_sink = (g.sink + tile - 1) / tile;
     if (g.n_sink > g.t_lo) g.n_sink = g.t_lo;
     g.n = g.n_sink + t_hi - g.t_lo;
     return g;
@@ -162,9 +162,9 @@ __device__ __forceinline__ size_t paged_out_row(const PagedArgs& p, const PagedR
     return ((size_t)w.b * p.H + w.h) * p.T + w.t;
 }
 
-// paged_tc.cu: bf16, tensor cores; rows 32, 64 or 128 per block. paged_simt.cu: fp32, CUDA cores;
-// rows kSimtRows.
-constexpr int kTcTile = 64;
+// paged_tc.cu: bf16, tensor cores; rows 32, 64 or 128 per block, and tiles of paged_tc_tile(d, rows)
+// keys. paged_simt.cu: fp32, CUDA cores; rows kSimtRows, tiles kSimtTile.
+__host__ __device__ constexpr int paged_tc_tile(int d, int rows) { return d == 64 && rows < 128 ? 128 : 64; }
 cudaError_t launch_paged_tc(const PagedArgs& p, cudaStream_t s);
 constexpr int kSimtRows = 8, kSimtTile = 64;
 cudaError_t launch_paged_simt(const PagedArgs& p, cudaStream_t s);

@@ -11,11 +11,13 @@ namespace {
 constexpr int kSms = 152;   // GB300
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Items that run at the same time, and the most that a call is split into. Small calls get
-// one round of items; larger ones more rounds, which level sequences of different lengths.
+// Items that run at the same time, and the most rounds of them that a call is split into.
 constexpr int kSlotsSimt = kSms * 3, kSlotsTc = kSms * 2;
-constexpr int kRounds = 4;
-constexpr int kMinTiles = 8;   // tiles of an item before a second round is worth its set-up
+constexpr int kRounds = 8;
+// What an item costs beside its tiles (the rows' counts, the first pages, the output, its share of
+// the join), in tiles. Measured: 32 sequences of 4K to 16K tokens, 8 key/value heads, d 128 take
+// 237, 211, 210, 218, 215 us with 2, 3, 5, 8, 12 items per sequence and head.
+constexpr int kSetUp = 10;
 
 // Joins the items of a row. kWarps warps share a row (a block of four warps holds 4 / kWarps
 // rows): with few items a warp each, with many the four warps of a block, whose loads are
@@ -112,7 +114,7 @@ cudaError_t launch_join(const PagedArgs& p, cudaStream_t s) {
 long long ceil_div(long long x, long long y) { return (x + y - 1) / y; }
 
 struct Plan {
-    int tile, rows[2];
+    int tile[2], rows[2];
     int nrb[2];
     long long units[2];    // (sequence, key/value head, row block) triples
     long long tiles[2];    // key tiles of one of them, at most, without a window
@@ -120,65 +122,86 @@ struct Plan {
     long long max_split;   // items of a row, at most, whatever the window
 };
 
-Plan make_plan(int B, int H, int Hkv, int T, int max_len, int P, bool bf16) {
+// Items along the keys of a part, at most: kRounds rounds of items over all units.
+long long most_chunks(const Plan& x, int part, long long tiles) {
+    const long long c = ceil_div(x.slots * kRounds, x.units[part]);
+    return c < tiles ? c : tiles;
+}
+
+Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, bool bf16) {
     Plan x;
-    x.tile = bf16 ? kTcTile : kSimtTile;
     x.slots = bf16 ? kSlotsTc : kSlotsSimt;
     const long long G = H / Hkv;
     const long long n[2] = {P > 0 ? G * B * T : 0, G * T};
-    long long rb[2];
+    const int keys[2] = {P, max_len};
+    x.max_split = 0;
     for (int i = 0; i < 2; ++i) {
         // tensor cores: copies of the rows fill the 128 of a tile (paged_tc.cu)
         x.rows[i] = !bf16 ? kSimtRows : n[i] <= 32 ? 32 : n[i] <= 64 ? 64 : 128;
-        rb[i] = ceil_div(n[i], x.rows[i]);
-    }
-    x.units[0] = rb[0] * Hkv;
-    x.units[1] = rb[1] * Hkv * B;
-    x.tiles[0] = ceil_div(P, x.tile);
-    x.tiles[1] = ceil_div(max_len, x.tile);
-    x.max_split = 0;
-    for (int i = 0; i < 2; ++i) {
-        x.nrb[i] = (int)rb[i];
-        if (x.units[i] == 0) continue;
-        const long long c = ceil_div(x.slots * kRounds, x.units[i]);
-        x.max_split += c < x.tiles[i] ? c : x.tiles[i];
+        x.tile[i] = bf16 ? paged_tc_tile(d, x.rows[i]) : kSimtTile;
+        x.nrb[i] = (int)ceil_div(n[i], x.rows[i]);
+        x.units[i] = (long long)x.nrb[i] * Hkv * (i ? B : 1);
+        x.tiles[i] = ceil_div(keys[i], x.tile[i]);
+        if (x.units[i]) x.max_split += most_chunks(x, i, x.tiles[i]);
     }
     return x;
 }
 
-// The items: both parts' tiles in equal shares of `per` tiles, at least total / (slots
-// kRounds); a part then has ceil(tiles / per) <= ceil(slots kRounds / units) items along
-// the keys (the bound that the workspace is sized by).
-void set_items(PagedArgs& p, const Plan& x, int nfrozen) {
-    long long nt[2] = {x.tiles[0], x.tiles[1]};
-    if (p.window > 0 && nfrozen == 0) {
-        // a block's rows stand within T positions in part 1 and past the prefix in part 0:
-        // the tiles that hold window + T - 1 consecutive keys, and those of the sinks
-        const long long span[2] = {p.window, (long long)p.window + p.T - 1};
-        for (int i = 0; i < 2; ++i) {
-            const long long off = i ? p.P : 0;
-            const long long sinks = p.sinks > off ? p.sinks - off : 0;
-            const long long n = ceil_div(span[i], x.tile) + 1 + ceil_div(sinks, x.tile);
-            if (n < nt[i]) nt[i] = n;
+// Items along the keys for `units` units of `nt` tiles each: the number that makes the part
+// shortest, with `slots` items at a time. even: the units have the same length, so that rounds
+// end together; else their lengths differ, and the last items run alone for a while.
+// Candidates: the most items that fit in 1, 2, ... rounds, and the minimum over c of
+// (units c / slots) (kSetUp + nt / c) + nt / c, the work and the tail of c items per unit.
+long long pick_chunks(long long units, long long nt, long long most, long long slots, bool even) {
+    long long best = 1;
+    double best_cost = 1e300;
+    for (int r = 0; r <= kRounds; ++r) {
+        long long c = r ? slots * r / units
+                        : (long long)sqrt((double)nt * (double)slots / ((double)units * (double)kSetUp));
+        c = c < 1 ? 1 : c > most ? most : c;
+        const long long per = ceil_div(nt, c);
+        const double rounds = (double)(units * ceil_div(nt, per)) / (double)slots;
+        const double cost = (even ? ceil(rounds) : rounds + 1.0) * (double)(kSetUp + per);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = c;
         }
     }
-    const long long total = x.units[0] * nt[0] + x.units[1] * nt[1];
-    const long long one = ceil_div(total, x.slots), most = ceil_div(total, x.slots * kRounds);
-    const long long per = one < kMinTiles ? one : most > kMinTiles ? most : kMinTiles;
-    // a prefix's items write many rows each: no more than one round of them
-    const long long shared = ceil_div(x.units[0] * nt[0], x.slots);
-    for (int i = 0; i < 2; ++i) {
-        const long long n = i == 0 && shared > per ? shared : per;
+    return best;
+}
+
+void set_items(PagedArgs& p, const Plan& x, int nfrozen) {
+    long long nt[2] = {x.tiles[0], x.tiles[1]};
+    const bool windowed = p.window > 0 && nfrozen == 0;
+    unsigned items[2];
+    long long slots = x.slots;
+    for (int i = 1; i >= 0; --i) {
         p.nrb[i] = x.nrb[i];
-        p.per_chunk[i] = (int)n;
-        p.chunks[i] = x.units[i] ? (int)ceil_div(nt[i], n) : 0;
+        p.rows[i] = x.rows[i];
+        p.tile[i] = x.tile[i];
+        p.chunks[i] = p.per_chunk[i] = 0;
+        items[i] = 0;
+        if (x.units[i] == 0) continue;
+        if (windowed) {
+            // a block's rows stand within T positions in part 1 and past the prefix in part 0:
+            // the tiles that hold window + T - 1 consecutive keys, and those of the sinks
+            const long long span = i ? (long long)p.window + p.T - 1 : p.window;
+            const long long off = i ? p.P : 0;
+            const long long sinks = p.sinks > off ? p.sinks - off : 0;
+            const long long n = ceil_div(span, x.tile[i]) + 1 + ceil_div(sinks, x.tile[i]);
+            if (n < nt[i]) nt[i] = n;
+        }
+        // (a prefix's units have the same length, and so have windows)
+        const long long c = pick_chunks(x.units[i], nt[i], most_chunks(x, i, nt[i]), slots, i == 0 || windowed);
+        p.per_chunk[i] = (int)ceil_div(nt[i], c);
+        p.chunks[i] = (int)ceil_div(nt[i], p.per_chunk[i]);
+        items[i] = (unsigned)(x.units[i] * p.chunks[i]);
+        // few own items run beside the prefix's, in the same round
+        if (items[i] < slots / 2) slots -= items[i];
     }
-    p.tile = x.tile;
-    p.rows[0] = x.rows[0];
-    p.rows[1] = x.rows[1];
     p.nsplit = p.chunks[0] + p.chunks[1];
-    p.items0 = x.units[0] * p.chunks[0];
-    p.items = p.items0 + x.units[1] * p.chunks[1];
+    p.items0 = items[0];
+    p.items = items[0] + items[1];
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -200,7 +223,7 @@ int check_sizes(int B, int H, int Hkv, int T, int d, int max_len, int prefix_len
     if (dt != SAF_BF16 && dt != SAF_FP32) return SAF_EINVAL;
     if (!head_dim_supported(d, dt)) return SAF_EUNSUPPORTED;
     if (max_len < 1 || prefix_len < 0 || (long long)max_len + prefix_len > (1ll << 30)) return SAF_EINVAL;
-    if ((long long)B * H * T > (1ll << 30)) return SAF_EINVAL;
+    if ((long long)B * H * T > (1ll << 29)) return SAF_EINVAL;   // (items are counted in 32 bits)
     return SAF_OK;
 }
 
@@ -245,7 +268,7 @@ int paged(const void* q, const void* k_cache, const void* v_cache, const int32_t
         return SAF_EALIGN;
     if (!workspace) return SAF_EWORKSPACE;
     if (!aligned(workspace, 256)) return SAF_EALIGN;
-    const Plan plan = make_plan(B, H, Hkv, T, max_len, prefix_len, dt == SAF_BF16);
+    const Plan plan = make_plan(B, H, Hkv, T, d, max_len, prefix_len, dt == SAF_BF16);
     size_t po_off;
     if (ws_bytes < workspace_bytes(plan, B, H, T, d, &po_off)) return SAF_EWORKSPACE;
     if ((st = check_device()) != SAF_OK) return st;
@@ -280,7 +303,6 @@ int paged(const void* q, const void* k_cache, const void* v_cache, const int32_t
     p.sinks = sinks < prefix_len + max_len ? sinks : prefix_len + max_len;
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)d);
     set_items(p, plan, nfrozen);
-    if (p.items > 0x7fffffffll) return SAF_EINVAL;
 
     cudaStream_t s = (cudaStream_t)stream;
     const bool bf16 = dt == SAF_BF16;
@@ -305,7 +327,7 @@ size_t saf_attn_paged_workspace_bytes(int B, int H, int Hkv, int T, int d, int m
                                       saf_dtype_t dt) {
     if (check_sizes(B, H, Hkv, T, d, max_len, prefix_len, dt) != SAF_OK) return 0;
     if (B == 0 || T == 0) return kStatusBytes;
-    return workspace_bytes(make_plan(B, H, Hkv, T, max_len, prefix_len, dt == SAF_BF16), B, H, T, d, nullptr);
+    return workspace_bytes(make_plan(B, H, Hkv, T, d, max_len, prefix_len, dt == SAF_BF16), B, H, T, d, nullptr);
 }
 
 int saf_attn_paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table, int max_pages,
