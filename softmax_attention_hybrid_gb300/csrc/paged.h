@@ -166,7 +166,7 @@ __device__ __forceinline__ size_t paged_out_row(const PagedArgs& p, const PagedR
 // keys. paged_simt.cu: fp32, CUDA cores; rows kSimtRows, tiles kSimtTile.
 __host__ __device__ constexpr int paged_tc_tile(int d, int rows) { return d == 64 && rows < 128 ? 128 : 64; }
 cudaError_t launch_paged_tc(const PagedArgs& p, cudaStream_t s);
-constexpr int kSimtRows = 8, kSimtTile = 64;
+constexpr int kSimtRows = 8, kSimtTile = 32;
 cudaError_t launch_paged_simt(const PagedArgs& p, cudaStream_t s);
 
 }  // namespace saf
