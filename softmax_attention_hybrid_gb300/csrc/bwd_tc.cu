@@ -53,7 +53,11 @@ namespace {
 using namespace tc;
 
 constexpr int kTileBytes = 128 * 64 * 2;
-constexpr int kThreads = 320;
+// The windowed instances run 12 warps, three warpgroups, of which the last (producer, issuer, two
+// idle) gives registers to the pattern warps (setmaxnreg), which hold an unrounded P there.
+constexpr int threads(bool win) { return win ? 384 : 320; }
+constexpr int kRegsLaunch = 168, kRegsPattern = 216, kRegsOther = 72;
+static_assert(2 * kRegsPattern + kRegsOther <= 3 * kRegsLaunch, "register split too large");
 constexpr int kStages = 3;
 constexpr int kRing = 4;
 constexpr int kSliceGroup = 8;
@@ -163,7 +167,7 @@ struct Barriers {
 // kWin: ordinary heads with a sliding window and sinks; their tiles are the query blocks
 // that see a key of the item's block.
 template <bool kGrouped, bool kWin>
-__global__ void __launch_bounds__(kThreads, 1) bwd_tc_kernel(const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(threads(kWin), 1) bwd_tc_kernel(const __grid_constant__ BwdParams p) {
     extern __shared__ uint8_t smem_raw[];
     // 1024-byte aligned base (swizzled tiles), derived from the shared array itself so that
     // every access through it stays a shared-memory access
@@ -211,6 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_tc_kernel(const __grid_consta
     const int nqb = p.nqb;
     const int G = kGrouped ? p.G : 1;   // query heads per key/value head
 
+    if (warp >= 8) {
+    if (kWin) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 8) {
         // ---------------------------------------------------------------- producer
         if (lane == 0) {
@@ -410,8 +416,10 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_tc_kernel(const __grid_consta
             mma_commit(&bars.mma_idle);
             mbar_wait_bounded(&bars.mma_idle, 0, kWaitLimitNs);
         }
+    }   // (kWin: warps 10, 11 idle)
     } else {
         // ---------------------------------------------------------------- pattern warps
+        if (kWin) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsPattern));
         const int quarter = warp & 3, half = warp >> 2;
         const int j = quarter * 32 + lane;                   // key row of the block = TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -505,6 +513,9 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_tc_kernel(const __grid_consta
                     tc_fence_after();
                     // P^T first: S^T row (64 columns) -> P (bf16 pairs); then dP^T row -> dS.
                     uint32_t pk[32];
+                    // kWin keeps P unrounded for dS (the windowed call's dq and dk are then off by one
+                    // rounding less) and packs it as dS is formed; the other instances take it from pk.
+                    float pf[kWin ? 64 : 1];
                     {
                         uint32_t sv[64];
                         tmem_ld32(lane_base + kColS + 64 * half, sv);
@@ -535,7 +546,12 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_tc_kernel(const __grid_consta
                                 if (diag && j > q0 + 1) p1 = 0.f;
                                 if (kWin && q0 >= q_far) p0 = 0.f;
                                 if (kWin && q0 + 1 >= q_far) p1 = 0.f;
-                                pk[(e + u) >> 1] = pack_bf16(p0, p1);
+                                if (kWin) {
+                                    pf[(kWin ? 1 : 0) * (e + u)] = p0;
+                                    pf[(kWin ? 1 : 0) * (e + u + 1)] = p1;
+                                } else {
+                                    pk[(e + u) >> 1] = pack_bf16(p0, p1);
+                                }
                             }
                         }
                     }
@@ -561,13 +577,16 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_tc_kernel(const __grid_consta
 #pragma unroll
                             for (int u = 0; u < 4; u += 2) {
                                 const int c = 32 * g2 + e + u;
-                                // dS = P o (dP - D) with P as rounded to bf16 for the MMAs
-                                const float2 pp = make_float2(__uint_as_float(pk[c >> 1] << 16),
-                                                              __uint_as_float(pk[c >> 1] & 0xffff0000u));
+                                // dS = P o (dP - D) with P as rounded to bf16 for the MMAs (kWin: unrounded)
+                                const float2 pp =
+                                    kWin ? make_float2(pf[(kWin ? 1 : 0) * c], pf[(kWin ? 1 : 0) * (c + 1)])
+                                         : make_float2(__uint_as_float(pk[c >> 1] << 16),
+                                                       __uint_as_float(pk[c >> 1] & 0xffff0000u));
                                 const float2 dd = fmul2(
                                     pp, fsub2(make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])),
                                               u == 0 ? make_float2(d4.x, d4.y) : make_float2(d4.z, d4.w)));
                                 dk[(e + u) >> 1] = pack_bf16(dd.x, dd.y);
+                                if (kWin) pk[c >> 1] = pack_bf16(pp.x, pp.y);
                             }
                         }
                         // dS row j, queries 64*half + 32*g2 .. +31: MN-major atom `half`, K-row j
@@ -802,9 +821,17 @@ cudaError_t launch_tc_bwd(const LayerArgs& a, cudaStream_t s) {
                                              : (p.G > 1 ? bwd_tc_kernel<true, false> : bwd_tc_kernel<false, false>);
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    const bool win = p.window > 0;
+    if (win) {
+        // a build that launches with fewer registers could never hand the pattern warps theirs
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, kernel);
+        if (e != cudaSuccess) return e;
+        if (2 * kRegsPattern + kRegsOther > 3 * fa.numRegs) return cudaErrorInvalidConfiguration;
+    }
     const int grid = p.n_items < sms ? p.n_items : sms;
     before_launch(SAF_KERNEL_BWD, s);
-    e = launch_ex(kernel, dim3(grid), dim3(kThreads), smem, s, true, 1, p);
+    e = launch_ex(kernel, dim3(grid), dim3(threads(win)), smem, s, true, 1, p);
     after_launch(SAF_KERNEL_BWD, s);
     if (e != cudaSuccess) return e;
     dim3 g2((unsigned)(((long long)a.T * 8 + 255) / 256), BH);

@@ -108,6 +108,8 @@ struct DhParams {
     float scale_log2;      // log2(e) / sqrt(d)
     float scale;           // 1 / sqrt(d)
     HeadMask mask;
+    int n_ord, n_frz;
+    uint8_t ord_heads[SAF_MAX_HEADS], frz_heads[SAF_MAX_HEADS];
 };
 
 // ---------------------------------------------------------------------------
@@ -139,8 +141,20 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
     grid_dep_wait();
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int qb = p.nqb - 1 - (int)blockIdx.x;   // the longest blocks first
-    const int bh = blockIdx.y;
+    int qb = p.nqb - 1 - (int)blockIdx.x;   // the longest blocks first
+    int bh = blockIdx.y;
+    if (kWin) {
+        // over the whole launch: the frozen heads' blocks, longest first, then the ordinary
+        // ones', which see the window only
+        long long u = (long long)blockIdx.y * p.nqb + blockIdx.x;
+        const long long n_frz = (long long)p.B * p.n_frz * p.nqb;
+        const bool first = u < n_frz;
+        if (!first) u -= n_frz;
+        const int heads = first ? p.n_frz : p.n_ord, slices = p.B * heads;
+        const int level = (int)(u / slices), slice = (int)(u - (long long)level * slices);
+        qb = p.nqb - 1 - level;
+        bh = slice / heads * p.H + (first ? p.frz_heads : p.ord_heads)[slice % heads];
+    }
     const int h = bh % p.H;
     const int bkv = (bh / p.H) * p.Hkv + h / p.G;   // key/value slice
     const bool frz = head_frozen(p.mask, h);
@@ -414,8 +428,15 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
     grid_dep_wait();
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kb = (int)blockIdx.x;
-    const int bkv = blockIdx.y;                        // key/value slice
+    int kb = (int)blockIdx.x;
+    int bkv = blockIdx.y;                              // key/value slice
+    if (kWin) {   // over the whole launch the longest first: blocks of sinks, which every query sees, and
+                  // the early blocks of frozen heads
+        const long long u = (long long)blockIdx.y * p.nqb + blockIdx.x;
+        const int slices = p.B * p.Hkv;
+        kb = (int)(u / slices);
+        bkv = (int)(u - (long long)kb * slices);
+    }
     const int b = bkv / p.Hkv, h0 = (bkv - b * p.Hkv) * p.G;   // its query heads: h0 .. h0 + G - 1
     // query tiles per query head: those that see a key of the block through a window
     const int nq_frz = p.nqb - kb, nq_ord = query_blocks<kWin>(kb, p.nqb, p.window, p.sinks, 128);
@@ -840,6 +861,12 @@ DhParams make_params(const LayerArgs& a) {
     p.G = a.H / p.Hkv;
     p.window = a.window;
     p.sinks = a.sinks;
+    for (int h = 0; h < a.H; ++h) {
+        if (head_frozen(a.mask, h))
+            p.frz_heads[p.n_frz++] = (uint8_t)h;
+        else
+            p.ord_heads[p.n_ord++] = (uint8_t)h;
+    }
     return p;
 }
 

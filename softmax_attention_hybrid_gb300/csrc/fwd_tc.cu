@@ -112,6 +112,10 @@ struct Item {
 // the next. A group's key and value tiles are re-read by each of its pairs, and
 // they stay in L2 while the group runs. (With one group for all slices this is
 // longest first over the whole launch.)
+//
+// With a window the ordinary slices' items are short and alike, and the frozen ones', which
+// see every key, the longest: those come first then.
+template <bool kWin>
 __device__ __forceinline__ Item decode_item(const FwdParams& p, int idx) {
     Item it;
     const int n_slices = p.B * p.H;
@@ -123,13 +127,14 @@ __device__ __forceinline__ Item decode_item(const FwdParams& p, int idx) {
     const int level = within / gsize;
     const int slice = grp * G + (within - level * gsize);
     it.pair = p.npairs - 1 - level;
-    const int n_ord_items = p.B * p.n_ord;
-    if (slice < n_ord_items) {
-        it.b = slice / p.n_ord;
-        it.h = p.ord_heads[slice - it.b * p.n_ord];
+    const int n_first = p.B * (kWin ? p.n_frz : p.n_ord);
+    if ((slice < n_first) != kWin) {
+        const int o = kWin ? slice - n_first : slice;
+        it.b = o / p.n_ord;
+        it.h = p.ord_heads[o - it.b * p.n_ord];
         it.frozen = false;
     } else {
-        const int f = slice - n_ord_items;
+        const int f = kWin ? slice : slice - n_first;
         it.b = f / p.n_frz;
         it.h = p.frz_heads[f - it.b * p.n_frz];
         it.frozen = true;
@@ -250,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
                 mbar_arrive(&bars.item_full[slot]);
                 slot = (slot + 1) % kRing;
                 if (idx < 0) break;
-                const Item it = decode_item(p, idx);
+                const Item it = decode_item<kWin>(p, idx);
                 const int bh = it.b * p.H + it.h;
                 const int bkv = it.b * p.Hkv + it.h / p.G;   // the key/value slice this head reads
                 const int qb0 = 2 * it.pair, qb1 = qb0 + 1;
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
                 if (lane == 0) mbar_arrive(&bars.item_empty[slot]);
                 slot = (slot + 1) % kRing;
                 if (idx < 0) break;
-                const Item it = decode_item(p, idx);
+                const Item it = decode_item<kWin>(p, idx);
                 const int qb0 = 2 * it.pair, qb1 = qb0 + 1;
                 const bool t1 = qb1 < p.nqb;
                 const int nblk = item_blocks<kWin>(p, it).n;                  // key blocks of the item
@@ -466,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
             if (lane == 0) mbar_arrive(&bars.item_empty[slot]);
             slot = (slot + 1) % kRing;
             if (idx < 0) break;
-            const Item it = decode_item(p, idx);
+            const Item it = decode_item<kWin>(p, idx);
             const KeyBlocks<kWin> blocks = item_blocks<kWin>(p, it);
             const int gblk0 = gblk;
             gblk += blocks.n;
