@@ -21,6 +21,7 @@ namespace saf {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr long long kFullGpu = 152ll * 2048;   // threads that the GPU holds
 
 struct AppendArgs {
     const void *q, *k, *v;
@@ -38,54 +39,51 @@ struct AppendArgs {
     uint8_t heads[2 * SAF_MAX_HEADS];   // nq query heads, then nk key heads
 };
 
+// 8 elements as they lie in memory.
 template <typename E>
-struct Vec;   // 8 elements
+struct Raw;
 template <>
-struct Vec<float> {
-    float x[8];
+struct Raw<float> {
+    float4 a, b;
     __device__ void load(const float* p) {
-        *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(p);
-        *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(p + 4);
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + 4);
     }
     __device__ void store(float* p) const {
-        *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(x);
-        *reinterpret_cast<float4*>(p + 4) = *reinterpret_cast<const float4*>(x + 4);
+        *reinterpret_cast<float4*>(p) = a;
+        *reinterpret_cast<float4*>(p + 4) = b;
+    }
+    __device__ void get(float* x) const {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+    __device__ void set(const float* x) {
+        a = make_float4(x[0], x[1], x[2], x[3]);
+        b = make_float4(x[4], x[5], x[6], x[7]);
     }
 };
 template <>
-struct Vec<__nv_bfloat16> {
-    float x[8];
-    __device__ void load(const __nv_bfloat16* p) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw<__nv_bfloat16> {
+    uint32_t w[4];
+    __device__ void load(const __nv_bfloat16* p) { *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p); }
+    __device__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w); }
+    __device__ void get(float* x) const {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             x[2 * e] = __uint_as_float(w[e] << 16);
             x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
         }
     }
-    __device__ void store(__nv_bfloat16* p) const {
-        uint32_t w[4];
+    __device__ void set(const float* x) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
             w[e] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 
 template <typename E>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs p) {
-    grid_dep_wait();
-    grid_dep_launch();
-    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const int u = (int)(id % p.units);
-    long long rest = id / p.units;
-    const int group = (int)(rest % p.groups);
-    rest /= p.groups;
-    const int t = (int)(rest % p.T), b = (int)(rest / p.T);
-    if (b >= p.B) return;
+__device__ __forceinline__ void append_token(const AppendArgs& p, int b, int t, int group, int u) {
     const int c = p.ctx[b];
     const int n = p.n_new ? p.n_new[b] : p.T;
     const long long room = (long long)p.max_pages << p.page_log2;
@@ -108,8 +106,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const int c0 = turn && !p.interleaved ? 8 * u : 16 * u;
     const int c1 = turn && !p.interleaved ? (p.rope >> 1) + 8 * u : 16 * u + 8;
     float cs[8], sn[8];
-    const int s0 = group * p.per, s1 = min(s0 + p.per, p.slots);
-    if (turn && s0 < p.nq + p.nk) {
+    if (turn && group < p.nq + p.nk) {
         const uint64_t pos = (uint64_t)(p.pos_base + slot);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -118,50 +115,79 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             sincospif((float)x * 4.656612873077393e-10f, &sn[e], &cs[e]);   // 2^-31
         }
     }
-    for (int s = s0; s < s1; ++s) {
-        const bool is_q = s < p.nq, is_v = s >= p.nq + p.nk;
-        const int h = is_v ? s - p.nq - p.nk : p.heads[s];
-        const E* src;
-        E* dst;
-        if (is_q) {
-            src = (const E*)p.q + b * p.sq[0] + h * p.sq[1] + t * p.sq[2];
-            dst = (E*)p.q_out + (((size_t)b * p.H + h) * p.T + t) * p.d;
-        } else {
-            if (page < 0) continue;
-            const long long* st = is_v ? p.sv : p.sk;
-            src = (const E*)(is_v ? p.v : p.k) + b * st[0] + h * st[1] + t * st[2];
-            dst = (E*)(is_v ? p.v_cache : p.k_cache) +
-                  ((((size_t)page * p.Hkv + h) << p.page_log2) + page_row) * p.d;
-        }
-        const int o0 = is_v ? 16 * u : c0, o1 = is_v ? 16 * u + 8 : c1;
-        Vec<E> x, y;
-        x.load(src + o0);
-        y.load(src + o1);
-        if (turn && !is_v) {
-            if (!p.interleaved) {
+    // My heads are group, group + groups, ...: the threads of a token then read rows that lie next to
+    // each other. Several rows are on their way at a time.
+    constexpr int kBatch = sizeof(E) == 2 ? 4 : 2;
+    for (int s0 = group; s0 < p.slots; s0 += kBatch * p.groups) {
+        Raw<E> x[kBatch], y[kBatch];
+        E* dst[kBatch];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float a = x.x[e], z = y.x[e];
-                    x.x[e] = a * cs[e] - z * sn[e];
-                    y.x[e] = a * sn[e] + z * cs[e];
-                }
+        for (int k = 0; k < kBatch; ++k) {
+            const int s = s0 + k * p.groups;
+            dst[k] = nullptr;
+            if (s >= p.slots) continue;
+            const bool is_v = s >= p.nq + p.nk;
+            const int h = is_v ? s - p.nq - p.nk : p.heads[s];
+            const E* src;
+            if (s < p.nq) {
+                src = (const E*)p.q + b * p.sq[0] + h * p.sq[1] + t * p.sq[2];
+                dst[k] = (E*)p.q_out + (((size_t)b * p.H + h) * p.T + t) * p.d;
             } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float a = x.x[2 * e], z = x.x[2 * e + 1];
-                    x.x[2 * e] = a * cs[e] - z * sn[e];
-                    x.x[2 * e + 1] = a * sn[e] + z * cs[e];
-                    a = y.x[2 * e], z = y.x[2 * e + 1];
-                    y.x[2 * e] = a * cs[4 + e] - z * sn[4 + e];
-                    y.x[2 * e + 1] = a * sn[4 + e] + z * cs[4 + e];
-                }
+                if (page < 0) continue;
+                const long long* st = is_v ? p.sv : p.sk;
+                src = (const E*)(is_v ? p.v : p.k) + b * st[0] + h * st[1] + t * st[2];
+                dst[k] = (E*)(is_v ? p.v_cache : p.k_cache) +
+                         ((((size_t)page * p.Hkv + h) << p.page_log2) + page_row) * p.d;
             }
+            x[k].load(src + (is_v ? 16 * u : c0));
+            y[k].load(src + (is_v ? 16 * u + 8 : c1));
         }
-        x.store(dst + o0);
-        y.store(dst + o1);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (!dst[k]) continue;
+            const bool is_v = s0 + k * p.groups >= p.nq + p.nk;
+            if (turn && !is_v) {
+                float a[8], z[8];
+                x[k].get(a);
+                y[k].get(z);
+                if (!p.interleaved) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float a0 = a[e], z0 = z[e];
+                        a[e] = a0 * cs[e] - z0 * sn[e];
+                        z[e] = a0 * sn[e] + z0 * cs[e];
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float a0 = a[2 * e], z0 = a[2 * e + 1];
+                        a[2 * e] = a0 * cs[e] - z0 * sn[e];
+                        a[2 * e + 1] = a0 * sn[e] + z0 * cs[e];
+                        a0 = z[2 * e], z0 = z[2 * e + 1];
+                        z[2 * e] = a0 * cs[4 + e] - z0 * sn[4 + e];
+                        z[2 * e + 1] = a0 * sn[4 + e] + z0 * cs[4 + e];
+                    }
+                }
+                x[k].set(a);
+                y[k].set(z);
+            }
+            x[k].store(dst[k] + (is_v ? 16 * u : c0));
+            y[k].store(dst[k] + (is_v ? 16 * u + 8 : c1));
+        }
     }
 }
 
+template <typename E>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs p) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const unsigned id = blockIdx.x * kThreads + threadIdx.x;   // (token, group of slots, unit) of a sequence
+    const unsigned w = id / (unsigned)p.units;
+    const int u = (int)(id - w * (unsigned)p.units);
+    const int t = (int)(w / (unsigned)p.groups), group = (int)(w - (unsigned)t * (unsigned)p.groups);
+    if (t >= p.T) return;
+    for (int b = blockIdx.y; b < p.B; b += gridDim.y) append_token<E>(p, b, t, group, u);
+}
 bool aligned(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 }  // namespace
@@ -245,16 +271,21 @@ extern "C" int saf_kv_append(const void* q, const void* k, const void* v, const 
     p.interleaved = interleaved;
     p.units = d / 16;
     p.slots = p.nq + p.nk + Hkv;
-    p.per = 1;
-    p.groups = p.slots;
-    const long long threads = (long long)B * T * p.groups * p.units;
+    // A thread takes several heads of its token, so that its angles serve them all, once the call
+    // has threads enough for the whole GPU (append_prompts, one and eight heads per thread: 53 and
+    // {PROMPTS} us); below that a head each (append_step: {STEP1} us, against {STEP8} us).
+    const long long all = (long long)B * T * p.slots * p.units;
+    p.per = all > 8ll * kFullGpu ? 8 : all > kFullGpu ? (int)(all / kFullGpu) : 1;
+    p.groups = (p.slots + p.per - 1) / p.per;
+    const long long threads = (long long)T * p.groups * p.units;   // of a sequence
     const long long blocks = (threads + kThreads - 1) / kThreads;
-    if (blocks > 0x7fffffffll) return SAF_EINVAL;
+    if (threads > 0x7fffffffll) return SAF_EINVAL;
+    const dim3 grid((unsigned)blocks, (unsigned)(B < 65535 ? B : 65535));
     cudaStream_t cs = (cudaStream_t)stream;
     before_launch(SAF_KERNEL_KV_APPEND, cs);
     const cudaError_t err =
-        dt == SAF_BF16 ? launch_ex(append_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(kThreads), 0, cs, true, 1, p)
-                       : launch_ex(append_kernel<float>, dim3((unsigned)blocks), dim3(kThreads), 0, cs, true, 1, p);
+        dt == SAF_BF16 ? launch_ex(append_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, cs, true, 1, p)
+                       : launch_ex(append_kernel<float>, grid, dim3(kThreads), 0, cs, true, 1, p);
     after_launch(SAF_KERNEL_KV_APPEND, cs);
     return launch_status(err);
 }

@@ -497,8 +497,6 @@ def saf_attn_bwd_window(q, k, v, o, do, lse, a, r, frozen, window, sinks=0, stat
 
 def _strided(t, idx, dt):
     """Address and (sequence, head, token) strides of a [B, heads, T, d] tensor with contiguous rows."""
-    if t is None:
-        return None, (0, 0, 0)
     s = t.stride()
     if t.get_device() != idx or t.dtype is not dt:
         _refuse(t, idx, dt)
@@ -529,32 +527,48 @@ def saf_kv_append(k, v, k_cache, v_cache, page_table, ctx, n_new=None, q=None, q
     whose first 8 bytes, zeroed once by the caller, collect errors for saf_device_status
     (None: errors are not recorded)."""
     idx, dt, i32 = _device(v), v.dtype, torch.int32
-    B, Hkv, T, d = v.shape
-    H = q.shape[1] if q is not None else len(frozen) if frozen is not None else Hkv
-    num_pages, heads, page_size, width = v_cache.shape
-    if heads != Hkv or width != d:
-        raise ValueError("the caches must be [num_pages, Hkv, page_size, d]")
-    _shapes(("k", k, v.shape), ("q", q, (B, H, T, d)), ("q_out", q_out, (B, H, T, d)), ("k_cache", k_cache, v_cache.shape))
+    shape, caches = v.shape, v_cache.shape
+    B, Hkv, T, d = shape
+    num_pages, heads, page_size, width = caches
     max_pages = _table(ctx, n_new, page_table, B)
-    qp, qs = _strided(q, idx, dt)
-    kp, ks = _strided(k, idx, dt)
-    vp, vs = _strided(v, idx, dt)
-    if q is not None and q_out is None:
-        # rows that are not written (frozen heads, rows without a token) come back as zeros
-        q_out = torch.zeros((B, H, T, d), dtype=dt, device=v.device)
+    if heads != Hkv or width != d or (k_cache is not None and k_cache.shape != caches):
+        raise ValueError("the caches must be [num_pages, Hkv, page_size, d]")
+    if k is not None and k.shape != shape:
+        raise ValueError("k must have v's shape")
+    if q is not None:
+        full = q.shape
+        H = full[1]
+        if full[0] != B or full[2] != T or full[3] != d:
+            raise ValueError("q must be [B, H, T, d]")
+        if q_out is None:
+            # rows that are not written (frozen heads, rows without a token) come back as zeros
+            q_out = torch.zeros(full, dtype=dt, device=v.device)
+        elif q_out.shape != full:
+            raise ValueError("q_out must have q's shape")
+        qp, (qb, qh, qt) = _strided(q, idx, dt)
+        qo = _at(q_out, idx, dt)
+    else:
+        H = len(frozen) if frozen is not None else Hkv
+        qp = qo = None
+        qb = qh = qt = 0
+    if k is not None:
+        kp, (kb, kh, kt) = _strided(k, idx, dt)
+    else:
+        kp, kb, kh, kt = None, 0, 0, 0
+    vp, (vb, vh, vt) = _strided(v, idx, dt)
     freq, rope = None, 0
     if inv_freq is not None:
         if not (torch.is_tensor(inv_freq) and inv_freq.dtype is torch.float64 and inv_freq.get_device() < 0
                 and inv_freq.is_contiguous()):
             inv_freq = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
-        freq, rope = inv_freq.data_ptr(), 2 * inv_freq.numel()
+        rope = 2 * inv_freq.numel()
+        freq = inv_freq.data_ptr() if rope else None
     if status is not None and status.numel() * status.element_size() < 8:
         raise ValueError("status needs 8 bytes")
-    _run("saf_kv_append", _lib.saf_kv_append, idx, stream, qp, kp, vp, _I64x9(*qs, *ks, *vs), _at(ctx, idx, i32),
-         _at(n_new, idx, i32), _at(page_table, idx, i32), max_pages, freq if rope else None, rope,
-         1 if interleaved else 0, pos_base, _flags(frozen, H), B, H, Hkv, T, d, num_pages, page_size, _dt(v),
-         _at(q_out, idx, dt), _at(k_cache, idx, dt), _at(v_cache, idx, dt),
-         None if status is None else _at(status, idx, status.dtype))
+    _run("saf_kv_append", _lib.saf_kv_append, idx, stream, qp, kp, vp, _I64x9(qb, qh, qt, kb, kh, kt, vb, vh, vt),
+         _at(ctx, idx, i32), _at(n_new, idx, i32), _at(page_table, idx, i32), max_pages, freq, rope,
+         1 if interleaved else 0, pos_base, _flags(frozen, H), B, H, Hkv, T, d, num_pages, page_size, _dt(v), qo,
+         _at(k_cache, idx, dt), _at(v_cache, idx, dt), None if status is None else _at(status, idx, status.dtype))
     return q_out
 
 
