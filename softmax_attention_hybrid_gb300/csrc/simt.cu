@@ -31,15 +31,21 @@ constexpr int kLd = kB + 1;     // padded fp32 row stride of a (key x query) til
 constexpr int kThreads = 256;
 // floats per tile slot: every tile, (rows x D) or (key x query), fits one slot
 template <int D>
-__host__ __device__ constexpr int tile_floats() { return kB * ((D > kB ? D : kB) + 1); }
+__host__ __device__ constexpr int tile_floats() { return kB * ((D > kB ? D : kB) + 4); }
 
-// rows r0 .. r0 + 63 of a [T, D] slice into shared memory, row stride D + 1
+// rows r0 .. r0 + 63 of a [T, D] slice into shared memory, row stride D + 4
 template <int D, typename E>
 __device__ __forceinline__ void load_tile(float* s, const E* g, int r0, int T) {
-    for (int e = threadIdx.x; e < kB * D; e += kThreads) {
+    for (int e = 4 * threadIdx.x; e < kB * D; e += 4 * kThreads) {
         const int rr = e / D, c = e - rr * D;
         const int row = r0 + rr;
-        s[rr * (D + 1) + c] = row < T ? to_f(g[(size_t)row * D + c]) : 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < T) {
+            const E* p = g + (size_t)row * D + c;
+            if constexpr (sizeof(E) == 4) x = *reinterpret_cast<const float4*>(p);
+            else x = make_float4(to_f(p[0]), to_f(p[1]), to_f(p[2]), to_f(p[3]));
+        }
+        *reinterpret_cast<float4*>(s + rr * (D + 4) + c) = x;
     }
 }
 
@@ -47,6 +53,31 @@ __device__ __forceinline__ void load_tile(float* s, const E* g, int r0, int T) {
 template <bool kWin>
 __device__ __forceinline__ bool in_window(const LayerArgs& p, int i, int j) {
     return !kWin || i - j < p.window || j < p.sinks;
+}
+
+// dot[i][c] += x_i . y_c over D, x_i row 4 ty + i of X, y_c row tx + 16 c of Y: each element is read
+// once for four products, 16 bytes at a time. (Every sum runs over e in order.)
+template <int D>
+__device__ __forceinline__ void tile_dots(const float* X, const float* Y, int ty, int tx, float (&dot)[4][4]) {
+    constexpr int LdD = D + 4;
+#pragma unroll 2
+    for (int e = 0; e < D; e += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = *reinterpret_cast<const float4*>(X + (ty * 4 + i) * LdD + e);
+            y[i] = *reinterpret_cast<const float4*>(Y + (tx + 16 * i) * LdD + e);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                dot[i][c] = fmaf(x[i].x, y[c].x, dot[i][c]);
+                dot[i][c] = fmaf(x[i].y, y[c].y, dot[i][c]);
+                dot[i][c] = fmaf(x[i].z, y[c].z, dot[i][c]);
+                dot[i][c] = fmaf(x[i].w, y[c].w, dot[i][c]);
+            }
+    }
 }
 
 __device__ __forceinline__ float quad16_max(float x) {
@@ -65,7 +96,7 @@ template <typename E, int D, bool kWin>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
     extern __shared__ float sm[];
     float* Qs = sm;
-    constexpr int LdD = D + 1, NC = D / 16, kT = tile_floats<D>();
+    constexpr int LdD = D + 4, NC = D / 16, kT = tile_floats<D>();
     float* Ks = Qs + kT;
     float* Vs = Ks + kT;
     float* Ps = Vs + kT;
@@ -104,7 +135,8 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
         if (!frozen) load_tile<D>(Ks, k, kb * kB, T);
         load_tile<D>(Vs, v, kb * kB, T);
         __syncthreads();
-        float s[4][4];
+        float s[4][4], dot[4][4] = {};
+        if (!frozen) tile_dots<D>(Qs, Ks, ty, tx, dot);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = q0 + ty * 4 + i;
@@ -116,12 +148,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
                     const bool ok = key <= row && row < T;
                     s[i][c] = ok ? expf(a[key] + r[row - key] - lzr[i]) : 0.f;
                 } else {
-                    float dot = 0.f;
-                    const float* qr = Qs + (ty * 4 + i) * LdD;
-                    const float* kr = Ks + (tx + 16 * c) * LdD;
-#pragma unroll 16
-                    for (int e = 0; e < D; ++e) dot = fmaf(qr[e], kr[e], dot);
-                    s[i][c] = (key <= row && key < T && in_window<kWin>(p, row, key)) ? dot * scale : -INFINITY;
+                    s[i][c] = (key <= row && key < T && in_window<kWin>(p, row, key)) ? dot[i][c] * scale : -INFINITY;
                 }
             }
         }
@@ -186,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
 template <typename E, int D, bool kWin>
 __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
     extern __shared__ float sm[];
-    constexpr int LdD = D + 1, NC = D / 16, kT = tile_floats<D>();
+    constexpr int LdD = D + 4, NC = D / 16, kT = tile_floats<D>();
     float* Ks = sm;
     float* Vs = Ks + kT;
     float* Qs = Vs + kT;
@@ -241,6 +268,11 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
             }
         }
         __syncthreads();
+        float dot[4][4] = {}, dpt[4][4] = {};
+        if (!frozen) {
+            tile_dots<D>(Ks, Qs, ty, tx, dot);
+            tile_dots<D>(Vs, dOs, ty, tx, dpt);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int key = k0 + ty * 4 + i;
@@ -253,18 +285,8 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
                 if (frozen) {
                     pt = ok ? expf(a[key] + r[qi - key] - rowstat[qq]) : 0.f;
                 } else {
-                    float dot = 0.f, dpt = 0.f;
-                    const float* kr = Ks + (ty * 4 + i) * LdD;
-                    const float* qr = Qs + qq * LdD;
-                    const float* vr = Vs + (ty * 4 + i) * LdD;
-                    const float* gr = dOs + qq * LdD;
-#pragma unroll 16
-                    for (int e = 0; e < D; ++e) {
-                        dot = fmaf(kr[e], qr[e], dot);
-                        dpt = fmaf(vr[e], gr[e], dpt);
-                    }
-                    pt = ok && in_window<kWin>(p, qi, key) ? expf(dot * scale - rowstat[qq]) : 0.f;
-                    dst = pt * (dpt - rowD[qq]);
+                    pt = ok && in_window<kWin>(p, qi, key) ? expf(fmaf(dot[i][c], scale, -rowstat[qq])) : 0.f;
+                    dst = pt * (dpt[i][c] - rowD[qq]);
                 }
                 Pt[(ty * 4 + i) * kLd + qq] = pt;
                 dSt[(ty * 4 + i) * kLd + qq] = dst;
@@ -314,7 +336,7 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
 template <typename E, int D, bool kWin>
 __global__ void __launch_bounds__(kThreads) bwd_q_kernel(LayerArgs p) {
     extern __shared__ float sm[];
-    constexpr int LdD = D + 1, NC = D / 16, kT = tile_floats<D>();
+    constexpr int LdD = D + 4, NC = D / 16, kT = tile_floats<D>();
     float* Qs = sm;
     float* dOs = Qs + kT;
     float* Ks = dOs + kT;
@@ -360,25 +382,18 @@ __global__ void __launch_bounds__(kThreads) bwd_q_kernel(LayerArgs p) {
         load_tile<D>(Ks, k, kb * kB, T);
         load_tile<D>(Vs, v, kb * kB, T);
         __syncthreads();
+        float dot[4][4] = {}, dp[4][4] = {};
+        tile_dots<D>(Qs, Ks, ty, tx, dot);
+        tile_dots<D>(dOs, Vs, ty, tx, dp);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = q0 + ty * 4 + i;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int key = kb * kB + tx + 16 * c;
-                float dot = 0.f, dp = 0.f;
-                const float* qr = Qs + (ty * 4 + i) * LdD;
-                const float* kr = Ks + (tx + 16 * c) * LdD;
-                const float* gr = dOs + (ty * 4 + i) * LdD;
-                const float* vr = Vs + (tx + 16 * c) * LdD;
-#pragma unroll 16
-                for (int e = 0; e < D; ++e) {
-                    dot = fmaf(qr[e], kr[e], dot);
-                    dp = fmaf(gr[e], vr[e], dp);
-                }
                 const bool ok = key <= row && row < T && in_window<kWin>(p, row, key);
-                const float pij = ok ? expf(dot * scale - lse[i]) : 0.f;
-                dSs[(ty * 4 + i) * kLd + tx + 16 * c] = pij * (dp - Dr[i]);
+                const float pij = ok ? expf(dot[i][c] * scale - lse[i]) : 0.f;
+                dSs[(ty * 4 + i) * kLd + tx + 16 * c] = pij * (dp[i][c] - Dr[i]);
             }
         }
         __syncthreads();
