@@ -196,7 +196,8 @@ void set_items(PagedArgs& p, const Plan& x, int nfrozen) {
         p.per_chunk[i] = (int)ceil_div(nt[i], c);
         p.chunks[i] = (int)ceil_div(nt[i], p.per_chunk[i]);
         items[i] = (unsigned)(x.units[i] * p.chunks[i]);
-        // few own items run beside the prefix's, in the same round
+        // Few own items run beside the prefix's, in the same round. (Half of the slots for the
+        // prefix beside many own items was slower: 176 against 111 us for 64 sequences after 32K.)
         if (items[i] < slots / 2) slots -= items[i];
     }
     p.nsplit = p.chunks[0] + p.chunks[1];

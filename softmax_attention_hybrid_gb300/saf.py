@@ -378,9 +378,11 @@ def saf_attn_bwd_prepared(q, k, v, o, do, lse, a, r, frozen, state, dq=None, dk=
     return dq, dk, dv
 
 
-# The calls below are short enough on the GPU that their checks in Python count: each tensor is
-# looked at once, and what is wrong is named on a second look (_refuse).
+# The calls below are short enough on the GPU that their checks in Python count: what every call
+# has is checked in one expression, and what is wrong is named on a second look (_at).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 _I64x9 = ctypes.c_int64 * 9
 
 
@@ -428,7 +430,7 @@ def _flags(frozen, H):
 
 def _run(where, fn, idx, stream, *args):
     """fn(*args, stream) with device `idx` current, on `stream` or the device's current one."""
-    if torch.cuda.current_device() != idx:
+    if _get_device() != idx:
         with torch.cuda.device(idx):
             return _run(where, fn, idx, stream, *args)
     if stream is not None:
@@ -459,7 +461,9 @@ def saf_attn_fwd_window(q, k, v, a, r, frozen, window, sinks=0, state=None, o=No
     idx, dt = _device(v), v.dtype
     B, H, Hkv, T, d = _gqa_shape(q, v, frozen)
     full, rows = (B, H, T, d), (B, H, T)
-    _shapes(("q", q, full), ("k", k, v.shape), ("o", o, full), ("lse", lse, rows))
+    if ((q is not None and q.shape != full) or (k is not None and k.shape != v.shape)
+            or (o is not None and o.shape != full) or (lse is not None and lse.shape != rows)):
+        _shapes(("q", q, full), ("k", k, v.shape), ("o", o, full), ("lse", lse, rows))
     if o is None:
         o = torch.empty(full, dtype=dt, device=v.device)
     if lse is None:
@@ -587,28 +591,37 @@ def alloc_paged_workspace(B, H, Hkv, T, d, max_len, dtype, prefix_len=0, device=
 
 def _paged(where, fn, q, k_cache, v_cache, prefix, P, page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o,
            lse, workspace, stream):
-    idx, dt, i32 = _device(q), q.dtype, torch.int32
-    full = q.shape
+    idx, dt = _device(q), q.dtype
+    full, caches, table = q.shape, v_cache.shape, page_table.shape
     B, H, T, d = full
-    num_pages, Hkv, page_size, width = v_cache.shape
-    if width != d or (k_cache is not None and k_cache.shape != v_cache.shape):
+    num_pages, Hkv, page_size, width = caches
+    if width != d or (k_cache is not None and k_cache.shape != caches):
         raise ValueError("the caches must both be [num_pages, Hkv, page_size, d]")
-    max_pages = _table(ctx, n_new, page_table, B)
+    if len(table) != 2 or table[0] != B:
+        raise ValueError("page_table must be [B, max_pages]")
+    if ctx.shape != (B,) or (n_new is not None and n_new.shape != (B,)):
+        raise ValueError("ctx and n_new must be [B]")
     if o is None:
         o = torch.empty(full, dtype=dt, device=q.device)
-    elif o.shape != full:
-        raise ValueError(f"o must have shape {tuple(full)}")
     if lse is None:
-        lse = torch.empty(full[:3], dtype=torch.float32, device=q.device)
-    elif lse.shape != full[:3]:
-        raise ValueError(f"lse must have shape {tuple(full[:3])}")
+        lse = torch.empty(full[:3], dtype=_F32, device=q.device)
+    if o.shape != full or lse.shape != full[:3]:
+        raise ValueError(f"o and lse must have shapes {tuple(full)} and {tuple(full[:3])}")
     if workspace is None:
         workspace = alloc_paged_workspace(B, H, Hkv, T, d, max_len, dt, P, q.device)
+    if not (idx == v_cache.get_device() == page_table.get_device() == ctx.get_device() == o.get_device()
+            == lse.get_device() == workspace.get_device()
+            and dt is v_cache.dtype and dt is o.dtype and lse.dtype is _F32 and page_table.dtype is _I32
+            and ctx.dtype is _I32 and workspace.dtype is _U8
+            and q.is_contiguous() and v_cache.is_contiguous() and page_table.is_contiguous() and ctx.is_contiguous()
+            and o.is_contiguous() and lse.is_contiguous() and workspace.is_contiguous()):
+        for t, want in ((q, dt), (v_cache, dt), (page_table, _I32), (ctx, _I32), (o, dt), (lse, _F32), (workspace, _U8)):
+            _at(t, idx, want)
     ap, rp, ld = _prior(a, r, H, idx, P + max_len)
-    _run(where, fn, idx, stream, _at(q, idx, dt), _at(k_cache, idx, dt), _at(v_cache, idx, dt), *prefix,
-         _at(page_table, idx, i32), max_pages, _at(ctx, idx, i32), _at(n_new, idx, i32), ap, rp, ld,
-         _flags(frozen, H), int(window), int(sinks), B, H, Hkv, T, d, max_len, num_pages, page_size, _dt(q), _at(o, idx, dt),
-         _at(lse, idx, torch.float32), _at(workspace, idx, torch.uint8), workspace.numel())
+    _run(where, fn, idx, stream, q.data_ptr(), _at(k_cache, idx, dt), v_cache.data_ptr(), *prefix,
+         page_table.data_ptr(), table[1], ctx.data_ptr(), _at(n_new, idx, _I32), ap, rp, ld,
+         _flags(frozen, H), int(window), int(sinks), B, H, Hkv, T, d, max_len, num_pages, page_size, _dt(q),
+         o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return o, lse
 
 

@@ -56,7 +56,7 @@ def test_window_refusals(saf):
 
 def _paged(lib, shared=False, **kw):
     x = dict(q=F, k=F, v=F, pp=F, P=100, table=F, mp=8, ctx=F, new=None, a=F, r=F, ld=1000, frozen=None, window=0,
-             sinks=0, B=2, H=4, Hkv=2, T=1, d=64, ml=128, np=64, ps=16, dt=0, o=F, lse=F, ws=F, wsb=1 << 30)
+             sinks=0, B=2, H=4, Hkv=2, T=1, d=64, ml=512, np=64, ps=64, dt=0, o=F, lse=F, ws=F, wsb=1 << 30)
     x.update(kw)
     fn = lib.saf_attn_paged_shared if shared else lib.saf_attn_paged
     mid = (x["pp"], x["P"]) if shared else ()
@@ -70,16 +70,16 @@ def test_paged_refusals(saf, shared):
     lib = saf.library()
     bad = lambda **kw: _paged(lib, shared, **kw)   # noqa: E731
     for kw in (dict(B=-1), dict(H=0), dict(Hkv=3), dict(H=300, Hkv=300), dict(T=-1), dict(dt=3), dict(ml=0),
-               dict(ml=129), dict(window=-1), dict(sinks=-2), dict(np=0), dict(mp=0), dict(ps=4), dict(ps=24),
+               dict(ml=513), dict(window=-1), dict(sinks=-2), dict(np=0), dict(mp=0), dict(ps=4), dict(ps=24),
                dict(ps=2048), dict(v=None), dict(q=None), dict(k=None), dict(table=None), dict(ctx=None), dict(o=None),
                dict(lse=None), dict(np=2 ** 30, Hkv=4), dict(B=2 ** 20, T=2 ** 10)):
         assert bad(**kw) == saf.SAF_EINVAL, kw
     assert bad(d=80) == saf.SAF_EUNSUPPORTED
     fz = bytes([0, 0, 1, 0])
     assert bad(frozen=fz, a=None) == saf.SAF_EINVAL
-    assert bad(frozen=fz, ld=127) == saf.SAF_EINVAL
+    assert bad(frozen=fz, ld=511) == saf.SAF_EINVAL
     if shared:
-        assert bad(frozen=fz, ld=227) == saf.SAF_EINVAL
+        assert bad(frozen=fz, ld=611) == saf.SAF_EINVAL
         assert bad(pp=None) == saf.SAF_EINVAL
         assert bad(P=-1) == saf.SAF_EINVAL
         assert bad(P=2 ** 30) == saf.SAF_EINVAL
@@ -87,7 +87,7 @@ def test_paged_refusals(saf, shared):
                dict(ctx=F + 2), dict(new=F + 3), dict(ws=F + 64)):
         assert bad(**kw) == saf.SAF_EALIGN, kw
     assert bad(ws=None) == saf.SAF_EWORKSPACE
-    need = lib.saf_attn_paged_workspace_bytes(2, 4, 2, 1, 64, 128, 100 if shared else 0, 0)
+    need = lib.saf_attn_paged_workspace_bytes(2, 4, 2, 1, 64, 512, 100 if shared else 0, 0)
     assert need > 256 and bad(wsb=need - 1) == saf.SAF_EWORKSPACE
     assert bad(T=0, q=None, v=None, ws=None) == saf.SAF_OK
     assert bad(B=0, q=None, v=None, ws=None) == saf.SAF_OK
