@@ -30,6 +30,8 @@
 // of the memory, against 512 cycles of MMAs.
 #include <string.h>
 
+#include <atomic>
+
 #include "paged.h"
 #include "tc_common.cuh"
 
@@ -712,14 +714,14 @@ cudaError_t launch_d(const TcParams& P, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // A build that launches with fewer registers could never hand the row warps theirs (a
     // property of the compiled kernel, looked up once).
-    static int regs = 0;
-    if (regs == 0) {
+    static std::atomic<int> regs{0};
+    if (regs.load() == 0) {
         cudaFuncAttributes fa;
         e = cudaFuncGetAttributes(&fa, paged_tc_kernel<kD>);
         if (e != cudaSuccess) return e;
-        regs = fa.numRegs;
+        regs.store(fa.numRegs);
     }
-    if (kRegsRows + kRegsOther > 2 * regs) return cudaErrorInvalidConfiguration;
+    if (kRegsRows + kRegsOther > 2 * regs.load()) return cudaErrorInvalidConfiguration;
     return launch_ex(paged_tc_kernel<kD>, dim3(P.a.items), dim3(kThreads), (size_t)smem, s, true, 1, P);
 }
 

@@ -199,6 +199,76 @@ def test_large_scores(saf):
         x.check(*x.call(saf))
 
 
+def test_positions_far_apart(saf):
+    # rows of one block 2500 positions apart: the frozen heads' patterns do not fit beside the tiles
+    for dtype, d in (("bf16", 64), ("bf16", 128), ("fp32", 64)):
+        frozen = [0, 1, 0, 0]
+        x = Batch(dtype, 4, 2, 1, d, 64, (0, 2500, 1200), (1, 1, 1), prefix=200, seed=13)
+        x.check(*x.call(saf, frozen), frozen)
+        x = Batch(dtype, 4, 2, 1, d, 64, (0, 2500, 1200), (1, 1, 1), prefix=200, seed=14)
+        x.check(*x.call(saf, frozen, 300, 5), frozen, 300, 5)
+
+
+def test_a_long_chunk_of_a_prompt(saf):
+    for dtype in ("bf16", "fp32"):
+        frozen = [0, 0, 0, 1]
+        x = Batch(dtype, 4, 1, 400, 64, 32, (700, 0), (400, 399), seed=15)
+        x.check(*x.call(saf, frozen, 260, 3), frozen, 260, 3)
+
+
+def test_large_pages_and_no_prefix(saf):
+    for dtype in ("bf16", "fp32"):
+        for page in (512, 1024):
+            x = Batch(dtype, 4, 4, 2, 64, page, (1500, 3), (2, 2), seed=page)
+            o, lse = x.call(saf, [0, 1, 0, 0])
+            x.check(o, lse, [0, 1, 0, 0])
+            o2, lse2 = saf.saf_attn_paged_shared(x.q.cuda(), x.kc.cuda(), x.vc.cuda(), None, 0, x.table.cuda(),
+                                                 x.ctx.cuda(), x.max_len, x.n_new.cuda(), x.a.cuda(), x.r.cuda(),
+                                                 [0, 1, 0, 0])
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp32", 64)])
+def test_offsets_past_32_bits(saf, dtype, d):
+    # caches of more than 2^32 elements, of which the last pages are used (the rest is never touched)
+    Hkv, page, used = 8, 64, 12
+    num = 2 ** 32 // (Hkv * page * d) + 1 + used
+    dt = DT[dtype]
+    g = torch.Generator().manual_seed(1)
+    kc, vc = (torch.empty(num, Hkv, page, d, dtype=dt, device="cuda") for _ in range(2))
+    assert kc[num - used:].storage_offset() > 2 ** 32
+    x = Batch(dtype, 8, Hkv, 1, d, page, (300, 290), (1, 1), seed=3)
+    perm = num - used + torch.randperm(used, generator=g)[:10].reshape(2, 5)
+    table = perm.int().cuda()
+    k, v = (torch.randn(2, Hkv, 300, d, generator=g).to(dt).cuda() for _ in range(2))
+    ctx0, n0 = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.tensor([300, 290], dtype=torch.int32).cuda()
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    saf.saf_kv_append(k, v, kc, vc, table, ctx0, n0, status=status)
+    k1, v1 = (torch.randn(2, Hkv, 1, d, generator=g).to(dt).cuda() for _ in range(2))
+    saf.saf_kv_append(k1, v1, kc, vc, table, n0, status=status)
+    o, lse = saf.saf_attn_paged(x.q.cuda(), kc, vc, table, n0, 301)
+    small = kc[num - used:].clone(), vc[num - used:].clone()
+    o2, lse2 = saf.saf_attn_paged(x.q.cuda(), *small, (table - (num - used)).int(), n0, 301)
+    assert saf.saf_device_status(status) == saf.SAF_OK
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for b, n in ((0, 300), (1, 290)):
+        at = torch.arange(n + 1)
+        got = small[1][(perm[b] - (num - used))[at // page].cuda(), :, (at % page).cuda()]
+        assert torch.equal(got[:n].transpose(0, 1), v[b, :, :n]) and torch.equal(got[n], v1[b, :, 0])
+
+
+def test_on_a_given_stream(saf):
+    x = Batch("bf16", 4, 2, 1, 64, 16, (100, 60), (1, 1), seed=5)
+    want = x.call(saf)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ws = saf.alloc_paged_workspace(2, 4, 2, 1, 64, x.max_len, torch.bfloat16)
+    torch.cuda.synchronize()
+    got = x.call(saf, stream=side, workspace=ws)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_counts_and_pages_out_of_bounds_are_reported(saf):
     # a bad entry reaches no memory: the keys of such a page are not seen, the counts are cut
     for dtype in ("bf16", "fp32"):

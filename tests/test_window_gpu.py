@@ -151,6 +151,33 @@ def test_prepared_state(saf):
         _check(dtype, x, b, frozen, 50, 3)
 
 
+def test_every_head_frozen_without_q_and_k(saf):
+    for dtype, d in (("bf16", 64), ("bf16", 128), ("fp32", 96)):
+        x, g = _inputs(dtype, 1, 4, 2, 300, d, (0, 1, 2, 3), seed=40)
+        frozen = bytes([1] * 4)
+        o, lse = saf.saf_attn_fwd_window(None, None, g["v"], g["a"], g["r"], frozen, 20, 2)
+        want, want_lse = saf.saf_attn_fwd_gqa(None, None, g["v"], g["a"], g["r"], frozen)
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
+        dq, dk, dv = saf.saf_attn_bwd_window(None, None, g["v"], o, g["do"], lse, g["a"], g["r"], frozen, 20, 2)
+        _, _, want_dv = saf.saf_attn_bwd_gqa(None, None, g["v"], o, g["do"], lse, g["a"], g["r"], frozen)
+        assert not dq.any() and not dk.any() and torch.equal(dv, want_dv)
+
+
+@pytest.mark.parametrize("B,T", [(0, 64), (2, 0)])
+def test_empty(saf, B, T):
+    q = torch.empty(B, 4, T, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.empty(B, 2, T, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = saf.saf_attn_fwd_window(q, k, k, None, None, None, 8, 1)
+    dq, dk, dv = saf.saf_attn_bwd_window(q, k, k, o, q, lse, None, None, None, 8, 1)
+    assert o.shape == q.shape and dq.shape == q.shape and dk.shape == dv.shape == k.shape
+
+
+def test_largest_head_count(saf):
+    x, g = _inputs("bf16", 1, 256, 64, 140, 64, tuple(h for h in range(256) if h % 4 == 3), seed=41)
+    flags = [h % 4 == 3 for h in range(256)]
+    _check("bf16", x, _run(saf, g, flags, 9, 2), flags, 9, 2)
+
+
 def test_nan_keys_outside_every_window(saf):
     # whole key blocks that no row of a query block sees are not visited: a NaN there stays there.
     # 640 tokens, window 100, no sinks: rows from 384 on see keys from 285 on, in blocks from 256 on
