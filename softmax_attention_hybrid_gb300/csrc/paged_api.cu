@@ -18,6 +18,10 @@ constexpr int kRounds = 8;
 // the join), in tiles. Measured: 32 sequences of 4K to 16K tokens, 8 key/value heads, d 128 take
 // 237, 211, 210, 218, 215 us with 2, 3, 5, 8, 12 items per sequence and head.
 constexpr int kSetUp = 10;
+// What the joining kernel costs, in tiles, where a call could do without one: one new token of
+// one sequence (12 heads, d 64) takes 6.1 and 7.1 us with 1 and 2 items for 256 keys, 7.6 with 1
+// and 4 for 512, 10.5 and 8.5 for 1024.
+constexpr int kJoin = 3;
 
 // Joins the items of a row. kWarps warps share a row (a block of four warps holds 4 / kWarps
 // rows): with few items a warp each, with many the four warps of a block, whose loads are
@@ -150,19 +154,20 @@ Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, bool bf1
 // Items along the keys for `units` units of `nt` tiles each: the number that makes the part
 // shortest, with `slots` items at a time. even: the units have the same length, so that rounds
 // end together; else their lengths differ, and the last items run alone for a while.
-// Candidates: the most items that fit in 1, 2, ... rounds, and the minimum over c of
+// Candidates: one, the most items that fit in 1, 2, ... rounds, and the minimum over c of
 // (units c / slots) (kSetUp + nt / c) + nt / c, the work and the tail of c items per unit.
-long long pick_chunks(long long units, long long nt, long long most, long long slots, bool even) {
+long long pick_chunks(long long units, long long nt, long long most, long long slots, bool even, bool joins_anyway) {
     long long best = 1;
     double best_cost = 1e300;
-    for (int r = 0; r <= kRounds; ++r) {
-        long long c = r ? slots * r / units
+    for (int r = -1; r <= kRounds; ++r) {
+        long long c = r < 0 ? 1 : r ? slots * r / units
                         : (long long)sqrt((double)nt * (double)slots / ((double)units * (double)kSetUp));
         c = c < 1 ? 1 : c > most ? most : c;
         const long long per = ceil_div(nt, c);
         const double rounds = (double)(units * ceil_div(nt, per)) / (double)slots;
-        const double cost = (even ? ceil(rounds) : rounds + 1.0) * (double)(kSetUp + per);
-        if (cost < best_cost) {
+        const double cost =
+            (even ? ceil(rounds) : rounds + 1.0) * (double)(kSetUp + per) + (c > 1 && !joins_anyway ? kJoin : 0);
+        if (cost < best_cost || (cost == best_cost && c < best)) {
             best_cost = cost;
             best = c;
         }
@@ -192,7 +197,8 @@ void set_items(PagedArgs& p, const Plan& x, int nfrozen) {
             if (n < nt[i]) nt[i] = n;
         }
         // (a prefix's units have the same length, and so have windows)
-        const long long c = pick_chunks(x.units[i], nt[i], most_chunks(x, i, nt[i]), slots, i == 0 || windowed);
+        const long long c = pick_chunks(x.units[i], nt[i], most_chunks(x, i, nt[i]), slots, i == 0 || windowed,
+                                        p.P > 0);
         p.per_chunk[i] = (int)ceil_div(nt[i], c);
         p.chunks[i] = (int)ceil_div(nt[i], p.per_chunk[i]);
         items[i] = (unsigned)(x.units[i] * p.chunks[i]);
