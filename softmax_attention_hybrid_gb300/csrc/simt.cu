@@ -15,10 +15,13 @@
 // kWin instances serve ordinary heads with a sliding window and sinks: they visit the key
 // (query) blocks that some row of the block sees and hide the other pairs.
 //
-// Tile: 64 query rows x 64 keys, head dimension D = 64, 96 or 128, 256
-// threads. Thread (ty, tx), ty = tid / 16, tx = tid % 16, owns rows
-// 4*ty .. 4*ty+3 and the columns tx, tx+16, ... of the key axis (4 of them)
-// or of the head-dimension axis (D / 16 of them).
+// Tile: 16 RT own rows (query rows, or keys in the key-block pass) x 64 of the
+// other axis, head dimension D = 64, 96 or 128, 256 threads, RT = 4. Thread
+// (ty, tx), ty = tid / 16, tx = tid % 16, owns rows RT ty .. RT ty + RT - 1 and
+// the columns tx, tx + 16, ... of the other axis (4 of them) or D / 16 columns
+// of the head dimension, in vectors of 4 (2 at D = 96). Windowed calls that
+// would leave most of the GPU idle take RT = 1: four times the programs, each
+// with a quarter of the rows, and the same sums in the same order.
 #include <math.h>
 
 #include "saf_internal.h"
@@ -27,16 +30,22 @@ namespace saf {
 namespace {
 
 constexpr int kB = 64;          // rows per tile (queries and keys)
-constexpr int kLd = kB + 1;     // padded fp32 row stride of a (key x query) tile
+constexpr int kLd = kB + 4;     // padded fp32 row stride of a (key x query) tile
 constexpr int kThreads = 256;
+// A windowed launch of fewer blocks of 64 rows takes blocks of 16. A training step with a window of 100
+// takes, with 64 and 16 rows: T 250, 4 heads, d 64 (16 blocks) 115 and 80 us; T 250, 16 heads over 4, d 96
+// (64 and 16 blocks) 337 and 262; T 512, 12 heads, d 64 (96) 167 and 170; T 500, 12 heads, d 128 (96)
+// 339 and 473; T 1000, 12 heads, d 64 (192) 334 and 343.
+constexpr long long kFewBlocks = 76;
 // floats per tile slot: every tile, (rows x D) or (key x query), fits one slot
 template <int D>
 __host__ __device__ constexpr int tile_floats() { return kB * ((D > kB ? D : kB) + 4); }
 
-// rows r0 .. r0 + 63 of a [T, D] slice into shared memory, row stride D + 4
-template <int D, typename E>
+// rows r0 .. r0 + R - 1 of a [T, D] slice into shared memory, row stride D + 4
+template <int D, int R, typename E>
 __device__ __forceinline__ void load_tile(float* s, const E* g, int r0, int T) {
-    for (int e = 4 * threadIdx.x; e < kB * D; e += 4 * kThreads) {
+#pragma unroll 4
+    for (int e = 4 * threadIdx.x; e < R * D; e += 4 * kThreads) {
         const int rr = e / D, c = e - rr * D;
         const int row = r0 + rr;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -55,21 +64,20 @@ __device__ __forceinline__ bool in_window(const LayerArgs& p, int i, int j) {
     return !kWin || i - j < p.window || j < p.sinks;
 }
 
-// dot[i][c] += x_i . y_c over D, x_i row 4 ty + i of X, y_c row tx + 16 c of Y: each element is read
-// once for four products, 16 bytes at a time. (Every sum runs over e in order.)
-template <int D>
-__device__ __forceinline__ void tile_dots(const float* X, const float* Y, int ty, int tx, float (&dot)[4][4]) {
+// dot[i][c] += x_i . y_c over D, x_i row RT ty + i of X, y_c row tx + 16 c of Y: each element is read
+// once for all of its products, 16 bytes at a time. (Every sum runs over e in order.)
+template <int D, int RT>
+__device__ __forceinline__ void tile_dots(const float* X, const float* Y, int ty, int tx, float (&dot)[RT][4]) {
     constexpr int LdD = D + 4;
 #pragma unroll 2
     for (int e = 0; e < D; e += 4) {
-        float4 x[4], y[4];
+        float4 x[RT], y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[i] = *reinterpret_cast<const float4*>(X + (ty * 4 + i) * LdD + e);
-            y[i] = *reinterpret_cast<const float4*>(Y + (tx + 16 * i) * LdD + e);
-        }
+        for (int i = 0; i < RT; ++i) x[i] = *reinterpret_cast<const float4*>(X + (ty * RT + i) * LdD + e);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const float4*>(Y + (tx + 16 * c) * LdD + e);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 dot[i][c] = fmaf(x[i].x, y[c].x, dot[i][c]);
@@ -77,6 +85,56 @@ __device__ __forceinline__ void tile_dots(const float* X, const float* Y, int ty
                 dot[i][c] = fmaf(x[i].z, y[c].z, dot[i][c]);
                 dot[i][c] = fmaf(x[i].w, y[c].w, dot[i][c]);
             }
+    }
+}
+
+// A thread's columns of the head dimension: NV vectors of VW, vector u at column at(u).
+template <int D>
+struct Cols {
+    static constexpr int VW = D == 96 ? 2 : 4, NV = D / 16 / VW;
+    static __device__ __forceinline__ int at(int u, int tx) { return VW * (tx + 16 * u); }
+    static __device__ __forceinline__ void load(float* x, const float* row, int tx) {   // row of a tile
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            if constexpr (VW == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(row + at(u, tx));
+                x[4 * u] = y.x, x[4 * u + 1] = y.y, x[4 * u + 2] = y.z, x[4 * u + 3] = y.w;
+            } else {
+                const float2 y = *reinterpret_cast<const float2*>(row + at(u, tx));
+                x[2 * u] = y.x, x[2 * u + 1] = y.y;
+            }
+        }
+    }
+    template <typename E>
+    static __device__ __forceinline__ void store(E* row, const float* x, float f, int tx) {
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+#pragma unroll
+            for (int e = 0; e < VW; ++e) from_f(row + at(u, tx) + e, x[VW * u + e] * f);
+    }
+};
+
+// acc[i][c] += sum over the 64 rows j of Y of w_ij Y[j][column c], w_ij row RT ty + i of W (stride
+// kLd); j in order.
+template <int D, int RT>
+__device__ __forceinline__ void tile_sums(const float* W, const float* Y, int ty, int tx, float (&acc)[RT][D / 16]) {
+    constexpr int NC = D / 16, LdD = D + 4;
+#pragma unroll 2
+    for (int j = 0; j < kB; j += 4) {
+        float w[RT][4], y[4][NC];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const float4 x = *reinterpret_cast<const float4*>(W + (ty * RT + i) * kLd + j);
+            w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) Cols<D>::load(y[u], Y + (j + u) * LdD, tx);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) acc[i][c] = fmaf(w[i][u], y[u][c], acc[i][c]);
     }
 }
 
@@ -90,13 +148,13 @@ __device__ __forceinline__ float quad16_sum(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// Forward. Grid (ceil(T/64), B*H).
+// Forward. Grid (ceil(T / 16 RT), B*H).
 // ---------------------------------------------------------------------------
-template <typename E, int D, bool kWin>
+template <typename E, int D, bool kWin, int RT>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
     extern __shared__ float sm[];
     float* Qs = sm;
-    constexpr int LdD = D + 4, NC = D / 16, kT = tile_floats<D>();
+    constexpr int NC = D / 16, kT = tile_floats<D>(), kR = 16 * RT;
     float* Ks = Qs + kT;
     float* Vs = Ks + kT;
     float* Ps = Vs + kT;
@@ -112,15 +170,15 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
     const E* v = (const E*)p.v + kvbase;
     const float* a = p.a + (size_t)h * p.ld_prior;
     const float* r = p.r + (size_t)h * p.ld_prior;
-    const int q0 = qb * kB;
+    const int q0 = qb * kR;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const float scale = 1.f / sqrtf((float)D);
 
-    if (!frozen) load_tile<D>(Qs, q, q0, T);
-    float m[4], l[4], lzr[4], acc[4][NC];
+    if (!frozen) load_tile<D, kR>(Qs, q, q0, T);
+    float m[RT], l[RT], lzr[RT], acc[RT][NC];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = q0 + ty * 4 + i;
+    for (int i = 0; i < RT; ++i) {
+        const int row = q0 + ty * RT + i;
         m[i] = -INFINITY;
         l[i] = 0.f;
         lzr[i] = (frozen && row < T) ? p.lz[(size_t)h * T + row] : 0.f;
@@ -128,18 +186,18 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
         for (int c = 0; c < NC; ++c) acc[i][c] = 0.f;
     }
 
-    const KeyBlocks<kWin> blocks(q0, qb, kWin && frozen ? T : p.window, p.sinks, kB);
+    const KeyBlocks<kWin> blocks(q0, (q0 + kR - 1) / kB, kWin && frozen ? T : p.window, p.sinks, kB);
     for (int jj = 0; jj < blocks.n; ++jj) {
         const int kb = blocks.id(jj);
         __syncthreads();
-        if (!frozen) load_tile<D>(Ks, k, kb * kB, T);
-        load_tile<D>(Vs, v, kb * kB, T);
+        if (!frozen) load_tile<D, kB>(Ks, k, kb * kB, T);
+        load_tile<D, kB>(Vs, v, kb * kB, T);
         __syncthreads();
-        float s[4][4], dot[4][4] = {};
-        if (!frozen) tile_dots<D>(Qs, Ks, ty, tx, dot);
+        float s[RT][4], dot[RT][4] = {};
+        if (!frozen) tile_dots<D, RT>(Qs, Ks, ty, tx, dot);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = q0 + ty * 4 + i;
+        for (int i = 0; i < RT; ++i) {
+            const int row = q0 + ty * RT + i;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int key = kb * kB + tx + 16 * c;
@@ -154,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
         }
         if (!frozen) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < RT; ++i) {
                 float mx = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
                 const float mnew = fmaxf(m[i], quad16_max(mx));
                 // a row of a windowed layer that has seen no key yet: any finite reference
@@ -173,47 +231,34 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) Ps[(ty * 4 + i) * kLd + tx + 16 * c] = s[i][c];
+            for (int c = 0; c < 4; ++c) Ps[(ty * RT + i) * kLd + tx + 16 * c] = s[i][c];
         __syncthreads();
-#pragma unroll 4
-        for (int j = 0; j < kB; ++j) {
-            float vv[NC];
-#pragma unroll
-            for (int c = 0; c < NC; ++c) vv[c] = Vs[j * LdD + tx + 16 * c];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float pij = Ps[(ty * 4 + i) * kLd + j];
-#pragma unroll
-                for (int c = 0; c < NC; ++c) acc[i][c] = fmaf(pij, vv[c], acc[i][c]);
-            }
-        }
+        tile_sums<D, RT>(Ps, Vs, ty, tx, acc);
     }
 
     E* o = (E*)p.out + base;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = q0 + ty * 4 + i;
+    for (int i = 0; i < RT; ++i) {
+        const int row = q0 + ty * RT + i;
         if (row >= T) continue;
-        const float inv = frozen ? 1.f : 1.f / l[i];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) from_f(o + (size_t)row * D + tx + 16 * c, acc[i][c] * inv);
+        Cols<D>::store(o + (size_t)row * D, acc[i], frozen ? 1.f : 1.f / l[i], tx);
         if (tx == 0) p.lse_out[(size_t)bh * T + row] = frozen ? lzr[i] : m[i] + logf(l[i]);
     }
 }
 
 // ---------------------------------------------------------------------------
-// Backward, key-block pass. Grid (ceil(T/64), B*Hkv). Program owns keys
-// k0..k0+63 of one key/value slice; loops over the query heads that share it
+// Backward, key-block pass. Grid (ceil(T / 16 RT), B*Hkv). Program owns keys
+// k0 .. k0 + 16 RT - 1 of one key/value slice; loops over the query heads that share it
 // (grouped-query layout; one head in the multi-head layer) and, for each, over
 // query blocks qb >= kb, so that the slice's dV and dK are group sums formed
 // without atomics. Thread rows = keys.
 // ---------------------------------------------------------------------------
-template <typename E, int D, bool kWin>
+template <typename E, int D, bool kWin, int RT>
 __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
     extern __shared__ float sm[];
-    constexpr int LdD = D + 4, NC = D / 16, kT = tile_floats<D>();
+    constexpr int NC = D / 16, kT = tile_floats<D>(), kR = 16 * RT;
     float* Ks = sm;
     float* Vs = Ks + kT;
     float* Qs = Vs + kT;
@@ -229,17 +274,17 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
     const size_t kvbase = (size_t)bkv * T * D;
     const E* k = (const E*)p.k + kvbase;
     const E* v = (const E*)p.v + kvbase;
-    const int k0 = kb * kB;
+    const int k0 = kb * kR;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const float scale = 1.f / sqrtf((float)D);
     bool any_ordinary = false;
     for (int gi = 0; gi < G; ++gi) any_ordinary |= !head_frozen(p.mask, hk * G + gi);
 
-    if (any_ordinary) load_tile<D>(Ks, k, k0, T);
-    load_tile<D>(Vs, v, k0, T);
-    float dv[4][NC], dk[4][NC];
+    if (any_ordinary) load_tile<D, kR>(Ks, k, k0, T);
+    load_tile<D, kR>(Vs, v, k0, T);
+    float dv[RT][NC], dk[RT][NC];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int c = 0; c < NC; ++c) dv[i][c] = dk[i][c] = 0.f;
 
@@ -252,12 +297,18 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
     const E* dO = (const E*)p.dO + base;
     const float* a = p.a + (size_t)h * p.ld_prior;
     const float* r = p.r + (size_t)h * p.ld_prior;
-    const int q_end = kb + (kWin && frozen ? nqb - kb : query_blocks<kWin>(kb, nqb, p.window, p.sinks, kB));
-    for (int qb = kb; qb < q_end; ++qb) {
+    // query blocks from the one of my first key on; with a window to the one of the last query that
+    // sees my last key
+    int q_end = nqb;
+    if (kWin && !frozen && k0 >= p.sinks) {
+        const long long last = ((long long)k0 + kR - 1 + p.window - 1) / kB;
+        q_end = last < nqb - 1 ? (int)last + 1 : nqb;
+    }
+    for (int qb = k0 / kB; qb < q_end; ++qb) {
         const int q0 = qb * kB;
         __syncthreads();
-        if (!frozen) load_tile<D>(Qs, q, q0, T);
-        load_tile<D>(dOs, dO, q0, T);
+        if (!frozen) load_tile<D, kB>(Qs, q, q0, T);
+        load_tile<D, kB>(dOs, dO, q0, T);
         if (tid < kB) {
             const int qi = q0 + tid;
             if (frozen) {
@@ -268,14 +319,14 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
             }
         }
         __syncthreads();
-        float dot[4][4] = {}, dpt[4][4] = {};
+        float dot[RT][4] = {}, dpt[RT][4] = {};
         if (!frozen) {
-            tile_dots<D>(Ks, Qs, ty, tx, dot);
-            tile_dots<D>(Vs, dOs, ty, tx, dpt);
+            tile_dots<D, RT>(Ks, Qs, ty, tx, dot);
+            tile_dots<D, RT>(Vs, dOs, ty, tx, dpt);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int key = k0 + ty * 4 + i;
+        for (int i = 0; i < RT; ++i) {
+            const int key = k0 + ty * RT + i;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int qq = tx + 16 * c;
@@ -288,55 +339,38 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
                     pt = ok && in_window<kWin>(p, qi, key) ? expf(fmaf(dot[i][c], scale, -rowstat[qq])) : 0.f;
                     dst = pt * (dpt[i][c] - rowD[qq]);
                 }
-                Pt[(ty * 4 + i) * kLd + qq] = pt;
-                dSt[(ty * 4 + i) * kLd + qq] = dst;
+                Pt[(ty * RT + i) * kLd + qq] = pt;
+                dSt[(ty * RT + i) * kLd + qq] = dst;
             }
         }
         __syncthreads();
-#pragma unroll 4
-        for (int qq = 0; qq < kB; ++qq) {
-            float g[NC], x[NC];
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                g[c] = dOs[qq * LdD + tx + 16 * c];
-                x[c] = frozen ? 0.f : Qs[qq * LdD + tx + 16 * c];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float pt = Pt[(ty * 4 + i) * kLd + qq];
-                const float ds = dSt[(ty * 4 + i) * kLd + qq];
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    dv[i][c] = fmaf(pt, g[c], dv[i][c]);
-                    dk[i][c] = fmaf(ds, x[c], dk[i][c]);
-                }
-            }
-        }
+        tile_sums<D, RT>(Pt, dOs, ty, tx, dv);
+        if (!frozen) tile_sums<D, RT>(dSt, Qs, ty, tx, dk);
     }
     }
 
     E* dvp = (E*)p.dv + kvbase;
     E* dkp = (E*)p.dk + kvbase;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int key = k0 + ty * 4 + i;
+    for (int i = 0; i < RT; ++i) {
+        const int key = k0 + ty * RT + i;
         if (key >= T) continue;
+        Cols<D>::store(dvp + (size_t)key * D, dv[i], 1.f, tx);
+        if (!any_ordinary)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            from_f(dvp + (size_t)key * D + tx + 16 * c, dv[i][c]);
-            from_f(dkp + (size_t)key * D + tx + 16 * c, any_ordinary ? dk[i][c] * scale : 0.f);
-        }
+            for (int c = 0; c < NC; ++c) dk[i][c] = 0.f;
+        Cols<D>::store(dkp + (size_t)key * D, dk[i], scale, tx);
     }
 }
 
 // ---------------------------------------------------------------------------
-// Backward, query-block pass (dQ). Grid (ceil(T/64), B*H). Frozen heads
+// Backward, query-block pass (dQ). Grid (ceil(T / 16 RT), B*H). Frozen heads
 // write zeros.
 // ---------------------------------------------------------------------------
-template <typename E, int D, bool kWin>
+template <typename E, int D, bool kWin, int RT>
 __global__ void __launch_bounds__(kThreads) bwd_q_kernel(LayerArgs p) {
     extern __shared__ float sm[];
-    constexpr int LdD = D + 4, NC = D / 16, kT = tile_floats<D>();
+    constexpr int NC = D / 16, kT = tile_floats<D>(), kR = 16 * RT;
     float* Qs = sm;
     float* dOs = Qs + kT;
     float* Ks = dOs + kT;
@@ -348,10 +382,10 @@ __global__ void __launch_bounds__(kThreads) bwd_q_kernel(LayerArgs p) {
     const bool frozen = head_frozen(p.mask, h);
     const size_t base = (size_t)bh * T * D;
     E* dq = (E*)p.dq + base;
-    const int q0 = qb * kB;
+    const int q0 = qb * kR;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     if (frozen) {
-        for (int e = tid; e < kB * D; e += kThreads) {
+        for (int e = tid; e < kR * D; e += kThreads) {
             const int row = q0 + e / D;
             if (row < T) from_f(dq + (size_t)row * D + e % D, 0.f);
         }
@@ -364,113 +398,122 @@ __global__ void __launch_bounds__(kThreads) bwd_q_kernel(LayerArgs p) {
     const E* dO = (const E*)p.dO + base;
     const float scale = 1.f / sqrtf((float)D);
 
-    load_tile<D>(Qs, q, q0, T);
-    load_tile<D>(dOs, dO, q0, T);
-    float lse[4], Dr[4], acc[4][NC];
+    load_tile<D, kR>(Qs, q, q0, T);
+    load_tile<D, kR>(dOs, dO, q0, T);
+    float lse[RT], Dr[RT], acc[RT][NC];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = q0 + ty * 4 + i;
+    for (int i = 0; i < RT; ++i) {
+        const int row = q0 + ty * RT + i;
         lse[i] = row < T ? p.lse[(size_t)bh * T + row] : 0.f;
         Dr[i] = row < T ? p.delta[(size_t)bh * T + row] : 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc[i][c] = 0.f;
     }
-    const KeyBlocks<kWin> blocks(q0, qb, p.window, p.sinks, kB);
+    const KeyBlocks<kWin> blocks(q0, (q0 + kR - 1) / kB, p.window, p.sinks, kB);
     for (int jj = 0; jj < blocks.n; ++jj) {
         const int kb = blocks.id(jj);
         __syncthreads();
-        load_tile<D>(Ks, k, kb * kB, T);
-        load_tile<D>(Vs, v, kb * kB, T);
+        load_tile<D, kB>(Ks, k, kb * kB, T);
+        load_tile<D, kB>(Vs, v, kb * kB, T);
         __syncthreads();
-        float dot[4][4] = {}, dp[4][4] = {};
-        tile_dots<D>(Qs, Ks, ty, tx, dot);
-        tile_dots<D>(dOs, Vs, ty, tx, dp);
+        float dot[RT][4] = {}, dp[RT][4] = {};
+        tile_dots<D, RT>(Qs, Ks, ty, tx, dot);
+        tile_dots<D, RT>(dOs, Vs, ty, tx, dp);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = q0 + ty * 4 + i;
+        for (int i = 0; i < RT; ++i) {
+            const int row = q0 + ty * RT + i;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int key = kb * kB + tx + 16 * c;
                 const bool ok = key <= row && row < T && in_window<kWin>(p, row, key);
                 const float pij = ok ? expf(dot[i][c] * scale - lse[i]) : 0.f;
-                dSs[(ty * 4 + i) * kLd + tx + 16 * c] = pij * (dp[i][c] - Dr[i]);
+                dSs[(ty * RT + i) * kLd + tx + 16 * c] = pij * (dp[i][c] - Dr[i]);
             }
         }
         __syncthreads();
-#pragma unroll 4
-        for (int j = 0; j < kB; ++j) {
-            float kk[NC];
-#pragma unroll
-            for (int c = 0; c < NC; ++c) kk[c] = Ks[j * LdD + tx + 16 * c];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float ds = dSs[(ty * 4 + i) * kLd + j];
-#pragma unroll
-                for (int c = 0; c < NC; ++c) acc[i][c] = fmaf(ds, kk[c], acc[i][c]);
-            }
-        }
+        tile_sums<D, RT>(dSs, Ks, ty, tx, acc);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = q0 + ty * 4 + i;
-        if (row >= T) continue;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) from_f(dq + (size_t)row * D + tx + 16 * c, acc[i][c] * scale);
+    for (int i = 0; i < RT; ++i) {
+        const int row = q0 + ty * RT + i;
+        if (row < T) Cols<D>::store(dq + (size_t)row * D, acc[i], scale, tx);
     }
 }
 
-template <int D, typename K>
+template <int D, int RT, typename K>
 cudaError_t launch(K kernel, int id, int tiles, const LayerArgs& p, cudaStream_t s, int slices) {
     const int smem = tiles * tile_floats<D>() * (int)sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    dim3 grid((p.T + kB - 1) / kB, slices);
+    dim3 grid((p.T + 16 * RT - 1) / (16 * RT), slices);
     before_launch(id, s);
     kernel<<<grid, kThreads, smem, s>>>(p);
     after_launch(id, s);
     return cudaGetLastError();
 }
 
-template <typename E, int D, bool kWin>
+template <typename E, int D, bool kWin, int RT>
 cudaError_t fwd_d(const LayerArgs& p, cudaStream_t s) {
-    return launch<D>(fwd_kernel<E, D, kWin>, SAF_KERNEL_FWD, 4, p, s, p.B * p.H);
+    return launch<D, RT>(fwd_kernel<E, D, kWin, RT>, SAF_KERNEL_FWD, 4, p, s, p.B * p.H);
 }
 
-template <typename E, int D, bool kWin>
-cudaError_t bwd_d(const LayerArgs& p, cudaStream_t s) {
-    cudaError_t e = launch<D>(bwd_kv_kernel<E, D, kWin>, SAF_KERNEL_BWD_KV, 6, p, s, p.B * p.Hkv);
-    if (e != cudaSuccess) return e;
-    return launch<D>(bwd_q_kernel<E, D, kWin>, SAF_KERNEL_BWD_Q, 5, p, s, p.B * p.H);
+template <typename E, int D, bool kWin, int RT>
+cudaError_t bwd_kv_d(const LayerArgs& p, cudaStream_t s) {
+    return launch<D, RT>(bwd_kv_kernel<E, D, kWin, RT>, SAF_KERNEL_BWD_KV, 6, p, s, p.B * p.Hkv);
 }
 
-template <bool kWin>
+template <typename E, int D, bool kWin, int RT>
+cudaError_t bwd_q_d(const LayerArgs& p, cudaStream_t s) {
+    return launch<D, RT>(bwd_q_kernel<E, D, kWin, RT>, SAF_KERNEL_BWD_Q, 5, p, s, p.B * p.H);
+}
+
+template <bool kWin, int RT>
 cudaError_t fwd_f32(const LayerArgs& p, cudaStream_t s) {
     switch (p.d) {
-        case 96: return fwd_d<float, 96, kWin>(p, s);
-        case 128: return fwd_d<float, 128, kWin>(p, s);
-        default: return fwd_d<float, 64, kWin>(p, s);
+        case 96: return fwd_d<float, 96, kWin, RT>(p, s);
+        case 128: return fwd_d<float, 128, kWin, RT>(p, s);
+        default: return fwd_d<float, 64, kWin, RT>(p, s);
     }
 }
 
-template <bool kWin>
-cudaError_t bwd_f32(const LayerArgs& p, cudaStream_t s) {
+template <bool kWin, int RT>
+cudaError_t bwd_kv_f32(const LayerArgs& p, cudaStream_t s) {
     switch (p.d) {
-        case 96: return bwd_d<float, 96, kWin>(p, s);
-        case 128: return bwd_d<float, 128, kWin>(p, s);
-        default: return bwd_d<float, 64, kWin>(p, s);
+        case 96: return bwd_kv_d<float, 96, kWin, RT>(p, s);
+        case 128: return bwd_kv_d<float, 128, kWin, RT>(p, s);
+        default: return bwd_kv_d<float, 64, kWin, RT>(p, s);
     }
 }
+
+template <bool kWin, int RT>
+cudaError_t bwd_q_f32(const LayerArgs& p, cudaStream_t s) {
+    switch (p.d) {
+        case 96: return bwd_q_d<float, 96, kWin, RT>(p, s);
+        case 128: return bwd_q_d<float, 128, kWin, RT>(p, s);
+        default: return bwd_q_d<float, 64, kWin, RT>(p, s);
+    }
+}
+
+// Whether blocks of 64 rows of `slices` slices leave most SMs without a program.
+bool few_blocks(const LayerArgs& p, int slices) { return (long long)((p.T + kB - 1) / kB) * slices < kFewBlocks; }
 
 }  // namespace
 
 cudaError_t launch_simt_fwd(const LayerArgs& p, bool bf16, cudaStream_t s) {
-    if (bf16) return fwd_d<__nv_bfloat16, 64, false>(p, s);
-    return p.window > 0 ? fwd_f32<true>(p, s) : fwd_f32<false>(p, s);
+    if (bf16) return fwd_d<__nv_bfloat16, 64, false, 4>(p, s);
+    if (p.window == 0) return fwd_f32<false, 4>(p, s);
+    return few_blocks(p, p.B * p.H) ? fwd_f32<true, 1>(p, s) : fwd_f32<true, 4>(p, s);
 }
 
 cudaError_t launch_simt_bwd(const LayerArgs& p, bool bf16, cudaStream_t s) {
-    if (bf16) return bwd_d<__nv_bfloat16, 64, false>(p, s);
-    return p.window > 0 ? bwd_f32<true>(p, s) : bwd_f32<false>(p, s);
+    cudaError_t e;
+    if (bf16) e = bwd_kv_d<__nv_bfloat16, 64, false, 4>(p, s);
+    else if (p.window == 0) e = bwd_kv_f32<false, 4>(p, s);
+    else e = few_blocks(p, p.B * p.Hkv) ? bwd_kv_f32<true, 1>(p, s) : bwd_kv_f32<true, 4>(p, s);
+    if (e != cudaSuccess) return e;
+    if (bf16) return bwd_q_d<__nv_bfloat16, 64, false, 4>(p, s);
+    if (p.window == 0) return bwd_q_f32<false, 4>(p, s);
+    return few_blocks(p, p.B * p.H) ? bwd_q_f32<true, 1>(p, s) : bwd_q_f32<true, 4>(p, s);
 }
 
 }  // namespace saf
