@@ -299,6 +299,7 @@ SAF_API int saf_attn_bwd_window(const void* q, const void* k, const void* v, con
  * Out: q_out [B,H,T,d] contiguous (q_out = q only where q is contiguous; else they must
  *      not overlap), the slots of k_cache and v_cache. Rows without a token, and every
  *      other slot, stay as they were. Two tokens of one call must not share a slot.
+ * T <= 2^21 and B T <= 2^30, else SAF_EINVAL.
  * status: DEVICE uint32[2] (see above), for example a paged workspace; NULL: not recorded.
  *
  * saf_attn_paged
@@ -311,6 +312,8 @@ SAF_API int saf_attn_bwd_window(const void* q, const void* k, const void* v, con
  *      max_pages * page_size, known on the host: it sets the launch's size.
  * Out: o [B,H,T,d], lse [B,H,T] as for saf_attn_fwd; o = 0, lse = -inf for rows without
  *      a token and rows that see no key.
+ * A key or value that one row sees must be finite where another row beside it does not see
+ * it, which takes it with weight 0; what no row sees may be anything.
  * T is 1 for a decoding step, a few for drafted tokens, and may be any length for a
  * chunk of a prompt. SAF_FP32 is computed in fp32 throughout; sums and softmax statistics
  * are fp32 in both types.

@@ -208,7 +208,7 @@ extern "C" int saf_kv_append(const void* q, const void* k, const void* v, const 
     if (!head_dim_supported(d, dt)) return SAF_EUNSUPPORTED;
     if (rope_dim < 0 || rope_dim > d || rope_dim % 16 != 0 || (rope_dim > 0 && !inv_freq)) return SAF_EINVAL;
     if (interleaved != 0 && interleaved != 1) return SAF_EINVAL;
-    if (pos_base < 0 || (long long)B * T > (1ll << 30)) return SAF_EINVAL;
+    if (pos_base < 0 || T > (1 << 21) || (long long)B * T > (1ll << 30)) return SAF_EINVAL;
     if (B == 0 || T == 0) return SAF_OK;
     if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return SAF_EINVAL;
     if (num_pages < 1 || max_pages < 1) return SAF_EINVAL;
@@ -281,9 +281,8 @@ extern "C" int saf_kv_append(const void* q, const void* k, const void* v, const 
     const long long all = (long long)B * T * p.slots * p.units;
     p.per = all > 8ll * kFullGpu ? 8 : all > kFullGpu ? (int)(all / kFullGpu) : 1;
     p.groups = (p.slots + p.per - 1) / p.per;
-    const long long threads = (long long)T * p.groups * p.units;   // of a sequence
+    const long long threads = (long long)T * p.groups * p.units;   // of a sequence: at most 2^21 x 96 x 8
     const long long blocks = (threads + kThreads - 1) / kThreads;
-    if (threads > 0x7fffffffll) return SAF_EINVAL;
     const dim3 grid((unsigned)blocks, (unsigned)(B < 65535 ? B : 65535));
     cudaStream_t cs = (cudaStream_t)stream;
     before_launch(SAF_KERNEL_KV_APPEND, cs);

@@ -187,7 +187,7 @@ using namespace saf;
 
 extern "C" {
 
-int saf_version(void) { return 100; }
+int saf_version(void) { return 101; }
 
 int saf_set_trace_events(int kernel, void* start, void* stop) {
     if (kernel < SAF_KERNEL_NONE || kernel >= kNumKernelIds) return SAF_EINVAL;

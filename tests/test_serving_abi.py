@@ -121,7 +121,8 @@ def test_append_refusals(saf):
     for kw in (dict(B=-1), dict(Hkv=3), dict(H=300, Hkv=300), dict(dt=9), dict(rope=8), dict(rope=80), dict(rope=-16),
                dict(freq=None), dict(freq=inf), dict(freq=nan), dict(inter=2), dict(base=-1), dict(ps=12), dict(ps=4),
                dict(np=0), dict(mp=0), dict(v=None), dict(vc=None), dict(k=None), dict(kc=None), dict(qo=None),
-               dict(ctx=None), dict(table=None), dict(B=2 ** 20, T=2 ** 11)):
+               dict(ctx=None), dict(table=None), dict(B=2 ** 20, T=2 ** 11),
+               dict(T=2 ** 21 + 1)):
         assert _append(lib, **kw) == saf.SAF_EINVAL, kw
     assert _append(lib, d=72) == saf.SAF_EUNSUPPORTED
     odd = (ctypes.c_int64 * 9)(512, 128, 64, 256, 68, 64, 256, 128, 64)
