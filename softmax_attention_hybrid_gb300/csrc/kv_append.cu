@@ -208,7 +208,7 @@ extern "C" int saf_kv_append(const void* q, const void* k, const void* v, const 
     if (!head_dim_supported(d, dt)) return SAF_EUNSUPPORTED;
     if (rope_dim < 0 || rope_dim > d || rope_dim % 16 != 0 || (rope_dim > 0 && !inv_freq)) return SAF_EINVAL;
     if (interleaved != 0 && interleaved != 1) return SAF_EINVAL;
-    if (pos_base < 0 || T > (1 << 21) || (long long)B * T > (1ll << 30)) return SAF_EINVAL;
+    if (pos_base < 0 || pos_base > (1ll << 62) || T > (1 << 21) || (long long)B * T > (1ll << 30)) return SAF_EINVAL;
     if (B == 0 || T == 0) return SAF_OK;
     if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return SAF_EINVAL;
     if (num_pages < 1 || max_pages < 1) return SAF_EINVAL;
