@@ -45,6 +45,7 @@ struct PagedArgs {
     int tile[2];                   // keys per tile of the kernel that runs: part 0, part 1
     int rows[2];                   // rows per block of the kernel that runs: part 0, part 1
     int nrb[2];                    // row blocks of part 0 and part 1
+    int head_blocks[2];            // row blocks of each head, 0: blocks run on from head to head
     int chunks[2];                 // items along the keys: part 0, part 1
     int per_chunk[2];              // tiles of an item
     int nsplit;                    // chunks[0] + chunks[1]
@@ -90,27 +91,48 @@ __device__ __forceinline__ int paged_tokens(const PagedArgs& p, int b, int* ctx,
 
 struct PagedRow {
     int h, b, t;
+    int gi;       // member of the group
     int i;        // position, -1: the row is not there or sees nothing
     bool there;   // the row is one of the output's
     bool frozen;
 };
 
-// Row `rr` of an item's (sequence,) key/value head: the group's ordinary heads come
-// first, and in a head the sequences (part 0) and tokens in order.
-__device__ __forceinline__ PagedRow paged_row(const PagedArgs& p, const PagedItem& it, int rr) {
+// The rows of an item's block: rows first .. first + there - 1 of one (sequence,) key/value
+// head's, in which the group's ordinary heads come first, and in a head the sequences (part 0)
+// and tokens in order. Blocks run on from head to head, except where a head fills several:
+// a block's positions then lie close together, and a window leaves it few keys.
+struct PagedBlock {
+    int first, there, per_head;
+};
+__device__ __forceinline__ PagedBlock paged_block(const PagedArgs& p, const PagedItem& it) {
+    PagedBlock k;
+    const int rows = p.rows[it.part], hb = p.head_blocks[it.part];
+    k.per_head = it.part ? p.T : p.B * p.T;
+    if (hb) {
+        const int gi = it.rb / hb, at = (it.rb - gi * hb) * rows;
+        k.first = gi * k.per_head + at;
+        k.there = k.per_head - at < rows ? k.per_head - at : rows;
+    } else {
+        k.first = it.rb * rows;
+        k.there = p.G * k.per_head - k.first < rows ? p.G * k.per_head - k.first : rows;
+    }
+    return k;
+}
+
+// Row x of the block.
+__device__ __forceinline__ PagedRow paged_row(const PagedArgs& p, const PagedItem& it, const PagedBlock& k, int x) {
     PagedRow w;
-    const int per_head = it.part ? p.T : p.B * p.T;
-    const int gi = rr / per_head;
-    w.there = gi < p.G;
-    w.h = w.b = w.t = 0;
+    w.there = x < k.there;
+    w.h = w.b = w.t = w.gi = 0;
     w.i = -1;
     w.frozen = false;
     if (!w.there) return w;
-    const int rem = rr - gi * per_head;
+    w.gi = (k.first + x) / k.per_head;
+    const int rem = k.first + x - w.gi * k.per_head;
     w.b = it.part ? it.b : rem / p.T;
     w.t = it.part ? rem : rem - w.b * p.T;
-    w.h = p.gheads[it.hk * p.G + gi];
-    w.frozen = gi >= p.gord[it.hk];
+    w.h = p.gheads[it.hk * p.G + w.gi];
+    w.frozen = w.gi >= p.gord[it.hk];
     int c;
     bool bad;
     const int n = paged_tokens(p, w.b, &c, &bad);

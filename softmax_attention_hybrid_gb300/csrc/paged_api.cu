@@ -119,7 +119,7 @@ long long ceil_div(long long x, long long y) { return (x + y - 1) / y; }
 
 struct Plan {
     int tile[2], rows[2];
-    int nrb[2];
+    int nrb[2], head_blocks[2];
     long long units[2];    // (sequence, key/value head, row block) triples
     long long tiles[2];    // key tiles of one of them, at most, without a window
     long long slots;       // items that run at the same time
@@ -143,7 +143,10 @@ Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, bool bf1
         // tensor cores: copies of the rows fill the 128 of a tile (paged_tc.cu)
         x.rows[i] = !bf16 ? kSimtRows : n[i] <= 32 ? 32 : n[i] <= 64 ? 64 : 128;
         x.tile[i] = bf16 ? paged_tc_tile(d, x.rows[i]) : kSimtTile;
-        x.nrb[i] = (int)ceil_div(n[i], x.rows[i]);
+        // several blocks to a head: each head begins its own
+        const long long per_head = n[i] / G;
+        x.head_blocks[i] = per_head >= 4 * x.rows[i] ? (int)ceil_div(per_head, x.rows[i]) : 0;
+        x.nrb[i] = (int)(x.head_blocks[i] ? G * x.head_blocks[i] : ceil_div(n[i], x.rows[i]));
         x.units[i] = (long long)x.nrb[i] * Hkv * (i ? B : 1);
         x.tiles[i] = ceil_div(keys[i], x.tile[i]);
         if (x.units[i]) x.max_split += most_chunks(x, i, x.tiles[i]);
@@ -182,15 +185,18 @@ void set_items(PagedArgs& p, const Plan& x, int nfrozen) {
     long long slots = x.slots;
     for (int i = 1; i >= 0; --i) {
         p.nrb[i] = x.nrb[i];
+        p.head_blocks[i] = x.head_blocks[i];
         p.rows[i] = x.rows[i];
         p.tile[i] = x.tile[i];
         p.chunks[i] = p.per_chunk[i] = 0;
         items[i] = 0;
         if (x.units[i] == 0) continue;
         if (windowed) {
-            // a block's rows stand within T positions in part 1 and past the prefix in part 0:
-            // the tiles that hold window + T - 1 consecutive keys, and those of the sinks
-            const long long span = i ? (long long)p.window + p.T - 1 : p.window;
+            // a block's rows stand within T positions (or as many as it has rows) in part 1 and past
+            // the prefix in part 0: the tiles that hold that many keys more than the window less
+            // one, and those of the sinks
+            const long long spread = i == 0 ? 1 : x.head_blocks[1] ? x.rows[1] : p.T;
+            const long long span = p.window + spread - 1;
             const long long off = i ? p.P : 0;
             const long long sinks = p.sinks > off ? p.sinks - off : 0;
             const long long n = ceil_div(span, x.tile[i]) + 1 + ceil_div(sinks, x.tile[i]);

@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
     grid_dep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const PagedItem it = paged_item(p, blockIdx.x);
-    const int r0 = it.rb * R;
+    const PagedBlock block = paged_block(p, it);
 
     if (tid == 0) {
         sm.imin = 0x7fffffff;
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
     }
     __syncthreads();
     if (tid < R) {
-        const PagedRow w = paged_row(p, it, r0 + tid);
+        const PagedRow w = paged_row(p, it, block, tid);
         sm.pos[tid] = w.i;
         sm.head[tid] = w.h;
         sm.out[tid] = w.there ? (int)paged_out_row(p, w) : -1;

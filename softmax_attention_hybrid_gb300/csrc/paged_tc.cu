@@ -252,7 +252,7 @@ __device__ __forceinline__ void pattern_warp(const TcParams& P, const Work& w, u
 // The rows' part of an item: kCopies copies of 128 / kCopies rows; thread t holds row t mod
 // (128 / kCopies) and the keys [kCols copy, ...) of every tile.
 template <int kD, int TK, int kCopies>
-__device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, const PagedRow& row, int gi, bool lost,
+__device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, const PagedRow& row, bool lost,
                                           uint8_t* sm, Bars& bars, const int* out_row, float* sh_m, float* sh_l,
                                           uint32_t tmem, volatile int* abort) {
     using S = Smem<kD, TK>;
@@ -269,7 +269,7 @@ __device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, cons
     const float* ra = p.a + (size_t)row.h * p.ld + w.off;
     const float* rr = p.r + (size_t)row.h * p.ld;
     // my staged pattern: a of my keys, and r of my keys from the far end on (entry k - c for key c)
-    const float* pat_a = reinterpret_cast<const float*>(sm + S::pat) + (frozen ? gi - w.f0 : 0) * w.pitch(TK) + c0;
+    const float* pat_a = reinterpret_cast<const float*>(sm + S::pat) + (frozen ? row.gi - w.f0 : 0) * w.pitch(TK) + c0;
     const float* pat_r = pat_a + TK - 2 * c0 + (TK - 1) + (frozen ? row.i - w.imin : 0);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -491,8 +491,7 @@ __device__ __forceinline__ void set_up_done() {
 
 // Warps 0-3 of an item with keys.
 template <int kD, int TK, int kCopies>
-__device__ __forceinline__ void run_rows(const TcParams& P, const Work& w, const PagedRow& row, int gi, uint8_t* sm,
-                                         Shared& sh) {
+__device__ __forceinline__ void run_rows(const TcParams& P, const Work& w, const PagedRow& row, uint8_t* sm, Shared& sh) {
     using S = Smem<kD, TK>;
     const PagedArgs& p = P.a;
     const int t = threadIdx.x;
@@ -516,7 +515,7 @@ __device__ __forceinline__ void run_rows(const TcParams& P, const Work& w, const
     set_up_done();
     const bool lost = sh.lost != 0;
     if (lost && t == 0) atomicOr(p.status, kStatusPage);
-    row_warps<kD, TK, kCopies>(P, w, row, gi, lost, sm, sh.bars, sh.out_row, sh.m, sh.l, sh.tmem_base, &sh.abort_flag);
+    row_warps<kD, TK, kCopies>(P, w, row, lost, sm, sh.bars, sh.out_row, sh.m, sh.l, sh.tmem_base, &sh.abort_flag);
 }
 
 // Warps 4-7 of an item with keys.
@@ -605,8 +604,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_cons
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     Work w;
     w.it = paged_item(p, blockIdx.x);
-    const int rows = p.rows[w.it.part], r0 = w.it.rb * rows;
-    const int per_head = w.it.part ? p.T : p.B * p.T;
+    const int rows = p.rows[w.it.part];
+    const PagedBlock block = paged_block(p, w.it);
     if (t == 0) {
         sh.abort_flag = 0;
         sh.imin = 0x7fffffff;
@@ -627,11 +626,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_cons
         fence_mbar_init();
     }
     PagedRow row;
-    int gi = 0;
     if (t < 128) {
-        const int rr = r0 + (t & (rows - 1));
-        row = paged_row(p, w.it, rr);
-        gi = rr / per_head;
+        row = paged_row(p, w.it, block, t & (rows - 1));
         sh.out_row[t] = row.there ? (int)paged_out_row(p, row) : -1;
     }
     __syncthreads();
@@ -658,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_cons
     w.imax = sh.imax;
     w.any_ord = (sh.kinds & 1) != 0;
     w.off = w.it.part ? p.P : 0;
-    w.there = min(rows, p.G * per_head - r0);
+    w.there = block.there;
     w.g = paged_range(p, w.it, w.imin, w.imax, (sh.kinds & 2) != 0 || p.window == 0);
     const int per = p.per_chunk[w.it.part];
     w.e0 = min(w.it.chunk * per, w.g.n);
@@ -677,9 +673,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_cons
         }
         return;
     }
-    // the block's frozen heads: of members r0 / per_head .. of the group those from gord on
-    w.f0 = max(r0 / per_head, (int)p.gord[w.it.hk]);
-    w.nf = min(p.G - 1, (r0 + w.there - 1) / per_head) - w.f0 + 1;
+    // the block's frozen heads: of its members of the group those from gord on
+    w.f0 = max(block.first / block.per_head, (int)p.gord[w.it.hk]);
+    w.nf = (block.first + w.there - 1) / block.per_head - w.f0 + 1;
     const int tile = p.tile[w.it.part];
     w.staged = (long long)w.nf * ((long long)w.imax - w.imin + 2 * tile + 3) <= kPatFloats;
 
@@ -687,9 +683,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_cons
     if (warp < 4) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
         switch (rows) {
-            case 32: run_rows<kD, paged_tc_tile(kD, 32), 4>(P, w, row, gi, sm, sh); break;
-            case 64: run_rows<kD, paged_tc_tile(kD, 64), 2>(P, w, row, gi, sm, sh); break;
-            default: run_rows<kD, paged_tc_tile(kD, 128), 1>(P, w, row, gi, sm, sh); break;
+            case 32: run_rows<kD, paged_tc_tile(kD, 32), 4>(P, w, row, sm, sh); break;
+            case 64: run_rows<kD, paged_tc_tile(kD, 64), 2>(P, w, row, sm, sh); break;
+            default: run_rows<kD, paged_tc_tile(kD, 128), 1>(P, w, row, sm, sh); break;
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
