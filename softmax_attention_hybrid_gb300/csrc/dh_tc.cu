@@ -670,20 +670,22 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
 
 // ---------------------------------------------------------------------------
 // Backward, query-block pass: dQ of query block qb of an ordinary slice (zeros
-// for frozen slices). K and V of the next key block load while this one runs.
-// TMEM: S [0, 128) fp32, overwritten chunk by chunk with dS as bf16 pairs
-//       (chunk c at [32 c, 32 c + 16)) | dP [128, 256) | dQ [256, 384).
+// for frozen slices). The scores of the next key block are computed while the rows
+// work on this one's, and its dP before this block's dQ: the rows then find S(j + 1)
+// ready, form P while dP(j + 1) and dQ(j) run, and only their dS waits for dP.
+// K has three buffers (S(j + 1) comes before dQ(j), which reads K(j)), V two.
+// TMEM: S of even blocks [0, 128) fp32 and of odd ones [384, 512), overwritten chunk by
+//       chunk with dS as bf16 pairs (chunk c at [32 c, 32 c + 16)) | dP [128, 256) |
+//       dQ [256, 384).
 // ---------------------------------------------------------------------------
 struct QSmem {
     static constexpr int q = 0, dO = kTile;
-    static constexpr int st = 2 * kTile;                  // 2 stages: K | V
-    static constexpr int st_k = 0, st_v = kTile;
-    static constexpr int st_bytes = 2 * kTile;
-    static constexpr int total = st + 2 * st_bytes;
+    static constexpr int k = 2 * kTile, v = k + 3 * kTile;
+    static constexpr int total = v + 2 * kTile;
 };
 
 struct QBars {
-    uint64_t q_full, st_full[2], st_empty[2], sdp_full, ds_ready, tile_done, mma_idle;
+    uint64_t q_full, k_full[3], k_empty[3], v_full[2], v_empty[2], s_full[2], dp_full, ds_ready, all_done, mma_idle;
 };
 
 template <bool kWin>
@@ -716,13 +718,18 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_c
     if (threadIdx.x == 0) {
         abort_flag = 0;
         mbar_init(&bars.q_full, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.st_full[i], 1);
-            mbar_init(&bars.st_empty[i], 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&bars.k_full[i], 1);
+            mbar_init(&bars.k_empty[i], 1);
         }
-        mbar_init(&bars.sdp_full, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.v_full[i], 1);
+            mbar_init(&bars.v_empty[i], 1);
+            mbar_init(&bars.s_full[i], 1);
+        }
+        mbar_init(&bars.dp_full, 1);
         mbar_init(&bars.ds_ready, 8);
-        mbar_init(&bars.tile_done, 1);
+        mbar_init(&bars.all_done, 1);
         mbar_init(&bars.mma_idle, 1);
         fence_mbar_init();
     }
@@ -742,13 +749,19 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_c
             mbar_expect_tx(&bars.q_full, 2 * kTile);
             load_tile(sm + QSmem::q, &p.tm_q, &bars.q_full, qb * 128, bh);
             load_tile(sm + QSmem::dO, &p.tm_do, &bars.q_full, qb * 128, bh);
+            int sk = 0, pk = 1;   // K buffer, and the parity of its empty phase
             for (int j = 0; j < nblk; ++j) {
-                const int s = j & 1;
-                if (!mbar_wait(&bars.st_empty[s], ((j >> 1) & 1) ^ 1u, abort, status, kStatusTimeout)) break;
-                uint8_t* st = sm + QSmem::st + s * QSmem::st_bytes;
-                mbar_expect_tx(&bars.st_full[s], 2 * kTile);
-                load_tile(st + QSmem::st_k, &p.tm_k, &bars.st_full[s], blocks.id(j) * 128, bkv);
-                load_tile(st + QSmem::st_v, &p.tm_v, &bars.st_full[s], blocks.id(j) * 128, bkv);
+                const int sv = j & 1;
+                if (!mbar_wait(&bars.k_empty[sk], pk, abort, status, kStatusTimeout)) break;
+                mbar_expect_tx(&bars.k_full[sk], kTile);
+                load_tile(sm + QSmem::k + sk * kTile, &p.tm_k, &bars.k_full[sk], blocks.id(j) * 128, bkv);
+                if (!mbar_wait(&bars.v_empty[sv], ((j >> 1) & 1) ^ 1u, abort, status, kStatusTimeout)) break;
+                mbar_expect_tx(&bars.v_full[sv], kTile);
+                load_tile(sm + QSmem::v + sv * kTile, &p.tm_v, &bars.v_full[sv], blocks.id(j) * 128, bkv);
+                if (++sk == 3) {
+                    sk = 0;
+                    pk ^= 1;
+                }
             }
         }
     } else if (warp == 9) {
@@ -756,27 +769,50 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_c
             const uint32_t id_s = idesc_bf16(128, 128, 0, 0);   // S = Q K^T, dP = dO V^T
             const uint32_t id_n = idesc_bf16(128, 128, 0, 1);   // dQ += dS K (K MN-major)
             const uint32_t sq = smem_u32(sm + QSmem::q), sdo = smem_u32(sm + QSmem::dO);
+            const uint32_t k0 = smem_u32(sm + QSmem::k), v0 = smem_u32(sm + QSmem::v);
             bool ok = mbar_wait(&bars.q_full, 0, abort, status, kStatusTimeout);
-            for (int j = 0; j < nblk && ok; ++j) {
-                const int s = j & 1;
-                if (!(ok = mbar_wait(&bars.st_full[s], (j >> 1) & 1, abort, status, kStatusTimeout))) break;
+            int sk = 0, pk = 0;   // K buffer of the next S, and the parity of its full phase
+            // S(j) may overwrite the columns of dS(j - 2): dQ(j - 2) was issued before it
+            auto issue_s = [&](int j) -> bool {
+                if (!mbar_wait(&bars.k_full[sk], pk, abort, status, kStatusTimeout)) return false;
                 tc_fence_after();
-                const uint32_t st = smem_u32(sm + QSmem::st + s * QSmem::st_bytes);
-                const uint32_t sk = st + QSmem::st_k, sv = st + QSmem::st_v;
-                // after the previous block's dQ MMAs, which read dS from columns [0, 128)
+                const uint32_t k_ = k0 + sk * kTile, col = (j & 1) ? 384u : 0u;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma_ss(tmem, kmaj(sq, k), kmaj(sk, k), id_s, k > 0);
+                for (int k = 0; k < 8; ++k) mma_ss(tmem + col, kmaj(sq, k), kmaj(k_, k), id_s, k > 0);
+                mma_commit(&bars.s_full[j & 1]);
+                if (++sk == 3) {
+                    sk = 0;
+                    pk ^= 1;
+                }
+                return true;
+            };
+            auto issue_dp = [&](int j) -> bool {
+                const int s = j & 1;
+                if (!mbar_wait(&bars.v_full[s], (j >> 1) & 1, abort, status, kStatusTimeout)) return false;
+                tc_fence_after();
+                const uint32_t v_ = v0 + s * kTile;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma_ss(tmem + 128, kmaj(sdo, k), kmaj(sv, k), id_s, k > 0);
-                mma_commit(&bars.sdp_full);
+                for (int k = 0; k < 8; ++k) mma_ss(tmem + 128, kmaj(sdo, k), kmaj(v_, k), id_s, k > 0);
+                mma_commit(&bars.dp_full);
+                mma_commit(&bars.v_empty[s]);
+                return true;
+            };
+            ok = ok && issue_s(0) && issue_dp(0);
+            int sq_k = 0;   // K buffer of block j
+            for (int j = 0; j < nblk && ok; ++j) {
+                if (j + 1 < nblk && !(ok = issue_s(j + 1))) break;
+                // the rows have read S(j) and dP(j), and dS(j) is there
                 if (!(ok = mbar_wait(&bars.ds_ready, j & 1, abort, status, kStatusTimeout))) break;
                 tc_fence_after();
+                if (j + 1 < nblk && !(ok = issue_dp(j + 1))) break;
+                const uint32_t k_ = k0 + sq_k * kTile, col = (j & 1) ? 384u : 0u;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    mma_ts(tmem + 256, tmem + chunk_col(k, 0), mnmaj(sk, k), id_n, (j > 0 || k > 0) ? 1u : 0u);
-                mma_commit(&bars.st_empty[s]);
-                mma_commit(&bars.tile_done);
+                    mma_ts(tmem + 256, tmem + col + chunk_col(k, 0), mnmaj(k_, k), id_n, (j > 0 || k > 0) ? 1u : 0u);
+                mma_commit(&bars.k_empty[sq_k]);
+                sq_k = sq_k == 2 ? 0 : sq_k + 1;
             }
+            mma_commit(&bars.all_done);
             mma_commit(&bars.mma_idle);
             mbar_wait_bounded(&bars.mma_idle, 0, kWaitLimitNs);
         }
@@ -790,37 +826,44 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_c
         const float l2 = rv[t], dd = rv[128 + t];
         bool ok = true;
         for (int j = 0; j < nblk; ++j) {
-            if (!(ok = mbar_wait(&bars.sdp_full, j & 1, abort, status, kStatusTimeout))) break;
+            if (!(ok = mbar_wait(&bars.s_full[j & 1], (j >> 1) & 1, abort, status, kStatusTimeout))) break;
             tc_fence_after();
+            const uint32_t s_base = lane_base + ((j & 1) ? 384u : 0u) + 64 * half;
             // keys of the block before k_near are hidden by the window unless they are sinks
             const int kb = blocks.id(j);
             const int k_near = kWin ? (qb - kb) * 128 + t - p.window + 1 : 0, sink = p.sinks - kb * 128;
+            uint32_t su[64];
+            tmem_ld32(s_base, su);
+            tmem_ld32(s_base + 32, su + 32);
+            tmem_ld_wait();
+            float pr[64];
+#pragma unroll
+            for (int e = 0; e < 64; ++e) {
+                const int k0 = 64 * half + e;
+                float x = fast_exp2(__uint_as_float(su[e]) * p.scale_log2 - l2);
+                if (kb == qb && k0 > t) x = 0.f;
+                if (kWin && k0 < k_near && k0 >= sink) x = 0.f;
+                pr[e] = x;
+            }
+            if (!(ok = mbar_wait(&bars.dp_full, j & 1, abort, status, kStatusTimeout))) break;
+            tc_fence_after();
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
-                const int c4 = 2 * half + cc;   // chunk of 32 keys
-                uint32_t su[32], du[32], dk[16];
-                tmem_ld32(lane_base + 32 * c4, su);
-                tmem_ld32(lane_base + 128 + 32 * c4, du);
+                uint32_t du[32], dk[16];
+                tmem_ld32(lane_base + 128 + 64 * half + 32 * cc, du);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const int k0 = 32 * c4 + e;
-                    float p0 = fast_exp2(__uint_as_float(su[e]) * p.scale_log2 - l2);
-                    float p1 = fast_exp2(__uint_as_float(su[e + 1]) * p.scale_log2 - l2);
-                    if (kb == qb && k0 > t) p0 = 0.f;
-                    if (kb == qb && k0 + 1 > t) p1 = 0.f;
-                    if (kWin && k0 < k_near && k0 >= sink) p0 = 0.f;
-                    if (kWin && k0 + 1 < k_near && k0 + 1 >= sink) p1 = 0.f;
-                    dk[e >> 1] = pack_bf16(p0 * (__uint_as_float(du[e]) - dd), p1 * (__uint_as_float(du[e + 1]) - dd));
-                }
-                tmem_st16(lane_base + 32 * c4, dk);   // chunk c4's own columns, already read
+                for (int e = 0; e < 32; e += 2)
+                    dk[e >> 1] = pack_bf16(pr[32 * cc + e] * (__uint_as_float(du[e]) - dd),
+                                           pr[32 * cc + e + 1] * (__uint_as_float(du[e + 1]) - dd));
+                tmem_st16(s_base + 32 * cc, dk);   // the chunk's own columns, already read
             }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.ds_ready);
         }
-        if (ok && mbar_wait_warp(&bars.tile_done, (nblk - 1) & 1, abort, status, kStatusTimeout)) {
+        if (ok && mbar_wait_warp(&bars.all_done, 0, abort, status, kStatusTimeout)) {
             tc_fence_after();
             const int c0 = 64 * half, n = min(64, p.d - c0);
             const int row0 = row - lane;
