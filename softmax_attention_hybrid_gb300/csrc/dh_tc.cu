@@ -43,16 +43,18 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
-// Descriptor of k-step k (16 columns of d) of a K-major [128 x 128] tile.
-__device__ __forceinline__ uint64_t kmaj(uint32_t tile, int k) {
-    return sdesc_sw128(tile + (uint32_t)(k >> 2) * kAtom + (uint32_t)(k & 3) * 32, 16, 1024);
+// Descriptors of a [128 x 128] tile, formed once per tile, and of its k-steps, which add a
+// constant: an MMA then takes a few instructions of the issuing thread and not twenty.
+// K-major: k-step k is 16 columns of d.
+__device__ __forceinline__ uint64_t kmaj_tile(uint32_t tile) { return sdesc_sw128(tile, 16, 1024); }
+__device__ __forceinline__ uint64_t kmaj(uint64_t tile, int k) {
+    return sdesc_advance(tile, (uint32_t)(k >> 2) * kAtom + (uint32_t)(k & 3) * 32);
 }
-// Descriptor of k-step k (16 rows) of a tile read MN-major (d as the N dimension):
-// the leading-dimension offset steps from the first 64 columns of d (atom 0) to the
-// next (atom 1), so one N = 128 MMA covers the whole padded head dimension.
-__device__ __forceinline__ uint64_t mnmaj(uint32_t tile, int k) {
-    return sdesc_sw128(tile + (uint32_t)k * 2048, kAtom, 1024);
-}
+// Read MN-major (d as the N dimension), k-step k is 16 rows: the leading-dimension offset steps
+// from the first 64 columns of d (atom 0) to the next (atom 1), so one N = 128 MMA covers the
+// whole padded head dimension.
+__device__ __forceinline__ uint64_t mnmaj_tile(uint32_t tile) { return sdesc_sw128(tile, kAtom, 1024); }
+__device__ __forceinline__ uint64_t mnmaj(uint64_t tile, int k) { return sdesc_advance(tile, (uint32_t)k * 2048); }
 
 // Load a [128 x 128] tile (two atoms) of tensor map `map` at row y of slice z.
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int y, int z) {
@@ -217,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
             const uint32_t id_s = idesc_bf16(128, 128, 0, 0);   // S = Q K^T
             const uint32_t id_o = idesc_bf16(128, 128, 0, 1);   // O += P V, V MN-major
             const uint32_t d_s = tmem, d_o = tmem + 128;
-            const uint32_t sq = smem_u32(sm + FwdSmem::q), sk = smem_u32(sm + FwdSmem::k);
-            const uint32_t sv = smem_u32(sm + FwdSmem::v);
+            const uint64_t sq = kmaj_tile(smem_u32(sm + FwdSmem::q)), sk = kmaj_tile(smem_u32(sm + FwdSmem::k));
+            const uint64_t sv = mnmaj_tile(smem_u32(sm + FwdSmem::v));
             bool ok = true;
             auto issue_s = [&](int j) -> bool {
                 if (!mbar_wait(&bars.k_full, j & 1, abort, status, kStatusTimeout)) return false;
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
         if (lane == 0) {
             const uint32_t id_s = idesc_bf16(128, 128, 0, 0);   // S^T = K Q^T, dP^T = V dO^T
             const uint32_t id_n = idesc_bf16(128, 128, 0, 1);   // dV += P^T dO, dK += dS^T Q (B MN-major)
-            const uint32_t sk = smem_u32(sm + KvSmem::k), sv = smem_u32(sm + KvSmem::v);
+            const uint64_t sk = kmaj_tile(smem_u32(sm + KvSmem::k)), sv = kmaj_tile(smem_u32(sm + KvSmem::v));
             bool ok = mbar_wait(&bars.kv_full, 0, abort, status, kStatusTimeout);
             auto tiles = [&](auto kinds) {
                 constexpr int M = decltype(kinds)::value;
@@ -515,7 +517,8 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                     if (!(ok = mbar_wait(&bars.st_full[s], (i >> 1) & 1, abort, status, kStatusTimeout))) break;
                     tc_fence_after();
                     const uint32_t st = smem_u32(sm + KvSmem::st + s * KvSmem::st_bytes);
-                    const uint32_t sq = st + KvSmem::st_q, sdo = st + KvSmem::st_do;
+                    const uint64_t sq = kmaj_tile(st + KvSmem::st_q), sdo = kmaj_tile(st + KvSmem::st_do);
+                    const uint64_t sqn = mnmaj_tile(st + KvSmem::st_q), sdon = mnmaj_tile(st + KvSmem::st_do);
                     if (!frz) {
                         // after the previous tile's dV and dK MMAs, which read columns [0, 128)
     #pragma unroll
@@ -528,11 +531,11 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                     tc_fence_after();
     #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_ts(tmem + 256, tmem + chunk_col(k, 0), mnmaj(sdo, k), id_n, (i > 0 || k > 0) ? 1u : 0u);
+                        mma_ts(tmem + 256, tmem + chunk_col(k, 0), mnmaj(sdon, k), id_n, (i > 0 || k > 0) ? 1u : 0u);
                     if (!frz) {
     #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            mma_ts(tmem + 384, tmem + chunk_col(k, 1), mnmaj(sq, k), id_n,
+                            mma_ts(tmem + 384, tmem + chunk_col(k, 1), mnmaj(sqn, k), id_n,
                                    (nord > 0 || k > 0) ? 1u : 0u);
                         ++nord;
                     }
@@ -768,15 +771,17 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_c
         if (lane == 0) {
             const uint32_t id_s = idesc_bf16(128, 128, 0, 0);   // S = Q K^T, dP = dO V^T
             const uint32_t id_n = idesc_bf16(128, 128, 0, 1);   // dQ += dS K (K MN-major)
-            const uint32_t sq = smem_u32(sm + QSmem::q), sdo = smem_u32(sm + QSmem::dO);
-            const uint32_t k0 = smem_u32(sm + QSmem::k), v0 = smem_u32(sm + QSmem::v);
+            const uint64_t sq = kmaj_tile(smem_u32(sm + QSmem::q)), sdo = kmaj_tile(smem_u32(sm + QSmem::dO));
+            const uint64_t k0 = kmaj_tile(smem_u32(sm + QSmem::k)), v0 = kmaj_tile(smem_u32(sm + QSmem::v));
+            const uint64_t kn0 = mnmaj_tile(smem_u32(sm + QSmem::k));
             bool ok = mbar_wait(&bars.q_full, 0, abort, status, kStatusTimeout);
             int sk = 0, pk = 0;   // K buffer of the next S, and the parity of its full phase
             // S(j) may overwrite the columns of dS(j - 2): dQ(j - 2) was issued before it
             auto issue_s = [&](int j) -> bool {
                 if (!mbar_wait(&bars.k_full[sk], pk, abort, status, kStatusTimeout)) return false;
                 tc_fence_after();
-                const uint32_t k_ = k0 + sk * kTile, col = (j & 1) ? 384u : 0u;
+                const uint64_t k_ = sdesc_advance(k0, sk * kTile);
+                const uint32_t col = (j & 1) ? 384u : 0u;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) mma_ss(tmem + col, kmaj(sq, k), kmaj(k_, k), id_s, k > 0);
                 mma_commit(&bars.s_full[j & 1]);
@@ -790,7 +795,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_c
                 const int s = j & 1;
                 if (!mbar_wait(&bars.v_full[s], (j >> 1) & 1, abort, status, kStatusTimeout)) return false;
                 tc_fence_after();
-                const uint32_t v_ = v0 + s * kTile;
+                const uint64_t v_ = sdesc_advance(v0, s * kTile);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) mma_ss(tmem + 128, kmaj(sdo, k), kmaj(v_, k), id_s, k > 0);
                 mma_commit(&bars.dp_full);
@@ -805,7 +810,8 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_c
                 if (!(ok = mbar_wait(&bars.ds_ready, j & 1, abort, status, kStatusTimeout))) break;
                 tc_fence_after();
                 if (j + 1 < nblk && !(ok = issue_dp(j + 1))) break;
-                const uint32_t k_ = k0 + sq_k * kTile, col = (j & 1) ? 384u : 0u;
+                const uint64_t k_ = sdesc_advance(kn0, sq_k * kTile);
+                const uint32_t col = (j & 1) ? 384u : 0u;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     mma_ts(tmem + 256, tmem + col + chunk_col(k, 0), mnmaj(k_, k), id_n, (j > 0 || k > 0) ? 1u : 0u);
