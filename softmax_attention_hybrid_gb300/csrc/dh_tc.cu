@@ -402,11 +402,16 @@ __device__ __forceinline__ uint32_t chunk_col(int k, int second) {
 // Backward, key-block pass: dV, dK of key block kb of key/value slice bkv. The
 // tiles run over the G query heads that share the slice (one head in the
 // multi-head layer) and, for each, the query blocks kb .. nqb - 1; dV sums every
-// head's share, dK the ordinary heads' (zeros when the group has none). Q, dO and
-// the row vectors of the next query tile load while this one runs (two stages).
-// TMEM: S^T [0, 128) fp32, overwritten chunk by chunk with P^T and dS^T as bf16
-//       pairs (chunk c: P^T at [32 c, +16), dS^T at [32 c + 16, +16)) |
-//       dP^T [128, 256) | dV [256, 384) | dK [384, 512).
+// head's share, dK the ordinary heads' (zeros when the group has none).
+// TMEM: two regions of 128 columns, [0, 128) and [128, 256), which even and odd tiles take in
+//       turn: S^T(i) fp32 is in region i % 2, overwritten chunk by chunk with P^T and dS^T as bf16
+//       pairs (chunk c: P^T at [32 c, +16), dS^T at [32 c + 16, +16)), dP^T(i) in the other |
+//       dV [256, 384) | dK [384, 512).
+// So the MMAs and the rows work on two tiles at once: S^T(i + 1) overwrites dP^T(i) as soon as the
+// rows have read it, then come dK(i) and, over the region that it has read, dP^T(i + 1), while the
+// rows form P^T(i + 1); dV(i + 1) runs while they form dS^T(i + 1). MMAs run in the order in which
+// they were issued, so a region is not overwritten before the products that read it.
+// The two stages hand Q (with the row vectors) and dO back apart: dO(i) is free after dV(i).
 // ---------------------------------------------------------------------------
 struct KvSmem {
     static constexpr int k = 0, v = kTile;
@@ -417,7 +422,10 @@ struct KvSmem {
 };
 
 struct KvBars {
-    uint64_t kv_full, st_full[2], st_empty[2], sdp_full, pds_ready, tile_done, mma_idle;
+    uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2];   // q: with the row vectors
+    // p: P^T or W^T. Two, for the tiles in turn: with frozen heads a row warp may be a tile
+    // ahead of another, and its arrival must not count for the other's tile.
+    uint64_t s_full, dp_full, p_ready[2], ds_ready, mma_idle;
 };
 
 template <bool kWin>
@@ -453,12 +461,15 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
         abort_flag = 0;
         mbar_init(&bars.kv_full, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.st_full[i], 1);
-            mbar_init(&bars.st_empty[i], 1);
+            mbar_init(&bars.q_full[i], 1);
+            mbar_init(&bars.q_empty[i], 1);
+            mbar_init(&bars.do_full[i], 1);
+            mbar_init(&bars.do_empty[i], 1);
+            mbar_init(&bars.p_ready[i], 8);
         }
-        mbar_init(&bars.sdp_full, 1);
-        mbar_init(&bars.pds_ready, 8);
-        mbar_init(&bars.tile_done, 1);
+        mbar_init(&bars.s_full, 1);
+        mbar_init(&bars.dp_full, 1);
+        mbar_init(&bars.ds_ready, 8);
         mbar_init(&bars.mma_idle, 1);
         fence_mbar_init();
     }
@@ -486,16 +497,19 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                     qi = 0;
                     ++gi;
                 }
-                if (!mbar_wait(&bars.st_empty[s], ((i >> 1) & 1) ^ 1u, abort, status, kStatusTimeout)) break;
+                const uint32_t parity = ((i >> 1) & 1) ^ 1u;
+                if (!mbar_wait(&bars.do_empty[s], parity, abort, status, kStatusTimeout)) break;
                 uint8_t* st = sm + KvSmem::st + s * KvSmem::st_bytes;
                 float* vec = reinterpret_cast<float*>(st + KvSmem::st_vec);
-                mbar_expect_tx(&bars.st_full[s], (frz ? kTile : 2 * kTile) + 1024 + (frz ? 1024 : 0));
-                if (!frz) load_tile(st + KvSmem::st_q, &p.tm_q, &bars.st_full[s], qb * 128, bh);
-                load_tile(st + KvSmem::st_do, &p.tm_do, &bars.st_full[s], qb * 128, bh);
-                bulk_load(vec, p.rowvec + ((size_t)bh * p.nqb + qb) * 256, 1024, &bars.st_full[s]);
+                mbar_expect_tx(&bars.do_full[s], kTile);
+                load_tile(st + KvSmem::st_do, &p.tm_do, &bars.do_full[s], qb * 128, bh);
+                if (!mbar_wait(&bars.q_empty[s], parity, abort, status, kStatusTimeout)) break;
+                mbar_expect_tx(&bars.q_full[s], 1024 + (frz ? 1024 : kTile));
+                if (!frz) load_tile(st + KvSmem::st_q, &p.tm_q, &bars.q_full[s], qb * 128, bh);
+                bulk_load(vec, p.rowvec + ((size_t)bh * p.nqb + qb) * 256, 1024, &bars.q_full[s]);
                 if (frz)
                     bulk_load(vec + 256, p.r2p + (size_t)h * (p.Tp + 256) + (size_t)(qb - kb) * 128, 1024,
-                              &bars.st_full[s]);
+                              &bars.q_full[s]);
             }
         }
     } else if (warp == 9) {
@@ -504,43 +518,65 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
             const uint32_t id_n = idesc_bf16(128, 128, 0, 1);   // dV += P^T dO, dK += dS^T Q (B MN-major)
             const uint64_t sk = kmaj_tile(smem_u32(sm + KvSmem::k)), sv = kmaj_tile(smem_u32(sm + KvSmem::v));
             bool ok = mbar_wait(&bars.kv_full, 0, abort, status, kStatusTimeout);
+            auto stage = [&](int i) { return smem_u32(sm + KvSmem::st + (i & 1) * KvSmem::st_bytes); };
+            auto issue_s = [&](int i) -> bool {
+                if (!mbar_wait(&bars.q_full[i & 1], (i >> 1) & 1, abort, status, kStatusTimeout)) return false;
+                tc_fence_after();
+                const uint64_t sq = kmaj_tile(stage(i) + KvSmem::st_q);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mma_ss(tmem + 128 * (i & 1), kmaj(sk, k), kmaj(sq, k), id_s, k > 0);
+                mma_commit(&bars.s_full);
+                return true;
+            };
+            auto issue_dp = [&](int i) -> bool {
+                if (!mbar_wait(&bars.do_full[i & 1], (i >> 1) & 1, abort, status, kStatusTimeout)) return false;
+                tc_fence_after();
+                const uint64_t sdo = kmaj_tile(stage(i) + KvSmem::st_do);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mma_ss(tmem + 128 * (~i & 1), kmaj(sv, k), kmaj(sdo, k), id_s, k > 0);
+                mma_commit(&bars.dp_full);
+                return true;
+            };
             auto tiles = [&](auto kinds) {
                 constexpr int M = decltype(kinds)::value;
                 int nord = 0;   // ordinary tiles so far (the first one starts dK)
+                bool frz = M == 0 ? false : M == 1 ? true : head_frozen(p.mask, h0);
+                if (!frz) ok = ok && issue_s(0) && issue_dp(0);
                 for (int i = 0, gi = 0, qi = 0; i < ntiles && ok; ++i) {
                     const int s = i & 1;
-                    const bool frz = M == 0 ? false : M == 1 ? true : head_frozen(p.mask, h0 + gi);
                     if (++qi == (kWin && !frz ? nq_ord : nq_frz)) {
                         qi = 0;
                         ++gi;
                     }
-                    if (!(ok = mbar_wait(&bars.st_full[s], (i >> 1) & 1, abort, status, kStatusTimeout))) break;
-                    tc_fence_after();
-                    const uint32_t st = smem_u32(sm + KvSmem::st + s * KvSmem::st_bytes);
-                    const uint64_t sq = kmaj_tile(st + KvSmem::st_q), sdo = kmaj_tile(st + KvSmem::st_do);
-                    const uint64_t sqn = mnmaj_tile(st + KvSmem::st_q), sdon = mnmaj_tile(st + KvSmem::st_do);
-                    if (!frz) {
-                        // after the previous tile's dV and dK MMAs, which read columns [0, 128)
-    #pragma unroll
-                        for (int k = 0; k < 8; ++k) mma_ss(tmem, kmaj(sk, k), kmaj(sq, k), id_s, k > 0);
-    #pragma unroll
-                        for (int k = 0; k < 8; ++k) mma_ss(tmem + 128, kmaj(sv, k), kmaj(sdo, k), id_s, k > 0);
-                        mma_commit(&bars.sdp_full);
+                    // tile i + 1 is an ordinary one
+                    const bool next = M != 1 && i + 1 < ntiles && (M == 0 || !head_frozen(p.mask, h0 + gi));
+                    if (frz) {
+                        if (next && !(ok = issue_s(i + 1))) break;
+                        if (!(ok = mbar_wait(&bars.do_full[s], (i >> 1) & 1, abort, status, kStatusTimeout))) break;
                     }
-                    if (!(ok = mbar_wait(&bars.pds_ready, i & 1, abort, status, kStatusTimeout))) break;
+                    if (!(ok = mbar_wait(&bars.p_ready[s], (i >> 1) & 1, abort, status, kStatusTimeout))) break;
                     tc_fence_after();
-    #pragma unroll
+                    const uint64_t sdon = mnmaj_tile(stage(i) + KvSmem::st_do);
+                    const uint32_t region = tmem + 128 * s;
+#pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_ts(tmem + 256, tmem + chunk_col(k, 0), mnmaj(sdon, k), id_n, (i > 0 || k > 0) ? 1u : 0u);
+                        mma_ts(tmem + 256, region + chunk_col(k, 0), mnmaj(sdon, k), id_n, (i > 0 || k > 0) ? 1u : 0u);
+                    mma_commit(&bars.do_empty[s]);
                     if (!frz) {
-    #pragma unroll
+                        // the rows have read dP^T, and dS^T is there
+                        if (!(ok = mbar_wait(&bars.ds_ready, nord & 1, abort, status, kStatusTimeout))) break;
+                        tc_fence_after();
+                        if (next && !(ok = issue_s(i + 1))) break;
+                        const uint64_t sqn = mnmaj_tile(stage(i) + KvSmem::st_q);
+#pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            mma_ts(tmem + 384, tmem + chunk_col(k, 1), mnmaj(sqn, k), id_n,
+                            mma_ts(tmem + 384, region + chunk_col(k, 1), mnmaj(sqn, k), id_n,
                                    (nord > 0 || k > 0) ? 1u : 0u);
                         ++nord;
                     }
-                    mma_commit(&bars.st_empty[s]);
-                    mma_commit(&bars.tile_done);
+                    mma_commit(&bars.q_empty[s]);
+                    if (next && !(ok = issue_dp(i + 1))) break;
+                    if (M == 2) frz = !next;
                 }
             };
             if (!any_frz)
@@ -575,22 +611,22 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                     ++gi;
                 }
                 const int s = i & 1;
-                if (!(ok = mbar_wait(&bars.st_full[s], (i >> 1) & 1, abort, status, kStatusTimeout))) break;
+                const uint32_t region = lane_base + 128 * s;
+                if (!(ok = mbar_wait(&bars.q_full[s], (i >> 1) & 1, abort, status, kStatusTimeout))) break;
                 const float* vec =
                     reinterpret_cast<const float*>(sm + KvSmem::st + s * KvSmem::st_bytes + KvSmem::st_vec);
                 if (!frz) {
-                    // S^T, dP^T of this tile; their commit also means the previous tile's MMAs are done
-                    if (!(ok = mbar_wait(&bars.sdp_full, nord & 1, abort, status, kStatusTimeout))) break;
-                    ++nord;
+                    // the commit of S^T also means that the MMAs of tile i - 2 are done
+                    if (!(ok = mbar_wait(&bars.s_full, nord & 1, abort, status, kStatusTimeout))) break;
                     tc_fence_after();
-    #pragma unroll
+                    float pr[64];
+#pragma unroll
                     for (int cc = 0; cc < 2; ++cc) {
                         const int c4 = 2 * half + cc;   // chunk of 32 queries
-                        uint32_t su[32], du[32], pk[16], dk[16];
-                        tmem_ld32(lane_base + 32 * c4, su);
-                        tmem_ld32(lane_base + 128 + 32 * c4, du);
+                        uint32_t su[32], pk[16];
+                        tmem_ld32(region + 32 * c4, su);
                         tmem_ld_wait();
-    #pragma unroll
+#pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             const int q0 = 32 * c4 + e;
                             float p0 = fast_exp2(__uint_as_float(su[e]) * p.scale_log2 - vec[q0]);
@@ -599,20 +635,43 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                             if (diag && q0 + 1 < t) p1 = 0.f;
                             if (kWin && q0 >= q_far) p0 = 0.f;
                             if (kWin && q0 + 1 >= q_far) p1 = 0.f;
-                            const float d0 = p0 * (__uint_as_float(du[e]) - vec[128 + q0]);
-                            const float d1 = p1 * (__uint_as_float(du[e + 1]) - vec[128 + q0 + 1]);
+                            pr[32 * cc + e] = p0;
+                            pr[32 * cc + e + 1] = p1;
                             pk[e >> 1] = pack_bf16(p0, p1);
-                            dk[e >> 1] = pack_bf16(d0, d1);
                         }
-                        // chunk c4's own columns, already read
-                        tmem_st16(lane_base + 32 * c4, pk);
-                        tmem_st16(lane_base + 32 * c4 + 16, dk);
+                        tmem_st16(region + 32 * c4, pk);   // the chunk's own columns, already read
                     }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.p_ready[s]);
+                    if (!(ok = mbar_wait(&bars.dp_full, nord & 1, abort, status, kStatusTimeout))) break;
+                    ++nord;
+                    tc_fence_after();
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc) {
+                        const int c4 = 2 * half + cc;
+                        uint32_t du[32], dk[16];
+                        tmem_ld32(lane_base + 128 * (s ^ 1) + 32 * c4, du);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const int q0 = 32 * c4 + e;
+                            dk[e >> 1] = pack_bf16(pr[32 * cc + e] * (__uint_as_float(du[e]) - vec[128 + q0]),
+                                                   pr[32 * cc + e + 1] * (__uint_as_float(du[e + 1]) - vec[128 + q0 + 1]));
+                        }
+                        tmem_st16(region + 32 * c4 + 16, dk);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.ds_ready);
                 } else {
                     // W^T(key, q) = exp2(a2[key] + r2[q - key] - log2 Z(q)); the band holds r at
-                    // distance i 128 + c - t at entry 127 + c - t. The previous tile's dV MMA has
-                    // read its W^T before this one is written.
-                    if (i > 0 && !(ok = mbar_wait(&bars.tile_done, (i - 1) & 1, abort, status, kStatusTimeout))) break;
+                    // distance i 128 + c - t at entry 127 + c - t. The MMAs of tile i - 2 have
+                    // read the region before it is written.
+                    if (i > 1 && !(ok = mbar_wait(&bars.q_empty[s], ((i >> 1) & 1) ^ 1u, abort, status, kStatusTimeout)))
+                        break;
                     tc_fence_after();
                     const float* band = vec + 256 + 127 - t;
     #pragma unroll
@@ -625,13 +684,13 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                             pk[e >> 1] = pack_bf16(fast_exp2(a2k + band[c] - vec[c]),
                                                    fast_exp2(a2k + band[c + 1] - vec[c + 1]));
                         }
-                        tmem_st16(lane_base + 32 * c4, pk);
+                        tmem_st16(region + 32 * c4, pk);
                     }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.p_ready[s]);
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.pds_ready);
             }
         };
         if (!any_frz)
@@ -642,7 +701,8 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
             tiles(HeadKinds<2>{});
         // tcgen05.ld is warp-collective: every lane loads, only rows inside T are stored;
         // each half of the warps writes its 64 columns of dV and dK (those inside d)
-        if (ok && mbar_wait_warp(&bars.tile_done, (ntiles - 1) & 1, abort, status, kStatusTimeout)) {
+        if (ok &&
+            mbar_wait_warp(&bars.q_empty[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1, abort, status, kStatusTimeout)) {
             tc_fence_after();
             const int c0 = 64 * half, n = min(64, p.d - c0);
             const int key0 = key - lane;
