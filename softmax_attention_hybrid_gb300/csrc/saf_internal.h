@@ -40,7 +40,8 @@ __host__ __device__ inline bool head_frozen(const HeadMask& m, int h) {
 // have completed and their memory is visible (at once when the kernel was
 // launched without the attribute), so a kernel that was scheduled early never
 // touches data that is still being written. Every CTA runs it, early exits
-// included, so that a kernel's completion implies its predecessors'.
+// included, so that a kernel's completion implies its predecessors' (dh_bwd_q_kernel does
+// with one CTA, and says why).
 // grid_dep_launch() then lets the next kernel on the stream be scheduled while
 // this one runs; that kernel's own grid_dep_wait() holds it back until this
 // one has completed.
