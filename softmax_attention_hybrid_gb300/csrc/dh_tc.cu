@@ -257,37 +257,40 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
             if (!frz) {
                 if (!(ok = mbar_wait(&bars.s_full, j & 1, abort, status, kStatusTimeout))) break;
                 tc_fence_after();
-                float sv[128];
+                uint32_t sr[128];   // this row of S, raw scores; hidden keys -inf
 #pragma unroll
-                for (int c4 = 0; c4 < 4; ++c4) {
-                    uint32_t u[32];
-                    tmem_ld32(lane_base + 32 * c4, u);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) sv[32 * c4 + e] = __uint_as_float(u[e]) * p.scale_log2;
-                }
+                for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(lane_base + 32 * c4, sr + 32 * c4);
+                tmem_ld_wait();
                 const int kb = blocks.id(j);
                 if (kWin && window_cuts(qb, kb, p.window, 128)) {
                     // hidden past the diagonal, and before the window unless a sink
                     const int hi = (qb - kb) * 128 + t, lo = hi - p.window + 1, sink = p.sinks - kb * 128;
 #pragma unroll
                     for (int c = 0; c < 128; ++c)
-                        if (c > hi || (c < lo && c >= sink)) sv[c] = -INFINITY;
+                        if (c > hi || (c < lo && c >= sink)) sr[c] = __float_as_uint(-INFINITY);
                 } else if (kb == qb) {
 #pragma unroll
                     for (int c = 0; c < 128; ++c)
-                        if (c > t) sv[c] = -INFINITY;
+                        if (c > t) sr[c] = __float_as_uint(-INFINITY);
                 }
-                float mx = m;
+                // row max of the raw scores (the scale is positive): two chains of 3-input max
+                float ma = -INFINITY, mb = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 128; ++c) mx = fmaxf(mx, sv[c]);
+                for (int c = 0; c < 128; c += 4) {
+                    ma = fmax3(ma, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+                    mb = fmax3(mb, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
+                }
+                const float mx = fmaxf(m, fmaxf(ma, mb) * p.scale_log2);
                 // a row of a windowed layer that has seen no key yet: weights 2^-inf = 0 with any
                 // finite reference
                 const float m_ref = kWin && mx == -INFINITY ? 0.f : mx;
+                const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), m2 = make_float2(m_ref, m_ref);
                 float sum = 0.f;
 #pragma unroll
                 for (int c = 0; c < 128; c += 2) {
-                    const float e0 = fast_exp2(sv[c] - m_ref), e1 = fast_exp2(sv[c + 1] - m_ref);
+                    const float2 x = fsub2(
+                        fmul2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc2), m2);
+                    const float e0 = fast_exp2(x.x), e1 = fast_exp2(x.y);
                     sum += e0 + e1;
                     pk[c >> 1] = pack_bf16(e0, e1);
                 }
