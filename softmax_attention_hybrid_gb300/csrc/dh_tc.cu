@@ -102,7 +102,7 @@ struct DhParams {
     const float* lz;       // [H, T]: log Z of frozen heads
     const float* a2p;      // [H, Tp]: a * log2(e), -inf padded
     const float* r2p;      // [H, Tp + 256]: r * log2(e) shifted by 127, -inf padded
-    float* rowvec;         // [B, H, nqb, 256]: lse * log2(e) | D per query block
+    float* rowvec;         // [B, H, nqb, 256]: -lse * log2(e) | D per query block
     uint32_t* status;
     int B, H, T, d, Tp, nqb;
     int Hkv, G;            // key/value heads; query head h reads key/value head h / G
@@ -284,12 +284,12 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
                 // a row of a windowed layer that has seen no key yet: weights 2^-inf = 0 with any
                 // finite reference
                 const float m_ref = kWin && mx == -INFINITY ? 0.f : mx;
-                const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), m2 = make_float2(m_ref, m_ref);
+                const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-m_ref, -m_ref);
                 float sum = 0.f;
 #pragma unroll
                 for (int c = 0; c < 128; c += 2) {
-                    const float2 x = fsub2(
-                        fmul2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc2), m2);
+                    const float2 x =
+                        ffma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc2, nm2);
                     const float e0 = fast_exp2(x.x), e1 = fast_exp2(x.y);
                     sum += e0 + e1;
                     pk[c >> 1] = pack_bf16(e0, e1);
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------------------
-// Backward prep: rowvec[bh, qb, 0..127] = lse * log2(e) (+inf past T),
+// Backward prep: rowvec[bh, qb, 0..127] = -lse * log2(e) (-inf past T),
 // rowvec[bh, qb, 128..255] = D = sum_c dO_c O_c (0 past T, and for frozen heads,
 // which do not use it). One thread per row, grid (Tp / 128, B H).
 // ---------------------------------------------------------------------------
@@ -368,10 +368,10 @@ __global__ void __launch_bounds__(128) dh_rowvec_kernel(const __grid_constant__ 
     grid_dep_launch();
     const int bh = blockIdx.y, qb = blockIdx.x;
     const int i = qb * 128 + threadIdx.x;
-    float l2 = INFINITY, dd = 0.f;
+    float nl2 = -INFINITY, dd = 0.f;
     if (i < p.T) {
         const size_t row = (size_t)bh * p.T + i;
-        l2 = p.lse_in[row] * kLog2e;
+        nl2 = -(p.lse_in[row] * kLog2e);
         if (!head_frozen(p.mask, bh % p.H)) {
             const uint4* po = reinterpret_cast<const uint4*>(p.o_in + row * p.d);
             const uint4* pd = reinterpret_cast<const uint4*>(p.dO + row * p.d);
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(128) dh_rowvec_kernel(const __grid_constant__ 
         }
     }
     float* v = p.rowvec + ((size_t)bh * p.nqb + qb) * 256;
-    v[threadIdx.x] = l2;
+    v[threadIdx.x] = nl2;
     v[128 + threadIdx.x] = dd;
 }
 
@@ -415,7 +415,7 @@ __device__ __forceinline__ uint32_t chunk_col(int k, int second) {
 // ---------------------------------------------------------------------------
 struct KvSmem {
     static constexpr int k = 0, v = kTile;
-    static constexpr int st = 2 * kTile;                  // 2 stages: Q | dO | lse2 [128] | D [128] | r2 band [256]
+    static constexpr int st = 2 * kTile;                  // 2 stages: Q | dO | -lse2 [128] | D [128] | r2 band [256]
     static constexpr int st_q = 0, st_do = kTile, st_vec = 2 * kTile;
     static constexpr int st_bytes = 2 * kTile + 2048;
     static constexpr int total = st + 2 * st_bytes;
@@ -596,12 +596,15 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
             constexpr int M = decltype(kinds)::value;
             int nord = 0;     // ordinary tiles so far: phases of sdp_full
             float a2k = 0.f;  // a * log2(e) of my key for the current query head (frozen heads)
+            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
             for (int i = 0, gi = 0, qi = 0; i < ntiles; ++i) {
                 const bool diag = qi == 0;   // the query head's first tile: query block kb
                 const int h = h0 + gi;
                 const bool frz = M == 0 ? false : M == 1 ? true : head_frozen(p.mask, h);
                 // queries of the tile from q_far on do not see my key through the window
                 const int q_far = !kWin || key < p.sinks ? 128 : t + p.window - qi * 128;
+                // some key of the block does not see some query of the tile through the window
+                const bool cut = kWin && p.window < (qi + 1) * 128 && kb * 128 + 127 >= p.sinks;
                 if (frz && diag) a2k = p.a2p[(size_t)h * p.Tp + key];   // in flight during the wait below
                 if (++qi == (kWin && !frz ? nq_ord : nq_frz)) {
                     qi = 0;
@@ -616,27 +619,39 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                     // the commit of S^T also means that the MMAs of tile i - 2 are done
                     if (!(ok = mbar_wait(&bars.s_full, nord & 1, abort, status, kStatusTimeout))) break;
                     tc_fence_after();
+                    // the vector's element pairs of this warp's queries
+                    const float2* nl2 = reinterpret_cast<const float2*>(vec) + 32 * half;
+                    const float2* dd2 = nl2 + 64;
+                    uint32_t su[64];
+                    tmem_ld32(region + 64 * half, su);
+                    tmem_ld32(region + 64 * half + 32, su + 32);
+                    tmem_ld_wait();
                     float pr[64];
 #pragma unroll
-                    for (int cc = 0; cc < 2; ++cc) {
-                        const int c4 = 2 * half + cc;   // chunk of 32 queries
-                        uint32_t su[32], pk[16];
-                        tmem_ld32(region + 32 * c4, su);
-                        tmem_ld_wait();
+                    for (int e = 0; e < 64; e += 2) {
+                        const float2 x = ffma2(make_float2(__uint_as_float(su[e]), __uint_as_float(su[e + 1])), sc2,
+                                               nl2[e >> 1]);
+                        pr[e] = fast_exp2(x.x);
+                        pr[e + 1] = fast_exp2(x.y);
+                    }
+                    // only the diagonal and the window's end hide anything
+                    if (diag) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const int q0 = 32 * c4 + e;
-                            float p0 = fast_exp2(__uint_as_float(su[e]) * p.scale_log2 - vec[q0]);
-                            float p1 = fast_exp2(__uint_as_float(su[e + 1]) * p.scale_log2 - vec[q0 + 1]);
-                            if (diag && q0 < t) p0 = 0.f;
-                            if (diag && q0 + 1 < t) p1 = 0.f;
-                            if (kWin && q0 >= q_far) p0 = 0.f;
-                            if (kWin && q0 + 1 >= q_far) p1 = 0.f;
-                            pr[32 * cc + e] = p0;
-                            pr[32 * cc + e + 1] = p1;
-                            pk[e >> 1] = pack_bf16(p0, p1);
-                        }
-                        tmem_st16(region + 32 * c4, pk);   // the chunk's own columns, already read
+                        for (int e = 0; e < 64; ++e)
+                            if (64 * half + e < t) pr[e] = 0.f;
+                    }
+                    if (kWin && cut) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e)
+                            if (64 * half + e >= q_far) pr[e] = 0.f;
+                    }
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc) {   // chunks of 32 queries: their own columns, already read
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            pk[e] = pack_bf16(pr[32 * cc + 2 * e], pr[32 * cc + 2 * e + 1]);
+                        tmem_st16(region + 64 * half + 32 * cc, pk);
                     }
                     tmem_st_wait();
                     tc_fence_before();
@@ -645,19 +660,21 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                     if (!(ok = mbar_wait(&bars.dp_full, nord & 1, abort, status, kStatusTimeout))) break;
                     ++nord;
                     tc_fence_after();
+                    tmem_ld32(lane_base + 128 * (s ^ 1) + 64 * half, su);
+                    tmem_ld32(lane_base + 128 * (s ^ 1) + 64 * half + 32, su + 32);
+                    tmem_ld_wait();
 #pragma unroll
                     for (int cc = 0; cc < 2; ++cc) {
-                        const int c4 = 2 * half + cc;
-                        uint32_t du[32], dk[16];
-                        tmem_ld32(lane_base + 128 * (s ^ 1) + 32 * c4, du);
-                        tmem_ld_wait();
+                        uint32_t dk[16];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const int q0 = 32 * c4 + e;
-                            dk[e >> 1] = pack_bf16(pr[32 * cc + e] * (__uint_as_float(du[e]) - vec[128 + q0]),
-                                                   pr[32 * cc + e + 1] * (__uint_as_float(du[e + 1]) - vec[128 + q0 + 1]));
+                        for (int e = 0; e < 16; ++e) {
+                            const int q = 32 * cc + 2 * e;
+                            const float2 x = fmul2(
+                                make_float2(pr[q], pr[q + 1]),
+                                fsub2(make_float2(__uint_as_float(su[q]), __uint_as_float(su[q + 1])), dd2[q >> 1]));
+                            dk[e] = pack_bf16(x.x, x.y);
                         }
-                        tmem_st16(region + 32 * c4 + 16, dk);
+                        tmem_st16(region + 64 * half + 32 * cc + 16, dk);
                     }
                     tmem_st_wait();
                     tc_fence_before();
@@ -678,8 +695,9 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
     #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             const int c = 32 * c4 + e;
-                            pk[e >> 1] = pack_bf16(fast_exp2(a2k + band[c] - vec[c]),
-                                                   fast_exp2(a2k + band[c + 1] - vec[c + 1]));
+                            const float2 x = fadd2(fadd2(make_float2(a2k, a2k), make_float2(band[c], band[c + 1])),
+                                                   *reinterpret_cast<const float2*>(vec + c));
+                            pk[e >> 1] = pack_bf16(fast_exp2(x.x), fast_exp2(x.y));
                         }
                         tmem_st16(region + 32 * c4, pk);
                     }
@@ -893,7 +911,9 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_c
         const int row = qb * 128 + t;
         const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
         const float* rv = p.rowvec + ((size_t)bh * p.nqb + qb) * 256;
-        const float l2 = rv[t], dd = rv[128 + t];
+        const float nl2 = rv[t], dd = rv[128 + t];
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+        const float2 nl22 = make_float2(nl2, nl2), dd2 = make_float2(dd, dd);
         bool ok = true;
         for (int j = 0; j < nblk; ++j) {
             if (!(ok = mbar_wait(&bars.s_full[j & 1], (j >> 1) & 1, abort, status, kStatusTimeout))) break;
@@ -908,24 +928,38 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_c
             tmem_ld_wait();
             float pr[64];
 #pragma unroll
-            for (int e = 0; e < 64; ++e) {
-                const int k0 = 64 * half + e;
-                float x = fast_exp2(__uint_as_float(su[e]) * p.scale_log2 - l2);
-                if (kb == qb && k0 > t) x = 0.f;
-                if (kWin && k0 < k_near && k0 >= sink) x = 0.f;
-                pr[e] = x;
+            for (int e = 0; e < 64; e += 2) {
+                const float2 x = ffma2(make_float2(__uint_as_float(su[e]), __uint_as_float(su[e + 1])), sc2, nl22);
+                pr[e] = fast_exp2(x.x);
+                pr[e + 1] = fast_exp2(x.y);
+            }
+            // only the diagonal and the window's beginning hide anything
+            if (kb == qb) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                    if (64 * half + e > t) pr[e] = 0.f;
+            }
+            if (kWin && window_cuts(qb, kb, p.window, 128)) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                    if (64 * half + e < k_near && 64 * half + e >= sink) pr[e] = 0.f;
             }
             if (!(ok = mbar_wait(&bars.dp_full, j & 1, abort, status, kStatusTimeout))) break;
             tc_fence_after();
+            tmem_ld32(lane_base + 128 + 64 * half, su);
+            tmem_ld32(lane_base + 128 + 64 * half + 32, su + 32);
+            tmem_ld_wait();
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
-                uint32_t du[32], dk[16];
-                tmem_ld32(lane_base + 128 + 64 * half + 32 * cc, du);
-                tmem_ld_wait();
+                uint32_t dk[16];
 #pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                    dk[e >> 1] = pack_bf16(pr[32 * cc + e] * (__uint_as_float(du[e]) - dd),
-                                           pr[32 * cc + e + 1] * (__uint_as_float(du[e + 1]) - dd));
+                for (int e = 0; e < 16; ++e) {
+                    const int k0 = 32 * cc + 2 * e;
+                    const float2 x =
+                        fmul2(make_float2(pr[k0], pr[k0 + 1]),
+                              fsub2(make_float2(__uint_as_float(su[k0]), __uint_as_float(su[k0 + 1])), dd2));
+                    dk[e] = pack_bf16(x.x, x.y);
+                }
                 tmem_st16(s_base + 32 * cc, dk);   // the chunk's own columns, already read
             }
             tmem_st_wait();
