@@ -22,6 +22,9 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "saf_internal.h"
 #include "tc_common.cuh"
 
@@ -103,6 +106,11 @@ struct DhParams {
     const float* a2p;      // [H, Tp]: a * log2(e), -inf padded
     const float* r2p;      // [H, Tp + 256]: r * log2(e) shifted by 127, -inf padded
     float* rowvec;         // [B, H, nqb, 256]: -lse * log2(e) | D per query block
+    // key-block pass, windowed: the first split_blocks key blocks are done in up to `parts` blocks
+    // of threads each, whose sums and a count of the ended ones are here (see plan_parts)
+    float* part_sums;
+    uint32_t* part_count;
+    int split_blocks, parts;
     uint32_t* status;
     int B, H, T, d, Tp, nqb;
     int Hkv, G;            // key/value heads; query head h reads key/value head h / G
@@ -118,19 +126,26 @@ struct DhParams {
 // Forward. Two CTAs share an SM (about 99 KB of shared memory and 256 TMEM
 // columns each), so that one CTA's MMAs run while the other's rows are in the
 // softmax. K and V have a buffer each: K(j + 1) loads while the rows work on
-// S(j), V(j + 1) while they work on S(j + 1).
-// TMEM: S [0, 128) fp32, P written over S[0, 64) as bf16 pairs | O [128, 256).
+// S(j), V(j + 1) while they work on S(j + 1). A frozen head, which needs no K, has
+// its odd blocks' V in the K buffer, and their W in the second half of S's columns: its
+// loads and its MMAs run beside the rows. (All heads frozen, H32/Hkv8 d128, B2 T4096:
+// 264 us with one buffer, 206 us so: a load takes about 2000 cycles, a tile of W 1500.)
+// TMEM: S [0, 128) fp32, P written over S[0, 64) as bf16 pairs (frozen: W of even
+// blocks, and [64, 128) of odd ones) | O [128, 256).
 // ---------------------------------------------------------------------------
 struct FwdSmem {
     static constexpr int q = 0;
     static constexpr int k = kTile;
     static constexpr int v = 2 * kTile;
-    static constexpr int vec = 3 * kTile;   // frozen: a2 slice [128] | r2 band [256]
-    static constexpr int total = vec + 2048;
+    static constexpr int vec = 3 * kTile;   // frozen, two: a2 slice [128] | r2 band [256]
+    static constexpr int vec_bytes = 1536;
+    static constexpr int total = vec + 2 * vec_bytes;
 };
 
 struct FwdBars {
-    uint64_t q_full, k_full, k_empty, v_full, v_empty, s_full, p_ready, o_done, mma_idle;
+    // v: frozen heads' even blocks, k: their odd ones; p_ready: two for a frozen head's blocks in
+    // turn, since its warps may be a block ahead of one another
+    uint64_t q_full, k_full, k_empty, v_full, v_empty, s_full, p_ready[2], o_done, mma_idle;
 };
 
 template <bool kWin>
@@ -168,7 +183,8 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
         mbar_init(&bars.v_full, 1);
         mbar_init(&bars.v_empty, 1);
         mbar_init(&bars.s_full, 1);
-        mbar_init(&bars.p_ready, 4);
+        mbar_init(&bars.p_ready[0], 4);
+        mbar_init(&bars.p_ready[1], 4);
         mbar_init(&bars.o_done, 1);
         mbar_init(&bars.mma_idle, 1);
         fence_mbar_init();
@@ -191,22 +207,27 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
                 mbar_expect_tx(&bars.q_full, kTile);
                 load_tile(sm + FwdSmem::q, &p.tm_q, &bars.q_full, qb * 128, bh);
             }
-            float* vec = reinterpret_cast<float*>(sm + FwdSmem::vec);
             for (int j = 0; j < nblk; ++j) {
                 // the K buffer is free once S(j - 1) has been computed, the V buffer
-                // (and the frozen rows' vectors) once P(j - 1) V has
+                // once P(j - 1) V has; a frozen head's buffers, with the vectors, once W(j - 2) V has
                 if (!frz) {
                     if (!mbar_wait(&bars.k_empty, (j & 1) ^ 1u, abort, status, kStatusTimeout)) break;
                     mbar_expect_tx(&bars.k_full, kTile);
                     load_tile(sm + FwdSmem::k, &p.tm_k, &bars.k_full, blocks.id(j) * 128, bkv);
-                }
-                if (!mbar_wait(&bars.v_empty, (j & 1) ^ 1u, abort, status, kStatusTimeout)) break;
-                mbar_expect_tx(&bars.v_full, frz ? kTile + 512 + 1024 : kTile);
-                load_tile(sm + FwdSmem::v, &p.tm_v, &bars.v_full, blocks.id(j) * 128, bkv);
-                if (frz) {   // (a frozen head visits block j as its j-th)
-                    bulk_load(vec, p.a2p + (size_t)h * p.Tp + (size_t)j * 128, 512, &bars.v_full);
-                    bulk_load(vec + 128, p.r2p + (size_t)h * (p.Tp + 256) + (size_t)(qb - j) * 128, 1024,
-                              &bars.v_full);
+                    if (!mbar_wait(&bars.v_empty, (j & 1) ^ 1u, abort, status, kStatusTimeout)) break;
+                    mbar_expect_tx(&bars.v_full, kTile);
+                    load_tile(sm + FwdSmem::v, &p.tm_v, &bars.v_full, blocks.id(j) * 128, bkv);
+                } else {   // (it visits block j as its j-th)
+                    const bool odd = j & 1;
+                    uint64_t* full = odd ? &bars.k_full : &bars.v_full;
+                    float* vec = reinterpret_cast<float*>(sm + FwdSmem::vec + odd * FwdSmem::vec_bytes);
+                    if (!mbar_wait(odd ? &bars.k_empty : &bars.v_empty, ((j >> 1) & 1) ^ 1u, abort, status,
+                                   kStatusTimeout))
+                        break;
+                    mbar_expect_tx(full, kTile + 512 + 1024);
+                    bulk_load(vec, p.a2p + (size_t)h * p.Tp + (size_t)j * 128, 512, full);
+                    bulk_load(vec + 128, p.r2p + (size_t)h * (p.Tp + 256) + (size_t)(qb - j) * 128, 1024, full);
+                    load_tile(sm + (odd ? FwdSmem::k : FwdSmem::v), &p.tm_v, full, j * 128, bkv);
                 }
             }
         }
@@ -228,17 +249,33 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
                 mma_commit(&bars.k_empty);
                 return true;
             };
-            if (!frz) ok = mbar_wait(&bars.q_full, 0, abort, status, kStatusTimeout) && issue_s(0);
-            for (int j = 0; j < nblk && ok; ++j) {
-                if (!(ok = mbar_wait(&bars.v_full, j & 1, abort, status, kStatusTimeout))) break;
-                if (!(ok = mbar_wait(&bars.p_ready, j & 1, abort, status, kStatusTimeout))) break;
-                tc_fence_after();
+            if (!frz) {
+                ok = mbar_wait(&bars.q_full, 0, abort, status, kStatusTimeout) && issue_s(0);
+                for (int j = 0; j < nblk && ok; ++j) {
+                    if (!(ok = mbar_wait(&bars.v_full, j & 1, abort, status, kStatusTimeout))) break;
+                    if (!(ok = mbar_wait(&bars.p_ready[0], j & 1, abort, status, kStatusTimeout))) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma_ts(d_o, d_s + 8 * k, mnmaj(sv, k), id_o, (j > 0 || k > 0) ? 1u : 0u);
-                mma_commit(&bars.o_done);
-                mma_commit(&bars.v_empty);
-                // S(j + 1) overwrites the columns P(j) is read from; MMAs run in issue order
-                if (!frz && j + 1 < nblk) ok = issue_s(j + 1);
+                    for (int k = 0; k < 8; ++k)
+                        mma_ts(d_o, d_s + 8 * k, mnmaj(sv, k), id_o, (j > 0 || k > 0) ? 1u : 0u);
+                    mma_commit(&bars.o_done);
+                    mma_commit(&bars.v_empty);
+                    // S(j + 1) overwrites the columns P(j) is read from; MMAs run in issue order
+                    if (j + 1 < nblk) ok = issue_s(j + 1);
+                }
+            } else {
+                const uint64_t sv1 = mnmaj_tile(smem_u32(sm + FwdSmem::k));
+                for (int j = 0; j < nblk; ++j) {
+                    const bool odd = j & 1;
+                    const uint32_t parity = (j >> 1) & 1;
+                    if (!mbar_wait(odd ? &bars.k_full : &bars.v_full, parity, abort, status, kStatusTimeout)) break;
+                    if (!mbar_wait(&bars.p_ready[odd], parity, abort, status, kStatusTimeout)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_ts(d_o, d_s + 64 * odd + 8 * k, mnmaj(odd ? sv1 : sv, k), id_o, (j > 0 || k > 0) ? 1u : 0u);
+                    mma_commit(odd ? &bars.k_empty : &bars.v_empty);
+                }
             }
             mma_commit(&bars.mma_idle);
             mbar_wait_bounded(&bars.mma_idle, 0, kWaitLimitNs);
@@ -250,10 +287,10 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
         const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
         float m = -INFINITY, l = 0.f;
         const float lz2 = (frz && row < p.T) ? p.lz[(size_t)h * p.T + row] * kLog2e : INFINITY;
-        const float* vec = reinterpret_cast<const float*>(sm + FwdSmem::vec);
         bool ok = true;
         for (int j = 0; j < nblk; ++j) {
             uint32_t pk[64];
+            uint32_t p_base = lane_base;
             if (!frz) {
                 if (!(ok = mbar_wait(&bars.s_full, j & 1, abort, status, kStatusTimeout))) break;
                 tc_fence_after();
@@ -317,27 +354,37 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
                 }
                 m = mx;
             } else {
-                if (!(ok = mbar_wait(&bars.v_full, j & 1, abort, status, kStatusTimeout))) break;
-                if (j > 0 && !(ok = mbar_wait(&bars.o_done, (j - 1) & 1, abort, status, kStatusTimeout))) break;
+                // the block's vectors, and W(j - 2) V done, which read the columns of this W
+                const bool odd = j & 1;
+                const uint32_t parity = (j >> 1) & 1;
+                if (!(ok = mbar_wait(odd ? &bars.k_full : &bars.v_full, parity, abort, status, kStatusTimeout))) break;
+                if (j > 1 &&
+                    !(ok = mbar_wait(odd ? &bars.k_empty : &bars.v_empty, parity ^ 1u, abort, status, kStatusTimeout)))
+                    break;
                 tc_fence_after();
+                p_base = lane_base + 64 * odd;
+                const float* vec = reinterpret_cast<const float*>(sm + FwdSmem::vec + odd * FwdSmem::vec_bytes);
                 // W(row, key) = exp2(a2[key] + r2[row - key] - log2 Z(row)) (Eq. 3); the band
                 // holds r at distance (qb - j) 128 + t - c at entry 127 + t - c
                 const float* band = vec + 128 + 127 + t;
+                const float2 lz22 = make_float2(lz2, lz2);
 #pragma unroll
                 for (int c = 0; c < 128; c += 2) {
-                    const float w0 = fast_exp2(vec[c] + band[-c] - lz2);
-                    const float w1 = fast_exp2(vec[c + 1] + band[-c - 1] - lz2);
-                    pk[c >> 1] = pack_bf16(w0, w1);
+                    const float2 x = fsub2(fadd2(*reinterpret_cast<const float2*>(vec + c),
+                                                 make_float2(band[-c], band[-c - 1])), lz22);
+                    pk[c >> 1] = pack_bf16(fast_exp2(x.x), fast_exp2(x.y));
                 }
             }
-            tmem_st32(lane_base, pk);
-            tmem_st32(lane_base + 32, pk + 32);
+            tmem_st32(p_base, pk);
+            tmem_st32(p_base + 32, pk + 32);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.p_ready);
+            if (lane == 0) mbar_arrive(&bars.p_ready[frz ? j & 1 : 0]);
         }
-        if (ok && mbar_wait_warp(&bars.o_done, (nblk - 1) & 1, abort, status, kStatusTimeout)) {
+        uint64_t* done = !frz ? &bars.o_done : (nblk - 1) & 1 ? &bars.k_empty : &bars.v_empty;
+        const uint32_t parity = (frz ? (nblk - 1) >> 1 : nblk - 1) & 1;
+        if (ok && mbar_wait_warp(done, parity, abort, status, kStatusTimeout)) {
             tc_fence_after();
             const float inv = frz ? 1.f : 1.f / l;
             uint32_t ov[128];
@@ -387,9 +434,14 @@ __global__ void __launch_bounds__(128) dh_rowvec_kernel(const __grid_constant__ 
         }
     }
     float* v = p.rowvec + ((size_t)bh * p.nqb + qb) * 256;
+    if (threadIdx.x == 0 && (size_t)bh * p.nqb + qb < (size_t)p.B * p.Hkv * p.split_blocks)
+        p.part_count[(size_t)bh * p.nqb + qb] = 0;
     v[threadIdx.x] = nl2;
     v[128 + threadIdx.x] = dd;
 }
+
+// Barrier of the 8 row warps of a backward block.
+__device__ __forceinline__ void row_warps_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // TMEM column of k-step k (16 rows of the contraction) of an operand written in
 // chunks of 32 rows: chunk c holds its 16 packed pairs at [32 c, 32 c + 16) and the
@@ -411,18 +463,21 @@ __device__ __forceinline__ uint32_t chunk_col(int k, int second) {
 // rows have read it, then come dK(i) and, over the region that it has read, dP^T(i + 1), while the
 // rows form P^T(i + 1); dV(i + 1) runs while they form dS^T(i + 1). MMAs run in the order in which
 // they were issued, so a region is not overwritten before the products that read it.
-// The two stages hand Q (with the row vectors) and dO back apart: dO(i) is free after dV(i).
+// The two stages hand Q and dO back apart: dO(i) is free after dV(i). The row vectors, which the
+// rows need first, are loaded two tiles earlier than Q and dO (a load takes about 2000 cycles).
 // ---------------------------------------------------------------------------
 struct KvSmem {
     static constexpr int k = 0, v = kTile;
-    static constexpr int st = 2 * kTile;                  // 2 stages: Q | dO | -lse2 [128] | D [128] | r2 band [256]
-    static constexpr int st_q = 0, st_do = kTile, st_vec = 2 * kTile;
-    static constexpr int st_bytes = 2 * kTile + 2048;
-    static constexpr int total = st + 2 * st_bytes;
+    static constexpr int st = 2 * kTile;      // 2 stages: Q | dO
+    static constexpr int st_q = 0, st_do = kTile, st_bytes = 2 * kTile;
+    static constexpr int vec = st + 2 * st_bytes;   // 4: -lse2 [128] | D [128] | r2 band [256]
+    static constexpr int vec_bytes = 2048;
+    static constexpr int total = vec + 4 * vec_bytes;
 };
 
 struct KvBars {
-    uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2];   // q: with the row vectors
+    // q_empty: the tile's MMAs are all done
+    uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], vec_full[4];
     // p: P^T or W^T. Two, for the tiles in turn: with frozen heads a row warp may be a tile
     // ahead of another, and its arrival must not count for the other's tile.
     uint64_t s_full, dp_full, p_ready[2], ds_ready, mma_idle;
@@ -434,25 +489,44 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ KvBars bars;
     __shared__ uint32_t tmem_base_sh;
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, last_flag;
     grid_dep_wait();
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // Over the whole launch the longest first: blocks of sinks, which every query sees, and early
-    // blocks, which have the most query blocks after them
-    const long long u = (long long)blockIdx.y * p.nqb + blockIdx.x;
+    // blocks, which have the most query blocks after them.
+    long long u = (long long)blockIdx.y * gridDim.x + blockIdx.x;
     const int slices = p.B * p.Hkv;
-    const int kb = (int)(u / slices);
-    const int bkv = (int)(u - (long long)kb * slices);   // key/value slice
+    const long long n_parts = kWin ? (long long)p.split_blocks * p.parts * slices : 0;
+    const bool split = kWin && u < n_parts;
+    if (!split) u -= n_parts;
+    const int level = (int)(u / slices);
+    const int bkv = (int)(u - (long long)level * slices);   // key/value slice
+    const int kb = split ? level / p.parts : (kWin ? p.split_blocks : 0) + level;
     const int b = bkv / p.Hkv, h0 = (bkv - b * p.Hkv) * p.G;   // its query heads: h0 .. h0 + G - 1
     // query tiles per query head: those that see a key of the block through a window
     const int nq_frz = p.nqb - kb, nq_ord = query_blocks<kWin>(kb, p.nqb, p.window, p.sinks, 128);
-    int ntiles = 0;
+    int ntiles = 0, gi0 = 0, qi0 = 0, gi1 = p.G;   // tiles, the first one's head and block, the heads' end
+    int part = 0, nparts = 1;
+    if (split) {   // a part of the tiles, of which every head has nq_frz
+        // (all of them where every head is frozen: the block is then like its neighbours)
+        bool all_frz = true;
+        for (int gi = 0; gi < p.G; ++gi) all_frz = all_frz && head_frozen(p.mask, h0 + gi);
+        const int total = p.G * nq_frz, each = all_frz ? total : (total + p.parts - 1) / p.parts;
+        nparts = (total + each - 1) / each;
+        part = level % p.parts;
+        if (part >= nparts) return;
+        const int first = part * each;
+        ntiles = min(each, total - first);
+        gi0 = first / nq_frz;
+        qi0 = first - gi0 * nq_frz;
+        gi1 = (first + ntiles - 1) / nq_frz + 1;
+    }
     bool any_ord = false, any_frz = false;
-    for (int gi = 0; gi < p.G; ++gi) {
+    for (int gi = gi0; gi < gi1; ++gi) {
         const bool frz = head_frozen(p.mask, h0 + gi);
         (frz ? any_frz : any_ord) = true;
-        ntiles += kWin && !frz ? nq_ord : nq_frz;
+        if (!split) ntiles += kWin && !frz ? nq_ord : nq_frz;
     }
     if (threadIdx.x == 0) {
         abort_flag = 0;
@@ -464,6 +538,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
             mbar_init(&bars.do_empty[i], 1);
             mbar_init(&bars.p_ready[i], 8);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(&bars.vec_full[i], 1);
         mbar_init(&bars.s_full, 1);
         mbar_init(&bars.dp_full, 1);
         mbar_init(&bars.ds_ready, 8);
@@ -486,27 +561,44 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
             mbar_expect_tx(&bars.kv_full, any_ord ? 2 * kTile : kTile);
             if (any_ord) load_tile(sm + KvSmem::k, &p.tm_k, &bars.kv_full, kb * 128, bkv);
             load_tile(sm + KvSmem::v, &p.tm_v, &bars.kv_full, kb * 128, bkv);
-            for (int i = 0, gi = 0, qi = 0; i < ntiles; ++i) {   // tile i: query head h0 + gi, block kb + qi
-                const int qb = kb + qi, s = i & 1;
-                const int h = h0 + gi, bh = b * p.H + h;
-                const bool frz = head_frozen(p.mask, h);
-                if (++qi == (kWin && !frz ? nq_ord : nq_frz)) {
+            // tile i: query head h0 + gi, block kb + qi
+            auto advance = [&](int& gi, int& qi) {
+                if (++qi == (kWin && !head_frozen(p.mask, h0 + gi) ? nq_ord : nq_frz)) {
                     qi = 0;
                     ++gi;
                 }
+            };
+            int vi = 0, vgi = gi0, vqi = qi0;
+            auto load_vec = [&]() {   // the vectors of the next tile
+                const int h = h0 + vgi;
+                const bool frz = head_frozen(p.mask, h);
+                uint64_t* bar = &bars.vec_full[vi & 3];
+                float* vec = reinterpret_cast<float*>(sm + KvSmem::vec + (vi & 3) * KvSmem::vec_bytes);
+                mbar_expect_tx(bar, 1024 + (frz ? 1024 : 0));
+                bulk_load(vec, p.rowvec + ((size_t)(b * p.H + h) * p.nqb + kb + vqi) * 256, 1024, bar);
+                if (frz) bulk_load(vec + 256, p.r2p + (size_t)h * (p.Tp + 256) + (size_t)vqi * 128, 1024, bar);
+                advance(vgi, vqi);
+                ++vi;
+            };
+            load_vec();
+            if (ntiles > 1) load_vec();
+            for (int i = 0, gi = gi0, qi = qi0; i < ntiles; ++i) {
+                const int s = i & 1, y = (kb + qi) * 128, bh = b * p.H + h0 + gi;
+                const bool frz = head_frozen(p.mask, h0 + gi);
+                advance(gi, qi);
                 const uint32_t parity = ((i >> 1) & 1) ^ 1u;
-                if (!mbar_wait(&bars.do_empty[s], parity, abort, status, kStatusTimeout)) break;
                 uint8_t* st = sm + KvSmem::st + s * KvSmem::st_bytes;
-                float* vec = reinterpret_cast<float*>(st + KvSmem::st_vec);
+                if (!mbar_wait(&bars.do_empty[s], parity, abort, status, kStatusTimeout)) break;
                 mbar_expect_tx(&bars.do_full[s], kTile);
-                load_tile(st + KvSmem::st_do, &p.tm_do, &bars.do_full[s], qb * 128, bh);
+                load_tile(st + KvSmem::st_do, &p.tm_do, &bars.do_full[s], y, bh);
                 if (!mbar_wait(&bars.q_empty[s], parity, abort, status, kStatusTimeout)) break;
-                mbar_expect_tx(&bars.q_full[s], 1024 + (frz ? 1024 : kTile));
-                if (!frz) load_tile(st + KvSmem::st_q, &p.tm_q, &bars.q_full[s], qb * 128, bh);
-                bulk_load(vec, p.rowvec + ((size_t)bh * p.nqb + qb) * 256, 1024, &bars.q_full[s]);
-                if (frz)
-                    bulk_load(vec + 256, p.r2p + (size_t)h * (p.Tp + 256) + (size_t)(qb - kb) * 128, 1024,
-                              &bars.q_full[s]);
+                if (!frz) {
+                    mbar_expect_tx(&bars.q_full[s], kTile);
+                    load_tile(st + KvSmem::st_q, &p.tm_q, &bars.q_full[s], y, bh);
+                } else {
+                    mbar_arrive(&bars.q_full[s]);   // nothing to load: the phase passes
+                }
+                if (vi < ntiles) load_vec();   // of tile i + 2, over those of tile i - 2
             }
         }
     } else if (warp == 9) {
@@ -537,9 +629,9 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
             auto tiles = [&](auto kinds) {
                 constexpr int M = decltype(kinds)::value;
                 int nord = 0;   // ordinary tiles so far (the first one starts dK)
-                bool frz = M == 0 ? false : M == 1 ? true : head_frozen(p.mask, h0);
+                bool frz = M == 0 ? false : M == 1 ? true : head_frozen(p.mask, h0 + gi0);
                 if (!frz) ok = ok && issue_s(0) && issue_dp(0);
-                for (int i = 0, gi = 0, qi = 0; i < ntiles && ok; ++i) {
+                for (int i = 0, gi = gi0, qi = qi0; i < ntiles && ok; ++i) {
                     const int s = i & 1;
                     if (++qi == (kWin && !frz ? nq_ord : nq_frz)) {
                         qi = 0;
@@ -597,7 +689,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
             int nord = 0;     // ordinary tiles so far: phases of sdp_full
             float a2k = 0.f;  // a * log2(e) of my key for the current query head (frozen heads)
             const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-            for (int i = 0, gi = 0, qi = 0; i < ntiles; ++i) {
+            for (int i = 0, gi = gi0, qi = qi0; i < ntiles; ++i) {
                 const bool diag = qi == 0;   // the query head's first tile: query block kb
                 const int h = h0 + gi;
                 const bool frz = M == 0 ? false : M == 1 ? true : head_frozen(p.mask, h);
@@ -605,16 +697,15 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                 const int q_far = !kWin || key < p.sinks ? 128 : t + p.window - qi * 128;
                 // some key of the block does not see some query of the tile through the window
                 const bool cut = kWin && p.window < (qi + 1) * 128 && kb * 128 + 127 >= p.sinks;
-                if (frz && diag) a2k = p.a2p[(size_t)h * p.Tp + key];   // in flight during the wait below
+                if (frz && (diag || i == 0)) a2k = p.a2p[(size_t)h * p.Tp + key];   // in flight during the wait below
                 if (++qi == (kWin && !frz ? nq_ord : nq_frz)) {
                     qi = 0;
                     ++gi;
                 }
                 const int s = i & 1;
                 const uint32_t region = lane_base + 128 * s;
-                if (!(ok = mbar_wait(&bars.q_full[s], (i >> 1) & 1, abort, status, kStatusTimeout))) break;
-                const float* vec =
-                    reinterpret_cast<const float*>(sm + KvSmem::st + s * KvSmem::st_bytes + KvSmem::st_vec);
+                if (!(ok = mbar_wait(&bars.vec_full[i & 3], (i >> 2) & 1, abort, status, kStatusTimeout))) break;
+                const float* vec = reinterpret_cast<const float*>(sm + KvSmem::vec + (i & 3) * KvSmem::vec_bytes);
                 if (!frz) {
                     // the commit of S^T also means that the MMAs of tile i - 2 are done
                     if (!(ok = mbar_wait(&bars.s_full, nord & 1, abort, status, kStatusTimeout))) break;
@@ -716,25 +807,55 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
             tiles(HeadKinds<2>{});
         // tcgen05.ld is warp-collective: every lane loads, only rows inside T are stored;
         // each half of the warps writes its 64 columns of dV and dK (those inside d)
-        if (ok &&
-            mbar_wait_warp(&bars.q_empty[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1, abort, status, kStatusTimeout)) {
-            tc_fence_after();
-            const int c0 = 64 * half, n = min(64, p.d - c0);
-            const int key0 = key - lane;
+        ok = __all_sync(0xffffffffu, ok) &&
+             mbar_wait_warp(&bars.q_empty[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1, abort, status, kStatusTimeout);
+        tc_fence_after();
+        const int c0 = 64 * half, n = min(64, p.d - c0);
+        const int key0 = key - lane;
+        const bool joined = split && nparts > 1;
+        // a part's dV and dK: [dV | dK][column][key] in fp32
+        const size_t part_floats = (size_t)2 * p.d * 128;
+        float* parts = p.part_sums + ((size_t)bkv * p.split_blocks + kb) * p.parts * part_floats + c0 * 128 + t;
+        for (int i = 0; i < 2 && ok; ++i) {   // dV, dK
             uint32_t v[64];
-            tmem_ld32(lane_base + 256 + c0, v);
-            tmem_ld32(lane_base + 256 + c0 + 32, v + 32);
-            tmem_ld_wait();
-            store_rows_cols(p.dv + ((size_t)bkv * p.T + key0) * p.d, p.d, p.T - key0, c0, n, v, 1.f);
-            if (any_ord) {
-                tmem_ld32(lane_base + 384 + c0, v);
-                tmem_ld32(lane_base + 384 + c0 + 32, v + 32);
+            if (i == 0 || any_ord) {
+                tmem_ld32(lane_base + 256 + 128 * i + c0, v);
+                tmem_ld32(lane_base + 256 + 128 * i + c0 + 32, v + 32);
                 tmem_ld_wait();
             } else {
 #pragma unroll
                 for (int c = 0; c < 64; ++c) v[c] = 0u;
             }
-            store_rows_cols(p.dk + ((size_t)bkv * p.T + key0) * p.d, p.d, p.T - key0, c0, n, v, p.scale);
+            __nv_bfloat16* out = (i == 0 ? p.dv : p.dk) + ((size_t)bkv * p.T + key0) * p.d;
+            if (!joined) {
+                store_rows_cols(out, p.d, p.T - key0, c0, n, v, i == 0 ? 1.f : p.scale);
+            } else {
+                float* mine = parts + part * part_floats + (size_t)i * p.d * 128;
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    if (c < n) __stcg(mine + c * 128, __uint_as_float(v[c]));
+            }
+        }
+        if (joined) {   // the block that ends last adds the parts up in their order
+            __threadfence();
+            row_warps_sync();
+            if (threadIdx.x == 0)
+                last_flag = atomicAdd(p.part_count + (size_t)bkv * p.split_blocks + kb, 1u) == (uint32_t)nparts - 1;
+            row_warps_sync();
+            __threadfence();
+            for (int i = 0; i < 2 && last_flag; ++i) {
+                float v[64];
+#pragma unroll
+                for (int c = 0; c < 64; ++c) v[c] = 0.f;
+                for (int k = 0; k < nparts; ++k) {
+                    const float* src = parts + k * part_floats + (size_t)i * p.d * 128;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if (c < n) v[c] += __ldcg(src + c * 128);
+                }
+                __nv_bfloat16* out = (i == 0 ? p.dv : p.dk) + ((size_t)bkv * p.T + key0) * p.d;
+                store_rows_cols(out, p.d, p.T - key0, c0, n, reinterpret_cast<const uint32_t*>(v), i == 0 ? 1.f : p.scale);
+            }
         }
     }
 
@@ -1045,9 +1166,39 @@ cudaError_t launch_dh_fwd(const LayerArgs& a, cudaStream_t s) {
     return e;
 }
 
+// Parts of the key blocks that hold sinks: every query sees such a block, so it has G nqb tiles
+// where another has G times the window's, and alone it would be the length of the launch. Each
+// part gets about half of an SM's share of the tiles (an ordinary one counted as two frozen
+// ones). The sums are kept where the d = 64 backward accumulates dQ.
+// (H32/Hkv8 d128, window 512, 16 sinks, B2 T4096: forward and backward @@@ us with whole blocks,
+// @@@ us with parts.)
+void plan_parts(DhParams& p, const LayerArgs& a) {
+    p.split_blocks = 0;
+    p.parts = 1;
+    if (a.window == 0 || a.sinks == 0 || p.n_ord == 0) return;
+    const int n_sink = a.sinks >= a.T ? p.nqb : (a.sinks + 127) / 128;
+    const double nq = std::min<double>(p.nqb, (126.0 + a.window) / 128 + 1);
+    const double ord = n_sink * (double)p.nqb + (p.nqb - n_sink) * nq, frz = 0.5 * p.nqb * (p.nqb + 1.0);
+    const double share = a.B * (p.n_ord * ord + 0.5 * p.n_frz * frz) / 152;
+    const double longest = p.G * (double)p.nqb * (p.n_ord + 0.5 * p.n_frz) / p.H;
+    const size_t items = (size_t)a.B * p.Hkv * n_sink;
+    const size_t counts = (items * sizeof(uint32_t) + 255) / 256 * 256;
+    const size_t bytes = (size_t)a.B * a.H * a.T * kHeadDim * sizeof(float);   // of dq_acc
+    const size_t part_bytes = (size_t)2 * a.d * 128 * sizeof(float);
+    const size_t fit = bytes > counts ? (bytes - counts) / (items * part_bytes) : 0;
+    const double want = std::min(longest / std::max(0.5 * share, 16.0), 32.0);
+    const int parts = (int)std::min<double>(std::ceil(want), (double)fit);
+    if (parts < 2) return;
+    p.split_blocks = n_sink;
+    p.parts = parts;
+    p.part_count = (uint32_t*)a.dq_acc;
+    p.part_sums = (float*)((uint8_t*)a.dq_acc + counts);
+}
+
 cudaError_t launch_dh_bwd(const LayerArgs& a, cudaStream_t s) {
     DhParams p = make_params(a);
     if (!make_maps(p, a, true)) return cudaErrorInvalidValue;
+    plan_parts(p, a);
     p.o_in = (const __nv_bfloat16*)a.o;
     p.dO = (const __nv_bfloat16*)a.dO;
     p.lse_in = a.lse;
@@ -1066,7 +1217,8 @@ cudaError_t launch_dh_bwd(const LayerArgs& a, cudaStream_t s) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(q_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
     if (e != cudaSuccess) return e;
     before_launch(SAF_KERNEL_BWD_KV, s);
-    e = launch_ex(kv_kernel, dim3((unsigned)p.nqb, (unsigned)(a.B * p.Hkv)), dim3(kThreadsBwd),
+    const unsigned levels = (unsigned)(p.nqb + p.split_blocks * (p.parts - 1));
+    e = launch_ex(kv_kernel, dim3(levels, (unsigned)(a.B * p.Hkv)), dim3(kThreadsBwd),
                   (size_t)smem_kv, s, true, 1, p);
     after_launch(SAF_KERNEL_BWD_KV, s);
     if (e != cudaSuccess) return e;
