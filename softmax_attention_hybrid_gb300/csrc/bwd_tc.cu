@@ -85,6 +85,7 @@ struct BwdParams {
     uint32_t* status;
     int B, H, Hkv, G, T, Tp;
     int window, sinks;                 // ordinary heads (kWin kernels)
+    SinkParts sp;                      // (kWin kernels)
     int nqb, n_items, n_act_items;
     int n_act, n_pas;                  // key/value heads with / without an ordinary query head
     uint8_t act_kv[SAF_MAX_HEADS];     // the former
@@ -111,18 +112,39 @@ struct Smem {
 struct Item {
     int b, hk, kb;
     int nord;   // ordinary query heads of the group (their tiles come first); 0: no K, V, dK
+    int part;   // part of a key block of sinks, -1: a whole item
+    int q0, nq_ord, nq_frz;   // query blocks q0 .. of an ordinary, of a frozen head (a part may have none)
 };
 
+template <bool kWin, bool kParts>
 __device__ __forceinline__ Item decode_item(const BwdParams& p, int idx) {
     Item it;
+    it.part = -1;
+    const int split_blocks = kParts ? p.sp.blocks : 0;
+    const int n_slices = p.B * p.n_act;
+    const int n_parts = split_blocks * p.sp.parts * n_slices;
+    if (kParts && idx < n_parts) {   // the parts of blocks of sinks
+        const int level = idx / n_slices, slice = idx - level * n_slices;
+        it.kb = level / p.sp.parts;
+        it.part = level - it.kb * p.sp.parts;
+        it.b = slice / p.n_act;
+        it.hk = p.act_kv[slice - it.b * p.n_act];
+        it.nord = p.gord[it.hk];
+        const SinkParts::Range run = p.sp.range(it.kb, p.nqb, it.part);
+        it.q0 = it.kb + run.first;
+        it.nq_ord = it.nq_frz = run.n;
+        return it;
+    }
     if (idx < p.n_act_items) {
-        const int n_slices = p.B * p.n_act;
-        const int per_group = kSliceGroup * p.nqb;
+        idx -= n_parts;
+        const int levels = p.nqb - split_blocks;
+        const int per_group = kSliceGroup * levels;
         const int g = idx / per_group;
         const int gsize = min(kSliceGroup, n_slices - g * kSliceGroup);
         const int within = idx - g * per_group;
-        it.kb = within / gsize;
-        const int slice = g * kSliceGroup + (within - it.kb * gsize);
+        const int level = within / gsize;
+        it.kb = split_blocks + level;
+        const int slice = g * kSliceGroup + (within - level * gsize);
         it.b = slice / p.n_act;
         it.hk = p.act_kv[slice - it.b * p.n_act];
     } else {
@@ -134,6 +156,9 @@ __device__ __forceinline__ Item decode_item(const BwdParams& p, int idx) {
         it.hk = p.pas_kv[rem - it.b * p.n_pas];
     }
     it.nord = p.gord[it.hk];
+    it.q0 = it.kb;
+    it.nq_ord = query_blocks<kWin>(it.kb, p.nqb, p.window, p.sinks, 128);
+    it.nq_frz = p.nqb - it.kb;
     return it;
 }
 
@@ -166,7 +191,9 @@ struct Barriers {
 // head) with the group size fixed at 1, so that its loops keep their simple form.
 // kWin: ordinary heads with a sliding window and sinks; their tiles are the query blocks
 // that see a key of the item's block.
-template <bool kGrouped, bool kWin>
+// kParts: some of its items are parts of key blocks that hold sinks. (An instance of its own: with
+// the parts' registers the whole launch would spill: 626 us for 585 at a layer without parts.)
+template <bool kGrouped, bool kWin, bool kParts>
 __global__ void __launch_bounds__(threads(kWin), 1) bwd_tc_kernel(const __grid_constant__ BwdParams p) {
     extern __shared__ uint8_t smem_raw[];
     // 1024-byte aligned base (swizzled tiles), derived from the shared array itself so that
@@ -239,8 +266,8 @@ __global__ void __launch_bounds__(threads(kWin), 1) bwd_tc_kernel(const __grid_c
                 mbar_arrive(&bars.item_full[slot]);
                 slot = (slot + 1) % kRing;
                 if (idx < 0) break;
-                const Item it = decode_item(p, idx);
-                if (it.nord > 0) {
+                const Item it = decode_item<kWin, kParts>(p, idx);
+                if (it.nord > 0 && (!kParts || it.nq_ord > 0)) {
                     if (!(ok = mbar_wait(&bars.kv_empty, kv_empty_ph, abort, status, kStatusTimeout))) break;
                     kv_empty_ph ^= 1;
                     uint8_t* kv = sm + Smem::kv;
@@ -255,8 +282,8 @@ __global__ void __launch_bounds__(threads(kWin), 1) bwd_tc_kernel(const __grid_c
                     const int bh = it.b * p.H + h;
                     const bool frz = gi >= it.nord;
                     const bool exact = frz && (p.hflag[h] & 2u) != 0;
-                    const int q_end = it.kb + (frz ? nqb - it.kb : query_blocks<kWin>(it.kb, nqb, p.window, p.sinks, 128));
-                    for (int qb = it.kb; qb < q_end; ++qb) {
+                    const int q_end = it.q0 + (frz ? it.nq_frz : it.nq_ord);
+                    for (int qb = it.q0; qb < q_end; ++qb) {
                         if (!(ok = mbar_wait(&bars.st_empty[stage], (st_empty_bits >> stage) & 1u, abort, status,
                                              kStatusTimeout)))
                             break;
@@ -337,10 +364,10 @@ __global__ void __launch_bounds__(threads(kWin), 1) bwd_tc_kernel(const __grid_c
                 mbar_arrive(&bars.item_empty[slot]);
                 slot = (slot + 1) % kRing;
                 if (idx < 0) break;
-                const Item it = decode_item(p, idx);
+                const Item it = decode_item<kWin, kParts>(p, idx);
                 // its ordinary tiles come first
-                const int n_ord = it.nord * query_blocks<kWin>(it.kb, nqb, p.window, p.sinks, 128);
-                const int n = n_ord + (G - it.nord) * (nqb - it.kb);   // tiles of the item
+                const int n_ord = it.nord * it.nq_ord;
+                const int n = n_ord + (G - it.nord) * it.nq_frz;   // tiles of the item
                 if (n_ord > 0) {
                     if (!(ok = mbar_wait(&bars.kv_full, kv_full_ph, abort, status, kStatusTimeout))) break;
                     kv_full_ph ^= 1;
@@ -478,15 +505,15 @@ __global__ void __launch_bounds__(threads(kWin), 1) bwd_tc_kernel(const __grid_c
             if (lane == 0) mbar_arrive(&bars.item_empty[slot]);
             slot = (slot + 1) % kRing;
             if (idx < 0) break;
-            const Item it = decode_item(p, idx);
+            const Item it = decode_item<kWin, kParts>(p, idx);
             const int bkv = it.b * p.Hkv + it.hk;   // the key/value slice whose dK, dV this item writes
             const int key = it.kb * 128 + j;
             // tile i: query head gheads[hk G + gi] (ordinary for gi < nord), query block qb
-            int gi = 0, qb = it.kb;
-            const int nq_ord = query_blocks<kWin>(it.kb, nqb, p.window, p.sinks, 128);   // of an ordinary head
-            const int q_last = it.kb + nq_ord - 1;
-            const int n_ord = it.nord * nq_ord;   // the ordinary tiles come first
-            const int n = n_ord + (G - it.nord) * (nqb - it.kb);
+            int gi = 0, qb = it.q0;
+            const int q_last = it.q0 + it.nq_ord - 1;   // of an ordinary head
+            const int n_ord = it.nord * it.nq_ord;      // the ordinary tiles come first
+            const int n = n_ord + (G - it.nord) * it.nq_frz;
+            if (kParts && n == 0) continue;   // a part without query blocks
             // In the multi-head layer a frozen item's tiles all belong to one head: the factor
             // exp(a[j] - A) of its key rows stays out of W^T and is applied to dV at the end.
             // A group of query heads puts it into each W^T tile instead.
@@ -496,7 +523,7 @@ __global__ void __launch_bounds__(threads(kWin), 1) bwd_tc_kernel(const __grid_c
             // the multi-head layer has one query head per item: its slice and kind are fixed
             const int h_item = p.gheads[it.hk * G];
             for (int i = 0; i < n && ok; ++i) {
-                if (!kGrouped) qb = it.kb + i;
+                if (!kGrouped) qb = it.q0 + i;
                 const bool diag = qb == it.kb;
                 const int h = kGrouped ? p.gheads[it.hk * G + gi] : h_item;
                 const int bh = it.b * p.H + h;
@@ -668,14 +695,14 @@ __global__ void __launch_bounds__(threads(kWin), 1) bwd_tc_kernel(const __grid_c
                 if (!kGrouped) {
                     if (!frz && i > 0) drain_dq(bh, qb - 1, dsbuf(gto & 1));
                 } else if (i > 0 && i - 1 < n_ord) {
-                    const bool first = qb == it.kb;
+                    const bool first = qb == it.q0;
                     const int bhp = it.b * p.H + p.gheads[it.hk * G + (first ? gi - 1 : gi)];
                     drain_dq(bhp, first ? q_last : qb - 1, dsbuf((frz ? gto - 1 : gto) & 1));
                 }
                 pending = stage;
                 stage = (stage + 1) % kStages;
-                if (kGrouped && ++qb == (frz ? nqb : q_last + 1)) {   // next query head of the group
-                    qb = it.kb;
+                if (kGrouped && ++qb == (frz ? it.q0 + it.nq_frz : q_last + 1)) {   // next query head of the group
+                    qb = it.q0;
                     if (++gi >= it.nord && gi < G) exact = (p.hflag[p.gheads[it.hk * G + gi]] & 2u) != 0;
                 }
             }
@@ -691,7 +718,15 @@ __global__ void __launch_bounds__(threads(kWin), 1) bwd_tc_kernel(const __grid_c
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.dkv_free);
-            {
+            if (kParts && it.part >= 0) {   // sums of a part (a group that has an ordinary head)
+                float* sums = p.sp.sums + (((size_t)bkv * p.sp.blocks + it.kb) * p.sp.parts + it.part) * (2 * 128 * 64);
+                uint4* dst = reinterpret_cast<uint4*>(sums + j * 64 + 32 * half);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    dst[c] = make_uint4(dv[4 * c], dv[4 * c + 1], dv[4 * c + 2], dv[4 * c + 3]);
+                    dst[c + 128 * 64 / 4] = make_uint4(dk[4 * c], dk[4 * c + 1], dk[4 * c + 2], dk[4 * c + 3]);
+                }
+            } else {
                 // exp(a[j] - A) of my key, when the item left it out of W^T (factorised form)
                 float fv = 1.f;
                 if (ea_at_end && !exact) fv = p.eap[(size_t)p.gheads[it.hk * G] * p.Tp + key];
@@ -808,8 +843,11 @@ cudaError_t launch_tc_bwd(const LayerArgs& a, cudaStream_t s) {
         else
             p.pas_kv[p.n_pas++] = (uint8_t)hk;
     }
-    p.n_act_items = a.B * p.n_act * p.nqb;
-    p.n_items = BHkv * p.nqb;
+    // dq serves as scratch until dq_finish_kernel writes it
+    p.sp = plan_sink_parts(a, (float*)a.dq, (size_t)BH * a.T * kHeadDim * sizeof(__nv_bfloat16));
+    const int extra = a.B * p.n_act * p.sp.blocks * (p.sp.parts - 1);   // items that are parts, less the whole ones
+    p.n_act_items = a.B * p.n_act * p.nqb + extra;
+    p.n_items = BHkv * p.nqb + extra;
 
     // (the dQ accumulator of the ordinary heads was zeroed by bwd_prep_kernel)
     cudaError_t e;
@@ -817,8 +855,11 @@ cudaError_t launch_tc_bwd(const LayerArgs& a, cudaStream_t s) {
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int smem = Smem::total + 1024;
-    void (*kernel)(BwdParams) = p.window > 0 ? (p.G > 1 ? bwd_tc_kernel<true, true> : bwd_tc_kernel<false, true>)
-                                             : (p.G > 1 ? bwd_tc_kernel<true, false> : bwd_tc_kernel<false, false>);
+    const bool grouped = p.G > 1;
+    void (*kernel)(BwdParams) =
+        p.sp.blocks > 0  ? (grouped ? bwd_tc_kernel<true, true, true> : bwd_tc_kernel<false, true, true>)
+        : p.window > 0   ? (grouped ? bwd_tc_kernel<true, true, false> : bwd_tc_kernel<false, true, false>)
+                         : (grouped ? bwd_tc_kernel<true, false, false> : bwd_tc_kernel<false, false, false>);
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const bool win = p.window > 0;
@@ -833,6 +874,7 @@ cudaError_t launch_tc_bwd(const LayerArgs& a, cudaStream_t s) {
     before_launch(SAF_KERNEL_BWD, s);
     e = launch_ex(kernel, dim3(grid), dim3(threads(win)), smem, s, true, 1, p);
     after_launch(SAF_KERNEL_BWD, s);
+    if (e == cudaSuccess && p.sp.blocks > 0) e = launch_join_parts(a, p.sp, s);
     if (e != cudaSuccess) return e;
     dim3 g2((unsigned)(((long long)a.T * 8 + 255) / 256), BH);
     before_launch(SAF_KERNEL_DQ_FINISH, s);

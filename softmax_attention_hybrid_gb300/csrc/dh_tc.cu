@@ -22,9 +22,6 @@
 #include <math.h>
 #include <string.h>
 
-#include <algorithm>
-#include <cmath>
-
 #include "saf_internal.h"
 #include "tc_common.cuh"
 
@@ -106,11 +103,7 @@ struct DhParams {
     const float* a2p;      // [H, Tp]: a * log2(e), -inf padded
     const float* r2p;      // [H, Tp + 256]: r * log2(e) shifted by 127, -inf padded
     float* rowvec;         // [B, H, nqb, 256]: -lse * log2(e) | D per query block
-    // key-block pass, windowed: the first split_blocks key blocks are done in up to `parts` blocks
-    // of threads each, whose sums and a count of the ended ones are here (see plan_parts)
-    float* part_sums;
-    uint32_t* part_count;
-    int split_blocks, parts;
+    SinkParts sp;          // key-block pass, windowed
     uint32_t* status;
     int B, H, T, d, Tp, nqb;
     int Hkv, G;            // key/value heads; query head h reads key/value head h / G
@@ -434,14 +427,9 @@ __global__ void __launch_bounds__(128) dh_rowvec_kernel(const __grid_constant__ 
         }
     }
     float* v = p.rowvec + ((size_t)bh * p.nqb + qb) * 256;
-    if (threadIdx.x == 0 && (size_t)bh * p.nqb + qb < (size_t)p.B * p.Hkv * p.split_blocks)
-        p.part_count[(size_t)bh * p.nqb + qb] = 0;
     v[threadIdx.x] = nl2;
     v[128 + threadIdx.x] = dd;
 }
-
-// Barrier of the 8 row warps of a backward block.
-__device__ __forceinline__ void row_warps_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // TMEM column of k-step k (16 rows of the contraction) of an operand written in
 // chunks of 32 rows: chunk c holds its 16 packed pairs at [32 c, 32 c + 16) and the
@@ -489,7 +477,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ KvBars bars;
     __shared__ uint32_t tmem_base_sh;
-    __shared__ int abort_flag, last_flag;
+    __shared__ int abort_flag;
     grid_dep_wait();
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -497,37 +485,29 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
     // blocks, which have the most query blocks after them.
     long long u = (long long)blockIdx.y * gridDim.x + blockIdx.x;
     const int slices = p.B * p.Hkv;
-    const long long n_parts = kWin ? (long long)p.split_blocks * p.parts * slices : 0;
-    const bool split = kWin && u < n_parts;
-    if (!split) u -= n_parts;
+    const long long n_parts = kWin ? (long long)p.sp.blocks * p.sp.parts * slices : 0;
+    const bool in_parts = kWin && u < n_parts;
+    if (!in_parts) u -= n_parts;
     const int level = (int)(u / slices);
     const int bkv = (int)(u - (long long)level * slices);   // key/value slice
-    const int kb = split ? level / p.parts : (kWin ? p.split_blocks : 0) + level;
+    const int kb = in_parts ? level / p.sp.parts : (kWin ? p.sp.blocks : 0) + level;
     const int b = bkv / p.Hkv, h0 = (bkv - b * p.Hkv) * p.G;   // its query heads: h0 .. h0 + G - 1
-    // query tiles per query head: those that see a key of the block through a window
-    const int nq_frz = p.nqb - kb, nq_ord = query_blocks<kWin>(kb, p.nqb, p.window, p.sinks, 128);
-    int ntiles = 0, gi0 = 0, qi0 = 0, gi1 = p.G;   // tiles, the first one's head and block, the heads' end
-    int part = 0, nparts = 1;
-    if (split) {   // a part of the tiles, of which every head has nq_frz
-        // (all of them where every head is frozen: the block is then like its neighbours)
-        bool all_frz = true;
-        for (int gi = 0; gi < p.G; ++gi) all_frz = all_frz && head_frozen(p.mask, h0 + gi);
-        const int total = p.G * nq_frz, each = all_frz ? total : (total + p.parts - 1) / p.parts;
-        nparts = (total + each - 1) / each;
-        part = level % p.parts;
-        if (part >= nparts) return;
-        const int first = part * each;
-        ntiles = min(each, total - first);
-        gi0 = first / nq_frz;
-        qi0 = first - gi0 * nq_frz;
-        gi1 = (first + ntiles - 1) / nq_frz + 1;
-    }
     bool any_ord = false, any_frz = false;
-    for (int gi = gi0; gi < gi1; ++gi) {
-        const bool frz = head_frozen(p.mask, h0 + gi);
-        (frz ? any_frz : any_ord) = true;
-        if (!split) ntiles += kWin && !frz ? nq_ord : nq_frz;
+    for (int gi = 0; gi < p.G; ++gi) (head_frozen(p.mask, h0 + gi) ? any_frz : any_ord) = true;
+    // Query tiles kb + q0 .. of a head, those that see a key of the block through a window. A part
+    // has a run of them (the first one all of them where every head is frozen: the block is then
+    // like its neighbours).
+    int q0 = 0, nq_frz = p.nqb - kb, nq_ord = query_blocks<kWin>(kb, p.nqb, p.window, p.sinks, 128);
+    const bool split = in_parts && any_ord;
+    const int part = in_parts ? level % p.sp.parts : 0;
+    if (split) {
+        const SinkParts::Range run = p.sp.range(kb, p.nqb, part);
+        q0 = run.first;
+        nq_frz = nq_ord = run.n;
     }
+    if (in_parts && (split ? nq_ord == 0 : part > 0)) return;
+    int ntiles = 0;
+    for (int gi = 0; gi < p.G; ++gi) ntiles += kWin && !head_frozen(p.mask, h0 + gi) ? nq_ord : nq_frz;
     if (threadIdx.x == 0) {
         abort_flag = 0;
         mbar_init(&bars.kv_full, 1);
@@ -563,12 +543,12 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
             load_tile(sm + KvSmem::v, &p.tm_v, &bars.kv_full, kb * 128, bkv);
             // tile i: query head h0 + gi, block kb + qi
             auto advance = [&](int& gi, int& qi) {
-                if (++qi == (kWin && !head_frozen(p.mask, h0 + gi) ? nq_ord : nq_frz)) {
-                    qi = 0;
+                if (++qi == q0 + (kWin && !head_frozen(p.mask, h0 + gi) ? nq_ord : nq_frz)) {
+                    qi = q0;
                     ++gi;
                 }
             };
-            int vi = 0, vgi = gi0, vqi = qi0;
+            int vi = 0, vgi = 0, vqi = q0;
             auto load_vec = [&]() {   // the vectors of the next tile
                 const int h = h0 + vgi;
                 const bool frz = head_frozen(p.mask, h);
@@ -582,7 +562,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
             };
             load_vec();
             if (ntiles > 1) load_vec();
-            for (int i = 0, gi = gi0, qi = qi0; i < ntiles; ++i) {
+            for (int i = 0, gi = 0, qi = q0; i < ntiles; ++i) {
                 const int s = i & 1, y = (kb + qi) * 128, bh = b * p.H + h0 + gi;
                 const bool frz = head_frozen(p.mask, h0 + gi);
                 advance(gi, qi);
@@ -629,12 +609,12 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
             auto tiles = [&](auto kinds) {
                 constexpr int M = decltype(kinds)::value;
                 int nord = 0;   // ordinary tiles so far (the first one starts dK)
-                bool frz = M == 0 ? false : M == 1 ? true : head_frozen(p.mask, h0 + gi0);
+                bool frz = M == 0 ? false : M == 1 ? true : head_frozen(p.mask, h0);
                 if (!frz) ok = ok && issue_s(0) && issue_dp(0);
-                for (int i = 0, gi = gi0, qi = qi0; i < ntiles && ok; ++i) {
+                for (int i = 0, gi = 0, qi = q0; i < ntiles && ok; ++i) {
                     const int s = i & 1;
-                    if (++qi == (kWin && !frz ? nq_ord : nq_frz)) {
-                        qi = 0;
+                    if (++qi == q0 + (kWin && !frz ? nq_ord : nq_frz)) {
+                        qi = q0;
                         ++gi;
                     }
                     // tile i + 1 is an ordinary one
@@ -689,17 +669,17 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
             int nord = 0;     // ordinary tiles so far: phases of sdp_full
             float a2k = 0.f;  // a * log2(e) of my key for the current query head (frozen heads)
             const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-            for (int i = 0, gi = gi0, qi = qi0; i < ntiles; ++i) {
-                const bool diag = qi == 0;   // the query head's first tile: query block kb
+            for (int i = 0, gi = 0, qi = q0; i < ntiles; ++i) {
+                const bool diag = qi == 0, first = qi == q0;   // query block kb; the head's first tile
                 const int h = h0 + gi;
                 const bool frz = M == 0 ? false : M == 1 ? true : head_frozen(p.mask, h);
                 // queries of the tile from q_far on do not see my key through the window
                 const int q_far = !kWin || key < p.sinks ? 128 : t + p.window - qi * 128;
                 // some key of the block does not see some query of the tile through the window
                 const bool cut = kWin && p.window < (qi + 1) * 128 && kb * 128 + 127 >= p.sinks;
-                if (frz && (diag || i == 0)) a2k = p.a2p[(size_t)h * p.Tp + key];   // in flight during the wait below
-                if (++qi == (kWin && !frz ? nq_ord : nq_frz)) {
-                    qi = 0;
+                if (frz && first) a2k = p.a2p[(size_t)h * p.Tp + key];   // in flight during the wait below
+                if (++qi == q0 + (kWin && !frz ? nq_ord : nq_frz)) {
+                    qi = q0;
                     ++gi;
                 }
                 const int s = i & 1;
@@ -812,10 +792,6 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
         tc_fence_after();
         const int c0 = 64 * half, n = min(64, p.d - c0);
         const int key0 = key - lane;
-        const bool joined = split && nparts > 1;
-        // a part's dV and dK: [dV | dK][column][key] in fp32
-        const size_t part_floats = (size_t)2 * p.d * 128;
-        float* parts = p.part_sums + ((size_t)bkv * p.split_blocks + kb) * p.parts * part_floats + c0 * 128 + t;
         for (int i = 0; i < 2 && ok; ++i) {   // dV, dK
             uint32_t v[64];
             if (i == 0 || any_ord) {
@@ -826,35 +802,15 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
 #pragma unroll
                 for (int c = 0; c < 64; ++c) v[c] = 0u;
             }
-            __nv_bfloat16* out = (i == 0 ? p.dv : p.dk) + ((size_t)bkv * p.T + key0) * p.d;
-            if (!joined) {
-                store_rows_cols(out, p.d, p.T - key0, c0, n, v, i == 0 ? 1.f : p.scale);
+            if (!split) {
+                store_rows_cols((i == 0 ? p.dv : p.dk) + ((size_t)bkv * p.T + key0) * p.d, p.d, p.T - key0, c0, n, v,
+                                i == 0 ? 1.f : p.scale);
             } else {
-                float* mine = parts + part * part_floats + (size_t)i * p.d * 128;
+                float* sums = p.sp.sums + ((((size_t)bkv * p.sp.blocks + kb) * p.sp.parts + part) * 2 + i) * 128 * p.d;
+                uint4* dst = reinterpret_cast<uint4*>(sums + (size_t)t * p.d + c0);
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
-                    if (c < n) __stcg(mine + c * 128, __uint_as_float(v[c]));
-            }
-        }
-        if (joined) {   // the block that ends last adds the parts up in their order
-            __threadfence();
-            row_warps_sync();
-            if (threadIdx.x == 0)
-                last_flag = atomicAdd(p.part_count + (size_t)bkv * p.split_blocks + kb, 1u) == (uint32_t)nparts - 1;
-            row_warps_sync();
-            __threadfence();
-            for (int i = 0; i < 2 && last_flag; ++i) {
-                float v[64];
-#pragma unroll
-                for (int c = 0; c < 64; ++c) v[c] = 0.f;
-                for (int k = 0; k < nparts; ++k) {
-                    const float* src = parts + k * part_floats + (size_t)i * p.d * 128;
-#pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if (c < n) v[c] += __ldcg(src + c * 128);
-                }
-                __nv_bfloat16* out = (i == 0 ? p.dv : p.dk) + ((size_t)bkv * p.T + key0) * p.d;
-                store_rows_cols(out, p.d, p.T - key0, c0, n, reinterpret_cast<const uint32_t*>(v), i == 0 ? 1.f : p.scale);
+                for (int c = 0; c < 16; ++c)
+                    if (4 * c < n) dst[c] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
             }
         }
     }
@@ -1166,39 +1122,11 @@ cudaError_t launch_dh_fwd(const LayerArgs& a, cudaStream_t s) {
     return e;
 }
 
-// Parts of the key blocks that hold sinks: every query sees such a block, so it has G nqb tiles
-// where another has G times the window's, and alone it would be the length of the launch. Each
-// part gets about half of an SM's share of the tiles (an ordinary one counted as two frozen
-// ones). The sums are kept where the d = 64 backward accumulates dQ.
-// (H32/Hkv8 d128, window 512, 16 sinks, B2 T4096: forward and backward @@@ us with whole blocks,
-// @@@ us with parts.)
-void plan_parts(DhParams& p, const LayerArgs& a) {
-    p.split_blocks = 0;
-    p.parts = 1;
-    if (a.window == 0 || a.sinks == 0 || p.n_ord == 0) return;
-    const int n_sink = a.sinks >= a.T ? p.nqb : (a.sinks + 127) / 128;
-    const double nq = std::min<double>(p.nqb, (126.0 + a.window) / 128 + 1);
-    const double ord = n_sink * (double)p.nqb + (p.nqb - n_sink) * nq, frz = 0.5 * p.nqb * (p.nqb + 1.0);
-    const double share = a.B * (p.n_ord * ord + 0.5 * p.n_frz * frz) / 152;
-    const double longest = p.G * (double)p.nqb * (p.n_ord + 0.5 * p.n_frz) / p.H;
-    const size_t items = (size_t)a.B * p.Hkv * n_sink;
-    const size_t counts = (items * sizeof(uint32_t) + 255) / 256 * 256;
-    const size_t bytes = (size_t)a.B * a.H * a.T * kHeadDim * sizeof(float);   // of dq_acc
-    const size_t part_bytes = (size_t)2 * a.d * 128 * sizeof(float);
-    const size_t fit = bytes > counts ? (bytes - counts) / (items * part_bytes) : 0;
-    const double want = std::min(longest / std::max(0.5 * share, 16.0), 32.0);
-    const int parts = (int)std::min<double>(std::ceil(want), (double)fit);
-    if (parts < 2) return;
-    p.split_blocks = n_sink;
-    p.parts = parts;
-    p.part_count = (uint32_t*)a.dq_acc;
-    p.part_sums = (float*)((uint8_t*)a.dq_acc + counts);
-}
-
 cudaError_t launch_dh_bwd(const LayerArgs& a, cudaStream_t s) {
     DhParams p = make_params(a);
     if (!make_maps(p, a, true)) return cudaErrorInvalidValue;
-    plan_parts(p, a);
+    // (the accumulator of the d = 64 backward's dQ is not used here)
+    p.sp = plan_sink_parts(a, a.dq_acc, (size_t)a.B * a.H * a.T * kHeadDim * sizeof(float));
     p.o_in = (const __nv_bfloat16*)a.o;
     p.dO = (const __nv_bfloat16*)a.dO;
     p.lse_in = a.lse;
@@ -1217,7 +1145,7 @@ cudaError_t launch_dh_bwd(const LayerArgs& a, cudaStream_t s) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(q_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
     if (e != cudaSuccess) return e;
     before_launch(SAF_KERNEL_BWD_KV, s);
-    const unsigned levels = (unsigned)(p.nqb + p.split_blocks * (p.parts - 1));
+    const unsigned levels = (unsigned)(p.nqb + p.sp.blocks * (p.sp.parts - 1));
     e = launch_ex(kv_kernel, dim3(levels, (unsigned)(a.B * p.Hkv)), dim3(kThreadsBwd),
                   (size_t)smem_kv, s, true, 1, p);
     after_launch(SAF_KERNEL_BWD_KV, s);
@@ -1225,6 +1153,7 @@ cudaError_t launch_dh_bwd(const LayerArgs& a, cudaStream_t s) {
     before_launch(SAF_KERNEL_BWD_Q, s);
     e = launch_ex(q_kernel, grid, dim3(kThreadsBwd), (size_t)smem_q, s, true, 1, p);
     after_launch(SAF_KERNEL_BWD_Q, s);
+    if (e == cudaSuccess && p.sp.blocks > 0) e = launch_join_parts(a, p.sp, s);
     return e;
 }
 

@@ -190,6 +190,25 @@ __device__ __forceinline__ bool window_cuts(int qb, int kb, int window, int blk)
     return (qb - kb) * blk + blk - 1 >= window;
 }
 
+// Key blocks that hold sinks, in parts (sink_parts.cu): the first `blocks` key blocks are split,
+// each into up to `parts` runs of query blocks, whose dV and dK go to
+// sums [B Hkv, blocks, parts, dV | dK, 128 keys, d].
+struct SinkParts {
+    int blocks, parts;
+    float* sums;
+    struct Range {
+        int first, n;
+    };
+    // the query blocks kb + first .. kb + first + n - 1 of nqb (n = 0: the block has fewer parts)
+    __device__ __forceinline__ Range range(int kb, int nqb, int part) const {
+        const int len = nqb - kb, each = (len + parts - 1) / parts, first = part * each;
+        return {first, max(0, min(each, len - first))};
+    }
+};
+// sums, bytes: where the parts may go (blocks = 0 when nothing is split)
+SinkParts plan_sink_parts(const LayerArgs& a, float* sums, size_t bytes);
+cudaError_t launch_join_parts(const LayerArgs& a, const SinkParts& sp, cudaStream_t s);
+
 // saf_api.cu: SAF_OK on an sm_103 device, else the error to return; a launch's result as a status.
 int check_device();
 int launch_status(cudaError_t e);

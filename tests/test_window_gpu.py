@@ -136,8 +136,7 @@ def test_blocks_of_sinks_in_parts(saf, d, H, Hkv, frozen, T, window, sinks):
     out = _run(saf, g, flags, window, sinks)
     _check("bf16", x, out, flags, window, sinks)
     again = _run(saf, g, flags, window, sinks)
-    if d != 64:   # (dv of mixed groups, in one order whichever part ends last)
-        assert torch.equal(out["dk"], again["dk"]) and torch.equal(out["dv"], again["dv"])
+    assert torch.equal(out["dk"], again["dk"]) and torch.equal(out["dv"], again["dv"])
 
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 96), ("fp32", 64)])
