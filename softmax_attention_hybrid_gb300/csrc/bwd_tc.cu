@@ -130,8 +130,8 @@ __device__ __forceinline__ Item decode_item(const BwdParams& p, int idx) {
         it.b = slice / p.n_act;
         it.hk = p.act_kv[slice - it.b * p.n_act];
         it.nord = p.gord[it.hk];
-        const SinkParts::Range run = p.sp.range(it.kb, p.nqb, it.part);
-        it.q0 = it.kb + run.first;
+        const SinkParts::Range run = p.sp.range(it.kb, p.T, it.part);
+        it.q0 = run.first;
         it.nq_ord = it.nq_frz = run.n;
         return it;
     }
@@ -719,8 +719,7 @@ __global__ void __launch_bounds__(threads(kWin), 1) bwd_tc_kernel(const __grid_c
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.dkv_free);
             if (kParts && it.part >= 0) {   // sums of a part (a group that has an ordinary head)
-                float* sums = p.sp.sums + (((size_t)bkv * p.sp.blocks + it.kb) * p.sp.parts + it.part) * (2 * 128 * 64);
-                uint4* dst = reinterpret_cast<uint4*>(sums + j * 64 + 32 * half);
+                uint4* dst = reinterpret_cast<uint4*>(p.sp.at(bkv, it.kb, it.part, 0, 64) + j * 64 + 32 * half);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     dst[c] = make_uint4(dv[4 * c], dv[4 * c + 1], dv[4 * c + 2], dv[4 * c + 3]);
@@ -844,7 +843,7 @@ cudaError_t launch_tc_bwd(const LayerArgs& a, cudaStream_t s) {
             p.pas_kv[p.n_pas++] = (uint8_t)hk;
     }
     // dq serves as scratch until dq_finish_kernel writes it
-    p.sp = plan_sink_parts(a, (float*)a.dq, (size_t)BH * a.T * kHeadDim * sizeof(__nv_bfloat16));
+    p.sp = plan_sink_parts(a, 128, 128, 152, 16, a.dq, (size_t)BH * a.T * kHeadDim * sizeof(__nv_bfloat16));
     const int extra = a.B * p.n_act * p.sp.blocks * (p.sp.parts - 1);   // items that are parts, less the whole ones
     p.n_act_items = a.B * p.n_act * p.nqb + extra;
     p.n_items = BHkv * p.nqb + extra;
@@ -874,7 +873,7 @@ cudaError_t launch_tc_bwd(const LayerArgs& a, cudaStream_t s) {
     before_launch(SAF_KERNEL_BWD, s);
     e = launch_ex(kernel, dim3(grid), dim3(threads(win)), smem, s, true, 1, p);
     after_launch(SAF_KERNEL_BWD, s);
-    if (e == cudaSuccess && p.sp.blocks > 0) e = launch_join_parts(a, p.sp, s);
+    if (e == cudaSuccess && p.sp.blocks > 0) e = launch_join_parts<__nv_bfloat16>(a, p.sp, s);
     if (e != cudaSuccess) return e;
     dim3 g2((unsigned)(((long long)a.T * 8 + 255) / 256), BH);
     before_launch(SAF_KERNEL_DQ_FINISH, s);

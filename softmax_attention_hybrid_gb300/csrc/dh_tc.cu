@@ -501,8 +501,8 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
     const bool split = in_parts && any_ord;
     const int part = in_parts ? level % p.sp.parts : 0;
     if (split) {
-        const SinkParts::Range run = p.sp.range(kb, p.nqb, part);
-        q0 = run.first;
+        const SinkParts::Range run = p.sp.range(kb, p.T, part);
+        q0 = run.first - kb;
         nq_frz = nq_ord = run.n;
     }
     if (in_parts && (split ? nq_ord == 0 : part > 0)) return;
@@ -806,8 +806,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                 store_rows_cols((i == 0 ? p.dv : p.dk) + ((size_t)bkv * p.T + key0) * p.d, p.d, p.T - key0, c0, n, v,
                                 i == 0 ? 1.f : p.scale);
             } else {
-                float* sums = p.sp.sums + ((((size_t)bkv * p.sp.blocks + kb) * p.sp.parts + part) * 2 + i) * 128 * p.d;
-                uint4* dst = reinterpret_cast<uint4*>(sums + (size_t)t * p.d + c0);
+                uint4* dst = reinterpret_cast<uint4*>(p.sp.at(bkv, kb, part, i, p.d) + (size_t)t * p.d + c0);
 #pragma unroll
                 for (int c = 0; c < 16; ++c)
                     if (4 * c < n) dst[c] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
@@ -1126,7 +1125,7 @@ cudaError_t launch_dh_bwd(const LayerArgs& a, cudaStream_t s) {
     DhParams p = make_params(a);
     if (!make_maps(p, a, true)) return cudaErrorInvalidValue;
     // (the accumulator of the d = 64 backward's dQ is not used here)
-    p.sp = plan_sink_parts(a, a.dq_acc, (size_t)a.B * a.H * a.T * kHeadDim * sizeof(float));
+    p.sp = plan_sink_parts(a, 128, 128, 152, 16, a.dq_acc, (size_t)a.B * a.H * a.T * kHeadDim * sizeof(float));
     p.o_in = (const __nv_bfloat16*)a.o;
     p.dO = (const __nv_bfloat16*)a.dO;
     p.lse_in = a.lse;
@@ -1153,7 +1152,7 @@ cudaError_t launch_dh_bwd(const LayerArgs& a, cudaStream_t s) {
     before_launch(SAF_KERNEL_BWD_Q, s);
     e = launch_ex(q_kernel, grid, dim3(kThreadsBwd), (size_t)smem_q, s, true, 1, p);
     after_launch(SAF_KERNEL_BWD_Q, s);
-    if (e == cudaSuccess && p.sp.blocks > 0) e = launch_join_parts(a, p.sp, s);
+    if (e == cudaSuccess && p.sp.blocks > 0) e = launch_join_parts<__nv_bfloat16>(a, p.sp, s);
     return e;
 }
 

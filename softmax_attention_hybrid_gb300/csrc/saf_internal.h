@@ -190,23 +190,31 @@ __device__ __forceinline__ bool window_cuts(int qb, int kb, int window, int blk)
     return (qb - kb) * blk + blk - 1 >= window;
 }
 
-// Key blocks that hold sinks, in parts (sink_parts.cu): the first `blocks` key blocks are split,
-// each into up to `parts` runs of query blocks, whose dV and dK go to
-// sums [B Hkv, blocks, parts, dV | dK, 128 keys, d].
+// Key blocks that hold sinks, in parts (sink_parts.cu): of the key blocks (of `rows` keys) the first
+// `blocks` are split, each into up to `parts` runs of query blocks (of `q_rows`), whose dV and dK go
+// to sums [B Hkv, blocks, parts, dV | dK, rows, d].
 struct SinkParts {
     int blocks, parts;
+    int rows, q_rows;
     float* sums;
     struct Range {
         int first, n;
     };
-    // the query blocks kb + first .. kb + first + n - 1 of nqb (n = 0: the block has fewer parts)
-    __device__ __forceinline__ Range range(int kb, int nqb, int part) const {
-        const int len = nqb - kb, each = (len + parts - 1) / parts, first = part * each;
-        return {first, max(0, min(each, len - first))};
+    // the query blocks first .. first + n - 1 (n = 0: the key block has fewer parts)
+    __device__ __forceinline__ Range range(int kb, int T, int part) const {
+        const int start = kb * rows / q_rows, end = (T + q_rows - 1) / q_rows;
+        const int each = (end - start + parts - 1) / parts, first = start + part * each;
+        return {first, max(0, min(each, end - first))};
+    }
+    // where part `part` of key block kb of a slice leaves dV (which = 0) or dK (1)
+    __device__ __forceinline__ float* at(int bkv, int kb, int part, int which, int d) const {
+        return sums + ((((size_t)bkv * blocks + kb) * parts + part) * 2 + which) * rows * d;
     }
 };
-// sums, bytes: where the parts may go (blocks = 0 when nothing is split)
-SinkParts plan_sink_parts(const LayerArgs& a, float* sums, size_t bytes);
+// sums, bytes: where the parts may go; slots: blocks of threads that run at once; few: the least
+// tiles worth a part (blocks = 0 when nothing is split)
+SinkParts plan_sink_parts(const LayerArgs& a, int rows, int q_rows, int slots, int few, void* sums, size_t bytes);
+template <typename E>
 cudaError_t launch_join_parts(const LayerArgs& a, const SinkParts& sp, cudaStream_t s);
 
 // saf_api.cu: SAF_OK on an sm_103 device, else the error to return; a launch's result as a status.

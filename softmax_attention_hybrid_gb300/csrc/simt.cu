@@ -253,10 +253,11 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
 // k0 .. k0 + 16 RT - 1 of one key/value slice; loops over the query heads that share it
 // (grouped-query layout; one head in the multi-head layer) and, for each, over
 // query blocks qb >= kb, so that the slice's dV and dK are group sums formed
-// without atomics. Thread rows = keys.
+// without atomics. Thread rows = keys. With a window the grid begins with the parts of
+// the key blocks that hold sinks (SinkParts), each of which has a run of the query blocks.
 // ---------------------------------------------------------------------------
 template <typename E, int D, bool kWin, int RT>
-__global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
+__global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p, SinkParts sp) {
     extern __shared__ float sm[];
     constexpr int NC = D / 16, kT = tile_floats<D>(), kR = 16 * RT;
     float* Ks = sm;
@@ -270,16 +271,22 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
 
     const int T = p.T;
     const int G = p.H / p.Hkv;
-    const int kb = blockIdx.x, bkv = blockIdx.y, b = bkv / p.Hkv, hk = bkv % p.Hkv;
+    const int bkv = blockIdx.y, b = bkv / p.Hkv, hk = bkv % p.Hkv;
+    bool any_ordinary = false;
+    for (int gi = 0; gi < G; ++gi) any_ordinary |= !head_frozen(p.mask, hk * G + gi);
+    const int n_parts = kWin ? sp.blocks * sp.parts : 0, x = blockIdx.x;
+    const bool in_parts = kWin && x < n_parts, split = in_parts && any_ordinary;
+    const int kb = in_parts ? x / sp.parts : x - n_parts + (kWin ? sp.blocks : 0);
+    const int part = in_parts ? x % sp.parts : 0;
+    SinkParts::Range run{0, 0};
+    if (split) run = sp.range(kb, T, part);
+    if (in_parts && (split ? run.n == 0 : part > 0)) return;   // (a frozen group's block is not split)
     const size_t kvbase = (size_t)bkv * T * D;
     const E* k = (const E*)p.k + kvbase;
     const E* v = (const E*)p.v + kvbase;
     const int k0 = kb * kR;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const float scale = 1.f / sqrtf((float)D);
-    bool any_ordinary = false;
-    for (int gi = 0; gi < G; ++gi) any_ordinary |= !head_frozen(p.mask, hk * G + gi);
-
     if (any_ordinary) load_tile<D, kR>(Ks, k, k0, T);
     load_tile<D, kR>(Vs, v, k0, T);
     float dv[RT][NC], dk[RT][NC];
@@ -304,7 +311,12 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
         const long long last = ((long long)k0 + kR - 1 + p.window - 1) / kB;
         q_end = last < nqb - 1 ? (int)last + 1 : nqb;
     }
-    for (int qb = k0 / kB; qb < q_end; ++qb) {
+    int qb = k0 / kB;
+    if (split) {
+        qb = run.first;
+        q_end = run.first + run.n;
+    }
+    for (; qb < q_end; ++qb) {
         const int q0 = qb * kB;
         __syncthreads();
         if (!frozen) load_tile<D, kB>(Qs, q, q0, T);
@@ -349,6 +361,17 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p) {
     }
     }
 
+    if constexpr (kWin) {
+        if (split) {
+            float* sums = sp.at(bkv, kb, part, 0, D);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                Cols<D>::store(sums + (ty * RT + i) * D, dv[i], 1.f, tx);
+                Cols<D>::store(sums + (kR + ty * RT + i) * D, dk[i], 1.f, tx);
+            }
+            return;
+        }
+    }
     E* dvp = (E*)p.dv + kvbase;
     E* dkp = (E*)p.dk + kvbase;
 #pragma unroll
@@ -440,31 +463,35 @@ __global__ void __launch_bounds__(kThreads) bwd_q_kernel(LayerArgs p) {
     }
 }
 
-template <int D, int RT, typename K>
-cudaError_t launch(K kernel, int id, int tiles, const LayerArgs& p, cudaStream_t s, int slices) {
+template <int D, int RT, typename K, typename... Args>
+cudaError_t launch(K kernel, int id, int tiles, const LayerArgs& p, cudaStream_t s, int slices, int extra, Args... args) {
     const int smem = tiles * tile_floats<D>() * (int)sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    dim3 grid((p.T + 16 * RT - 1) / (16 * RT), slices);
+    dim3 grid((p.T + 16 * RT - 1) / (16 * RT) + extra, slices);
     before_launch(id, s);
-    kernel<<<grid, kThreads, smem, s>>>(p);
+    kernel<<<grid, kThreads, smem, s>>>(p, args...);
     after_launch(id, s);
     return cudaGetLastError();
 }
 
 template <typename E, int D, bool kWin, int RT>
 cudaError_t fwd_d(const LayerArgs& p, cudaStream_t s) {
-    return launch<D, RT>(fwd_kernel<E, D, kWin, RT>, SAF_KERNEL_FWD, 4, p, s, p.B * p.H);
+    return launch<D, RT>(fwd_kernel<E, D, kWin, RT>, SAF_KERNEL_FWD, 4, p, s, p.B * p.H, 0);
 }
 
 template <typename E, int D, bool kWin, int RT>
 cudaError_t bwd_kv_d(const LayerArgs& p, cudaStream_t s) {
-    return launch<D, RT>(bwd_kv_kernel<E, D, kWin, RT>, SAF_KERNEL_BWD_KV, 6, p, s, p.B * p.Hkv);
+    // dq serves as scratch until the query-block pass writes it; two blocks of threads an SM
+    const SinkParts sp = plan_sink_parts(p, 16 * RT, kB, 304, 4, p.dq, (size_t)p.B * p.H * p.T * p.d * sizeof(float));
+    const cudaError_t e = launch<D, RT>(bwd_kv_kernel<E, D, kWin, RT>, SAF_KERNEL_BWD_KV, 6, p, s, p.B * p.Hkv,
+                                        sp.blocks * (sp.parts - 1), sp);
+    return e == cudaSuccess && sp.blocks > 0 ? launch_join_parts<float>(p, sp, s) : e;
 }
 
 template <typename E, int D, bool kWin, int RT>
 cudaError_t bwd_q_d(const LayerArgs& p, cudaStream_t s) {
-    return launch<D, RT>(bwd_q_kernel<E, D, kWin, RT>, SAF_KERNEL_BWD_Q, 5, p, s, p.B * p.H);
+    return launch<D, RT>(bwd_q_kernel<E, D, kWin, RT>, SAF_KERNEL_BWD_Q, 5, p, s, p.B * p.H, 0);
 }
 
 template <bool kWin, int RT>

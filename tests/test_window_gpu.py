@@ -126,15 +126,15 @@ def test_grouped(saf, dtype, d, frozen, T, window, sinks):
         assert (np.abs(_np(out["dv"])[:, hk] - dv[:, hk]) <= (2 * u + slack) * A + u * np.abs(dv[:, hk])).all()
 
 
-@pytest.mark.parametrize("d", [64, 96, 128])
-@pytest.mark.parametrize("H,Hkv,frozen", [(8, 1, ()), (8, 1, (1, 3, 6)), (8, 2, (4, 5, 6, 7)), (3, 3, (2,))])
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 96), ("bf16", 128), ("fp32", 64), ("fp32", 96)])
+@pytest.mark.parametrize("H,Hkv,frozen", [(8, 1, ()), (8, 1, (1, 3, 6)), (8, 2, (4, 5, 6, 7)), (8, 4, (1,)), (3, 3, (2,))])
 @pytest.mark.parametrize("T,window,sinks", [(1100, 100, 200), (1409, 200, 16)])
-def test_blocks_of_sinks_in_parts(saf, d, H, Hkv, frozen, T, window, sinks):
+def test_blocks_of_sinks_in_parts(saf, dtype, d, H, Hkv, frozen, T, window, sinks):
     # every query sees the blocks of sinks: their gradients are summed in parts where heads share them
     flags = [1 if h in frozen else 0 for h in range(H)]
-    x, g = _inputs("bf16", 1, H, Hkv, T, d, frozen, seed=T + d)
+    x, g = _inputs(dtype, 1, H, Hkv, T, d, frozen, seed=T + d)
     out = _run(saf, g, flags, window, sinks)
-    _check("bf16", x, out, flags, window, sinks)
+    _check(dtype, x, out, flags, window, sinks)
     again = _run(saf, g, flags, window, sinks)
     assert torch.equal(out["dk"], again["dk"]) and torch.equal(out["dv"], again["dv"])
 
