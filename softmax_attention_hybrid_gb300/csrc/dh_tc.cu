@@ -401,34 +401,50 @@ __global__ void __launch_bounds__(kThreads, 2) dh_fwd_kernel(const __grid_consta
 // ---------------------------------------------------------------------------
 // Backward prep: rowvec[bh, qb, 0..127] = -lse * log2(e) (-inf past T),
 // rowvec[bh, qb, 128..255] = D = sum_c dO_c O_c (0 past T, and for frozen heads,
-// which do not use it). One thread per row, grid (Tp / 128, B H).
+// which do not use it). Grid (Tp / 128, B H). Bound by reading o and dO: 16 lanes read a row
+// of them (a thread per row read every line twice), two rows a warp, eight rows' loads in
+// flight. (H32 d128, B2 T4096: 21.6 us, 35 us with a thread per row, and the layer's forward and
+// backward with window 512 478 us for 533.)
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(128) dh_rowvec_kernel(const __grid_constant__ DhParams p) {
     grid_dep_wait();
     grid_dep_launch();
     const int bh = blockIdx.y, qb = blockIdx.x;
+    float* v = p.rowvec + ((size_t)bh * p.nqb + qb) * 256;
     const int i = qb * 128 + threadIdx.x;
-    float nl2 = -INFINITY, dd = 0.f;
-    if (i < p.T) {
-        const size_t row = (size_t)bh * p.T + i;
-        nl2 = -(p.lse_in[row] * kLog2e);
-        if (!head_frozen(p.mask, bh % p.H)) {
-            const uint4* po = reinterpret_cast<const uint4*>(p.o_in + row * p.d);
-            const uint4* pd = reinterpret_cast<const uint4*>(p.dO + row * p.d);
-            for (int c = 0; c < p.d / 8; ++c) {
-                const uint4 x = __ldg(po + c), y = __ldg(pd + c);
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    v[threadIdx.x] = i < p.T ? -(p.lse_in[(size_t)bh * p.T + i] * kLog2e) : -INFINITY;
+    if (head_frozen(p.mask, bh % p.H)) {
+        v[128 + threadIdx.x] = 0.f;
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = lane & 15;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    dd = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), dd);
-                    dd = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), dd);
-                }
+    for (int it0 = 0; it0 < 16; it0 += 4) {
+        uint4 x[4], y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int row = qb * 128 + 32 * warp + 2 * (it0 + u) + (lane >> 4);
+            x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < p.T && 8 * part < p.d) {
+                const size_t at = ((size_t)bh * p.T + row) * p.d + 8 * part;
+                x[u] = __ldg(reinterpret_cast<const uint4*>(p.o_in + at));
+                y[u] = __ldg(reinterpret_cast<const uint4*>(p.dO + at));
             }
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, ys[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+            float dd = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                dd = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), dd);
+                dd = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), dd);
+            }
+#pragma unroll
+            for (int m = 8; m > 0; m >>= 1) dd += __shfl_xor_sync(0xffffffffu, dd, m);
+            if (part == 0) v[128 + 32 * warp + 2 * (it0 + u) + (lane >> 4)] = dd;
+        }
     }
-    float* v = p.rowvec + ((size_t)bh * p.nqb + qb) * 256;
-    v[threadIdx.x] = nl2;
-    v[128 + threadIdx.x] = dd;
 }
 
 // TMEM column of k-step k (16 rows of the contraction) of an operand written in
