@@ -162,6 +162,12 @@ __device__ __forceinline__ Item decode_item(const BwdParams& p, int idx) {
     return it;
 }
 
+// Whether a tile has pairs to mask, as a compile-time tag.
+template <bool M>
+struct Masked {
+    static constexpr bool value = M;
+};
+
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -191,8 +197,8 @@ struct Barriers {
 // head) with the group size fixed at 1, so that its loops keep their simple form.
 // kWin: ordinary heads with a sliding window and sinks; their tiles are the query blocks
 // that see a key of the item's block.
-// kParts: some of its items are parts of key blocks that hold sinks. (An instance of its own: with
-// the parts' registers the whole launch would spill: 626 us for 585 at a layer without parts.)
+// kParts: some of its items are parts of key blocks that hold sinks. (An instance of its own:
+// a layer without parts takes 588 us with this one, 575 us without.)
 template <bool kGrouped, bool kWin, bool kParts>
 __global__ void __launch_bounds__(threads(kWin), 1) bwd_tc_kernel(const __grid_constant__ BwdParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -556,31 +562,41 @@ __global__ void __launch_bounds__(threads(kWin), 1) bwd_tc_kernel(const __grid_c
                         const int q_far = !cut || key < p.sinks ? 128 : key + p.window - qb * 128;
                         // lse * log2(e) of four query columns per (broadcast) shared-memory load
                         const float4* lse4 = reinterpret_cast<const float4*>(vec + 64 * half);
+                        // only the diagonal and the window's end hide anything: a loop of its own
+                        auto weights = [&](auto tag) {
+                            constexpr bool kMask = decltype(tag)::value;
 #pragma unroll
-                        for (int e = 0; e < 64; e += 4) {
-                            const float4 l4 = lse4[e >> 2];
+                            for (int e = 0; e < 64; e += 4) {
+                                const float4 l4 = lse4[e >> 2];
 #pragma unroll
-                            for (int u = 0; u < 4; u += 2) {
-                                const int q0 = 64 * half + e + u;
-                                // x = S * log2(e) / sqrt(d) - lse * log2(e), two columns per instruction
-                                const float2 x = ffma2(
-                                    make_float2(__uint_as_float(sv[e + u]), __uint_as_float(sv[e + u + 1])),
-                                    make_float2(kScaleLog2, kScaleLog2),
-                                    u == 0 ? make_float2(-l4.x, -l4.y) : make_float2(-l4.z, -l4.w));
-                                float p0 = fast_exp2(x.x);
-                                float p1 = fast_exp2(x.y);
-                                if (diag && j > q0) p0 = 0.f;
-                                if (diag && j > q0 + 1) p1 = 0.f;
-                                if (kWin && q0 >= q_far) p0 = 0.f;
-                                if (kWin && q0 + 1 >= q_far) p1 = 0.f;
-                                if (kWin) {
-                                    pf[(kWin ? 1 : 0) * (e + u)] = p0;
-                                    pf[(kWin ? 1 : 0) * (e + u + 1)] = p1;
-                                } else {
-                                    pk[(e + u) >> 1] = pack_bf16(p0, p1);
+                                for (int u = 0; u < 4; u += 2) {
+                                    const int q0 = 64 * half + e + u;
+                                    // x = S * log2(e) / sqrt(d) - lse * log2(e), two columns per instruction
+                                    const float2 x = ffma2(
+                                        make_float2(__uint_as_float(sv[e + u]), __uint_as_float(sv[e + u + 1])),
+                                        make_float2(kScaleLog2, kScaleLog2),
+                                        u == 0 ? make_float2(-l4.x, -l4.y) : make_float2(-l4.z, -l4.w));
+                                    float p0 = fast_exp2(x.x);
+                                    float p1 = fast_exp2(x.y);
+                                    if (kMask) {
+                                        if (diag && j > q0) p0 = 0.f;
+                                        if (diag && j > q0 + 1) p1 = 0.f;
+                                        if (kWin && q0 >= q_far) p0 = 0.f;
+                                        if (kWin && q0 + 1 >= q_far) p1 = 0.f;
+                                    }
+                                    if (kWin) {
+                                        pf[(kWin ? 1 : 0) * (e + u)] = p0;
+                                        pf[(kWin ? 1 : 0) * (e + u + 1)] = p1;
+                                    } else {
+                                        pk[(e + u) >> 1] = pack_bf16(p0, p1);
+                                    }
                                 }
                             }
-                        }
+                        };
+                        if (diag || cut)
+                            weights(Masked<true>{});
+                        else
+                            weights(Masked<false>{});
                     }
                     uint32_t dp[64];
                     tmem_ld32(lane_base + kColDP + 64 * half, dp);
