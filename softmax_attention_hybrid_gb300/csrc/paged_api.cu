@@ -45,20 +45,19 @@ __global__ void __launch_bounds__(128) join_kernel(const float2* __restrict__ ml
         const float2* r = ml + row * nsplit;
         for (int s = lane; s < nsplit; s += 32) M = fmaxf(M, r[s].x);
         for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-        if (M > -INFINITY) {
+        const float base = M == -INFINITY ? 0.f : M;   // a row that sees no key
 #pragma unroll 4
-            for (int s = mine * kSide + side; s < nsplit; s += kWarps * kSide) {
-                const float2 e = r[s];
-                const float w = exp2f(e.x - M);
-                l += w * e.y;
-                // an item whose keys the row does not see wrote no output
-                if (w > 0.f && c < kLanes) {
-                    const float4 x = *reinterpret_cast<const float4*>(po + (row * nsplit + s) * D + 4 * c);
-                    acc.x = fmaf(w, x.x, acc.x);
-                    acc.y = fmaf(w, x.y, acc.y);
-                    acc.z = fmaf(w, x.z, acc.z);
-                    acc.w = fmaf(w, x.w, acc.w);
-                }
+        for (int s = mine * kSide + side; s < nsplit; s += kWarps * kSide) {
+            const float2 e = r[s];
+            const float w = exp2f(e.x - base);
+            l += w * e.y;   // (a NaN sum stays one, whatever its weight)
+            // an item whose keys the row does not see wrote no output
+            if (w > 0.f && c < kLanes) {
+                const float4 x = *reinterpret_cast<const float4*>(po + (row * nsplit + s) * D + 4 * c);
+                acc.x = fmaf(w, x.x, acc.x);
+                acc.y = fmaf(w, x.y, acc.y);
+                acc.z = fmaf(w, x.z, acc.z);
+                acc.w = fmaf(w, x.w, acc.w);
             }
         }
     }
@@ -85,7 +84,7 @@ __global__ void __launch_bounds__(128) join_kernel(const float2* __restrict__ ml
         }
     }
     if (row >= rows) return;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
     if (side == 0 && c < kLanes) {
         E* dst = o + row * D + 4 * c;
         from_f(dst, acc.x * inv);
@@ -93,7 +92,7 @@ __global__ void __launch_bounds__(128) join_kernel(const float2* __restrict__ ml
         from_f(dst + 2, acc.z * inv);
         from_f(dst + 3, acc.w * inv);
     }
-    if (lane == 0) lse[row] = l > 0.f ? (M + log2f(l)) * kLn2 : -INFINITY;
+    if (lane == 0) lse[row] = l != 0.f ? (M + log2f(l)) * kLn2 : -INFINITY;
 }
 
 template <typename E, int D>

@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
             const size_t row = (size_t)sm.out[x];
             const float lx = sm.l[x];
             if (p.nsplit == 1) {
-                ((float*)p.o)[row * D + col] = lx > 0.f ? acc[x] / lx : 0.f;
-                if (col == 0) p.lse[row] = lx > 0.f ? (sm.m[x] + log2f(lx)) * kLn2 : -INFINITY;
+                ((float*)p.o)[row * D + col] = lx != 0.f ? acc[x] / lx : 0.f;
+                if (col == 0) p.lse[row] = lx != 0.f ? (sm.m[x] + log2f(lx)) * kLn2 : -INFINITY;
             } else {
                 p.po[(row * p.nsplit + split) * D + col] = acc[x];
                 if (col == 0) p.ml[row * p.nsplit + split] = make_float2(sm.m[x], lx);

@@ -439,7 +439,7 @@ __device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, cons
 #pragma unroll
     for (int c = 0; c < kCopies; ++c) {
         const float mc = sh_m[c * kRows + r];
-        if (mc != -INFINITY) L += sh_l[c * kRows + r] * fast_exp2(mc - M);
+        L += sh_l[c * kRows + r] * (mc == -INFINITY ? 0.f : fast_exp2(mc - M));   // (a NaN sum stays one)
     }
     asm volatile("bar.sync 1, 128;" ::: "memory");
     sh_m[t] = M;
@@ -455,7 +455,7 @@ __device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, cons
         const size_t at = (size_t)out_row[x];
         const float l_row = sh_l[x], m_row = sh_m[x];
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (l_row > 0.f)
+        if (l_row != 0.f)
 #pragma unroll
             for (int k = 0; k < kCopies; ++k) {
                 const float4 z = *reinterpret_cast<const float4*>(out + (k * kRows + x) * S::out_pitch + col);
@@ -465,11 +465,11 @@ __device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, cons
             if (col < p.d) *reinterpret_cast<float4*>(p.po + (at * p.nsplit + split) * p.d + col) = y;
             if (col == 0) p.ml[at * p.nsplit + split] = make_float2(m_row, l_row);
         } else {
-            const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
+            const float inv = l_row != 0.f ? 1.f / l_row : 0.f;
             if (col < p.d)
                 *reinterpret_cast<uint2*>((__nv_bfloat16*)p.o + at * p.d + col) =
                     make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
-            if (col == 0) p.lse[at] = l_row > 0.f ? (m_row + log2f(l_row)) * kLn2 : -INFINITY;
+            if (col == 0) p.lse[at] = l_row != 0.f ? (m_row + log2f(l_row)) * kLn2 : -INFINITY;
         }
     }
 }

@@ -199,6 +199,21 @@ def test_large_scores(saf):
         x.check(*x.call(saf))
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+@pytest.mark.parametrize("ctx", [3, 40, 5000])
+@pytest.mark.parametrize("bad", ["q", "inf"])
+def test_a_row_of_nan_stays_one_and_alone(saf, dtype, d, ctx, bad):
+    # a NaN query has NaN for its output, in one item or joined from several; so has one whose scores
+    # are infinite. The other rows of its block keep their bits.
+    x = Batch(dtype, 4, 2, 2, d, 64, (ctx, 7), (2, 2), seed=71)
+    want, want_lse = x.call(saf)
+    x.q[0, 1, 0] = float("nan") if bad == "q" else float("inf")
+    o, lse = x.call(saf)
+    assert o[0, 1, 0].isnan().all() and lse[0, 1, 0].isnan()
+    o[0, 1, 0], lse[0, 1, 0] = want[0, 1, 0], want_lse[0, 1, 0]
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
 def test_positions_far_apart(saf):
     # rows of one block 2500 positions apart: the frozen heads' patterns do not fit beside the tiles
     for dtype, d in (("bf16", 64), ("bf16", 128), ("fp32", 64)):
