@@ -248,7 +248,8 @@ SAF_API int saf_attn_bwd_prepared(const void* q, const void* k, const void* v, c
  * saf_frozen_prepare for these a, r and frozen (as for the _prepared calls).
  * Everything else (shapes, workspace, empty calls, errors, outputs) is as for the
  * calls named above. Keys and values that the window hides from a row must still be
- * finite where another row of the same 128-row block (64 in SAF_FP32) sees them. */
+ * finite where another row of the same 128-row block (64 in SAF_FP32) sees them.
+ * The outputs overlap nothing else (dq also holds partial sums until the call ends). */
 SAF_API int saf_attn_fwd_window(const void* q, const void* k, const void* v, const float* a, const float* r,
                                 int ld_prior, const uint8_t* frozen, const void* state, int window, int sinks, int B,
                                 int H, int Hkv, int T, int d, saf_dtype_t dt, void* o, float* lse, void* workspace,

@@ -428,18 +428,23 @@ def _flags(frozen, H):
     return bytes(_frozen_bytes(frozen, H))
 
 
-def _run(where, fn, idx, stream, *args):
-    """fn(*args, stream) with device `idx` current, on `stream` or the device's current one."""
+def _run(where, fn, idx, *args):
+    """fn(*args, stream) with device `idx` current, on its current stream."""
     if _get_device() != idx:
         with torch.cuda.device(idx):
-            return _run(where, fn, idx, stream, *args)
-    if stream is not None:
-        raw = stream.cuda_stream
-    else:
-        raw = _raw_stream(idx) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+            return _run(where, fn, idx, *args)
+    raw = _raw_stream(idx) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
     st = fn(*args, raw)
     if st != SAF_OK:
         raise SafError(st, where)
+
+
+def _on(stream, t, call):
+    """call() on `stream`, of t's device: what the call allocates and clears belongs to that stream."""
+    if stream.device != t.device:
+        raise ValueError("stream and tensors must be of one device")
+    with torch.cuda.stream(stream):
+        return call()
 
 
 def _prior(a, r, H, idx, none):
@@ -458,6 +463,9 @@ def saf_attn_fwd_window(q, k, v, a, r, frozen, window, sinks=0, state=None, o=No
     `sinks` (query i: keys j <= i with i - j < window or j < sinks; window 0: every key);
     returns (o, lse). q: [B, H, T, d]; k, v: [B, Hkv, T, d]; a, r, frozen as for
     saf_attn_fwd_gqa; state: a prepared frozen-pattern state (saf_frozen_prepare) or None."""
+    if stream is not None:
+        return _on(stream, v, lambda: saf_attn_fwd_window(q, k, v, a, r, frozen, window, sinks, state, o,
+                   lse, workspace))
     idx, dt = _device(v), v.dtype
     B, H, Hkv, T, d = _gqa_shape(q, v, frozen)
     full, rows = (B, H, T, d), (B, H, T)
@@ -471,7 +479,7 @@ def saf_attn_fwd_window(q, k, v, a, r, frozen, window, sinks=0, state=None, o=No
     if workspace is None:
         workspace = alloc_workspace(B, H, T, d, dt, False, v.device)
     ap, rp, ld = _prior(a, r, H, idx, T)
-    _run("saf_attn_fwd_window", _lib.saf_attn_fwd_window, idx, stream, _at(q, idx, dt), _at(k, idx, dt),
+    _run("saf_attn_fwd_window", _lib.saf_attn_fwd_window, idx, _at(q, idx, dt), _at(k, idx, dt),
          _at(v, idx, dt), ap, rp, ld, _flags(frozen, H), _at(state, idx, torch.uint8), int(window), int(sinks), B, H, Hkv, T, d,
          _dt(v), _at(o, idx, dt), _at(lse, idx, torch.float32), _at(workspace, idx, torch.uint8), workspace.numel())
     return o, lse
@@ -481,6 +489,9 @@ def saf_attn_bwd_window(q, k, v, o, do, lse, a, r, frozen, window, sinks=0, stat
                         workspace=None, stream=None):
     """Backward of saf_attn_fwd_window (o, lse: its outputs for the same inputs); returns
     dq [B, H, T, d] and dk, dv [B, Hkv, T, d]."""
+    if stream is not None:
+        return _on(stream, v, lambda: saf_attn_bwd_window(q, k, v, o, do, lse, a, r, frozen, window, sinks,
+                   state, dq, dk, dv, workspace))
     idx, dt = _device(v), v.dtype
     B, H, Hkv, T, d = _gqa_shape(q, v, frozen)
     full, kv = (B, H, T, d), v.shape
@@ -492,7 +503,7 @@ def saf_attn_bwd_window(q, k, v, o, do, lse, a, r, frozen, window, sinks=0, stat
     if workspace is None:
         workspace = alloc_workspace(B, H, T, d, dt, True, v.device)
     ap, rp, ld = _prior(a, r, H, idx, T)
-    _run("saf_attn_bwd_window", _lib.saf_attn_bwd_window, idx, stream, _at(q, idx, dt), _at(k, idx, dt),
+    _run("saf_attn_bwd_window", _lib.saf_attn_bwd_window, idx, _at(q, idx, dt), _at(k, idx, dt),
          _at(v, idx, dt), _at(o, idx, dt), _at(do, idx, dt), _at(lse, idx, torch.float32), ap, rp, ld,
          _flags(frozen, H), _at(state, idx, torch.uint8), int(window), int(sinks), B, H, Hkv, T, d, _dt(v), _at(dq, idx, dt),
          _at(dk, idx, dt), _at(dv, idx, dt), _at(workspace, idx, torch.uint8), workspace.numel())
@@ -530,6 +541,9 @@ def saf_kv_append(k, v, k_cache, v_cache, page_table, ctx, n_new=None, q=None, q
     reads, are left alone); without q it also gives H (default Hkv). status: a CUDA tensor
     whose first 8 bytes, zeroed once by the caller, collect errors for saf_device_status
     (None: errors are not recorded)."""
+    if stream is not None:
+        return _on(stream, v, lambda: saf_kv_append(k, v, k_cache, v_cache, page_table, ctx, n_new, q,
+                   q_out, inv_freq, interleaved, pos_base, frozen, status))
     idx, dt, i32 = _device(v), v.dtype, torch.int32
     shape, caches = v.shape, v_cache.shape
     B, Hkv, T, d = shape
@@ -569,7 +583,7 @@ def saf_kv_append(k, v, k_cache, v_cache, page_table, ctx, n_new=None, q=None, q
         freq = inv_freq.data_ptr() if rope else None
     if status is not None and status.numel() * status.element_size() < 8:
         raise ValueError("status needs 8 bytes")
-    _run("saf_kv_append", _lib.saf_kv_append, idx, stream, qp, kp, vp, _I64x9(qb, qh, qt, kb, kh, kt, vb, vh, vt),
+    _run("saf_kv_append", _lib.saf_kv_append, idx, qp, kp, vp, _I64x9(qb, qh, qt, kb, kh, kt, vb, vh, vt),
          _at(ctx, idx, i32), _at(n_new, idx, i32), _at(page_table, idx, i32), max_pages, freq, rope,
          1 if interleaved else 0, pos_base, _flags(frozen, H), B, H, Hkv, T, d, num_pages, page_size, _dt(v), qo,
          _at(k_cache, idx, dt), _at(v_cache, idx, dt), None if status is None else _at(status, idx, status.dtype))
@@ -590,7 +604,7 @@ def alloc_paged_workspace(B, H, Hkv, T, d, max_len, dtype, prefix_len=0, device=
 
 
 def _paged(where, fn, q, k_cache, v_cache, prefix, P, page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o,
-           lse, workspace, stream):
+           lse, workspace):
     idx, dt = _device(q), q.dtype
     full, caches, table = q.shape, v_cache.shape, page_table.shape
     B, H, T, d = full
@@ -618,7 +632,7 @@ def _paged(where, fn, q, k_cache, v_cache, prefix, P, page_table, ctx, max_len, 
         for t, want in ((q, dt), (v_cache, dt), (page_table, _I32), (ctx, _I32), (o, dt), (lse, _F32), (workspace, _U8)):
             _at(t, idx, want)
     ap, rp, ld = _prior(a, r, H, idx, P + max_len)
-    _run(where, fn, idx, stream, q.data_ptr(), _at(k_cache, idx, dt), v_cache.data_ptr(), *prefix,
+    _run(where, fn, idx, q.data_ptr(), _at(k_cache, idx, dt), v_cache.data_ptr(), *prefix,
          page_table.data_ptr(), table[1], ctx.data_ptr(), _at(n_new, idx, _I32), ap, rp, ld,
          _flags(frozen, H), int(window), int(sinks), B, H, Hkv, T, d, max_len, num_pages, page_size, _dt(q),
          o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
@@ -632,8 +646,11 @@ def saf_attn_paged(q, k_cache, v_cache, page_table, ctx, max_len, n_new=None, a=
     ctx[b] + t; rows t >= n_new[b] come back as o = 0, lse = -inf. max_len: an upper bound of
     ctx[b] + n_new[b]. a, r [H, ld_prior >= max_len] and frozen as for saf_attn_fwd; window and
     sinks as for saf_attn_fwd_window. workspace: alloc_paged_workspace."""
+    if stream is not None:
+        return _on(stream, q, lambda: saf_attn_paged(q, k_cache, v_cache, page_table, ctx, max_len, n_new,
+                   a, r, frozen, window, sinks, o, lse, workspace))
     return _paged("saf_attn_paged", _lib.saf_attn_paged, q, k_cache, v_cache, (), 0, page_table, ctx, max_len, n_new, a,
-                  r, frozen, window, sinks, o, lse, workspace, stream)
+                  r, frozen, window, sinks, o, lse, workspace)
 
 
 def saf_attn_paged_shared(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, ctx, max_len, n_new=None, a=None,
@@ -641,11 +658,14 @@ def saf_attn_paged_shared(q, k_cache, v_cache, prefix_pages, prefix_len, page_ta
     """saf_attn_paged for sequences that share a prefix of prefix_len tokens, held once in the
     pages prefix_pages (int32, on the device): token t of sequence b stands at position
     prefix_len + ctx[b] + t, and ctx, n_new, max_len and page_table count own tokens."""
+    if stream is not None:
+        return _on(stream, q, lambda: saf_attn_paged_shared(q, k_cache, v_cache, prefix_pages, prefix_len,
+                   page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o, lse, workspace))
     if prefix_pages is not None and prefix_pages.numel() * v_cache.shape[2] < prefix_len:
         raise ValueError("prefix_pages holds fewer pages than prefix_len tokens take")
     prefix = (_at(prefix_pages, _device(q), torch.int32), prefix_len)
     return _paged("saf_attn_paged_shared", _lib.saf_attn_paged_shared, q, k_cache, v_cache, prefix, prefix_len,
-                  page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o, lse, workspace, stream)
+                  page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o, lse, workspace)
 
 
 def saf_set_trace_events(kernel: int, start=None, stop=None) -> None:

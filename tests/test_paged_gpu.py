@@ -284,6 +284,29 @@ def test_on_a_given_stream(saf):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_on_a_stream_beside_a_busy_one(saf):
+    # what a call allocates and clears belongs to the stream it is given, not to the current one
+    x = Batch("bf16", 4, 2, 3, 64, 16, (900, 60), (3, 2), seed=6)
+    head = [t.cuda() for t in (x.q, x.kc, x.vc, x.table, x.ctx)]
+    n_new, a, r = (t.cuda() for t in (x.n_new, x.a, x.r))
+    k, v = (torch.randn(2, 2, 3, 64, device="cuda").bfloat16() for _ in range(2))
+    side = torch.cuda.Stream()
+    kw = dict(n_new=n_new, a=a, r=r, frozen=[0, 1, 0, 0])
+    freq = [1.0, 0.1, 0.01, 0.5, 0.2, 0.3, 0.4, 0.6]
+    # the new tokens go to the first slots of pages of their own: a sequence has its page alone
+    pages = torch.arange(2, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    kc, vc, none = torch.zeros_like(head[1]), torch.zeros_like(head[2]), torch.zeros_like(head[4])
+    want = saf.saf_kv_append(k, v, kc, vc, pages, none, n_new, q=head[0], inv_freq=freq), \
+        *saf.saf_attn_paged(*head, x.max_len, **kw)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)   # about 50 ms on the current stream
+    q = saf.saf_kv_append(k, v, kc, vc, pages, none, n_new, q=head[0], inv_freq=freq, stream=side)
+    o, lse = saf.saf_attn_paged(*head, x.max_len, **kw, stream=side)
+    torch.cuda.synchronize()
+    for got, ref in zip((q, o, lse), want):
+        assert torch.equal(got, ref)
+
+
 def test_counts_and_pages_out_of_bounds_are_reported(saf):
     # a bad entry reaches no memory: the keys of such a page are not seen, the counts are cut
     for dtype in ("bf16", "fp32"):
