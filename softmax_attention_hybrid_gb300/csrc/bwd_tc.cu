@@ -21,7 +21,8 @@
 // order: items of key/value heads that have an ordinary query head, in groups
 // of kSliceGroup (batch, key/value head) slices, each group by ascending kb
 // (longest first, and the group's dQ accumulator rows stay in L2), then the
-// items whose query heads are all frozen, by ascending kb.
+// items whose query heads are all frozen, by ascending kb. With a window, items that
+// are parts of key blocks with sinks (SinkParts) come before all of them.
 //
 // Per (kb, qb) tile of an ordinary head (key row j of the block):
 //   S^T  = K Q^T          (tcgen05, TMEM)      P^T = exp(S^T / sqrt(d) - lse)

@@ -12,11 +12,12 @@
 //   forward     dh_fwd_kernel        one CTA per (query block, slice): online
 //                                    softmax (ordinary) or Eq. 3 in its exact
 //                                    form (frozen), O in tensor memory
-//   backward    dh_rowvec_kernel     lse * log2(e) and D = dO . O per query block
+//   backward    dh_rowvec_kernel     -lse * log2(e) and D = dO . O per query block
 //               dh_bwd_kv_kernel     one CTA per (key block, slice): dV, dK
 //               dh_bwd_q_kernel      one CTA per (query block, slice): dQ
-// Each CTA: warps 0-3 own one tile row per thread (the TMEM lanes), warp 4 loads
-// with TMA, warp 5 owns tensor memory and issues the MMAs from one thread.
+// Each CTA: in the forward warps 0-3 own one tile row per thread (the TMEM lanes), warp 4
+// loads with TMA, warp 5 owns tensor memory and issues the MMAs from one thread; in the
+// backward passes warps 0-7 are the row warps (half of a row each), 8 and 9 the other two.
 // Every wait is bounded (mbar_wait): on expiry the CTA records the timeout in the
 // call's status word, every role gives up, and tensor memory is freed.
 #include <math.h>
