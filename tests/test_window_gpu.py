@@ -132,7 +132,7 @@ def test_grouped(saf, dtype, d, frozen, T, window, sinks):
 def test_blocks_of_sinks_in_parts(saf, dtype, d, H, Hkv, frozen, T, window, sinks):
     # every query sees the blocks of sinks: their gradients are summed in parts where heads share them
     flags = [1 if h in frozen else 0 for h in range(H)]
-    x, g = _inputs(dtype, 1, H, Hkv, T, d, frozen, seed=T + d)
+    x, g = _inputs(dtype, 2 if Hkv == 2 else 1, H, Hkv, T, d, frozen, seed=T + d)
     out = _run(saf, g, flags, window, sinks)
     _check(dtype, x, out, flags, window, sinks)
     again = _run(saf, g, flags, window, sinks)
@@ -222,6 +222,39 @@ def test_gradients_against_differences(saf):
         diff, want = (f[0] - f[1]) / 0.04, (out[grad].double() * dirn.double()).sum().item()
         scale = out[grad].double().norm().item()
         assert abs(diff - want) <= 2e-3 * scale, (n, diff, want)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+def test_parts_captured_and_beside_another_call(saf, dtype, d):
+    # a captured backward with blocks of sinks in parts, replayed while an eager call with its own
+    # workspace runs on another stream
+    frozen = [0, 0, 1, 0, 0, 0, 0, 0]
+    x, g = _inputs(dtype, 1, 8, 1, 1100, d, (2,), seed=31)
+    first = _run(saf, g, frozen, 100, 16)
+    ws = saf.alloc_workspace(1, 8, 1100, d, g["v"].dtype, True)
+    grads = [torch.empty_like(first[n]) for n in ("dq", "dk", "dv")]
+
+    def step():
+        saf.saf_attn_bwd_window(g["q"], g["k"], g["v"], first["o"], g["do"], first["lse"], g["a"], g["r"], frozen,
+                                100, 16, dq=grads[0], dk=grads[1], dv=grads[2], workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        for t in grads:
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        other = saf.saf_attn_bwd_window(g["q"], g["k"], g["v"], first["o"], g["do"], first["lse"], g["a"], g["r"],
+                                        frozen, 100, 16, stream=side)
+        torch.cuda.synchronize()
+        for dq, dk, dv in (grads, other):
+            assert torch.equal(dk, first["dk"]) and torch.equal(dv, first["dv"])
+            torch.testing.assert_close(dq, first["dq"], rtol=2.0 ** -7, atol=1e-5)
 
 
 def test_captured_and_replayed(saf):
