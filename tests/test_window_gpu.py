@@ -224,6 +224,52 @@ def test_gradients_against_differences(saf):
         assert abs(diff - want) <= 2e-3 * scale, (n, diff, want)
 
 
+@pytest.mark.parametrize("dtype,d,T", [("bf16", 64, 20011), ("bf16", 128, 20011), ("fp32", 64, 6007)])
+def test_a_long_sequence(saf, dtype, d, T):
+    """Every element against 64-bit sums over the visible keys alone (window + sinks of them a row).
+
+    Off by at most: the weights' rounding (u), the results' (u), D from the rounded o, dS' rounding (u),
+    and 1e-4 of the terms for fp32: a score of d products is off by d 2^-24 sum |q k| / sqrt(d), below
+    8e-5 here, which its weight takes over as a factor."""
+    window, sinks, H = 200, 7, 4
+    x, g = _inputs(dtype, 1, H, 1, T, d, (), seed=77)
+    out = _run(saf, g, [0] * H, window, sinks)
+    u = _bounds.HALF[dtype]
+    eps = 1e-4
+    i = torch.arange(T, device="cuda")[:, None]
+    recent = i - torch.arange(window, device="cuda")          # the window's keys
+    first = torch.arange(sinks, device="cuda").expand(T, -1)   # the sinks before it
+    idx = torch.cat([recent, first], 1)
+    seen = torch.cat([recent >= 0, first <= i - window], 1)
+    idx = idx.clamp(min=0)
+    f = {n: g[n].double()[0] for n in ("q", "k", "v", "do")}
+    k, v = f["k"][0], f["v"][0]
+    K, V = k[idx], v[idx]
+    dk, dv, tk, tv = (torch.zeros_like(k) for _ in range(4))
+    for h in range(H):
+        q, do = f["q"][h], f["do"][h]
+        S = torch.einsum("td,tjd->tj", q, K) / d ** 0.5
+        S = S.masked_fill(~seen, -float("inf"))
+        P = torch.softmax(S, 1)
+        o = torch.einsum("tj,tjd->td", P, V)
+        to = (u + eps) * torch.einsum("tj,tjd->td", P, V.abs()) + u * o.abs()
+        assert ((out["o"][0, h].double() - o).abs() <= to).all()
+        assert ((out["lse"][0, h].double() - torch.logsumexp(S, 1)).abs() <= 2e-4).all()
+        dP = torch.einsum("td,tjd->tj", do, V)
+        D = (do * o).sum(1, keepdim=True)
+        dS = P * (dP - D)
+        err = P * (u * (dP - D).abs() + (do.abs() * to).sum(1, keepdim=True) + eps * (dP.abs() + D.abs()))
+        dq = torch.einsum("tj,tjd->td", dS, K) / d ** 0.5
+        tq = torch.einsum("tj,tjd->td", err, K.abs()) / d ** 0.5 + u * dq.abs()
+        assert ((out["dq"][0, h].double() - dq).abs() <= tq).all()
+        flat = idx.flatten()
+        for total, w, y in ((dk, dS / d ** 0.5, q), (tk, err / d ** 0.5, q.abs()), (dv, P, do),
+                            (tv, (u + eps) * P, do.abs())):
+            total.index_add_(0, flat, (w[:, :, None] * y[:, None, :]).reshape(-1, d))
+    assert ((out["dk"][0, 0].double() - dk).abs() <= tk + u * dk.abs()).all()
+    assert ((out["dv"][0, 0].double() - dv).abs() <= tv + u * dv.abs()).all()
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
 def test_parts_captured_and_beside_another_call(saf, dtype, d):
     # a captured backward with blocks of sinks in parts, replayed while an eager call with its own
