@@ -355,6 +355,7 @@ template <typename E>
 __global__ void __launch_bounds__(256)
 bwd_delta_kernel(const E* __restrict__ o, const E* __restrict__ dO, float* __restrict__ delta, long long rows,
                  int d) {
+    grid_dep_wait();   // (the next launch follows when this one ends: see simt.cu)
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (row >= rows) return;
     const int lane = threadIdx.x & 31;
@@ -478,13 +479,13 @@ cudaError_t launch_bwd_delta(const LayerArgs& p, bool bf16, cudaStream_t s) {
     const long long rows = (long long)p.B * p.H * p.T;
     const unsigned blocks = (unsigned)((rows + 7) / 8);
     before_launch(SAF_KERNEL_BWD_DELTA, s);
-    if (bf16)
-        bwd_delta_kernel<__nv_bfloat16><<<blocks, 256, 0, s>>>(
-            (const __nv_bfloat16*)p.o, (const __nv_bfloat16*)p.dO, p.delta, rows, p.d);
-    else
-        bwd_delta_kernel<float><<<blocks, 256, 0, s>>>((const float*)p.o, (const float*)p.dO, p.delta, rows, p.d);
+    const cudaError_t e =
+        bf16 ? launch_ex(bwd_delta_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, s, true, 1,
+                         (const __nv_bfloat16*)p.o, (const __nv_bfloat16*)p.dO, p.delta, rows, p.d)
+             : launch_ex(bwd_delta_kernel<float>, dim3(blocks), dim3(256), 0, s, true, 1, (const float*)p.o,
+                         (const float*)p.dO, p.delta, rows, p.d);
     after_launch(SAF_KERNEL_BWD_DELTA, s);
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_bwd_prep(const LayerArgs& p, cudaStream_t s, bool frozen_part) {

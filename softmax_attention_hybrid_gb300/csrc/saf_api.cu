@@ -169,13 +169,13 @@ LayerArgs make_args(const void* q, const void* k, const void* v, const float* a,
 // for the frozen heads, finds max a, max r and (tensor-core path) writes the
 // padded a, r slices. The forward then computes log Z (and on the tensor-core
 // path 1 / Z'); the tensor-core backward reads log Z back from lse in its prep
-// kernel (launched by saf_attn_bwd), the fp32 backward recomputes it. The
-// tensor-core path launches every kernel with programmatic dependent launch.
+// kernel (launched by saf_attn_bwd), the fp32 backward recomputes it.
+// Every kernel of the layer's calls is launched with programmatic dependent launch.
 cudaError_t begin_call(const LayerArgs& p, const Common& c, bool backward, bool bf16, cudaStream_t s) {
     const int kid = backward ? SAF_KERNEL_PATTERN_PREP : SAF_KERNEL_LOGNORM;
     trace_begin(kid, s);
-    cudaError_t e = launch_call_init(p, bf16, bf16, s);
-    if (e == cudaSuccess && c.nfrozen > 0 && !(backward && bf16)) e = launch_lognorm(p, bf16, bf16, s);
+    cudaError_t e = launch_call_init(p, bf16, true, s);
+    if (e == cudaSuccess && c.nfrozen > 0 && !(backward && bf16)) e = launch_lognorm(p, bf16, true, s);
     after_launch(kid, s);
     return e;
 }
@@ -362,10 +362,10 @@ void use_state(LayerArgs& p, const void* state, int H, int T, bool bf16) {
 // and work counters) and nothing else: with no frozen head in its mask the init
 // kernel touches no frozen-pattern data, and its per-head flags go to the
 // workspace's own (unused) flag region.
-cudaError_t clear_call(const LayerArgs& ws_view, bool bf16, cudaStream_t s) {
+cudaError_t clear_call(const LayerArgs& ws_view, cudaStream_t s) {
     LayerArgs q = ws_view;
     memset(&q.mask, 0, sizeof(q.mask));
-    return launch_call_init(q, false, bf16, s);
+    return launch_call_init(q, false, true, s);
 }
 // A window that reaches every key is none: the call then runs the layer's own kernels.
 void set_window(LayerArgs& p, int window, int sinks) {
@@ -395,7 +395,7 @@ int saf_attn_fwd_prepared(const void* q, const void* k, const void* v, const flo
     p.d = d;
     p.out = o;
     p.lse_out = lse;
-    cudaError_t e = clear_call(p, bf16, s);
+    cudaError_t e = clear_call(p, s);
     use_state(p, state, H, T, bf16);
     if (e == cudaSuccess)
         e = !bf16 ? launch_simt_fwd(p, false, s) : d == kHeadDim ? launch_tc_fwd(p, s) : launch_dh_fwd(p, s);
@@ -429,7 +429,7 @@ int saf_attn_bwd_prepared(const void* q, const void* k, const void* v, const voi
     p.dq = dq;
     p.dk = dk;
     p.dv = dv;
-    cudaError_t e = clear_call(p, bf16, s);
+    cudaError_t e = clear_call(p, s);
     use_state(p, state, H, T, bf16);
     if (bf16 && d != kHeadDim) {
         if (e == cudaSuccess) e = launch_dh_bwd(p, s);
@@ -467,7 +467,7 @@ int saf_attn_fwd_window(const void* q, const void* k, const void* v, const float
     p.out = o;
     p.lse_out = lse;
     set_window(p, window, sinks);
-    cudaError_t e = state ? clear_call(p, bf16, s) : begin_call(p, c, false, bf16, s);
+    cudaError_t e = state ? clear_call(p, s) : begin_call(p, c, false, bf16, s);
     if (state) use_state(p, state, H, T, bf16);
     if (e == cudaSuccess)
         e = !bf16 ? launch_simt_fwd(p, false, s) : d == kHeadDim ? launch_tc_fwd(p, s) : launch_dh_fwd(p, s);
@@ -500,7 +500,7 @@ int saf_attn_bwd_window(const void* q, const void* k, const void* v, const void*
     p.dk = dk;
     p.dv = dv;
     set_window(p, window, sinks);
-    cudaError_t e = state ? clear_call(p, bf16, s) : begin_call(p, c, true, bf16, s);
+    cudaError_t e = state ? clear_call(p, s) : begin_call(p, c, true, bf16, s);
     if (state) use_state(p, state, H, T, bf16);
     if (bf16 && d != kHeadDim) {
         if (e == cudaSuccess) e = launch_dh_bwd(p, s);
