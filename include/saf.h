@@ -244,7 +244,10 @@ SAF_API int saf_attn_bwd_prepared(const void* q, const void* k, const void* v, c
  * (Eq. 3): it is a fixed matrix, cut by its own r.
  *
  * window >= 0, sinks >= 0 (else SAF_EINVAL); window = 0 or window >= T is the layer
- * without a window, with the same bits. state: NULL, or the prepared state of
+ * without a window, the forward with the same bits. The SAF_BF16 backward is nearer to
+ * the exact gradients than the layer's: at d = 64 it forms dS from unrounded weights,
+ * and where no row sees more than 16 keys, or T <= 32, it sums dO . o over the keys in
+ * fp32 (the rounding of o would be the largest error of dq and dk). state: NULL, or the prepared state of
  * saf_frozen_prepare for these a, r and frozen (as for the _prepared calls).
  * Everything else (shapes, workspace, empty calls, errors, outputs) is as for the
  * calls named above. Keys and values that the window hides from a row must still be

@@ -866,7 +866,8 @@ cudaError_t launch_tc_bwd(const LayerArgs& a, cudaStream_t s) {
     p.n_items = BHkv * p.nqb + extra;
 
     // (the dQ accumulator of the ordinary heads was zeroed by bwd_prep_kernel)
-    cudaError_t e;
+    cudaError_t e = launch_narrow_d(a, s);
+    if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -1153,6 +1153,7 @@ cudaError_t launch_dh_bwd(const LayerArgs& a, cudaStream_t s) {
     before_launch(SAF_KERNEL_BWD_DELTA, s);
     cudaError_t e = launch_ex(dh_rowvec_kernel, grid, dim3(128), 0, s, true, 1, p);
     after_launch(SAF_KERNEL_BWD_DELTA, s);
+    if (e == cudaSuccess) e = launch_narrow_d(a, s);
     if (e != cudaSuccess) return e;
     const int smem_kv = KvSmem::total + 1024, smem_q = QSmem::total + 1024;
     void (*kv_kernel)(DhParams) = a.window > 0 ? dh_bwd_kv_kernel<true> : dh_bwd_kv_kernel<false>;

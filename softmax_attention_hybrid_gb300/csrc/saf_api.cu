@@ -367,9 +367,10 @@ cudaError_t clear_call(const LayerArgs& ws_view, cudaStream_t s) {
     memset(&q.mask, 0, sizeof(q.mask));
     return launch_call_init(q, false, true, s);
 }
-// A window that reaches every key is none: the call then runs the layer's own kernels.
-void set_window(LayerArgs& p, int window, int sinks) {
-    p.window = window >= p.T ? 0 : window;
+// A window that reaches every key is none: the call then runs the layer's own kernels. keep: such a
+// window stays one of T keys (the windowed instances).
+void set_window(LayerArgs& p, int window, int sinks, bool keep) {
+    p.window = window > 0 && window < p.T ? window : keep ? p.T : 0;
     p.sinks = sinks < p.T ? sinks : p.T;
 }
 }  // namespace
@@ -466,7 +467,7 @@ int saf_attn_fwd_window(const void* q, const void* k, const void* v, const float
     p.d = d;
     p.out = o;
     p.lse_out = lse;
-    set_window(p, window, sinks);
+    set_window(p, window, sinks, false);
     cudaError_t e = state ? clear_call(p, s) : begin_call(p, c, false, bf16, s);
     if (state) use_state(p, state, H, T, bf16);
     if (e == cudaSuccess)
@@ -499,7 +500,9 @@ int saf_attn_bwd_window(const void* q, const void* k, const void* v, const void*
     p.dq = dq;
     p.dk = dk;
     p.dv = dv;
-    set_window(p, window, sinks);
+    p.exact_d = true;
+    // (the windowed instance of the d = 64 backward forms dS from the unrounded P)
+    set_window(p, window, sinks, bf16 && d == kHeadDim);
     cudaError_t e = state ? clear_call(p, s) : begin_call(p, c, true, bf16, s);
     if (state) use_state(p, state, H, T, bf16);
     if (bf16 && d != kHeadDim) {

@@ -146,8 +146,9 @@ struct LayerArgs {
     int Hkv;             // key/value heads: query head h reads key/value head h / (H / Hkv)
     int d;               // head dimension
     // ordinary heads: query i sees the keys j <= i with i - j < window or j < sinks
-    // (window 0: every j <= i); 0 < window < T otherwise. Frozen heads are not cut.
+    // (window 0: every j <= i); 0 < window <= T otherwise. Frozen heads are not cut.
     int window, sinks;
+    bool exact_d;        // bf16 backward: D summed over the keys where rows see few (narrow_d.cu)
     HeadMask mask;
     // diagnostic forward only (saf_attn_fwd_diag): a shorter limit for every bounded
     // wait (0: the default), and a producer that withholds every work item
@@ -216,6 +217,10 @@ struct SinkParts {
 SinkParts plan_sink_parts(const LayerArgs& a, int rows, int q_rows, int slots, int few, void* sums, size_t bytes);
 template <typename E>
 cudaError_t launch_join_parts(const LayerArgs& a, const SinkParts& sp, cudaStream_t s);
+
+// narrow_d.cu: D of rows that see few keys, over the one in rowvec (nothing where exact_d is off or
+// rows see many).
+cudaError_t launch_narrow_d(const LayerArgs& a, cudaStream_t s);
 
 // saf_api.cu: SAF_OK on an sm_103 device, else the error to return; a launch's result as a status.
 int check_device();
