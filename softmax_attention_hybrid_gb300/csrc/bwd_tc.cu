@@ -92,7 +92,7 @@ struct BwdParams {
     uint8_t act_kv[SAF_MAX_HEADS];     // the former
     uint8_t pas_kv[SAF_MAX_HEADS];     // the latter
     uint8_t gheads[SAF_MAX_HEADS];     // query heads of key/value head hk at [hk G, hk G + G), ordinary first
-    uint8_t gord[SAF_MAX_HEADS];       // ordinary query heads of key/value head hk
+    uint16_t gord[SAF_MAX_HEADS];      // ordinary query heads of key/value head hk (up to 256)
 };
 
 struct Smem {
@@ -853,7 +853,7 @@ cudaError_t launch_tc_bwd(const LayerArgs& a, cudaStream_t s) {
             }
         int nord = 0;
         for (int gi = 0; gi < p.G; ++gi) nord += head_frozen(a.mask, hk * p.G + gi) ? 0 : 1;
-        p.gord[hk] = (uint8_t)nord;
+        p.gord[hk] = (uint16_t)nord;
         if (nord > 0)
             p.act_kv[p.n_act++] = (uint8_t)hk;
         else

@@ -53,7 +53,7 @@ struct PagedArgs {
     float scale_log2;              // log2(e) / sqrt(d)
     HeadMask mask;
     uint8_t gheads[SAF_MAX_HEADS]; // query heads of key/value head hk at [hk G, hk G + G), ordinary first
-    uint8_t gord[SAF_MAX_HEADS];   // ordinary query heads of key/value head hk
+    uint16_t gord[SAF_MAX_HEADS];  // ordinary query heads of key/value head hk (up to 256)
 };
 
 struct PagedItem {

@@ -268,7 +268,7 @@ int paged(const void* q, const void* k_cache, const void* v_cache, const int32_t
                 p.mask.w[(hk * G + gi) >> 6] |= 1ull << ((hk * G + gi) & 63);
                 ++f;
             }
-        p.gord[hk] = (uint8_t)(G - f);
+        p.gord[hk] = (uint16_t)(G - f);
         nfrozen += f;
     }
     if (!v_cache || !page_table || !ctx || !o || !lse || (prefix_len > 0 && !prefix_pages)) return SAF_EINVAL;

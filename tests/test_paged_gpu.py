@@ -165,6 +165,19 @@ def test_shared_prefix(saf, dtype, d, prefix, page, H, Hkv, T, window, sinks):
         x.check(*x.call(saf, fz, window, sinks), fz, window, sinks)
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+@pytest.mark.parametrize("prefix", [0, 100])
+@pytest.mark.parametrize("frozen", [(), (0,), tuple(range(256))])
+def test_one_group_of_the_largest_head_count(saf, dtype, d, prefix, frozen):
+    # 256 query heads over one key/value head: a count of ordinary heads that takes more than 8 bits
+    flags = [h in frozen for h in range(256)]
+    x = Batch(dtype, 256, 1, 2, d, 16, (90, 37), (2, 1), prefix=prefix, seed=44)
+    none = {} if frozen else dict(a=None, r=None)
+    x.check(*x.call(saf, flags, **none), flags)
+    if not frozen:
+        x.check(*x.call(saf, flags, 20, 3, **none), flags, 20, 3)
+
+
 def test_many_sequences_share_a_prefix(saf):
     # more rows than one tile holds, in both kinds of head
     for dtype in ("bf16", "fp32"):

@@ -191,6 +191,22 @@ def test_largest_head_count(saf):
     _check("bf16", x, _run(saf, g, flags, 9, 2), flags, 9, 2)
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+@pytest.mark.parametrize("frozen", [(), (255,)])
+@pytest.mark.parametrize("window,sinks", [(9, 2), (0, 0)])
+def test_one_group_of_the_largest_head_count(saf, dtype, d, frozen, window, sinks):
+    # 256 query heads over one key/value head: a count of ordinary heads that takes more than 8 bits
+    flags = [h in frozen for h in range(256)]
+    x, g = _inputs(dtype, 1, 256, 1, 140, d, frozen, seed=43)
+    if not frozen:
+        g["a"] = g["r"] = None
+    _check(dtype, x, _run(saf, g, flags, window, sinks), flags, window, sinks)
+    if not window:
+        o, lse = saf.saf_attn_fwd_gqa(g["q"], g["k"], g["v"], g["a"], g["r"], flags)
+        dq, dk, dv = saf.saf_attn_bwd_gqa(g["q"], g["k"], g["v"], o, g["do"], lse, g["a"], g["r"], flags)
+        _check(dtype, x, {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}, flags, 0, 0)
+
+
 def test_nan_keys_outside_every_window(saf):
     # whole key blocks that no row of a query block sees are not visited: a NaN there stays there.
     # 640 tokens, window 100, no sinks: rows from 384 on see keys from 285 on, in blocks from 256 on
