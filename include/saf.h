@@ -151,7 +151,8 @@ SAF_API int saf_attn_fwd_noalloc(const void* q, const void* k, const void* v,
  *      same inputs; a, r, frozen as in saf_attn_fwd.
  * Out: dq, dk, dv [B,H,T,d] (dt). Ordinary heads: the gradient of Eqs. 5-7.
  *      Frozen heads: dv = W^T dO; dq and dk are written as exact zeros
- *      (§3.3, App. D.2).
+ *      (§3.3, App. D.2). dq may be the buffer of q or of dO, here and in every
+ *      other backward call: it is then written when nothing reads that any more.
  * Supported: d in {64, 96, 128} for both types. */
 SAF_API int saf_attn_bwd(const void* q, const void* k, const void* v, const void* o, const void* dO,
                  const float* lse, const float* a, const float* r, int ld_prior,
@@ -252,7 +253,8 @@ SAF_API int saf_attn_bwd_prepared(const void* q, const void* k, const void* v, c
  * Everything else (shapes, workspace, empty calls, errors, outputs) is as for the
  * calls named above. Keys and values that the window hides from a row must still be
  * finite where another row of the same 128-row block (64 in SAF_FP32) sees them.
- * The outputs overlap nothing else (dq also holds partial sums until the call ends). */
+ * The outputs overlap nothing else, but that dq may be the buffer of q or of dO (dq also holds
+ * partial sums until the call ends, of blocks of sinks that are then not split: slower). */
 SAF_API int saf_attn_fwd_window(const void* q, const void* k, const void* v, const float* a, const float* r,
                                 int ld_prior, const uint8_t* frozen, const void* state, int window, int sinks, int B,
                                 int H, int Hkv, int T, int d, saf_dtype_t dt, void* o, float* lse, void* workspace,

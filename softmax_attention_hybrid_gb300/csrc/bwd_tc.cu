@@ -859,8 +859,9 @@ cudaError_t launch_tc_bwd(const LayerArgs& a, cudaStream_t s) {
         else
             p.pas_kv[p.n_pas++] = (uint8_t)hk;
     }
-    // dq serves as scratch until dq_finish_kernel writes it
-    p.sp = plan_sink_parts(a, 128, 128, 152, 16, a.dq, (size_t)BH * a.T * kHeadDim * sizeof(__nv_bfloat16));
+    // dq serves as scratch until dq_finish_kernel writes it, unless it lies over what is read till then
+    const size_t scratch = dq_over_inputs(a, sizeof(__nv_bfloat16)) ? 0 : (size_t)BH * a.T * kHeadDim * sizeof(__nv_bfloat16);
+    p.sp = plan_sink_parts(a, 128, 128, 152, 16, a.dq, scratch);
     const int extra = a.B * p.n_act * p.sp.blocks * (p.sp.parts - 1);   // items that are parts, less the whole ones
     p.n_act_items = a.B * p.n_act * p.nqb + extra;
     p.n_items = BHkv * p.nqb + extra;

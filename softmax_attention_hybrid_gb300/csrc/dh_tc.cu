@@ -109,6 +109,7 @@ struct DhParams {
     int B, H, T, d, Tp, nqb;
     int Hkv, G;            // key/value heads; query head h reads key/value head h / G
     int window, sinks;     // ordinary heads (kWin kernels)
+    bool q_waits;          // query-block pass: dq lies over what the key-block pass reads
     float scale_log2;      // log2(e) / sqrt(d)
     float scale;           // 1 / sqrt(d)
     HeadMask mask;
@@ -850,7 +851,8 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
 // has begun, which each does after its own grid_dep_wait(), so the row vectors are there. Only
 // block 0 waits for that launch, at its end, so that this one's completion implies it.
 // (H32/Hkv8 d128, window 512, B2 T4096, forward and backward: 643 us with the wait at the
-// beginning, 595 us so; T1024: 152 and 132 us.)
+// beginning, 595 us so; T1024: 152 and 132 us.) Where dq lies over q or dO, which that launch
+// still reads, every block waits at its beginning.
 // TMEM: S of even blocks [0, 128) fp32 and of odd ones [384, 512), overwritten chunk by
 //       chunk with dS as bf16 pairs (chunk c at [32 c, 32 c + 16)) | dP [128, 256) |
 //       dQ [256, 384).
@@ -872,6 +874,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_q_kernel(const __grid_c
     __shared__ QBars bars;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_flag;
+    if (p.q_waits) grid_dep_wait();
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long u = (long long)blockIdx.y * p.nqb + blockIdx.x;
@@ -1149,6 +1152,7 @@ cudaError_t launch_dh_bwd(const LayerArgs& a, cudaStream_t s) {
     p.dq = (__nv_bfloat16*)a.dq;
     p.dk = (__nv_bfloat16*)a.dk;
     p.dv = (__nv_bfloat16*)a.dv;
+    p.q_waits = dq_over_inputs(a, sizeof(__nv_bfloat16));
     const dim3 grid((unsigned)p.nqb, (unsigned)(a.B * a.H));
     before_launch(SAF_KERNEL_BWD_DELTA, s);
     cudaError_t e = launch_ex(dh_rowvec_kernel, grid, dim3(128), 0, s, true, 1, p);

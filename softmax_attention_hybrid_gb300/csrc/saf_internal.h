@@ -7,6 +7,8 @@
 #include <stdint.h>
 #include <stddef.h>
 
+#include <initializer_list>
+
 #include "saf.h"
 
 namespace saf {
@@ -155,6 +157,16 @@ struct LayerArgs {
     unsigned long long diag_wait_ns;
     int diag_withhold;
 };
+
+// Whether dq lies over q or dO (a caller may pass dq = q or dq = dO). A row of q and dO is read by the
+// block that writes its row of dq, before it does, and by the key-block pass: dq must then hold nothing
+// until that pass has ended.
+inline bool dq_over_inputs(const LayerArgs& a, size_t element) {
+    const uintptr_t n = (uintptr_t)a.B * a.H * a.T * a.d * element, dq = (uintptr_t)a.dq;
+    for (const void* in : {a.q, a.dO})
+        if (in && dq < (uintptr_t)in + n && (uintptr_t)in < dq + n) return true;
+    return false;
+}
 
 // The key blocks that a run of query rows sees through a sliding window with sinks, for
 // blocks of `blk` keys: blocks [0, n_sink) hold sinks, blocks [lo, last] the window. Block

@@ -405,8 +405,8 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p, SinkParts
 // write zeros. beside: the pass reads nothing that the key-block pass before it writes, and runs
 // beside it; every block of that launch has begun, after its own grid_dep_wait(), before one of
 // this runs, and block (0, 0) waits for it at its end, so that this launch's completion implies
-// that one's. (Where both grids together leave every block an SM of its own, and dq does not hold
-// parts' sums.)
+// that one's. (Where both grids together leave every block an SM of its own, and dq neither holds
+// parts' sums nor lies over q or dO, which the key-block pass reads.)
 // ---------------------------------------------------------------------------
 template <typename E, int D, bool kWin, int RT>
 __global__ void __launch_bounds__(kThreads) bwd_q_kernel(LayerArgs p, bool beside) {
@@ -505,8 +505,10 @@ cudaError_t fwd_d(const LayerArgs& p, cudaStream_t s) {
 // parts: whether dq was used for the parts' sums
 template <typename E, int D, bool kWin, int RT>
 cudaError_t bwd_kv_d(const LayerArgs& p, cudaStream_t s, bool* parts) {
-    // dq serves as scratch until the query-block pass writes it; two blocks of threads an SM
-    const SinkParts sp = plan_sink_parts(p, 16 * RT, kB, 304, 4, p.dq, (size_t)p.B * p.H * p.T * p.d * sizeof(float));
+    // dq serves as scratch until the query-block pass writes it, unless it lies over what is read till
+    // then; two blocks of threads an SM
+    const size_t scratch = dq_over_inputs(p, sizeof(float)) ? 0 : (size_t)p.B * p.H * p.T * p.d * sizeof(float);
+    const SinkParts sp = plan_sink_parts(p, 16 * RT, kB, 304, 4, p.dq, scratch);
     const cudaError_t e = launch<D, RT>(bwd_kv_kernel<E, D, kWin, RT>, SAF_KERNEL_BWD_KV, 6, p, s, p.B * p.Hkv,
                                         sp.blocks * (sp.parts - 1), sp);
     *parts = sp.blocks > 0;
@@ -567,7 +569,7 @@ cudaError_t launch_simt_bwd(const LayerArgs& p, bool bf16, cudaStream_t s) {
         const int rows = p.window > 0 && few_blocks(p, slices) ? 16 : 64;
         return (long long)((p.T + rows - 1) / rows) * slices;
     };
-    const bool beside = !parts && blocks(p.B * p.Hkv) + blocks(p.B * p.H) <= kSms;
+    const bool beside = !parts && !dq_over_inputs(p, sizeof(float)) && blocks(p.B * p.Hkv) + blocks(p.B * p.H) <= kSms;
     if (bf16) return bwd_q_d<__nv_bfloat16, 64, false, 4>(p, s, false);
     if (p.window == 0) return bwd_q_f32<false, 4>(p, s, beside);
     return few_blocks(p, p.B * p.H) ? bwd_q_f32<true, 1>(p, s, beside) : bwd_q_f32<true, 4>(p, s, beside);

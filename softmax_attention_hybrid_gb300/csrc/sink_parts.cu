@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(256) join_parts_kernel(SinkParts sp, E* __rest
 }  // namespace
 
 // Each part gets about half of a slot's share of the launch's tiles (a frozen head's counted as half
-// an ordinary one's), at least `few`; at most 32 parts and what `bytes` hold.
+// an ordinary one's), at least `few`; at most 32 parts and what `bytes` hold (0: nothing is split).
 SinkParts plan_sink_parts(const LayerArgs& a, int rows, int q_rows, int slots, int few, void* sums, size_t bytes) {
     const SinkParts none{0, 1, rows, q_rows, nullptr};
     if (a.window == 0 || a.sinks == 0) return none;
