@@ -638,6 +638,10 @@ __global__ void __launch_bounds__(kThreadsBwd, 1) dh_bwd_kv_kernel(const __grid_
                     // tile i + 1 is an ordinary one
                     const bool next = M != 1 && i + 1 < ntiles && (M == 0 || !head_frozen(p.mask, h0 + gi));
                     if (frz) {
+                        // (no Q was loaded, but its phase is waited for: a later tile's wait on the barrier
+                        // could otherwise take the end of the phase before this one for its own)
+                        if (M == 2 && !(ok = mbar_wait(&bars.q_full[s], (i >> 1) & 1, abort, status, kStatusTimeout)))
+                            break;
                         if (next && !(ok = issue_s(i + 1))) break;
                         if (!(ok = mbar_wait(&bars.do_full[s], (i >> 1) & 1, abort, status, kStatusTimeout))) break;
                     }

@@ -207,6 +207,20 @@ def test_one_group_of_the_largest_head_count(saf, dtype, d, frozen, window, sink
         _check(dtype, x, {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}, flags, 0, 0)
 
 
+@pytest.mark.parametrize("d", [96, 128])
+@pytest.mark.parametrize("frozen", [(1, 2), (1, 2, 3, 4, 6), (0, 1, 2, 4, 5)])
+@pytest.mark.parametrize("T,window,sinks", [(100, 9, 2), (100, 0, 0), (300, 40, 0), (520, 130, 3)])
+def test_adjacent_frozen_heads_between_ordinary_ones(saf, d, frozen, T, window, sinks):
+    # short runs of a head's tiles: a stage's Q goes unused once or more before an ordinary head's is loaded
+    flags = [h in frozen for h in range(8)]
+    x, g = _inputs("bf16", 2, 8, 1, T, d, frozen, seed=T + d)
+    out = _run(saf, g, flags, window, sinks)
+    _check("bf16", x, out, flags, window, sinks)
+    for _ in range(8):
+        again = _run(saf, g, flags, window, sinks)
+        assert all(torch.equal(out[n], again[n]) for n in out)
+
+
 def test_nan_keys_outside_every_window(saf):
     # whole key blocks that no row of a query block sees are not visited: a NaN there stays there.
     # 640 tokens, window 100, no sinks: rows from 384 on see keys from 285 on, in blocks from 256 on
