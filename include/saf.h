@@ -251,8 +251,16 @@ SAF_API int saf_attn_bwd_prepared(const void* q, const void* k, const void* v, c
  * fp32 (the rounding of o would be the largest error of dq and dk). state: NULL, or the prepared state of
  * saf_frozen_prepare for these a, r and frozen (as for the _prepared calls).
  * Everything else (shapes, workspace, empty calls, errors, outputs) is as for the
- * calls named above. Keys and values that the window hides from a row must still be
- * finite where another row of the same 128-row block (64 in SAF_FP32) sees them.
+ * calls named above.
+ *
+ * What is hidden must still be finite in most places. A block of rows visits whole blocks of keys:
+ * those of the sinks, and those from its first row's first key to its last row (all up to there for a
+ * frozen head). A hidden pair of a visited block has weight 0, and 0 * NaN is NaN: a NaN or an
+ * infinity in the k or v of a key reaches o and dq of every row whose block visits the key's, and one
+ * in the q, o, dO or lse of a row reaches dk and dv of every key whose block the row's visits. What
+ * is not visited may be anything. Blocks hold 128 keys and 128 rows, 256 rows in the forward of
+ * SAF_BF16 at d = 64, and 64 of each in SAF_FP32.
+ *
  * The outputs overlap nothing else, but that dq may be the buffer of q or of dO (dq also holds
  * partial sums until the call ends, of blocks of sinks that are then not split: slower). */
 SAF_API int saf_attn_fwd_window(const void* q, const void* k, const void* v, const float* a, const float* r,

@@ -232,6 +232,59 @@ def test_nan_keys_outside_every_window(saf):
         assert torch.equal(o[:, :, 384:], clean[:, :, 384:])
 
 
+def _visits(T, window, sinks, rows, keys, key_blocks):
+    """Boolean [T]: rows whose block (of `rows`) visits one of the key blocks (of `keys`)."""
+    out = np.zeros(T, dtype=bool)
+    for r0 in range(0, T, rows):
+        first = max(0, r0 - window + 1) // keys
+        last = (min(T, r0 + rows) - 1) // keys
+        seen = set(range(first, last + 1)) | set(range(min(-(-sinks // keys), last + 1)))
+        out[r0:r0 + rows] = bool(seen & key_blocks)
+    return out
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 96), ("bf16", 128), ("fp32", 64), ("fp32", 128)])
+@pytest.mark.parametrize("T,window,sinks,p0,p1", [(256, 128, 0, 0, 1), (640, 100, 0, 128, 256), (640, 100, 0, 0, 128),
+                                                  (900, 130, 5, 200, 201), (1100, 60, 3, 500, 640)])
+def test_nan_reaches_the_rows_that_visit_its_block_only(saf, dtype, d, T, window, sinks, p0, p1):
+    # as the header states it: what a block of rows (256 in the d 64 forward) does not visit may be anything
+    x, g = _inputs(dtype, 1, 4, 2, T, d, (), seed=T + d)
+    clean = _run(saf, g, None, window, sinks)
+    keys, fwd = (128, 256 if d == 64 else 128) if dtype == "bf16" else (64, 64)
+    blocks = set(range(p0 // keys, (p1 - 1) // keys + 1))
+    for what in ("k", "v"):
+        y = dict(g)
+        y[what] = g[what].clone()
+        y[what][:, :, p0:p1] = float("nan")
+        o, lse = saf.saf_attn_fwd_window(y["q"], y["k"], y["v"], None, None, None, window, sinks)
+        free = torch.from_numpy(~_visits(T, window, sinks, fwd, keys, blocks)).cuda()
+        assert torch.equal(o[:, :, free], clean["o"][:, :, free])
+        assert torch.equal(lse[:, :, free], clean["lse"][:, :, free])
+        dq, dk, dv = saf.saf_attn_bwd_window(y["q"], y["k"], y["v"], clean["o"], y["do"], clean["lse"], None, None,
+                                             None, window, sinks)
+        free = torch.from_numpy(~_visits(T, window, sinks, keys, keys, blocks)).cuda()
+        if dtype == "bf16" and d == 64:   # key blocks' shares in any order, then one rounding
+            torch.testing.assert_close(dq[:, :, free], clean["dq"][:, :, free], rtol=2.0 ** -7, atol=1e-5)
+        else:
+            assert torch.equal(dq[:, :, free], clean["dq"][:, :, free])
+        other = torch.ones(T, dtype=torch.bool, device="cuda")
+        other[p0:p1] = False
+        for got, want in ((dk, clean["dk"]), (dv, clean["dv"])):
+            assert torch.equal(got[:, :, other], want[:, :, other])
+    for what in ("q", "do", "o", "lse"):   # of rows: the keys of the blocks that theirs visit
+        y = dict(g, o=clean["o"], lse=clean["lse"])
+        y[what] = y[what].clone()
+        y[what][:, :, p0:p1] = float("nan")
+        _, dk, dv = saf.saf_attn_bwd_window(y["q"], y["k"], y["v"], y["o"], y["do"], y["lse"], None, None, None, window,
+                                            sinks)
+        free = torch.ones(T, dtype=torch.bool, device="cuda")
+        for kb in range(-(-T // keys)):
+            visited = _visits(T, window, sinks, keys, keys, {kb})[p0:p1].any()
+            free[kb * keys:(kb + 1) * keys] = not visited
+        assert torch.equal(dk[:, :, free], clean["dk"][:, :, free])
+        assert torch.equal(dv[:, :, free], clean["dv"][:, :, free])
+
+
 @pytest.mark.parametrize("d", [64, 96, 128])
 @pytest.mark.parametrize("T,window,sinks", [(600, 2, 0), (601, 3, 0), (555, 3, 1), (4, 9, 0), (700, 15, 1), (32, 40, 0)])
 def test_rows_of_few_keys_lose_nothing_to_the_rounded_output(saf, d, T, window, sinks):
