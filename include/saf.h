@@ -302,8 +302,8 @@ SAF_API int saf_attn_bwd_window(const void* q, const void* k, const void* v, con
  *     w = (pos_base + ctx[b] + t) inv_freq[c],
  * for the rope_dim / 2 pairs of the first rope_dim elements (a multiple of 16, 0: no
  * rotation): elements (c, c + rope_dim / 2), or (2c, 2c + 1) when interleaved = 1. The
- * rest is copied. The angle is exact modulo a turn for every position, in fp32 from there
- * on; results are rounded once to dt.
+ * rest is copied. The angle modulo a turn is off by at most 2^-64 of a turn per position
+ * (frequencies as given, in double), and in fp32 from there on; results are rounded once to dt.
  * In:  q [B,H,T,d] (NULL: no q), k, v [B,Hkv,T,d] with element strides (sequence, head,
  *      token) strides[0..2], [3..5], [6..8] (HOST; NULL: contiguous), rows of d elements
  *      contiguous, every row 16-byte aligned: slices of one projection's output do.
@@ -313,7 +313,7 @@ SAF_API int saf_attn_bwd_window(const void* q, const void* k, const void* v, con
  * Out: q_out [B,H,T,d] contiguous (q_out = q only where q is contiguous; else they must
  *      not overlap), the slots of k_cache and v_cache. Rows without a token, and every
  *      other slot, stay as they were. Two tokens of one call must not share a slot.
- * T <= 2^21 and B T <= 2^30, else SAF_EINVAL.
+ * 0 <= pos_base <= 2^40, T <= 2^21 and B T <= 2^30, else SAF_EINVAL.
  * status: DEVICE uint32[2] (see above), for example a paged workspace; NULL: not recorded.
  *
  * saf_attn_paged

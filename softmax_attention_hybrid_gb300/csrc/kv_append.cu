@@ -6,8 +6,9 @@
 // pos * f_c with pos = pos_base + x:
 //     (y0, y1) = (x0 cos - x1 sin, x0 sin + x1 cos),
 // in fp32, rounded once to the cache's type. Angles of far positions keep their digits: the
-// host turns f_c into F_c = (f_c / 2 pi mod 1) 2^64, and pos * F_c in 64-bit integers is the
-// angle in turns, modulo one, to 2^-64 of a turn per position.
+// host turns f_c into F_c = (f_c / 2 pi mod 1) 2^64, rounded to an integer from two doubles, and
+// pos * F_c in 64-bit integers is the angle in turns, modulo one, off by pos 2^-64 at most: by
+// 2^-24 of a turn, what fp32 leaves anyway, at the last position that is taken, 2^40.
 //
 // Bound by memory: every element is read once and written once; the angles cost one
 // sincospif per pair and token for several heads. Thread = 16 elements of a row (8 pairs) of
@@ -193,6 +194,24 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 }
 bool aligned(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
+// x modulo 1 in units of 2^-64, to the nearest (x - trunc(x) and the scaling are exact).
+uint64_t turn_units(double x) {
+    const double y = (x - trunc(x)) * 18446744073709551616.0;
+    const uint64_t n = (uint64_t)nearbyint(fabs(y));
+    return y < 0.0 ? 0 - n : n;
+}
+
+// f / (2 pi) modulo 1 in units of 2^-64. 1 / (2 pi) is taken as a sum of two doubles (off by 2^-110)
+// and the product's rounding error as a third: a single double would leave f / (2 pi) with 53 bits,
+// 2^-56 for f near 1, which positions in the billions show.
+uint64_t frequency(double f) {
+    constexpr double hi = 0.15915494309189535, lo = -9.839338337591243e-18;
+    const double p = f * hi, e = fma(f, hi, -p) + f * lo;
+    return turn_units(p) + turn_units(e);
+}
+
+constexpr int64_t kLastBase = 1ll << 40;   // of pos_base
+
 }  // namespace
 }  // namespace saf
 
@@ -208,7 +227,7 @@ extern "C" int saf_kv_append(const void* q, const void* k, const void* v, const 
     if (!head_dim_supported(d, dt)) return SAF_EUNSUPPORTED;
     if (rope_dim < 0 || rope_dim > d || rope_dim % 16 != 0 || (rope_dim > 0 && !inv_freq)) return SAF_EINVAL;
     if (interleaved != 0 && interleaved != 1) return SAF_EINVAL;
-    if (pos_base < 0 || pos_base > (1ll << 62) || T > (1 << 21) || (long long)B * T > (1ll << 30)) return SAF_EINVAL;
+    if (pos_base < 0 || pos_base > kLastBase || T > (1 << 21) || (long long)B * T > (1ll << 30)) return SAF_EINVAL;
     if (B == 0 || T == 0) return SAF_OK;
     if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return SAF_EINVAL;
     if (num_pages < 1 || max_pages < 1) return SAF_EINVAL;
@@ -245,9 +264,7 @@ extern "C" int saf_kv_append(const void* q, const void* k, const void* v, const 
     }
     for (int c = 0; c < rope_dim / 2; ++c) {
         if (!isfinite(inv_freq[c])) return SAF_EINVAL;
-        const double turns = inv_freq[c] * 0.15915494309189533577;   // 1 / (2 pi)
-        const double frac = turns - floor(turns);                    // in [0, 1]
-        p.freq[c] = frac < 1.0 ? (uint64_t)(frac * 18446744073709551616.0) : 0;
+        p.freq[c] = frequency(inv_freq[c]);
     }
     int s = check_device();
     if (s != SAF_OK) return s;

@@ -4,6 +4,8 @@ the fp64 reference, with bounds from tests/_bounds.py.
 Whatever no token owns is poisoned: free pages, the slots behind a sequence's last token and the
 page table's entries behind it hold NaN, infinities or numbers that are no page.
 """
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -433,6 +435,42 @@ def test_append_at_far_positions(saf):
     got = _np(kc2)[int(table[0, 0]), 0, 3]
     # the frequencies are doubles: pos * 2^-53 * freq radians of them, and a few steps of fp32
     assert np.abs(got - want).max() <= (2.0 ** -20 + far * 2.0 ** -53) * 2 * np.abs(_np(k)).max()
+
+
+def _turns(f, pos):
+    """pos * f / (2 pi) modulo 1 as a float, pi from Machin's formula in integers of 400 bits."""
+    one = 1 << 400
+
+    def arctan(n):   # of 1 / n
+        term = total = one // n
+        k = 1
+        while term:
+            term = -term // (n * n)
+            k += 2
+            total += term // k
+        return total
+
+    two_pi = Fraction(8 * (4 * arctan(5) - arctan(239)), one)
+    return float(pos * Fraction(f) / two_pi % 1)
+
+
+@pytest.mark.parametrize("pos", [0, 1, 12345, 10 ** 9, 2 ** 36 + 7, 2 ** 40])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_angles_of_far_positions_are_exact(saf, pos, interleaved):
+    # a frequency is taken to 2^-64 of a turn; from the reduced angle on, x half turns in fp32 (2^-25 of a
+    # half turn) and its sine and cosine
+    d = 64
+    table, kc, vc, q, k, v = _append_case("fp32", 1, 1, 1, d, 16, (3,), (1,), 4, False)
+    freq = 10000.0 ** (-np.arange(0, d, 2) / d)
+    freq[1:6] = (-0.3, 3.7, 1e5, -1e-30, 2.0 ** -60)
+    kc2, vc2 = kc.cuda(), vc.cuda()
+    ctx = torch.tensor([3 if pos >= 3 else pos]).int().cuda()
+    saf.saf_kv_append(k, v, kc2, vc2, table.cuda(), ctx, inv_freq=freq, interleaved=interleaved,
+                      pos_base=pos - int(ctx))
+    angles = 2 * np.pi * np.array([_turns(f, pos) for f in freq])
+    want = so.rotate(_np(k)[0, 0], [1], angles, interleaved)[0]
+    got = _np(kc2)[int(table[0, 0]), 0, int(ctx)]
+    _append_check("fp32", got, want, np.abs(_np(k)).max(), 2 * np.pi * pos * 2.0 ** -64 + np.pi * 2.0 ** -25)
 
 
 def test_append_in_place_and_without_q(saf):

@@ -135,6 +135,12 @@ def test_append_refusals(saf):
     assert _append(lib, B=0, q=None, k=None, v=None) == saf.SAF_OK
 
 
+def test_append_takes_positions_whose_angles_keep_their_digits(saf):
+    lib = saf.library()
+    assert _append(lib, base=2 ** 40, B=0) == saf.SAF_OK
+    assert _append(lib, base=2 ** 40 + 1, B=0) == saf.SAF_EINVAL
+
+
 def test_binding_refusals_without_a_device(saf):
     x = torch.zeros(1, 4, 1, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
