@@ -287,8 +287,8 @@ SAF_API int saf_attn_bwd_window(const void* q, const void* k, const void* v, con
  *
  * What the device finds outside its bounds (a negative ctx, an n_new outside [0, T],
  * tokens past max_pages * page_size or max_len, a page outside [0, num_pages)) never
- * leads to an access: counts are cut to their bounds (a negative ctx: no tokens), keys
- * of such a page are not written and not seen, and the call ORs a bit into its status
+ * leads to an access: counts are cut to their bounds (a negative ctx: no tokens; what is
+ * cut off is no token, its rows of q_out and o are those of none), keys of such a page are not written and not seen, and the call ORs a bit into its status
  * words, which saf_device_status answers with SAF_EPAGE. The status words of these
  * calls stay as they are until the caller clears them; zero them when you make them.
  * Entries of page_table behind a sequence's last token, and behind the window of a call

@@ -97,8 +97,9 @@ __device__ __forceinline__ void append_token(const AppendArgs& p, int b, int t, 
     }
     if (t >= n) return;
     const long long slot = (long long)c + t;
-    int page = slot < room ? p.table[(size_t)b * p.max_pages + (slot >> p.page_log2)] : -1;
-    if (slot < room && (page < 0 || page >= p.num_pages)) {
+    if (slot >= room) return;   // no token: the count is cut to the room
+    int page = p.table[(size_t)b * p.max_pages + (slot >> p.page_log2)];
+    if (page < 0 || page >= p.num_pages) {
         if (group == 0 && u == 0 && p.status) atomicOr(p.status, kStatusPage);
         page = -1;
     }

@@ -511,6 +511,25 @@ def test_append_out_of_bounds_is_reported_and_writes_nothing(saf):
         assert sorted(zip(pages, slots)) == sorted([(int(table[1, 2]), 8), (int(table[1, 2]), 9)])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_append_cuts_counts_for_q_too(saf, dtype):
+    # tokens past the pages' room are none: their q rows stay as they were, like those behind n_new
+    table, kc, vc, q, k, v = _append_case(dtype, 2, 2, 3, 64, 16, (20, 40), (3, 3), 6, False)
+    room = table.shape[1] * 16
+    ctx = torch.tensor([room - 1, 40]).int().cuda()
+    q_out = torch.full(q.shape, 9.0, dtype=DT[dtype], device="cuda")
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    kc2, vc2 = kc.cuda(), vc.cuda()
+    saf.saf_kv_append(k, v, kc2, vc2, table.cuda(), ctx, torch.tensor([3, 7]).int().cuda(), q=q, q_out=q_out,
+                      inv_freq=[1.0] * 32, status=status)
+    assert saf.saf_device_status(status) == saf.SAF_EPAGE
+    assert (q_out[0, :, 1:] == 9.0).all() and (q_out[0, :, 0] != 9.0).any()
+    assert (q_out[1] != 9.0).any(dim=-1).all()   # 7 of 3 tokens: all three
+    pages, slots = np.nonzero((_np(vc2) != _np(vc)).any(axis=(1, 3)))
+    want = [(int(table[0, -1]), 15)] + [(int(table[1, 2]), x) for x in (8, 9, 10)]
+    assert sorted(zip(pages, slots)) == sorted(want)
+
+
 # ---------------------------------------------------------------------------
 # The calls together
 # ---------------------------------------------------------------------------
