@@ -384,6 +384,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 _I64x9 = ctypes.c_int64 * 9
+_2G = 2 ** 31   # ctypes would cut a larger int to its low 32 bits
+
+
+def _fits(top=_2G, **given):
+    """Raise for the first of the given numbers that a C integer of [-top, top) does not hold."""
+    for name, x in given.items():
+        if not -top <= x < top:
+            raise ValueError(f"{name} = {x} is out of range")
 
 
 def _at(t, idx, dtype):
@@ -466,6 +474,7 @@ def saf_attn_fwd_window(q, k, v, a, r, frozen, window, sinks=0, state=None, o=No
     if stream is not None:
         return _on(stream, v, lambda: saf_attn_fwd_window(q, k, v, a, r, frozen, window, sinks, state, o,
                    lse, workspace))
+    _fits(window=window, sinks=sinks)
     idx, dt = _device(v), v.dtype
     B, H, Hkv, T, d = _gqa_shape(q, v, frozen)
     full, rows = (B, H, T, d), (B, H, T)
@@ -492,6 +501,7 @@ def saf_attn_bwd_window(q, k, v, o, do, lse, a, r, frozen, window, sinks=0, stat
     if stream is not None:
         return _on(stream, v, lambda: saf_attn_bwd_window(q, k, v, o, do, lse, a, r, frozen, window, sinks,
                    state, dq, dk, dv, workspace))
+    _fits(window=window, sinks=sinks)
     idx, dt = _device(v), v.dtype
     B, H, Hkv, T, d = _gqa_shape(q, v, frozen)
     full, kv = (B, H, T, d), v.shape
@@ -544,6 +554,7 @@ def saf_kv_append(k, v, k_cache, v_cache, page_table, ctx, n_new=None, q=None, q
     if stream is not None:
         return _on(stream, v, lambda: saf_kv_append(k, v, k_cache, v_cache, page_table, ctx, n_new, q,
                    q_out, inv_freq, interleaved, pos_base, frozen, status))
+    _fits(2 ** 63, pos_base=pos_base)
     idx, dt, i32 = _device(v), v.dtype, torch.int32
     shape, caches = v.shape, v_cache.shape
     B, Hkv, T, d = shape
@@ -592,6 +603,8 @@ def saf_kv_append(k, v, k_cache, v_cache, page_table, ctx, n_new=None, q=None, q
 
 def saf_attn_paged_workspace_bytes(B, H, Hkv, T, d, max_len, dtype, prefix_len=0) -> int:
     dt = SAF_BF16 if dtype in (torch.bfloat16, SAF_BF16, "bf16") else SAF_FP32
+    if not all(-_2G <= n < _2G for n in (B, H, Hkv, T, d, max_len, prefix_len)):
+        return 0
     return int(_lib.saf_attn_paged_workspace_bytes(B, H, Hkv, T, d, int(max_len), int(prefix_len), dt))
 
 
@@ -605,6 +618,8 @@ def alloc_paged_workspace(B, H, Hkv, T, d, max_len, dtype, prefix_len=0, device=
 
 def _paged(where, fn, q, k_cache, v_cache, prefix, P, page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o,
            lse, workspace):
+    if not (-_2G <= window < _2G and -_2G <= sinks < _2G and -_2G <= max_len < _2G):
+        _fits(window=window, sinks=sinks, max_len=max_len)
     idx, dt = _device(q), q.dtype
     full, caches, table = q.shape, v_cache.shape, page_table.shape
     B, H, T, d = full
@@ -661,6 +676,7 @@ def saf_attn_paged_shared(q, k_cache, v_cache, prefix_pages, prefix_len, page_ta
     if stream is not None:
         return _on(stream, q, lambda: saf_attn_paged_shared(q, k_cache, v_cache, prefix_pages, prefix_len,
                    page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o, lse, workspace))
+    _fits(prefix_len=prefix_len)
     if prefix_pages is not None and prefix_pages.numel() * v_cache.shape[2] < prefix_len:
         raise ValueError("prefix_pages holds fewer pages than prefix_len tokens take")
     prefix = (_at(prefix_pages, _device(q), torch.int32), prefix_len)

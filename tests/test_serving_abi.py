@@ -149,3 +149,26 @@ def test_binding_refusals_without_a_device(saf):
         saf.saf_attn_fwd_window(x, x, x, None, None, None, 1)
     with pytest.raises(ValueError):
         saf.saf_kv_append(x, x, x, x, torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+def test_binding_refuses_numbers_past_a_c_integer(saf):
+    # cut to 32 bits, a window of 2^32 + 5 would be one of 5
+    x = torch.zeros(1, 4, 1, 64, dtype=torch.bfloat16)
+    table, ctx = torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    big = 2 ** 32 + 5
+    for n in ("window", "sinks"):
+        kw = {"window": 1, n: big}
+        with pytest.raises(ValueError, match=n):
+            saf.saf_attn_fwd_window(x, x, x, None, None, None, **kw)
+        with pytest.raises(ValueError, match=n):
+            saf.saf_attn_bwd_window(x, x, x, x, x, x, None, None, None, **kw)
+        with pytest.raises(ValueError, match=n):
+            saf.saf_attn_paged(x, x, x, table, ctx, 1, **kw)
+    with pytest.raises(ValueError, match="max_len"):
+        saf.saf_attn_paged(x, x, x, table, ctx, big)
+    with pytest.raises(ValueError, match="prefix_len"):
+        saf.saf_attn_paged_shared(x, x, x, None, big, table, ctx, 1)
+    with pytest.raises(ValueError, match="pos_base"):
+        saf.saf_kv_append(x, x, x, x, table, ctx, pos_base=2 ** 64 + 1)
+    assert saf.saf_attn_paged_workspace_bytes(2, 4, 2, 1, 64, big, "bf16") == 0
+    assert saf.saf_attn_paged_workspace_bytes(2, 4, 2, 1, 64, 128, "bf16", prefix_len=big) == 0
