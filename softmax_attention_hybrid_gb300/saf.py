@@ -340,6 +340,13 @@ def saf_frozen_prepare(a, r, frozen, T, dtype, state=None, stream=None):
     return state
 
 
+def _state(state, H, T, dt):
+    """The prepared state, which the kernels read by the sizes of the call."""
+    if state is not None and state.numel() * state.element_size() < _lib.saf_frozen_state_bytes(H, T, dt):
+        raise ValueError(f"the prepared state is shorter than one of {H} heads and {T} tokens")
+    return state
+
+
 def saf_attn_fwd_prepared(q, k, v, a, r, frozen, state, o=None, lse=None, workspace=None, stream=None):
     """Forward with the frozen-pattern data from a prepared state (grouped-query
     shapes allowed: k, v [B, Hkv, T, d]); returns (o, lse)."""
@@ -352,8 +359,8 @@ def saf_attn_fwd_prepared(q, k, v, a, r, frozen, state, o=None, lse=None, worksp
         workspace = alloc_workspace(B, H, T, d, v.dtype, False, v.device)
     ld = a.shape[1] if a is not None else T
     st = _lib.saf_attn_fwd_prepared(_ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(r), int(ld), _frozen_bytes(frozen, H),
-                                    _ptr(state), B, H, Hkv, T, d, _dt(v), _ptr(o), _ptr(lse), _ptr(workspace),
-                                    workspace.numel(), _stream(stream))
+                                    _ptr(_state(state, H, T, _dt(v))), B, H, Hkv, T, d, _dt(v), _ptr(o), _ptr(lse),
+                                    _ptr(workspace), workspace.numel(), _stream(stream))
     if st != SAF_OK:
         raise SafError(st, "saf_attn_fwd_prepared")
     return o, lse
@@ -370,8 +377,8 @@ def saf_attn_bwd_prepared(q, k, v, o, do, lse, a, r, frozen, state, dq=None, dk=
         workspace = alloc_workspace(B, H, T, d, v.dtype, True, v.device)
     ld = a.shape[1] if a is not None else T
     st = _lib.saf_attn_bwd_prepared(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(a), _ptr(r),
-                                    int(ld), _frozen_bytes(frozen, H), _ptr(state), B, H, Hkv, T, d, _dt(v),
-                                    _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(),
+                                    int(ld), _frozen_bytes(frozen, H), _ptr(_state(state, H, T, _dt(v))), B, H, Hkv,
+                                    T, d, _dt(v), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(),
                                     _stream(stream))
     if st != SAF_OK:
         raise SafError(st, "saf_attn_bwd_prepared")
@@ -489,8 +496,8 @@ def saf_attn_fwd_window(q, k, v, a, r, frozen, window, sinks=0, state=None, o=No
         workspace = alloc_workspace(B, H, T, d, dt, False, v.device)
     ap, rp, ld = _prior(a, r, H, idx, T)
     _run("saf_attn_fwd_window", _lib.saf_attn_fwd_window, idx, _at(q, idx, dt), _at(k, idx, dt),
-         _at(v, idx, dt), ap, rp, ld, _flags(frozen, H), _at(state, idx, torch.uint8), int(window), int(sinks), B, H, Hkv, T, d,
-         _dt(v), _at(o, idx, dt), _at(lse, idx, torch.float32), _at(workspace, idx, torch.uint8), workspace.numel())
+         _at(v, idx, dt), ap, rp, ld, _flags(frozen, H), _at(_state(state, H, T, _dt(v)), idx, torch.uint8), int(window),
+         int(sinks), B, H, Hkv, T, d, _dt(v), _at(o, idx, dt), _at(lse, idx, torch.float32), _at(workspace, idx, torch.uint8), workspace.numel())
     return o, lse
 
 
@@ -515,7 +522,8 @@ def saf_attn_bwd_window(q, k, v, o, do, lse, a, r, frozen, window, sinks=0, stat
     ap, rp, ld = _prior(a, r, H, idx, T)
     _run("saf_attn_bwd_window", _lib.saf_attn_bwd_window, idx, _at(q, idx, dt), _at(k, idx, dt),
          _at(v, idx, dt), _at(o, idx, dt), _at(do, idx, dt), _at(lse, idx, torch.float32), ap, rp, ld,
-         _flags(frozen, H), _at(state, idx, torch.uint8), int(window), int(sinks), B, H, Hkv, T, d, _dt(v), _at(dq, idx, dt),
+         _flags(frozen, H), _at(_state(state, H, T, _dt(v)), idx, torch.uint8), int(window), int(sinks), B, H, Hkv, T, d,
+         _dt(v), _at(dq, idx, dt),
          _at(dk, idx, dt), _at(dv, idx, dt), _at(workspace, idx, torch.uint8), workspace.numel())
     return dq, dk, dv
 

@@ -164,6 +164,25 @@ def test_prepared_state(saf):
         _check(dtype, x, b, frozen, 50, 3)
 
 
+def test_a_state_of_fewer_tokens_is_refused(saf):
+    # the kernels read it by the call's sizes
+    for dtype, d in (("bf16", 64), ("bf16", 128), ("fp32", 64)):
+        frozen = [0, 1, 0, 1]
+        _, g = _inputs(dtype, 1, 4, 4, 333, d, (1, 3), seed=9)
+        state = saf.saf_frozen_prepare(g["a"], g["r"], frozen, 200, g["v"].dtype)
+        lse = torch.zeros(1, 4, 333, device="cuda")
+        fwd, bwd = [g["q"], g["k"], g["v"]], [g["q"], g["k"], g["v"], g["q"], g["do"], lse]
+        tail = (g["a"], g["r"], frozen)
+        for call in (lambda: saf.saf_attn_fwd_window(*fwd, *tail, 50, 3, state=state),
+                     lambda: saf.saf_attn_bwd_window(*bwd, *tail, 50, 3, state=state),
+                     lambda: saf.saf_attn_fwd_prepared(*fwd, *tail, state),
+                     lambda: saf.saf_attn_bwd_prepared(*bwd, *tail, state)):
+            before = saf.saf_launch_count()
+            with pytest.raises(ValueError, match="state"):
+                call()
+            assert saf.saf_launch_count() == before
+
+
 def test_every_head_frozen_without_q_and_k(saf):
     for dtype, d in (("bf16", 64), ("bf16", 128), ("fp32", 96)):
         x, g = _inputs(dtype, 1, 4, 2, 300, d, (0, 1, 2, 3), seed=40)
