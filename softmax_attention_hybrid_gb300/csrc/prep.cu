@@ -351,18 +351,17 @@ lognorm_kernel(const float* __restrict__ a_all, const float* __restrict__ r_all,
 }
 
 // D_i = sum_c dO_ic * O_ic, one warp per row (head dimension d: d / 32 elements per lane).
-template <typename E>
 __global__ void __launch_bounds__(256)
-bwd_delta_kernel(const E* __restrict__ o, const E* __restrict__ dO, float* __restrict__ delta, long long rows,
+bwd_delta_kernel(const float* __restrict__ o, const float* __restrict__ dO, float* __restrict__ delta, long long rows,
                  int d) {
     grid_dep_wait();   // (the next launch follows when this one ends: see simt.cu)
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (row >= rows) return;
     const int lane = threadIdx.x & 31;
-    const E* po = o + row * d;
-    const E* pd = dO + row * d;
+    const float* po = o + row * d;
+    const float* pd = dO + row * d;
     float x = 0.f;
-    for (int c = lane; c < d; c += 32) x = fmaf(to_f(po[c]), to_f(pd[c]), x);
+    for (int c = lane; c < d; c += 32) x = fmaf(po[c], pd[c], x);
     for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
     if (lane == 0) delta[row] = x;
 }
@@ -475,15 +474,12 @@ cudaError_t launch_lognorm(const LayerArgs& p, bool pre, bool pdl, cudaStream_t 
                      (float*)nullptr, p.hflag, p.status);
 }
 
-cudaError_t launch_bwd_delta(const LayerArgs& p, bool bf16, cudaStream_t s) {
+cudaError_t launch_bwd_delta(const LayerArgs& p, cudaStream_t s) {
     const long long rows = (long long)p.B * p.H * p.T;
     const unsigned blocks = (unsigned)((rows + 7) / 8);
     before_launch(SAF_KERNEL_BWD_DELTA, s);
-    const cudaError_t e =
-        bf16 ? launch_ex(bwd_delta_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, s, true, 1,
-                         (const __nv_bfloat16*)p.o, (const __nv_bfloat16*)p.dO, p.delta, rows, p.d)
-             : launch_ex(bwd_delta_kernel<float>, dim3(blocks), dim3(256), 0, s, true, 1, (const float*)p.o,
-                         (const float*)p.dO, p.delta, rows, p.d);
+    const cudaError_t e = launch_ex(bwd_delta_kernel, dim3(blocks), dim3(256), 0, s, true, 1, (const float*)p.o,
+                                    (const float*)p.dO, p.delta, rows, p.d);
     after_launch(SAF_KERNEL_BWD_DELTA, s);
     return e;
 }

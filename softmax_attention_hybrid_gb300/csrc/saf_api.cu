@@ -230,7 +230,7 @@ int saf_attn_fwd_gqa(const void* q, const void* k, const void* v, const float* a
     const bool bf16 = dt == SAF_BF16;
     cudaError_t e = begin_call(p, c, false, bf16, s);
     if (e == cudaSuccess)
-        e = !bf16 ? launch_simt_fwd(p, false, s) : d == kHeadDim ? launch_tc_fwd(p, s) : launch_dh_fwd(p, s);
+        e = !bf16 ? launch_simt_fwd(p, s) : d == kHeadDim ? launch_tc_fwd(p, s) : launch_dh_fwd(p, s);
     return launch_status(e);
 }
 
@@ -296,8 +296,8 @@ int saf_attn_bwd_gqa(const void* q, const void* k, const void* v, const void* o,
         if (e == cudaSuccess) e = launch_bwd_prep(p, s);
         if (e == cudaSuccess) e = launch_tc_bwd(p, s);
     } else {
-        if (e == cudaSuccess && c.nfrozen < H) e = launch_bwd_delta(p, false, s);
-        if (e == cudaSuccess) e = launch_simt_bwd(p, false, s);
+        if (e == cudaSuccess && c.nfrozen < H) e = launch_bwd_delta(p, s);
+        if (e == cudaSuccess) e = launch_simt_bwd(p, s);
     }
     return launch_status(e);
 }
@@ -399,7 +399,7 @@ int saf_attn_fwd_prepared(const void* q, const void* k, const void* v, const flo
     cudaError_t e = clear_call(p, s);
     use_state(p, state, H, T, bf16);
     if (e == cudaSuccess)
-        e = !bf16 ? launch_simt_fwd(p, false, s) : d == kHeadDim ? launch_tc_fwd(p, s) : launch_dh_fwd(p, s);
+        e = !bf16 ? launch_simt_fwd(p, s) : d == kHeadDim ? launch_tc_fwd(p, s) : launch_dh_fwd(p, s);
     return launch_status(e);
 }
 
@@ -438,8 +438,8 @@ int saf_attn_bwd_prepared(const void* q, const void* k, const void* v, const voi
         if (e == cudaSuccess) e = launch_bwd_prep(p, s, false);
         if (e == cudaSuccess) e = launch_tc_bwd(p, s);
     } else {
-        if (e == cudaSuccess && c.nfrozen < H) e = launch_bwd_delta(p, false, s);
-        if (e == cudaSuccess) e = launch_simt_bwd(p, false, s);
+        if (e == cudaSuccess && c.nfrozen < H) e = launch_bwd_delta(p, s);
+        if (e == cudaSuccess) e = launch_simt_bwd(p, s);
     }
     return launch_status(e);
 }
@@ -471,7 +471,7 @@ int saf_attn_fwd_window(const void* q, const void* k, const void* v, const float
     cudaError_t e = state ? clear_call(p, s) : begin_call(p, c, false, bf16, s);
     if (state) use_state(p, state, H, T, bf16);
     if (e == cudaSuccess)
-        e = !bf16 ? launch_simt_fwd(p, false, s) : d == kHeadDim ? launch_tc_fwd(p, s) : launch_dh_fwd(p, s);
+        e = !bf16 ? launch_simt_fwd(p, s) : d == kHeadDim ? launch_tc_fwd(p, s) : launch_dh_fwd(p, s);
     return launch_status(e);
 }
 
@@ -511,8 +511,8 @@ int saf_attn_bwd_window(const void* q, const void* k, const void* v, const void*
         if (e == cudaSuccess) e = launch_bwd_prep(p, s, !state);
         if (e == cudaSuccess) e = launch_tc_bwd(p, s);
     } else {
-        if (e == cudaSuccess && c.nfrozen < H) e = launch_bwd_delta(p, false, s);
-        if (e == cudaSuccess) e = launch_simt_bwd(p, false, s);
+        if (e == cudaSuccess && c.nfrozen < H) e = launch_bwd_delta(p, s);
+        if (e == cudaSuccess) e = launch_simt_bwd(p, s);
     }
     return launch_status(e);
 }

@@ -262,7 +262,7 @@ cudaError_t launch_lognorm(const LayerArgs& p, bool pre, bool pdl, cudaStream_t 
 // frozen_part: also 1 / Z' and the exact-form flags of the frozen heads, from the
 // log Z rows of lse (false when a prepared frozen-pattern state already holds them).
 cudaError_t launch_bwd_prep(const LayerArgs& p, cudaStream_t s, bool frozen_part = true);
-cudaError_t launch_bwd_delta(const LayerArgs& p, bool bf16, cudaStream_t s);
+cudaError_t launch_bwd_delta(const LayerArgs& p, cudaStream_t s);
 
 // fwd_tc.cu: tensor-core forward (bf16)
 cudaError_t launch_tc_fwd(const LayerArgs& p, cudaStream_t s);
@@ -276,8 +276,8 @@ cudaError_t launch_tc_bwd(const LayerArgs& p, cudaStream_t s);
 cudaError_t launch_dh_fwd(const LayerArgs& p, cudaStream_t s);
 cudaError_t launch_dh_bwd(const LayerArgs& p, cudaStream_t s);
 
-// simt.cu: fp32-arithmetic path (any dtype), used for SAF_FP32
-cudaError_t launch_simt_fwd(const LayerArgs& p, bool bf16, cudaStream_t s);
-cudaError_t launch_simt_bwd(const LayerArgs& p, bool bf16, cudaStream_t s);
+// simt.cu: the CUDA-core path of SAF_FP32
+cudaError_t launch_simt_fwd(const LayerArgs& p, cudaStream_t s);
+cudaError_t launch_simt_bwd(const LayerArgs& p, cudaStream_t s);
 
 }  // namespace saf

@@ -42,18 +42,14 @@ template <int D>
 __host__ __device__ constexpr int tile_floats() { return kB * ((D > kB ? D : kB) + 4); }
 
 // rows r0 .. r0 + R - 1 of a [T, D] slice into shared memory, row stride D + 4
-template <int D, int R, typename E>
-__device__ __forceinline__ void load_tile(float* s, const E* g, int r0, int T) {
+template <int D, int R>
+__device__ __forceinline__ void load_tile(float* s, const float* g, int r0, int T) {
 #pragma unroll 4
     for (int e = 4 * threadIdx.x; e < R * D; e += 4 * kThreads) {
         const int rr = e / D, c = e - rr * D;
         const int row = r0 + rr;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (row < T) {
-            const E* p = g + (size_t)row * D + c;
-            if constexpr (sizeof(E) == 4) x = *reinterpret_cast<const float4*>(p);
-            else x = make_float4(to_f(p[0]), to_f(p[1]), to_f(p[2]), to_f(p[3]));
-        }
+        if (row < T) x = *reinterpret_cast<const float4*>(g + (size_t)row * D + c);
         *reinterpret_cast<float4*>(s + rr * (D + 4) + c) = x;
     }
 }
@@ -105,12 +101,11 @@ struct Cols {
             }
         }
     }
-    template <typename E>
-    static __device__ __forceinline__ void store(E* row, const float* x, float f, int tx) {
+    static __device__ __forceinline__ void store(float* row, const float* x, float f, int tx) {
 #pragma unroll
         for (int u = 0; u < NV; ++u)
 #pragma unroll
-            for (int e = 0; e < VW; ++e) from_f(row + at(u, tx) + e, x[VW * u + e] * f);
+            for (int e = 0; e < VW; ++e) row[at(u, tx) + e] = x[VW * u + e] * f;
     }
 };
 
@@ -161,7 +156,7 @@ __device__ __forceinline__ void begin_block() {
 // ---------------------------------------------------------------------------
 // Forward. Grid (ceil(T / 16 RT), B*H).
 // ---------------------------------------------------------------------------
-template <typename E, int D, bool kWin, int RT>
+template <int D, bool kWin, int RT>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
     begin_block();
     extern __shared__ float sm[];
@@ -177,9 +172,9 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
     const size_t base = (size_t)bh * T * D;
     // key/value slice of this query head (grouped-query layout: head h reads h / (H / Hkv))
     const size_t kvbase = ((size_t)(bh / p.H) * p.Hkv + h / (p.H / p.Hkv)) * T * D;
-    const E* q = (const E*)p.q + base;
-    const E* k = (const E*)p.k + kvbase;
-    const E* v = (const E*)p.v + kvbase;
+    const float* q = (const float*)p.q + base;
+    const float* k = (const float*)p.k + kvbase;
+    const float* v = (const float*)p.v + kvbase;
     const float* a = p.a + (size_t)h * p.ld_prior;
     const float* r = p.r + (size_t)h * p.ld_prior;
     const int q0 = qb * kR;
@@ -250,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
         tile_sums<D, RT>(Ps, Vs, ty, tx, acc);
     }
 
-    E* o = (E*)p.out + base;
+    float* o = (float*)p.out + base;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         const int row = q0 + ty * RT + i;
@@ -269,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) fwd_kernel(LayerArgs p) {
 // the key blocks that hold sinks (SinkParts), each of which has a run of the query blocks
 // (H8/Hkv2 d64, T4096, window 512, 16 sinks, forward and backward: 2979 us whole, 1047 us so).
 // ---------------------------------------------------------------------------
-template <typename E, int D, bool kWin, int RT>
+template <int D, bool kWin, int RT>
 __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p, SinkParts sp) {
     begin_block();
     extern __shared__ float sm[];
@@ -296,8 +291,8 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p, SinkParts
     if (split) run = sp.range(kb, T, part);
     if (in_parts && (split ? run.n == 0 : part > 0)) return;   // (a frozen group's block is not split)
     const size_t kvbase = (size_t)bkv * T * D;
-    const E* k = (const E*)p.k + kvbase;
-    const E* v = (const E*)p.v + kvbase;
+    const float* k = (const float*)p.k + kvbase;
+    const float* v = (const float*)p.v + kvbase;
     const int k0 = kb * kR;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const float scale = 1.f / sqrtf((float)D);
@@ -314,8 +309,8 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p, SinkParts
     const int h = hk * G + gi, bh = b * p.H + h;
     const bool frozen = head_frozen(p.mask, h);
     const size_t base = (size_t)bh * T * D;
-    const E* q = (const E*)p.q + base;
-    const E* dO = (const E*)p.dO + base;
+    const float* q = (const float*)p.q + base;
+    const float* dO = (const float*)p.dO + base;
     const float* a = p.a + (size_t)h * p.ld_prior;
     const float* r = p.r + (size_t)h * p.ld_prior;
     // query blocks from the one of my first key on; with a window to the one of the last query that
@@ -386,8 +381,8 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p, SinkParts
             return;
         }
     }
-    E* dvp = (E*)p.dv + kvbase;
-    E* dkp = (E*)p.dk + kvbase;
+    float* dvp = (float*)p.dv + kvbase;
+    float* dkp = (float*)p.dk + kvbase;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         const int key = k0 + ty * RT + i;
@@ -408,7 +403,7 @@ __global__ void __launch_bounds__(kThreads) bwd_kv_kernel(LayerArgs p, SinkParts
 // that one's. (Where both grids together leave every block an SM of its own, and dq neither holds
 // parts' sums nor lies over q or dO, which the key-block pass reads.)
 // ---------------------------------------------------------------------------
-template <typename E, int D, bool kWin, int RT>
+template <int D, bool kWin, int RT>
 __global__ void __launch_bounds__(kThreads) bwd_q_kernel(LayerArgs p, bool beside) {
     if (!beside) grid_dep_wait();
     if (one_block_an_sm()) grid_dep_launch();
@@ -424,22 +419,22 @@ __global__ void __launch_bounds__(kThreads) bwd_q_kernel(LayerArgs p, bool besid
     const int qb = blockIdx.x, bh = blockIdx.y, h = bh % p.H;
     const bool frozen = head_frozen(p.mask, h);
     const size_t base = (size_t)bh * T * D;
-    E* dq = (E*)p.dq + base;
+    float* dq = (float*)p.dq + base;
     const int q0 = qb * kR;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     if (frozen) {
         for (int e = tid; e < kR * D; e += kThreads) {
             const int row = q0 + e / D;
-            if (row < T) from_f(dq + (size_t)row * D + e % D, 0.f);
+            if (row < T) dq[(size_t)row * D + e % D] = 0.f;
         }
         if (beside && blockIdx.x == 0 && blockIdx.y == 0) grid_dep_wait();
         return;
     }
     const size_t kvbase = ((size_t)(bh / p.H) * p.Hkv + h / (p.H / p.Hkv)) * T * D;
-    const E* q = (const E*)p.q + base;
-    const E* k = (const E*)p.k + kvbase;
-    const E* v = (const E*)p.v + kvbase;
-    const E* dO = (const E*)p.dO + base;
+    const float* q = (const float*)p.q + base;
+    const float* k = (const float*)p.k + kvbase;
+    const float* v = (const float*)p.v + kvbase;
+    const float* dO = (const float*)p.dO + base;
     const float scale = 1.f / sqrtf((float)D);
 
     load_tile<D, kR>(Qs, q, q0, T);
@@ -497,53 +492,53 @@ cudaError_t launch(K kernel, int id, int tiles, const LayerArgs& p, cudaStream_t
     return e;
 }
 
-template <typename E, int D, bool kWin, int RT>
+template <int D, bool kWin, int RT>
 cudaError_t fwd_d(const LayerArgs& p, cudaStream_t s) {
-    return launch<D, RT>(fwd_kernel<E, D, kWin, RT>, SAF_KERNEL_FWD, 4, p, s, p.B * p.H, 0);
+    return launch<D, RT>(fwd_kernel<D, kWin, RT>, SAF_KERNEL_FWD, 4, p, s, p.B * p.H, 0);
 }
 
 // parts: whether dq was used for the parts' sums
-template <typename E, int D, bool kWin, int RT>
+template <int D, bool kWin, int RT>
 cudaError_t bwd_kv_d(const LayerArgs& p, cudaStream_t s, bool* parts) {
     // dq serves as scratch until the query-block pass writes it, unless it lies over what is read till
     // then; two blocks of threads an SM
     const size_t scratch = dq_over_inputs(p, sizeof(float)) ? 0 : (size_t)p.B * p.H * p.T * p.d * sizeof(float);
     const SinkParts sp = plan_sink_parts(p, 16 * RT, kB, 304, 4, p.dq, scratch);
-    const cudaError_t e = launch<D, RT>(bwd_kv_kernel<E, D, kWin, RT>, SAF_KERNEL_BWD_KV, 6, p, s, p.B * p.Hkv,
+    const cudaError_t e = launch<D, RT>(bwd_kv_kernel<D, kWin, RT>, SAF_KERNEL_BWD_KV, 6, p, s, p.B * p.Hkv,
                                         sp.blocks * (sp.parts - 1), sp);
     *parts = sp.blocks > 0;
     return e == cudaSuccess && *parts ? launch_join_parts<float>(p, sp, s) : e;
 }
 
-template <typename E, int D, bool kWin, int RT>
+template <int D, bool kWin, int RT>
 cudaError_t bwd_q_d(const LayerArgs& p, cudaStream_t s, bool beside) {
-    return launch<D, RT>(bwd_q_kernel<E, D, kWin, RT>, SAF_KERNEL_BWD_Q, 5, p, s, p.B * p.H, 0, beside);
+    return launch<D, RT>(bwd_q_kernel<D, kWin, RT>, SAF_KERNEL_BWD_Q, 5, p, s, p.B * p.H, 0, beside);
 }
 
 template <bool kWin, int RT>
 cudaError_t fwd_f32(const LayerArgs& p, cudaStream_t s) {
     switch (p.d) {
-        case 96: return fwd_d<float, 96, kWin, RT>(p, s);
-        case 128: return fwd_d<float, 128, kWin, RT>(p, s);
-        default: return fwd_d<float, 64, kWin, RT>(p, s);
+        case 96: return fwd_d<96, kWin, RT>(p, s);
+        case 128: return fwd_d<128, kWin, RT>(p, s);
+        default: return fwd_d<64, kWin, RT>(p, s);
     }
 }
 
 template <bool kWin, int RT>
 cudaError_t bwd_kv_f32(const LayerArgs& p, cudaStream_t s, bool* parts) {
     switch (p.d) {
-        case 96: return bwd_kv_d<float, 96, kWin, RT>(p, s, parts);
-        case 128: return bwd_kv_d<float, 128, kWin, RT>(p, s, parts);
-        default: return bwd_kv_d<float, 64, kWin, RT>(p, s, parts);
+        case 96: return bwd_kv_d<96, kWin, RT>(p, s, parts);
+        case 128: return bwd_kv_d<128, kWin, RT>(p, s, parts);
+        default: return bwd_kv_d<64, kWin, RT>(p, s, parts);
     }
 }
 
 template <bool kWin, int RT>
 cudaError_t bwd_q_f32(const LayerArgs& p, cudaStream_t s, bool beside) {
     switch (p.d) {
-        case 96: return bwd_q_d<float, 96, kWin, RT>(p, s, beside);
-        case 128: return bwd_q_d<float, 128, kWin, RT>(p, s, beside);
-        default: return bwd_q_d<float, 64, kWin, RT>(p, s, beside);
+        case 96: return bwd_q_d<96, kWin, RT>(p, s, beside);
+        case 128: return bwd_q_d<128, kWin, RT>(p, s, beside);
+        default: return bwd_q_d<64, kWin, RT>(p, s, beside);
     }
 }
 
@@ -552,17 +547,15 @@ bool few_blocks(const LayerArgs& p, int slices) { return (long long)((p.T + kB -
 
 }  // namespace
 
-cudaError_t launch_simt_fwd(const LayerArgs& p, bool bf16, cudaStream_t s) {
-    if (bf16) return fwd_d<__nv_bfloat16, 64, false, 4>(p, s);
+cudaError_t launch_simt_fwd(const LayerArgs& p, cudaStream_t s) {
     if (p.window == 0) return fwd_f32<false, 4>(p, s);
     return few_blocks(p, p.B * p.H) ? fwd_f32<true, 1>(p, s) : fwd_f32<true, 4>(p, s);
 }
 
-cudaError_t launch_simt_bwd(const LayerArgs& p, bool bf16, cudaStream_t s) {
+cudaError_t launch_simt_bwd(const LayerArgs& p, cudaStream_t s) {
     cudaError_t e;
     bool parts = false;
-    if (bf16) e = bwd_kv_d<__nv_bfloat16, 64, false, 4>(p, s, &parts);
-    else if (p.window == 0) e = bwd_kv_f32<false, 4>(p, s, &parts);
+    if (p.window == 0) e = bwd_kv_f32<false, 4>(p, s, &parts);
     else e = few_blocks(p, p.B * p.Hkv) ? bwd_kv_f32<true, 1>(p, s, &parts) : bwd_kv_f32<true, 4>(p, s, &parts);
     if (e != cudaSuccess) return e;
     const auto blocks = [&](int slices) {
@@ -570,7 +563,6 @@ cudaError_t launch_simt_bwd(const LayerArgs& p, bool bf16, cudaStream_t s) {
         return (long long)((p.T + rows - 1) / rows) * slices;
     };
     const bool beside = !parts && !dq_over_inputs(p, sizeof(float)) && blocks(p.B * p.Hkv) + blocks(p.B * p.H) <= kSms;
-    if (bf16) return bwd_q_d<__nv_bfloat16, 64, false, 4>(p, s, false);
     if (p.window == 0) return bwd_q_f32<false, 4>(p, s, beside);
     return few_blocks(p, p.B * p.H) ? bwd_q_f32<true, 1>(p, s, beside) : bwd_q_f32<true, 4>(p, s, beside);
 }
