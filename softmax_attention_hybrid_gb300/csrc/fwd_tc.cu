@@ -155,6 +155,7 @@ struct Barriers {
     uint64_t s_full[2], s_empty[2], p_full[2], o_done[2];
     uint64_t w_full[2][2];   // frozen items: W buffer b of tile g is written (4 arrivals)
     uint64_t w_done[2][2];   // frozen items: P V of tile g that read W buffer b has completed
+    uint64_t frz_go[2];      // a frozen item of tile g: every K/V stage before its first has been filled
     uint64_t item_full[kRing], item_empty[kRing];   // work-item ring (10 consumer warps)
     uint64_t mma_idle[2];   // every MMA issuer g issued has completed (before TMEM is freed)
 };
@@ -204,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
             mbar_init(&bars.w_done[g][1], 1);
             mbar_init(&bars.w_full[g][0], 4);
             mbar_init(&bars.w_full[g][1], 4);
+            mbar_init(&bars.frz_go[g], 1);
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&bars.item_full[i], 1);
@@ -340,6 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
                     q_full_bits ^= 1u << qs;
                     d_q = sdesc_sw128(smem_u32(sm + SmemLayout::q + qs * SmemLayout::q_slot_bytes) + g * kTileBytes, 16,
                                       1024);
+                } else if (ng > 0 && lane == 0) {
+                    mbar_arrive(&bars.frz_go[g]);
                 }
                 // stage index of block j is (stage + j) mod kStages
                 auto stage_of = [&](int j) { return (stage + j) % kStages; };
@@ -425,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
         const int g = warp >> 2;               // 0 or 1
         const int r = threadIdx.x & 127;       // row within the tile = TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 * g;
-        uint32_t s_full_ph = 0, o_done_ph = 0;
+        uint32_t s_full_ph = 0, o_done_ph = 0, frz_go_ph = 0;
         uint32_t w_done_ph[2] = {0, 0};
         bool w_pend[2] = {false, false};   // a P V that read W buffer b may not have been waited for
         auto wait_w = [&](int b) -> bool {
@@ -579,6 +583,12 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_tc_kernel(const __grid_consta
             } else {
                 // frozen item: the exact or the factorised form of Eq. 3 (per-head flag)
                 const bool exact = (p.hflag[it.h] & 2u) != 0;
+                // A wait on kv_full takes the end of any phase of its parity for its own, and this
+                // group has not seen the stages of the blocks that it did not work on (an ordinary
+                // item's, an item's that has no tile for it, tile 0's last one): one of the last kStages
+                // may still be on its way. The issuer has waited for all of them, in order.
+                if (!(ok = mbar_wait(&bars.frz_go[g], frz_go_ph, abort, status, kStatusTimeout, p.wait_ns))) break;
+                frz_go_ph ^= 1;
                 const float lz2 = row < p.T ? p.lz[(size_t)it.h * p.T + row] * kLog2e : INFINITY;   // log2 Z(i)
                 for (int j = 0; j < nblk && ok; ++j) {
                     // Frozen tile of Eq. 3 from the key block's a values and the band of r values

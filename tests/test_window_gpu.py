@@ -226,6 +226,32 @@ def test_one_group_of_the_largest_head_count(saf, dtype, d, frozen, window, sink
         _check(dtype, x, {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}, flags, 0, 0)
 
 
+@pytest.mark.parametrize("B,H,Hkv,frozen,T,window,sinks", [
+    (8, 12, 12, (11,), 1590, 16, 1), (8, 16, 4, (15,), 2687, 96, 1), (3, 32, 32, tuple(range(3, 32, 4)), 1367, 2, 16),
+    (8, 6, 2, (1, 3, 5), 3635, 8, 16), (8, 16, 16, (15,), 870, 62, 4), (8, 16, 16, (0, 5, 15), 870, 0, 0),
+    (16, 12, 12, (0, 3, 6, 9, 11), 385, 0, 0)])
+def test_frozen_heads_after_items_of_one_tile(saf, B, H, Hkv, frozen, T, window, sinks):
+    # an odd number of query blocks: one of each pair's two row groups has nothing to do in a slice's
+    # first item, and may come to a frozen item while that one's keys are still on their way
+    flags = [h in frozen for h in range(H)]
+    _, g = _inputs("bf16", B, H, Hkv, T, 64, frozen, seed=T)
+    call = lambda: saf.saf_attn_fwd_window(g["q"], g["k"], g["v"], g["a"], g["r"], flags, window, sinks)   # noqa: E731
+    o, lse = call()
+    i = torch.arange(T, device="cuda")
+    gap = i[:, None] - i[None, :]
+    # weights and results rounded to bf16, and 1e-4 of the terms for logits of up to 60 in fp32
+    u = _bounds.HALF["bf16"]
+    for h in frozen:
+        logits = (g["a"][h, :T].double()[None, :] + g["r"][h].double()[gap.clamp(min=0)]).masked_fill(gap < 0, -np.inf)
+        W = torch.softmax(logits, -1)
+        v = g["v"][:, h // (H // Hkv)].double()
+        want = W @ v
+        assert ((o[:, h].double() - want).abs() <= (u + 1e-4) * (W @ v.abs()) + u * want.abs()).all(), h
+    for _ in range(60):
+        o2, lse2 = call()
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("d", [96, 128])
 @pytest.mark.parametrize("frozen", [(1, 2), (1, 2, 3, 4, 6), (0, 1, 2, 4, 5)])
 @pytest.mark.parametrize("T,window,sinks", [(100, 9, 2), (100, 0, 0), (300, 40, 0), (520, 130, 3)])
