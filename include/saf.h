@@ -321,7 +321,8 @@ SAF_API int saf_attn_bwd_window(const void* q, const void* k, const void* v, con
  * token t of sequence b stands at position i = ctx[b] + t and sees the keys j <= i,
  * ordinary heads within (window, sinks) as for saf_attn_fwd_window (window = 0: all),
  * frozen heads with the weights of Eq. 3 at row i (k is not read for them):
- * ld_prior >= max_len.
+ * ld_prior >= max_len. Entries of a and r may be -infinity; a logit a + r below -2.3e38,
+ * the type's lowest value among them, counts as -infinity: a key that is not seen.
  * In:  q [B,H,T,d]; max_len: an upper bound of ctx[b] + n_new[b], at most
  *      max_pages * page_size, known on the host: it sets the launch's size.
  * Out: o [B,H,T,d], lse [B,H,T] as for saf_attn_fwd; o = 0, lse = -inf for rows without
@@ -342,8 +343,9 @@ SAF_API int saf_attn_bwd_window(const void* q, const void* k, const void* v, con
  * values are read for all sequences together.
  *
  * workspace: DEVICE, 256-byte aligned, saf_attn_paged_workspace_bytes(...) bytes (enough
- * for every window and choice of frozen heads; 0 for invalid sizes); it begins with the
- * status words. Calls that share one must be ordered on one stream, replays of captured
+ * for every window and choice of frozen heads; 0 for invalid sizes; fewer sequences are
+ * split into more items and may need more: ask for every batch size that shares one); it
+ * begins with the status words. Calls that share one must be ordered on one stream, replays of captured
  * graphs among them.
  * Errors before any work is enqueued: SAF_EINVAL, SAF_EALIGN, SAF_EWORKSPACE,
  * SAF_EUNSUPPORTED, SAF_ECUDA as elsewhere (prefix_len + max_len <= 2^30 and B H T <= 2^29,

@@ -496,8 +496,9 @@ def saf_attn_fwd_window(q, k, v, a, r, frozen, window, sinks=0, state=None, o=No
         workspace = alloc_workspace(B, H, T, d, dt, False, v.device)
     ap, rp, ld = _prior(a, r, H, idx, T)
     _run("saf_attn_fwd_window", _lib.saf_attn_fwd_window, idx, _at(q, idx, dt), _at(k, idx, dt),
-         _at(v, idx, dt), ap, rp, ld, _flags(frozen, H), _at(_state(state, H, T, _dt(v)), idx, torch.uint8), int(window),
-         int(sinks), B, H, Hkv, T, d, _dt(v), _at(o, idx, dt), _at(lse, idx, torch.float32), _at(workspace, idx, torch.uint8), workspace.numel())
+         _at(v, idx, dt), ap, rp, ld, _flags(frozen, H), _at(_state(state, H, T, _dt(v)), idx, torch.uint8),
+         int(window), int(sinks), B, H, Hkv, T, d, _dt(v), _at(o, idx, dt), _at(lse, idx, torch.float32),
+         _at(workspace, idx, torch.uint8), workspace.numel())
     return o, lse
 
 
@@ -522,8 +523,8 @@ def saf_attn_bwd_window(q, k, v, o, do, lse, a, r, frozen, window, sinks=0, stat
     ap, rp, ld = _prior(a, r, H, idx, T)
     _run("saf_attn_bwd_window", _lib.saf_attn_bwd_window, idx, _at(q, idx, dt), _at(k, idx, dt),
          _at(v, idx, dt), _at(o, idx, dt), _at(do, idx, dt), _at(lse, idx, torch.float32), ap, rp, ld,
-         _flags(frozen, H), _at(_state(state, H, T, _dt(v)), idx, torch.uint8), int(window), int(sinks), B, H, Hkv, T, d,
-         _dt(v), _at(dq, idx, dt),
+         _flags(frozen, H), _at(_state(state, H, T, _dt(v)), idx, torch.uint8), int(window), int(sinks), B, H, Hkv,
+         T, d, _dt(v), _at(dq, idx, dt),
          _at(dk, idx, dt), _at(dv, idx, dt), _at(workspace, idx, torch.uint8), workspace.numel())
     return dq, dk, dv
 
@@ -617,7 +618,8 @@ def saf_attn_paged_workspace_bytes(B, H, Hkv, T, d, max_len, dtype, prefix_len=0
 
 
 def alloc_paged_workspace(B, H, Hkv, T, d, max_len, dtype, prefix_len=0, device="cuda"):
-    """A workspace for saf_attn_paged / saf_attn_paged_shared with cleared status words."""
+    """A workspace for saf_attn_paged / saf_attn_paged_shared with cleared status words (for these
+    sizes: a smaller batch may need a larger one)."""
     n = saf_attn_paged_workspace_bytes(B, H, Hkv, T, d, max_len, dtype, prefix_len)
     w = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
     w[:256].zero_()

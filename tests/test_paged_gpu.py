@@ -190,6 +190,22 @@ def test_many_sequences_share_a_prefix(saf):
         x.check(*x.call(saf, frozen), frozen)
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+@pytest.mark.parametrize("masked", [-float("inf"), torch.finfo(torch.float32).min])
+@pytest.mark.parametrize("prefix", [0, 40])
+def test_keys_that_a_pattern_masks(saf, dtype, d, masked, prefix):
+    # a head whose pattern leaves nothing: zeros and -infinity; one that masks some keys: no weight there
+    frozen = [0, 1, 1, 0]
+    x = Batch(dtype, 4, 2, 2, d, 16, (0, 100, 300), (2, 2, 1), prefix=prefix, seed=3)
+    x.a[1], x.a[2, 3:7] = masked, masked
+    o, lse = x.call(saf, frozen)
+    assert not o[:, 1].any() and torch.isneginf(lse[:, 1]).all()
+    # (the first row sees key 0 alone and the next ones 1, 2, ...: never only masked keys)
+    x.a[1], x.a[2, 3:7] = 0.0, -200.0   # e^-200: nothing in the outputs' bits
+    o[:, 1], lse[:, 1] = (t[:, 1] for t in x.call(saf, frozen))
+    x.check(o, lse, frozen)
+
+
 def test_every_head_frozen_reads_no_keys(saf):
     for dtype in ("bf16", "fp32"):
         x = Batch(dtype, 4, 2, 2, 64, 16, (30, 50), (2, 1), seed=2)
