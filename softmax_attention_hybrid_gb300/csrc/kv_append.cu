@@ -13,9 +13,9 @@
 // Bound by memory: every element is read once and written once; the angles cost one
 // sincospif per pair and token for several heads. Thread = 16 elements of a row (8 pairs) of
 // `per` heads of a token, so that neighbouring threads read whole rows. The prompts of eight
-// sequences (105 MB) take 25 us, 4.2 TB/s, 62% of a plain copy's rate: a thread waits for its
+// sequences (105 MB) take 23 us, 4.6 TB/s, 67% of a plain copy's rate: a thread waits for its
 // counts, then its page, then its rows. (The angles of a block's tokens computed once, into
-// shared memory, took 27 us: they are not what bounds it.)
+// shared memory, took 2 us more: they are not what bounds it.)
 #include <math.h>
 #include <string.h>
 
@@ -294,8 +294,8 @@ extern "C" int saf_kv_append(const void* q, const void* k, const void* v, const 
     p.slots = p.nq + p.nk + Hkv;
     // A thread takes several heads of its token, so that its angles serve them all, once the call
     // has threads enough for the whole GPU. The prompts of eight sequences of 4096 tokens (12 heads,
-    // d 64) take 65, 40, 30, 25, 27 us with 1, 2, 4, 8, 16 heads per thread; one token of 32
-    // sequences (32 + 2 x 8 heads, d 128) 6.2 us with 1 to 4, 6.9 with 8, 8.3 with 16.
+    // d 64) take 62, 38, 28, 23, 24 us with 1, 2, 4, 8, 16 heads per thread; one token of 32
+    // sequences (32 + 2 x 8 heads, d 128) 3.4, 3.6, 4.0, 5.1, 6.7 us, one call behind another.
     const long long all = (long long)B * T * p.slots * p.units;
     p.per = all > 8ll * kFullGpu ? 8 : all > kFullGpu ? (int)(all / kFullGpu) : 1;
     p.groups = (p.slots + p.per - 1) / p.per;

@@ -1,7 +1,7 @@
 // Paged attention on the 5th-generation tensor cores (bf16; see paged.h for the split).
 //
-// An item holds up to 128 query rows, the M = 128 rows of its MMAs, and walks its tiles of 64
-// keys: S = Q K^T, online softmax with one thread per row, O += P V. Keys and values come
+// An item holds up to 128 query rows, the M = 128 rows of its MMAs, and walks its tiles of 64 or
+// 128 keys: S = Q K^T, online softmax with one thread per row, O += P V. Keys and values come
 // page by page through TMA, straight into the swizzled operand layout.
 //
 // Copies. A decoding step has far fewer rows than 128 (the query heads of a group times the new
