@@ -391,7 +391,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 _I64x9 = ctypes.c_int64 * 9
-_2G = 2 ** 31   # ctypes would cut a larger int to its low 32 bits
+_2G, _8E = 2 ** 31, 2 ** 63   # ctypes would cut a larger int to its low 32 (64) bits
 
 
 def _fits(top=_2G, **given):
@@ -481,7 +481,8 @@ def saf_attn_fwd_window(q, k, v, a, r, frozen, window, sinks=0, state=None, o=No
     if stream is not None:
         return _on(stream, v, lambda: saf_attn_fwd_window(q, k, v, a, r, frozen, window, sinks, state, o,
                    lse, workspace))
-    _fits(window=window, sinks=sinks)
+    if not (-_2G <= window < _2G and -_2G <= sinks < _2G):
+        _fits(window=window, sinks=sinks)
     idx, dt = _device(v), v.dtype
     B, H, Hkv, T, d = _gqa_shape(q, v, frozen)
     full, rows = (B, H, T, d), (B, H, T)
@@ -509,7 +510,8 @@ def saf_attn_bwd_window(q, k, v, o, do, lse, a, r, frozen, window, sinks=0, stat
     if stream is not None:
         return _on(stream, v, lambda: saf_attn_bwd_window(q, k, v, o, do, lse, a, r, frozen, window, sinks,
                    state, dq, dk, dv, workspace))
-    _fits(window=window, sinks=sinks)
+    if not (-_2G <= window < _2G and -_2G <= sinks < _2G):
+        _fits(window=window, sinks=sinks)
     idx, dt = _device(v), v.dtype
     B, H, Hkv, T, d = _gqa_shape(q, v, frozen)
     full, kv = (B, H, T, d), v.shape
@@ -563,7 +565,8 @@ def saf_kv_append(k, v, k_cache, v_cache, page_table, ctx, n_new=None, q=None, q
     if stream is not None:
         return _on(stream, v, lambda: saf_kv_append(k, v, k_cache, v_cache, page_table, ctx, n_new, q,
                    q_out, inv_freq, interleaved, pos_base, frozen, status))
-    _fits(2 ** 63, pos_base=pos_base)
+    if not -_8E <= pos_base < _8E:
+        _fits(_8E, pos_base=pos_base)
     idx, dt, i32 = _device(v), v.dtype, torch.int32
     shape, caches = v.shape, v_cache.shape
     B, Hkv, T, d = shape
@@ -686,7 +689,8 @@ def saf_attn_paged_shared(q, k_cache, v_cache, prefix_pages, prefix_len, page_ta
     if stream is not None:
         return _on(stream, q, lambda: saf_attn_paged_shared(q, k_cache, v_cache, prefix_pages, prefix_len,
                    page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o, lse, workspace))
-    _fits(prefix_len=prefix_len)
+    if not -_2G <= prefix_len < _2G:
+        _fits(prefix_len=prefix_len)
     if prefix_pages is not None and prefix_pages.numel() * v_cache.shape[2] < prefix_len:
         raise ValueError("prefix_pages holds fewer pages than prefix_len tokens take")
     prefix = (_at(prefix_pages, _device(q), torch.int32), prefix_len)
