@@ -355,6 +355,8 @@ __device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, cons
         const float ref = m == -INFINITY ? 0.f : m;   // a row that has seen no key yet: weights 2^-inf = 0
         const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-ref, -ref);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+        // The weights are rounded to bf16 for P V (both operands of an MMA have V's type): o is off by up
+        // to 2^-8 of sum_j P_j |v_j|. l adds them unrounded, which lse and the joins of items need.
         uint32_t pk[kCols / 2];
 #pragma unroll
         for (int c = 0; c < kCols / 2; ++c) {
