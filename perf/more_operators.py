@@ -398,22 +398,22 @@ def _own(s):
     fz = s["frozen"] if c["F"] else None
     cache = (s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"])
     if c["op"] == "append":
-        saf.saf_kv_append_e4m3(s["k"], s["v"], *cache, s["table"], s["ctx"], s["n_new"], q=s["q"], q_out=s["q_out"],
+        saf.saf_kv_append_quant(s["k"], s["v"], *cache, s["table"], s["ctx"], s["n_new"], q=s["q"], q_out=s["q_out"],
                                inv_freq=s["inv_freq"], interleaved=c["interleaved"], frozen=fz)
         return [s["q_out"], *cache]
     if c["op"] == "read":
-        return list(saf.saf_kv_read_e4m3(*cache, s["table"], s["ctx"], s["n_new"], k_out=s["k_out"],
+        return list(saf.saf_kv_read_quant(*cache, s["table"], s["ctx"], s["n_new"], k_out=s["k_out"],
                                          v_out=s["v_out"]))
     ws = s["workspace"]
     B, H, Hkv, T, d = (c[n] for n in ("B", "H", "Hkv", "T", "d"))
     if not ws:
-        ws["w"] = saf.alloc_paged_e4m3_workspace(B, H, Hkv, T, d, c["max_len"], s["q"].dtype, prefix_len=c["prefix"])
+        ws["w"] = saf.alloc_paged_quant_workspace(B, H, Hkv, T, d, c["max_len"], s["q"].dtype, prefix_len=c["prefix"])
     if c["op"] == "paged":
-        o, lse = saf.saf_attn_paged_e4m3(s["q"], *cache, s["table"], s["ctx"], c["max_len"], n_new=s["n_new"],
+        o, lse = saf.saf_attn_paged_quant(s["q"], *cache, s["table"], s["ctx"], c["max_len"], n_new=s["n_new"],
                                          a=s["a"], r=s["r"], frozen=fz, window=c["window"], sinks=c["sinks"],
                                          o=s["o"], lse=s["lse"], workspace=ws["w"])
     else:
-        o, lse = saf.saf_attn_paged_shared_e4m3(s["q"], *cache, s["prefix_pages"], c["prefix"], s["table"], s["ctx"],
+        o, lse = saf.saf_attn_paged_shared_quant(s["q"], *cache, s["prefix_pages"], c["prefix"], s["table"], s["ctx"],
                                                 c["max_len"], n_new=s["n_new"], a=s["a"], r=s["r"], frozen=fz,
                                                 window=c["window"], sinks=c["sinks"], o=s["o"], lse=s["lse"],
                                                 workspace=ws["w"])
