@@ -370,6 +370,58 @@ SAF_API int saf_attn_paged_shared(const void* q, const void* k_cache, const void
                                   saf_dtype_t dt, void* o, float* lse, void* workspace, size_t ws_bytes,
                                   void* stream);
 
+/* ---- 8-bit paged cache ---------------------------------------------------------
+ * The paged cache in 8 bits: k_cache, v_cache [num_pages, Hkv, page_size, d] hold codes of
+ * float8 e4m3 (4 exponent and 3 mantissa bits, largest 448, no infinity), and k_scale, v_scale
+ * [num_pages, Hkv, page_size] (fp32, 16-byte aligned) one scale for each row of d codes. A row
+ * stands for the values code_c * scale. dt is the type of q, k, v, o and of rows read back.
+ *
+ * saf_kv_append_quant is saf_kv_append into such caches. A row y (k after its rotation, which is
+ * not rounded before) is written as
+ *     scale = max(max_c |y_c| / 448, 2^-126),   code_c = y_c / scale, rounded to nearest even,
+ * in fp32: a code is off by half a step of e4m3 (2^-4 of the value, or 2^-10 scale near zero, and
+ * 2^-22 of the value by the arithmetic before it). A NaN keeps its place; a row with an infinity
+ * has an infinite scale and reads back as NaN. q is rotated and rounded to dt as there.
+ * k_scale may be NULL where k_cache may. The scales of slots that are not written stay as they were.
+ *
+ * saf_kv_read_quant reads rows back: row t of sequence b, t < count[b], is its slot first[b] + t,
+ * as code_c * scale rounded to dt. first [B] (DEVICE int32; NULL: 0) and count [B] (DEVICE int32;
+ * NULL: T each), 0 <= count[b] <= T.
+ * Out: k_out, v_out [B, Hkv, T, d] (dt), contiguous, all of them written: rows without a token, and
+ * rows of a page outside the cache, as zeros. k_cache, k_scale and k_out may be NULL together
+ * (values only). Counts and pages outside their bounds are reported in status as by saf_kv_append.
+ * B T <= 2^30 and T <= 2^21, else SAF_EINVAL.
+ *
+ * saf_attn_paged_quant and saf_attn_paged_shared_quant are saf_attn_paged and saf_attn_paged_shared
+ * over such caches: every rule above holds, with code_c * scale for the cache's values. Scales that
+ * a row sees must be finite and not negative; those of slots that no row sees may be anything, as
+ * the codes. The workspace is that of saf_attn_paged_quant_workspace_bytes. */
+SAF_API int saf_kv_append_quant(const void* q, const void* k, const void* v, const int64_t* strides,
+                               const int32_t* ctx, const int32_t* n_new, const int32_t* page_table, int max_pages,
+                               const double* inv_freq, int rope_dim, int interleaved, int64_t pos_base,
+                               const uint8_t* frozen, int B, int H, int Hkv, int T, int d, int num_pages,
+                               int page_size, saf_dtype_t dt, void* q_out, void* k_cache, void* v_cache,
+                               float* k_scale, float* v_scale, uint32_t* status, void* stream);
+SAF_API int saf_kv_read_quant(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                             const int32_t* page_table, int max_pages, const int32_t* first, const int32_t* count,
+                             int B, int Hkv, int T, int d, int num_pages, int page_size, saf_dtype_t dt, void* k_out,
+                             void* v_out, uint32_t* status, void* stream);
+SAF_API size_t saf_attn_paged_quant_workspace_bytes(int B, int H, int Hkv, int T, int d, int max_len, int prefix_len,
+                                                   saf_dtype_t dt);
+SAF_API int saf_attn_paged_quant(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                const float* v_scale, const int32_t* page_table, int max_pages, const int32_t* ctx,
+                                const int32_t* n_new, const float* a, const float* r, int ld_prior,
+                                const uint8_t* frozen, int window, int sinks, int B, int H, int Hkv, int T, int d,
+                                int max_len, int num_pages, int page_size, saf_dtype_t dt, void* o, float* lse,
+                                void* workspace, size_t ws_bytes, void* stream);
+SAF_API int saf_attn_paged_shared_quant(const void* q, const void* k_cache, const void* v_cache,
+                                       const float* k_scale, const float* v_scale, const int32_t* prefix_pages,
+                                       int prefix_len, const int32_t* page_table, int max_pages, const int32_t* ctx,
+                                       const int32_t* n_new, const float* a, const float* r, int ld_prior,
+                                       const uint8_t* frozen, int window, int sinks, int B, int H, int Hkv, int T,
+                                       int d, int max_len, int num_pages, int page_size, saf_dtype_t dt, void* o,
+                                       float* lse, void* workspace, size_t ws_bytes, void* stream);
+
 /* Diagnostic forward pass for testing failure detection (the paper has no
  * counterpart; it exercises this library's bounded waits).
  *
@@ -522,8 +574,9 @@ typedef enum {
     SAF_KERNEL_PATTERN_PREP = 8, /* backward: init kernel (clears the status   *
                                   * words; maxima and padded a, r slices)       */
     SAF_KERNEL_PATTERN_GRAD = 9, /* saf_pattern_grad_tc: all of its launches    */
-    SAF_KERNEL_KV_APPEND = 10,  /* saf_kv_append                               */
-    SAF_KERNEL_PAGED = 11       /* saf_attn_paged(_shared): all of its launches */
+    SAF_KERNEL_KV_APPEND = 10,  /* saf_kv_append(_quant)                        */
+    SAF_KERNEL_PAGED = 11,      /* saf_attn_paged(_shared)(_quant): all of its launches */
+    SAF_KERNEL_KV_READ = 12     /* saf_kv_read_quant                            */
 } saf_kernel_t;
 
 /* From the next call on, record `start` (a cudaEvent_t as void*) on the

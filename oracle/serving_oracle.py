@@ -113,3 +113,34 @@ def paged_fwd(q, k_cache, v_cache, table, ctx, n_new, a, r, frozen, window=0, si
                                            None if r is None else r[h], frozen[h], window, sinks)
             o[b, h, :n] = W @ v[:, h // G]
     return o, lse
+
+
+# ---------------------------------------------------------------------------
+# 8-bit caches: rows of e4m3 codes with one scale each
+# ---------------------------------------------------------------------------
+def e4m3_values():
+    """The 256 values of float8 e4m3 by code: sign, 4 exponent bits (bias 7), 3 mantissa bits; code
+    0x7f (0xff) is NaN, there is no infinity, exponent 0 holds the subnormals."""
+    code = np.arange(256)
+    e, m = (code >> 3) & 15, code & 7
+    x = np.where(e == 0, m * 2.0 ** -9, (8 + m) * 2.0 ** (e.astype(np.float64) - 10))
+    x[(code & 127) == 127] = np.nan
+    return np.where(code >> 7, -x, x)
+
+
+def quantise(y):
+    """Codes (uint8) and scales of the rows y [..., d]: scale = max(max |y| / 448, 2^-126), code = y / scale
+    rounded to the nearest value of e4m3, ties to the even code."""
+    y = np.asarray(y, dtype=np.float64)
+    scale = np.maximum(np.abs(y).max(axis=-1) / 448.0, 2.0 ** -126)
+    z = np.abs(y / scale[..., None])
+    val = e4m3_values()[:127]
+    hi = np.clip(np.searchsorted(val, z), 1, 126)
+    lo = hi - 1
+    up = (z - val[lo] > val[hi] - z) | ((z - val[lo] == val[hi] - z) & (hi % 2 == 0))
+    return np.where(up, hi, lo).astype(np.uint8) | (np.signbit(y).astype(np.uint8) << 7), scale
+
+
+def dequantise(codes, scale):
+    """What the rows of codes [..., d] with scales [...] stand for."""
+    return e4m3_values()[codes] * np.asarray(scale, dtype=np.float64)[..., None]

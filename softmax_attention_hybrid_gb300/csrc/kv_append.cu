@@ -16,6 +16,12 @@
 // sequences (105 MB) take 23 us, 4.6 TB/s, 67% of a plain copy's rate: a thread waits for its
 // counts, then its page, then its rows. (The angles of a block's tokens computed once, into
 // shared memory, took 2 us more: they are not what bounds it.)
+//
+// 8-bit caches (saf_kv_append_quant). A row y is held as codes and one scale,
+//     scale = max(max_c |y_c| / 448, 2^-126),   code_c = y_c / scale, rounded to e4m3,
+// with y rotated but not rounded before. The threads of a row are then neighbouring lanes (4, or
+// 8 of which 6 work at d = 96) that find the row's maximum by shuffles.
+#include <cuda_fp8.h>
 #include <math.h>
 #include <string.h>
 
@@ -30,6 +36,7 @@ constexpr long long kFullGpu = 152ll * 2048;   // threads that the GPU holds
 struct AppendArgs {
     const void *q, *k, *v;
     void *q_out, *k_cache, *v_cache;
+    float *k_scale, *v_scale;        // 8-bit caches: [num_pages, Hkv, page]
     const int32_t *ctx, *n_new, *table;
     uint32_t* status;
     long long sq[3], sk[3], sv[3];   // element strides (sequence, head, token)
@@ -37,6 +44,7 @@ struct AppendArgs {
     int B, H, Hkv, T, d, max_pages, num_pages, page_log2;
     int rope, interleaved;
     int units;                       // d / 16
+    int lanes;                       // threads of a row: units, or for 8-bit caches 4 or 8
     int nq, nk, slots;               // heads of q, of k, and all with v's that are moved
     int per, groups;                 // slots of a thread; ceil(slots / per)
     uint64_t freq[64];               // F_c
@@ -86,7 +94,16 @@ struct Raw<__nv_bfloat16> {
     }
 };
 
-template <typename E>
+// 8 values as codes of e4m3 (out of range: the largest; NaN stays NaN).
+__device__ __forceinline__ uint2 codes8(const float* x, float inv) {
+    uint32_t c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        c[e] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * e] * inv, x[2 * e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+template <typename E, bool kQ8>
 __device__ __forceinline__ void append_token(const AppendArgs& p, int b, int t, int group, int u) {
     const int c = p.ctx[b];
     const int n = p.n_new ? p.n_new[b] : p.T;
@@ -107,6 +124,7 @@ __device__ __forceinline__ void append_token(const AppendArgs& p, int b, int t, 
 
     // my 16 elements: two runs of 8, for a rotated row's pairs (8u + e, rope / 2 + 8u + e) when
     // the pairs are halves apart
+    const bool mine = !kQ8 || u < p.units;   // (a lane without elements still takes part in the shuffles)
     const bool turn = 16 * u < p.rope;
     const int c0 = turn && !p.interleaved ? 8 * u : 16 * u;
     const int c1 = turn && !p.interleaved ? (p.rope >> 1) + 8 * u : 16 * u + 8;
@@ -125,7 +143,8 @@ __device__ __forceinline__ void append_token(const AppendArgs& p, int b, int t, 
     constexpr int kBatch = sizeof(E) == 2 ? 4 : 2;
     for (int s0 = group; s0 < p.slots; s0 += kBatch * p.groups) {
         Raw<E> x[kBatch], y[kBatch];
-        E* dst[kBatch];
+        E* dst[kBatch];          // the row in q_out or in the cache
+        size_t at[kQ8 ? kBatch : 1];   // 8-bit caches: the row's number
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int s = s0 + k * p.groups;
@@ -141,9 +160,15 @@ __device__ __forceinline__ void append_token(const AppendArgs& p, int b, int t, 
                 if (page < 0) continue;
                 const long long* st = is_v ? p.sv : p.sk;
                 src = (const E*)(is_v ? p.v : p.k) + b * st[0] + h * st[1] + t * st[2];
-                dst[k] = (E*)(is_v ? p.v_cache : p.k_cache) +
-                         ((((size_t)page * p.Hkv + h) << p.page_log2) + page_row) * p.d;
+                const size_t row = (((size_t)page * p.Hkv + h) << p.page_log2) + page_row;
+                if constexpr (kQ8) {
+                    at[k] = row;
+                    dst[k] = (E*)(is_v ? p.v_cache : p.k_cache);
+                } else {
+                    dst[k] = (E*)(is_v ? p.v_cache : p.k_cache) + row * p.d;
+                }
             }
+            if (!mine) continue;
             x[k].load(src + (is_v ? 16 * u : c0));
             y[k].load(src + (is_v ? 16 * u + 8 : c1));
         }
@@ -151,10 +176,19 @@ __device__ __forceinline__ void append_token(const AppendArgs& p, int b, int t, 
         for (int k = 0; k < kBatch; ++k) {
             if (!dst[k]) continue;
             const bool is_v = s0 + k * p.groups >= p.nq + p.nk;
+            const bool coded = kQ8 && s0 + k * p.groups >= p.nq;
+            if (!coded && !mine) continue;
+            float a[8], z[8];
+            if (coded || (turn && !is_v)) {
+                if (!mine) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) a[e] = z[e] = 0.f;
+                } else {
+                    x[k].get(a);
+                    y[k].get(z);
+                }
+            }
             if (turn && !is_v) {
-                float a[8], z[8];
-                x[k].get(a);
-                y[k].get(z);
                 if (!p.interleaved) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -173,8 +207,28 @@ __device__ __forceinline__ void append_token(const AppendArgs& p, int b, int t, 
                         z[2 * e + 1] = a0 * sn[4 + e] + z0 * cs[4 + e];
                     }
                 }
-                x[k].set(a);
-                y[k].set(z);
+                if (!coded) {
+                    x[k].set(a);
+                    y[k].set(z);
+                }
+            }
+            if constexpr (kQ8) {
+                if (coded) {
+                    float m = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(a[e]), fabsf(z[e])));
+                    const unsigned first = threadIdx.x & 31u & ~(unsigned)(p.lanes - 1);
+                    const unsigned mask = ((1u << p.lanes) - 1u) << first;
+                    for (int o = p.lanes >> 1; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
+                    const float scale = fmaxf(__fdiv_rn(m, 448.f), 0x1p-126f), inv = 1.f / scale;
+                    if (mine) {
+                        uint8_t* row = (uint8_t*)dst[k] + at[k] * p.d;
+                        *reinterpret_cast<uint2*>(row + (is_v ? 16 * u : c0)) = codes8(a, inv);
+                        *reinterpret_cast<uint2*>(row + (is_v ? 16 * u + 8 : c1)) = codes8(z, inv);
+                    }
+                    if (u == 0) (is_v ? p.v_scale : p.k_scale)[at[k]] = scale;
+                    continue;
+                }
             }
             x[k].store(dst[k] + (is_v ? 16 * u : c0));
             y[k].store(dst[k] + (is_v ? 16 * u + 8 : c1));
@@ -182,16 +236,17 @@ __device__ __forceinline__ void append_token(const AppendArgs& p, int b, int t, 
     }
 }
 
-template <typename E>
+template <typename E, bool kQ8>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs p) {
     grid_dep_wait();
     grid_dep_launch();
     const unsigned id = blockIdx.x * kThreads + threadIdx.x;   // (token, group of slots, unit) of a sequence
-    const unsigned w = id / (unsigned)p.units;
-    const int u = (int)(id - w * (unsigned)p.units);
+    const unsigned lanes = (unsigned)(kQ8 ? p.lanes : p.units);
+    const unsigned w = id / lanes;
+    const int u = (int)(id - w * lanes);
     const int t = (int)(w / (unsigned)p.groups), group = (int)(w - (unsigned)t * (unsigned)p.groups);
     if (t >= p.T) return;
-    for (int b = blockIdx.y; b < p.B; b += gridDim.y) append_token<E>(p, b, t, group, u);
+    for (int b = blockIdx.y; b < p.B; b += gridDim.y) append_token<E, kQ8>(p, b, t, group, u);
 }
 bool aligned(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
@@ -213,16 +268,11 @@ uint64_t frequency(double f) {
 
 constexpr int64_t kLastBase = 1ll << 40;   // of pos_base
 
-}  // namespace
-}  // namespace saf
-
-using namespace saf;
-
-extern "C" int saf_kv_append(const void* q, const void* k, const void* v, const int64_t* strides, const int32_t* ctx,
-                             const int32_t* n_new, const int32_t* page_table, int max_pages, const double* inv_freq,
-                             int rope_dim, int interleaved, int64_t pos_base, const uint8_t* frozen, int B, int H,
-                             int Hkv, int T, int d, int num_pages, int page_size, saf_dtype_t dt, void* q_out,
-                             void* k_cache, void* v_cache, uint32_t* status, void* stream) {
+int append(const void* q, const void* k, const void* v, const int64_t* strides, const int32_t* ctx,
+           const int32_t* n_new, const int32_t* page_table, int max_pages, const double* inv_freq,
+           int rope_dim, int interleaved, int64_t pos_base, const uint8_t* frozen, int B, int H,
+           int Hkv, int T, int d, int num_pages, int page_size, saf_dtype_t dt, bool coded, void* q_out, void* k_cache,
+           void* v_cache, float* k_scale, float* v_scale, uint32_t* status, void* stream) {
     if (B < 0 || H <= 0 || T < 0 || H > SAF_MAX_HEADS || Hkv <= 0 || H % Hkv != 0) return SAF_EINVAL;
     if (dt != SAF_BF16 && dt != SAF_FP32) return SAF_EINVAL;
     if (!head_dim_supported(d, dt)) return SAF_EUNSUPPORTED;
@@ -245,9 +295,10 @@ extern "C" int saf_kv_append(const void* q, const void* k, const void* v, const 
     }
     if (!v || !v_cache || !ctx || !page_table || (p.nq > 0 && !q_out)) return SAF_EINVAL;
     if (p.nk > 0 && (!k || !k_cache)) return SAF_EINVAL;
+    if (coded && (!v_scale || (p.nk > 0 && !k_scale))) return SAF_EINVAL;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) ||
         !aligned(v_cache, 16) || !aligned(ctx, 4) || !aligned(n_new, 4) || !aligned(page_table, 4) ||
-        !aligned(status, 4))
+        !aligned(status, 4) || (coded && (!aligned(k_scale, 16) || !aligned(v_scale, 16))))
         return SAF_EALIGN;
     const long long row = d, e = dt == SAF_BF16 ? 2 : 4;
     long long* st[3] = {p.sq, p.sk, p.sv};
@@ -275,6 +326,8 @@ extern "C" int saf_kv_append(const void* q, const void* k, const void* v, const 
     p.q_out = q_out;
     p.k_cache = k_cache;
     p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
     p.ctx = ctx;
     p.n_new = n_new;
     p.table = page_table;
@@ -291,22 +344,53 @@ extern "C" int saf_kv_append(const void* q, const void* k, const void* v, const 
     p.rope = rope_dim;
     p.interleaved = interleaved;
     p.units = d / 16;
+    p.lanes = !coded ? p.units : p.units <= 4 ? 4 : 8;
     p.slots = p.nq + p.nk + Hkv;
     // A thread takes several heads of its token, so that its angles serve them all, once the call
     // has threads enough for the whole GPU. The prompts of eight sequences of 4096 tokens (12 heads,
     // d 64) take 62, 38, 28, 23, 24 us with 1, 2, 4, 8, 16 heads per thread; one token of 32
     // sequences (32 + 2 x 8 heads, d 128) 3.4, 3.6, 4.0, 5.1, 6.7 us, one call behind another.
-    const long long all = (long long)B * T * p.slots * p.units;
+    const long long all = (long long)B * T * p.slots * p.lanes;
     p.per = all > 8ll * kFullGpu ? 8 : all > kFullGpu ? (int)(all / kFullGpu) : 1;
     p.groups = (p.slots + p.per - 1) / p.per;
-    const long long threads = (long long)T * p.groups * p.units;   // of a sequence: at most 2^21 x 96 x 8
+    const long long threads = (long long)T * p.groups * p.lanes;   // of a sequence: at most 2^21 x 96 x 8
     const long long blocks = (threads + kThreads - 1) / kThreads;
     const dim3 grid((unsigned)blocks, (unsigned)(B < 65535 ? B : 65535));
     cudaStream_t cs = (cudaStream_t)stream;
     before_launch(SAF_KERNEL_KV_APPEND, cs);
     const cudaError_t err =
-        dt == SAF_BF16 ? launch_ex(append_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, cs, true, 1, p)
-                       : launch_ex(append_kernel<float>, grid, dim3(kThreads), 0, cs, true, 1, p);
+        launch_ex(coded ? (dt == SAF_BF16 ? append_kernel<__nv_bfloat16, true> : append_kernel<float, true>)
+                        : (dt == SAF_BF16 ? append_kernel<__nv_bfloat16, false> : append_kernel<float, false>),
+                  grid, dim3(kThreads), 0, cs, true, 1, p);
     after_launch(SAF_KERNEL_KV_APPEND, cs);
     return launch_status(err);
 }
+
+}  // namespace
+}  // namespace saf
+
+using namespace saf;
+
+extern "C" {
+
+int saf_kv_append(const void* q, const void* k, const void* v, const int64_t* strides, const int32_t* ctx,
+                  const int32_t* n_new, const int32_t* page_table, int max_pages, const double* inv_freq, int rope_dim,
+                  int interleaved, int64_t pos_base, const uint8_t* frozen, int B, int H, int Hkv, int T, int d,
+                  int num_pages, int page_size, saf_dtype_t dt, void* q_out, void* k_cache, void* v_cache,
+                  uint32_t* status, void* stream) {
+    return append(q, k, v, strides, ctx, n_new, page_table, max_pages, inv_freq, rope_dim, interleaved, pos_base,
+                  frozen, B, H, Hkv, T, d, num_pages, page_size, dt, false, q_out, k_cache, v_cache, nullptr, nullptr,
+                  status, stream);
+}
+
+int saf_kv_append_quant(const void* q, const void* k, const void* v, const int64_t* strides, const int32_t* ctx,
+                       const int32_t* n_new, const int32_t* page_table, int max_pages, const double* inv_freq,
+                       int rope_dim, int interleaved, int64_t pos_base, const uint8_t* frozen, int B, int H, int Hkv,
+                       int T, int d, int num_pages, int page_size, saf_dtype_t dt, void* q_out, void* k_cache,
+                       void* v_cache, float* k_scale, float* v_scale, uint32_t* status, void* stream) {
+    return append(q, k, v, strides, ctx, n_new, page_table, max_pages, inv_freq, rope_dim, interleaved, pos_base,
+                  frozen, B, H, Hkv, T, d, num_pages, page_size, dt, true, q_out, k_cache, v_cache, k_scale, v_scale,
+                  status, stream);
+}
+
+}  // extern "C"

@@ -28,6 +28,8 @@ struct PagedArgs {
     const void* q;                 // [B, H, T, d]
     const void* k_cache;           // [num_pages, Hkv, page, d]
     const void* v_cache;
+    const float* k_scale;          // 8-bit caches (codes of e4m3): a scale per row [num_pages, Hkv, page]; else NULL
+    const float* v_scale;
     const int32_t* prefix_pages;   // [ceil(P / page)]
     const int32_t* page_table;     // [B, max_pages]
     const int32_t* ctx;            // [B]
@@ -190,5 +192,7 @@ __host__ __device__ constexpr int paged_tc_tile(int d, int rows) { return d == 6
 cudaError_t launch_paged_tc(const PagedArgs& p, cudaStream_t s);
 constexpr int kSimtRows = 8, kSimtTile = 32;
 cudaError_t launch_paged_simt(const PagedArgs& p, cudaStream_t s);
+// 8-bit caches: the same kernel, for q and o of bf16 or fp32.
+cudaError_t launch_paged_simt_q8(const PagedArgs& p, bool bf16, cudaStream_t s);
 
 }  // namespace saf

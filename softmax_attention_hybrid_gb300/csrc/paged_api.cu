@@ -131,7 +131,12 @@ long long most_chunks(const Plan& x, int part, long long tiles) {
     return c < tiles ? c : tiles;
 }
 
-Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, bool bf16) {
+// Kernels of a call: by the type of q, and whether the cache is one of 8 bits.
+enum class Kind { kTc, kSimt, kSimtQ8 };
+Kind kind_of(saf_dtype_t dt, bool q8) { return q8 ? Kind::kSimtQ8 : dt == SAF_BF16 ? Kind::kTc : Kind::kSimt; }
+
+Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, Kind kind) {
+    const bool bf16 = kind == Kind::kTc;
     Plan x;
     x.slots = bf16 ? kSlotsTc : kSlotsSimt;
     const long long G = H / Hkv;
@@ -229,7 +234,7 @@ size_t workspace_bytes(const Plan& x, int B, int H, int T, int d, size_t* po_off
 bool power_of_two(int n) { return n > 0 && (n & (n - 1)) == 0; }
 bool aligned(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
-// Sizes, in the order of the workspace query and of both calls.
+// Sizes, in the order of the workspace query and of the calls.
 int check_sizes(int B, int H, int Hkv, int T, int d, int max_len, int prefix_len, saf_dtype_t dt) {
     if (B < 0 || H <= 0 || T < 0 || H > SAF_MAX_HEADS || Hkv <= 0 || H % Hkv != 0) return SAF_EINVAL;
     if (dt != SAF_BF16 && dt != SAF_FP32) return SAF_EINVAL;
@@ -239,8 +244,9 @@ int check_sizes(int B, int H, int Hkv, int T, int d, int max_len, int prefix_len
     return SAF_OK;
 }
 
-int paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* prefix_pages, int prefix_len,
-          const int32_t* page_table, int max_pages, const int32_t* ctx, const int32_t* n_new, const float* a,
+// q8: the caches hold codes of e4m3, with scales.
+int paged(const void* q, const void* k_cache, const void* v_cache, bool q8, const float* k_scale,
+          const float* v_scale, const int32_t* prefix_pages, int prefix_len, const int32_t* page_table, int max_pages, const int32_t* ctx, const int32_t* n_new, const float* a,
           const float* r, int ld_prior, const uint8_t* frozen, int window, int sinks, int B, int H, int Hkv, int T,
           int d, int max_len, int num_pages, int page_size, saf_dtype_t dt, void* o, float* lse, void* workspace,
           size_t ws_bytes, void* stream) {
@@ -273,14 +279,16 @@ int paged(const void* q, const void* k_cache, const void* v_cache, const int32_t
     }
     if (!v_cache || !page_table || !ctx || !o || !lse || (prefix_len > 0 && !prefix_pages)) return SAF_EINVAL;
     if (nfrozen < H && (!q || !k_cache)) return SAF_EINVAL;
+    if (q8 && (!v_scale || (nfrozen < H && !k_scale))) return SAF_EINVAL;
     if (nfrozen > 0 && (!a || !r || ld_prior < prefix_len + max_len)) return SAF_EINVAL;
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
         !aligned(a, 4) || !aligned(r, 4) || !aligned(page_table, 4) || !aligned(prefix_pages, 4) ||
-        !aligned(ctx, 4) || !aligned(n_new, 4))
+        !aligned(ctx, 4) || !aligned(n_new, 4) || !aligned(k_scale, 16) || !aligned(v_scale, 16))
         return SAF_EALIGN;
     if (!workspace) return SAF_EWORKSPACE;
     if (!aligned(workspace, 256)) return SAF_EALIGN;
-    const Plan plan = make_plan(B, H, Hkv, T, d, max_len, prefix_len, dt == SAF_BF16);
+    const Kind kind = kind_of(dt, q8);
+    const Plan plan = make_plan(B, H, Hkv, T, d, max_len, prefix_len, kind);
     size_t po_off;
     if (ws_bytes < workspace_bytes(plan, B, H, T, d, &po_off)) return SAF_EWORKSPACE;
     if ((st = check_device()) != SAF_OK) return st;
@@ -288,6 +296,8 @@ int paged(const void* q, const void* k_cache, const void* v_cache, const int32_t
     p.q = q;
     p.k_cache = k_cache;
     p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
     p.prefix_pages = prefix_pages;
     p.page_table = page_table;
     p.ctx = ctx;
@@ -319,13 +329,20 @@ int paged(const void* q, const void* k_cache, const void* v_cache, const int32_t
     cudaStream_t s = (cudaStream_t)stream;
     const bool bf16 = dt == SAF_BF16;
     before_launch(SAF_KERNEL_PAGED, s);
-    cudaError_t e = bf16 ? launch_paged_tc(p, s) : launch_paged_simt(p, s);
+    cudaError_t e = kind == Kind::kTc ? launch_paged_tc(p, s)
+                                      : kind == Kind::kSimt ? launch_paged_simt(p, s) : launch_paged_simt_q8(p, bf16, s);
     if (e == cudaSuccess && p.nsplit > 1) {
         note_launch();
         e = bf16 ? launch_join<__nv_bfloat16>(p, s) : launch_join<float>(p, s);
     }
     after_launch(SAF_KERNEL_PAGED, s);
     return launch_status(e);
+}
+
+size_t workspace_size(int B, int H, int Hkv, int T, int d, int max_len, int prefix_len, saf_dtype_t dt, bool q8) {
+    if (check_sizes(B, H, Hkv, T, d, max_len, prefix_len, dt) != SAF_OK) return 0;
+    if (B == 0 || T == 0) return kStatusBytes;
+    return workspace_bytes(make_plan(B, H, Hkv, T, d, max_len, prefix_len, kind_of(dt, q8)), B, H, T, d, nullptr);
 }
 
 }  // namespace
@@ -337,9 +354,7 @@ extern "C" {
 
 size_t saf_attn_paged_workspace_bytes(int B, int H, int Hkv, int T, int d, int max_len, int prefix_len,
                                       saf_dtype_t dt) {
-    if (check_sizes(B, H, Hkv, T, d, max_len, prefix_len, dt) != SAF_OK) return 0;
-    if (B == 0 || T == 0) return kStatusBytes;
-    return workspace_bytes(make_plan(B, H, Hkv, T, d, max_len, prefix_len, dt == SAF_BF16), B, H, T, d, nullptr);
+    return workspace_size(B, H, Hkv, T, d, max_len, prefix_len, dt, false);
 }
 
 int saf_attn_paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table, int max_pages,
@@ -347,8 +362,9 @@ int saf_attn_paged(const void* q, const void* k_cache, const void* v_cache, cons
                    const uint8_t* frozen, int window, int sinks, int B, int H, int Hkv, int T, int d, int max_len,
                    int num_pages, int page_size, saf_dtype_t dt, void* o, float* lse, void* workspace,
                    size_t ws_bytes, void* stream) {
-    return paged(q, k_cache, v_cache, nullptr, 0, page_table, max_pages, ctx, n_new, a, r, ld_prior, frozen, window,
-                 sinks, B, H, Hkv, T, d, max_len, num_pages, page_size, dt, o, lse, workspace, ws_bytes, stream);
+    return paged(q, k_cache, v_cache, false, nullptr, nullptr, nullptr, 0, page_table, max_pages, ctx, n_new, a, r,
+                 ld_prior, frozen, window, sinks, B, H, Hkv, T, d, max_len, num_pages, page_size, dt, o, lse,
+                 workspace, ws_bytes, stream);
 }
 
 int saf_attn_paged_shared(const void* q, const void* k_cache, const void* v_cache, const int32_t* prefix_pages,
@@ -357,9 +373,37 @@ int saf_attn_paged_shared(const void* q, const void* k_cache, const void* v_cach
                           int window, int sinks, int B, int H, int Hkv, int T, int d, int max_len, int num_pages,
                           int page_size, saf_dtype_t dt, void* o, float* lse, void* workspace, size_t ws_bytes,
                           void* stream) {
-    return paged(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, max_pages, ctx, n_new, a, r, ld_prior,
-                 frozen, window, sinks, B, H, Hkv, T, d, max_len, num_pages, page_size, dt, o, lse, workspace,
-                 ws_bytes, stream);
+    return paged(q, k_cache, v_cache, false, nullptr, nullptr, prefix_pages, prefix_len, page_table, max_pages, ctx,
+                 n_new, a, r, ld_prior, frozen, window, sinks, B, H, Hkv, T, d, max_len, num_pages, page_size, dt, o,
+                 lse, workspace, ws_bytes, stream);
+}
+
+size_t saf_attn_paged_quant_workspace_bytes(int B, int H, int Hkv, int T, int d, int max_len, int prefix_len,
+                                           saf_dtype_t dt) {
+    return workspace_size(B, H, Hkv, T, d, max_len, prefix_len, dt, true);
+}
+
+int saf_attn_paged_quant(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                        const float* v_scale, const int32_t* page_table, int max_pages, const int32_t* ctx,
+                        const int32_t* n_new, const float* a, const float* r, int ld_prior, const uint8_t* frozen,
+                        int window, int sinks, int B, int H, int Hkv, int T, int d, int max_len, int num_pages,
+                        int page_size, saf_dtype_t dt, void* o, float* lse, void* workspace, size_t ws_bytes,
+                        void* stream) {
+    return paged(q, k_cache, v_cache, true, k_scale, v_scale, nullptr, 0, page_table, max_pages, ctx, n_new, a, r,
+                 ld_prior, frozen, window, sinks, B, H, Hkv, T, d, max_len, num_pages, page_size, dt, o, lse,
+                 workspace, ws_bytes, stream);
+}
+
+int saf_attn_paged_shared_quant(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                               const float* v_scale, const int32_t* prefix_pages, int prefix_len,
+                               const int32_t* page_table, int max_pages, const int32_t* ctx, const int32_t* n_new,
+                               const float* a, const float* r, int ld_prior, const uint8_t* frozen, int window,
+                               int sinks, int B, int H, int Hkv, int T, int d, int max_len, int num_pages,
+                               int page_size, saf_dtype_t dt, void* o, float* lse, void* workspace, size_t ws_bytes,
+                               void* stream) {
+    return paged(q, k_cache, v_cache, true, k_scale, v_scale, prefix_pages, prefix_len, page_table, max_pages, ctx,
+                 n_new, a, r, ld_prior, frozen, window, sinks, B, H, Hkv, T, d, max_len, num_pages, page_size, dt, o,
+                 lse, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -39,7 +39,8 @@ EXPORTED = ("saf_attn_workspace_bytes", "saf_attn_fwd", "saf_attn_bwd", "saf_dev
             "saf_attn_fwd_diag", "saf_frozen_state_bytes", "saf_frozen_prepare", "saf_attn_fwd_prepared",
             "saf_attn_bwd_prepared", "saf_pattern_grad_tc_workspace_bytes", "saf_pattern_grad_tc",
             "saf_attn_fwd_window", "saf_attn_bwd_window", "saf_kv_append", "saf_attn_paged_workspace_bytes",
-            "saf_attn_paged", "saf_attn_paged_shared")
+            "saf_attn_paged", "saf_attn_paged_shared", "saf_kv_append_quant", "saf_kv_read_quant",
+            "saf_attn_paged_quant_workspace_bytes", "saf_attn_paged_quant", "saf_attn_paged_shared_quant")
 
 SAF_KERNEL_NONE = 0
 SAF_KERNEL_LOGNORM = 1
@@ -53,6 +54,7 @@ SAF_KERNEL_PATTERN_PREP = 8
 SAF_KERNEL_PATTERN_GRAD = 9
 SAF_KERNEL_KV_APPEND = 10
 SAF_KERNEL_PAGED = 11
+SAF_KERNEL_KV_READ = 12
 
 
 class SafError(RuntimeError):
@@ -135,6 +137,19 @@ def _load():
     lib.saf_attn_paged_shared.argtypes = [vp, vp, vp, vp, i, vp, i, vp, vp, vp, vp, i, vp, i, i, i, i, i, i, i, i, i,
                                           i, i, vp, vp, vp, sz, vp]
     lib.saf_attn_paged_shared.restype = i
+    lib.saf_kv_append_quant.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, vp, i, i, ctypes.c_int64, vp, i, i, i, i, i, i,
+                                       i, i, vp, vp, vp, vp, vp, vp, vp]
+    lib.saf_kv_append_quant.restype = i
+    lib.saf_kv_read_quant.argtypes = [vp, vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, i, vp, vp, vp, vp]
+    lib.saf_kv_read_quant.restype = i
+    lib.saf_attn_paged_quant_workspace_bytes.argtypes = [i, i, i, i, i, i, i, i]
+    lib.saf_attn_paged_quant_workspace_bytes.restype = sz
+    lib.saf_attn_paged_quant.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, vp, vp, vp, i, vp, i, i, i, i, i, i, i, i, i,
+                                        i, i, vp, vp, vp, sz, vp]
+    lib.saf_attn_paged_quant.restype = i
+    lib.saf_attn_paged_shared_quant.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, i, vp, vp, vp, vp, i, vp, i, i, i, i, i,
+                                               i, i, i, i, i, i, vp, vp, vp, sz, vp]
+    lib.saf_attn_paged_shared_quant.restype = i
     return lib
 
 
@@ -389,7 +404,7 @@ def saf_attn_bwd_prepared(q, k, v, o, do, lse, a, r, frozen, state, dq=None, dk=
 # has is checked in one expression, and what is wrong is named on a second look (_at).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+_F32, _I32, _U8, _E4M3 = torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
 _I64x9 = ctypes.c_int64 * 9
 _2G, _8E = 2 ** 31, 2 ** 63   # ctypes would cut a larger int to its low 32 (64) bits
 
@@ -629,8 +644,31 @@ def alloc_paged_workspace(B, H, Hkv, T, d, max_len, dtype, prefix_len=0, device=
     return w
 
 
+def saf_attn_paged_quant_workspace_bytes(B, H, Hkv, T, d, max_len, dtype, prefix_len=0) -> int:
+    dt = SAF_BF16 if dtype in (torch.bfloat16, SAF_BF16, "bf16") else SAF_FP32
+    if not all(-_2G <= n < _2G for n in (B, H, Hkv, T, d, max_len, prefix_len)):
+        return 0
+    return int(_lib.saf_attn_paged_quant_workspace_bytes(B, H, Hkv, T, d, int(max_len), int(prefix_len), dt))
+
+
+def alloc_paged_quant_workspace(B, H, Hkv, T, d, max_len, dtype, prefix_len=0, device="cuda"):
+    """alloc_paged_workspace for saf_attn_paged_quant / saf_attn_paged_shared_quant (dtype: q's)."""
+    n = saf_attn_paged_quant_workspace_bytes(B, H, Hkv, T, d, max_len, dtype, prefix_len)
+    w = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    w[:256].zero_()
+    return w
+
+
+def _scales(k_scale, v_scale, caches, idx):
+    """Addresses of the scales of 8-bit caches of shape `caches`."""
+    if v_scale.shape != caches[:3] or (k_scale is not None and k_scale.shape != caches[:3]):
+        raise ValueError("the scales must be [num_pages, Hkv, page_size]")
+    return _at(k_scale, idx, _F32), _at(v_scale, idx, _F32)
+
+
 def _paged(where, fn, q, k_cache, v_cache, prefix, P, page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o,
-           lse, workspace):
+           lse, workspace, scales=None):
+    # scales: those of 8-bit caches, (k_scale, v_scale)
     if not (-_2G <= window < _2G and -_2G <= sinks < _2G and -_2G <= max_len < _2G):
         _fits(window=window, sinks=sinks, max_len=max_len)
     idx, dt = _device(q), q.dtype
@@ -649,18 +687,22 @@ def _paged(where, fn, q, k_cache, v_cache, prefix, P, page_table, ctx, max_len, 
         lse = torch.empty(full[:3], dtype=_F32, device=q.device)
     if o.shape != full or lse.shape != full[:3]:
         raise ValueError(f"o and lse must have shapes {tuple(full)} and {tuple(full[:3])}")
+    cdt, at_scales = dt, ()
+    if scales is not None:
+        cdt, at_scales = _E4M3, _scales(*scales, caches, idx)
     if workspace is None:
-        workspace = alloc_paged_workspace(B, H, Hkv, T, d, max_len, dt, P, q.device)
+        alloc = alloc_paged_workspace if scales is None else alloc_paged_quant_workspace
+        workspace = alloc(B, H, Hkv, T, d, max_len, dt, P, q.device)
     if not (idx == v_cache.get_device() == page_table.get_device() == ctx.get_device() == o.get_device()
             == lse.get_device() == workspace.get_device()
-            and dt is v_cache.dtype and dt is o.dtype and lse.dtype is _F32 and page_table.dtype is _I32
+            and cdt is v_cache.dtype and dt is o.dtype and lse.dtype is _F32 and page_table.dtype is _I32
             and ctx.dtype is _I32 and workspace.dtype is _U8
             and q.is_contiguous() and v_cache.is_contiguous() and page_table.is_contiguous() and ctx.is_contiguous()
             and o.is_contiguous() and lse.is_contiguous() and workspace.is_contiguous()):
-        for t, want in ((q, dt), (v_cache, dt), (page_table, _I32), (ctx, _I32), (o, dt), (lse, _F32), (workspace, _U8)):
+        for t, want in ((q, dt), (v_cache, cdt), (page_table, _I32), (ctx, _I32), (o, dt), (lse, _F32), (workspace, _U8)):
             _at(t, idx, want)
     ap, rp, ld = _prior(a, r, H, idx, P + max_len)
-    _run(where, fn, idx, q.data_ptr(), _at(k_cache, idx, dt), v_cache.data_ptr(), *prefix,
+    _run(where, fn, idx, q.data_ptr(), _at(k_cache, idx, cdt), v_cache.data_ptr(), *at_scales, *prefix,
          page_table.data_ptr(), table[1], ctx.data_ptr(), _at(n_new, idx, _I32), ap, rp, ld,
          _flags(frozen, H), int(window), int(sinks), B, H, Hkv, T, d, max_len, num_pages, page_size, _dt(q),
          o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
@@ -696,6 +738,134 @@ def saf_attn_paged_shared(q, k_cache, v_cache, prefix_pages, prefix_len, page_ta
     prefix = (_at(prefix_pages, _device(q), torch.int32), prefix_len)
     return _paged("saf_attn_paged_shared", _lib.saf_attn_paged_shared, q, k_cache, v_cache, prefix, prefix_len,
                   page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o, lse, workspace)
+
+
+def saf_kv_append_quant(k, v, k_cache, v_cache, k_scale, v_scale, page_table, ctx, n_new=None, q=None, q_out=None,
+                       inv_freq=None, interleaved=False, pos_base=0, frozen=None, status=None, stream=None):
+    """saf_kv_append into 8-bit caches: k_cache, v_cache [num_pages, Hkv, page_size, d] of
+    torch.float8_e4m3fn with fp32 scales k_scale, v_scale [num_pages, Hkv, page_size]. A row y is
+    held as scale = max(max |y| / 448, 2^-126) and codes y / scale. k, v and q are bf16 or fp32;
+    everything else is as for saf_kv_append."""
+    if stream is not None:
+        return _on(stream, v, lambda: saf_kv_append_quant(k, v, k_cache, v_cache, k_scale, v_scale, page_table, ctx,
+                   n_new, q, q_out, inv_freq, interleaved, pos_base, frozen, status))
+    if not -_8E <= pos_base < _8E:
+        _fits(_8E, pos_base=pos_base)
+    idx, dt = _device(v), v.dtype
+    shape, caches = v.shape, v_cache.shape
+    B, Hkv, T, d = shape
+    num_pages, heads, page_size, width = caches
+    max_pages = _table(ctx, n_new, page_table, B)
+    if heads != Hkv or width != d or (k_cache is not None and k_cache.shape != caches):
+        raise ValueError("the caches must be [num_pages, Hkv, page_size, d]")
+    ks, vs = _scales(k_scale, v_scale, caches, idx)
+    if k is not None and k.shape != shape:
+        raise ValueError("k must have v's shape")
+    qp = qo = kp = None
+    q_strides = k_strides = (0, 0, 0)
+    if q is not None:
+        full = q.shape
+        H = full[1]
+        if full[0] != B or full[2] != T or full[3] != d:
+            raise ValueError("q must be [B, H, T, d]")
+        if q_out is None:
+            # rows that are not written (frozen heads, rows without a token) come back as zeros
+            q_out = torch.zeros(full, dtype=dt, device=v.device)
+        elif q_out.shape != full:
+            raise ValueError("q_out must have q's shape")
+        qp, q_strides = _strided(q, idx, dt)
+        qo = _at(q_out, idx, dt)
+    else:
+        H = len(frozen) if frozen is not None else Hkv
+    if k is not None:
+        kp, k_strides = _strided(k, idx, dt)
+    vp, v_strides = _strided(v, idx, dt)
+    freq, rope = None, 0
+    if inv_freq is not None:
+        if not (torch.is_tensor(inv_freq) and inv_freq.dtype is torch.float64 and inv_freq.get_device() < 0
+                and inv_freq.is_contiguous()):
+            inv_freq = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
+        rope = 2 * inv_freq.numel()
+        freq = inv_freq.data_ptr() if rope else None
+    if status is not None and status.numel() * status.element_size() < 8:
+        raise ValueError("status needs 8 bytes")
+    _run("saf_kv_append_quant", _lib.saf_kv_append_quant, idx, qp, kp, vp, _I64x9(*q_strides, *k_strides, *v_strides),
+         _at(ctx, idx, _I32), _at(n_new, idx, _I32), _at(page_table, idx, _I32), max_pages, freq, rope,
+         1 if interleaved else 0, pos_base, _flags(frozen, H), B, H, Hkv, T, d, num_pages, page_size, _dt(v), qo,
+         _at(k_cache, idx, _E4M3), _at(v_cache, idx, _E4M3), ks, vs,
+         None if status is None else _at(status, idx, status.dtype))
+    return q_out
+
+
+def saf_kv_read_quant(k_cache, v_cache, k_scale, v_scale, page_table, first=None, count=None, T=None, dtype=None,
+                     k_out=None, v_out=None, status=None, stream=None):
+    """Rows of 8-bit caches read back: slots first[b] .. first[b] + count[b] - 1 of each sequence of
+    page_table [B, max_pages] as k_out, v_out [B, Hkv, T, d] (bf16 or fp32; rows behind them are
+    zeros); returns (k_out, v_out). first, count: int32 [B] on the device (None: 0, and T each).
+    T and dtype size the outputs where v_out is not given. k_cache and k_scale may be None
+    (values only: k_out is None). status as for saf_kv_append."""
+    if stream is not None:
+        return _on(stream, v_cache, lambda: saf_kv_read_quant(k_cache, v_cache, k_scale, v_scale, page_table, first,
+                   count, T, dtype, k_out, v_out, status))
+    idx, caches = _device(v_cache), v_cache.shape
+    num_pages, Hkv, page_size, d = caches
+    if len(page_table.shape) != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, max_pages = page_table.shape
+    _shapes(("k_cache", k_cache, caches), ("first", first, (B,)), ("count", count, (B,)))
+    if k_cache is None and (k_scale is not None or k_out is not None):
+        raise ValueError("k_scale and k_out need k_cache")
+    if k_cache is not None and k_scale is None:
+        raise ValueError("k_cache needs k_scale")
+    ks, vs = _scales(k_scale, v_scale, caches, idx)
+    if v_out is None:
+        if T is None or dtype is None:
+            raise ValueError("T and dtype are needed without v_out")
+        _fits(T=T)
+        v_out = torch.empty((B, Hkv, T, d), dtype=dtype, device=v_cache.device)
+    dt, full = v_out.dtype, v_out.shape
+    if len(full) != 4 or full[0] != B or full[1] != Hkv or full[3] != d:
+        raise ValueError("v_out must be [B, Hkv, T, d]")
+    if (T is not None and T != full[2]) or (dtype is not None and dtype != dt):
+        raise ValueError("v_out is of another T or dtype")
+    if k_cache is not None and k_out is None:
+        k_out = torch.empty(full, dtype=dt, device=v_cache.device)
+    _shapes(("k_out", k_out, full))
+    if status is not None and status.numel() * status.element_size() < 8:
+        raise ValueError("status needs 8 bytes")
+    _run("saf_kv_read_quant", _lib.saf_kv_read_quant, idx, _at(k_cache, idx, _E4M3), _at(v_cache, idx, _E4M3), ks, vs,
+         _at(page_table, idx, _I32), max_pages, _at(first, idx, _I32), _at(count, idx, _I32), B, Hkv, full[2], d,
+         num_pages, page_size, _dt(v_out), _at(k_out, idx, dt), _at(v_out, idx, dt),
+         None if status is None else _at(status, idx, status.dtype))
+    return k_out, v_out
+
+
+def saf_attn_paged_quant(q, k_cache, v_cache, k_scale, v_scale, page_table, ctx, max_len, n_new=None, a=None, r=None,
+                        frozen=None, window=0, sinks=0, o=None, lse=None, workspace=None, stream=None):
+    """saf_attn_paged over 8-bit caches (torch.float8_e4m3fn [num_pages, Hkv, page_size, d]) with fp32
+    scales [num_pages, Hkv, page_size]; q, o bf16 or fp32. workspace: alloc_paged_quant_workspace."""
+    if stream is not None:
+        return _on(stream, q, lambda: saf_attn_paged_quant(q, k_cache, v_cache, k_scale, v_scale, page_table, ctx,
+                   max_len, n_new, a, r, frozen, window, sinks, o, lse, workspace))
+    return _paged("saf_attn_paged_quant", _lib.saf_attn_paged_quant, q, k_cache, v_cache, (), 0, page_table, ctx,
+                  max_len, n_new, a, r, frozen, window, sinks, o, lse, workspace, (k_scale, v_scale))
+
+
+def saf_attn_paged_shared_quant(q, k_cache, v_cache, k_scale, v_scale, prefix_pages, prefix_len, page_table, ctx,
+                               max_len, n_new=None, a=None, r=None, frozen=None, window=0, sinks=0, o=None, lse=None,
+                               workspace=None, stream=None):
+    """saf_attn_paged_shared over 8-bit caches, as saf_attn_paged_quant."""
+    if stream is not None:
+        return _on(stream, q, lambda: saf_attn_paged_shared_quant(q, k_cache, v_cache, k_scale, v_scale, prefix_pages,
+                   prefix_len, page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o, lse, workspace))
+    if not -_2G <= prefix_len < _2G:
+        _fits(prefix_len=prefix_len)
+    if prefix_pages is not None and prefix_pages.numel() * v_cache.shape[2] < prefix_len:
+        raise ValueError("prefix_pages holds fewer pages than prefix_len tokens take")
+    prefix = (_at(prefix_pages, _device(q), torch.int32), prefix_len)
+    return _paged("saf_attn_paged_shared_quant", _lib.saf_attn_paged_shared_quant, q, k_cache, v_cache, prefix,
+                  prefix_len, page_table, ctx, max_len, n_new, a, r, frozen, window, sinks, o, lse, workspace,
+                  (k_scale, v_scale))
 
 
 def saf_set_trace_events(kernel: int, start=None, stop=None) -> None:
