@@ -192,7 +192,9 @@ __host__ __device__ constexpr int paged_tc_tile(int d, int rows) { return d == 6
 cudaError_t launch_paged_tc(const PagedArgs& p, cudaStream_t s);
 constexpr int kSimtRows = 8, kSimtTile = 32;
 cudaError_t launch_paged_simt(const PagedArgs& p, cudaStream_t s);
-// 8-bit caches: the same kernel, for q and o of bf16 or fp32.
-cudaError_t launch_paged_simt_q8(const PagedArgs& p, bool bf16, cudaStream_t s);
+cudaError_t launch_paged_simt_q8(const PagedArgs& p, cudaStream_t s);   // 8-bit caches, fp32 q and o
+// paged_q8_tc.cu: 8-bit caches, bf16 q and o, tensor cores; rows 8, 16 or 32 per block, tiles kQ8Tile.
+constexpr int kQ8Tile = 128;
+cudaError_t launch_paged_q8(const PagedArgs& p, cudaStream_t s);
 
 }  // namespace saf

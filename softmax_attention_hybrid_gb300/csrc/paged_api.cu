@@ -132,11 +132,14 @@ long long most_chunks(const Plan& x, int part, long long tiles) {
 }
 
 // Kernels of a call: by the type of q, and whether the cache is one of 8 bits.
-enum class Kind { kTc, kSimt, kSimtQ8 };
-Kind kind_of(saf_dtype_t dt, bool q8) { return q8 ? Kind::kSimtQ8 : dt == SAF_BF16 ? Kind::kTc : Kind::kSimt; }
+enum class Kind { kTc, kSimt, kTcQ8, kSimtQ8 };
+Kind kind_of(saf_dtype_t dt, bool q8) {
+    if (dt == SAF_BF16) return q8 ? Kind::kTcQ8 : Kind::kTc;
+    return q8 ? Kind::kSimtQ8 : Kind::kSimt;
+}
 
 Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, Kind kind) {
-    const bool bf16 = kind == Kind::kTc;
+    const bool bf16 = kind == Kind::kTc || kind == Kind::kTcQ8;
     Plan x;
     x.slots = bf16 ? kSlotsTc : kSlotsSimt;
     const long long G = H / Hkv;
@@ -147,6 +150,11 @@ Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, Kind kin
         // tensor cores: copies of the rows fill the 128 of a tile (paged_tc.cu)
         x.rows[i] = !bf16 ? kSimtRows : n[i] <= 32 ? 32 : n[i] <= 64 ? 64 : 128;
         x.tile[i] = bf16 ? paged_tc_tile(d, x.rows[i]) : kSimtTile;
+        if (kind == Kind::kTcQ8) {   // one kernel serves both parts: its rows are those of the larger need
+            const long long most = n[0] > n[1] ? n[0] : n[1];
+            x.rows[i] = most <= 8 ? 8 : most <= 16 ? 16 : 32;
+            x.tile[i] = kQ8Tile;
+        }
         // several blocks to a head: each head begins its own
         const long long per_head = n[i] / G;
         x.head_blocks[i] = per_head >= 4 * x.rows[i] ? (int)ceil_div(per_head, x.rows[i]) : 0;
@@ -329,8 +337,10 @@ int paged(const void* q, const void* k_cache, const void* v_cache, bool q8, cons
     cudaStream_t s = (cudaStream_t)stream;
     const bool bf16 = dt == SAF_BF16;
     before_launch(SAF_KERNEL_PAGED, s);
-    cudaError_t e = kind == Kind::kTc ? launch_paged_tc(p, s)
-                                      : kind == Kind::kSimt ? launch_paged_simt(p, s) : launch_paged_simt_q8(p, bf16, s);
+    cudaError_t e = kind == Kind::kTc      ? launch_paged_tc(p, s)
+                    : kind == Kind::kSimt ? launch_paged_simt(p, s)
+                    : kind == Kind::kTcQ8 ? launch_paged_q8(p, s)
+                                          : launch_paged_simt_q8(p, s);
     if (e == cudaSuccess && p.nsplit > 1) {
         note_launch();
         e = bf16 ? launch_join<__nv_bfloat16>(p, s) : launch_join<float>(p, s);

@@ -1,0 +1,678 @@
+// Paged attention over 8-bit caches on the tensor cores (bf16 q and o; see paged.h for the split).
+//
+// Few rows meet many keys in a decoding step, so the keys take the M = 128 lanes of the MMAs
+// and the rows (R = 8, 16 or 32 of a block) the columns:
+//     S^T [128 keys, rows] = K q^T,      O^T [d, rows] += V^T P^T,
+// with K and V as they lie in the cache: codes of e4m3 (kind::f8f6f4), never unpacked. A thread of
+// the softmax holds one key of the tile, with that key's two scales, for all rows.
+//
+// The other operand is e4m3 too, as a sum of terms in columns of their own, which are added in
+// fp32 when they are read:
+//   q, scaled by a power of two so that the row's largest lies in (224, 448]: hi = e4m3(q),
+//     lo = e4m3(16 (q - hi)), S = S_hi + S_lo / 16. Off by 2^-14 near zero, 2^-21 of the largest, else exact
+//     (bf16 has 8 bits, each term 4).
+//   w = P s_v 2^(4 - V) <= 256 with s_v <= 2^V the scales so far: hi = e4m3(w), mid = e4m3(16 (w - hi)),
+//     lo = e4m3(256 (w - hi - mid / 16)). Off by 2^-12 of itself (bf16: 2^-8), or 2^-18 near zero, 2^-22 of a
+//     weight at the maximum.
+// Sums are fp32 in tensor memory. The scale of a key multiplies its scores, that of its value the weight.
+//
+// The running maxima m (one per row) and V (one for all) are those of the whole block: a tile whose
+// scores stay below m + 4 and whose scales stay below 2^V leaves them (one barrier with an OR); else
+// they are found anew, and O and l are scaled.
+//
+// Warps (224 threads, two CTAs per SM): 0-3 softmax, 4 loads K, V and their scales (each of its lanes
+// fetches one page of the tile), 5 owns tensor memory and issues S, 6 issues P V.
+// Shared memory: q's terms (K-major, 128-byte swizzle), P's terms of two tiles (MN-major: the 16 bytes of
+// a key's columns next to each other), and a ring of tiles of 128 keys with their scales, filled in the order in
+// which the MMAs use them: K0, K1, V0, K2, V1, ... (V0, V1, ... where no row is ordinary). Rows of d < 128
+// codes are filled up with zeros by TMA.
+#include <string.h>
+
+#include "paged_tc.cuh"
+
+namespace saf {
+namespace {
+
+using namespace paged_tc;
+
+constexpr int kThreads = 224;
+constexpr int kTile = kQ8Tile;            // keys of a tile
+constexpr int kTileBytes = kTile * 128;
+constexpr int kScaleBytes = kTile * 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 4.0f;            // scores may pass the maximum by this much (base 2)
+constexpr float kWeight = 16.0f;          // 2^(8 - kSlack): a weight of the maximum, before the value's scale
+
+struct Q8Params {
+    CUtensorMap tm_k, tm_v;
+    PagedArgs a;
+    int box;   // keys of a TMA box: min(page, 128)
+};
+
+template <int R>
+struct Cfg {
+    static constexpr int ns = 2 * R;                  // columns of S: hi, lo
+    static constexpr int blocks = (3 * R + 15) / 16;  // 16-byte blocks of a key's weights: hi, mid, lo
+    static constexpr int np = 16 * blocks;            // columns of O
+    static constexpr int slots = R == 8 ? 6 : R == 16 ? 5 : 4;
+    static constexpr int ring = 0;
+    static constexpr int q = ring + slots * kTileBytes;
+    static constexpr int p = q + ns * 128;
+    static constexpr int p_bytes = blocks * kTile * 16;
+    static constexpr int scales = p + 2 * p_bytes;
+    static constexpr int total = scales + slots * kScaleBytes;
+    static constexpr uint32_t col_o = 2 * ns;         // S of two tiles, then O
+    static constexpr uint32_t cols = R == 8 ? 64 : R == 16 ? 128 : 256;
+    static_assert(col_o + np <= cols, "tensor memory");
+    static_assert(p % 128 == 0 && q % 1024 == 0, "operand alignment");
+};
+constexpr int kMaxSlots = 6;
+
+struct Bars {
+    uint64_t full[kMaxSlots], empty[kMaxSlots];
+    uint64_t s_full[2], s_empty[2], p_ready[2], o_done[2], mma_idle[2];
+};
+
+struct Shared {
+    Bars bars;
+    uint32_t tmem_base;
+    int abort_flag, imin, imax, kinds, lost;
+    // rows of the block
+    int out_row[32], pos[32];      // place in o (-1: none), last visible slot of the part (-1: none)
+    float scale[32];               // what a score times its key's scale is multiplied by: log2(e) / sqrt(d), and q's factor back
+    uint32_t frozen;               // bit per row
+    const float* a[32];            // frozen rows: a and r at the part's slot 0 and at the row's distance from it
+    const float* r[32];
+    float m[32];                   // running maxima
+    float part[4][32 + 1];         // the warps' maxima (and of the scales), and sums
+};
+
+struct Work {
+    PagedItem it;
+    PagedRange g;
+    int e0, e1;       // tiles
+    int imin, imax;   // positions of the rows that see anything
+    int off;          // position of the part's slot 0
+    int there;        // rows of the block that are rows of the output
+    bool any_ord;     // an ordinary row is among them: K is loaded
+
+    // place of tile e0 + j's K and V in the order of loads
+    __device__ __forceinline__ int k_load(int j) const { return j == 0 ? 0 : 2 * j - 1; }
+    __device__ __forceinline__ int v_load(int j) const {
+        if (!any_ord) return j;
+        return j + 1 < e1 - e0 ? 2 * j + 2 : 2 * j + 1;
+    }
+};
+
+// OR over the 128 softmax threads, who all wait for each other.
+__device__ __forceinline__ bool rows_any(bool x) {
+    uint32_t y;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(y)
+        : "r"((uint32_t)x)
+        : "memory");
+    return y != 0;
+}
+__device__ __forceinline__ void rows_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+// Largest of a warp's values (NaN left out), by integers that have the order of the floats.
+__device__ __forceinline__ float warp_max(float x) {
+    int k = x == x ? __float_as_int(x) : (int)0xff800000;
+    k ^= (k >> 31) & 0x7fffffff;
+    k = __reduce_max_sync(0xffffffffu, k);
+    return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+}
+
+__device__ __forceinline__ float pow2i(int e) {   // 2^e, -149 <= e <= 127
+    return e >= -126 ? __int_as_float((e + 127) << 23) : __int_as_float(1 << (e + 149));
+}
+
+// The loading warp. Lane l fetches box l of every tile, from its page, and the box's scales.
+template <int R>
+__device__ __forceinline__ void load_warp(const Q8Params& P, const Work& w, uint8_t* sm, Bars& bars,
+                                          volatile int* abort) {
+    using C = Cfg<R>;
+    const PagedArgs& p = P.a;
+    const int lane = threadIdx.x & 31;
+    const int nbox = kTile / P.box, n = w.e1 - w.e0;
+    const int in_page = (1 << p.page_log2) - 1;
+    const uint32_t box_bytes = (uint32_t)P.box * (128u + 4u);
+    // The pages of a batch of tiles are looked up together, lane l those of tile l / nbox, box
+    // l mod nbox, a batch ahead of their use: a lookup for each tile would wait for the memory
+    // in every one.
+    const int batch = 32 / nbox;
+    auto look = [&](int first) -> int {   // a page as the table has it, -1: nothing to fetch
+        const int j = first + lane / nbox;
+        if (j >= n) return -1;
+        const int bx = paged_tile(w.g, w.e0 + j) * kTile + (lane & (nbox - 1)) * P.box;
+        if (!box_seen(w.g, bx, P.box)) return -1;
+        const int at = bx >> p.page_log2;
+        return __ldg(w.it.part ? p.page_table + (size_t)w.it.b * p.max_pages + at : p.prefix_pages + at);
+    };
+    int looked = look(0), ahead = look(batch);   // tiles [base, base + batch), and the batch behind
+    int base = 0;
+    if (lane == 0) {
+        tma_prefetch_desc(&P.tm_k);
+        tma_prefetch_desc(&P.tm_v);
+    }
+    auto page_of = [&](int j) -> int {   // my box's page of tile j (ascending), -1: nothing to fetch
+        if (j == base + batch) {
+            base = j;
+            looked = ahead;
+            ahead = look(base + batch);
+        }
+        const int pg = __shfl_sync(0xffffffffu, looked, ((j - base) * nbox + lane) & 31);
+        return lane < nbox && pg >= 0 && pg < p.num_pages ? pg : -1;
+    };
+    auto fetch = [&](int load, const CUtensorMap* map, const float* scales, int j, int pg) -> bool {
+        const int s = load % C::slots;
+        if (!wait_all(&bars.empty[s], ((load / C::slots) & 1) ^ 1u, abort, p.status)) return false;
+        const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0);
+        if (lane == 0) mbar_expect_tx(&bars.full[s], __popc(have) * box_bytes);
+        __syncwarp();
+        if (pg >= 0) {
+            const int in = (paged_tile(w.g, w.e0 + j) * kTile + lane * P.box) & in_page;
+            const int z = pg * p.Hkv + w.it.hk;
+            tma_load_3d(sm + C::ring + s * kTileBytes + lane * P.box * 128, map, &bars.full[s], 0, in, z);
+            bulk_load(sm + C::scales + s * kScaleBytes + lane * P.box * 4, scales + ((size_t)z << p.page_log2) + in,
+                      (uint32_t)P.box * 4u, &bars.full[s]);
+        }
+        __syncwarp();
+        return true;
+    };
+    int pg = page_of(0);
+    bool ok = !w.any_ord || fetch(0, &P.tm_k, p.k_scale, 0, pg);
+    for (int j = 0; j < n && ok; ++j) {
+        const int next = j + 1 < n ? page_of(j + 1) : -1;
+        if (w.any_ord && j + 1 < n) ok = fetch(w.k_load(j + 1), &P.tm_k, p.k_scale, j + 1, next);
+        ok = ok && fetch(w.v_load(j), &P.tm_v, p.v_scale, j, pg);
+        pg = next;
+    }
+}
+
+// q's terms of the block's ordinary rows, a warp per row, and the rows' factors.
+template <int R>
+__device__ __forceinline__ void put_q(const Q8Params& P, const Work& w, uint8_t* sm, Shared& sh) {
+    const PagedArgs& p = P.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int r = warp; r < R; r += 4) {
+        if (r >= w.there || sh.pos[r] < 0 || ((sh.frozen >> r) & 1u)) continue;   // (uniform)
+        const bool mine = 4 * lane < p.d;
+        uint2 x = make_uint2(0, 0);
+        if (mine) x = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)p.q + (size_t)sh.out_row[r] * p.d) + lane);
+        const float v[4] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                            __uint_as_float(x.y & 0xffff0000u)};
+        // the row's largest magnitude as bits: above 0x7f7fffff it holds an infinity or a NaN
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) top = max(top, __float_as_uint(v[c]) & 0x7fffffffu);
+        top = __reduce_max_sync(0xffffffffu, top);
+        // 448 = 1.75 x 2^8
+        int e = 8 - ((int)(top >> 23) - 127) - ((top & 0x7fffffu) > 0x600000u);
+        e = top >= 0x7f800000u ? 0 : e < -120 ? -120 : e > 120 ? 120 : e;
+        const float f = pow2i(e);
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float y0 = v[2 * c] * f, y1 = v[2 * c + 1] * f;
+            hi[c] = pack_e4m3(y0, y1);
+            const float2 z = unpack_e4m3(hi[c]);
+            lo[c] = pack_e4m3(16.f * (y0 - z.x), 16.f * (y1 - z.y));
+        }
+        uint32_t word[2] = {hi[0] | hi[1] << 16, lo[0] | lo[1] << 16};
+        if (top >= 0x7f800000u) word[0] = word[1] = 0x7f7f7f7fu;   // (saturation would hide an infinity)
+        if (mine) {
+            *reinterpret_cast<uint32_t*>(sm + Cfg<R>::q + sw128_offset(r, 4 * lane)) = word[0];
+            *reinterpret_cast<uint32_t*>(sm + Cfg<R>::q + sw128_offset(R + r, 4 * lane)) = word[1];
+        }
+        if (lane == 0) sh.scale[r] = p.scale_log2 * pow2i(-e);
+    }
+}
+
+template <int R>
+__device__ __forceinline__ void read_s(uint32_t addr, float* s) {   // hi + lo / 16
+    if constexpr (R == 8) {
+        uint32_t x[16];
+        tmem_ld16(addr, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int r = 0; r < 8; ++r) s[r] = fmaf(__uint_as_float(x[8 + r]), 0.0625f, __uint_as_float(x[r]));
+    } else if constexpr (R == 16) {
+        uint32_t x[32];
+        tmem_ld32(addr, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = fmaf(__uint_as_float(x[16 + r]), 0.0625f, __uint_as_float(x[r]));
+    } else {
+        uint32_t x[32], y[32];
+        tmem_ld32(addr, x);
+        tmem_ld32(addr + 32, y);
+        tmem_ld_wait();
+#pragma unroll
+        for (int r = 0; r < 32; ++r) s[r] = fmaf(__uint_as_float(y[r]), 0.0625f, __uint_as_float(x[r]));
+    }
+}
+
+// Warps 0-3. Thread t holds key t of every tile.
+template <int R>
+__device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool lost, uint8_t* sm, Shared& sh) {
+    using C = Cfg<R>;
+    const PagedArgs& p = P.a;
+    Bars& bars = sh.bars;
+    volatile int* abort = &sh.abort_flag;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const uint32_t tmem = sh.tmem_base + ((uint32_t)(warp * 32) << 16);
+    const int there = w.there;
+    const uint32_t frozen = sh.frozen;
+    const int my_box = t / P.box * P.box;
+    float l[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) l[r] = 0.f;
+    float vtop = 0.f, vinv = 0.f;   // 2^V (0: no value seen yet) and 2^-V
+    int vexp = 0;
+    bool ok = true;
+
+    int n = 0;
+    for (int e = w.e0; e < w.e1; ++e, ++n) {
+        const int x0 = paged_tile(w.g, e) * kTile, x = x0 + t, buf = n & 1;
+        float s[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[r] = -INFINITY;
+        // the fixed patterns' logits (Eq. 3): neighbouring keys, neighbouring entries
+        if (frozen) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if ((frozen >> r) & 1u) {
+                    const int y = max(min(x, sh.pos[r]), 0);   // (keys past the row's own position are masked below)
+                    s[r] = (__ldg(sh.a[r] + y) + __ldg(sh.r[r] - y)) * kLog2e;
+                }
+        }
+        float ks = 0.f;
+        if (w.any_ord) {
+            const int ld = w.k_load(n), slot = ld % C::slots;
+            ok = mbar_wait(&bars.s_full[buf], (n >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
+            ok = mbar_wait(&bars.full[slot], (ld / C::slots) & 1, abort, p.status, kStatusTimeout) && ok;
+            __syncwarp();
+            tc_fence_after();
+            ks = reinterpret_cast<const float*>(sm + C::scales + slot * kScaleBytes)[t];
+            float q[R];
+            read_s<R>(tmem + buf * C::ns, q);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars.s_empty[buf]);
+                mbar_arrive(&bars.empty[slot]);
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r < there && !((frozen >> r) & 1u)) s[r] = q[r] * (ks * sh.scale[r]);
+        }
+        const int ldv = w.v_load(n), vslot = ldv % C::slots;
+        ok = mbar_wait(&bars.full[vslot], (ldv / C::slots) & 1, abort, p.status, kStatusTimeout) && ok;
+        float vs = reinterpret_cast<const float*>(sm + C::scales + vslot * kScaleBytes)[t];
+        // masks, in tiles that some row does not see whole
+        if (lost || x0 + kTile > w.g.hi || x0 + kTile - 1 > w.imin - w.off ||
+            (p.window > 0 && x0 <= w.imax - w.off - p.window)) {
+            const bool have = !(lost && box_seen(w.g, x0 + my_box, P.box) && paged_page(p, w.it, x0 + my_box) < 0);
+            const bool any = have && x < w.g.hi && (x >= w.g.lo || x < w.g.sink);
+            const int sink = p.sinks - w.off;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r < there) {
+                    const int i = sh.pos[r];
+                    const int lo = ((frozen >> r) & 1u) || p.window == 0 ? -1 : i - p.window;   // slots <= lo: sinks only
+                    if (!(any && x <= i && (x > lo || x < sink))) s[r] = -INFINITY;
+                }
+            if (!any) {   // codes and scales of slots that no row sees may be anything: zeros, for 0 * NaN is none
+                vs = 0.f;
+                uint4* row = reinterpret_cast<uint4*>(sm + C::ring + vslot * kTileBytes + t * 128);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
+            }
+        }
+        bool up = vs > vtop;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (r < there) up |= s[r] > sh.m[r] + kSlack;
+        if (rows_any(up || !ok)) {
+            if (rows_any(!ok)) break;   // every thread leaves here
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r < there) {
+                    const float mx = warp_max(s[r]);
+                    if (lane == 0) sh.part[warp][r] = mx;
+                }
+            {
+                const float mx = warp_max(vs);
+                if (lane == 0) sh.part[warp][32] = mx;
+            }
+            rows_sync();
+            const float vmax = fmaxf(fmaxf(sh.part[0][32], sh.part[1][32]), fmaxf(sh.part[2][32], sh.part[3][32]));
+            float fv = 1.f;   // of O, for the scales
+            if (vmax > vtop) {
+                int ex = (int)((__float_as_uint(vmax) >> 23) & 255u) - 126;   // vmax < 2^ex
+                ex = ex < -125 ? -125 : ex > 127 ? 127 : ex;
+                fv = vtop > 0.f ? exp2f((float)(vexp - ex)) : 0.f;
+                vexp = ex;
+                vtop = pow2i(ex);
+                vinv = pow2i(-ex);
+            }
+            const bool scale_o = n > 0;
+            if (scale_o)   // P V of the previous tile is done: O is stable
+                ok = mbar_wait(&bars.o_done[buf ^ 1], ((n - 1) >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
+            __syncwarp();
+            tc_fence_after();
+            float f[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                f[r] = 1.f;
+                if (r < there) {
+                    const float old = sh.m[r];
+                    const float now = fmaxf(fmaxf(fmaxf(sh.part[0][r], sh.part[1][r]), fmaxf(sh.part[2][r], sh.part[3][r])), old);
+                    if (now > old) f[r] = fast_exp2(old - now);
+                    l[r] *= f[r];
+                }
+            }
+            if (scale_o) {
+#pragma unroll
+                for (int c = 0; c < C::np; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(tmem + C::col_o + c, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * (f[(c + k) % R] * fv));
+                    tmem_st16(tmem + C::col_o + c, o);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+            }
+            rows_sync();   // the old maxima are read
+            if (t < there) {
+                const float now = fmaxf(fmaxf(sh.part[0][t], sh.part[1][t]), fmaxf(sh.part[2][t], sh.part[3][t]));
+                sh.m[t] = fmaxf(sh.m[t], now);
+            }
+            rows_sync();
+        }
+        if (n > 1)   // P V of the tile before the previous one is done: its weights' buffer is free
+            ok = mbar_wait(&bars.o_done[buf], ((n - 2) >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
+        const float vw = vs * vinv * kWeight;
+        uint8_t* mine = sm + C::p + buf * C::p_bytes + t * 16;
+        uint32_t word[3 * R / 4];   // bytes: columns of the terms, hi, mid, lo
+#pragma unroll
+        for (int r = 0; r < R; r += 4) {
+            float y[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                y[c] = 0.f;
+                if (r + c < there) {
+                    const float m = sh.m[r + c];
+                    const float pr = fast_exp2(s[r + c] - (m == -INFINITY ? 0.f : m));   // (a row that has seen no key yet)
+                    l[r + c] += pr;
+                    y[c] = pr * vw;
+                }
+            }
+            uint32_t h[2], md[2], lo[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                h[c] = pack_e4m3(y[2 * c], y[2 * c + 1]);
+                float2 z = unpack_e4m3(h[c]);
+                const float a0 = 16.f * (y[2 * c] - z.x), a1 = 16.f * (y[2 * c + 1] - z.y);
+                md[c] = pack_e4m3(a0, a1);
+                z = unpack_e4m3(md[c]);
+                lo[c] = pack_e4m3(16.f * (a0 - z.x), 16.f * (a1 - z.y));
+            }
+            word[r / 4] = h[0] | h[1] << 16;
+            word[R / 4 + r / 4] = md[0] | md[1] << 16;
+            word[R / 2 + r / 4] = lo[0] | lo[1] << 16;
+        }
+#pragma unroll
+        for (int b = 0; b < C::blocks; ++b) {
+            uint4 z;
+            z.x = word[4 * b];
+            z.y = word[4 * b + 1];
+            z.z = 4 * b + 2 < 3 * R / 4 ? word[4 * b + 2 < 3 * R / 4 ? 4 * b + 2 : 0] : 0u;
+            z.w = 4 * b + 3 < 3 * R / 4 ? word[4 * b + 3 < 3 * R / 4 ? 4 * b + 3 : 0] : 0u;
+            *reinterpret_cast<uint4*>(mine + b * kTile * 16) = z;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&bars.p_ready[buf]);
+            mbar_arrive(&bars.empty[vslot]);
+        }
+    }
+    // (a lane whose wait ran out has left with all the others, or does so here)
+    if (n > 0) ok = mbar_wait(&bars.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
+    __syncwarp();
+    tc_fence_after();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (r >= there) continue;
+        float x = l[r];
+        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == 0) sh.part[warp][r] = x;
+    }
+    if (rows_any(!ok)) return;
+    // O of element t of a row: the terms' sums
+    const int split = w.it.part ? p.chunks[0] + w.it.chunk : w.it.chunk;
+    const float back = pow2i(vexp - 4 < -149 ? -149 : vexp - 4);   // 2^V / kWeight
+    float o[R];
+#pragma unroll
+    for (int term = 2; term >= 0; --term) {
+#pragma unroll
+        for (int c = 0; c < R; c += 8) {
+            uint32_t y[8];
+            tmem_ld8(tmem + C::col_o + term * R + c, y);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                o[c + k] = term == 2 ? __uint_as_float(y[k]) : fmaf(o[c + k], 0.0625f, __uint_as_float(y[k]));
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (r >= there) continue;
+        const size_t at = (size_t)sh.out_row[r];
+        const bool sees = sh.pos[r] >= 0;
+        const float lr = sees ? (sh.part[0][r] + sh.part[1][r]) + (sh.part[2][r] + sh.part[3][r]) : 0.f;
+        const float mr = sees ? sh.m[r] : -INFINITY;
+        const float y = lr != 0.f ? o[r] * back : 0.f;
+        if (p.nsplit > 1) {
+            if (t < p.d) p.po[(at * p.nsplit + split) * p.d + t] = y;
+            if (t == 0) p.ml[at * p.nsplit + split] = make_float2(mr, lr);
+        } else {
+            if (t < p.d) ((__nv_bfloat16*)p.o)[at * p.d + t] = __float2bfloat16_rn(lr != 0.f ? y / lr : 0.f);
+            if (t == 0) p.lse[at] = lr != 0.f ? (mr + log2f(lr)) * kLn2 : -INFINITY;
+        }
+    }
+}
+
+// Every warp but the loading one: q's terms, tensor memory and the check of the pages are done.
+__device__ __forceinline__ void set_up_done() {
+    tc_fence_before();
+    asm volatile("bar.sync 2, 192;" ::: "memory");
+    tc_fence_after();
+}
+
+template <int R>
+__global__ void __launch_bounds__(kThreads, 2) paged_q8_kernel(const __grid_constant__ Q8Params P) {
+    using C = Cfg<R>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ Shared sh;
+    const PagedArgs& p = P.a;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    Work w;
+    w.it = paged_item(p, blockIdx.x);
+    const PagedBlock block = paged_block(p, w.it);
+    w.off = w.it.part ? p.P : 0;
+    w.there = block.there;
+    if (warp == 0) {   // the block's rows, a lane each
+        const PagedRow row = paged_row(p, w.it, block, lane);
+        sh.out_row[lane] = row.there ? (int)paged_out_row(p, row) : -1;
+        sh.pos[lane] = row.i < 0 ? -1 : row.i - w.off;
+        sh.m[lane] = -INFINITY;
+        sh.scale[lane] = 0.f;
+        sh.a[lane] = p.a + (size_t)row.h * p.ld + w.off;
+        sh.r[lane] = p.r + (size_t)row.h * p.ld + (row.i < 0 ? 0 : row.i - w.off);
+        const bool seen = row.i >= 0;
+        const uint32_t fz = __ballot_sync(0xffffffffu, seen && row.frozen);
+        const uint32_t ord = __ballot_sync(0xffffffffu, seen && !row.frozen);
+        const int lo = __reduce_min_sync(0xffffffffu, seen ? row.i : 0x7fffffff);
+        const int hi = __reduce_max_sync(0xffffffffu, row.i);
+        if (lane == 0) {
+            sh.imin = lo;
+            sh.imax = hi;
+            sh.frozen = fz;
+            sh.kinds = (ord ? 1 : 0) | (fz ? 2 : 0);
+        }
+    } else if (t == 32) {
+        sh.abort_flag = sh.lost = 0;
+        for (int i = 0; i < C::slots; ++i) {
+            mbar_init(&sh.bars.full[i], 1);
+            mbar_init(&sh.bars.empty[i], 5);   // the MMAs, and four warps that read the scales
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.bars.s_full[i], 1);
+            mbar_init(&sh.bars.s_empty[i], 4);
+            mbar_init(&sh.bars.p_ready[i], 4);
+            mbar_init(&sh.bars.o_done[i], 1);
+            mbar_init(&sh.bars.mma_idle[i], 1);
+        }
+        fence_mbar_init();
+    } else if (t == 64 && w.it.part == 1 && w.it.chunk == 0 && w.it.rb == 0 && w.it.hk == 0) {
+        int c;   // each sequence's counts are checked once
+        bool bad;
+        paged_tokens(p, w.it.b, &c, &bad);
+        if (bad) atomicOr(p.status, kStatusPage);
+    }
+    __syncthreads();
+    w.imin = sh.imin;
+    w.imax = sh.imax;
+    w.any_ord = (sh.kinds & 1) != 0;
+    w.g = paged_range(p, w.it, w.imin, w.imax, (sh.kinds & 2) != 0 || p.window == 0);
+    const int per = p.per_chunk[w.it.part];
+    w.e0 = min(w.it.chunk * per, w.g.n);
+    w.e1 = min(w.e0 + per, w.g.n);
+    if (w.e0 >= w.e1) {   // no keys: nothing but the rows' empty sums
+        write_empty(p, w.it, w.there, sh.out_row, kThreads);
+        return;
+    }
+    const int n = w.e1 - w.e0;
+    Bars& bars = sh.bars;
+    volatile int* abort = &sh.abort_flag;
+    if (warp == 4) {   // K and V need nothing but the range of keys: on their way under the rest of the set-up
+        load_warp<R>(P, w, sm, bars, abort);
+    } else if (warp < 4) {
+        if (w.any_ord) {
+            put_q<R>(P, w, sm, sh);
+            fence_proxy_async_smem();
+        }
+        set_up_done();
+        const bool lost = sh.lost != 0;
+        if (lost && t == 0) atomicOr(p.status, kStatusPage);
+        row_warps<R>(P, w, lost, sm, sh);
+    } else {
+        if (warp == 5) {
+            tmem_alloc(&sh.tmem_base, C::cols);
+            tmem_relinquish();
+        }
+        {   // pages that the item needs and the table does not have
+            const int nbox = kTile / P.box, end = n * nbox;
+            bool lost = false;
+            for (int b = t - 160; b < end; b += 64) {
+                const int bx = paged_tile(w.g, w.e0 + b / nbox) * kTile + (b & (nbox - 1)) * P.box;
+                if (box_seen(w.g, bx, P.box) && paged_page(p, w.it, bx) < 0) lost = true;
+            }
+            if (lost) sh.lost = 1;
+        }
+        set_up_done();
+        const uint32_t tmem = sh.tmem_base;
+        const uint32_t ring = smem_u32(sm + C::ring);
+        if (warp == 5) {
+            // S of tile j, when K is there and the rows have read S of tile j - 2
+            constexpr uint32_t id_s = idesc_e4m3(128, C::ns, 0, 0);
+            const uint64_t d_q = sdesc_sw128(smem_u32(sm + C::q), 16, 1024);   // K-major, as K
+            const uint64_t d_ring = sdesc_sw128(ring, 16, 1024);
+            const int steps = p.d / 32;
+            for (int j = 0; j < n && w.any_ord; ++j) {
+                const int ld = w.k_load(j), s = ld % C::slots;
+                if (!wait_all(&bars.full[s], (ld / C::slots) & 1, abort, p.status)) break;
+                if (j > 1 && !wait_all(&bars.s_empty[j & 1], ((j - 2) >> 1) & 1, abort, p.status)) break;
+                tc_fence_after();
+                const uint64_t d_k = sdesc_advance(d_ring, s * kTileBytes);
+                for (int k = 0; k < steps; ++k)
+                    mma_ss_e4m3_warp(tmem + (j & 1) * C::ns, sdesc_advance(d_k, 32 * k), sdesc_advance(d_q, 32 * k),
+                                     id_s, k > 0);
+                mma_commit_warp(&bars.s_full[j & 1]);
+                mma_commit_warp(&bars.empty[s]);
+            }
+        } else {
+            // O^T += V^T P^T of tile j, when V and the weights are there
+            constexpr uint32_t id_o = idesc_e4m3(128, C::np, 1, 1);
+            const uint64_t d_ring = sdesc_sw128(ring, 16384, 1024);                        // MN-major
+            const uint64_t d_p = sdesc_none(smem_u32(sm + C::p), 128, kTile * 16);
+            for (int j = 0; j < n; ++j) {
+                const int ld = w.v_load(j), s = ld % C::slots;
+                if (!wait_all(&bars.full[s], (ld / C::slots) & 1, abort, p.status)) break;
+                if (!wait_all(&bars.p_ready[j & 1], (j >> 1) & 1, abort, p.status)) break;
+                tc_fence_after();
+                const uint64_t d_v = sdesc_advance(d_ring, s * kTileBytes);
+                const uint64_t d_w = sdesc_advance(d_p, (j & 1) * C::p_bytes);
+#pragma unroll
+                for (int k = 0; k < kTile / 32; ++k)
+                    mma_ss_e4m3_warp(tmem + C::col_o, sdesc_advance(d_v, 4096 * k), sdesc_advance(d_w, 512 * k), id_o,
+                                     (j > 0 || k > 0) ? 1u : 0u);
+                mma_commit_warp(&bars.o_done[j & 1]);
+                mma_commit_warp(&bars.empty[s]);
+            }
+        }
+        // every MMA issued here is done before tensor memory is freed
+        mma_commit_warp(&bars.mma_idle[warp - 5]);
+        if (lane == 0) mbar_wait_bounded(&bars.mma_idle[warp - 5], 0, kWaitLimitNs);
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(sh.tmem_base, C::cols);
+    }
+}
+
+template <int R>
+cudaError_t launch_r(const Q8Params& P, cudaStream_t s) {
+    constexpr int smem = Cfg<R>::total + 1024;
+    static_assert(Cfg<R>::slots <= kMaxSlots, "barriers of the ring");
+    const cudaError_t e =
+        cudaFuncSetAttribute(paged_q8_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_ex(paged_q8_kernel<R>, dim3(P.a.items), dim3(kThreads), (size_t)smem, s, true, 1, P);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_q8(const PagedArgs& a, cudaStream_t s) {
+    Q8Params P;
+    P.a = a;
+    const int page = 1 << a.page_log2;
+    P.box = page < kTile ? page : kTile;
+    const uint64_t slices = (uint64_t)a.num_pages * a.Hkv;
+    const void* k = a.k_cache ? a.k_cache : a.v_cache;   // (no K is loaded when every head is frozen)
+    if (!make_tmap_u8_3d(&P.tm_k, k, a.d, page, slices, 128, P.box) ||
+        !make_tmap_u8_3d(&P.tm_v, a.v_cache, a.d, page, slices, 128, P.box))
+        return cudaErrorInvalidValue;
+    switch (a.rows[1]) {
+        case 8: return launch_r<8>(P, s);
+        case 16: return launch_r<16>(P, s);
+        default: return launch_r<32>(P, s);
+    }
+}
+
+}  // namespace saf

@@ -77,8 +77,8 @@ struct Codes {
     }
 };
 
-// E: the type of q and o. kQ8: 8-bit caches (else of type E, float).
-template <int D, typename E, bool kQ8>
+// kQ8: 8-bit caches.
+template <int D, bool kQ8>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_constant__ PagedArgs p) {
     extern __shared__ __align__(16) uint8_t raw[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
@@ -153,10 +153,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
         for (int u = tid; u < R * (D / 4); u += kThreads) {
             const int rr = u / (D / 4), c = 4 * (u - rr * (D / 4));
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (sm.pos[rr] >= 0 && !sm.frozen[rr]) {
-                const E* src = (const E*)p.q + (size_t)sm.out[rr] * D + c;
-                x = make_float4(to_f(src[0]), to_f(src[1]), to_f(src[2]), to_f(src[3]));
-            }
+            if (sm.pos[rr] >= 0 && !sm.frozen[rr])
+                x = *reinterpret_cast<const float4*>((const float*)p.q + (size_t)sm.out[rr] * D + c);
             *reinterpret_cast<float4*>(&sm.q[rr][c]) = x;
         }
     __syncthreads();
@@ -306,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
             const size_t row = (size_t)sm.out[x];
             const float lx = sm.l[x];
             if (p.nsplit == 1) {
-                from_f((E*)p.o + row * D + col, lx != 0.f ? acc[x] / lx : 0.f);
+                ((float*)p.o)[row * D + col] = lx != 0.f ? acc[x] / lx : 0.f;
                 if (col == 0) p.lse[row] = lx != 0.f ? (sm.m[x] + log2f(lx)) * kLn2 : -INFINITY;
             } else {
                 p.po[(row * p.nsplit + split) * D + col] = acc[x];
@@ -316,30 +314,28 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
     }
 }
 
-template <int D, typename E, bool kQ8>
+template <int D, bool kQ8>
 cudaError_t launch_d(const PagedArgs& p, cudaStream_t s) {
     const size_t smem = sizeof(Smem<D>);
     cudaError_t e =
-        cudaFuncSetAttribute(paged_simt_kernel<D, E, kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(paged_simt_kernel<D, kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_ex(paged_simt_kernel<D, E, kQ8>, dim3(p.items), dim3(kThreads), smem, s, true, 1, p);
+    return launch_ex(paged_simt_kernel<D, kQ8>, dim3(p.items), dim3(kThreads), smem, s, true, 1, p);
 }
 
-template <typename E, bool kQ8>
+template <bool kQ8>
 cudaError_t launch_type(const PagedArgs& p, cudaStream_t s) {
     switch (p.d) {
-        case 96: return launch_d<96, E, kQ8>(p, s);
-        case 128: return launch_d<128, E, kQ8>(p, s);
-        default: return launch_d<64, E, kQ8>(p, s);
+        case 96: return launch_d<96, kQ8>(p, s);
+        case 128: return launch_d<128, kQ8>(p, s);
+        default: return launch_d<64, kQ8>(p, s);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_paged_simt(const PagedArgs& p, cudaStream_t s) { return launch_type<float, false>(p, s); }
+cudaError_t launch_paged_simt(const PagedArgs& p, cudaStream_t s) { return launch_type<false>(p, s); }
 
-cudaError_t launch_paged_simt_q8(const PagedArgs& p, bool bf16, cudaStream_t s) {
-    return bf16 ? launch_type<__nv_bfloat16, true>(p, s) : launch_type<float, true>(p, s);
-}
+cudaError_t launch_paged_simt_q8(const PagedArgs& p, cudaStream_t s) { return launch_type<true>(p, s); }
 
 }  // namespace saf

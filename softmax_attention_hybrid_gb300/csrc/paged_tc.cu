@@ -32,13 +32,12 @@
 
 #include <atomic>
 
-#include "paged.h"
-#include "tc_common.cuh"
+#include "paged_tc.cuh"
 
 namespace saf {
 namespace {
 
-using namespace tc;
+using namespace paged_tc;
 
 constexpr int kThreads = 256;
 // Register split (setmaxnreg): warps 4-7 drop to kRegsOther, the row warps rise to kRegsRows, within
@@ -83,12 +82,6 @@ struct Bars {
     uint64_t s_full, s_empty, p_ready, o_done, pat_full[2], pat_empty[2], mma_idle[2];
 };
 
-__device__ __forceinline__ float fast_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 template <int N>
 __device__ __forceinline__ void tmem_ld_n(uint32_t addr, uint32_t* r) {
     if constexpr (N == 64) {
@@ -131,16 +124,6 @@ struct Work {
     // key) .. imax - (first key), rounded up to whole 16 bytes
     __device__ __forceinline__ int pitch(int TK) const { return (2 * TK + (imax - imin) + 3) & ~3; }
 };
-
-// A wait of a converged warp: every lane waits and the warp goes on, or gives up, together.
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, kStatusTimeout));
-}
-
-// Whether keys [bx, bx + box) of the part hold one that some row sees.
-__device__ __forceinline__ bool box_seen(const PagedRange& g, int bx, int box) {
-    return bx < g.hi && (bx + box > g.lo || bx < g.sink);
-}
 
 // The loading warp. Lane l fetches box l of every tile, from its page.
 template <int kD, int TK>
@@ -662,17 +645,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_tc_kernel(const __grid_cons
     w.e0 = min(w.it.chunk * per, w.g.n);
     w.e1 = min(w.e0 + per, w.g.n);
     if (w.e0 >= w.e1) {   // no keys: nothing but the rows' empty sums
-        const int split = w.it.part ? p.chunks[0] + w.it.chunk : w.it.chunk;
-        if (p.nsplit > 1) {
-            for (int x = t; x < w.there; x += kThreads)
-                p.ml[(size_t)sh.out_row[x] * p.nsplit + split] = make_float2(-INFINITY, 0.f);
-        } else {
-            for (int x = warp; x < w.there; x += kThreads / 32) {
-                const size_t at = (size_t)sh.out_row[x];
-                for (int c = 2 * lane; c < p.d; c += 64) *reinterpret_cast<uint32_t*>((__nv_bfloat16*)p.o + at * p.d + c) = 0u;
-                if (lane == 0) p.lse[at] = -INFINITY;
-            }
-        }
+        write_empty(p, w.it, w.there, sh.out_row, kThreads);
         return;
     }
     // the block's frozen heads: of its members of the group those from gord on

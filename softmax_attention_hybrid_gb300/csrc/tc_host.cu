@@ -46,6 +46,11 @@ bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t
     return make_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, n0, n1, n2, b0, b1);
 }
 
+bool make_tmap_u8_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1, uint64_t n2, uint32_t b0,
+                     uint32_t b1) {
+    return make_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, n0, n1, n2, b0, b1);
+}
+
 bool make_tmap_f32_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1, uint64_t n2, uint32_t b0,
                       uint32_t b1) {
     return make_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, n0, n1, n2, b0, b1);
