@@ -152,7 +152,7 @@ Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, Kind kin
         x.tile[i] = bf16 ? paged_tc_tile(d, x.rows[i]) : kSimtTile;
         if (kind == Kind::kTcQ8) {   // one kernel serves both parts: its rows are those of the larger need
             const long long most = n[0] > n[1] ? n[0] : n[1];
-            x.rows[i] = most <= 8 ? 8 : most <= 16 ? 16 : 32;
+            x.rows[i] = most <= 4 ? 4 : most <= 8 ? 8 : most <= 16 ? 16 : 32;
             x.tile[i] = kQ8Tile;
         }
         // several blocks to a head: each head begins its own

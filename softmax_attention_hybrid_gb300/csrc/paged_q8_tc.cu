@@ -1,7 +1,7 @@
 // Paged attention over 8-bit caches on the tensor cores (bf16 q and o; see paged.h for the split).
 //
 // Few rows meet many keys in a decoding step, so the keys take the M = 128 lanes of the MMAs
-// and the rows (R = 8, 16 or 32 of a block) the columns:
+// and the rows (R = 4, 8, 16 or 32 of a block) the columns:
 //     S^T [128 keys, rows] = K q^T,      O^T [d, rows] += V^T P^T,
 // with K and V as they lie in the cache: codes of e4m3 (kind::f8f6f4), never unpacked. A thread of
 // the softmax holds one key of the tile, with that key's two scales, for all rows.
@@ -18,7 +18,8 @@
 //
 // The running maxima m (one per row) and V (one for all) are those of the whole block: a tile whose
 // scores stay below m + 4 and whose scales stay below 2^V leaves them (one barrier with an OR); else
-// they are found anew, and O and l are scaled.
+// they are found anew, and O and l are scaled. Tiles are walked from the newest key to the oldest: the
+// patterns of frozen heads, and most ordinary rows, look nearby first, so that the maximum is found early.
 //
 // Warps (224 threads, two CTAs per SM): 0-3 softmax, 4 loads K, V and their scales (each of its lanes
 // fetches one page of the tile), 5 owns tensor memory and issues S, 6 issues P V.
@@ -42,6 +43,8 @@ constexpr int kScaleBytes = kTile * 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 4.0f;            // scores may pass the maximum by this much (base 2)
+// A row that has seen no key yet: below every finite score (those of patterns are at least -2.3e38 log2(e)).
+constexpr float kNoMax = -3.4e38f;
 constexpr float kWeight = 16.0f;          // 2^(8 - kSlack): a weight of the maximum, before the value's scale
 
 struct Q8Params {
@@ -52,10 +55,10 @@ struct Q8Params {
 
 template <int R>
 struct Cfg {
-    static constexpr int ns = 2 * R;                  // columns of S: hi, lo
+    static constexpr int ns = R == 4 ? 16 : 2 * R;    // columns of S: hi, lo (of an MMA at least 16)
     static constexpr int blocks = (3 * R + 15) / 16;  // 16-byte blocks of a key's weights: hi, mid, lo
     static constexpr int np = 16 * blocks;            // columns of O
-    static constexpr int slots = R == 8 ? 6 : R == 16 ? 5 : 4;
+    static constexpr int slots = R <= 8 ? 6 : R == 16 ? 5 : 4;
     static constexpr int ring = 0;
     static constexpr int q = ring + slots * kTileBytes;
     static constexpr int p = q + ns * 128;
@@ -63,7 +66,7 @@ struct Cfg {
     static constexpr int scales = p + 2 * p_bytes;
     static constexpr int total = scales + slots * kScaleBytes;
     static constexpr uint32_t col_o = 2 * ns;         // S of two tiles, then O
-    static constexpr uint32_t cols = R == 8 ? 64 : R == 16 ? 128 : 256;
+    static constexpr uint32_t cols = R <= 8 ? 64 : R == 16 ? 128 : 256;
     static_assert(col_o + np <= cols, "tensor memory");
     static_assert(p % 128 == 0 && q % 1024 == 0, "operand alignment");
 };
@@ -79,12 +82,13 @@ struct Shared {
     uint32_t tmem_base;
     int abort_flag, imin, imax, kinds, lost;
     // rows of the block
+    alignas(16) float scale[32];   // what a score times its key's scale is multiplied by: log2(e) / sqrt(d), and q's factor back
+    alignas(16) float m[32];       // running maxima
+    alignas(16) float fall[32];    // 2^(old maximum - new one)
     int out_row[32], pos[32];      // place in o (-1: none), last visible slot of the part (-1: none)
-    float scale[32];               // what a score times its key's scale is multiplied by: log2(e) / sqrt(d), and q's factor back
-    uint32_t frozen;               // bit per row
+    int f0;                        // rows f0 and up are those of frozen heads
     const float* a[32];            // frozen rows: a and r at the part's slot 0 and at the row's distance from it
     const float* r[32];
-    float m[32];                   // running maxima
     float part[4][32 + 1];         // the warps' maxima (and of the scales), and sums
 };
 
@@ -97,7 +101,10 @@ struct Work {
     int there;        // rows of the block that are rows of the output
     bool any_ord;     // an ordinary row is among them: K is loaded
 
-    // place of tile e0 + j's K and V in the order of loads
+    __device__ __forceinline__ int slot0(int j) const {   // first slot of the j-th tile, the newest first
+        return paged_tile(g, e1 - 1 - j) * kTile;
+    }
+    // place of its K and V in the order of loads
     __device__ __forceinline__ int k_load(int j) const { return j == 0 ? 0 : 2 * j - 1; }
     __device__ __forceinline__ int v_load(int j) const {
         if (!any_ord) return j;
@@ -147,7 +154,7 @@ __device__ __forceinline__ void load_warp(const Q8Params& P, const Work& w, uint
     auto look = [&](int first) -> int {   // a page as the table has it, -1: nothing to fetch
         const int j = first + lane / nbox;
         if (j >= n) return -1;
-        const int bx = paged_tile(w.g, w.e0 + j) * kTile + (lane & (nbox - 1)) * P.box;
+        const int bx = w.slot0(j) + (lane & (nbox - 1)) * P.box;
         if (!box_seen(w.g, bx, P.box)) return -1;
         const int at = bx >> p.page_log2;
         return __ldg(w.it.part ? p.page_table + (size_t)w.it.b * p.max_pages + at : p.prefix_pages + at);
@@ -174,7 +181,7 @@ __device__ __forceinline__ void load_warp(const Q8Params& P, const Work& w, uint
         if (lane == 0) mbar_expect_tx(&bars.full[s], __popc(have) * box_bytes);
         __syncwarp();
         if (pg >= 0) {
-            const int in = (paged_tile(w.g, w.e0 + j) * kTile + lane * P.box) & in_page;
+            const int in = (w.slot0(j) + lane * P.box) & in_page;
             const int z = pg * p.Hkv + w.it.hk;
             tma_load_3d(sm + C::ring + s * kTileBytes + lane * P.box * 128, map, &bars.full[s], 0, in, z);
             bulk_load(sm + C::scales + s * kScaleBytes + lane * P.box * 4, scales + ((size_t)z << p.page_log2) + in,
@@ -200,7 +207,7 @@ __device__ __forceinline__ void put_q(const Q8Params& P, const Work& w, uint8_t*
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
     for (int r = warp; r < R; r += 4) {
-        if (r >= w.there || sh.pos[r] < 0 || ((sh.frozen >> r) & 1u)) continue;   // (uniform)
+        if (r >= w.there || r >= sh.f0 || sh.pos[r] < 0) continue;   // (uniform)
         const bool mine = 4 * lane < p.d;
         uint2 x = make_uint2(0, 0);
         if (mine) x = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)p.q + (size_t)sh.out_row[r] * p.d) + lane);
@@ -235,29 +242,18 @@ __device__ __forceinline__ void put_q(const Q8Params& P, const Work& w, uint8_t*
 
 template <int R>
 __device__ __forceinline__ void read_s(uint32_t addr, float* s) {   // hi + lo / 16
-    if constexpr (R == 8) {
-        uint32_t x[16];
-        tmem_ld16(addr, x);
-        tmem_ld_wait();
+    uint32_t x[2 * R];
+    if constexpr (R == 4) tmem_ld8(addr, x);
+    else if constexpr (R == 8) tmem_ld16(addr, x);
+    else tmem_ld32(addr, x);
+    if constexpr (R == 32) tmem_ld32(addr + 32, x + 32);
+    tmem_ld_wait();
 #pragma unroll
-        for (int r = 0; r < 8; ++r) s[r] = fmaf(__uint_as_float(x[8 + r]), 0.0625f, __uint_as_float(x[r]));
-    } else if constexpr (R == 16) {
-        uint32_t x[32];
-        tmem_ld32(addr, x);
-        tmem_ld_wait();
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = fmaf(__uint_as_float(x[16 + r]), 0.0625f, __uint_as_float(x[r]));
-    } else {
-        uint32_t x[32], y[32];
-        tmem_ld32(addr, x);
-        tmem_ld32(addr + 32, y);
-        tmem_ld_wait();
-#pragma unroll
-        for (int r = 0; r < 32; ++r) s[r] = fmaf(__uint_as_float(y[r]), 0.0625f, __uint_as_float(x[r]));
-    }
+    for (int r = 0; r < R; ++r) s[r] = fmaf(__uint_as_float(x[R + r]), 0.0625f, __uint_as_float(x[r]));
 }
 
-// Warps 0-3. Thread t holds key t of every tile.
+// Warps 0-3. Thread t holds key t of every tile. Loops over rows have no branches: rows behind
+// the last one have columns of their own that nobody reads.
 template <int R>
 __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool lost, uint8_t* sm, Shared& sh) {
     using C = Cfg<R>;
@@ -266,8 +262,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool
     volatile int* abort = &sh.abort_flag;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const uint32_t tmem = sh.tmem_base + ((uint32_t)(warp * 32) << 16);
-    const int there = w.there;
-    const uint32_t frozen = sh.frozen;
+    const int there = w.there, f0 = sh.f0, tiles = w.e1 - w.e0;
     const int my_box = t / P.box * P.box;
     float l[R];
 #pragma unroll
@@ -276,31 +271,35 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool
     int vexp = 0;
     bool ok = true;
 
-    int n = 0;
-    for (int e = w.e0; e < w.e1; ++e, ++n) {
-        const int x0 = paged_tile(w.g, e) * kTile, x = x0 + t, buf = n & 1;
-        float s[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) s[r] = -INFINITY;
-        // the fixed patterns' logits (Eq. 3): neighbouring keys, neighbouring entries
-        if (frozen) {
+    // the fixed patterns' entries (Eq. 3) of my key: neighbouring keys, neighbouring entries. Few rows: a tile ahead.
+    constexpr bool kAhead = R <= 8;
+    float fa[kAhead ? R : 1], fr[kAhead ? R : 1];
+    auto ahead = [&](int j) {
+        const int x = w.slot0(j) + t;
+        if constexpr (kAhead) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                if ((frozen >> r) & 1u) {
+                if (r >= f0 && r < there) {
                     const int y = max(min(x, sh.pos[r]), 0);   // (keys past the row's own position are masked below)
-                    s[r] = (__ldg(sh.a[r] + y) + __ldg(sh.r[r] - y)) * kLog2e;
+                    fa[r] = __ldg(sh.a[r] + y);
+                    fr[r] = __ldg(sh.r[r] - y);
                 }
         }
-        float ks = 0.f;
+    };
+    if (f0 < there) ahead(0);
+
+    int n = 0;
+    for (; n < tiles; ++n) {
+        const int x0 = w.slot0(n), x = x0 + t, buf = n & 1;
+        float s[R];
         if (w.any_ord) {
             const int ld = w.k_load(n), slot = ld % C::slots;
             ok = mbar_wait(&bars.s_full[buf], (n >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
             ok = mbar_wait(&bars.full[slot], (ld / C::slots) & 1, abort, p.status, kStatusTimeout) && ok;
             __syncwarp();
             tc_fence_after();
-            ks = reinterpret_cast<const float*>(sm + C::scales + slot * kScaleBytes)[t];
-            float q[R];
-            read_s<R>(tmem + buf * C::ns, q);
+            const float ks = reinterpret_cast<const float*>(sm + C::scales + slot * kScaleBytes)[t];
+            read_s<R>(tmem + buf * C::ns, s);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -308,8 +307,38 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool
                 mbar_arrive(&bars.empty[slot]);
             }
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r < there && !((frozen >> r) & 1u)) s[r] = q[r] * (ks * sh.scale[r]);
+            for (int r = 0; r < R; r += 4) {
+                const float4 q = *reinterpret_cast<const float4*>(&sh.scale[r]);
+                s[r] *= ks * q.x;
+                s[r + 1] *= ks * q.y;
+                s[r + 2] *= ks * q.z;
+                s[r + 3] *= ks * q.w;
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) s[r] = -INFINITY;
+        }
+        if (f0 < there) {
+            if constexpr (kAhead) {
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    if (r >= f0 && r < there) s[r] = (fa[r] + fr[r]) * kLog2e;
+                if (n + 1 < tiles) ahead(n + 1);
+            } else {   // four rows' loads at a time
+#pragma unroll
+                for (int r = 0; r < R; r += 4)
+                    if (r + 4 > f0 && r < there) {
+                        float y[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int z = max(min(x, sh.pos[r + c]), 0);
+                            y[c] = __ldg(sh.a[r + c] + z) + __ldg(sh.r[r + c] - z);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (r + c >= f0) s[r + c] = y[c] * kLog2e;
+                    }
+            }
         }
         const int ldv = w.v_load(n), vslot = ldv % C::slots;
         ok = mbar_wait(&bars.full[vslot], (ldv / C::slots) & 1, abort, p.status, kStatusTimeout) && ok;
@@ -321,12 +350,11 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool
             const bool any = have && x < w.g.hi && (x >= w.g.lo || x < w.g.sink);
             const int sink = p.sinks - w.off;
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r < there) {
-                    const int i = sh.pos[r];
-                    const int lo = ((frozen >> r) & 1u) || p.window == 0 ? -1 : i - p.window;   // slots <= lo: sinks only
-                    if (!(any && x <= i && (x > lo || x < sink))) s[r] = -INFINITY;
-                }
+            for (int r = 0; r < R; ++r) {
+                const int i = sh.pos[r];
+                const int lo = r >= f0 || p.window == 0 ? -1 : i - p.window;   // slots <= lo: sinks only
+                if (!(any && x <= i && (x > lo || x < sink))) s[r] = -INFINITY;
+            }
             if (!any) {   // codes and scales of slots that no row sees may be anything: zeros, for 0 * NaN is none
                 vs = 0.f;
                 uint4* row = reinterpret_cast<uint4*>(sm + C::ring + vslot * kTileBytes + t * 128);
@@ -334,18 +362,20 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool
                 for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
             }
         }
-        bool up = vs > vtop;
+        float past = 0.f;   // by how much a score passes its row's maximum (a NaN does not)
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (r < there) up |= s[r] > sh.m[r] + kSlack;
-        if (rows_any(up || !ok)) {
+        for (int r = 0; r < R; r += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(&sh.m[r]);
+            past = fmax3(past, s[r] - m.x, s[r + 1] - m.y);
+            past = fmax3(past, s[r + 2] - m.z, s[r + 3] - m.w);
+        }
+        if (rows_any(past > kSlack || vs > vtop || !ok)) {
             if (rows_any(!ok)) break;   // every thread leaves here
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r < there) {
-                    const float mx = warp_max(s[r]);
-                    if (lane == 0) sh.part[warp][r] = mx;
-                }
+            for (int r = 0; r < R; ++r) {
+                const float mx = warp_max(s[r]);
+                if (lane == 0) sh.part[warp][r] = mx;
+            }
             {
                 const float mx = warp_max(vs);
                 if (lane == 0) sh.part[warp][32] = mx;
@@ -361,66 +391,52 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool
                 vtop = pow2i(ex);
                 vinv = pow2i(-ex);
             }
-            const bool scale_o = n > 0;
-            if (scale_o)   // P V of the previous tile is done: O is stable
-                ok = mbar_wait(&bars.o_done[buf ^ 1], ((n - 1) >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
-            __syncwarp();
-            tc_fence_after();
-            float f[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                f[r] = 1.f;
-                if (r < there) {
-                    const float old = sh.m[r];
-                    const float now = fmaxf(fmaxf(fmaxf(sh.part[0][r], sh.part[1][r]), fmaxf(sh.part[2][r], sh.part[3][r])), old);
-                    if (now > old) f[r] = fast_exp2(old - now);
-                    l[r] *= f[r];
-                }
+            if (t < R) {
+                const float old = sh.m[t];
+                const float now = fmaxf(fmaxf(fmaxf(sh.part[0][t], sh.part[1][t]), fmaxf(sh.part[2][t], sh.part[3][t])), old);
+                sh.m[t] = now;
+                sh.fall[t] = now > old ? fast_exp2(old - now) : 1.f;
             }
-            if (scale_o) {
+            rows_sync();
+#pragma unroll
+            for (int r = 0; r < R; ++r) l[r] *= sh.fall[r];
+            if (n > 0) {   // P V of the previous tile is done: O is stable
+                ok = mbar_wait(&bars.o_done[buf ^ 1], ((n - 1) >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
+                __syncwarp();
+                tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < C::np; c += 16) {
                     uint32_t o[16];
                     tmem_ld16(tmem + C::col_o + c, o);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * (f[(c + k) % R] * fv));
+                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * (sh.fall[(c + k) % R] * fv));
                     tmem_st16(tmem + C::col_o + c, o);
                 }
                 tmem_st_wait();
                 tc_fence_before();
             }
-            rows_sync();   // the old maxima are read
-            if (t < there) {
-                const float now = fmaxf(fmaxf(sh.part[0][t], sh.part[1][t]), fmaxf(sh.part[2][t], sh.part[3][t]));
-                sh.m[t] = fmaxf(sh.m[t], now);
-            }
-            rows_sync();
         }
         if (n > 1)   // P V of the tile before the previous one is done: its weights' buffer is free
             ok = mbar_wait(&bars.o_done[buf], ((n - 2) >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
         const float vw = vs * vinv * kWeight;
         uint8_t* mine = sm + C::p + buf * C::p_bytes + t * 16;
-        uint32_t word[3 * R / 4];   // bytes: columns of the terms, hi, mid, lo
+        uint32_t word[4 * C::blocks];   // bytes: columns of the terms, hi, mid, lo
+        word[4 * C::blocks - 1] = word[4 * C::blocks - 2] = 0u;   // (what the terms leave of the last block)
 #pragma unroll
         for (int r = 0; r < R; r += 4) {
-            float y[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                y[c] = 0.f;
-                if (r + c < there) {
-                    const float m = sh.m[r + c];
-                    const float pr = fast_exp2(s[r + c] - (m == -INFINITY ? 0.f : m));   // (a row that has seen no key yet)
-                    l[r + c] += pr;
-                    y[c] = pr * vw;
-                }
-            }
+            const float4 m = *reinterpret_cast<const float4*>(&sh.m[r]);
+            const float pr[4] = {fast_exp2(s[r] - m.x), fast_exp2(s[r + 1] - m.y), fast_exp2(s[r + 2] - m.z),
+                                 fast_exp2(s[r + 3] - m.w)};
             uint32_t h[2], md[2], lo[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                h[c] = pack_e4m3(y[2 * c], y[2 * c + 1]);
+                l[r + 2 * c] += pr[2 * c];
+                l[r + 2 * c + 1] += pr[2 * c + 1];
+                const float y0 = pr[2 * c] * vw, y1 = pr[2 * c + 1] * vw;
+                h[c] = pack_e4m3(y0, y1);
                 float2 z = unpack_e4m3(h[c]);
-                const float a0 = 16.f * (y[2 * c] - z.x), a1 = 16.f * (y[2 * c + 1] - z.y);
+                const float a0 = 16.f * (y0 - z.x), a1 = 16.f * (y1 - z.y);
                 md[c] = pack_e4m3(a0, a1);
                 z = unpack_e4m3(md[c]);
                 lo[c] = pack_e4m3(16.f * (a0 - z.x), 16.f * (a1 - z.y));
@@ -430,14 +446,9 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool
             word[R / 2 + r / 4] = lo[0] | lo[1] << 16;
         }
 #pragma unroll
-        for (int b = 0; b < C::blocks; ++b) {
-            uint4 z;
-            z.x = word[4 * b];
-            z.y = word[4 * b + 1];
-            z.z = 4 * b + 2 < 3 * R / 4 ? word[4 * b + 2 < 3 * R / 4 ? 4 * b + 2 : 0] : 0u;
-            z.w = 4 * b + 3 < 3 * R / 4 ? word[4 * b + 3 < 3 * R / 4 ? 4 * b + 3 : 0] : 0u;
-            *reinterpret_cast<uint4*>(mine + b * kTile * 16) = z;
-        }
+        for (int b = 0; b < C::blocks; ++b)
+            *reinterpret_cast<uint4*>(mine + b * kTile * 16) =
+                make_uint4(word[4 * b], word[4 * b + 1], word[4 * b + 2], word[4 * b + 3]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -445,13 +456,12 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool
             mbar_arrive(&bars.empty[vslot]);
         }
     }
-    // (a lane whose wait ran out has left with all the others, or does so here)
+    // (a lane whose wait ran out has left with all the others, or does so below)
     if (n > 0) ok = mbar_wait(&bars.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
     __syncwarp();
     tc_fence_after();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        if (r >= there) continue;
         float x = l[r];
         for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (lane == 0) sh.part[warp][r] = x;
@@ -459,33 +469,25 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool
     if (rows_any(!ok)) return;
     // O of element t of a row: the terms' sums
     const int split = w.it.part ? p.chunks[0] + w.it.chunk : w.it.chunk;
-    const float back = pow2i(vexp - 4 < -149 ? -149 : vexp - 4);   // 2^V / kWeight
-    float o[R];
+    const float back = pow2i(vexp - 4);   // 2^V / kWeight
+    uint32_t y[C::np];
 #pragma unroll
-    for (int term = 2; term >= 0; --term) {
-#pragma unroll
-        for (int c = 0; c < R; c += 8) {
-            uint32_t y[8];
-            tmem_ld8(tmem + C::col_o + term * R + c, y);
-            tmem_ld_wait();
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                o[c + k] = term == 2 ? __uint_as_float(y[k]) : fmaf(o[c + k], 0.0625f, __uint_as_float(y[k]));
-        }
-    }
+    for (int c = 0; c < C::np; c += 16) tmem_ld16(tmem + C::col_o + c, y + c);
+    tmem_ld_wait();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         if (r >= there) continue;
+        const float o = fmaf(fmaf(__uint_as_float(y[2 * R + r]), 0.0625f, __uint_as_float(y[R + r])), 0.0625f,
+                             __uint_as_float(y[r])) * back;
         const size_t at = (size_t)sh.out_row[r];
         const bool sees = sh.pos[r] >= 0;
         const float lr = sees ? (sh.part[0][r] + sh.part[1][r]) + (sh.part[2][r] + sh.part[3][r]) : 0.f;
-        const float mr = sees ? sh.m[r] : -INFINITY;
-        const float y = lr != 0.f ? o[r] * back : 0.f;
+        const float mr = lr != 0.f ? sh.m[r] : -INFINITY;
         if (p.nsplit > 1) {
-            if (t < p.d) p.po[(at * p.nsplit + split) * p.d + t] = y;
+            if (t < p.d) p.po[(at * p.nsplit + split) * p.d + t] = lr != 0.f ? o : 0.f;
             if (t == 0) p.ml[at * p.nsplit + split] = make_float2(mr, lr);
         } else {
-            if (t < p.d) ((__nv_bfloat16*)p.o)[at * p.d + t] = __float2bfloat16_rn(lr != 0.f ? y / lr : 0.f);
+            if (t < p.d) ((__nv_bfloat16*)p.o)[at * p.d + t] = __float2bfloat16_rn(lr != 0.f ? o / lr : 0.f);
             if (t == 0) p.lse[at] = lr != 0.f ? (mr + log2f(lr)) * kLn2 : -INFINITY;
         }
     }
@@ -517,19 +519,20 @@ __global__ void __launch_bounds__(kThreads, 2) paged_q8_kernel(const __grid_cons
         const PagedRow row = paged_row(p, w.it, block, lane);
         sh.out_row[lane] = row.there ? (int)paged_out_row(p, row) : -1;
         sh.pos[lane] = row.i < 0 ? -1 : row.i - w.off;
-        sh.m[lane] = -INFINITY;
+        sh.m[lane] = kNoMax;
         sh.scale[lane] = 0.f;
         sh.a[lane] = p.a + (size_t)row.h * p.ld + w.off;
         sh.r[lane] = p.r + (size_t)row.h * p.ld + (row.i < 0 ? 0 : row.i - w.off);
         const bool seen = row.i >= 0;
         const uint32_t fz = __ballot_sync(0xffffffffu, seen && row.frozen);
+        const uint32_t kind = __ballot_sync(0xffffffffu, row.there && row.frozen);
         const uint32_t ord = __ballot_sync(0xffffffffu, seen && !row.frozen);
         const int lo = __reduce_min_sync(0xffffffffu, seen ? row.i : 0x7fffffff);
         const int hi = __reduce_max_sync(0xffffffffu, row.i);
         if (lane == 0) {
             sh.imin = lo;
             sh.imax = hi;
-            sh.frozen = fz;
+            sh.f0 = kind ? __ffs(kind) - 1 : 32;
             sh.kinds = (ord ? 1 : 0) | (fz ? 2 : 0);
         }
     } else if (t == 32) {
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_q8_kernel(const __grid_cons
             const int nbox = kTile / P.box, end = n * nbox;
             bool lost = false;
             for (int b = t - 160; b < end; b += 64) {
-                const int bx = paged_tile(w.g, w.e0 + b / nbox) * kTile + (b & (nbox - 1)) * P.box;
+                const int bx = w.slot0(b / nbox) + (b & (nbox - 1)) * P.box;
                 if (box_seen(w.g, bx, P.box) && paged_page(p, w.it, bx) < 0) lost = true;
             }
             if (lost) sh.lost = 1;
@@ -669,6 +672,7 @@ cudaError_t launch_paged_q8(const PagedArgs& a, cudaStream_t s) {
         !make_tmap_u8_3d(&P.tm_v, a.v_cache, a.d, page, slices, 128, P.box))
         return cudaErrorInvalidValue;
     switch (a.rows[1]) {
+        case 4: return launch_r<4>(P, s);
         case 8: return launch_r<8>(P, s);
         case 16: return launch_r<16>(P, s);
         default: return launch_r<32>(P, s);
