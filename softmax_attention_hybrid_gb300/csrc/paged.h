@@ -121,8 +121,8 @@ __device__ __forceinline__ PagedBlock paged_block(const PagedArgs& p, const Page
     return k;
 }
 
-// Row x of the block.
-__device__ __forceinline__ PagedRow paged_row(const PagedArgs& p, const PagedItem& it, const PagedBlock& k, int x) {
+// Row x of the block, its position left out.
+__device__ __forceinline__ PagedRow paged_place(const PagedArgs& p, const PagedItem& it, const PagedBlock& k, int x) {
     PagedRow w;
     w.there = x < k.there;
     w.h = w.b = w.t = w.gi = 0;
@@ -135,6 +135,13 @@ __device__ __forceinline__ PagedRow paged_row(const PagedArgs& p, const PagedIte
     w.t = it.part ? rem : rem - w.b * p.T;
     w.h = p.gheads[it.hk * p.G + w.gi];
     w.frozen = w.gi >= p.gord[it.hk];
+    return w;
+}
+
+// Row x of the block.
+__device__ __forceinline__ PagedRow paged_row(const PagedArgs& p, const PagedItem& it, const PagedBlock& k, int x) {
+    PagedRow w = paged_place(p, it, k, x);
+    if (!w.there) return w;
     int c;
     bool bad;
     const int n = paged_tokens(p, w.b, &c, &bad);

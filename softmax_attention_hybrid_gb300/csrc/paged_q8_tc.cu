@@ -29,12 +29,12 @@
 // codes are filled up with zeros by TMA.
 #include <string.h>
 
-#include "paged_tc.cuh"
+#include "paged_q8.cuh"
 
 namespace saf {
 namespace {
 
-using namespace paged_tc;
+using namespace paged_q8;
 
 constexpr int kThreads = 224;
 constexpr int kTile = kQ8Tile;            // keys of a tile
@@ -47,18 +47,14 @@ constexpr float kSlack = 4.0f;            // scores may pass the maximum by this
 constexpr float kNoMax = -3.4e38f;
 constexpr float kWeight = 16.0f;          // 2^(8 - kSlack): a weight of the maximum, before the value's scale
 
-struct Q8Params {
-    CUtensorMap tm_k, tm_v;
-    PagedArgs a;
-    int box;   // keys of a TMA box: min(page, 128)
-};
-
 template <int R>
 struct Cfg {
     static constexpr int ns = R == 4 ? 16 : 2 * R;    // columns of S: hi, lo (of an MMA at least 16)
     static constexpr int blocks = (3 * R + 15) / 16;  // 16-byte blocks of a key's weights: hi, mid, lo
     static constexpr int np = 16 * blocks;            // columns of O
-    static constexpr int slots = R <= 8 ? 6 : R == 16 ? 5 : 4;
+    static constexpr int tile = kTile;
+    static constexpr int ctas = R == 4 ? 3 : 2;       // of an SM
+    static constexpr int slots = R == 4 ? 4 : R == 8 ? 6 : R == 16 ? 5 : 4;
     static constexpr int ring = 0;
     static constexpr int q = ring + slots * kTileBytes;
     static constexpr int p = q + ns * 128;
@@ -80,36 +76,16 @@ struct Bars {
 struct Shared {
     Bars bars;
     uint32_t tmem_base;
-    int abort_flag, imin, imax, kinds, lost;
+    int abort_flag;
+    int lost;                      // a page that the item needs is not in the cache (set before its tile is there)
     // rows of the block
     alignas(16) float scale[32];   // what a score times its key's scale is multiplied by: log2(e) / sqrt(d), and q's factor back
     alignas(16) float m[32];       // running maxima
     alignas(16) float fall[32];    // 2^(old maximum - new one)
     int out_row[32], pos[32];      // place in o (-1: none), last visible slot of the part (-1: none)
-    int f0;                        // rows f0 and up are those of frozen heads
     const float* a[32];            // frozen rows: a and r at the part's slot 0 and at the row's distance from it
     const float* r[32];
     float part[4][32 + 1];         // the warps' maxima (and of the scales), and sums
-};
-
-struct Work {
-    PagedItem it;
-    PagedRange g;
-    int e0, e1;       // tiles
-    int imin, imax;   // positions of the rows that see anything
-    int off;          // position of the part's slot 0
-    int there;        // rows of the block that are rows of the output
-    bool any_ord;     // an ordinary row is among them: K is loaded
-
-    __device__ __forceinline__ int slot0(int j) const {   // first slot of the j-th tile, the newest first
-        return paged_tile(g, e1 - 1 - j) * kTile;
-    }
-    // place of its K and V in the order of loads
-    __device__ __forceinline__ int k_load(int j) const { return j == 0 ? 0 : 2 * j - 1; }
-    __device__ __forceinline__ int v_load(int j) const {
-        if (!any_ord) return j;
-        return j + 1 < e1 - e0 ? 2 * j + 2 : 2 * j + 1;
-    }
 };
 
 // OR over the 128 softmax threads, who all wait for each other.
@@ -133,84 +109,31 @@ __device__ __forceinline__ float warp_max(float x) {
     return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
 }
 
-__device__ __forceinline__ float pow2i(int e) {   // 2^e, -149 <= e <= 127
-    return e >= -126 ? __int_as_float((e + 127) << 23) : __int_as_float(1 << (e + 149));
-}
-
-// The loading warp. Lane l fetches box l of every tile, from its page, and the box's scales.
+// Rows of q on their way, a warp's every fourth (in: the rows' places in o).
 template <int R>
-__device__ __forceinline__ void load_warp(const Q8Params& P, const Work& w, uint8_t* sm, Bars& bars,
-                                          volatile int* abort) {
-    using C = Cfg<R>;
-    const PagedArgs& p = P.a;
-    const int lane = threadIdx.x & 31;
-    const int nbox = kTile / P.box, n = w.e1 - w.e0;
-    const int in_page = (1 << p.page_log2) - 1;
-    const uint32_t box_bytes = (uint32_t)P.box * (128u + 4u);
-    // The pages of a batch of tiles are looked up together, lane l those of tile l / nbox, box
-    // l mod nbox, a batch ahead of their use: a lookup for each tile would wait for the memory
-    // in every one.
-    const int batch = 32 / nbox;
-    auto look = [&](int first) -> int {   // a page as the table has it, -1: nothing to fetch
-        const int j = first + lane / nbox;
-        if (j >= n) return -1;
-        const int bx = w.slot0(j) + (lane & (nbox - 1)) * P.box;
-        if (!box_seen(w.g, bx, P.box)) return -1;
-        const int at = bx >> p.page_log2;
-        return __ldg(w.it.part ? p.page_table + (size_t)w.it.b * p.max_pages + at : p.prefix_pages + at);
-    };
-    int looked = look(0), ahead = look(batch);   // tiles [base, base + batch), and the batch behind
-    int base = 0;
-    if (lane == 0) {
-        tma_prefetch_desc(&P.tm_k);
-        tma_prefetch_desc(&P.tm_v);
-    }
-    auto page_of = [&](int j) -> int {   // my box's page of tile j (ascending), -1: nothing to fetch
-        if (j == base + batch) {
-            base = j;
-            looked = ahead;
-            ahead = look(base + batch);
-        }
-        const int pg = __shfl_sync(0xffffffffu, looked, ((j - base) * nbox + lane) & 31);
-        return lane < nbox && pg >= 0 && pg < p.num_pages ? pg : -1;
-    };
-    auto fetch = [&](int load, const CUtensorMap* map, const float* scales, int j, int pg) -> bool {
-        const int s = load % C::slots;
-        if (!wait_all(&bars.empty[s], ((load / C::slots) & 1) ^ 1u, abort, p.status)) return false;
-        const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0);
-        if (lane == 0) mbar_expect_tx(&bars.full[s], __popc(have) * box_bytes);
-        __syncwarp();
-        if (pg >= 0) {
-            const int in = (w.slot0(j) + lane * P.box) & in_page;
-            const int z = pg * p.Hkv + w.it.hk;
-            tma_load_3d(sm + C::ring + s * kTileBytes + lane * P.box * 128, map, &bars.full[s], 0, in, z);
-            bulk_load(sm + C::scales + s * kScaleBytes + lane * P.box * 4, scales + ((size_t)z << p.page_log2) + in,
-                      (uint32_t)P.box * 4u, &bars.full[s]);
-        }
-        __syncwarp();
-        return true;
-    };
-    int pg = page_of(0);
-    bool ok = !w.any_ord || fetch(0, &P.tm_k, p.k_scale, 0, pg);
-    for (int j = 0; j < n && ok; ++j) {
-        const int next = j + 1 < n ? page_of(j + 1) : -1;
-        if (w.any_ord && j + 1 < n) ok = fetch(w.k_load(j + 1), &P.tm_k, p.k_scale, j + 1, next);
-        ok = ok && fetch(w.v_load(j), &P.tm_v, p.v_scale, j, pg);
-        pg = next;
-    }
-}
-
-// q's terms of the block's ordinary rows, a warp per row, and the rows' factors.
-template <int R>
-__device__ __forceinline__ void put_q(const Q8Params& P, const Work& w, uint8_t* sm, Shared& sh) {
+__device__ __forceinline__ void get_q(const Q8Params& P, const Work& w, int place, uint2* x) {
     const PagedArgs& p = P.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-    for (int r = warp; r < R; r += 4) {
-        if (r >= w.there || r >= sh.f0 || sh.pos[r] < 0) continue;   // (uniform)
-        const bool mine = 4 * lane < p.d;
-        uint2 x = make_uint2(0, 0);
-        if (mine) x = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)p.q + (size_t)sh.out_row[r] * p.d) + lane);
+    for (int k = 0; k < R / 4; ++k) {
+        const int r = 4 * k + warp, at = __shfl_sync(0xffffffffu, place, r);
+        x[k] = make_uint2(0, 0);
+        if (r < w.there && r < w.f0 && 4 * lane < p.d)
+            x[k] = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)p.q + (size_t)at * p.d) + lane);
+    }
+}
+
+// q's terms of the block's ordinary rows, and the rows' factors.
+template <int R>
+__device__ __forceinline__ void put_q(const Q8Params& P, const Work& w, uint8_t* sm, Shared& sh, const uint2* q) {
+    const PagedArgs& p = P.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool mine = 4 * lane < p.d;
+#pragma unroll
+    for (int k = 0; k < R / 4; ++k) {
+        const int r = 4 * k + warp;
+        if (r >= w.there || r >= w.f0 || sh.pos[r] < 0) continue;   // (uniform)
+        const uint2 x = q[k];
         const float v[4] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
                             __uint_as_float(x.y & 0xffff0000u)};
         // the row's largest magnitude as bits: above 0x7f7fffff it holds an infinity or a NaN
@@ -240,6 +163,13 @@ __device__ __forceinline__ void put_q(const Q8Params& P, const Work& w, uint8_t*
     }
 }
 
+// Every warp but the loading one: q's terms and tensor memory are there.
+__device__ __forceinline__ void set_up_done() {
+    tc_fence_before();
+    asm volatile("bar.sync 2, 192;" ::: "memory");
+    tc_fence_after();
+}
+
 template <int R>
 __device__ __forceinline__ void read_s(uint32_t addr, float* s) {   // hi + lo / 16
     uint32_t x[2 * R];
@@ -255,14 +185,13 @@ __device__ __forceinline__ void read_s(uint32_t addr, float* s) {   // hi + lo /
 // Warps 0-3. Thread t holds key t of every tile. Loops over rows have no branches: rows behind
 // the last one have columns of their own that nobody reads.
 template <int R>
-__device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool lost, uint8_t* sm, Shared& sh) {
+__device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, const uint2* q, uint8_t* sm, Shared& sh) {
     using C = Cfg<R>;
     const PagedArgs& p = P.a;
     Bars& bars = sh.bars;
     volatile int* abort = &sh.abort_flag;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const uint32_t tmem = sh.tmem_base + ((uint32_t)(warp * 32) << 16);
-    const int there = w.there, f0 = sh.f0, tiles = w.e1 - w.e0;
+    const int there = w.there, f0 = w.f0, tiles = w.e1 - w.e0;
     const int my_box = t / P.box * P.box;
     float l[R];
 #pragma unroll
@@ -275,7 +204,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool
     constexpr bool kAhead = R <= 8;
     float fa[kAhead ? R : 1], fr[kAhead ? R : 1];
     auto ahead = [&](int j) {
-        const int x = w.slot0(j) + t;
+        const int x = w.slot0(j, kTile) + t;
         if constexpr (kAhead) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -287,10 +216,16 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool
         }
     };
     if (f0 < there) ahead(0);
+    if (w.any_ord) {
+        put_q<R>(P, w, sm, sh, q);
+        fence_proxy_async_smem();
+    }
+    set_up_done();
+    const uint32_t tmem = sh.tmem_base + ((uint32_t)(warp * 32) << 16);
 
     int n = 0;
     for (; n < tiles; ++n) {
-        const int x0 = w.slot0(n), x = x0 + t, buf = n & 1;
+        const int x0 = w.slot0(n, kTile), x = x0 + t, buf = n & 1;
         float s[R];
         if (w.any_ord) {
             const int ld = w.k_load(n), slot = ld % C::slots;
@@ -343,6 +278,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool
         const int ldv = w.v_load(n), vslot = ldv % C::slots;
         ok = mbar_wait(&bars.full[vslot], (ldv / C::slots) & 1, abort, p.status, kStatusTimeout) && ok;
         float vs = reinterpret_cast<const float*>(sm + C::scales + vslot * kScaleBytes)[t];
+        const bool lost = *(volatile int*)&sh.lost != 0;
         // masks, in tiles that some row does not see whole
         if (lost || x0 + kTile > w.g.hi || x0 + kTile - 1 > w.imin - w.off ||
             (p.window > 0 && x0 <= w.imax - w.off - p.window)) {
@@ -493,49 +429,15 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, bool
     }
 }
 
-// Every warp but the loading one: q's terms, tensor memory and the check of the pages are done.
-__device__ __forceinline__ void set_up_done() {
-    tc_fence_before();
-    asm volatile("bar.sync 2, 192;" ::: "memory");
-    tc_fence_after();
-}
-
 template <int R>
-__global__ void __launch_bounds__(kThreads, 2) paged_q8_kernel(const __grid_constant__ Q8Params P) {
+__global__ void __launch_bounds__(kThreads, Cfg<R>::ctas) paged_q8_kernel(const __grid_constant__ Q8Params P) {
     using C = Cfg<R>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Shared sh;
     const PagedArgs& p = P.a;
-    grid_dep_wait();
-    grid_dep_launch();
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    Work w;
-    w.it = paged_item(p, blockIdx.x);
-    const PagedBlock block = paged_block(p, w.it);
-    w.off = w.it.part ? p.P : 0;
-    w.there = block.there;
-    if (warp == 0) {   // the block's rows, a lane each
-        const PagedRow row = paged_row(p, w.it, block, lane);
-        sh.out_row[lane] = row.there ? (int)paged_out_row(p, row) : -1;
-        sh.pos[lane] = row.i < 0 ? -1 : row.i - w.off;
-        sh.m[lane] = kNoMax;
-        sh.scale[lane] = 0.f;
-        sh.a[lane] = p.a + (size_t)row.h * p.ld + w.off;
-        sh.r[lane] = p.r + (size_t)row.h * p.ld + (row.i < 0 ? 0 : row.i - w.off);
-        const bool seen = row.i >= 0;
-        const uint32_t fz = __ballot_sync(0xffffffffu, seen && row.frozen);
-        const uint32_t kind = __ballot_sync(0xffffffffu, row.there && row.frozen);
-        const uint32_t ord = __ballot_sync(0xffffffffu, seen && !row.frozen);
-        const int lo = __reduce_min_sync(0xffffffffu, seen ? row.i : 0x7fffffff);
-        const int hi = __reduce_max_sync(0xffffffffu, row.i);
-        if (lane == 0) {
-            sh.imin = lo;
-            sh.imax = hi;
-            sh.f0 = kind ? __ffs(kind) - 1 : 32;
-            sh.kinds = (ord ? 1 : 0) | (fz ? 2 : 0);
-        }
-    } else if (t == 32) {
+    if (t == 0) {
         sh.abort_flag = sh.lost = 0;
         for (int i = 0; i < C::slots; ++i) {
             mbar_init(&sh.bars.full[i], 1);
@@ -549,51 +451,66 @@ __global__ void __launch_bounds__(kThreads, 2) paged_q8_kernel(const __grid_cons
             mbar_init(&sh.bars.mma_idle[i], 1);
         }
         fence_mbar_init();
-    } else if (t == 64 && w.it.part == 1 && w.it.chunk == 0 && w.it.rb == 0 && w.it.hk == 0) {
-        int c;   // each sequence's counts are checked once
-        bool bad;
-        paged_tokens(p, w.it.b, &c, &bad);
-        if (bad) atomicOr(p.status, kStatusPage);
     }
+    Work w;
+    w.it = paged_item(p, blockIdx.x);
+    w.off = w.it.part ? p.P : 0;
+    const PagedBlock block = paged_block(p, w.it);
+    w.there = block.there;
+    // every warp finds the rows for itself, a lane each: nobody waits for another's loads
+    const PagedRow row = paged_place(p, w.it, block, lane);
+    const int place = row.there ? (int)paged_out_row(p, row) : -1;
+    const uint32_t kind = __ballot_sync(0xffffffffu, row.there && row.frozen);
+    w.f0 = kind ? __ffs(kind) - 1 : 32;
     __syncthreads();
-    w.imin = sh.imin;
-    w.imax = sh.imax;
-    w.any_ord = (sh.kinds & 1) != 0;
-    w.g = paged_range(p, w.it, w.imin, w.imax, (sh.kinds & 2) != 0 || p.window == 0);
+    grid_dep_wait();
+    grid_dep_launch();
+    uint2 q[R / 4];
+    if (warp < 4) get_q<R>(P, w, place, q);
+    int i = -1;
+    if (row.there) {
+        int c;
+        bool bad;
+        const int n = paged_tokens(p, row.b, &c, &bad);
+        if (row.t < n) i = p.P + c + row.t;
+        // each sequence's counts are checked once
+        if (bad && t == 0 && w.it.part == 1 && w.it.chunk == 0 && w.it.rb == 0 && w.it.hk == 0)
+            atomicOr(p.status, kStatusPage);
+    }
+    w.imin = __reduce_min_sync(0xffffffffu, i >= 0 ? i : 0x7fffffff);
+    w.imax = __reduce_max_sync(0xffffffffu, i);
+    w.any_ord = __ballot_sync(0xffffffffu, i >= 0 && !row.frozen) != 0;
+    const bool any_frozen = __ballot_sync(0xffffffffu, i >= 0 && row.frozen) != 0;
+    w.g = paged_range(p, w.it, w.imin, w.imax, any_frozen || p.window == 0);
     const int per = p.per_chunk[w.it.part];
     w.e0 = min(w.it.chunk * per, w.g.n);
     w.e1 = min(w.e0 + per, w.g.n);
+    if (warp == 0) {
+        sh.out_row[lane] = place;
+        sh.pos[lane] = i < 0 ? -1 : i - w.off;
+        // (rows that see nothing, whose columns of S may hold anything: no score passes their maximum)
+        sh.m[lane] = i < 0 ? INFINITY : kNoMax;
+        sh.scale[lane] = 0.f;
+        sh.a[lane] = p.a + (size_t)row.h * p.ld + w.off;
+        sh.r[lane] = p.r + (size_t)row.h * p.ld + (i < 0 ? 0 : i - w.off);
+    }
     if (w.e0 >= w.e1) {   // no keys: nothing but the rows' empty sums
+        __syncthreads();
         write_empty(p, w.it, w.there, sh.out_row, kThreads);
         return;
     }
     const int n = w.e1 - w.e0;
     Bars& bars = sh.bars;
     volatile int* abort = &sh.abort_flag;
-    if (warp == 4) {   // K and V need nothing but the range of keys: on their way under the rest of the set-up
-        load_warp<R>(P, w, sm, bars, abort);
+    if (warp == 4) {
+        load_warp<C>(P, w, sm, sh);
     } else if (warp < 4) {
-        if (w.any_ord) {
-            put_q<R>(P, w, sm, sh);
-            fence_proxy_async_smem();
-        }
-        set_up_done();
-        const bool lost = sh.lost != 0;
-        if (lost && t == 0) atomicOr(p.status, kStatusPage);
-        row_warps<R>(P, w, lost, sm, sh);
+        rows_sync();   // the rows' places
+        row_warps<R>(P, w, q, sm, sh);
     } else {
         if (warp == 5) {
             tmem_alloc(&sh.tmem_base, C::cols);
             tmem_relinquish();
-        }
-        {   // pages that the item needs and the table does not have
-            const int nbox = kTile / P.box, end = n * nbox;
-            bool lost = false;
-            for (int b = t - 160; b < end; b += 64) {
-                const int bx = w.slot0(b / nbox) + (b & (nbox - 1)) * P.box;
-                if (box_seen(w.g, bx, P.box) && paged_page(p, w.it, bx) < 0) lost = true;
-            }
-            if (lost) sh.lost = 1;
         }
         set_up_done();
         const uint32_t tmem = sh.tmem_base;
