@@ -12,7 +12,7 @@ constexpr int kSms = 152;   // GB300
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Items that run at the same time, and the most rounds of them that a call is split into.
-constexpr int kSlotsSimt = kSms * 3, kSlotsTc = kSms * 2;
+constexpr int kSlotsSimt = kSms * 3, kSlotsTc = kSms * 2, kSlotsQ8Rows = kSms;
 constexpr int kRounds = 8;
 // What an item costs beside its tiles (the rows' counts, the first pages, the output, its share of
 // the join), in tiles. Measured: 32 sequences of 4K to 16K tokens, 8 key/value heads, d 128 take
@@ -121,13 +121,13 @@ struct Plan {
     int nrb[2], head_blocks[2];
     long long units[2];    // (sequence, key/value head, row block) triples
     long long tiles[2];    // key tiles of one of them, at most, without a window
-    long long slots;       // items that run at the same time
+    long long slots[2];    // items that run at the same time
     long long max_split;   // items of a row, at most, whatever the window
 };
 
 // Items along the keys of a part, at most: kRounds rounds of items over all units.
 long long most_chunks(const Plan& x, int part, long long tiles) {
-    const long long c = ceil_div(x.slots * kRounds, x.units[part]);
+    const long long c = ceil_div(x.slots[part] * kRounds, x.units[part]);
     return c < tiles ? c : tiles;
 }
 
@@ -141,19 +141,21 @@ Kind kind_of(saf_dtype_t dt, bool q8) {
 Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, Kind kind) {
     const bool bf16 = kind == Kind::kTc || kind == Kind::kTcQ8;
     Plan x;
-    x.slots = bf16 ? kSlotsTc : kSlotsSimt;
     const long long G = H / Hkv;
     const long long n[2] = {P > 0 ? G * B * T : 0, G * T};
     const int keys[2] = {P, max_len};
     x.max_split = 0;
     for (int i = 0; i < 2; ++i) {
+        x.slots[i] = bf16 ? kSlotsTc : kSlotsSimt;
         // tensor cores: copies of the rows fill the 128 of a tile (paged_tc.cu)
         x.rows[i] = !bf16 ? kSimtRows : n[i] <= 32 ? 32 : n[i] <= 64 ? 64 : 128;
         x.tile[i] = bf16 ? paged_tc_tile(d, x.rows[i]) : kSimtTile;
-        if (kind == Kind::kTcQ8) {   // one kernel serves both parts: its rows are those of the larger need
-            const long long most = n[0] > n[1] ? n[0] : n[1];
-            x.rows[i] = most <= 4 ? 4 : most <= 8 ? 8 : most <= 16 ? 16 : 32;
-            x.tile[i] = kQ8Tile;
+        if (kind == Kind::kTcQ8) {
+            // few rows: the keys in the lanes; a launch serves both parts, with the rows of the larger need
+            const long long most = n[0] > n[1] && n[0] <= 32 ? n[0] : n[1];
+            x.rows[i] = n[i] > 32 ? kQ8Rows : most <= 4 ? 4 : most <= 8 ? 8 : most <= 16 ? 16 : 32;
+            x.tile[i] = n[i] > 32 ? kQ8RowsTile : kQ8Tile;
+            x.slots[i] = n[i] > 32 ? kSlotsQ8Rows : x.rows[i] == 4 ? kSms * 3 : kSms * 2;
         }
         // several blocks to a head: each head begins its own
         const long long per_head = n[i] / G;
@@ -194,7 +196,7 @@ void set_items(PagedArgs& p, const Plan& x, int nfrozen) {
     long long nt[2] = {x.tiles[0], x.tiles[1]};
     const bool windowed = p.window > 0 && nfrozen == 0;
     unsigned items[2];
-    long long slots = x.slots;
+    long long beside = 0;   // slots that the own items take while the prefix's run
     for (int i = 1; i >= 0; --i) {
         p.nrb[i] = x.nrb[i];
         p.head_blocks[i] = x.head_blocks[i];
@@ -215,14 +217,15 @@ void set_items(PagedArgs& p, const Plan& x, int nfrozen) {
             if (n < nt[i]) nt[i] = n;
         }
         // (a prefix's units have the same length, and so have windows)
-        const long long c = pick_chunks(x.units[i], nt[i], most_chunks(x, i, nt[i]), slots, i == 0 || windowed,
-                                        p.P > 0);
+        const long long c = pick_chunks(x.units[i], nt[i], most_chunks(x, i, nt[i]), x.slots[i] - beside,
+                                        i == 0 || windowed, p.P > 0);
         p.per_chunk[i] = (int)ceil_div(nt[i], c);
         p.chunks[i] = (int)ceil_div(nt[i], p.per_chunk[i]);
         items[i] = (unsigned)(x.units[i] * p.chunks[i]);
         // Few own items run beside the prefix's, in the same round. (Half of the slots for the
         // prefix beside many own items was slower: 176 against 111 us for 64 sequences after 32K.)
-        if (items[i] < slots / 2) slots -= items[i];
+        // (Parts that run in launches of their own are not beside each other.)
+        if ((x.rows[0] == kQ8Rows) == (x.rows[1] == kQ8Rows) && items[i] < x.slots[i] / 2) beside = items[i];
     }
     p.nsplit = p.chunks[0] + p.chunks[1];
     p.items0 = items[0];
@@ -250,6 +253,25 @@ int check_sizes(int B, int H, int Hkv, int T, int d, int max_len, int prefix_len
     if (max_len < 1 || prefix_len < 0 || (long long)max_len + prefix_len > (1ll << 30)) return SAF_EINVAL;
     if ((long long)B * H * T > (1ll << 29)) return SAF_EINVAL;   // (items are counted in 32 bits)
     return SAF_OK;
+}
+
+// The kernels over 8-bit caches: one launch, or one for each part where one part has few rows and the other many.
+cudaError_t launch_q8(const PagedArgs& p, cudaStream_t s) {
+    const unsigned items1 = p.items - p.items0;
+    if (p.items0 == 0 || items1 == 0 || p.rows[0] == p.rows[1]) {
+        const int rows = p.items0 ? p.rows[0] : p.rows[1];
+        return rows == kQ8Rows ? launch_paged_q8_rows(p, p.items, s) : launch_paged_q8(p, rows, p.items, s);
+    }
+    PagedArgs own = p;   // part 1 alone
+    own.items0 = 0;
+    for (int part = 0; part < 2; ++part) {
+        if (part) note_launch();
+        const cudaError_t e = p.rows[part] == kQ8Rows
+                                  ? launch_paged_q8_rows(part ? own : p, part ? items1 : p.items0, s)
+                                  : launch_paged_q8(part ? own : p, p.rows[part], part ? items1 : p.items0, s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 // q8: the caches hold codes of e4m3, with scales.
@@ -339,7 +361,7 @@ int paged(const void* q, const void* k_cache, const void* v_cache, bool q8, cons
     before_launch(SAF_KERNEL_PAGED, s);
     cudaError_t e = kind == Kind::kTc      ? launch_paged_tc(p, s)
                     : kind == Kind::kSimt ? launch_paged_simt(p, s)
-                    : kind == Kind::kTcQ8 ? launch_paged_q8(p, s)
+                    : kind == Kind::kTcQ8 ? launch_q8(p, s)
                                           : launch_paged_simt_q8(p, s);
     if (e == cudaSuccess && p.nsplit > 1) {
         note_launch();

@@ -106,5 +106,16 @@ __device__ __forceinline__ void load_warp(const Q8Params& P, const Work& w, uint
     }
 }
 
+// What a launch passes on: the tensor maps of the caches, read in boxes of at most `tile` keys.
+inline bool q8_params(Q8Params* P, const PagedArgs& a, int tile) {
+    P->a = a;
+    const int page = 1 << a.page_log2;
+    P->box = page < tile ? page : tile;
+    const uint64_t slices = (uint64_t)a.num_pages * a.Hkv;
+    const void* k = a.k_cache ? a.k_cache : a.v_cache;   // (no K is loaded when every head is frozen)
+    return make_tmap_u8_3d(&P->tm_k, k, a.d, page, slices, 128, P->box) &&
+           make_tmap_u8_3d(&P->tm_v, a.v_cache, a.d, page, slices, 128, P->box);
+}
+
 }  // namespace paged_q8
 }  // namespace saf

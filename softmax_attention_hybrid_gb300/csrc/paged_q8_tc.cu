@@ -567,32 +567,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::ctas) paged_q8_kernel(const 
 }
 
 template <int R>
-cudaError_t launch_r(const Q8Params& P, cudaStream_t s) {
+cudaError_t launch_r(const Q8Params& P, unsigned items, cudaStream_t s) {
     constexpr int smem = Cfg<R>::total + 1024;
     static_assert(Cfg<R>::slots <= kMaxSlots, "barriers of the ring");
     const cudaError_t e =
         cudaFuncSetAttribute(paged_q8_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_ex(paged_q8_kernel<R>, dim3(P.a.items), dim3(kThreads), (size_t)smem, s, true, 1, P);
+    return launch_ex(paged_q8_kernel<R>, dim3(items), dim3(kThreads), (size_t)smem, s, true, 1, P);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_q8(const PagedArgs& a, cudaStream_t s) {
+cudaError_t launch_paged_q8(const PagedArgs& a, int rows, unsigned items, cudaStream_t s) {
     Q8Params P;
-    P.a = a;
-    const int page = 1 << a.page_log2;
-    P.box = page < kTile ? page : kTile;
-    const uint64_t slices = (uint64_t)a.num_pages * a.Hkv;
-    const void* k = a.k_cache ? a.k_cache : a.v_cache;   // (no K is loaded when every head is frozen)
-    if (!make_tmap_u8_3d(&P.tm_k, k, a.d, page, slices, 128, P.box) ||
-        !make_tmap_u8_3d(&P.tm_v, a.v_cache, a.d, page, slices, 128, P.box))
-        return cudaErrorInvalidValue;
-    switch (a.rows[1]) {
-        case 4: return launch_r<4>(P, s);
-        case 8: return launch_r<8>(P, s);
-        case 16: return launch_r<16>(P, s);
-        default: return launch_r<32>(P, s);
+    if (!q8_params(&P, a, kTile)) return cudaErrorInvalidValue;
+    switch (rows) {
+        case 4: return launch_r<4>(P, items, s);
+        case 8: return launch_r<8>(P, items, s);
+        case 16: return launch_r<16>(P, items, s);
+        default: return launch_r<32>(P, items, s);
     }
 }
 
