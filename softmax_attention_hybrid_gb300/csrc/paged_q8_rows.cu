@@ -2,22 +2,24 @@
 // a prefix that a batch shares. See paged.h for the split, paged_q8_tc.cu for few rows.
 //
 // Up to 256 rows of one key/value head, in two groups of M = 128 (a thread per row), meet tiles of
-// 64 keys:
+// 128 keys:
 //   S = q K^T with K's codes as they lie in the cache (kind::f8f6f4): q, scaled by a power of two so that
 //     its largest lies in (224, 448], as hi = e4m3(q) and lo = e4m3(q - hi), two products into one sum.
 //     What they leave is at most 2^-10, 2^-17 of the row's largest.
-//   O += P V in fp16 (kind::f16): a code of e4m3 is an fp16 number, exactly; four warps unpack the tile of V
-//     once for all rows. The weight takes its value's scale, P_j s_v[j] 2^(7 - V) <= 2^15 with s_v <= 2^V
-//     the scales so far, and is rounded to fp16: off by 2^-11, or by 2^-32 of a weight at the maximum.
+//   O += P V in fp16 (kind::f16). Four warps turn a tile of V into code s_v 2^(7 - V) <= 57344, once for all
+//     rows, with s_v <= 2^V the scales so far (the scale and the product are rounded: 2^-11); the weight is
+//     2^7 of itself in fp16, at most 2^15 (2^-12, or 2^-32 of a weight at the maximum).
 // The key's scale multiplies the scores. Sums are fp32 in tensor memory, l adds the weights unrounded.
 //
-// Bound by exponentials: 256 x 64 of a tile take 1024 cycles of an SM, its MMAs 512. (256 rows to
-// a CTA because 128 would read each tile twice as often from L2: 32 bytes a cycle and SM.)
+// A group's S and P share their columns of tensor memory, so that its S, softmax and P V follow one
+// another; the two groups do so in turn. The softmax goes over the tile twice, 32 keys at a time: scaled
+// and masked scores back to tensor memory with their maximum, then the weights.
+// (256 rows to a CTA because 128 would read each tile twice as often from L2.)
 //
 // Warps (512 threads, one CTA per SM): 0-7 rows, 8-11 unpack V and hand out the scales, 12 loads K, V and
-// scales, 13 owns tensor memory and issues S, 14 issues P V, 15 brings the frozen heads' a and r
+// scales, 13 and 14 issue a group's MMAs each (13 owns tensor memory), 15 brings the frozen heads' a and r
 // of the next tile into shared memory.
-// Tensor memory, per group: S (64 columns) | P (32, fp16 pairs) | O.
+// Tensor memory, per group: S, then P (fp16 pairs) in its place | O.
 // Shared memory: q's terms, a ring of tiles of K or V in the order in which they are used (K0, K1, V0,
 // K2, V1, ...; V0, V1, ... where no row is ordinary), two tiles of V in fp16, the patterns.
 #include <string.h>
@@ -39,14 +41,15 @@ constexpr int TK = kQ8RowsTile;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;   // lazy rescale: factor 256
-constexpr int kWeightExp = 7;               // a weight of the maximum is 2^7, before the value's scale
-constexpr int kPatFloats = 2048;            // room for the frozen heads' patterns of a tile
+constexpr int kWeightExp = 7;               // a weight of the maximum is 2^7; values of the largest scale are 2^7 codes
+constexpr int kNoExp = -1000;               // no scale seen yet
+constexpr int kPatFloats = 2560;            // room for the frozen heads' patterns of a tile
 
 // kD: columns of O as the tiles hold them (64, or 128 for 96 and 128).
 template <int kD>
 struct Cfg {
     static constexpr int tile = TK;
-    static constexpr int slots = 8;
+    static constexpr int slots = 4;
     static constexpr int q = 0;                                   // group g, term t at 16384 (2 g + t)
     static constexpr int ring = q + 4 * 128 * 128;
     static constexpr int v16_atom = TK * 128;                     // TK keys x 64 columns
@@ -56,13 +59,13 @@ struct Cfg {
     static constexpr int pat = scales + slots * TK * 4;
     static constexpr int total = pat + 2 * kPatFloats * 4;
     // tensor-memory columns of a group (S at 0)
-    static constexpr uint32_t group = 256, col_p = TK, col_o = 128;
-    static_assert(col_p + TK / 2 <= col_o && col_o + kD <= group, "tensor memory");
+    static constexpr uint32_t group = 256, col_o = TK;
+    static_assert(col_o + kD <= group, "tensor memory");
 };
 
 struct Bars {
-    uint64_t full[8], empty[8];
-    uint64_t s_full[2], s_empty[2], p_ready[2], o_done[2];   // of a group
+    uint64_t full[4], empty[4];
+    uint64_t s_full[2], p_ready[2], o_done[2];               // of a group
     uint64_t sc_ready[2], v_ready[2], v_free[2];             // of the tile's parity
     uint64_t pat_full[2], pat_empty[2], mma_idle[2];
 };
@@ -72,7 +75,6 @@ struct Shared {
     uint32_t tmem_base;
     int abort_flag, imin, imax, kinds, frozen_warps, lost;
     alignas(16) float ks[2][TK];   // scales of a tile's keys
-    alignas(16) float vs[2][TK];   // of its values, times 2^(7 - V); 0 where no row sees the key
     int vexp[2];                   // V
 };
 
@@ -143,6 +145,12 @@ __device__ __forceinline__ void pattern_warp(const Q8Params& P, const RowsWork& 
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Warps 8-11: the scales of a tile, then its values as fp16.
 template <int kD>
 __device__ __forceinline__ void unpack_warps(const Q8Params& P, const RowsWork& w, uint8_t* sm, Shared& sh) {
@@ -162,55 +170,66 @@ __device__ __forceinline__ void unpack_warps(const Q8Params& P, const RowsWork& 
             const int ld = w.k_load(j), s = ld % C::slots;
             if (!wait_all(&bars.full[s], (ld / C::slots) & 1, abort, p.status)) break;
             const float* ks = reinterpret_cast<const float*>(sm + C::scales + s * TK * 4);
-            if (warp == 0) *reinterpret_cast<float2*>(&sh.ks[buf][2 * lane]) = *reinterpret_cast<const float2*>(&ks[2 * lane]);
+            if (warp == 0) *reinterpret_cast<float4*>(&sh.ks[buf][4 * lane]) = *reinterpret_cast<const float4*>(&ks[4 * lane]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.empty[s]);
         }
         const int ld = w.v_load(j), s = ld % C::slots;
         if (!wait_all(&bars.full[s], (ld / C::slots) & 1, abort, p.status)) break;
-        float2 vs = *reinterpret_cast<const float2*>(sm + C::scales + s * TK * 4 + 8 * lane);
+        const float* vs = reinterpret_cast<const float*>(sm + C::scales + s * TK * 4);
         // codes and scales of slots that no row sees may be anything: zeros, for 0 * NaN is none
         const bool lost = *(volatile int*)&sh.lost != 0;
-        uint32_t seen0 = 0xffffffffu, seen1 = 0xffffffffu;   // keys 2 lane, 2 lane + 1
         const bool cut = lost || x0 + TK > w.g.hi || (x0 < w.g.lo && x0 + TK > w.g.sink);
-        if (cut) {
-            auto seen = [&](int k) {
-                const int x = x0 + k, bx = x0 + k / P.box * P.box;
-                return x < w.g.hi && (x >= w.g.lo || x < w.g.sink) && !(lost && paged_page(p, w.it, bx) < 0);
-            };
-            const bool a = seen(2 * lane), b = seen(2 * lane + 1);
-            seen0 = __ballot_sync(0xffffffffu, a);
-            seen1 = __ballot_sync(0xffffffffu, b);
-            if (!a) vs.x = 0.f;
-            if (!b) vs.y = 0.f;
+        float v[TK / 32];        // of keys lane, lane + 32, ...
+        uint32_t seen[TK / 32];
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < TK / 32; ++k) {
+            v[k] = vs[32 * k + lane];
+            seen[k] = 0xffffffffu;
+            if (cut) {
+                const int x = x0 + 32 * k + lane, bx = x0 + (32 * k + lane) / P.box * P.box;
+                const bool a = x < w.g.hi && (x >= w.g.lo || x < w.g.sink) && !(lost && paged_page(p, w.it, bx) < 0);
+                seen[k] = __ballot_sync(0xffffffffu, a);
+                if (!a) v[k] = 0.f;
+            }
+            top = fmaxf(top, v[k]);
         }
         // (scales are not negative: their bits have their order)
-        const float vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs.x, vs.y))));
-        if (vmax > vtop) {
-            int ex = (int)((__float_as_uint(vmax) >> 23) & 255u) - 126;   // vmax < 2^ex
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+        if (top > vtop) {
+            const int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 126;   // top < 2^ex
             vexp = ex < -110 ? -110 : ex > 127 ? 127 : ex;
             vtop = pow2i(vexp);
         }
         if (warp == 0) {
-            const float f = pow2i(kWeightExp - vexp);
-            *reinterpret_cast<float2*>(&sh.vs[buf][2 * lane]) = make_float2(vs.x * f, vs.y * f);
-            if (lane == 0) sh.vexp[buf] = vtop > 0.f ? vexp : -1000;
+            if (lane == 0) {
+                sh.vexp[buf] = vtop > 0.f ? vexp : kNoExp;
+                mbar_arrive(&bars.sc_ready[buf]);   // (behind the other lanes' scales: the warp met since)
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.sc_ready[buf]);
         }
-        // A warp takes 16 keys, 4 at a time; lane: 16 codes of a key.
+        const float f = pow2i(kWeightExp - vexp);
+        // A warp takes a quarter of the keys; lane: 16 codes of a key.
         const uint8_t* src = sm + C::ring + s * TK * 128;
         uint8_t* dst = sm + C::v16 + buf * C::v16_tile;
         constexpr int kChunks = kD / 16;            // of 16 codes in a row
         constexpr int kKeys = 32 / kChunks;         // keys at a time
         const int c = lane % kChunks;
+        static_assert(TK == 128, "a warp takes the keys whose scales lie in v[warp]");
+        const float mine = warp == 0 ? v[0] : warp == 1 ? v[1] : warp == 2 ? v[2] : v[3];
+        const uint32_t here = warp == 0 ? seen[0] : warp == 1 ? seen[1] : warp == 2 ? seen[2] : seen[3];
 #pragma unroll
-        for (int k0 = 0; k0 < 16; k0 += kKeys) {
-            const int key = 16 * warp + k0 + lane / kChunks;
+        for (int k0 = 0; k0 < 32; k0 += kKeys) {
+            const int in = k0 + lane / kChunks, key = 32 * warp + in;
             uint4 x = *reinterpret_cast<const uint4*>(src + sw128_offset(key, 16 * c));
-            if (cut && !(((key & 1 ? seen1 : seen0) >> (key >> 1)) & 1u)) x = make_uint4(0, 0, 0, 0);
-            const uint4 a = make_uint4(codes_f16(x.x), codes_f16(x.x >> 16), codes_f16(x.y), codes_f16(x.y >> 16));
-            const uint4 b = make_uint4(codes_f16(x.z), codes_f16(x.z >> 16), codes_f16(x.w), codes_f16(x.w >> 16));
+            const float sv = __shfl_sync(0xffffffffu, mine, in) * f;
+            const uint32_t s2 = pack_f16(sv, sv);
+            if (!((here >> in) & 1u)) x = make_uint4(0, 0, 0, 0);
+            const uint4 a = make_uint4(hmul2(codes_f16(x.x), s2), hmul2(codes_f16(x.x >> 16), s2),
+                                       hmul2(codes_f16(x.y), s2), hmul2(codes_f16(x.y >> 16), s2));
+            const uint4 b = make_uint4(hmul2(codes_f16(x.z), s2), hmul2(codes_f16(x.z >> 16), s2),
+                                       hmul2(codes_f16(x.w), s2), hmul2(codes_f16(x.w >> 16), s2));
             // 32 bytes of a row of 64 columns; lanes of the second atom write theirs in the other order, to other banks
             uint8_t* row = dst + (c >> 2) * C::v16_atom;
             const uint32_t o0 = sw128_offset(key, 32 * (c & 3)), o1 = sw128_offset(key, 32 * (c & 3) + 16);
@@ -223,9 +242,15 @@ __device__ __forceinline__ void unpack_warps(const Q8Params& P, const RowsWork& 
         if (lane == 0) {
             mbar_arrive(&bars.v_ready[buf]);
             mbar_arrive(&bars.empty[s]);
-            if (warp == 0) mbar_arrive(&bars.empty[s]);   // (a slot's barrier counts the MMAs of K too)
+            if (warp < w.groups) mbar_arrive(&bars.empty[s]);   // (a slot's barrier counts the groups' MMAs on K too)
         }
     }
+}
+
+// Keys [first, first + 32) of which those below `end` are set.
+__device__ __forceinline__ uint32_t below(int end, int first) {
+    const int n = end - first;
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
 // Warps 0-7 of a group that has rows: thread = row.
@@ -238,7 +263,6 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
     volatile int* abort = &sh.abort_flag;
     const int t = threadIdx.x, g = t >> 7, warp = (t >> 5) & 3, lane = t & 31;
     const uint32_t tmem = sh.tmem_base + g * C::group + ((uint32_t)(warp * 32) << 16);
-    const int box_log2 = __ffs(P.box) - 1;
     const int i = row.i < 0 ? -1 : row.i - w.off;   // my last visible slot of the part
     const bool frozen = row.frozen && i >= 0;
     const float sc = row.frozen ? kLog2e : qscale;
@@ -248,87 +272,89 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
     // my staged pattern: a of the tile's keys, and r from the far end on (entry k - c for key c)
     const float* pat_a = reinterpret_cast<const float*>(sm + C::pat) + (frozen ? row.gi - w.fz0 : 0) * w.pitch();
     const float* pat_r = pat_a + TK + (TK - 1) + (frozen ? row.i - w.imin : 0);
-    float m = -INFINITY, l = 0.f;
-    int vexp = -1000;
+    float m = -INFINITY, l = 0.f;   // (l: times 2^kWeightExp)
+    int vexp = kNoExp;
     bool ok = true;
 
     const int tiles = w.e1 - w.e0;
     int n = 0;
     for (; n < tiles; ++n) {
         const int x0 = w.slot0(n, TK), buf = n & 1;
-        uint32_t sv[TK];
-        if (w.any_ord) {
-            if (!(ok = mbar_wait(&bars.s_full[g], n & 1, abort, p.status, kStatusTimeout))) break;
-            tc_fence_after();
-            tmem_ld32(tmem, sv);
-            tmem_ld32(tmem + 32, sv + 32);
-            tmem_ld_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.s_empty[g]);
-        }
-        if (!(ok = mbar_wait(&bars.sc_ready[buf], (n >> 1) & 1, abort, p.status, kStatusTimeout))) break;
-        if (w.any_ord && any_scaled) {
-#pragma unroll
-            for (int c = 0; c < TK; c += 4) {
-                const float4 ks = *reinterpret_cast<const float4*>(&sh.ks[buf][c]);
-                const float2 a = fmul2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), make_float2(ks.x, ks.y));
-                const float2 b = fmul2(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), make_float2(ks.z, ks.w));
-                sv[c] = __float_as_uint(a.x);
-                sv[c + 1] = __float_as_uint(a.y);
-                sv[c + 2] = __float_as_uint(b.x);
-                sv[c + 3] = __float_as_uint(b.y);
+        if (!(ok = wait_all(&bars.sc_ready[buf], (n >> 1) & 1, abort, p.status))) break;
+        if (any_frozen && w.staged && !(ok = wait_all(&bars.pat_full[buf], (n >> 1) & 1, abort, p.status))) break;
+        // S is there; and P V of the previous tile, after which it was issued, is done: O is stable
+        if (w.any_ord) ok = wait_all(&bars.s_full[g], n & 1, abort, p.status);
+        else if (n > 0) ok = wait_all(&bars.o_done[g], (n - 1) & 1, abort, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const bool lost = *(volatile int*)&sh.lost != 0;
+        // masks, in tiles that some row does not see whole
+        const bool cut = lost || x0 + TK > w.g.hi || x0 + TK - 1 > w.imin - w.off ||
+                         (p.window > 0 && x0 <= w.imax - w.off - p.window);
+        float ma = -INFINITY, mb = -INFINITY;
+        uint32_t sv[32];
+#pragma unroll 1
+        for (int c0 = 0; c0 < TK; c0 += 32) {
+            if (w.any_ord) {
+                tmem_ld32(tmem + c0, sv);
+                tmem_ld_wait();
             }
-        }
-        if (any_frozen) {   // the fixed pattern's logits (Eq. 3)
-            if (w.staged) {
-                if (!(ok = mbar_wait(&bars.pat_full[buf], (n >> 1) & 1, abort, p.status, kStatusTimeout))) break;
-                if (frozen) {
-                    const float* qa = pat_a + buf * kPatFloats;
-                    const float* qr = pat_r + buf * kPatFloats;
+            if (any_scaled) {
 #pragma unroll
-                    for (int c = 0; c < TK; c += 4) {
-                        const float4 a4 = *reinterpret_cast<const float4*>(qa + c);
-                        sv[c] = __float_as_uint(a4.x + qr[-c]);
-                        sv[c + 1] = __float_as_uint(a4.y + qr[-c - 1]);
-                        sv[c + 2] = __float_as_uint(a4.z + qr[-c - 2]);
-                        sv[c + 3] = __float_as_uint(a4.w + qr[-c - 3]);
+                for (int c = 0; c < 32; c += 4) {
+                    const float4 ks = *reinterpret_cast<const float4*>(&sh.ks[buf][c0 + c]);
+                    const float2 a = fmul2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), make_float2(ks.x, ks.y));
+                    const float2 b = fmul2(make_float2(__uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3])), make_float2(ks.z, ks.w));
+                    sv[c] = __float_as_uint(a.x);
+                    sv[c + 1] = __float_as_uint(a.y);
+                    sv[c + 2] = __float_as_uint(b.x);
+                    sv[c + 3] = __float_as_uint(b.y);
+                }
+            }
+            if (any_frozen) {   // the fixed pattern's logits (Eq. 3)
+                if (w.staged) {
+                    const float* qa = pat_a + buf * kPatFloats + c0;
+                    const float* qr = pat_r + buf * kPatFloats - c0;
+                    if (frozen) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 a4 = *reinterpret_cast<const float4*>(qa + c);
+                            sv[c] = __float_as_uint(a4.x + qr[-c]);
+                            sv[c + 1] = __float_as_uint(a4.y + qr[-c - 1]);
+                            sv[c + 2] = __float_as_uint(a4.z + qr[-c - 2]);
+                            sv[c + 3] = __float_as_uint(a4.w + qr[-c - 3]);
+                        }
+                    }
+                } else if (frozen) {   // (keys past my own position are masked below)
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const int y = min(x0 + c0 + c, i);
+                        sv[c] = __float_as_uint(__ldg(ra + y) + __ldg(rr + i - y));
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.pat_empty[buf]);
-            } else if (frozen) {   // (keys past my own position are masked below)
-#pragma unroll
-                for (int c = 0; c < TK; ++c) {
-                    const int y = min(x0 + c, i);
-                    sv[c] = __float_as_uint(__ldg(ra + y) + __ldg(rr + i - y));
-                }
             }
-        }
-        // masks, in tiles that some row does not see whole
-        const bool lost = *(volatile int*)&sh.lost != 0;
-        if (lost || x0 + TK > w.g.hi || x0 + TK - 1 > w.imin - w.off ||
-            (p.window > 0 && x0 <= w.imax - w.off - p.window)) {
-            uint32_t have = 0xffffffffu;   // boxes whose page is in the cache
-            if (lost)
-                for (int b = 0; b < TK / P.box; ++b) {
-                    const int bx = x0 + b * P.box;
-                    if (box_seen(w.g, bx, P.box) && paged_page(p, w.it, bx) < 0) have &= ~(1u << b);
-                }
-            const int lo = row.frozen || p.window == 0 ? -1 : i - p.window;   // slots <= lo: sinks only
-            const int sink = p.sinks - w.off, last = min(i, w.g.hi - 1);   // (a prefix ends before i)
+            if (cut) {
+                const int first = x0 + c0, last = min(i, w.g.hi - 1);   // (a prefix ends before i)
+                uint32_t vis = below(last + 1, first);
+                if (!row.frozen && p.window > 0) vis &= ~below(i - p.window + 1, first) | below(p.sinks - w.off, first);
+                if (lost)
+                    for (int bx = first & ~(P.box - 1); bx < first + 32; bx += P.box)
+                        if (box_seen(w.g, bx, P.box) && paged_page(p, w.it, bx) < 0)
+                            vis &= ~(below(bx + P.box, first) & ~below(bx, first));
 #pragma unroll
-            for (int c = 0; c < TK; ++c) {
-                const int x = x0 + c;
-                const bool seen = x <= last && (x > lo || x < sink) && ((have >> (c >> box_log2)) & 1u);
-                if (!seen) sv[c] = __float_as_uint(-INFINITY);
+                for (int c = 0; c < 32; ++c)
+                    if (!((vis >> c) & 1u)) sv[c] = __float_as_uint(-INFINITY);
             }
-        }
-        float ma = -INFINITY, mb = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < TK; c += 4) {
-            ma = fmax3(ma, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-            mb = fmax3(mb, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+            for (int c = 0; c < 32; c += 4) {
+                ma = fmax3(ma, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+                mb = fmax3(mb, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+            }
+            tmem_st32(tmem + c0, sv);
+        }
+        if (any_frozen && w.staged) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.pat_empty[buf]);
         }
         const float m_new = fmaxf(m, fmaxf(ma, mb) * sc);
         float f = 1.f;   // of O
@@ -340,60 +366,56 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
         }
         const int now = sh.vexp[buf];   // (the same for every row)
         if (now != vexp) {
-            f *= vexp == -1000 ? 0.f : exp2f((float)(vexp - now));
+            f *= vexp == kNoExp ? 0.f : exp2f((float)(vexp - now));
             vexp = now;
             need = true;
         }
-        const float ref = m == -INFINITY ? 0.f : m;   // a row that has seen no key yet: weights 2^-inf = 0
-        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-ref, -ref);
-        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-        uint32_t pk[TK / 2];
-#pragma unroll
-        for (int c = 0; c < TK / 2; c += 2) {
-            const float4 vs = *reinterpret_cast<const float4*>(&sh.vs[buf][2 * c]);
-            const float2 x = ffma2(make_float2(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), sc2, nm2);
-            const float2 y = ffma2(make_float2(__uint_as_float(sv[2 * c + 2]), __uint_as_float(sv[2 * c + 3])), sc2, nm2);
-            const float2 ex = make_float2(fast_exp2(x.x), fast_exp2(x.y)), ey = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-            acc0 = fadd2(acc0, ex);
-            acc1 = fadd2(acc1, ey);
-            const float2 wx = fmul2(ex, make_float2(vs.x, vs.y)), wy = fmul2(ey, make_float2(vs.z, vs.w));
-            pk[c] = pack_f16(wx.x, wx.y);
-            pk[c + 1] = pack_f16(wy.x, wy.y);
-        }
-        l += (acc0.x + acc1.x) + (acc0.y + acc1.y);
-        if (n > 0) {   // P V of the previous tile is done: P is free, O is stable
-            if (!(ok = mbar_wait(&bars.o_done[g], (n - 1) & 1, abort, p.status, kStatusTimeout))) break;
-            tc_fence_after();
-        }
-        tmem_st32(tmem + C::col_p, pk);
+        tmem_st_wait();
         if (n > 0 && __any_sync(0xffffffffu, need)) {
-            uint32_t ov[32];
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < kD; q += 32) {
-                tmem_ld32(tmem + C::col_o + q, ov);
+                tmem_ld32(tmem + C::col_o + q, sv);
                 tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * f);
-                tmem_st32(tmem + C::col_o + q, ov);
+                for (int c = 0; c < 32; ++c) sv[c] = __float_as_uint(__uint_as_float(sv[c]) * f);
+                tmem_st32(tmem + C::col_o + q, sv);
             }
         }
+        const float ref = m == -INFINITY ? 0.f : m;   // a row that has seen no key yet: weights 2^-inf = 0
+        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(kWeightExp - ref, kWeightExp - ref);
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int c0 = 0; c0 < TK; c0 += 32) {
+            tmem_ld32(tmem + c0, sv);
+            tmem_ld_wait();
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const float2 x = ffma2(make_float2(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), sc2, nm2);
+                const float2 ex = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                if (c & 1) acc1 = fadd2(acc1, ex);
+                else acc0 = fadd2(acc0, ex);
+                pk[c] = pack_f16(ex.x, ex.y);
+            }
+            tmem_st16(tmem + c0 / 2, pk);   // (in the place of scores that are read)
+        }
+        l += (acc0.x + acc1.x) + (acc0.y + acc1.y);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_ready[g]);
     }
-    // (a lane whose wait ran out leaves its warp's loop alone; the warp meets again here)
-    __syncwarp();
-    ok = __all_sync(0xffffffffu, ok) && mbar_wait_warp(&bars.o_done[g], (n - 1) & 1, abort, p.status, kStatusTimeout);
+    ok = ok && mbar_wait_warp(&bars.o_done[g], (n - 1) & 1, abort, p.status, kStatusTimeout);
     tc_fence_after();
     if (!ok) return;
     // my row
+    l *= pow2i(-kWeightExp);
     const bool sees = row.i >= 0 && l != 0.f;   // (a NaN sum is one)
     const size_t at = paged_out_row(p, row);
     const int split = w.it.part ? p.chunks[0] + w.it.chunk : w.it.chunk;
-    const float back = vexp == -1000 ? 0.f : pow2i(vexp - kWeightExp);
+    const float back = vexp == kNoExp ? 0.f : pow2i(vexp - 2 * kWeightExp);
     const float mul = p.nsplit > 1 ? back : back * (1.f / l);
-#pragma unroll
+#pragma unroll 1
     for (int q = 0; q < kD; q += 32) {
         uint32_t ov[32];
         tmem_ld32(tmem + C::col_o + q, ov);
@@ -417,6 +439,52 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
     if (!row.there) return;
     if (p.nsplit > 1) p.ml[at * p.nsplit + split] = sees ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
     else p.lse[at] = sees ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// Warps 13 and 14: a group's MMAs. S of tile j + 1 takes the place of P of tile j, so it waits for its P V.
+template <int kD>
+__device__ __forceinline__ void issue_warp(const Q8Params& P, const RowsWork& w, int g, uint8_t* sm, Shared& sh) {
+    using C = Cfg<kD>;
+    const PagedArgs& p = P.a;
+    Bars& bars = sh.bars;
+    volatile int* abort = &sh.abort_flag;
+    constexpr uint32_t id_s = idesc_e4m3(128, TK, 0, 0), id_o = idesc_f16(128, kD, 0, 1);
+    const uint64_t d_q = sdesc_sw128(smem_u32(sm + C::q) + g * 2 * 16384, 16, 1024);   // K-major, as K
+    const uint64_t d_ring = sdesc_sw128(smem_u32(sm + C::ring), 16, 1024);
+    const uint64_t d_v16 = sdesc_sw128(smem_u32(sm + C::v16), C::v16_atom, 1024);      // MN-major
+    const uint32_t tmem = sh.tmem_base + g * C::group;
+    const int n = w.e1 - w.e0, steps = p.d / 32;
+    auto scores = [&](int j) -> bool {
+        const int ld = w.k_load(j), s = ld % C::slots;
+        if (!wait_all(&bars.full[s], (ld / C::slots) & 1, abort, p.status)) return false;
+        if (j > 0 && !wait_all(&bars.o_done[g], (j - 1) & 1, abort, p.status)) return false;
+        tc_fence_after();
+        const uint64_t d_k = sdesc_advance(d_ring, s * TK * 128);
+        for (int term = 0; term < 2; ++term)   // hi, then lo
+            for (int k = 0; k < steps; ++k)
+                mma_ss_e4m3_warp(tmem, sdesc_advance(d_q, term * 16384 + 32 * k), sdesc_advance(d_k, 32 * k), id_s,
+                                 term + k > 0);
+        mma_commit_warp(&bars.s_full[g]);
+        mma_commit_warp(&bars.empty[s]);
+        return true;
+    };
+    bool ok = !w.any_ord || scores(0);
+    for (int j = 0; j < n && ok; ++j) {
+        if (!wait_all(&bars.v_ready[j & 1], (j >> 1) & 1, abort, p.status)) break;
+        if (!wait_all(&bars.p_ready[g], j & 1, abort, p.status)) break;
+        tc_fence_after();
+        const uint64_t d_v = sdesc_advance(d_v16, (j & 1) * C::v16_tile);
+#pragma unroll
+        for (int k = 0; k < TK / 16; ++k)
+            mma_ts_warp(tmem + C::col_o, tmem + 8 * k, sdesc_advance(d_v, k * 2048), id_o, (j > 0 || k > 0) ? 1u : 0u);
+        mma_commit_warp(&bars.o_done[g]);
+        mma_commit_warp(&bars.v_free[j & 1]);
+        if (w.any_ord && j + 1 < n) ok = scores(j + 1);
+    }
+    // every MMA issued here is done before tensor memory is freed
+    mma_commit_warp(&bars.mma_idle[g]);
+    if ((threadIdx.x & 31) == 0) mbar_wait_bounded(&bars.mma_idle[g], 0, kWaitLimitNs);
+    __syncwarp();
 }
 
 // Every warp but the loading one: q's terms and tensor memory are there.
@@ -488,6 +556,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q8_rows_kernel(const __grid
     const PagedArgs& p = P.a;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     Bars& bars = sh.bars;
+    RowsWork w;
+    w.it = paged_item(p, blockIdx.x);
+    const PagedBlock block = paged_block(p, w.it);
+    w.there = block.there;
+    w.groups = block.there > 128 ? 2 : 1;
     if (warp == 0) {
         if (lane == 0) {
             sh.abort_flag = 0;
@@ -497,24 +570,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q8_rows_kernel(const __grid
         }
         if (lane < C::slots) {
             mbar_init(&bars.full[lane], 1);
-            mbar_init(&bars.empty[lane], 5);   // K: its MMAs and the four warps that read its scales; V: those warps
+            mbar_init(&bars.empty[lane], 4 + w.groups);   // K: the groups' MMAs and the four warps that read its scales
         } else if (lane < C::slots + 2) {
             const int i = lane - C::slots;
             mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.s_empty[i], 4);
             mbar_init(&bars.p_ready[i], 4);
             mbar_init(&bars.o_done[i], 1);
             mbar_init(&bars.sc_ready[i], 1);
             mbar_init(&bars.v_ready[i], 4);
-            mbar_init(&bars.v_free[i], 1);
+            mbar_init(&bars.v_free[i], w.groups);
             mbar_init(&bars.pat_full[i], 1);
             mbar_init(&bars.mma_idle[i], 1);
         }
         fence_mbar_init();
     }
-    RowsWork w;
-    w.it = paged_item(p, blockIdx.x);
-    const PagedBlock block = paged_block(p, w.it);
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
@@ -543,8 +612,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q8_rows_kernel(const __grid
     w.imax = sh.imax;
     w.any_ord = (sh.kinds & 1) != 0;
     w.off = w.it.part ? p.P : 0;
-    w.there = block.there;
-    w.groups = block.there > 128 ? 2 : 1;
     w.g = paged_range(p, w.it, w.imin, w.imax, (sh.kinds & 2) != 0 || p.window == 0);
     const int per = p.per_chunk[w.it.part];
     w.e0 = min(w.it.chunk * per, w.g.n);
@@ -566,8 +633,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q8_rows_kernel(const __grid
     w.fz0 = max(block.first / block.per_head, (int)p.gord[w.it.hk]);
     w.nf = (block.first + w.there - 1) / block.per_head - w.fz0 + 1;
     w.staged = (long long)w.nf * ((long long)w.imax - w.imin + 2 * TK + 3) <= kPatFloats;
-    const int n = w.e1 - w.e0;
-    volatile int* abort = &sh.abort_flag;
 
     // one setmaxnreg for each warpgroup
     if (warp < 8) {
@@ -595,61 +660,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q8_rows_kernel(const __grid
                 tmem_relinquish();
             }
             set_up_done();
-            const uint32_t tmem = sh.tmem_base;
-            if (warp == 13) {
-                // S of tile j, when K is there and the group has read S of tile j - 1
-                constexpr uint32_t id_s = idesc_e4m3(128, TK, 0, 0);
-                const uint64_t d_q = sdesc_sw128(smem_u32(sm + C::q), 16, 1024);   // K-major, as K
-                const uint64_t d_ring = sdesc_sw128(smem_u32(sm + C::ring), 16, 1024);
-                const int steps = p.d / 32;
-                for (int j = 0; j < n && w.any_ord; ++j) {
-                    const int ld = w.k_load(j), s = ld % C::slots;
-                    if (!wait_all(&bars.full[s], (ld / C::slots) & 1, abort, p.status)) break;
-                    const uint64_t d_k = sdesc_advance(d_ring, s * TK * 128);
-                    bool ok = true;
-                    for (int g = 0; g < w.groups && ok; ++g) {
-                        ok = j == 0 || wait_all(&bars.s_empty[g], (j - 1) & 1, abort, p.status);
-                        if (!ok) break;
-                        tc_fence_after();
-                        for (int k = 0; k < 2 * steps; ++k) {   // hi, then lo
-                            const int term = k >= steps, kk = k - term * steps;
-                            mma_ss_e4m3_warp(tmem + g * C::group, sdesc_advance(d_q, (2 * g + term) * 16384 + 32 * kk),
-                                             sdesc_advance(d_k, 32 * kk), id_s, k > 0);
-                        }
-                        mma_commit_warp(&bars.s_full[g]);
-                    }
-                    if (!ok) break;
-                    mma_commit_warp(&bars.empty[s]);
-                }
-            } else if (warp == 14) {
-                // O += P V of tile j, when V is unpacked and the group's weights are there
-                constexpr uint32_t id_o = idesc_f16(128, kD, 0, 1);
-                const uint64_t d_v16 = sdesc_sw128(smem_u32(sm + C::v16), C::v16_atom, 1024);   // MN-major
-                for (int j = 0; j < n; ++j) {
-                    if (!wait_all(&bars.v_ready[j & 1], (j >> 1) & 1, abort, p.status)) break;
-                    const uint64_t d_v = sdesc_advance(d_v16, (j & 1) * C::v16_tile);
-                    bool ok = true;
-                    for (int g = 0; g < w.groups && ok; ++g) {
-                        ok = wait_all(&bars.p_ready[g], j & 1, abort, p.status);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t base = tmem + g * C::group;
-#pragma unroll
-                        for (int k = 0; k < TK / 16; ++k)
-                            mma_ts_warp(base + C::col_o, base + C::col_p + 8 * k, sdesc_advance(d_v, k * 2048), id_o,
-                                        (j > 0 || k > 0) ? 1u : 0u);
-                        mma_commit_warp(&bars.o_done[g]);
-                    }
-                    if (!ok) break;
-                    mma_commit_warp(&bars.v_free[j & 1]);
-                }
+            if (warp < 15) {
+                if (warp - 13 < w.groups) issue_warp<kD>(P, w, warp - 13, sm, sh);
             } else if (sh.frozen_warps > 0 && w.staged) {
                 pattern_warp<kD>(P, w, sm, sh);
-            }
-            if (warp < 15) {   // every MMA issued here is done before tensor memory is freed
-                mma_commit_warp(&bars.mma_idle[warp - 13]);
-                if (lane == 0) mbar_wait_bounded(&bars.mma_idle[warp - 13], 0, kWaitLimitNs);
-                __syncwarp();
             }
         }
     }
