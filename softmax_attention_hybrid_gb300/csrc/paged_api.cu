@@ -18,6 +18,8 @@ constexpr int kRounds = 8;
 // the join), in tiles. Measured: 32 sequences of 4K to 16K tokens, 8 key/value heads, d 128 take
 // 237, 211, 210, 218, 215 us with 2, 3, 5, 8, 12 items per sequence and head.
 constexpr int kSetUp = 10;
+// 8-bit caches: of the kernel for few rows and of the one for many.
+constexpr int kSetUpQ8 = 7, kSetUpQ8Rows = 8;
 // What the joining kernel costs, in tiles, where a call could do without one: one new token of
 // one sequence (12 heads, d 64) takes 6.1 and 7.1 us with 1 and 2 items for 256 keys, 7.6 with 1
 // and 4 for 512, 10.5 and 8.5 for 1024.
@@ -117,7 +119,7 @@ cudaError_t launch_join(const PagedArgs& p, cudaStream_t s) {
 long long ceil_div(long long x, long long y) { return (x + y - 1) / y; }
 
 struct Plan {
-    int tile[2], rows[2];
+    int tile[2], rows[2], set_up[2];
     int nrb[2], head_blocks[2];
     long long units[2];    // (sequence, key/value head, row block) triples
     long long tiles[2];    // key tiles of one of them, at most, without a window
@@ -146,6 +148,7 @@ Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, Kind kin
     const int keys[2] = {P, max_len};
     x.max_split = 0;
     for (int i = 0; i < 2; ++i) {
+        x.set_up[i] = kSetUp;
         x.slots[i] = bf16 ? kSlotsTc : kSlotsSimt;
         // tensor cores: copies of the rows fill the 128 of a tile (paged_tc.cu)
         x.rows[i] = !bf16 ? kSimtRows : n[i] <= 32 ? 32 : n[i] <= 64 ? 64 : 128;
@@ -153,8 +156,9 @@ Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, Kind kin
         if (kind == Kind::kTcQ8) {
             // few rows: the keys in the lanes; a launch serves both parts, with the rows of the larger need
             const long long most = n[0] > n[1] && n[0] <= 32 ? n[0] : n[1];
-            x.rows[i] = n[i] > 32 ? kQ8Rows : most <= 4 ? 4 : most <= 8 ? 8 : most <= 16 ? 16 : 32;
+            x.rows[i] = n[i] > 32 ? kQ8Rows : most <= 4 ? 4 : most <= 8 ? 8 : most <= 16 ? 16 : most <= 24 ? 24 : 32;
             x.tile[i] = n[i] > 32 ? kQ8RowsTile : kQ8Tile;
+            x.set_up[i] = n[i] > 32 ? kSetUpQ8Rows : kSetUpQ8;
             x.slots[i] = n[i] > 32 ? kSlotsQ8Rows : x.rows[i] == 4 ? kSms * 3 : kSms * 2;
         }
         // several blocks to a head: each head begins its own
@@ -172,18 +176,19 @@ Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, Kind kin
 // shortest, with `slots` items at a time. even: the units have the same length, so that rounds
 // end together; else their lengths differ, and the last items run alone for a while.
 // Candidates: one, the most items that fit in 1, 2, ... rounds, and the minimum over c of
-// (units c / slots) (kSetUp + nt / c) + nt / c, the work and the tail of c items per unit.
-long long pick_chunks(long long units, long long nt, long long most, long long slots, bool even, bool joins_anyway) {
+// (units c / slots) (set_up + nt / c) + nt / c, the work and the tail of c items per unit.
+long long pick_chunks(long long units, long long nt, long long most, long long slots, int set_up, bool even,
+                      bool joins_anyway) {
     long long best = 1;
     double best_cost = 1e300;
     for (int r = -1; r <= kRounds; ++r) {
         long long c = r < 0 ? 1 : r ? slots * r / units
-                        : (long long)sqrt((double)nt * (double)slots / ((double)units * (double)kSetUp));
+                        : (long long)sqrt((double)nt * (double)slots / ((double)units * (double)set_up));
         c = c < 1 ? 1 : c > most ? most : c;
         const long long per = ceil_div(nt, c);
         const double rounds = (double)(units * ceil_div(nt, per)) / (double)slots;
         const double cost =
-            (even ? ceil(rounds) : rounds + 1.0) * (double)(kSetUp + per) + (c > 1 && !joins_anyway ? kJoin : 0);
+            (even ? ceil(rounds) : rounds + 1.0) * (double)(set_up + per) + (c > 1 && !joins_anyway ? kJoin : 0);
         if (cost < best_cost || (cost == best_cost && c < best)) {
             best_cost = cost;
             best = c;
@@ -216,9 +221,9 @@ void set_items(PagedArgs& p, const Plan& x, int nfrozen) {
             const long long n = ceil_div(span, x.tile[i]) + 1 + ceil_div(sinks, x.tile[i]);
             if (n < nt[i]) nt[i] = n;
         }
-        // (a prefix's units have the same length, and so have windows)
+        // (a prefix's units have the same length, and so have windows; paged_q8_rows.cu runs the longest first)
         const long long c = pick_chunks(x.units[i], nt[i], most_chunks(x, i, nt[i]), x.slots[i] - beside,
-                                        i == 0 || windowed, p.P > 0);
+                                        x.set_up[i], i == 0 || windowed || x.rows[i] == kQ8Rows, p.P > 0);
         p.per_chunk[i] = (int)ceil_div(nt[i], c);
         p.chunks[i] = (int)ceil_div(nt[i], p.per_chunk[i]);
         items[i] = (unsigned)(x.units[i] * p.chunks[i]);

@@ -80,11 +80,13 @@ __device__ __forceinline__ void load_warp(const Q8Params& P, const Work& w, uint
         }
         return pg;
     };
+    int last = -1;   // the last load that was begun
     auto fetch = [&](int load, const CUtensorMap* map, const float* scales, int j, int pg) -> bool {
         const int s = load % C::slots;
         if (!wait_all(&bars.empty[s], ((load / C::slots) & 1) ^ 1u, abort, p.status)) return false;
         const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0);
         if (lane == 0) mbar_expect_tx(&bars.full[s], __popc(have) * box_bytes);
+        last = load;
         __syncwarp();
         if (pg >= 0) {
             const int in = (w.slot0(j, kTile) + lane * P.box) & in_page;
@@ -104,6 +106,11 @@ __device__ __forceinline__ void load_warp(const Q8Params& P, const Work& w, uint
         ok = ok && fetch(w.v_load(j), &P.tm_v, p.v_scale, j, pg);
         pg = next;
     }
+    // no copy is on its way when the warp leaves (after a wait that ran out, nobody may have waited for the last ones)
+    if (lane == 0)
+        for (int load = last < C::slots ? 0 : last - C::slots + 1; load <= last; ++load)
+            mbar_wait_bounded(&bars.full[load % C::slots], (load / C::slots) & 1, kWaitLimitNs);
+    __syncwarp();
 }
 
 // What a launch passes on: the tensor maps of the caches, read in boxes of at most `tile` keys.

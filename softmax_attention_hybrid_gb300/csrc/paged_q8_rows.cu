@@ -34,6 +34,7 @@ namespace {
 using namespace paged_q8;
 
 constexpr int kThreads = 512;
+constexpr int kMostOrdered = 256;   // sequences of a batch that are put in order
 // Register split (setmaxnreg), within the kRegsLaunch per thread that the launch hands out (checked on the host).
 constexpr int kRegsLaunch = 128, kRegsRows = 168, kRegsOther = 80;
 static_assert(kRegsRows + kRegsOther <= 2 * kRegsLaunch, "register split too large");
@@ -68,6 +69,7 @@ struct Bars {
     uint64_t s_full[2], p_ready[2], o_done[2];               // of a group
     uint64_t sc_ready[2], v_ready[2], v_free[2];             // of the tile's parity
     uint64_t pat_full[2], pat_empty[2], mma_idle[2];
+    uint64_t first;                                          // group 0 has read its first scores
 };
 
 struct Shared {
@@ -76,6 +78,10 @@ struct Shared {
     int abort_flag, imin, imax, kinds, frozen_warps, lost;
     alignas(16) float ks[2][TK];   // scales of a tile's keys
     int vexp[2];                   // V
+    int out_row[256], q_row[256];  // the rows' places in o, and in q where they are ordinary; -1: none
+    float q_scale[256];            // what a score times its key's scale is multiplied by
+    alignas(16) int length[kMostOrdered];
+    int sequence;
 };
 
 struct RowsWork : Work {
@@ -85,8 +91,12 @@ struct RowsWork : Work {
     int fz0, nf;
     bool staged;
     // floats of one staged pattern: a of the tile's keys, and r of the distances imin - (last key) ..
-    // imax - (first key), rounded up to whole 16 bytes
-    __device__ __forceinline__ int pitch() const { return (2 * TK + (imax - imin) + 3) & ~3; }
+    // imax - (first key), in whole 16-byte lines
+    __device__ __forceinline__ int pitch() const { return (2 * TK + (imax - imin) + 9) & ~3; }
+    // how far into a line the run of r begins (tiles are a multiple of a line apart)
+    __device__ __forceinline__ int shift(const PagedArgs& p, size_t h) const {
+        return (int)((((uintptr_t)(p.r + h * p.ld) >> 2) + (uintptr_t)(imin - off - (TK - 1))) & 3);
+    }
 };
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -103,46 +113,48 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t codes) {
 }
 
 // The pattern warp: a and r of the block's frozen heads for every tile. A row at position i and
-// key x need a[x] and r[i - x]; for all rows of a head and TK keys that is a run of r of
-// imax - imin + TK entries, read here in whole lines.
+// key x need a[x] and r[i - x]; for all rows of a head and TK keys that is a run of r of imax - imin + TK
+// entries, copied as whole 16-byte lines (so that an entry lies as far into a line as in r; at most three entries
+// of other rows, or behind the array's last line's end, come with it). The copies arrive on their barrier by themselves.
 template <int kD>
 __device__ __forceinline__ void pattern_warp(const Q8Params& P, const RowsWork& w, uint8_t* sm, Shared& sh) {
     using C = Cfg<kD>;
     const PagedArgs& p = P.a;
     Bars& bars = sh.bars;
-    volatile int* abort = &sh.abort_flag;
     const int lane = threadIdx.x & 31;
-    const int band = w.imax - w.imin + TK, pitch = w.pitch();
-    const uint32_t pat = smem_u32(sm + C::pat);
-    auto copy = [&](uint32_t dst, const float* src) {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-    };
+    const int pitch = w.pitch();
     const int n = w.e1 - w.e0;
-    for (int j = 0; j <= n; ++j) {
-        if (j < n) {   // tile j's copies are on their way while the rows work on tile j - 1
-            const int b = j & 1, x0 = w.slot0(j, TK);
-            if (!wait_all(&bars.pat_empty[b], ((j >> 1) & 1) ^ 1u, abort, p.status)) break;
-            for (int f = 0; f < w.nf; ++f) {
-                const size_t h = p.gheads[w.it.hk * p.G + w.fz0 + f];
-                const float* a = p.a + h * p.ld;
-                const float* r = p.r + h * p.ld;
-                const uint32_t out = pat + 4u * (uint32_t)(b * kPatFloats + f * pitch);
-                // (entries of keys past a row's own position are masked: any will do)
-#pragma unroll
-                for (int c = lane; c < TK; c += 32) copy(out + 4 * c, a + min(w.off + x0 + c, p.ld - 1));
-                const int first = w.imin - w.off - x0 - (TK - 1);
-#pragma unroll 4
-                for (int c = lane; c < band; c += 32) copy(out + 4 * (TK + c), r + min(max(first + c, 0), p.ld - 1));
+    for (int j = 0; j < n; ++j) {
+        const int b = j & 1, x0 = w.slot0(j, TK);
+        if (!wait_all(&bars.pat_empty[b], ((j >> 1) & 1) ^ 1u, &sh.abort_flag, p.status)) break;
+        float* out = reinterpret_cast<float*>(sm + C::pat) + b * kPatFloats;
+        const int r0 = w.imin - w.off - x0 - (TK - 1), r1 = w.imax - w.off - x0;   // (entries of keys past
+        const int lo = max(r0, 0), hi = min(r1, p.ld - 1);                         // a row's position are masked)
+        uint32_t bytes = 0;
+        for (int f = 0; f < w.nf; ++f) {
+            const size_t h = p.gheads[w.it.hk * p.G + w.fz0 + f];
+            const float* a = p.a + h * p.ld + w.off + x0;
+            const float* r = p.r + h * p.ld;
+            const int keys = min(TK, p.ld - w.off - x0);
+            for (int c = lane; c < keys; c += 32)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(out + f * pitch + c)), "l"(a + c) : "memory");
+            if (hi >= lo) {
+                const int first = lo - (int)(((uintptr_t)(r + lo) >> 2) & 3), count = (hi - first + 4) & ~3;
+                if (lane == 0)
+                    bulk_load(out + f * pitch + TK + w.shift(p, h) + first - r0, r + first, 4u * (uint32_t)count,
+                              &bars.pat_full[b]);
+                bytes += 4u * (uint32_t)count;
             }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (j > 0) {
-            asm volatile("cp.async.wait_group 1;" ::: "memory");   // tile j - 1's
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.pat_full[(j - 1) & 1]);
-        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars.pat_full[b])) : "memory");
+        if (lane == 0) mbar_expect_tx(&bars.pat_full[b], bytes);
+        __syncwarp();
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // no copy is on its way when the warp leaves
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (lane == 0)
+        for (int j = n < 2 ? 0 : n - 2; j < n; ++j) mbar_wait_bounded(&bars.pat_full[j & 1], (j >> 1) & 1, kWaitLimitNs);
+    __syncwarp();
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -255,8 +267,8 @@ __device__ __forceinline__ uint32_t below(int end, int first) {
 
 // Warps 0-7 of a group that has rows: thread = row.
 template <int kD>
-__device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, const PagedRow& row, float qscale,
-                                          uint8_t* sm, Shared& sh) {
+__device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, const PagedRow& row, uint8_t* sm,
+                                          Shared& sh) {
     using C = Cfg<kD>;
     const PagedArgs& p = P.a;
     Bars& bars = sh.bars;
@@ -265,13 +277,13 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
     const uint32_t tmem = sh.tmem_base + g * C::group + ((uint32_t)(warp * 32) << 16);
     const int i = row.i < 0 ? -1 : row.i - w.off;   // my last visible slot of the part
     const bool frozen = row.frozen && i >= 0;
-    const float sc = row.frozen ? kLog2e : qscale;
+    const float sc = row.frozen ? kLog2e : sh.q_scale[t];
     const bool any_frozen = __any_sync(0xffffffffu, frozen), any_scaled = __any_sync(0xffffffffu, i >= 0 && !row.frozen);
     const float* ra = p.a + (size_t)row.h * p.ld + w.off;
     const float* rr = p.r + (size_t)row.h * p.ld;
     // my staged pattern: a of the tile's keys, and r from the far end on (entry k - c for key c)
     const float* pat_a = reinterpret_cast<const float*>(sm + C::pat) + (frozen ? row.gi - w.fz0 : 0) * w.pitch();
-    const float* pat_r = pat_a + TK + (TK - 1) + (frozen ? row.i - w.imin : 0);
+    const float* pat_r = pat_a + TK + (TK - 1) + (frozen ? row.i - w.imin + w.shift(p, row.h) : 0);
     float m = -INFINITY, l = 0.f;   // (l: times 2^kWeightExp)
     int vexp = kNoExp;
     bool ok = true;
@@ -371,6 +383,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
             need = true;
         }
         tmem_st_wait();
+        if (n == 0 && t == 0) mbar_arrive(&bars.first);
         if (n > 0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll 1
             for (int q = 0; q < kD; q += 32) {
@@ -411,32 +424,40 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
     // my row
     l *= pow2i(-kWeightExp);
     const bool sees = row.i >= 0 && l != 0.f;   // (a NaN sum is one)
-    const size_t at = paged_out_row(p, row);
     const int split = w.it.part ? p.chunks[0] + w.it.chunk : w.it.chunk;
     const float back = vexp == kNoExp ? 0.f : pow2i(vexp - 2 * kWeightExp);
     const float mul = p.nsplit > 1 ? back : back * (1.f / l);
+    // 32 columns of the warp's rows at a time through its part of the group's q, which is no longer read, so that
+    // whole lines are written: 8 lanes to a row
+    float* stage = reinterpret_cast<float*>(sm + C::q + (t >> 5) * 8192);
+    const int sub = lane >> 3, c4 = lane & 7;
 #pragma unroll 1
-    for (int q = 0; q < kD; q += 32) {
+    for (int q = 0; q < p.d; q += 32) {
         uint32_t ov[32];
         tmem_ld32(tmem + C::col_o + q, ov);
         tmem_ld_wait();
-        if (!row.there || q >= p.d) continue;
-        float y[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) y[c] = sees ? __uint_as_float(ov[c]) * mul : 0.f;
-        if (p.nsplit > 1) {
-            float4* out = reinterpret_cast<float4*>(p.po + (at * p.nsplit + split) * p.d + q);
+        for (int c = 0; c < 8; ++c)   // (16-byte chunks, turned by the row)
+            *reinterpret_cast<float4*>(stage + lane * 32 + 4 * (c ^ (lane & 7))) =
+                sees ? make_float4(__uint_as_float(ov[4 * c]) * mul, __uint_as_float(ov[4 * c + 1]) * mul,
+                                   __uint_as_float(ov[4 * c + 2]) * mul, __uint_as_float(ov[4 * c + 3]) * mul)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        __syncwarp();
 #pragma unroll
-            for (int c = 0; c < 8; ++c) out[c] = make_float4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
-        } else {
-            uint4* out = reinterpret_cast<uint4*>((__nv_bfloat16*)p.o + at * p.d + q);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                out[c] = make_uint4(pack_bf16(y[8 * c], y[8 * c + 1]), pack_bf16(y[8 * c + 2], y[8 * c + 3]),
-                                    pack_bf16(y[8 * c + 4], y[8 * c + 5]), pack_bf16(y[8 * c + 6], y[8 * c + 7]));
+        for (int k = 0; k < 32; k += 4) {
+            const int at = sh.out_row[(t & ~31) + k + sub];
+            const float4 y = *reinterpret_cast<const float4*>(stage + (k + sub) * 32 + 4 * (c4 ^ ((k + sub) & 7)));
+            if (at < 0) continue;
+            if (p.nsplit > 1)
+                *reinterpret_cast<float4*>(p.po + ((size_t)at * p.nsplit + split) * p.d + q + 4 * c4) = y;
+            else
+                *reinterpret_cast<uint2*>((__nv_bfloat16*)p.o + (size_t)at * p.d + q + 4 * c4) =
+                    make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
         }
+        __syncwarp();
     }
     if (!row.there) return;
+    const size_t at = (size_t)sh.out_row[t];
     if (p.nsplit > 1) p.ml[at * p.nsplit + split] = sees ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
     else p.lse[at] = sees ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
@@ -453,21 +474,24 @@ __device__ __forceinline__ void issue_warp(const Q8Params& P, const RowsWork& w,
     const uint64_t d_ring = sdesc_sw128(smem_u32(sm + C::ring), 16, 1024);
     const uint64_t d_v16 = sdesc_sw128(smem_u32(sm + C::v16), C::v16_atom, 1024);      // MN-major
     const uint32_t tmem = sh.tmem_base + g * C::group;
-    const int n = w.e1 - w.e0, steps = p.d / 32;
+    const int n = w.e1 - w.e0;
     auto scores = [&](int j) -> bool {
         const int ld = w.k_load(j), s = ld % C::slots;
         if (!wait_all(&bars.full[s], (ld / C::slots) & 1, abort, p.status)) return false;
         if (j > 0 && !wait_all(&bars.o_done[g], (j - 1) & 1, abort, p.status)) return false;
         tc_fence_after();
         const uint64_t d_k = sdesc_advance(d_ring, s * TK * 128);
-        for (int term = 0; term < 2; ++term)   // hi, then lo
-            for (int k = 0; k < steps; ++k)
-                mma_ss_e4m3_warp(tmem, sdesc_advance(d_q, term * 16384 + 32 * k), sdesc_advance(d_k, 32 * k), id_s,
-                                 term + k > 0);
+#pragma unroll
+        for (int k = 0; k < kD / 16; ++k) {   // hi, then lo
+            const int term = k / (kD / 32), at = k % (kD / 32);
+            mma_ss_e4m3_warp(tmem, sdesc_advance(d_q, term * 16384 + 32 * at), sdesc_advance(d_k, 32 * at), id_s, k > 0);
+        }
         mma_commit_warp(&bars.s_full[g]);
         mma_commit_warp(&bars.empty[s]);
         return true;
     };
+    // The second group begins half a tile later: in step, both would wait for their MMAs at the same time.
+    if (g == 1) wait_all(&bars.first, 0, abort, p.status);
     bool ok = !w.any_ord || scores(0);
     for (int j = 0; j < n && ok; ++j) {
         if (!wait_all(&bars.v_ready[j & 1], (j >> 1) & 1, abort, p.status)) break;
@@ -494,57 +518,86 @@ __device__ __forceinline__ void set_up_done() {
     tc_fence_after();
 }
 
-// q's terms, one row per thread (zeros for frozen rows and those without a token); the row's scale.
-template <int kD>
-__device__ __forceinline__ float put_q(const Q8Params& P, const PagedRow& row, uint8_t* sm) {
-    using C = Cfg<kD>;
-    const PagedArgs& p = P.a;
-    const int t = threadIdx.x;
-    const bool have = row.i >= 0 && !row.frozen;
-    const uint4* src = reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.q + paged_out_row(p, row) * p.d);
-    uint4 x[kD / 8];
-#pragma unroll
-    for (int c = 0; c < kD / 8; ++c) x[c] = have && 8 * c < p.d ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-    // the row's largest magnitude as bits: above 0x7f7f it holds an infinity or a NaN
-    uint32_t top = 0;
-#pragma unroll
-    for (int c = 0; c < kD / 8; ++c) {
-        const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top = __vmaxu2(top, v[k] & 0x7fff7fffu);
+// Rows of q: 16 lanes of 8 elements to a row, a warp's 32 rows in four batches, of which the first is on its way
+// before anything about the sequences is known.
+struct RowsOfQ {
+    uint4 x[4];
+    __device__ __forceinline__ static int row(int batch, int k) {
+        return 32 * (int)(threadIdx.x >> 5) + 8 * batch + 2 * k + (int)((threadIdx.x >> 4) & 1);
     }
-    top = max(top & 0xffffu, top >> 16);
-    const bool bad = top >= 0x7f80u;
-    // 448 = 1.75 x 2^8
-    int e = 8 - ((int)(top >> 7) - 127) - ((top & 0x7fu) > 0x60u);
-    e = bad ? 0 : e < -120 ? -120 : e > 120 ? 120 : e;
-    const float f = pow2i(e);
-    uint8_t* hi = sm + C::q + (t >> 7) * 2 * 128 * 128;
-    uint8_t* lo = hi + 128 * 128;
-#pragma unroll
-    for (int c = 0; c < kD / 16; ++c) {
-        const uint32_t v[8] = {x[2 * c].x, x[2 * c].y, x[2 * c].z, x[2 * c].w,
-                               x[2 * c + 1].x, x[2 * c + 1].y, x[2 * c + 1].z, x[2 * c + 1].w};
-        uint32_t h[4], r[4];
+    __device__ __forceinline__ void get(const PagedArgs& p, const Shared& sh, int batch) {
+        const int c = threadIdx.x & 15;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            uint32_t hp[2], rp[2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const float y0 = __uint_as_float(v[2 * k + b] << 16) * f, y1 = __uint_as_float(v[2 * k + b] & 0xffff0000u) * f;
-                hp[b] = pack_e4m3(y0, y1);
-                const float2 z = unpack_e4m3(hp[b]);
-                rp[b] = pack_e4m3(y0 - z.x, y1 - z.y);
-            }
-            h[k] = hp[0] | hp[1] << 16;
-            r[k] = rp[0] | rp[1] << 16;
-            if (bad) h[k] = r[k] = 0x7f7f7f7fu;   // (saturation would hide an infinity)
+            const int at = sh.q_row[row(batch, k)];
+            x[k] = at >= 0 && 8 * c < p.d
+                       ? __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)p.q + (size_t)at * p.d) + c)
+                       : make_uint4(0, 0, 0, 0);
         }
-        *reinterpret_cast<uint4*>(hi + sw128_offset(t & 127, 16 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(lo + sw128_offset(t & 127, 16 * c)) = make_uint4(r[0], r[1], r[2], r[3]);
     }
-    fence_proxy_async_smem();
-    return p.scale_log2 * pow2i(-e);
+    // the rows' terms and factors
+    template <typename C, int kCols>
+    __device__ __forceinline__ void put(const PagedArgs& p, uint8_t* sm, Shared& sh, int batch) const {
+        const int c = threadIdx.x & 15;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            // the row's largest magnitude as bits: above 0x7f7f it holds an infinity or a NaN
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = __vmaxu2(top, v[e] & 0x7fff7fffu);
+#pragma unroll
+            for (int o = 8; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+            top = max(top & 0xffffu, top >> 16);
+            const bool bad = top >= 0x7f80u;
+            // 448 = 1.75 x 2^8
+            int e = 8 - ((int)(top >> 7) - 127) - ((top & 0x7fu) > 0x60u);
+            e = bad ? 0 : e < -120 ? -120 : e > 120 ? 120 : e;
+            const float f = pow2i(e);
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const float y0 = __uint_as_float(v[b] << 16) * f, y1 = __uint_as_float(v[b] & 0xffff0000u) * f;
+                h[b] = pack_e4m3(y0, y1);
+                const float2 z = unpack_e4m3(h[b]);
+                l[b] = pack_e4m3(y0 - z.x, y1 - z.y);
+            }
+            uint2 hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16), lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+            if (bad) hi = lo = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);   // (saturation would hide an infinity)
+            const int r = row(batch, k);
+            uint8_t* q = sm + C::q + (r >> 7) * 2 * 16384;
+            if (8 * c < kCols) {   // (zeros behind the row's end, as TMA leaves behind K's)
+                *reinterpret_cast<uint2*>(q + sw128_offset(r & 127, 8 * c)) = hi;
+                *reinterpret_cast<uint2*>(q + 16384 + sw128_offset(r & 127, 8 * c)) = lo;
+            }
+            if (c == 0) sh.q_scale[r] = p.scale_log2 * pow2i(-e);
+        }
+    }
+};
+
+// Items are as long as their sequences, a few to an SM: the longest sequences begin, so that the last items to
+// run are the shortest. (512 tokens of four prompts, one item to a block of rows: 342 us in the batch's order.)
+__device__ __forceinline__ void longest_first(const PagedArgs& p, PagedItem* it, Shared& sh) {
+    const int t = threadIdx.x;
+    if (t < kMostOrdered) {
+        int c = 0, n = 0;
+        bool bad;
+        if (t < p.B) n = paged_tokens(p, t, &c, &bad);
+        sh.length[t] = t >= p.B ? -1 : n > 0 ? c + n : 0;
+    }
+    __syncthreads();
+    if (t < p.B) {
+        const int mine = sh.length[t];
+        int before = 0;   // sequences that begin earlier
+        for (int u = 0; u < p.B; u += 4) {
+            const int4 x = *reinterpret_cast<const int4*>(&sh.length[u]);
+            before += (x.x > mine || (x.x == mine && u < t)) + (x.y > mine || (x.y == mine && u + 1 < t)) +
+                      (x.z > mine || (x.z == mine && u + 2 < t)) + (x.w > mine || (x.w == mine && u + 3 < t));
+        }
+        if (before == it->b) sh.sequence = t;
+    }
+    __syncthreads();
+    it->b = sh.sequence;
 }
 
 template <int kD>
@@ -568,6 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q8_rows_kernel(const __grid
             sh.imax = -1;
             sh.kinds = sh.frozen_warps = sh.lost = 0;
         }
+        if (lane == 31) mbar_init(&bars.first, 1);
         if (lane < C::slots) {
             mbar_init(&bars.full[lane], 1);
             mbar_init(&bars.empty[lane], 4 + w.groups);   // K: the groups' MMAs and the four warps that read its scales
@@ -579,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q8_rows_kernel(const __grid
             mbar_init(&bars.sc_ready[i], 1);
             mbar_init(&bars.v_ready[i], 4);
             mbar_init(&bars.v_free[i], w.groups);
-            mbar_init(&bars.pat_full[i], 1);
+            mbar_init(&bars.pat_full[i], 33);   // the pattern warp's lanes, and its count of bytes
             mbar_init(&bars.mma_idle[i], 1);
         }
         fence_mbar_init();
@@ -587,9 +641,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q8_rows_kernel(const __grid
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
+    if (w.it.part && p.B > 1 && p.B <= kMostOrdered) longest_first(p, &w.it, sh);
     PagedRow row;
     if (t < 256) {
-        row = paged_row(p, w.it, block, t);
+        row = paged_place(p, w.it, block, t);
+        sh.out_row[t] = row.there ? (int)paged_out_row(p, row) : -1;
+        sh.q_row[t] = row.there && !row.frozen ? sh.out_row[t] : -1;
+    }
+    __syncthreads();
+    RowsOfQ q;
+    if (t < 256) {
+        if (p.q) q.get(p, sh, 0);
+        if (row.there) {
+            int c;
+            bool bad;
+            const int n = paged_tokens(p, row.b, &c, &bad);
+            if (row.t < n) row.i = p.P + c + row.t;
+        }
         int lo = row.i >= 0 ? row.i : 0x7fffffff, hi = row.i;
         const int kinds = row.i < 0 ? 0 : row.frozen ? 2 : 1;
         lo = __reduce_min_sync(0xffffffffu, lo);
@@ -619,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q8_rows_kernel(const __grid
     if (w.e0 >= w.e1) {   // no keys: nothing but the rows' empty sums
         if (t < 256 && row.there) {
             const int split = w.it.part ? p.chunks[0] + w.it.chunk : w.it.chunk;
-            const size_t at = paged_out_row(p, row);
+            const size_t at = (size_t)sh.out_row[t];
             if (p.nsplit > 1) {
                 p.ml[at * p.nsplit + split] = make_float2(-INFINITY, 0.f);
             } else {
@@ -632,20 +700,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q8_rows_kernel(const __grid
     // the block's frozen heads: of its members of the group those from gord on
     w.fz0 = max(block.first / block.per_head, (int)p.gord[w.it.hk]);
     w.nf = (block.first + w.there - 1) / block.per_head - w.fz0 + 1;
-    w.staged = (long long)w.nf * ((long long)w.imax - w.imin + 2 * TK + 3) <= kPatFloats;
+    w.staged = (long long)w.nf * ((long long)w.imax - w.imin + 2 * TK + 9) <= kPatFloats;
 
     // one setmaxnreg for each warpgroup
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
-        float qscale = 0.f;
-        if (w.any_ord && (t >> 7) < w.groups) qscale = put_q<kD>(P, row, sm);
+        if (w.any_ord) {
+            RowsOfQ next;
+#pragma unroll 1
+            for (int batch = 0; batch < 4; batch += 2) {
+                next.get(p, sh, batch + 1);
+                q.put<C, kD>(p, sm, sh, batch);
+                if (batch == 0) q.get(p, sh, 2);
+                next.put<C, kD>(p, sm, sh, batch + 1);
+            }
+            fence_proxy_async_smem();
+        }
         if (t == 0 && sh.frozen_warps > 0) {
             mbar_init(&bars.pat_empty[0], sh.frozen_warps);
             mbar_init(&bars.pat_empty[1], sh.frozen_warps);
             fence_mbar_init();
         }
         set_up_done();
-        if ((t >> 7) < w.groups) row_warps<kD>(P, w, row, qscale, sm, sh);
+        if ((t >> 7) < w.groups) row_warps<kD>(P, w, row, sm, sh);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         set_up_done();

@@ -1,7 +1,7 @@
 // Paged attention over 8-bit caches on the tensor cores (bf16 q and o; see paged.h for the split).
 //
 // Few rows meet many keys in a decoding step, so the keys take the M = 128 lanes of the MMAs
-// and the rows (R = 4, 8, 16 or 32 of a block) the columns:
+// and the rows (R = 4, 8, 16, 24 or 32 of a block) the columns:
 //     S^T [128 keys, rows] = K q^T,      O^T [d, rows] += V^T P^T,
 // with K and V as they lie in the cache: codes of e4m3 (kind::f8f6f4), never unpacked. A thread of
 // the softmax holds one key of the tile, with that key's two scales, for all rows.
@@ -45,6 +45,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 4.0f;            // scores may pass the maximum by this much (base 2)
 // A row that has seen no key yet: below every finite score (those of patterns are at least -2.3e38 log2(e)).
 constexpr float kNoMax = -3.4e38f;
+constexpr int kStaged = 8;                // frozen rows whose patterns wait in shared memory
 constexpr float kWeight = 16.0f;          // 2^(8 - kSlack): a weight of the maximum, before the value's scale
 
 template <int R>
@@ -60,7 +61,11 @@ struct Cfg {
     static constexpr int p = q + ns * 128;
     static constexpr int p_bytes = blocks * kTile * 16;
     static constexpr int scales = p + 2 * p_bytes;
-    static constexpr int total = scales + slots * kScaleBytes;
+    // the patterns' entries of the next tile's keys, of the first kStaged frozen rows: a thread's own [row, a or r, key]
+    static constexpr bool staged = R > 8;
+    static constexpr int pat = scales + slots * kScaleBytes;
+    static constexpr int total = pat + (staged ? kStaged * 2 * kTile * 4 : 0);
+    static_assert(total + 1024 + 3072 <= (ctas == 3 ? 76 : 114) * 1024, "CTAs of an SM");
     static constexpr uint32_t col_o = 2 * ns;         // S of two tiles, then O
     static constexpr uint32_t cols = R <= 8 ? 64 : R == 16 ? 128 : 256;
     static_assert(col_o + np <= cols, "tensor memory");
@@ -98,6 +103,9 @@ __device__ __forceinline__ bool rows_any(bool x) {
         : "r"((uint32_t)x)
         : "memory");
     return y != 0;
+}
+__device__ __forceinline__ void copy4(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void rows_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
@@ -176,6 +184,7 @@ __device__ __forceinline__ void read_s(uint32_t addr, float* s) {   // hi + lo /
     if constexpr (R == 4) tmem_ld8(addr, x);
     else if constexpr (R == 8) tmem_ld16(addr, x);
     else tmem_ld32(addr, x);
+    if constexpr (R == 24) tmem_ld16(addr + 32, x + 32);
     if constexpr (R == 32) tmem_ld32(addr + 32, x + 32);
     tmem_ld_wait();
 #pragma unroll
@@ -200,9 +209,11 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
     int vexp = 0;
     bool ok = true;
 
-    // the fixed patterns' entries (Eq. 3) of my key: neighbouring keys, neighbouring entries. Few rows: a tile ahead.
-    constexpr bool kAhead = R <= 8;
+    // The fixed patterns' entries (Eq. 3) of my key, a tile ahead: neighbouring keys, neighbouring entries. Few rows keep
+    // them in registers, more in shared memory.
+    constexpr bool kAhead = !C::staged;
     float fa[kAhead ? R : 1], fr[kAhead ? R : 1];
+    float* staged = reinterpret_cast<float*>(sm + C::pat) + t;
     auto ahead = [&](int j) {
         const int x = w.slot0(j, kTile) + t;
         if constexpr (kAhead) {
@@ -213,6 +224,15 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
                     fa[r] = __ldg(sh.a[r] + y);
                     fr[r] = __ldg(sh.r[r] - y);
                 }
+        } else {
+            const int n = min(there - f0, kStaged);
+#pragma unroll 2
+            for (int k = 0; k < n; ++k) {
+                const int y = max(min(x, sh.pos[f0 + k]), 0);
+                copy4(staged + (2 * k) * kTile, sh.a[f0 + k] + y);
+                copy4(staged + (2 * k + 1) * kTile, sh.r[f0 + k] - y);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         }
     };
     if (f0 < there) ahead(0);
@@ -259,20 +279,22 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
                 for (int r = 0; r < R; ++r)
                     if (r >= f0 && r < there) s[r] = (fa[r] + fr[r]) * kLog2e;
                 if (n + 1 < tiles) ahead(n + 1);
-            } else {   // four rows' loads at a time
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
-                for (int r = 0; r < R; r += 4)
-                    if (r + 4 > f0 && r < there) {
-                        float y[4];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int z = max(min(x, sh.pos[r + c]), 0);
-                            y[c] = __ldg(sh.a[r + c] + z) + __ldg(sh.r[r + c] - z);
+                for (int r = 0; r < R; ++r)
+                    if (r >= f0 && r < there) {
+                        const int k = r - f0;
+                        float y;
+                        if (k < kStaged) {
+                            y = staged[(2 * k) * kTile] + staged[(2 * k + 1) * kTile];
+                        } else {
+                            const int z = max(min(x, sh.pos[r]), 0);
+                            y = __ldg(sh.a[r] + z) + __ldg(sh.r[r] - z);
                         }
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (r + c >= f0) s[r + c] = y[c] * kLog2e;
+                        s[r] = y * kLog2e;
                     }
+                if (n + 1 < tiles) ahead(n + 1);
             }
         }
         const int ldv = w.v_load(n), vslot = ldv % C::slots;
@@ -392,6 +414,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
             mbar_arrive(&bars.empty[vslot]);
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");   // (none is on its way, unless a wait ran out)
     // (a lane whose wait ran out has left with all the others, or does so below)
     if (n > 0) ok = mbar_wait(&bars.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
     __syncwarp();
@@ -527,8 +550,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::ctas) paged_q8_kernel(const 
                 if (j > 1 && !wait_all(&bars.s_empty[j & 1], ((j - 2) >> 1) & 1, abort, p.status)) break;
                 tc_fence_after();
                 const uint64_t d_k = sdesc_advance(d_ring, s * kTileBytes);
-                for (int k = 0; k < steps; ++k)
-                    mma_ss_e4m3_warp(tmem + (j & 1) * C::ns, sdesc_advance(d_k, 32 * k), sdesc_advance(d_q, 32 * k),
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < steps)
+                        mma_ss_e4m3_warp(tmem + (j & 1) * C::ns, sdesc_advance(d_k, 32 * k), sdesc_advance(d_q, 32 * k),
                                      id_s, k > 0);
                 mma_commit_warp(&bars.s_full[j & 1]);
                 mma_commit_warp(&bars.empty[s]);
@@ -585,6 +610,7 @@ cudaError_t launch_paged_q8(const PagedArgs& a, int rows, unsigned items, cudaSt
         case 4: return launch_r<4>(P, items, s);
         case 8: return launch_r<8>(P, items, s);
         case 16: return launch_r<16>(P, items, s);
+        case 24: return launch_r<24>(P, items, s);
         default: return launch_r<32>(P, items, s);
     }
 }
