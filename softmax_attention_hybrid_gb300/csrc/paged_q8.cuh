@@ -21,7 +21,7 @@ struct Work {
     int imin, imax;   // positions of the rows that see anything
     int off;          // position of the part's slot 0
     int there;        // rows of the block that are rows of the output
-    int f0;           // rows f0 and up are those of frozen heads
+    int nf;           // rows of frozen heads: the block's last ones
     bool any_ord;     // an ordinary row is among them: K is loaded
 
     __device__ __forceinline__ int slot0(int j, int tile) const {   // first slot of the j-th tile, the newest first

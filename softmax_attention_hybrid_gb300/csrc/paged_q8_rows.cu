@@ -86,9 +86,9 @@ struct Shared {
 
 struct RowsWork : Work {
     int groups;       // 1 or 2
-    // the frozen heads of the block: group members fz0 .. fz0 + nf - 1, whose patterns the tile's
+    // the frozen heads of the block: group members fz0 .. fz0 + heads - 1, whose patterns the tile's
     // threads read from shared memory (staged) or from a and r themselves
-    int fz0, nf;
+    int fz0, heads;
     bool staged;
     // floats of one staged pattern: a of the tile's keys, and r of the distances imin - (last key) ..
     // imax - (first key), in whole 16-byte lines
@@ -131,7 +131,7 @@ __device__ __forceinline__ void pattern_warp(const Q8Params& P, const RowsWork& 
         const int r0 = w.imin - w.off - x0 - (TK - 1), r1 = w.imax - w.off - x0;   // (entries of keys past
         const int lo = max(r0, 0), hi = min(r1, p.ld - 1);                         // a row's position are masked)
         uint32_t bytes = 0;
-        for (int f = 0; f < w.nf; ++f) {
+        for (int f = 0; f < w.heads; ++f) {
             const size_t h = p.gheads[w.it.hk * p.G + w.fz0 + f];
             const float* a = p.a + h * p.ld + w.off + x0;
             const float* r = p.r + h * p.ld;
@@ -699,8 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_q8_rows_kernel(const __grid
     }
     // the block's frozen heads: of its members of the group those from gord on
     w.fz0 = max(block.first / block.per_head, (int)p.gord[w.it.hk]);
-    w.nf = (block.first + w.there - 1) / block.per_head - w.fz0 + 1;
-    w.staged = (long long)w.nf * ((long long)w.imax - w.imin + 2 * TK + 9) <= kPatFloats;
+    w.heads = (block.first + w.there - 1) / block.per_head - w.fz0 + 1;
+    w.staged = (long long)w.heads * ((long long)w.imax - w.imin + 2 * TK + 9) <= kPatFloats;
 
     // one setmaxnreg for each warpgroup
     if (warp < 8) {

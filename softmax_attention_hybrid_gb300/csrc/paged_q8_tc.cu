@@ -21,13 +21,17 @@
 // they are found anew, and O and l are scaled. Tiles are walked from the newest key to the oldest: the
 // patterns of frozen heads, and most ordinary rows, look nearby first, so that the maximum is found early.
 //
-// Warps (224 threads, two CTAs per SM): 0-3 softmax, 4 loads K, V and their scales (each of its lanes
-// fetches one page of the tile), 5 owns tensor memory and issues S, 6 issues P V.
+// Warps (256 threads, two CTAs per SM, three with 4 rows): 0-3 softmax, 4 loads K, V and their scales (each of its lanes
+// fetches one page of the tile), 5 owns tensor memory and issues S, 6 issues P V. (7 completes the second
+// warpgroup: from 16 rows on the softmax takes registers over from it, since what it spills costs the latency
+// of the L2 each time in the little L1 that is left.)
 // Shared memory: q's terms (K-major, 128-byte swizzle), P's terms of two tiles (MN-major: the 16 bytes of
 // a key's columns next to each other), and a ring of tiles of 128 keys with their scales, filled in the order in
 // which the MMAs use them: K0, K1, V0, K2, V1, ... (V0, V1, ... where no row is ordinary). Rows of d < 128
 // codes are filled up with zeros by TMA.
 #include <string.h>
+
+#include <atomic>
 
 #include "paged_q8.cuh"
 
@@ -36,7 +40,10 @@ namespace {
 
 using namespace paged_q8;
 
-constexpr int kThreads = 224;
+constexpr int kThreads = 256;
+// Register split (setmaxnreg) from 16 rows on, within the kRegsLaunch per thread that the launch hands out (checked on the host).
+constexpr int kRegsLaunch = 128, kRegsRows = 184, kRegsOther = 72;
+static_assert(kRegsRows + kRegsOther <= 2 * kRegsLaunch, "register split too large");
 constexpr int kTile = kQ8Tile;            // keys of a tile
 constexpr int kTileBytes = kTile * 128;
 constexpr int kScaleBytes = kTile * 4;
@@ -45,7 +52,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 4.0f;            // scores may pass the maximum by this much (base 2)
 // A row that has seen no key yet: below every finite score (those of patterns are at least -2.3e38 log2(e)).
 constexpr float kNoMax = -3.4e38f;
-constexpr int kStaged = 8;                // frozen rows whose patterns wait in shared memory
+constexpr int kAhead = 8;                 // frozen rows whose patterns are loaded a tile ahead
 constexpr float kWeight = 16.0f;          // 2^(8 - kSlack): a weight of the maximum, before the value's scale
 
 template <int R>
@@ -61,10 +68,8 @@ struct Cfg {
     static constexpr int p = q + ns * 128;
     static constexpr int p_bytes = blocks * kTile * 16;
     static constexpr int scales = p + 2 * p_bytes;
-    // the patterns' entries of the next tile's keys, of the first kStaged frozen rows: a thread's own [row, a or r, key]
-    static constexpr bool staged = R > 8;
-    static constexpr int pat = scales + slots * kScaleBytes;
-    static constexpr int total = pat + (staged ? kStaged * 2 * kTile * 4 : 0);
+    static constexpr bool split = R > 8;
+    static constexpr int total = scales + slots * kScaleBytes;
     static_assert(total + 1024 + 3072 <= (ctas == 3 ? 76 : 114) * 1024, "CTAs of an SM");
     static constexpr uint32_t col_o = 2 * ns;         // S of two tiles, then O
     static constexpr uint32_t cols = R <= 8 ? 64 : R == 16 ? 128 : 256;
@@ -83,7 +88,7 @@ struct Shared {
     uint32_t tmem_base;
     int abort_flag;
     int lost;                      // a page that the item needs is not in the cache (set before its tile is there)
-    // rows of the block
+    // rows of the block: ordinary ones from the front, frozen ones from the back
     alignas(16) float scale[32];   // what a score times its key's scale is multiplied by: log2(e) / sqrt(d), and q's factor back
     alignas(16) float m[32];       // running maxima
     alignas(16) float fall[32];    // 2^(old maximum - new one)
@@ -104,9 +109,6 @@ __device__ __forceinline__ bool rows_any(bool x) {
         : "memory");
     return y != 0;
 }
-__device__ __forceinline__ void copy4(float* dst, const float* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
 __device__ __forceinline__ void rows_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
 // Largest of a warp's values (NaN left out), by integers that have the order of the floats.
@@ -126,7 +128,7 @@ __device__ __forceinline__ void get_q(const Q8Params& P, const Work& w, int plac
     for (int k = 0; k < R / 4; ++k) {
         const int r = 4 * k + warp, at = __shfl_sync(0xffffffffu, place, r);
         x[k] = make_uint2(0, 0);
-        if (r < w.there && r < w.f0 && 4 * lane < p.d)
+        if (r < w.there - w.nf && 4 * lane < p.d)
             x[k] = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)p.q + (size_t)at * p.d) + lane);
     }
 }
@@ -140,7 +142,7 @@ __device__ __forceinline__ void put_q(const Q8Params& P, const Work& w, uint8_t*
 #pragma unroll
     for (int k = 0; k < R / 4; ++k) {
         const int r = 4 * k + warp;
-        if (r >= w.there || r >= w.f0 || sh.pos[r] < 0) continue;   // (uniform)
+        if (r >= w.there - w.nf || sh.pos[r] < 0) continue;   // (uniform)
         const uint2 x = q[k];
         const float v[4] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
                             __uint_as_float(x.y & 0xffff0000u)};
@@ -200,7 +202,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
     Bars& bars = sh.bars;
     volatile int* abort = &sh.abort_flag;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const int there = w.there, f0 = w.f0, tiles = w.e1 - w.e0;
+    const int nf = w.nf, tiles = w.e1 - w.e0;
     const int my_box = t / P.box * P.box;
     float l[R];
 #pragma unroll
@@ -209,33 +211,26 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
     int vexp = 0;
     bool ok = true;
 
-    // The fixed patterns' entries (Eq. 3) of my key, a tile ahead: neighbouring keys, neighbouring entries. Few rows keep
-    // them in registers, more in shared memory.
-    constexpr bool kAhead = !C::staged;
-    float fa[kAhead ? R : 1], fr[kAhead ? R : 1];
-    float* staged = reinterpret_cast<float*>(sm + C::pat) + t;
+    // The fixed patterns' entries (Eq. 3) of my key, a tile ahead: neighbouring keys, neighbouring entries. Frozen
+    // rows stand at the end, the first of them last, so that registers hold them; four at a time, for a branch for each
+    // row costs as much as its entries (keys past the row's own position are masked below, and what is loaded for
+    // a place without a frozen row is not used).
+    constexpr int kA = R < kAhead ? R : kAhead;
+    float fa[kA], fr[kA];
     auto ahead = [&](int j) {
         const int x = w.slot0(j, kTile) + t;
-        if constexpr (kAhead) {
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r >= f0 && r < there) {
-                    const int y = max(min(x, sh.pos[r]), 0);   // (keys past the row's own position are masked below)
-                    fa[r] = __ldg(sh.a[r] + y);
-                    fr[r] = __ldg(sh.r[r] - y);
+        for (int k0 = 0; k0 < kA; k0 += 4)
+            if (k0 < nf) {
+#pragma unroll
+                for (int k = k0; k < k0 + 4; ++k) {
+                    const int y = max(min(x, sh.pos[R - 1 - k]), 0);
+                    fa[k] = __ldg(sh.a[R - 1 - k] + y);
+                    fr[k] = __ldg(sh.r[R - 1 - k] - y);
                 }
-        } else {
-            const int n = min(there - f0, kStaged);
-#pragma unroll 2
-            for (int k = 0; k < n; ++k) {
-                const int y = max(min(x, sh.pos[f0 + k]), 0);
-                copy4(staged + (2 * k) * kTile, sh.a[f0 + k] + y);
-                copy4(staged + (2 * k + 1) * kTile, sh.r[f0 + k] - y);
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        }
     };
-    if (f0 < there) ahead(0);
+    if (nf > 0) ahead(0);
     if (w.any_ord) {
         put_q<R>(P, w, sm, sh, q);
         fence_proxy_async_smem();
@@ -273,29 +268,24 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
 #pragma unroll
             for (int r = 0; r < R; ++r) s[r] = -INFINITY;
         }
-        if (f0 < there) {
-            if constexpr (kAhead) {
+        if (nf > 0) {
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (r >= f0 && r < there) s[r] = (fa[r] + fr[r]) * kLog2e;
-                if (n + 1 < tiles) ahead(n + 1);
-            } else {
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            for (int k0 = 0; k0 < R; k0 += 4)
+                if (k0 < nf) {
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (r >= f0 && r < there) {
-                        const int k = r - f0;
+                    for (int k = k0; k < k0 + 4; ++k) {
+                        const int r = R - 1 - k;
                         float y;
-                        if (k < kStaged) {
-                            y = staged[(2 * k) * kTile] + staged[(2 * k + 1) * kTile];
+                        if (k < kA) {
+                            y = fa[k < kA ? k : 0] + fr[k < kA ? k : 0];
                         } else {
                             const int z = max(min(x, sh.pos[r]), 0);
                             y = __ldg(sh.a[r] + z) + __ldg(sh.r[r] - z);
                         }
-                        s[r] = y * kLog2e;
+                        s[r] = k < nf ? y * kLog2e : s[r];
                     }
-                if (n + 1 < tiles) ahead(n + 1);
-            }
+                }
+            if (n + 1 < tiles) ahead(n + 1);
         }
         const int ldv = w.v_load(n), vslot = ldv % C::slots;
         ok = mbar_wait(&bars.full[vslot], (ldv / C::slots) & 1, abort, p.status, kStatusTimeout) && ok;
@@ -310,7 +300,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int i = sh.pos[r];
-                const int lo = r >= f0 || p.window == 0 ? -1 : i - p.window;   // slots <= lo: sinks only
+                const int lo = r >= R - nf || p.window == 0 ? -1 : i - p.window;   // slots <= lo: sinks only
                 if (!(any && x <= i && (x > lo || x < sink))) s[r] = -INFINITY;
             }
             if (!any) {   // codes and scales of slots that no row sees may be anything: zeros, for 0 * NaN is none
@@ -414,7 +404,6 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
             mbar_arrive(&bars.empty[vslot]);
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");   // (none is on its way, unless a wait ran out)
     // (a lane whose wait ran out has left with all the others, or does so below)
     if (n > 0) ok = mbar_wait(&bars.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
     __syncwarp();
@@ -435,7 +424,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
     tmem_ld_wait();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        if (r >= there) continue;
+        if (sh.out_row[r] < 0) continue;
         const float o = fmaf(fmaf(__uint_as_float(y[2 * R + r]), 0.0625f, __uint_as_float(y[R + r])), 0.0625f,
                              __uint_as_float(y[r])) * back;
         const size_t at = (size_t)sh.out_row[r];
@@ -450,6 +439,67 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
             if (t == 0) p.lse[at] = lr != 0.f ? (mr + log2f(lr)) * kLn2 : -INFINITY;
         }
     }
+}
+
+// Warps 5 and 6: the MMAs.
+template <int R>
+__device__ __forceinline__ void issue_warps(const Q8Params& P, const Work& w, uint8_t* sm, Shared& sh) {
+    using C = Cfg<R>;
+    const PagedArgs& p = P.a;
+    Bars& bars = sh.bars;
+    volatile int* abort = &sh.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = w.e1 - w.e0;
+    if (warp == 5) {
+        tmem_alloc(&sh.tmem_base, C::cols);
+        tmem_relinquish();
+    }
+    set_up_done();
+    const uint32_t tmem = sh.tmem_base;
+    const uint32_t ring = smem_u32(sm + C::ring);
+    if (warp == 5) {
+        // S of tile j, when K is there and the rows have read S of tile j - 2
+        constexpr uint32_t id_s = idesc_e4m3(128, C::ns, 0, 0);
+        const uint64_t d_q = sdesc_sw128(smem_u32(sm + C::q), 16, 1024);   // K-major, as K
+        const uint64_t d_ring = sdesc_sw128(ring, 16, 1024);
+        const int steps = p.d / 32;
+        for (int j = 0; j < n && w.any_ord; ++j) {
+            const int ld = w.k_load(j), s = ld % C::slots;
+            if (!wait_all(&bars.full[s], (ld / C::slots) & 1, abort, p.status)) break;
+            if (j > 1 && !wait_all(&bars.s_empty[j & 1], ((j - 2) >> 1) & 1, abort, p.status)) break;
+            tc_fence_after();
+            const uint64_t d_k = sdesc_advance(d_ring, s * kTileBytes);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < steps)
+                    mma_ss_e4m3_warp(tmem + (j & 1) * C::ns, sdesc_advance(d_k, 32 * k), sdesc_advance(d_q, 32 * k),
+                                 id_s, k > 0);
+            mma_commit_warp(&bars.s_full[j & 1]);
+            mma_commit_warp(&bars.empty[s]);
+        }
+    } else {
+        // O^T += V^T P^T of tile j, when V and the weights are there
+        constexpr uint32_t id_o = idesc_e4m3(128, C::np, 1, 1);
+        const uint64_t d_ring = sdesc_sw128(ring, 16384, 1024);                        // MN-major
+        const uint64_t d_p = sdesc_none(smem_u32(sm + C::p), 128, kTile * 16);
+        for (int j = 0; j < n; ++j) {
+            const int ld = w.v_load(j), s = ld % C::slots;
+            if (!wait_all(&bars.full[s], (ld / C::slots) & 1, abort, p.status)) break;
+            if (!wait_all(&bars.p_ready[j & 1], (j >> 1) & 1, abort, p.status)) break;
+            tc_fence_after();
+            const uint64_t d_v = sdesc_advance(d_ring, s * kTileBytes);
+            const uint64_t d_w = sdesc_advance(d_p, (j & 1) * C::p_bytes);
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k)
+                mma_ss_e4m3_warp(tmem + C::col_o, sdesc_advance(d_v, 4096 * k), sdesc_advance(d_w, 512 * k), id_o,
+                                 (j > 0 || k > 0) ? 1u : 0u);
+            mma_commit_warp(&bars.o_done[j & 1]);
+            mma_commit_warp(&bars.empty[s]);
+        }
+    }
+    // every MMA issued here is done before tensor memory is freed
+    mma_commit_warp(&bars.mma_idle[warp - 5]);
+    if (lane == 0) mbar_wait_bounded(&bars.mma_idle[warp - 5], 0, kWaitLimitNs);
+    __syncwarp();
 }
 
 template <int R>
@@ -484,7 +534,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::ctas) paged_q8_kernel(const 
     const PagedRow row = paged_place(p, w.it, block, lane);
     const int place = row.there ? (int)paged_out_row(p, row) : -1;
     const uint32_t kind = __ballot_sync(0xffffffffu, row.there && row.frozen);
-    w.f0 = kind ? __ffs(kind) - 1 : 32;
+    w.nf = __popc(kind);   // (they are the block's last rows)
+    const int slot = lane < w.there - w.nf ? lane : R - 1 - (lane - (w.there - w.nf));   // the row's place here
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
@@ -508,80 +559,29 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::ctas) paged_q8_kernel(const 
     const int per = p.per_chunk[w.it.part];
     w.e0 = min(w.it.chunk * per, w.g.n);
     w.e1 = min(w.e0 + per, w.g.n);
-    if (warp == 0) {
-        sh.out_row[lane] = place;
-        sh.pos[lane] = i < 0 ? -1 : i - w.off;
+    if (warp == 0 && lane < R) {
+        sh.out_row[slot] = place;
+        sh.pos[slot] = i < 0 ? -1 : i - w.off;
         // (rows that see nothing, whose columns of S may hold anything: no score passes their maximum)
-        sh.m[lane] = i < 0 ? INFINITY : kNoMax;
-        sh.scale[lane] = 0.f;
-        sh.a[lane] = p.a + (size_t)row.h * p.ld + w.off;
-        sh.r[lane] = p.r + (size_t)row.h * p.ld + (i < 0 ? 0 : i - w.off);
+        sh.m[slot] = i < 0 ? INFINITY : kNoMax;
+        sh.scale[slot] = 0.f;
+        sh.a[slot] = p.a + (size_t)row.h * p.ld + w.off;
+        sh.r[slot] = p.r + (size_t)row.h * p.ld + (i < 0 ? 0 : i - w.off);
     }
     if (w.e0 >= w.e1) {   // no keys: nothing but the rows' empty sums
         __syncthreads();
-        write_empty(p, w.it, w.there, sh.out_row, kThreads);
+        write_empty(p, w.it, R, sh.out_row, kThreads);
         return;
     }
-    const int n = w.e1 - w.e0;
-    Bars& bars = sh.bars;
-    volatile int* abort = &sh.abort_flag;
-    if (warp == 4) {
-        load_warp<C>(P, w, sm, sh);
-    } else if (warp < 4) {
+    // (one setmaxnreg for each warpgroup)
+    if (warp < 4) {
+        if constexpr (C::split) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
         rows_sync();   // the rows' places
         row_warps<R>(P, w, q, sm, sh);
     } else {
-        if (warp == 5) {
-            tmem_alloc(&sh.tmem_base, C::cols);
-            tmem_relinquish();
-        }
-        set_up_done();
-        const uint32_t tmem = sh.tmem_base;
-        const uint32_t ring = smem_u32(sm + C::ring);
-        if (warp == 5) {
-            // S of tile j, when K is there and the rows have read S of tile j - 2
-            constexpr uint32_t id_s = idesc_e4m3(128, C::ns, 0, 0);
-            const uint64_t d_q = sdesc_sw128(smem_u32(sm + C::q), 16, 1024);   // K-major, as K
-            const uint64_t d_ring = sdesc_sw128(ring, 16, 1024);
-            const int steps = p.d / 32;
-            for (int j = 0; j < n && w.any_ord; ++j) {
-                const int ld = w.k_load(j), s = ld % C::slots;
-                if (!wait_all(&bars.full[s], (ld / C::slots) & 1, abort, p.status)) break;
-                if (j > 1 && !wait_all(&bars.s_empty[j & 1], ((j - 2) >> 1) & 1, abort, p.status)) break;
-                tc_fence_after();
-                const uint64_t d_k = sdesc_advance(d_ring, s * kTileBytes);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k < steps)
-                        mma_ss_e4m3_warp(tmem + (j & 1) * C::ns, sdesc_advance(d_k, 32 * k), sdesc_advance(d_q, 32 * k),
-                                     id_s, k > 0);
-                mma_commit_warp(&bars.s_full[j & 1]);
-                mma_commit_warp(&bars.empty[s]);
-            }
-        } else {
-            // O^T += V^T P^T of tile j, when V and the weights are there
-            constexpr uint32_t id_o = idesc_e4m3(128, C::np, 1, 1);
-            const uint64_t d_ring = sdesc_sw128(ring, 16384, 1024);                        // MN-major
-            const uint64_t d_p = sdesc_none(smem_u32(sm + C::p), 128, kTile * 16);
-            for (int j = 0; j < n; ++j) {
-                const int ld = w.v_load(j), s = ld % C::slots;
-                if (!wait_all(&bars.full[s], (ld / C::slots) & 1, abort, p.status)) break;
-                if (!wait_all(&bars.p_ready[j & 1], (j >> 1) & 1, abort, p.status)) break;
-                tc_fence_after();
-                const uint64_t d_v = sdesc_advance(d_ring, s * kTileBytes);
-                const uint64_t d_w = sdesc_advance(d_p, (j & 1) * C::p_bytes);
-#pragma unroll
-                for (int k = 0; k < kTile / 32; ++k)
-                    mma_ss_e4m3_warp(tmem + C::col_o, sdesc_advance(d_v, 4096 * k), sdesc_advance(d_w, 512 * k), id_o,
-                                     (j > 0 || k > 0) ? 1u : 0u);
-                mma_commit_warp(&bars.o_done[j & 1]);
-                mma_commit_warp(&bars.empty[s]);
-            }
-        }
-        // every MMA issued here is done before tensor memory is freed
-        mma_commit_warp(&bars.mma_idle[warp - 5]);
-        if (lane == 0) mbar_wait_bounded(&bars.mma_idle[warp - 5], 0, kWaitLimitNs);
-        __syncwarp();
+        if constexpr (C::split) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == 4) load_warp<C>(P, w, sm, sh);
+        else if (warp < 7) issue_warps<R>(P, w, sm, sh);
     }
     tc_fence_before();
     __syncthreads();
@@ -598,6 +598,18 @@ cudaError_t launch_r(const Q8Params& P, unsigned items, cudaStream_t s) {
     const cudaError_t e =
         cudaFuncSetAttribute(paged_q8_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    if constexpr (Cfg<R>::split) {
+        // A build that launches with fewer registers could never hand the softmax theirs (a property of the
+        // compiled kernel, looked up once).
+        static std::atomic<int> regs{0};
+        if (regs.load() == 0) {
+            cudaFuncAttributes fa;
+            const cudaError_t f = cudaFuncGetAttributes(&fa, paged_q8_kernel<R>);
+            if (f != cudaSuccess) return f;
+            regs.store(fa.numRegs);
+        }
+        if (kRegsRows + kRegsOther > 2 * regs.load()) return cudaErrorInvalidConfiguration;
+    }
     return launch_ex(paged_q8_kernel<R>, dim3(items), dim3(kThreads), (size_t)smem, s, true, 1, P);
 }
 
