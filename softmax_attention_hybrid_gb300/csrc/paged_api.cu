@@ -173,11 +173,15 @@ Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, Kind kin
 }
 
 // Items along the keys for `units` units of `nt` tiles each: the number that makes the part
-// shortest, with `slots` items at a time. even: the units have the same length, so that rounds
-// end together; else their lengths differ, and the last items run alone for a while.
+// shortest, with `slots` items at a time. kEven: the units have the same length, so that rounds
+// end together. kSpread: their lengths differ, and the last items run alone for a while. kMixed (8-bit caches): the mean
+// of what it costs if all sequences are as long as the bound, in whole rounds, and if they fill two thirds of it on
+// the average. (32 sequences of 4K to 16K tokens: 143, 114, 128, 120, 118, 124 us with 1 .. 6 items; 16 of 2K to 8K
+// with up to five tokens each: 78, 66, 87, 86 us with 2 .. 5, where three take two rounds once the sequences are alike.)
 // Candidates: one, the most items that fit in 1, 2, ... rounds, and the minimum over c of
 // (units c / slots) (set_up + nt / c) + nt / c, the work and the tail of c items per unit.
-long long pick_chunks(long long units, long long nt, long long most, long long slots, int set_up, bool even,
+enum class Lengths { kEven, kSpread, kMixed };
+long long pick_chunks(long long units, long long nt, long long most, long long slots, int set_up, Lengths lengths,
                       bool joins_anyway) {
     long long best = 1;
     double best_cost = 1e300;
@@ -187,8 +191,12 @@ long long pick_chunks(long long units, long long nt, long long most, long long s
         c = c < 1 ? 1 : c > most ? most : c;
         const long long per = ceil_div(nt, c);
         const double rounds = (double)(units * ceil_div(nt, per)) / (double)slots;
-        const double cost =
-            (even ? ceil(rounds) : rounds + 1.0) * (double)(set_up + per) + (c > 1 && !joins_anyway ? kJoin : 0);
+        const double some = 0.66 * rounds;
+        const double turns = lengths == Lengths::kEven     ? ceil(rounds)
+                             : lengths == Lengths::kSpread ? rounds + 1.0
+                                                           : 0.5 * (ceil(rounds) + (some <= 1.0 ? 1.0 : some + 0.5));
+        const double cost = turns * (double)(set_up + per) + (c > 1 && !joins_anyway ? kJoin : 0) +
+                            (lengths == Lengths::kMixed ? 0.15 * (double)c : 0.0);
         if (cost < best_cost || (cost == best_cost && c < best)) {
             best_cost = cost;
             best = c;
@@ -223,7 +231,11 @@ void set_items(PagedArgs& p, const Plan& x, int nfrozen) {
         }
         // (a prefix's units have the same length, and so have windows; paged_q8_rows.cu runs the longest first)
         const long long c = pick_chunks(x.units[i], nt[i], most_chunks(x, i, nt[i]), x.slots[i] - beside,
-                                        x.set_up[i], i == 0 || windowed || x.rows[i] == kQ8Rows, p.P > 0);
+                                        x.set_up[i],
+                                        i == 0 || windowed || x.rows[i] == kQ8Rows ? Lengths::kEven
+                                        : x.set_up[i] == kSetUpQ8 && p.P == 0      ? Lengths::kMixed
+                                                                                   : Lengths::kSpread,
+                                        p.P > 0);
         p.per_chunk[i] = (int)ceil_div(nt[i], c);
         p.chunks[i] = (int)ceil_div(nt[i], p.per_chunk[i]);
         items[i] = (unsigned)(x.units[i] * p.chunks[i]);
