@@ -94,6 +94,17 @@ struct Raw<__nv_bfloat16> {
     }
 };
 
+__device__ __forceinline__ float max3_abs(float m, float x, float y) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(x)), "f"(fabsf(y)));
+    return r;
+}
+__device__ __forceinline__ float reciprocal(float x) {   // to a step of fp32; x at least 2^-126
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // 8 values as codes of e4m3 (out of range: the largest; NaN stays NaN).
 __device__ __forceinline__ uint2 codes8(const float* x, float inv) {
     uint32_t c[4];
@@ -140,7 +151,7 @@ __device__ __forceinline__ void append_token(const AppendArgs& p, int b, int t, 
     }
     // My heads are group, group + groups, ...: the threads of a token then read rows that lie next to
     // each other. Several rows are on their way at a time.
-    constexpr int kBatch = sizeof(E) == 2 ? 4 : 2;
+    constexpr int kBatch = sizeof(E) == 2 && !kQ8 ? 4 : 2;
     for (int s0 = group; s0 < p.slots; s0 += kBatch * p.groups) {
         Raw<E> x[kBatch], y[kBatch];
         E* dst[kBatch];          // the row in q_out or in the cache
@@ -214,13 +225,13 @@ __device__ __forceinline__ void append_token(const AppendArgs& p, int b, int t, 
             }
             if constexpr (kQ8) {
                 if (coded) {
-                    float m = 0.f;
+                    float m = 0.f;   // (a NaN is left out)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(a[e]), fabsf(z[e])));
+                    for (int e = 0; e < 8; ++e) m = max3_abs(m, a[e], z[e]);
                     const unsigned first = threadIdx.x & 31u & ~(unsigned)(p.lanes - 1);
                     const unsigned mask = ((1u << p.lanes) - 1u) << first;
                     for (int o = p.lanes >> 1; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
-                    const float scale = fmaxf(__fdiv_rn(m, 448.f), 0x1p-126f), inv = 1.f / scale;
+                    const float scale = fmaxf(m * (1.f / 448.f), 0x1p-126f), inv = reciprocal(scale);
                     if (mine) {
                         uint8_t* row = (uint8_t*)dst[k] + at[k] * p.d;
                         *reinterpret_cast<uint2*>(row + (is_v ? 16 * u : c0)) = codes8(a, inv);
@@ -237,7 +248,7 @@ __device__ __forceinline__ void append_token(const AppendArgs& p, int b, int t, 
 }
 
 template <typename E, bool kQ8>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs p) {
+__device__ __forceinline__ void append_threads(const AppendArgs& p) {
     grid_dep_wait();
     grid_dep_launch();
     const unsigned id = blockIdx.x * kThreads + threadIdx.x;   // (token, group of slots, unit) of a sequence
@@ -248,6 +259,16 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     if (t >= p.T) return;
     for (int b = blockIdx.y; b < p.B; b += gridDim.y) append_token<E, kQ8>(p, b, t, group, u);
 }
+template <typename E>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs p) {
+    append_threads<E, false>(p);
+}
+// (six blocks to an SM: more loads on their way than with the 128 registers that it would take)
+template <typename E>
+__global__ void __launch_bounds__(kThreads, 6) append_codes_kernel(const __grid_constant__ AppendArgs p) {
+    append_threads<E, true>(p);
+}
+
 bool aligned(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 // x modulo 1 in units of 2^-64, to the nearest (x - trunc(x) and the scaling are exact).
@@ -351,7 +372,9 @@ int append(const void* q, const void* k, const void* v, const int64_t* strides, 
     // d 64) take 62, 38, 28, 23, 24 us with 1, 2, 4, 8, 16 heads per thread; one token of 32
     // sequences (32 + 2 x 8 heads, d 128) 3.4, 3.6, 4.0, 5.1, 6.7 us, one call behind another.
     const long long all = (long long)B * T * p.slots * p.lanes;
-    p.per = all > 8ll * kFullGpu ? 8 : all > kFullGpu ? (int)(all / kFullGpu) : 1;
+    // (8-bit caches, the same prompts: 40, 35, 36, 32, 39 us with 4, 6, 8, 12, 18.)
+    const int most = coded ? 12 : 8;
+    p.per = all > most * kFullGpu ? most : all > kFullGpu ? (int)(all / kFullGpu) : 1;
     p.groups = (p.slots + p.per - 1) / p.per;
     const long long threads = (long long)T * p.groups * p.lanes;   // of a sequence: at most 2^21 x 96 x 8
     const long long blocks = (threads + kThreads - 1) / kThreads;
@@ -359,8 +382,8 @@ int append(const void* q, const void* k, const void* v, const int64_t* strides, 
     cudaStream_t cs = (cudaStream_t)stream;
     before_launch(SAF_KERNEL_KV_APPEND, cs);
     const cudaError_t err =
-        launch_ex(coded ? (dt == SAF_BF16 ? append_kernel<__nv_bfloat16, true> : append_kernel<float, true>)
-                        : (dt == SAF_BF16 ? append_kernel<__nv_bfloat16, false> : append_kernel<float, false>),
+        launch_ex(coded ? (dt == SAF_BF16 ? append_codes_kernel<__nv_bfloat16> : append_codes_kernel<float>)
+                        : (dt == SAF_BF16 ? append_kernel<__nv_bfloat16> : append_kernel<float>),
                   grid, dim3(kThreads), 0, cs, true, 1, p);
     after_launch(SAF_KERNEL_KV_APPEND, cs);
     return launch_status(err);
