@@ -307,11 +307,9 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
         uint32_t sv[32];
 #pragma unroll 1
         for (int c0 = 0; c0 < TK; c0 += 32) {
-            if (w.any_ord) {
+            if (any_scaled) {
                 tmem_ld32(tmem + c0, sv);
                 tmem_ld_wait();
-            }
-            if (any_scaled) {
 #pragma unroll
                 for (int c = 0; c < 32; c += 4) {
                     const float4 ks = *reinterpret_cast<const float4*>(&sh.ks[buf][c0 + c]);
@@ -322,6 +320,9 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
                     sv[c + 2] = __float_as_uint(b.x);
                     sv[c + 3] = __float_as_uint(b.y);
                 }
+            } else {   // (rows without a token: anything finite)
+#pragma unroll
+                for (int c = 0; c < 32; ++c) sv[c] = 0u;
             }
             if (any_frozen) {   // the fixed pattern's logits (Eq. 3)
                 if (w.staged) {
