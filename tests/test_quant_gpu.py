@@ -333,6 +333,103 @@ def test_a_nan_in_the_cache_reaches_the_rows_that_see_it(saf):
                     assert o[0, 2:, :, 7].isnan().all() and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("G,T", [(1, 1), (4, 1), (5, 1), (8, 1), (3, 3), (4, 4), (17, 1), (6, 4), (5, 5), (8, 4), (11, 3),
+                                 (2, 63), (43, 3), (4, 64), (1, 257), (6, 100)])
+@pytest.mark.parametrize("kind", ["ordinary", "frozen", "mixed", "window"])
+def test_every_number_of_rows_to_a_block(saf, d, G, T, kind):
+    # (1 to 600 rows to a key/value head: every size of block, full and with one row more)
+    H = 2 * G
+    frozen = [kind == "frozen" or (kind == "mixed" and h % 2 == 1) for h in range(H)]
+    window, sinks = (70, 3) if kind == "window" else (0, 0)
+    x = Batch("bf16", H, 2, T, d, 32, (300, 0, 161), (T, max(1, T // 3), T), seed=G + T)
+    x.check(*x.call(saf, frozen, window, sinks), frozen, window, sinks)
+
+
+def test_many_sequences(saf):
+    # more sequences than a block of many rows puts in order, of very unequal lengths
+    for B, H, T in ((300, 40, 1), (300, 2, 1), (257, 2, 20), (256, 40, 1)):
+        ctx = [(37 * b) % 200 if b % 7 else 0 for b in range(B)]
+        frozen = [h % 5 == 4 for h in range(H)]
+        x = Batch("bf16", H, 1, T, 64, 16, ctx, [T if b % 3 else T // 2 for b in range(B)], seed=B + H)
+        x.check(*x.call(saf, frozen), frozen)
+
+
+def test_positions_far_apart_in_blocks_of_many_rows(saf):
+    # the frozen heads' patterns of a block do not fit into shared memory, or just do
+    for spread in (1500, 2300, 4000):
+        ctx = [0, spread] + [(spread * b) // 20 for b in range(18)]
+        frozen = [0, 0, 1, 1]
+        x = Batch("bf16", 4, 1, 1, 64, 64, ctx, [1] * 20, prefix=150, seed=spread)
+        x.check(*x.call(saf, frozen), frozen)
+
+
+def test_priors_of_any_alignment(saf):
+    # rows of a and r that begin anywhere in a 16-byte line, ending with the last position
+    for extra in range(4):
+        for T in (1, 40):
+            x = Batch("bf16", 4, 1, T, 64, 16, (77 + extra, 3), (T, T), seed=91)
+            big = torch.full((2, 4 * x.a.shape[1] + 1), float("nan"))
+            a, r = (y[1:].view(4, x.a.shape[1]) for y in big.cuda())   # 4 bytes into a line
+            a.copy_(x.a)
+            r.copy_(x.r)
+            o, lse = x.call(saf, [0, 1, 1, 0], a=a, r=r)
+            x.check(o, lse, [0, 1, 1, 0])
+
+
+def test_sequences_that_share_pages(saf):
+    # the same pages in two sequences' tables, and twice in one
+    x = Batch("bf16", 4, 2, 2, 64, 16, (100, 100, 40), (2, 2, 2), seed=92)
+    x.table[1] = x.table[0]
+    x.table[0, 1] = x.table[0, 0]
+    x.q[1] = x.q[0]
+    o, lse = x.call(saf, [0, 1, 0, 0])
+    x.check(o, lse, [0, 1, 0, 0])
+    x.table[1] = x.table[0]
+    o, lse = x.call(saf, [0, 1, 0, 0])
+    assert torch.equal(o[0], o[1]) and torch.equal(lse[0], lse[1])
+
+
+def test_empty_calls(saf):
+    x = Batch("bf16", 4, 2, 1, 64, 16, (10,), (1,), seed=93)
+    none = torch.zeros(0, x.table.shape[1], dtype=torch.int32, device="cuda")
+    count = torch.zeros(0, dtype=torch.int32, device="cuda")
+    o, lse = saf.saf_attn_paged_quant(x.q[:0].cuda(), *x.cache(), none, count, 16)
+    assert o.shape == (0, 4, 1, 64) and lse.shape == (0, 4, 1)
+    k, v = saf.saf_kv_read_quant(*x.cache(), x.table.cuda(), T=0, dtype=torch.bfloat16)
+    assert k.shape == v.shape == (1, 2, 0, 64)
+    k, v = saf.saf_kv_read_quant(*x.cache(), none, T=5, dtype=torch.float32)
+    assert k.shape == v.shape == (0, 2, 5, 64)
+    rows = torch.zeros(1, 2, 0, 64, dtype=torch.bfloat16, device="cuda")
+    before = x.cache()
+    assert saf.saf_kv_append_quant(rows, rows, *before, x.table.cuda(), x.ctx.cuda()) is None
+
+
+def test_refused_tensors(saf):
+    x = Batch("bf16", 4, 2, 1, 64, 16, (10,), (1,), seed=94)
+    kc, vc, ks, vs = x.cache()
+    q, table, ctx = x.q.cuda(), x.table.cuda(), x.ctx.cuda()
+    call = saf.saf_attn_paged_quant
+    for args, err in (((q, kc.view(torch.uint8), vc, ks, vs), TypeError), ((q, kc, vc.view(torch.uint8), ks, vs), TypeError),
+                      ((q, kc, vc, ks.double(), vs), TypeError), ((q, kc, vc, ks, vs.half()), TypeError),
+                      ((q, kc, vc, ks, vs[:, :, :8]), ValueError), ((q, kc, vc, ks[1:], vs), ValueError),
+                      ((q, kc, vc, ks.transpose(0, 1).contiguous().transpose(0, 1), vs), ValueError),
+                      ((q, kc, vc, ks, vs.cpu()), ValueError), ((q.half(), kc, vc, ks, vs), TypeError),
+                      ((q[..., :32].contiguous(), kc, vc, ks, vs), ValueError)):
+        with pytest.raises(err):
+            call(*args, table, ctx, 11)
+    for kw in (dict(), dict(T=3), dict(dtype=torch.bfloat16), dict(T=3, dtype=torch.float16),
+               dict(k_out=torch.zeros(1, 2, 4, 64, device="cuda"), v_out=torch.zeros(1, 2, 3, 64, device="cuda")),
+               dict(v_out=torch.zeros(1, 2, 3, 64, device="cuda"), T=4),
+               dict(T=3, dtype=torch.float32, status=torch.zeros(1, dtype=torch.int32, device="cuda"))):
+        with pytest.raises((ValueError, TypeError)):
+            saf.saf_kv_read_quant(kc, vc, ks, vs, table, **kw)
+    with pytest.raises(ValueError):
+        saf.saf_kv_read_quant(None, vc, ks, vs, table, T=3, dtype=torch.float32)
+    with pytest.raises(TypeError):
+        saf.saf_kv_append_quant(q[:, :2], q[:, :2], kc.view(torch.uint8), vc, ks, vs, table, ctx)
+
+
 def test_positions_far_apart(saf):
     for dtype, d in SOME:
         frozen = [0, 1, 0, 0]
