@@ -199,7 +199,10 @@ __host__ __device__ constexpr int paged_tc_tile(int d, int rows) { return d == 6
 cudaError_t launch_paged_tc(const PagedArgs& p, cudaStream_t s);
 constexpr int kSimtRows = 8, kSimtTile = 32;
 cudaError_t launch_paged_simt(const PagedArgs& p, cudaStream_t s);
-cudaError_t launch_paged_simt_q8(const PagedArgs& p, cudaStream_t s);   // 8-bit caches, fp32 q and o
+// 8-bit caches, fp32 q and o, CUDA cores (paged_q8_simt.cu): blocks of 2, 4, 6 or 8 rows, tiles kQ8SimtTile.
+constexpr int kQ8SimtTile = 128;
+__host__ __device__ constexpr int paged_q8_simt_ctas(int d) { return d == 64 ? 4 : d == 96 ? 3 : 2; }   // of an SM
+cudaError_t launch_paged_q8_simt(const PagedArgs& p, cudaStream_t s);
 // 8-bit caches, bf16 q and o, tensor cores. paged_q8_tc.cu: blocks of 4, 8, 16, 24 or 32 rows, tiles kQ8Tile;
 // paged_q8_rows.cu: blocks of 256 rows, tiles kQ8RowsTile. `items` of p's, the first ones.
 constexpr int kQ8Tile = 128, kQ8RowsTile = 128, kQ8Rows = 256;

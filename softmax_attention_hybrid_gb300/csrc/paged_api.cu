@@ -18,8 +18,9 @@ constexpr int kRounds = 8;
 // the join), in tiles. Measured: 32 sequences of 4K to 16K tokens, 8 key/value heads, d 128 take
 // 237, 211, 210, 218, 215 us with 2, 3, 5, 8, 12 items per sequence and head.
 constexpr int kSetUp = 10;
-// 8-bit caches: of the kernel for few rows and of the one for many.
-constexpr int kSetUpQ8 = 7, kSetUpQ8Rows = 8;
+// 8-bit caches: of the kernel for few rows, of the one for many, and of the one for fp32 (four sequences of up to
+// 2000 tokens, five tokens each, 16 heads: 19.1, 19.1, 20.5, 26.9 us with 2, 3, 5, 8).
+constexpr int kSetUpQ8 = 7, kSetUpQ8Rows = 8, kSetUpQ8Simt = 3;
 // What the joining kernel costs, in tiles, where a call could do without one: one new token of
 // one sequence (12 heads, d 64) takes 6.1 and 7.1 us with 1 and 2 items for 256 keys, 7.6 with 1
 // and 4 for 512, 10.5 and 8.5 for 1024.
@@ -160,6 +161,13 @@ Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, Kind kin
             x.tile[i] = n[i] > 32 ? kQ8RowsTile : kQ8Tile;
             x.set_up[i] = n[i] > 32 ? kSetUpQ8Rows : kSetUpQ8;
             x.slots[i] = n[i] > 32 ? kSlotsQ8Rows : x.rows[i] == 4 ? kSms * 3 : kSms * 2;
+        }
+        if (kind == Kind::kSimtQ8) {   // a launch serves both parts
+            const long long most = n[0] > n[1] ? n[0] : n[1];
+            x.rows[i] = most <= 2 ? 2 : most <= 4 ? 4 : most <= 6 ? 6 : 8;
+            x.tile[i] = kQ8SimtTile;
+            x.set_up[i] = kSetUpQ8Simt;
+            x.slots[i] = kSms * paged_q8_simt_ctas(d);
         }
         // several blocks to a head: each head begins its own
         const long long per_head = n[i] / G;
@@ -379,7 +387,7 @@ int paged(const void* q, const void* k_cache, const void* v_cache, bool q8, cons
     cudaError_t e = kind == Kind::kTc      ? launch_paged_tc(p, s)
                     : kind == Kind::kSimt ? launch_paged_simt(p, s)
                     : kind == Kind::kTcQ8 ? launch_q8(p, s)
-                                          : launch_paged_simt_q8(p, s);
+                                          : launch_paged_q8_simt(p, s);
     if (e == cudaSuccess && p.nsplit > 1) {
         note_launch();
         e = bf16 ? launch_join<__nv_bfloat16>(p, s) : launch_join<float>(p, s);

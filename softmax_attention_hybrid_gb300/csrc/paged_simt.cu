@@ -8,11 +8,6 @@
 //   output   a thread per column of d: the rows' weights (broadcast) times the column's values
 // Bound by shared memory and the cache's bytes alike: a tile at d = 96 is 24 KB, 1000 cycles of an
 // SM's share of the memory, and about as many of shared-memory reads.
-//
-// 8-bit caches: the next tile's codes wait in registers and are written to shared memory as
-// code * scale in fp32 (each product rounded once) when this tile is done.
-#include <cuda_fp8.h>
-
 #include "paged.h"
 
 namespace saf {
@@ -42,43 +37,7 @@ __device__ __forceinline__ void copy16(void* dst, const float* src, bool have) {
                  : "memory");
 }
 
-// 8-bit caches: a tile on its way, 16 codes and their row's scale per register set.
 template <int D>
-struct Codes {
-    static constexpr int sets = (TK * D / 16 + kThreads - 1) / kThreads;
-    uint4 c[sets];
-    float scale[sets];
-    __device__ __forceinline__ void fetch(const uint8_t* cache, const float* scales, const long long* at) {
-#pragma unroll
-        for (int i = 0; i < sets; ++i) {
-            const int u = (int)threadIdx.x + i * kThreads, kk = u / (D / 16), col = 16 * (u - kk * (D / 16));
-            c[i] = make_uint4(0, 0, 0, 0);
-            scale[i] = 0.f;
-            if (kk >= TK || at[kk] < 0) continue;
-            c[i] = *reinterpret_cast<const uint4*>(cache + at[kk] + col);
-            scale[i] = scales[at[kk] / D];
-        }
-    }
-    template <int kPitch>
-    __device__ __forceinline__ void put(float (*tile)[kPitch]) const {
-#pragma unroll
-        for (int i = 0; i < sets; ++i) {
-            const int u = (int)threadIdx.x + i * kThreads, kk = u / (D / 16), col = 16 * (u - kk * (D / 16));
-            if (kk >= TK) continue;
-            const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 x = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w[e], __NV_E4M3)));
-                const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e] >> 16), __NV_E4M3)));
-                *reinterpret_cast<float4*>(&tile[kk][col + 4 * e]) =
-                    make_float4(x.x * scale[i], x.y * scale[i], y.x * scale[i], y.y * scale[i]);
-            }
-        }
-    }
-};
-
-// kQ8: 8-bit caches.
-template <int D, bool kQ8>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_constant__ PagedArgs p) {
     extern __shared__ __align__(16) uint8_t raw[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
@@ -118,8 +77,6 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
     const int off = it.part ? p.P : 0;
     const float* kc = (const float*)p.k_cache;
     const float* vc = (const float*)p.v_cache;
-    const uint8_t* kc8 = (const uint8_t*)p.k_cache;
-    const uint8_t* vc8 = (const uint8_t*)p.v_cache;
     const bool any_ord = sm.any_ord != 0;
 
     // where key `lane` of tile e lies (warp 0); keys that no row sees, and those of pages outside
@@ -158,19 +115,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
             *reinterpret_cast<float4*>(&sm.q[rr][c]) = x;
         }
     __syncthreads();
-    Codes<D> k8, v8;
-    if constexpr (kQ8) {
-        if (e0 < e1) {
-            if (any_ord) {
-                k8.fetch(kc8, p.k_scale, sm.at[0]);
-                k8.put(sm.k[0]);
-            }
-            v8.fetch(vc8, p.v_scale, sm.at[0]);
-            v8.put(sm.v[0]);
-        }
-    } else {
-        if (e0 < e1) copy_tile(0);
-    }
+    if (e0 < e1) copy_tile(0);
 
     // this warp's two rows
     int ri[2];
@@ -204,14 +149,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
             if (fz[u] && j <= ri[u]) lg[u] = __ldg(ra[u] + j) + __ldg(rr[u] + ri[u] - j);
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();   // the tile is there, and everyone is done with the one before
-        if (e + 1 < e1) {
-            if constexpr (kQ8) {
-                if (any_ord) k8.fetch(kc8, p.k_scale, sm.at[s ^ 1]);
-                v8.fetch(vc8, p.v_scale, sm.at[s ^ 1]);
-            } else {
-                copy_tile(s ^ 1);
-            }
-        }
+        if (e + 1 < e1) copy_tile(s ^ 1);
         const long long live = sm.at[s][lane];
         const long long next = warp == 0 ? look(e + 2) : -1;
         float dot[2] = {0.f, 0.f};
@@ -269,12 +207,6 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
                 acc[7] = fmaf(pb.w, vx, acc[7]);
             }
         }
-        if constexpr (kQ8) {   // (the other tile's last reader is done since the first barrier above)
-            if (e + 1 < e1) {
-                if (any_ord) k8.put(sm.k[s ^ 1]);
-                v8.put(sm.v[s ^ 1]);
-            }
-        }
     }
 
 #pragma unroll
@@ -314,28 +246,22 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const __grid_const
     }
 }
 
-template <int D, bool kQ8>
+template <int D>
 cudaError_t launch_d(const PagedArgs& p, cudaStream_t s) {
     const size_t smem = sizeof(Smem<D>);
-    cudaError_t e =
-        cudaFuncSetAttribute(paged_simt_kernel<D, kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_ex(paged_simt_kernel<D, kQ8>, dim3(p.items), dim3(kThreads), smem, s, true, 1, p);
-}
-
-template <bool kQ8>
-cudaError_t launch_type(const PagedArgs& p, cudaStream_t s) {
-    switch (p.d) {
-        case 96: return launch_d<96, kQ8>(p, s);
-        case 128: return launch_d<128, kQ8>(p, s);
-        default: return launch_d<64, kQ8>(p, s);
-    }
+    return launch_ex(paged_simt_kernel<D>, dim3(p.items), dim3(kThreads), smem, s, true, 1, p);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_simt(const PagedArgs& p, cudaStream_t s) { return launch_type<false>(p, s); }
-
-cudaError_t launch_paged_simt_q8(const PagedArgs& p, cudaStream_t s) { return launch_type<true>(p, s); }
+cudaError_t launch_paged_simt(const PagedArgs& p, cudaStream_t s) {
+    switch (p.d) {
+        case 96: return launch_d<96>(p, s);
+        case 128: return launch_d<128>(p, s);
+        default: return launch_d<64>(p, s);
+    }
+}
 
 }  // namespace saf
