@@ -251,8 +251,11 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
             const float ks = reinterpret_cast<const float*>(sm + C::scales + slot * kScaleBytes)[t];
             read_s<R>(tmem + buf * C::ns, s);
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
+            // Every lane's scale must be in its register before the slot is given back, and nothing here waits for that
+            // otherwise: reads of shared memory that other blocks' writes hold up (masked tiles) then found the next load's
+            // scales. So the arrival takes a value from them (the comparison always holds).
+            const bool read = __reduce_or_sync(0xffffffffu, __float_as_uint(ks) & 0x7fffffffu) != 0xffffffffu;
+            if (lane == 0 && read) {
                 mbar_arrive(&bars.s_empty[buf]);
                 mbar_arrive(&bars.empty[slot]);
             }

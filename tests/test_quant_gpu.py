@@ -346,6 +346,51 @@ def test_every_number_of_rows_to_a_block(saf, d, G, T, kind):
     x.check(*x.call(saf, frozen, window, sinks), frozen, window, sinks)
 
 
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("G,T", [(1, 1), (2, 1), (3, 1), (1, 4), (5, 1), (3, 2), (1, 7), (4, 2), (3, 3), (5, 5), (1, 40)])
+@pytest.mark.parametrize("kind", ["ordinary", "frozen", "mixed", "window", "prefix"])
+def test_every_number_of_rows_to_a_block_fp32(saf, d, G, T, kind):
+    H = 2 * G
+    frozen = [kind == "frozen" or (kind in ("mixed", "prefix") and h % 2 == 1) for h in range(H)]
+    window, sinks = (70, 3) if kind == "window" else (0, 0)
+    ctx, n_new = ((300, 0, 161), (T, max(1, T // 3), T)) if (G + T) % 2 else ((257,), (T,))
+    x = Batch("fp32", H, 2, T, d, 32, ctx, n_new, prefix=150 if kind == "prefix" else 0, seed=G + T)
+    x.check(*x.call(saf, frozen, window, sinks), frozen, window, sinks)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_magnitudes_of_q_and_of_the_scales(saf, dt):
+    # sums over codes of q of every size: scores, not what leads to them, decide
+    for q, k in ((2.0 ** 100, 2.0 ** -100), (2.0 ** -100, 2.0 ** 100), (2.0 ** -110, 2.0 ** -10), (2.0 ** 60, 2.0 ** -60)):
+        x = Batch(dt, 4, 2, 2, 64, 16, (90, 33), (2, 2), seed=95)
+        x.q = x.q * q
+        x.scales[0] = x.scales[0] * k
+        x.check(*x.call(saf))
+
+
+@pytest.mark.parametrize("H,T,d,page,window,sinks", [
+    (32, 1, 128, 128, 1000, 4), (32, 1, 128, 128, 0, 0), (32, 1, 64, 128, 1000, 4), (32, 1, 128, 16, 1000, 4),
+    (64, 1, 128, 128, 1000, 4), (160, 1, 128, 128, 1000, 4), (32, 4, 128, 128, 1000, 4), (32, 64, 128, 128, 300, 4)])
+def test_the_same_bits_every_time(saf, H, T, d, page, window, sinks):
+    # several blocks to an SM, all of them with masked tiles: what one block holds up, another must wait for
+    B, Hkv, max_len = 48, 8, 1500
+    g = torch.Generator(device="cuda").manual_seed(96)
+    per = -(-max_len // page)
+    shape = (B * per, Hkv, page, d)
+    cache = [torch.randn(*shape, generator=g, device="cuda").to(E4M3) for _ in range(2)]
+    scales = [0.5 + torch.rand(shape[:3], generator=g, device="cuda") for _ in range(2)]
+    table = torch.randperm(B * per, generator=g, device="cuda").int().view(B, per)
+    ctx = torch.randint(T, max_len - T, (B,), generator=g, device="cuda", dtype=torch.int32)
+    q = torch.randn(B, H, T, d, generator=g, device="cuda").to(torch.bfloat16)
+    first = None
+    for _ in range(12):
+        o, lse = saf.saf_attn_paged_quant(q, *cache, *scales, table, ctx, max_len, window=window, sinks=sinks)
+        torch.cuda.synchronize()
+        if first is None:
+            first = o.clone(), lse.clone()
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+
+
 def test_many_sequences(saf):
     # more sequences than a block of many rows puts in order, of very unequal lengths
     for B, H, T in ((300, 40, 1), (300, 2, 1), (257, 2, 20), (256, 40, 1)):
