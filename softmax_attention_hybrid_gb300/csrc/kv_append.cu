@@ -20,7 +20,10 @@
 // 8-bit caches (saf_kv_append_quant). A row y is held as codes and one scale,
 //     scale = max(max_c |y_c| / 448, 2^-126),   code_c = y_c / scale, rounded to e4m3,
 // with y rotated but not rounded before. The threads of a row are then neighbouring lanes (4, or
-// 8 of which 6 work at d = 96) that find the row's maximum by shuffles.
+// 8 of which 6 work at d = 96) that find the row's maximum by shuffles, and the reciprocal of the scale is
+// the hardware's, off by a step of fp32. The prompts of eight sequences (111 MB, 12 heads of 64)
+// take 32 us, 3.4 TB/s: instructions fill 58% of the issue slots (rotation, maximum, conversion), and the chain of
+// loads is the same.
 #include <cuda_fp8.h>
 #include <math.h>
 #include <string.h>

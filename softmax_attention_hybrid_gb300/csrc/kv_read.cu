@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
             ck[k] = cv[k] = typename X::Codes{};
             sk[k] = sv[k] = 0.f;
             if (page[k] >= 0) {
-                const size_t row = (((size_t)page[k] * p.Hkv + hk) << p.page_log2) + ((c + t) & ((1 << p.page_log2) - 1));
+                const size_t row = (((size_t)page[k] * p.Hkv + hk) << p.page_log2) + (((unsigned)c + (unsigned)t) & ((1u << p.page_log2) - 1u));
                 if (p.k_cache) {
                     ck[k] = *reinterpret_cast<const typename X::Codes*>(p.k_cache + row * p.d + X::count * u);
                     sk[k] = p.k_scale[row];

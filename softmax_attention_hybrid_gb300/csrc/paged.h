@@ -1,5 +1,6 @@
-// Shared declarations of the paged attention kernels (paged_tc.cu, paged_simt.cu),
-// their host entry points and the joining kernel (paged_api.cu).
+// Shared declarations of the paged attention kernels (paged_tc.cu, paged_simt.cu; over
+// 8-bit caches paged_q8_tc.cu, paged_q8_rows.cu, paged_q8_simt.cu), their host entry points and
+// the joining kernel (paged_api.cu).
 //
 // One call answers T new tokens of each of B sequences. Query row (b, h, t), t below
 // the sequence's number n of new tokens, stands at position i = P + ctx[b] + t (P: the

@@ -1,4 +1,4 @@
-// Host side of attention over a paged cache (saf_attn_paged, saf_attn_paged_shared):
+// Host side of attention over a paged cache (saf_attn_paged, saf_attn_paged_shared, and their _quant forms):
 // argument checks, the split of the keys over work items, the workspace, and the kernel
 // that joins the items of a row.
 #include <string.h>

@@ -21,6 +21,11 @@
 // they are found anew, and O and l are scaled. Tiles are walked from the newest key to the oldest: the
 // patterns of frozen heads, and most ordinary rows, look nearby first, so that the maximum is found early.
 //
+// 32 sequences of 4K to 16K tokens, 32 heads over 8 of 128 (a quarter frozen): 118 us, 6.0 TB/s, 88% of a plain copy's rate.
+// 64 sequences with a window of 1024: 41 us (512 items of 10 tiles on 456 places, and what an item costs beside its
+// tiles: counts, page, first load, softmax and product one after the other, 7 us). Five tokens each of 16 sequences, 20
+// rows: 78 us; a tile takes the four softmax warps of a CTA 4700 cycles (issue slots 34%), since its rows are all theirs.
+//
 // Warps (256 threads, two CTAs per SM, three with 4 rows): 0-3 softmax, 4 loads K, V and their scales (each of its lanes
 // fetches one page of the tile), 5 owns tensor memory and issues S, 6 issues P V. (7 completes the second
 // warpgroup: from 16 rows on the softmax takes registers over from it, since what it spills costs the latency

@@ -1,4 +1,5 @@
-// What the tensor-core kernels of paged attention share (paged_tc.cu, paged_q8_tc.cu).
+// What the tensor-core kernels of paged attention share (paged_tc.cu, paged_q8_tc.cu, paged_q8_rows.cu;
+// paged_q8_simt.cu takes its addresses of shared memory).
 #pragma once
 
 #include "paged.h"
