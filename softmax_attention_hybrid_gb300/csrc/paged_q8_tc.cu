@@ -75,7 +75,7 @@ struct Cfg {
     static constexpr int scales = p + 2 * p_bytes;
     static constexpr bool split = R > 8;
     static constexpr int total = scales + slots * kScaleBytes;
-    static_assert(total + 1024 + 3072 <= (ctas == 3 ? 76 : 114) * 1024, "CTAs of an SM");
+    static_assert(total + 4 * 1024 <= (ctas == 3 ? 76 : 114) * 1024, "CTAs of an SM");
     static constexpr uint32_t col_o = 2 * ns;         // S of two tiles, then O
     static constexpr uint32_t cols = R <= 8 ? 64 : R == 16 ? 128 : 256;
     static_assert(col_o + np <= cols, "tensor memory");
