@@ -185,7 +185,7 @@ Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, Kind kin
 // end together. kSpread: their lengths differ, and the last items run alone for a while. kMixed (8-bit caches): the mean
 // of what it costs if all sequences are as long as the bound, in whole rounds, and if they fill two thirds of it on
 // the average. (32 sequences of 4K to 16K tokens: 143, 114, 128, 120, 118, 124 us with 1 .. 6 items; 16 of 2K to 8K
-// with up to five tokens each: 78, 66, 87, 86 us with 2 .. 5, where three take two rounds once the sequences are alike.)
+// with up to five tokens each: 72, 59, 71, 73 us with 2 .. 5, and 74, 92, 85, 96 once all are as long as the bound.)
 // Candidates: one, the most items that fit in 1, 2, ... rounds, and the minimum over c of
 // (units c / slots) (set_up + nt / c) + nt / c, the work and the tail of c items per unit.
 enum class Lengths { kEven, kSpread, kMixed };

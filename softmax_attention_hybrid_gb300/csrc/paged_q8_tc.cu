@@ -24,12 +24,14 @@
 // 32 sequences of 4K to 16K tokens, 32 heads over 8 of 128 (a quarter frozen): 118 us, 6.0 TB/s, 88% of a plain copy's rate.
 // 64 sequences with a window of 1024: 41 us (512 items of 10 tiles on 456 places, and what an item costs beside its
 // tiles: counts, page, first load, softmax and product one after the other, 7 us). Five tokens each of 16 sequences, 20
-// rows: 78 us; a tile takes the four softmax warps of a CTA 4700 cycles (issue slots 34%), since its rows are all theirs.
+// rows: 71 us with two warpgroups in the softmax (78 with one); a tile takes a CTA 2700 cycles alone, two on an SM 4200
+// (issue slots 45%), and SMs with two of the longest items run the longest.
 //
-// Warps (256 threads, two CTAs per SM, three with 4 rows): 0-3 softmax, 4 loads K, V and their scales (each of its lanes
-// fetches one page of the tile), 5 owns tensor memory and issues S, 6 issues P V. (7 completes the second
-// warpgroup: from 16 rows on the softmax takes registers over from it, since what it spills costs the latency
-// of the L2 each time in the little L1 that is left.)
+// Warps (256 threads, two CTAs per SM, three with 4 rows; 384 threads from 16 rows on): a warpgroup of the softmax, from 16 rows
+// on two with half of the rows each; then a warp that loads K, V and their scales (each of its lanes fetches one page of the
+// tile), one that owns tensor memory and issues S, one that issues P V. (The last completes the
+// warpgroup: from 16 rows on the softmax takes registers over from it, since what it spills costs the latency of the L2
+// each time in the little L1 that is left.)
 // Shared memory: q's terms (K-major, 128-byte swizzle), P's terms of two tiles (MN-major: the 16 bytes of
 // a key's columns next to each other), and a ring of tiles of 128 keys with their scales, filled in the order in
 // which the MMAs use them: K0, K1, V0, K2, V1, ... (V0, V1, ... where no row is ordinary). Rows of d < 128
@@ -45,10 +47,9 @@ namespace {
 
 using namespace paged_q8;
 
-constexpr int kThreads = 256;
 // Register split (setmaxnreg) from 16 rows on, within the kRegsLaunch per thread that the launch hands out (checked on the host).
-constexpr int kRegsLaunch = 128, kRegsRows = 184, kRegsOther = 72;
-static_assert(kRegsRows + kRegsOther <= 2 * kRegsLaunch, "register split too large");
+constexpr int kRegsLaunch = 80, kRegsRows = 96, kRegsOther = 48;
+static_assert(2 * kRegsRows + kRegsOther <= 3 * kRegsLaunch, "register split too large");
 constexpr int kTile = kQ8Tile;            // keys of a tile
 constexpr int kTileBytes = kTile * 128;
 constexpr int kScaleBytes = kTile * 4;
@@ -62,9 +63,14 @@ constexpr float kWeight = 16.0f;          // 2^(8 - kSlack): a weight of the max
 
 template <int R>
 struct Cfg {
-    static constexpr int ns = R == 4 ? 16 : 2 * R;    // columns of S: hi, lo (of an MMA at least 16)
-    static constexpr int blocks = (3 * R + 15) / 16;  // 16-byte blocks of a key's weights: hi, mid, lo
-    static constexpr int np = 16 * blocks;            // columns of O
+    static constexpr int groups = R > 8 ? 2 : 1;      // warpgroups of the softmax,
+    static constexpr int rows = R / groups;           // and the rows of each
+    static constexpr int threads = 128 * groups + 128;
+    static constexpr int ns = R == 4 ? 16 : 2 * R;    // columns of S: a group's hi, lo, the next one's (of an MMA at least 16)
+    // columns of O, and bytes of a key's weights: a group's hi, mid, lo, the next one's, in 16-byte blocks
+    static constexpr int pb = groups == 1 ? (3 * R + 15) / 16 * 16 : (3 * rows + 7) / 8 * 8;
+    static constexpr int np = groups * pb;
+    static constexpr int blocks = np / 16;
     static constexpr int tile = kTile;
     static constexpr int ctas = R == 4 ? 3 : 2;       // of an SM
     static constexpr int slots = R == 4 ? 4 : R == 8 ? 6 : R == 16 ? 5 : 4;
@@ -73,7 +79,7 @@ struct Cfg {
     static constexpr int p = q + ns * 128;
     static constexpr int p_bytes = blocks * kTile * 16;
     static constexpr int scales = p + 2 * p_bytes;
-    static constexpr bool split = R > 8;
+    static constexpr bool split = groups == 2;
     static constexpr int total = scales + slots * kScaleBytes;
     static_assert(total + 4 * 1024 <= (ctas == 3 ? 76 : 114) * 1024, "CTAs of an SM");
     static constexpr uint32_t col_o = 2 * ns;         // S of two tiles, then O
@@ -100,21 +106,23 @@ struct Shared {
     int out_row[32], pos[32];      // place in o (-1: none), last visible slot of the part (-1: none)
     const float* a[32];            // frozen rows: a and r at the part's slot 0 and at the row's distance from it
     const float* r[32];
-    float part[4][32 + 1];         // the warps' maxima (and of the scales), and sums
+    float part[8][16 + 1];         // the warps' maxima (and of the scales), and sums
 };
 
-// OR over the 128 softmax threads, who all wait for each other.
-__device__ __forceinline__ bool rows_any(bool x) {
+// OR over the 128 threads of a warpgroup of the softmax, who all wait for each other.
+__device__ __forceinline__ bool rows_any(bool x, int group) {
     uint32_t y;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(y)
-        : "r"((uint32_t)x)
+        : "r"((uint32_t)x), "r"(1 + 2 * group)
         : "memory");
     return y != 0;
 }
-__device__ __forceinline__ void rows_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void rows_sync(int group) {
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + 2 * group) : "memory");
+}
 
 // Largest of a warp's values (NaN left out), by integers that have the order of the floats.
 __device__ __forceinline__ float warp_max(float x) {
@@ -124,14 +132,14 @@ __device__ __forceinline__ float warp_max(float x) {
     return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
 }
 
-// Rows of q on their way, a warp's every fourth (in: the rows' places in o).
+// Rows of q on their way, a warp's every fourth or eighth (in: the rows' places in o).
 template <int R>
 __device__ __forceinline__ void get_q(const Q8Params& P, const Work& w, int place, uint2* x) {
     const PagedArgs& p = P.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-    for (int k = 0; k < R / 4; ++k) {
-        const int r = 4 * k + warp, at = __shfl_sync(0xffffffffu, place, r);
+    for (int k = 0; k < Cfg<R>::rows / 4; ++k) {
+        const int r = 4 * Cfg<R>::groups * k + warp, at = __shfl_sync(0xffffffffu, place, r);
         x[k] = make_uint2(0, 0);
         if (r < w.there - w.nf && 4 * lane < p.d)
             x[k] = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)p.q + (size_t)at * p.d) + lane);
@@ -145,8 +153,8 @@ __device__ __forceinline__ void put_q(const Q8Params& P, const Work& w, uint8_t*
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool mine = 4 * lane < p.d;
 #pragma unroll
-    for (int k = 0; k < R / 4; ++k) {
-        const int r = 4 * k + warp;
+    for (int k = 0; k < Cfg<R>::rows / 4; ++k) {
+        const int r = 4 * Cfg<R>::groups * k + warp, place = r + r / Cfg<R>::rows * Cfg<R>::rows;   // of its hi in S
         if (r >= w.there - w.nf || sh.pos[r] < 0) continue;   // (uniform)
         const uint2 x = q[k];
         const float v[4] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
@@ -171,47 +179,69 @@ __device__ __forceinline__ void put_q(const Q8Params& P, const Work& w, uint8_t*
         uint32_t word[2] = {hi[0] | hi[1] << 16, lo[0] | lo[1] << 16};
         if (top >= 0x7f800000u) word[0] = word[1] = 0x7f7f7f7fu;   // (saturation would hide an infinity)
         if (mine) {
-            *reinterpret_cast<uint32_t*>(sm + Cfg<R>::q + sw128_offset(r, 4 * lane)) = word[0];
-            *reinterpret_cast<uint32_t*>(sm + Cfg<R>::q + sw128_offset(R + r, 4 * lane)) = word[1];
+            *reinterpret_cast<uint32_t*>(sm + Cfg<R>::q + sw128_offset(place, 4 * lane)) = word[0];
+            *reinterpret_cast<uint32_t*>(sm + Cfg<R>::q + sw128_offset(place + Cfg<R>::rows, 4 * lane)) = word[1];
         }
         if (lane == 0) sh.scale[r] = p.scale_log2 * pow2i(-e);
     }
 }
 
 // Every warp but the loading one: q's terms and tensor memory are there.
+template <int R>
 __device__ __forceinline__ void set_up_done() {
     tc_fence_before();
-    asm volatile("bar.sync 2, 192;" ::: "memory");
+    asm volatile("bar.sync 2, %0;" ::"n"(128 * Cfg<R>::groups + 64) : "memory");
     tc_fence_after();
 }
 
-template <int R>
-__device__ __forceinline__ void read_s(uint32_t addr, float* s) {   // hi + lo / 16
-    uint32_t x[2 * R];
-    if constexpr (R == 4) tmem_ld8(addr, x);
-    else if constexpr (R == 8) tmem_ld16(addr, x);
-    else tmem_ld32(addr, x);
-    if constexpr (R == 24) tmem_ld16(addr + 32, x + 32);
-    if constexpr (R == 32) tmem_ld32(addr + 32, x + 32);
+// hi + lo / 16 of N rows
+template <int N>
+__device__ __forceinline__ void read_s(uint32_t addr, float* s) {
+    uint32_t x[2 * N];
+    if constexpr (N == 4) tmem_ld8(addr, x);
+    else if constexpr (N == 16) tmem_ld32(addr, x);
+    else tmem_ld16(addr, x);
+    if constexpr (N == 12) tmem_ld8(addr + 16, x + 16);
     tmem_ld_wait();
 #pragma unroll
-    for (int r = 0; r < R; ++r) s[r] = fmaf(__uint_as_float(x[R + r]), 0.0625f, __uint_as_float(x[r]));
+    for (int r = 0; r < N; ++r) s[r] = fmaf(__uint_as_float(x[N + r]), 0.0625f, __uint_as_float(x[r]));
 }
 
-// Warps 0-3. Thread t holds key t of every tile. Loops over rows have no branches: rows behind
+// N columns of tensor memory, 8 or 16 at a time.
+template <int N>
+__device__ __forceinline__ void read_columns(uint32_t addr, uint32_t* x) {
+    if constexpr (N == 16) tmem_ld16(addr, x);
+    else tmem_ld8(addr, x);
+}
+template <int N>
+__device__ __forceinline__ void write_columns(uint32_t addr, const uint32_t* x) {
+    if constexpr (N == 16) tmem_st16(addr, x);
+    else tmem_st8(addr, x);
+}
+
+// Warps 0-3, and 4-7 from 16 rows on: a warpgroup holds R / groups of the rows. Thread t of it holds key t of every
+// tile. Loops over rows have no branches: rows behind
 // the last one have columns of their own that nobody reads.
 template <int R>
 __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, const uint2* q, uint8_t* sm, Shared& sh) {
     using C = Cfg<R>;
+    constexpr int N = C::rows;
     const PagedArgs& p = P.a;
     Bars& bars = sh.bars;
     volatile int* abort = &sh.abort_flag;
-    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const int nf = w.nf, tiles = w.e1 - w.e0;
+    const int g = C::groups == 1 ? 0 : (int)(threadIdx.x >> 7), r0 = g * N;   // my group and its first row
+    const int t = threadIdx.x & 127, warp = t >> 5, lane = t & 31;
+    const int nf = C::groups == 1 ? w.nf : g ? min(w.nf, N) : max(w.nf - N, 0), tiles = w.e1 - w.e0;
+    const float* scale_q = sh.scale + r0;
+    const float* top = sh.m + r0;
+    const int* pos = sh.pos + r0;
+    const float* const* pa = sh.a + r0;
+    const float* const* ra_ = sh.r + r0;
+    float(*part)[16 + 1] = sh.part + 4 * g;
     const int my_box = t / P.box * P.box;
-    float l[R];
+    float l[N];
 #pragma unroll
-    for (int r = 0; r < R; ++r) l[r] = 0.f;
+    for (int r = 0; r < N; ++r) l[r] = 0.f;
     float vtop = 0.f, vinv = 0.f;   // 2^V (0: no value seen yet) and 2^-V
     int vexp = 0;
     bool ok = true;
@@ -220,7 +250,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
     // rows stand at the end, the first of them last, so that registers hold them; four at a time, for a branch for each
     // row costs as much as its entries (keys past the row's own position are masked below, and what is loaded for
     // a place without a frozen row is not used).
-    constexpr int kA = R < kAhead ? R : kAhead;
+    constexpr int kA = N < kAhead ? N : kAhead;
     float fa[kA], fr[kA];
     auto ahead = [&](int j) {
         const int x = w.slot0(j, kTile) + t;
@@ -229,9 +259,9 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
             if (k0 < nf) {
 #pragma unroll
                 for (int k = k0; k < k0 + 4; ++k) {
-                    const int y = max(min(x, sh.pos[R - 1 - k]), 0);
-                    fa[k] = __ldg(sh.a[R - 1 - k] + y);
-                    fr[k] = __ldg(sh.r[R - 1 - k] - y);
+                    const int y = max(min(x, pos[N - 1 - k]), 0);
+                    fa[k] = __ldg(pa[N - 1 - k] + y);
+                    fr[k] = __ldg(ra_[N - 1 - k] - y);
                 }
             }
     };
@@ -240,13 +270,14 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
         put_q<R>(P, w, sm, sh, q);
         fence_proxy_async_smem();
     }
-    set_up_done();
+    set_up_done<R>();
     const uint32_t tmem = sh.tmem_base + ((uint32_t)(warp * 32) << 16);
 
+    constexpr int kStep = C::pb % 16 ? 8 : 16;   // columns of O at a time
     int n = 0;
     for (; n < tiles; ++n) {
         const int x0 = w.slot0(n, kTile), x = x0 + t, buf = n & 1;
-        float s[R];
+        float s[N];
         if (w.any_ord) {
             const int ld = w.k_load(n), slot = ld % C::slots;
             ok = mbar_wait(&bars.s_full[buf], (n >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
@@ -254,7 +285,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
             __syncwarp();
             tc_fence_after();
             const float ks = reinterpret_cast<const float*>(sm + C::scales + slot * kScaleBytes)[t];
-            read_s<R>(tmem + buf * C::ns, s);
+            read_s<N>(tmem + buf * C::ns + g * 2 * N, s);
             tc_fence_before();
             // Every lane's scale must be in its register before the slot is given back, and nothing here waits for that
             // otherwise: reads of shared memory that other blocks' writes hold up (masked tiles) then found the next load's
@@ -265,8 +296,8 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
                 mbar_arrive(&bars.empty[slot]);
             }
 #pragma unroll
-            for (int r = 0; r < R; r += 4) {
-                const float4 q = *reinterpret_cast<const float4*>(&sh.scale[r]);
+            for (int r = 0; r < N; r += 4) {
+                const float4 q = *reinterpret_cast<const float4*>(&scale_q[r]);
                 s[r] *= ks * q.x;
                 s[r + 1] *= ks * q.y;
                 s[r + 2] *= ks * q.z;
@@ -274,21 +305,21 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
             }
         } else {
 #pragma unroll
-            for (int r = 0; r < R; ++r) s[r] = -INFINITY;
+            for (int r = 0; r < N; ++r) s[r] = -INFINITY;
         }
         if (nf > 0) {
 #pragma unroll
-            for (int k0 = 0; k0 < R; k0 += 4)
+            for (int k0 = 0; k0 < N; k0 += 4)
                 if (k0 < nf) {
 #pragma unroll
                     for (int k = k0; k < k0 + 4; ++k) {
-                        const int r = R - 1 - k;
+                        const int r = N - 1 - k;
                         float y;
                         if (k < kA) {
                             y = fa[k < kA ? k : 0] + fr[k < kA ? k : 0];
                         } else {
-                            const int z = max(min(x, sh.pos[r]), 0);
-                            y = __ldg(sh.a[r] + z) + __ldg(sh.r[r] - z);
+                            const int z = max(min(x, pos[r]), 0);
+                            y = __ldg(pa[r] + z) + __ldg(ra_[r] - z);
                         }
                         s[r] = k < nf ? y * kLog2e : s[r];
                     }
@@ -306,13 +337,15 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
             const bool any = have && x < w.g.hi && (x >= w.g.lo || x < w.g.sink);
             const int sink = p.sinks - w.off;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int i = sh.pos[r];
-                const int lo = r >= R - nf || p.window == 0 ? -1 : i - p.window;   // slots <= lo: sinks only
+            for (int r = 0; r < N; ++r) {
+                const int i = pos[r];
+                const int lo = r >= N - nf || p.window == 0 ? -1 : i - p.window;   // slots <= lo: sinks only
                 if (!(any && x <= i && (x > lo || x < sink))) s[r] = -INFINITY;
             }
             if (!any) {   // codes and scales of slots that no row sees may be anything: zeros, for 0 * NaN is none
                 vs = 0.f;
+            }
+            if (!any && g == 0) {
                 uint4* row = reinterpret_cast<uint4*>(sm + C::ring + vslot * kTileBytes + t * 128);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
@@ -320,24 +353,24 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
         }
         float past = 0.f;   // by how much a score passes its row's maximum (a NaN does not)
 #pragma unroll
-        for (int r = 0; r < R; r += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(&sh.m[r]);
+        for (int r = 0; r < N; r += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(&top[r]);
             past = fmax3(past, s[r] - m.x, s[r + 1] - m.y);
             past = fmax3(past, s[r + 2] - m.z, s[r + 3] - m.w);
         }
-        if (rows_any(past > kSlack || vs > vtop || !ok)) {
-            if (rows_any(!ok)) break;   // every thread leaves here
+        if (rows_any(past > kSlack || vs > vtop || !ok, g)) {
+            if (rows_any(!ok, g)) break;   // every thread leaves here
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
+            for (int r = 0; r < N; ++r) {
                 const float mx = warp_max(s[r]);
-                if (lane == 0) sh.part[warp][r] = mx;
+                if (lane == 0) part[warp][r] = mx;
             }
             {
                 const float mx = warp_max(vs);
-                if (lane == 0) sh.part[warp][32] = mx;
+                if (lane == 0) part[warp][16] = mx;
             }
-            rows_sync();
-            const float vmax = fmaxf(fmaxf(sh.part[0][32], sh.part[1][32]), fmaxf(sh.part[2][32], sh.part[3][32]));
+            rows_sync(g);
+            const float vmax = fmaxf(fmaxf(part[0][16], part[1][16]), fmaxf(part[2][16], part[3][16]));
             float fv = 1.f;   // of O, for the scales
             if (vmax > vtop) {
                 int ex = (int)((__float_as_uint(vmax) >> 23) & 255u) - 126;   // vmax < 2^ex
@@ -347,27 +380,28 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
                 vtop = pow2i(ex);
                 vinv = pow2i(-ex);
             }
-            if (t < R) {
-                const float old = sh.m[t];
-                const float now = fmaxf(fmaxf(fmaxf(sh.part[0][t], sh.part[1][t]), fmaxf(sh.part[2][t], sh.part[3][t])), old);
-                sh.m[t] = now;
-                sh.fall[t] = now > old ? fast_exp2(old - now) : 1.f;
+            if (t < N) {
+                const float old = top[t];
+                const float now = fmaxf(fmaxf(fmaxf(part[0][t], part[1][t]), fmaxf(part[2][t], part[3][t])), old);
+                sh.m[r0 + t] = now;
+                sh.fall[r0 + t] = now > old ? fast_exp2(old - now) : 1.f;
             }
-            rows_sync();
+            rows_sync(g);
 #pragma unroll
-            for (int r = 0; r < R; ++r) l[r] *= sh.fall[r];
+            for (int r = 0; r < N; ++r) l[r] *= sh.fall[r0 + r];
             if (n > 0) {   // P V of the previous tile is done: O is stable
                 ok = mbar_wait(&bars.o_done[buf ^ 1], ((n - 1) >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < C::np; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(tmem + C::col_o + c, o);
+                for (int c = 0; c < C::pb; c += kStep) {
+                    uint32_t o[kStep];
+                    read_columns<kStep>(tmem + C::col_o + g * C::pb + c, o);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * (sh.fall[(c + k) % R] * fv));
-                    tmem_st16(tmem + C::col_o + c, o);
+                    for (int k = 0; k < kStep; ++k)
+                        o[k] = __float_as_uint(__uint_as_float(o[k]) * (sh.fall[r0 + (c + k) % N] * fv));
+                    write_columns<kStep>(tmem + C::col_o + g * C::pb + c, o);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -377,11 +411,11 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
             ok = mbar_wait(&bars.o_done[buf], ((n - 2) >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
         const float vw = vs * vinv * kWeight;
         uint8_t* mine = sm + C::p + buf * C::p_bytes + t * 16;
-        uint32_t word[4 * C::blocks];   // bytes: columns of the terms, hi, mid, lo
-        word[4 * C::blocks - 1] = word[4 * C::blocks - 2] = 0u;   // (what the terms leave of the last block)
+        uint32_t word[C::pb / 4];   // bytes: columns of the terms, hi, mid, lo
+        word[C::pb / 4 - 1] = word[C::pb / 4 - 2] = 0u;   // (what the terms leave)
 #pragma unroll
-        for (int r = 0; r < R; r += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(&sh.m[r]);
+        for (int r = 0; r < N; r += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(&top[r]);
             const float pr[4] = {fast_exp2(s[r] - m.x), fast_exp2(s[r + 1] - m.y), fast_exp2(s[r + 2] - m.z),
                                  fast_exp2(s[r + 3] - m.w)};
             uint32_t h[2], md[2], lo[2];
@@ -398,13 +432,24 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
                 lo[c] = pack_e4m3(16.f * (a0 - z.x), 16.f * (a1 - z.y));
             }
             word[r / 4] = h[0] | h[1] << 16;
-            word[R / 4 + r / 4] = md[0] | md[1] << 16;
-            word[R / 2 + r / 4] = lo[0] | lo[1] << 16;
+            word[N / 4 + r / 4] = md[0] | md[1] << 16;
+            word[N / 2 + r / 4] = lo[0] | lo[1] << 16;
         }
+        if constexpr (C::pb % 16 == 0) {
 #pragma unroll
-        for (int b = 0; b < C::blocks; ++b)
-            *reinterpret_cast<uint4*>(mine + b * kTile * 16) =
-                make_uint4(word[4 * b], word[4 * b + 1], word[4 * b + 2], word[4 * b + 3]);
+            for (int b = 0; b < C::pb / 16; ++b)
+                *reinterpret_cast<uint4*>(mine + (g * (C::pb / 16) + b) * kTile * 16) =
+                    make_uint4(word[4 * b], word[4 * b + 1], word[4 * b + 2], word[4 * b + 3]);
+        } else {   // the groups share a block
+            const int skip = 2 * g;   // words of mine in it: the last two of group 0, the first two of group 1
+            *reinterpret_cast<uint2*>(mine + C::pb / 16 * kTile * 16 + 8 * g) =
+                g ? make_uint2(word[0], word[1]) : make_uint2(word[C::pb / 4 - 2], word[C::pb / 4 - 1]);
+#pragma unroll
+            for (int b = 0; b < C::pb / 16; ++b)
+                *reinterpret_cast<uint4*>(mine + (g * (C::pb / 16 + 1) + b) * kTile * 16) =
+                    skip ? make_uint4(word[4 * b + 2], word[4 * b + 3], word[4 * b + 4], word[4 * b + 5])
+                         : make_uint4(word[4 * b], word[4 * b + 1], word[4 * b + 2], word[4 * b + 3]);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -417,28 +462,28 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
     __syncwarp();
     tc_fence_after();
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < N; ++r) {
         float x = l[r];
         for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0) sh.part[warp][r] = x;
+        if (lane == 0) part[warp][r] = x;
     }
-    if (rows_any(!ok)) return;
+    if (rows_any(!ok, g)) return;
     // O of element t of a row: the terms' sums
     const int split = w.it.part ? p.chunks[0] + w.it.chunk : w.it.chunk;
     const float back = pow2i(vexp - 4);   // 2^V / kWeight
-    uint32_t y[C::np];
+    uint32_t y[C::pb];
 #pragma unroll
-    for (int c = 0; c < C::np; c += 16) tmem_ld16(tmem + C::col_o + c, y + c);
+    for (int c = 0; c < C::pb; c += kStep) read_columns<kStep>(tmem + C::col_o + g * C::pb + c, y + c);
     tmem_ld_wait();
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (sh.out_row[r] < 0) continue;
-        const float o = fmaf(fmaf(__uint_as_float(y[2 * R + r]), 0.0625f, __uint_as_float(y[R + r])), 0.0625f,
+    for (int r = 0; r < N; ++r) {
+        if (sh.out_row[r0 + r] < 0) continue;
+        const float o = fmaf(fmaf(__uint_as_float(y[2 * N + r]), 0.0625f, __uint_as_float(y[N + r])), 0.0625f,
                              __uint_as_float(y[r])) * back;
-        const size_t at = (size_t)sh.out_row[r];
-        const bool sees = sh.pos[r] >= 0;
-        const float lr = sees ? (sh.part[0][r] + sh.part[1][r]) + (sh.part[2][r] + sh.part[3][r]) : 0.f;
-        const float mr = lr != 0.f ? sh.m[r] : -INFINITY;
+        const size_t at = (size_t)sh.out_row[r0 + r];
+        const bool sees = pos[r] >= 0;
+        const float lr = sees ? (part[0][r] + part[1][r]) + (part[2][r] + part[3][r]) : 0.f;
+        const float mr = lr != 0.f ? top[r] : -INFINITY;
         if (p.nsplit > 1) {
             if (t < p.d) p.po[(at * p.nsplit + split) * p.d + t] = lr != 0.f ? o : 0.f;
             if (t == 0) p.ml[at * p.nsplit + split] = make_float2(mr, lr);
@@ -449,22 +494,22 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
     }
 }
 
-// Warps 5 and 6: the MMAs.
+// The first warp behind the loading one issues S, the second P V.
 template <int R>
 __device__ __forceinline__ void issue_warps(const Q8Params& P, const Work& w, uint8_t* sm, Shared& sh) {
     using C = Cfg<R>;
     const PagedArgs& p = P.a;
     Bars& bars = sh.bars;
     volatile int* abort = &sh.abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = w.e1 - w.e0;
-    if (warp == 5) {
+    const int role = (int)(threadIdx.x >> 5) - 4 * C::groups - 1, lane = threadIdx.x & 31, n = w.e1 - w.e0;
+    if (role == 0) {
         tmem_alloc(&sh.tmem_base, C::cols);
         tmem_relinquish();
     }
-    set_up_done();
+    set_up_done<R>();
     const uint32_t tmem = sh.tmem_base;
     const uint32_t ring = smem_u32(sm + C::ring);
-    if (warp == 5) {
+    if (role == 0) {
         // S of tile j, when K is there and the rows have read S of tile j - 2
         constexpr uint32_t id_s = idesc_e4m3(128, C::ns, 0, 0);
         const uint64_t d_q = sdesc_sw128(smem_u32(sm + C::q), 16, 1024);   // K-major, as K
@@ -505,29 +550,30 @@ __device__ __forceinline__ void issue_warps(const Q8Params& P, const Work& w, ui
         }
     }
     // every MMA issued here is done before tensor memory is freed
-    mma_commit_warp(&bars.mma_idle[warp - 5]);
-    if (lane == 0) mbar_wait_bounded(&bars.mma_idle[warp - 5], 0, kWaitLimitNs);
+    mma_commit_warp(&bars.mma_idle[role]);
+    if (lane == 0) mbar_wait_bounded(&bars.mma_idle[role], 0, kWaitLimitNs);
     __syncwarp();
 }
 
 template <int R>
-__global__ void __launch_bounds__(kThreads, Cfg<R>::ctas) paged_q8_kernel(const __grid_constant__ Q8Params P) {
+__global__ void __launch_bounds__(Cfg<R>::threads, Cfg<R>::ctas) paged_q8_kernel(const __grid_constant__ Q8Params P) {
     using C = Cfg<R>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Shared sh;
     const PagedArgs& p = P.a;
+    constexpr int kRowWarps = 4 * C::groups;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     if (t == 0) {
         sh.abort_flag = sh.lost = 0;
         for (int i = 0; i < C::slots; ++i) {
             mbar_init(&sh.bars.full[i], 1);
-            mbar_init(&sh.bars.empty[i], 5);   // the MMAs, and four warps that read the scales
+            mbar_init(&sh.bars.empty[i], 1 + kRowWarps);   // the MMAs, and the warps that read the scales
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.bars.s_full[i], 1);
-            mbar_init(&sh.bars.s_empty[i], 4);
-            mbar_init(&sh.bars.p_ready[i], 4);
+            mbar_init(&sh.bars.s_empty[i], kRowWarps);
+            mbar_init(&sh.bars.p_ready[i], kRowWarps);
             mbar_init(&sh.bars.o_done[i], 1);
             mbar_init(&sh.bars.mma_idle[i], 1);
         }
@@ -547,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::ctas) paged_q8_kernel(const 
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
-    uint2 q[R / 4];
-    if (warp < 4) get_q<R>(P, w, place, q);
+    uint2 q[C::rows / 4];
+    if (warp < kRowWarps) get_q<R>(P, w, place, q);
     int i = -1;
     if (row.there) {
         int c;
@@ -578,22 +624,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::ctas) paged_q8_kernel(const 
     }
     if (w.e0 >= w.e1) {   // no keys: nothing but the rows' empty sums
         __syncthreads();
-        write_empty(p, w.it, R, sh.out_row, kThreads);
+        write_empty(p, w.it, R, sh.out_row, C::threads);
         return;
     }
     // (one setmaxnreg for each warpgroup)
-    if (warp < 4) {
+    if (warp < kRowWarps) {
         if constexpr (C::split) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
-        rows_sync();   // the rows' places
+        asm volatile("barrier.cta.sync 4, %0;" ::"n"(32 * kRowWarps) : "memory");   // the rows' places
         row_warps<R>(P, w, q, sm, sh);
     } else {
         if constexpr (C::split) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-        if (warp == 4) load_warp<C>(P, w, sm, sh);
-        else if (warp < 7) issue_warps<R>(P, w, sm, sh);
+        if (warp == kRowWarps) load_warp<C>(P, w, sm, sh);
+        else if (warp < kRowWarps + 3) issue_warps<R>(P, w, sm, sh);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == kRowWarps + 1) {
         tc_fence_after();
         tmem_dealloc(sh.tmem_base, C::cols);
     }
@@ -616,9 +662,9 @@ cudaError_t launch_r(const Q8Params& P, unsigned items, cudaStream_t s) {
             if (f != cudaSuccess) return f;
             regs.store(fa.numRegs);
         }
-        if (kRegsRows + kRegsOther > 2 * regs.load()) return cudaErrorInvalidConfiguration;
+        if (2 * kRegsRows + kRegsOther > 3 * regs.load()) return cudaErrorInvalidConfiguration;
     }
-    return launch_ex(paged_q8_kernel<R>, dim3(items), dim3(kThreads), (size_t)smem, s, true, 1, P);
+    return launch_ex(paged_q8_kernel<R>, dim3(items), dim3(Cfg<R>::threads), (size_t)smem, s, true, 1, P);
 }
 
 }  // namespace
