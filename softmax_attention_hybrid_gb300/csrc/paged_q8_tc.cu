@@ -16,7 +16,7 @@
 //     weight at the maximum.
 // Sums are fp32 in tensor memory. The scale of a key multiplies its scores, that of its value the weight.
 //
-// The running maxima m (one per row) and V (one for all) are those of the whole block: a tile whose
+// The running maxima m (one per row) and V (one for a warpgroup's rows) are those of all 128 keys: a tile whose
 // scores stay below m + 4 and whose scales stay below 2^V leaves them (one barrier with an OR); else
 // they are found anew, and O and l are scaled. Tiles are walked from the newest key to the oldest: the
 // patterns of frozen heads, and most ordinary rows, look nearby first, so that the maximum is found early.
