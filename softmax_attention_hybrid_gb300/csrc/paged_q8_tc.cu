@@ -11,13 +11,14 @@
 //   q, scaled by a power of two so that the row's largest lies in (224, 448]: hi = e4m3(q),
 //     lo = e4m3(16 (q - hi)), S = S_hi + S_lo / 16. Off by 2^-14 near zero, 2^-21 of the largest, else exact
 //     (bf16 has 8 bits, each term 4).
-//   w = P s_v 2^(4 - V) <= 256 with s_v <= 2^V the scales so far: hi = e4m3(w), mid = e4m3(16 (w - hi)),
-//     lo = e4m3(256 (w - hi - mid / 16)). Off by 2^-12 of itself (bf16: 2^-8), or 2^-18 near zero, 2^-22 of a
-//     weight at the maximum.
+//   w = P s_v 2^(4 - E) <= 256 with P s_v <= 2^E the row's products so far: hi = e4m3(w), mid = e4m3(16 (w - hi)),
+//     lo = e4m3(256 (w - hi - mid / 16)). Off by 2^-12 of itself (bf16: 2^-8), or 2^-18 near zero, 2^-21 of the
+//     row's largest. E is the row's own: with the largest scale in its place, a key with a large value would take
+//     bits from rows that do not see it, or give it no weight.
 // Sums are fp32 in tensor memory. The scale of a key multiplies its scores, that of its value the weight.
 //
-// The running maxima m (one per row) and V (one for a warpgroup's rows) are those of all 128 keys: a tile whose
-// scores stay below m + 4 and whose scales stay below 2^V leaves them (one barrier with an OR); else
+// The running maxima m of the scores and E of log2(P s_v), one each per row, are those of all 128 keys: a tile whose
+// scores stay below m + 4 and whose products stay below 2^(E + 4) leaves them (one barrier with an OR); else
 // they are found anew, and O and l are scaled. Tiles are walked from the newest key to the oldest: the
 // patterns of frozen heads, and most ordinary rows, look nearby first, so that the maximum is found early.
 //
@@ -59,7 +60,9 @@ constexpr float kSlack = 4.0f;            // scores may pass the maximum by this
 // A row that has seen no key yet: below every finite score (those of patterns are at least -2.3e38 log2(e)).
 constexpr float kNoMax = -3.4e38f;
 constexpr int kAhead = 8;                 // frozen rows whose patterns are loaded a tile ahead
-constexpr float kWeight = 16.0f;          // 2^(8 - kSlack): a weight of the maximum, before the value's scale
+constexpr int kWeightExp = 4;              // 8 - kSlack: a weight times its value's scale at the maximum is 2^4
+// Bounds of E: 2^(4 - E) is a float, and no product of a weight below 2^4 and a finite scale is 2^128 or more.
+constexpr int kLeastExp = -123, kMostExp = 128;
 
 template <int R>
 struct Cfg {
@@ -94,19 +97,24 @@ struct Bars {
     uint64_t s_full[2], s_empty[2], p_ready[2], o_done[2], mma_idle[2];
 };
 
+template <int R>
 struct Shared {
     Bars bars;
     uint32_t tmem_base;
     int abort_flag;
     int lost;                      // a page that the item needs is not in the cache (set before its tile is there)
     // rows of the block: ordinary ones from the front, frozen ones from the back
-    alignas(16) float scale[32];   // what a score times its key's scale is multiplied by: log2(e) / sqrt(d), and q's factor back
-    alignas(16) float m[32];       // running maxima
-    alignas(16) float fall[32];    // 2^(old maximum - new one)
-    int out_row[32], pos[32];      // place in o (-1: none), last visible slot of the part (-1: none)
-    const float* a[32];            // frozen rows: a and r at the part's slot 0 and at the row's distance from it
-    const float* r[32];
-    float part[8][16 + 1];         // the warps' maxima (and of the scales), and sums
+    alignas(16) float scale[R];    // what a score times its key's scale is multiplied by: log2(e) / sqrt(d), and q's factor back
+    alignas(16) float nm[R];       // running maxima, negated
+    alignas(16) float nlim[R];     // E, negated
+    alignas(16) float gain[R];     // 2^(4 - E)
+    alignas(16) float fall[R];     // 2^(old maximum - new one)
+    alignas(16) float fall_o[R];   // the same of O, whose unit is 2^(m + E - 4)
+    float most[R];                 // log2 of the largest product of a weight and its value's scale
+    int out_row[R], pos[R];        // place in o (-1: none), last visible slot of the part (-1: none)
+    const float* a[R];             // frozen rows: a and r at the part's slot 0 and at the row's distance from it
+    const float* r[R];
+    float part[4 * Cfg<R>::groups][Cfg<R>::rows];   // the warps' maxima, and sums
 };
 
 // OR over the 128 threads of a warpgroup of the softmax, who all wait for each other.
@@ -122,6 +130,12 @@ __device__ __forceinline__ bool rows_any(bool x, int group) {
 }
 __device__ __forceinline__ void rows_sync(int group) {
     asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + 2 * group) : "memory");
+}
+
+__device__ __forceinline__ float log2_of(float x) {   // to 2^-22, or a step of it
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // Largest of a warp's values (NaN left out), by integers that have the order of the floats.
@@ -148,7 +162,7 @@ __device__ __forceinline__ void get_q(const Q8Params& P, const Work& w, int plac
 
 // q's terms of the block's ordinary rows, and the rows' factors.
 template <int R>
-__device__ __forceinline__ void put_q(const Q8Params& P, const Work& w, uint8_t* sm, Shared& sh, const uint2* q) {
+__device__ __forceinline__ void put_q(const Q8Params& P, const Work& w, uint8_t* sm, Shared<R>& sh, const uint2* q) {
     const PagedArgs& p = P.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool mine = 4 * lane < p.d;
@@ -223,7 +237,7 @@ __device__ __forceinline__ void write_columns(uint32_t addr, const uint32_t* x) 
 // tile. Loops over rows have no branches: rows behind
 // the last one have columns of their own that nobody reads.
 template <int R>
-__device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, const uint2* q, uint8_t* sm, Shared& sh) {
+__device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, const uint2* q, uint8_t* sm, Shared<R>& sh) {
     using C = Cfg<R>;
     constexpr int N = C::rows;
     const PagedArgs& p = P.a;
@@ -233,17 +247,17 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
     const int t = threadIdx.x & 127, warp = t >> 5, lane = t & 31;
     const int nf = C::groups == 1 ? w.nf : g ? min(w.nf, N) : max(w.nf - N, 0), tiles = w.e1 - w.e0;
     const float* scale_q = sh.scale + r0;
-    const float* top = sh.m + r0;
+    const float* nm = sh.nm + r0;
+    const float* nlim = sh.nlim + r0;
+    const float* gain = sh.gain + r0;
     const int* pos = sh.pos + r0;
     const float* const* pa = sh.a + r0;
     const float* const* ra_ = sh.r + r0;
-    float(*part)[16 + 1] = sh.part + 4 * g;
+    float(*part)[N] = sh.part + 4 * g;
     const int my_box = t / P.box * P.box;
     float l[N];
 #pragma unroll
     for (int r = 0; r < N; ++r) l[r] = 0.f;
-    float vtop = 0.f, vinv = 0.f;   // 2^V (0: no value seen yet) and 2^-V
-    int vexp = 0;
     bool ok = true;
 
     // The fixed patterns' entries (Eq. 3) of my key, a tile ahead: neighbouring keys, neighbouring entries. Frozen
@@ -351,40 +365,55 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
                 for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
             }
         }
-        float past = 0.f;   // by how much a score passes its row's maximum (a NaN does not)
+        // by how much a score passes its row's maximum, or its product with the value's scale the limit (a NaN does not)
+        float past = 0.f;
+        const float lv = log2_of(vs);
 #pragma unroll
         for (int r = 0; r < N; r += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(&top[r]);
-            past = fmax3(past, s[r] - m.x, s[r + 1] - m.y);
-            past = fmax3(past, s[r + 2] - m.z, s[r + 3] - m.w);
+            const float4 m = *reinterpret_cast<const float4*>(&nm[r]), e = *reinterpret_cast<const float4*>(&nlim[r]);
+            const float2 d0 = fadd2(make_float2(s[r], s[r + 1]), make_float2(m.x, m.y));
+            const float2 d1 = fadd2(make_float2(s[r + 2], s[r + 3]), make_float2(m.z, m.w));
+            const float2 u0 = fadd2(d0, fadd2(make_float2(lv, lv), make_float2(e.x, e.y)));
+            const float2 u1 = fadd2(d1, fadd2(make_float2(lv, lv), make_float2(e.z, e.w)));
+            past = fmax3(past, d0.x, d0.y);
+            past = fmax3(past, d1.x, d1.y);
+            past = fmax3(past, u0.x, u0.y);
+            past = fmax3(past, u1.x, u1.y);
         }
-        if (rows_any(past > kSlack || vs > vtop || !ok, g)) {
+        if (rows_any(past > kSlack || !ok, g)) {
             if (rows_any(!ok, g)) break;   // every thread leaves here
 #pragma unroll
             for (int r = 0; r < N; ++r) {
                 const float mx = warp_max(s[r]);
                 if (lane == 0) part[warp][r] = mx;
             }
-            {
-                const float mx = warp_max(vs);
-                if (lane == 0) part[warp][16] = mx;
+            rows_sync(g);
+            float rise = 0.f;   // of my row's maximum
+            if (t < N) {
+                const float old = -nm[t];
+                const float now = fmaxf(fmaxf(fmaxf(part[0][t], part[1][t]), fmaxf(part[2][t], part[3][t])), old);
+                rise = now > old ? now - old : 0.f;
+                sh.nm[r0 + t] = -now;
+                sh.fall[r0 + t] = fast_exp2(-rise);
             }
             rows_sync(g);
-            const float vmax = fmaxf(fmaxf(part[0][16], part[1][16]), fmaxf(part[2][16], part[3][16]));
-            float fv = 1.f;   // of O, for the scales
-            if (vmax > vtop) {
-                int ex = (int)((__float_as_uint(vmax) >> 23) & 255u) - 126;   // vmax < 2^ex
-                ex = ex < -125 ? -125 : ex > 127 ? 127 : ex;
-                fv = vtop > 0.f ? exp2f((float)(vexp - ex)) : 0.f;
-                vexp = ex;
-                vtop = pow2i(ex);
-                vinv = pow2i(-ex);
+            // (after the maximum was taken off: beside a large score the scale's part would be rounded away)
+#pragma unroll
+            for (int r = 0; r < N; ++r) {
+                const float mx = warp_max((s[r] + nm[r]) + lv);
+                if (lane == 0) part[warp][r] = mx;
             }
+            rows_sync(g);
             if (t < N) {
-                const float old = top[t];
-                const float now = fmaxf(fmaxf(fmaxf(part[0][t], part[1][t]), fmaxf(part[2][t], part[3][t])), old);
-                sh.m[r0 + t] = now;
-                sh.fall[r0 + t] = now > old ? fast_exp2(old - now) : 1.f;
+                const float most = fmaxf(fmaxf(fmaxf(part[0][t], part[1][t]), fmaxf(part[2][t], part[3][t])),
+                                         sh.most[r0 + t] - rise);
+                const float e = fminf(fmaxf(ceilf(most), (float)kLeastExp), (float)kMostExp);
+                // 2^(E - rise - new E), whole powers apart from the rest: the sum of both would round the rest
+                const float whole = rintf(rise), n2 = -nlim[t] - whole - e;
+                sh.fall_o[r0 + t] = n2 < -149.f ? 0.f : exp2f(whole - rise) * pow2i((int)n2);
+                sh.most[r0 + t] = most;
+                sh.nlim[r0 + t] = -e;
+                sh.gain[r0 + t] = pow2i(kWeightExp - (int)e);
             }
             rows_sync(g);
 #pragma unroll
@@ -400,7 +429,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
                     tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < kStep; ++k)
-                        o[k] = __float_as_uint(__uint_as_float(o[k]) * (sh.fall[r0 + (c + k) % N] * fv));
+                        o[k] = __float_as_uint(__uint_as_float(o[k]) * sh.fall_o[r0 + (c + k) % N]);
                     write_columns<kStep>(tmem + C::col_o + g * C::pb + c, o);
                 }
                 tmem_st_wait();
@@ -409,21 +438,24 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
         }
         if (n > 1)   // P V of the tile before the previous one is done: its weights' buffer is free
             ok = mbar_wait(&bars.o_done[buf], ((n - 2) >> 1) & 1, abort, p.status, kStatusTimeout) && ok;
-        const float vw = vs * vinv * kWeight;
         uint8_t* mine = sm + C::p + buf * C::p_bytes + t * 16;
         uint32_t word[C::pb / 4];   // bytes: columns of the terms, hi, mid, lo
         word[C::pb / 4 - 1] = word[C::pb / 4 - 2] = 0u;   // (what the terms leave)
 #pragma unroll
         for (int r = 0; r < N; r += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(&top[r]);
-            const float pr[4] = {fast_exp2(s[r] - m.x), fast_exp2(s[r + 1] - m.y), fast_exp2(s[r + 2] - m.z),
-                                 fast_exp2(s[r + 3] - m.w)};
+            const float4 m = *reinterpret_cast<const float4*>(&nm[r]), e = *reinterpret_cast<const float4*>(&gain[r]);
+            const float2 d[2] = {fadd2(make_float2(s[r], s[r + 1]), make_float2(m.x, m.y)),
+                                 fadd2(make_float2(s[r + 2], s[r + 3]), make_float2(m.z, m.w))};
+            const float2 up[2] = {make_float2(e.x, e.y), make_float2(e.z, e.w)};
             uint32_t h[2], md[2], lo[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                l[r + 2 * c] += pr[2 * c];
-                l[r + 2 * c + 1] += pr[2 * c + 1];
-                const float y0 = pr[2 * c] * vw, y1 = pr[2 * c + 1] * vw;
+                const float2 pr = make_float2(fast_exp2(d[c].x), fast_exp2(d[c].y));
+                l[r + 2 * c] += pr.x;
+                l[r + 2 * c + 1] += pr.y;
+                // (the gain last: a weight of 0 times a large scale stays 0, for any gain)
+                const float2 w2 = fmul2(fmul2(pr, make_float2(vs, vs)), up[c]);
+                const float y0 = w2.x, y1 = w2.y;
                 h[c] = pack_e4m3(y0, y1);
                 float2 z = unpack_e4m3(h[c]);
                 const float a0 = 16.f * (y0 - z.x), a1 = 16.f * (y1 - z.y);
@@ -470,7 +502,6 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
     if (rows_any(!ok, g)) return;
     // O of element t of a row: the terms' sums
     const int split = w.it.part ? p.chunks[0] + w.it.chunk : w.it.chunk;
-    const float back = pow2i(vexp - 4);   // 2^V / kWeight
     uint32_t y[C::pb];
 #pragma unroll
     for (int c = 0; c < C::pb; c += kStep) read_columns<kStep>(tmem + C::col_o + g * C::pb + c, y + c);
@@ -479,11 +510,11 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
     for (int r = 0; r < N; ++r) {
         if (sh.out_row[r0 + r] < 0) continue;
         const float o = fmaf(fmaf(__uint_as_float(y[2 * N + r]), 0.0625f, __uint_as_float(y[N + r])), 0.0625f,
-                             __uint_as_float(y[r])) * back;
+                             __uint_as_float(y[r])) * pow2i(-(int)nlim[r] - kWeightExp);
         const size_t at = (size_t)sh.out_row[r0 + r];
         const bool sees = pos[r] >= 0;
         const float lr = sees ? (part[0][r] + part[1][r]) + (part[2][r] + part[3][r]) : 0.f;
-        const float mr = lr != 0.f ? top[r] : -INFINITY;
+        const float mr = lr != 0.f ? -nm[r] : -INFINITY;
         if (p.nsplit > 1) {
             if (t < p.d) p.po[(at * p.nsplit + split) * p.d + t] = lr != 0.f ? o : 0.f;
             if (t == 0) p.ml[at * p.nsplit + split] = make_float2(mr, lr);
@@ -496,7 +527,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
 
 // The first warp behind the loading one issues S, the second P V.
 template <int R>
-__device__ __forceinline__ void issue_warps(const Q8Params& P, const Work& w, uint8_t* sm, Shared& sh) {
+__device__ __forceinline__ void issue_warps(const Q8Params& P, const Work& w, uint8_t* sm, Shared<R>& sh) {
     using C = Cfg<R>;
     const PagedArgs& p = P.a;
     Bars& bars = sh.bars;
@@ -560,7 +591,7 @@ __global__ void __launch_bounds__(Cfg<R>::threads, Cfg<R>::ctas) paged_q8_kernel
     using C = Cfg<R>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ Shared sh;
+    __shared__ Shared<R> sh;
     const PagedArgs& p = P.a;
     constexpr int kRowWarps = 4 * C::groups;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -617,7 +648,10 @@ __global__ void __launch_bounds__(Cfg<R>::threads, Cfg<R>::ctas) paged_q8_kernel
         sh.out_row[slot] = place;
         sh.pos[slot] = i < 0 ? -1 : i - w.off;
         // (rows that see nothing, whose columns of S may hold anything: no score passes their maximum)
-        sh.m[slot] = i < 0 ? INFINITY : kNoMax;
+        sh.nm[slot] = i < 0 ? -INFINITY : -kNoMax;
+        sh.nlim[slot] = (float)-kLeastExp;
+        sh.gain[slot] = pow2i(kWeightExp - kLeastExp);
+        sh.most[slot] = -INFINITY;
         sh.scale[slot] = 0.f;
         sh.a[slot] = p.a + (size_t)row.h * p.ld + w.off;
         sh.r[slot] = p.r + (size_t)row.h * p.ld + (i < 0 ? 0 : i - w.off);
