@@ -394,7 +394,8 @@ SAF_API int saf_attn_paged_shared(const void* q, const void* k_cache, const void
  *
  * saf_attn_paged_quant and saf_attn_paged_shared_quant are saf_attn_paged and saf_attn_paged_shared
  * over such caches: every rule above holds, with code_c * scale for the cache's values. Scales that
- * a row sees must be finite and not negative; those of slots that no row sees may be anything, as
+ * a row sees must be finite and not negative (an infinite one of a value, which stands for a row of
+ * NaN, makes NaN of the outputs that see it); those of slots that no row sees may be anything, as
  * the codes. The workspace is that of saf_attn_paged_quant_workspace_bytes. */
 SAF_API int saf_kv_append_quant(const void* q, const void* k, const void* v, const int64_t* strides,
                                const int32_t* ctx, const int32_t* n_new, const int32_t* page_table, int max_pages,

@@ -365,6 +365,8 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const Work& w, cons
                 for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
             }
         }
+        // (an infinite scale stands for rows of NaN; as a term of e4m3 the weight would saturate)
+        if (!(vs <= 3.402823466e38f)) vs = __int_as_float(0x7fffffff);
         // by how much a score passes its row's maximum, or its product with the value's scale the limit (a NaN does not)
         float past = 0.f;
         const float lv = log2_of(vs);

@@ -13,7 +13,7 @@ import torch
 
 from oracle import serving_oracle as so
 from tests import _bounds
-from tests.test_quant_gpu import SOME, Batch, _np, saf  # noqa: F401  (saf: the fixture)
+from tests.test_quant_gpu import DT, E4M3, SOME, Batch, _np, saf  # noqa: F401  (saf: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +116,25 @@ def test_value_scales_over_many_powers_of_two(saf, dtype, d, T, order):  # noqa:
             p = 120 * at // n - 60
             _scale_value(x, b, at, 2.0 ** (p if order == "rising" else -p if order == "falling" else at * 37 % 121 - 60))
     _check(x, *x.call(saf, frozen), frozen)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [1, 5, 40])
+def test_an_infinity_that_was_appended(saf, dtype, T):  # noqa: F811
+    # its row of values stands for NaN, and so does every output that sees it
+    H, Hkv, d, page = 4, 2, 64, 16
+    g = torch.Generator().manual_seed(51)
+    dt = DT[dtype]
+    n = 100 + T
+    k, v = (torch.randn(1, Hkv, n, d, generator=g).to(dt).cuda() for _ in range(2))
+    v[0, 1, 60, 7] = float("inf")
+    per = -(-n // page)
+    cache = [torch.zeros(per, Hkv, page, d, dtype=torch.uint8, device="cuda").view(E4M3) for _ in range(2)]
+    cache += [torch.zeros(per, Hkv, page, device="cuda") for _ in range(2)]
+    table = torch.arange(per, dtype=torch.int32, device="cuda")[None]
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    saf.saf_kv_append_quant(k, v, *cache, table, zero)
+    q = torch.randn(1, H, T, d, generator=g).to(dt).cuda()
+    o, lse = saf.saf_attn_paged_quant(q, *cache, table, zero + 100, n)
+    assert o[:, 2:].isnan().all()
+    assert torch.isfinite(o[:, :2].float()).all() and torch.isfinite(lse).all()
