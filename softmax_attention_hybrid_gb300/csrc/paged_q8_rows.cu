@@ -290,7 +290,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
     // my staged pattern: a of the tile's keys, and r from the far end on (entry k - c for key c)
     const float* pat_a = reinterpret_cast<const float*>(sm + C::pat) + (frozen ? row.gi - w.fz0 : 0) * w.pitch();
     const float* pat_r = pat_a + TK + (TK - 1) + (frozen ? row.i - w.imin + w.shift(p, row.h) : 0);
-    float m = -INFINITY, l = 0.f;   // (l: times 2^kWeightExp)
+    float m = -INFINITY, l = 0.f;   // (m: before the factor sc; l: times 2^kWeightExp)
     int vexp = kNoExp;
     bool ok = true;
 
@@ -375,11 +375,12 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.pat_empty[buf]);
         }
-        const float m_new = fmaxf(m, fmaxf(ma, mb) * sc);
+        // (a score that the factor makes -infinity is none)
+        const float most = fmaxf(ma, mb), m_new = most * sc > -INFINITY ? fmaxf(m, most) : m;
         float f = 1.f;   // of O
-        bool need = m_new > m + kRescaleThreshold;
+        bool need = (m_new - m) * sc > kRescaleThreshold;
         if (need) {
-            f = fast_exp2(m - m_new);
+            f = fast_exp2((m - m_new) * sc);
             l *= f;
             m = m_new;
         }
@@ -402,7 +403,9 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
             }
         }
         const float ref = m == -INFINITY ? 0.f : m;   // a row that has seen no key yet: weights 2^-inf = 0
-        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(kWeightExp - ref, kWeightExp - ref);
+        // The maximum is taken off before the factor: sc s - sc m in one step would leave the rounding of sc m,
+        // which is no longer small beside scores of 2^24 and more.
+        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-ref, -ref), up2 = make_float2(kWeightExp, kWeightExp);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int c0 = 0; c0 < TK; c0 += 32) {
@@ -411,7 +414,8 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
             uint32_t pk[16];
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-                const float2 x = ffma2(make_float2(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), sc2, nm2);
+                const float2 y = fadd2(make_float2(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])), nm2);
+                const float2 x = ffma2(y, sc2, up2);
                 const float2 ex = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                 if (c & 1) acc1 = fadd2(acc1, ex);
                 else acc0 = fadd2(acc0, ex);
@@ -431,6 +435,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
     // my row
     l *= pow2i(-kWeightExp);
     const bool sees = row.i >= 0 && l != 0.f;   // (a NaN sum is one)
+    m *= sc;
     const int split = w.it.part ? p.chunks[0] + w.it.chunk : w.it.chunk;
     const float back = vexp == kNoExp ? 0.f : pow2i(vexp - 2 * kWeightExp);
     const float mul = p.nsplit > 1 ? back : back * (1.f / l);
