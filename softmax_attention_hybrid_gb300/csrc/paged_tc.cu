@@ -255,6 +255,7 @@ __device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, cons
     const float* pat_a = reinterpret_cast<const float*>(sm + S::pat) + (frozen ? row.gi - w.f0 : 0) * w.pitch(TK) + c0;
     const float* pat_r = pat_a + TK - 2 * c0 + (TK - 1) + (frozen ? row.i - w.imin : 0);
     float m = -INFINITY, l = 0.f;
+    float m_raw = 0.f;   // the score that m is, before the factor sc
     bool ok = true;
 
     if (kCopies > 1) {   // the other copies' keys: weights that stay zero
@@ -328,15 +329,24 @@ __device__ __forceinline__ void row_warps(const TcParams& P, const Work& w, cons
             ma = fmax3(ma, __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
             mb = fmax3(mb, __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
         }
-        const float m_new = fmaxf(m, fmaxf(ma, mb) * sc);
+        const float most = fmaxf(ma, mb), m_new = fmaxf(m, most * sc);
         const bool need = m_new > m + kRescaleThreshold;
         const float f = need ? fast_exp2(m - m_new) : 1.f;
         if (need) {
             l *= f;
             m = m_new;
+            m_raw = most;
         }
         const float ref = m == -INFINITY ? 0.f : m;   // a row that has seen no key yet: weights 2^-inf = 0
-        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-ref, -ref);
+        float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-ref, -ref);
+        // sc s - m in one step leaves the rounding of m, which is no longer small beside scores past 2^20: the
+        // maximum is then taken off before the factor.
+        if (fabsf(ref) > 1048576.f) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) sv[c] = __float_as_uint((__uint_as_float(sv[c]) - m_raw) * sc);
+            sc2 = make_float2(1.f, 1.f);
+            nm2 = make_float2(0.f, 0.f);
+        }
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
         // The weights are rounded to bf16 for P V (both operands of an MMA have V's type): o is off by up
         // to 2^-8 of sum_j P_j |v_j|. l adds them unrounded, which lse and the joins of items need.

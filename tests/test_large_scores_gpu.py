@@ -15,7 +15,7 @@ from tests.test_quant_gpu import _np, saf  # noqa: F401  (saf: the fixture)
 
 pytestmark = pytest.mark.gpu
 
-KINDS = ["8-bit"]
+KINDS = ["8-bit", "paged"]
 
 
 def _batch(kind, dtype, T, seed):
