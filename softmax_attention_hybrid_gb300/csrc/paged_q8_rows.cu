@@ -7,8 +7,10 @@
 //     its largest lies in (224, 448], as hi = e4m3(q) and lo = e4m3(q - hi), two products into one sum.
 //     What they leave is at most 2^-10, 2^-17 of the row's largest.
 //   O += P V in fp16 (kind::f16). Four warps turn a tile of V into code s_v 2^(7 - V) <= 57344, once for all
-//     rows, with s_v <= 2^V the scales so far (the scale and the product are rounded: 2^-11); the weight is
-//     2^7 of itself in fp16, at most 2^15 (2^-12, or 2^-32 of a weight at the maximum).
+//     rows, with s_v <= 2^V the tile's scales (the scale and the product are rounded: 2^-11); the weight is
+//     P 2^(7 + V - E) in fp16, at most 2^15, with E the row's own bound of log2(P s_v) so far (off by 2^-12, or 2^-23
+//     of the row's largest). A tile whose scales lie further apart than 2^8 gives each key its own V, which its weights
+//     then take up one by one: with one V for all, keys with large values, seen or not, took the others' bits.
 // The key's scale multiplies the scores. Sums are fp32 in tensor memory, l adds the weights unrounded.
 //
 // A group's S and P share their columns of tensor memory, so that its S, softmax and P V follow one
@@ -49,7 +51,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;   // lazy rescale: factor 256
 constexpr int kWeightExp = 7;               // a weight of the maximum is 2^7; values of the largest scale are 2^7 codes
-constexpr int kNoExp = -1000;               // no scale seen yet
+constexpr int kEvenRange = 8;               // scales of a tile that share one V: within 2^8
+constexpr int kNoExp = -1000;               // no scale but zeros
+constexpr int kLeastV = -110, kMostV = 128; // 2^(7 - V) is a float
+constexpr int kLeastExp = -112, kMostExp = 130;   // of E: 2^(E - 14) is a float
+constexpr int kLeastShift = -60;        // weights of a tile whose values are nothing beside the row's: for the sums' sake
 constexpr int kPatFloats = 2560;            // room for the frozen heads' patterns of a tile
 
 // kD: columns of O as the tiles hold them (64, or 128 for 96 and 128).
@@ -83,7 +89,8 @@ struct Shared {
     uint32_t tmem_base;
     int abort_flag, imin, imax, kinds, frozen_warps, lost;
     alignas(16) float ks[2][TK];   // scales of a tile's keys
-    int vexp[2];                   // V
+    alignas(16) float ve[2][TK];   // of an uneven tile: a key's V less the tile's
+    int vexp[2], even[2];          // V; whether all keys share it
     int out_row[256], q_row[256];  // the rows' places in o, and in q where they are ordinary; -1: none
     float q_scale[256];            // what a score times its key's scale is multiplied by
     alignas(16) int length[kMostOrdered];
@@ -178,8 +185,6 @@ __device__ __forceinline__ void unpack_warps(const Q8Params& P, const RowsWork& 
     volatile int* abort = &sh.abort_flag;
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int n = w.e1 - w.e0;
-    float vtop = 0.f;   // 2^V, 0: no value seen yet
-    int vexp = 0;
     for (int j = 0; j < n; ++j) {
         const int buf = j & 1, x0 = w.slot0(j, TK);
         // P V of tile j - 2 is done: its scales are read, its values free
@@ -201,6 +206,7 @@ __device__ __forceinline__ void unpack_warps(const Q8Params& P, const RowsWork& 
         float v[TK / 32];        // of keys lane, lane + 32, ...
         uint32_t seen[TK / 32];
         float top = 0.f;
+        uint32_t low = 0x7f800000u;   // smallest scale of a key that some row sees
 #pragma unroll
         for (int k = 0; k < TK / 32; ++k) {
             v[k] = vs[32 * k + lane];
@@ -212,22 +218,30 @@ __device__ __forceinline__ void unpack_warps(const Q8Params& P, const RowsWork& 
                 if (!a) v[k] = 0.f;
             }
             top = fmaxf(top, v[k]);
+            if ((seen[k] >> lane) & 1u) low = min(low, __float_as_uint(v[k]));
         }
         // (scales are not negative: their bits have their order)
         top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-        if (top > vtop) {
-            const int ex = (int)((__float_as_uint(top) >> 23) & 255u) - 126;   // top < 2^ex
-            vexp = ex < -110 ? -110 : ex > 127 ? 127 : ex;
-            vtop = pow2i(vexp);
-        }
+        low = __reduce_min_sync(0xffffffffu, low);
+        auto exponent = [](float x) {   // x < 2^exponent
+            const int e = (int)((__float_as_uint(x) >> 23) & 255u) - 126;
+            return e < kLeastV ? kLeastV : e > kMostV ? kMostV : e;
+        };
+        const int vexp = exponent(top);
+        const bool even = top == 0.f || exponent(__uint_as_float(low)) >= vexp - kEvenRange;
         if (warp == 0) {
+            if (!even)   // (a value of scale zero has no part in what is the row's largest)
+#pragma unroll
+                for (int k = 0; k < TK / 32; ++k)
+                    sh.ve[buf][32 * k + lane] = v[k] == 0.f ? (float)kNoExp : (float)(exponent(v[k]) - vexp);
+            __syncwarp();
             if (lane == 0) {
-                sh.vexp[buf] = vtop > 0.f ? vexp : kNoExp;
-                mbar_arrive(&bars.sc_ready[buf]);   // (behind the other lanes' scales: the warp met since)
+                sh.vexp[buf] = top > 0.f ? vexp : kNoExp;
+                sh.even[buf] = even;
+                mbar_arrive(&bars.sc_ready[buf]);   // (behind the other lanes' scales)
             }
             __syncwarp();
         }
-        const float f = pow2i(kWeightExp - vexp);
         // A warp takes a quarter of the keys; lane: 16 codes of a key.
         const uint8_t* src = sm + C::ring + s * TK * 128;
         uint8_t* dst = sm + C::v16 + buf * C::v16_tile;
@@ -235,13 +249,14 @@ __device__ __forceinline__ void unpack_warps(const Q8Params& P, const RowsWork& 
         constexpr int kKeys = 32 / kChunks;         // keys at a time
         const int c = lane % kChunks;
         static_assert(TK == 128, "a warp takes the keys whose scales lie in v[warp]");
-        const float mine = warp == 0 ? v[0] : warp == 1 ? v[1] : warp == 2 ? v[2] : v[3];
+        float mine = warp == 0 ? v[0] : warp == 1 ? v[1] : warp == 2 ? v[2] : v[3];
+        mine *= pow2i(kWeightExp - (even ? vexp : exponent(mine)));
         const uint32_t here = warp == 0 ? seen[0] : warp == 1 ? seen[1] : warp == 2 ? seen[2] : seen[3];
 #pragma unroll
         for (int k0 = 0; k0 < 32; k0 += kKeys) {
             const int in = k0 + lane / kChunks, key = 32 * warp + in;
             uint4 x = *reinterpret_cast<const uint4*>(src + sw128_offset(key, 16 * c));
-            const float sv = __shfl_sync(0xffffffffu, mine, in) * f;
+            const float sv = __shfl_sync(0xffffffffu, mine, in);
             const uint32_t s2 = pack_f16(sv, sv);
             if (!((here >> in) & 1u)) x = make_uint4(0, 0, 0, 0);
             const uint4 a = make_uint4(hmul2(codes_f16(x.x), s2), hmul2(codes_f16(x.x >> 16), s2),
@@ -271,6 +286,29 @@ __device__ __forceinline__ uint32_t below(int end, int first) {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
+// An uneven tile's scores s become (s - m) sc + the key's V less the tile's. Returns the largest of them, and the sum of
+// the weights without the V's, times 2^kWeightExp. (Not inline: as a part of the loop it costs the chunk of 512 tokens
+// 318 us in place of 301, without a single uneven tile.)
+__device__ __noinline__ float2 uneven_scores(uint32_t tmem, float ref, float sc, const float* ve) {
+    float cand = -INFINITY, l = 0.f;
+    uint32_t sv[8];
+#pragma unroll 1
+    for (int c0 = 0; c0 < TK; c0 += 8) {
+        tmem_ld8(tmem + c0, sv);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const float z = (__uint_as_float(sv[c]) - ref) * sc, y = z + ve[c0 + c];
+            l += fast_exp2(z + kWeightExp);
+            cand = fmaxf(cand, y);
+            sv[c] = __float_as_uint(y);
+        }
+        tmem_st8(tmem + c0, sv);
+    }
+    tmem_st_wait();
+    return make_float2(cand, l);
+}
+
 // Warps 0-7 of a group that has rows: thread = row.
 template <int kD>
 __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, const PagedRow& row, uint8_t* sm,
@@ -291,7 +329,8 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
     const float* pat_a = reinterpret_cast<const float*>(sm + C::pat) + (frozen ? row.gi - w.fz0 : 0) * w.pitch();
     const float* pat_r = pat_a + TK + (TK - 1) + (frozen ? row.i - w.imin + w.shift(p, row.h) : 0);
     float m = -INFINITY, l = 0.f;   // (m: before the factor sc; l: times 2^kWeightExp)
-    int vexp = kNoExp;
+    int lim = kLeastExp;            // E
+    float largest = -INFINITY;      // log2 of the largest product of a weight and its value's scale
     bool ok = true;
 
     const int tiles = w.e1 - w.e0;
@@ -377,21 +416,36 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
         }
         // (a score that the factor makes -infinity is none)
         const float most = fmaxf(ma, mb), m_new = most * sc > -INFINITY ? fmaxf(m, most) : m;
-        float f = 1.f;   // of O
-        bool need = (m_new - m) * sc > kRescaleThreshold;
-        if (need) {
-            f = fast_exp2((m - m_new) * sc);
-            l *= f;
+        float rise = 0.f;   // of the maximum, in powers of two
+        if ((m_new - m) * sc > kRescaleThreshold) {
+            rise = (m_new - m) * sc;
+            l *= fast_exp2(-rise);
             m = m_new;
         }
-        const int now = sh.vexp[buf];   // (the same for every row)
-        if (now != vexp) {
-            f *= vexp == kNoExp ? 0.f : exp2f((float)(vexp - now));
-            vexp = now;
-            need = true;
-        }
+        const float ref = m == -INFINITY ? 0.f : m;   // a row that has seen no key yet: weights 2^-inf = 0
+        const int vexp = sh.vexp[buf];   // (the same for every row)
+        const bool even = sh.even[buf] != 0;
         tmem_st_wait();
         if (n == 0 && t == 0) mbar_arrive(&bars.first);
+        // The largest product of a weight and its value's scale, as a power of two: in an even tile at most its
+        // largest weight with its V.
+        float cand = (most - ref) * sc, uneven_l = 0.f;
+        if (!even) {
+            const float2 x = uneven_scores(tmem, ref, sc, sh.ve[buf]);
+            cand = x.x;
+            uneven_l = x.y;
+        }
+        cand = vexp == kNoExp ? -INFINITY : cand + (float)vexp;
+        float f = 1.f;   // of O, whose unit is 2^(m + E - 14)
+        const bool need = rise > 0.f || cand > (float)lim + kRescaleThreshold;
+        if (need) {
+            largest = fmaxf(largest - rise, cand);
+            const int e = (int)fminf(fmaxf(ceilf(largest), (float)kLeastExp), (float)kMostExp);
+            // whole powers apart from the rest: the sum of both would round the rest
+            const float whole = rintf(rise), n2 = (float)(lim - e) - whole;
+            f = n2 < -149.f ? 0.f : exp2f(whole - rise) * pow2i((int)n2);
+            lim = e;
+        }
         if (n > 0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll 1
             for (int q = 0; q < kD; q += 32) {
@@ -402,10 +456,13 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
                 tmem_st32(tmem + C::col_o + q, sv);
             }
         }
-        const float ref = m == -INFINITY ? 0.f : m;   // a row that has seen no key yet: weights 2^-inf = 0
         // The maximum is taken off before the factor: sc s - sc m in one step would leave the rounding of sc m,
         // which is no longer small beside scores of 2^24 and more.
-        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-ref, -ref), up2 = make_float2(kWeightExp, kWeightExp);
+        const float take = even ? -ref : 0.f, times = even ? sc : 1.f;
+        // from a weight to its product with the tile's V; the weights of the sum are those of the product, in other units
+        const int up = vexp == kNoExp ? 0 : max(vexp - lim, kLeastShift);
+        const float2 sc2 = make_float2(times, times), nm2 = make_float2(take, take);
+        const float2 up2 = make_float2((float)(up + kWeightExp), (float)(up + kWeightExp));
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int c0 = 0; c0 < TK; c0 += 32) {
@@ -423,7 +480,8 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
             }
             tmem_st16(tmem + c0 / 2, pk);   // (in the place of scores that are read)
         }
-        l += (acc0.x + acc1.x) + (acc0.y + acc1.y);
+        // (2^-up, and 0 below what a float holds)
+        l += even ? ((acc0.x + acc1.x) + (acc0.y + acc1.y)) * __int_as_float(max(127 - up, 0) << 23) : uneven_l;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -437,7 +495,7 @@ __device__ __forceinline__ void row_warps(const Q8Params& P, const RowsWork& w, 
     const bool sees = row.i >= 0 && l != 0.f;   // (a NaN sum is one)
     m *= sc;
     const int split = w.it.part ? p.chunks[0] + w.it.chunk : w.it.chunk;
-    const float back = vexp == kNoExp ? 0.f : pow2i(vexp - 2 * kWeightExp);
+    const float back = pow2i(lim - 2 * kWeightExp);
     const float mul = p.nsplit > 1 ? back : back * (1.f / l);
     // 32 columns of the warp's rows at a time through its part of the group's q, which is no longer read, so that
     // whole lines are written: 8 lanes to a row

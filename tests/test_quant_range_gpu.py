@@ -66,7 +66,7 @@ def _scale_value(x, b, at, factor):
 
 
 @pytest.mark.parametrize("dtype,d", SOME)
-@pytest.mark.parametrize("H,T", [(4, 2), (4, 5), (12, 3), (6, 9)])
+@pytest.mark.parametrize("H,T", [(4, 2), (4, 5), (12, 3), (6, 9), (4, 40)])
 @pytest.mark.parametrize("power", [12, 22, 40])
 def test_a_later_token_with_a_large_value(saf, dtype, d, H, T, power):  # noqa: F811
     # rows before the last token do not see its value, however large it is
@@ -78,7 +78,7 @@ def test_a_later_token_with_a_large_value(saf, dtype, d, H, T, power):  # noqa: 
 
 
 @pytest.mark.parametrize("dtype,d", SOME)
-@pytest.mark.parametrize("T", [1, 5])
+@pytest.mark.parametrize("T", [1, 5, 40])
 @pytest.mark.parametrize("power", [12, 22, 40])
 def test_a_large_value_behind_the_window(saf, dtype, d, T, power):  # noqa: F811
     # the frozen heads of a group see it, the ordinary ones do not
@@ -90,7 +90,7 @@ def test_a_large_value_behind_the_window(saf, dtype, d, T, power):  # noqa: F811
 
 
 @pytest.mark.parametrize("dtype,d", SOME)
-@pytest.mark.parametrize("T", [1, 5])
+@pytest.mark.parametrize("T", [1, 5, 40])
 @pytest.mark.parametrize("at", [0, 150, 290])
 @pytest.mark.parametrize("prefix", [0, 90])
 def test_a_large_value_without_weight(saf, dtype, d, T, at, prefix):  # noqa: F811
@@ -104,7 +104,7 @@ def test_a_large_value_without_weight(saf, dtype, d, T, at, prefix):  # noqa: F8
 
 
 @pytest.mark.parametrize("dtype,d", SOME)
-@pytest.mark.parametrize("T", [1, 5])
+@pytest.mark.parametrize("T", [1, 5, 40])
 @pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
 def test_value_scales_over_many_powers_of_two(saf, dtype, d, T, order):  # noqa: F811
     # scales from 2^-60 to 2^60 along the sequence
