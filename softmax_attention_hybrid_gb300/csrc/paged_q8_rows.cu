@@ -35,6 +35,7 @@
 #include <atomic>
 
 #include "paged_q8.cuh"
+#include "pattern_run.h"
 
 namespace saf {
 namespace {
@@ -125,10 +126,15 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t codes) {
     return h;
 }
 
+__device__ __forceinline__ void copy4(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // The pattern warp: a and r of the block's frozen heads for every tile. A row at position i and
 // key x need a[x] and r[i - x]; for all rows of a head and TK keys that is a run of r of imax - imin + TK
 // entries, copied as whole 16-byte lines (so that an entry lies as far into a line as in r; at most three entries
-// of other rows, or behind the array's last line's end, come with it). The copies arrive on their barrier by themselves.
+// of other rows come with it), and one by one where a line is not inside the array. The copies arrive on their
+// barrier by themselves.
 template <int kD>
 __device__ __forceinline__ void pattern_warp(const Q8Params& P, const RowsWork& w, uint8_t* sm, Shared& sh) {
     using C = Cfg<kD>;
@@ -149,14 +155,17 @@ __device__ __forceinline__ void pattern_warp(const Q8Params& P, const RowsWork& 
             const float* a = p.a + h * p.ld + w.off + x0;
             const float* r = p.r + h * p.ld;
             const int keys = min(TK, p.ld - w.off - x0);
-            for (int c = lane; c < keys; c += 32)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(out + f * pitch + c)), "l"(a + c) : "memory");
+            for (int c = lane; c < keys; c += 32) copy4(out + f * pitch + c, a + c);
             if (hi >= lo) {
-                const int first = lo - (int)(((uintptr_t)(r + lo) >> 2) & 3), count = (hi - first + 4) & ~3;
-                if (lane == 0)
-                    bulk_load(out + f * pitch + TK + w.shift(p, h) + first - r0, r + first, 4u * (uint32_t)count,
-                              &bars.pat_full[b]);
-                bytes += 4u * (uint32_t)count;
+                float* to = out + f * pitch + TK + w.shift(p, h) - r0;
+                const PatternRun run = pattern_run((uintptr_t)r, (long long)h * p.ld, (long long)(p.H - (int)h) * p.ld, lo, hi);
+                const uint32_t line_bytes = run.first < run.end ? 4u * (uint32_t)(run.end - run.first) : 0u;
+                if (lane == 0 && line_bytes) bulk_load(to + run.first, r + run.first, line_bytes, &bars.pat_full[b]);
+                bytes += line_bytes;
+                // the rest: below the lines, behind them, or all of it where there is none
+                const int c = lane < 8 ? lo + lane : max(run.end, lo) + lane - 8;
+                if (lane < 16 && c <= hi && (lane < 8 ? c < run.first || !line_bytes : line_bytes != 0))
+                    copy4(to + c, r + c);
             }
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars.pat_full[b])) : "memory");
