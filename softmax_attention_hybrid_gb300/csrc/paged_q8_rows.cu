@@ -130,6 +130,13 @@ __device__ __forceinline__ void copy4(float* dst, const float* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
+// The entries of a run that its lines leave: below them, behind them, or all of it where there is none. (Not inline: the
+// chunk of 512 tokens, which has none, takes 305 us with it and 302 without.)
+__device__ __noinline__ void copy_ends(float* to, const float* r, int first, int end, int lo, int hi) {
+    const int lane = threadIdx.x & 31, c = lane < 8 ? lo + lane : max(end, lo) + lane - 8;
+    if (lane < 16 && c <= hi && (lane < 8 ? c < first || first >= end : first < end)) copy4(to + c, r + c);
+}
+
 // The pattern warp: a and r of the block's frozen heads for every tile. A row at position i and
 // key x need a[x] and r[i - x]; for all rows of a head and TK keys that is a run of r of imax - imin + TK
 // entries, copied as whole 16-byte lines (so that an entry lies as far into a line as in r; at most three entries
@@ -162,10 +169,7 @@ __device__ __forceinline__ void pattern_warp(const Q8Params& P, const RowsWork& 
                 const uint32_t line_bytes = run.first < run.end ? 4u * (uint32_t)(run.end - run.first) : 0u;
                 if (lane == 0 && line_bytes) bulk_load(to + run.first, r + run.first, line_bytes, &bars.pat_full[b]);
                 bytes += line_bytes;
-                // the rest: below the lines, behind them, or all of it where there is none
-                const int c = lane < 8 ? lo + lane : max(run.end, lo) + lane - 8;
-                if (lane < 16 && c <= hi && (lane < 8 ? c < run.first || !line_bytes : line_bytes != 0))
-                    copy4(to + c, r + c);
+                if (run.first > lo || run.end <= hi) copy_ends(to, r, run.first, run.end, lo, hi);
             }
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars.pat_full[b])) : "memory");
