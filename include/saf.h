@@ -328,7 +328,8 @@ SAF_API int saf_attn_bwd_window(const void* q, const void* k, const void* v, con
  * Out: o [B,H,T,d], lse [B,H,T] as for saf_attn_fwd; o = 0, lse = -inf for rows without
  *      a token and rows that see no key.
  * A key or value that one row sees must be finite where another row beside it does not see
- * it, which takes it with weight 0; what no row sees may be anything.
+ * it, which takes it with weight 0, and so must a value that a pattern of -infinity alone hides; what
+ * lies behind the rows' positions or outside their windows, for all of them, may be anything.
  * T is 1 for a decoding step, a few for drafted tokens, and may be any length for a
  * chunk of a prompt. SAF_FP32 is computed in fp32 throughout; sums and softmax statistics
  * are fp32 in both types.

@@ -105,6 +105,21 @@ def test_a_large_value_without_weight(saf, dtype, d, T, at, prefix):  # noqa: F8
 
 @pytest.mark.parametrize("dtype,d", SOME)
 @pytest.mark.parametrize("T", [1, 5, 40])
+@pytest.mark.parametrize("masked", [-float("inf"), torch.finfo(torch.float32).min])
+def test_a_large_value_that_a_pattern_hides(saf, dtype, d, T, masked):  # noqa: F811
+    # some heads' patterns leave it no weight at all, however large it is; the others do not hide it
+    frozen = [1, 1, 0, 1]
+    x = Batch(dtype, 4, 1, T, d, 16, (300, 120), (T, T), seed=36)
+    for b in range(2):
+        _scale_value(x, b, 70, 2.0 ** 90)
+    x.a[:2, 70] = masked
+    o, lse = x.call(saf, frozen)
+    x.a[:2, 70] = -200.0   # e^-200 2^90: nothing in the outputs' bits
+    _check(x, o, lse, frozen)
+
+
+@pytest.mark.parametrize("dtype,d", SOME)
+@pytest.mark.parametrize("T", [1, 5, 40])
 @pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
 def test_value_scales_over_many_powers_of_two(saf, dtype, d, T, order):  # noqa: F811
     # scales from 2^-60 to 2^60 along the sequence
