@@ -186,6 +186,8 @@ Plan make_plan(int B, int H, int Hkv, int T, int d, int max_len, int P, Kind kin
 // of what it costs if all sequences are as long as the bound, in whole rounds, and if they fill two thirds of it on
 // the average. (32 sequences of 4K to 16K tokens: 143, 114, 128, 120, 118, 124 us with 1 .. 6 items; 16 of 2K to 8K
 // with up to five tokens each: 72, 59, 71, 73 us with 2 .. 5, and 74, 92, 85, 96 once all are as long as the bound.)
+// (Two thirds, the halves and 0.15 of a tile for an item's share of the join were chosen on these two batches; the
+// lengths themselves are not known on the host.)
 // Candidates: one, the most items that fit in 1, 2, ... rounds, and the minimum over c of
 // (units c / slots) (set_up + nt / c) + nt / c, the work and the tail of c items per unit.
 enum class Lengths { kEven, kSpread, kMixed };

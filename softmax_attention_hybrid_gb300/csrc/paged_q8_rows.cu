@@ -17,11 +17,12 @@
 // another; the two groups do so in turn. The softmax goes over the tile twice, 32 keys at a time: scaled
 // and masked scores back to tensor memory with their maximum, then the weights.
 //
-// 512 tokens of each of four prompts after up to 8K, 32 heads over 8 of 128, a quarter frozen: 290 us, 490 TFLOP/s (26% of
-// a large matrix product's rate; tensor pipe 29% active, issue slots 40%). A tile takes a group 2.95 us, the chain of
+// 512 tokens of each of four prompts after up to 8K, 32 heads over 8 of 128, a quarter frozen: 302 us, 472 TFLOP/s (25% of
+// a large matrix product's rate; tensor pipe 28% active, issue slots 43%). A tile takes a group about 3 us, the chain of
 // S, two passes of the softmax over tensor memory, and P V, with the other group's in between. 64 sequences
-// after 32K, all heads of a group in a block: 70 us for the prefix (one read of it takes 10).
-// Other forms of the same work, in us: tiles of 64 keys with the loops unrolled 369 (the loop leaves the instruction cache)
+// after 32K, all heads of a group in a block: 71 us for the prefix (one read of it takes 10). (289 us for the
+// chunk with the largest value scale so far as the unit of all values, which lost the others' bits.)
+// Other forms of the same work, in us, beside 290 at that time: tiles of 64 keys with the loops unrolled 369 (the loop leaves the instruction cache)
 // and rolled 401, two CTAs of 128 rows 412, two threads to a row 365.
 //
 // Warps (512 threads, one CTA per SM): 0-7 rows, 8-11 unpack V and hand out the scales, 12 loads K, V and
@@ -242,7 +243,7 @@ __device__ __forceinline__ void unpack_warps(const Q8Params& P, const RowsWork& 
         };
         const int vexp = exponent(top);
         const bool even = top == 0.f || exponent(__uint_as_float(low)) >= vexp - kEvenRange;
-        if (warp == 0) {
+        if (warp == 0) {   // (each lane has used what it read of the ring before the warp meets and its slot is given back)
             if (!even)   // (a value of scale zero has no part in what is the row's largest)
 #pragma unroll
                 for (int k = 0; k < TK / 32; ++k)

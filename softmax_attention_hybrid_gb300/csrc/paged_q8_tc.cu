@@ -22,11 +22,12 @@
 // they are found anew, and O and l are scaled. Tiles are walked from the newest key to the oldest: the
 // patterns of frozen heads, and most ordinary rows, look nearby first, so that the maximum is found early.
 //
-// 32 sequences of 4K to 16K tokens, 32 heads over 8 of 128 (a quarter frozen): 118 us, 6.0 TB/s, 88% of a plain copy's rate.
-// 64 sequences with a window of 1024: 41 us (512 items of 10 tiles on 456 places, and what an item costs beside its
+// 32 sequences of 4K to 16K tokens, 32 heads over 8 of 128 (a quarter frozen): 120 us, 5.9 TB/s, 87% of a plain copy's rate.
+// 64 sequences with a window of 1024: 42 us (512 items of 10 tiles on 456 places, and what an item costs beside its
 // tiles: counts, page, first load, softmax and product one after the other, 7 us). Five tokens each of 16 sequences, 20
-// rows: 71 us with two warpgroups in the softmax (78 with one); a tile takes a CTA 2700 cycles alone, two on an SM 4200
-// (issue slots 45%), and SMs with two of the longest items run the longest.
+// rows: 72 us with two warpgroups in the softmax (some 7 more with one); a tile takes a CTA about 2700 cycles alone, two on
+// an SM 4200 (issue slots 49%), and SMs with two of the longest items run the longest. (With one unit for all rows of a
+// warpgroup, the largest value scale, these took 119, 41 and 71 us, and rows beside large values came out wrong.)
 //
 // Warps (256 threads, two CTAs per SM, three with 4 rows; 384 threads from 16 rows on): a warpgroup of the softmax, from 16 rows
 // on two with half of the rows each; then a warp that loads K, V and their scales (each of its lanes fetches one page of the
